@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -32,6 +33,8 @@ EXPORTED = ("mx_codes_bytes", "mx_sf_bytes", "mx_scale_count", "mx_amax", "mx_qu
             "mx_gemm_amax", "mx_gemm_quantized",
             "mx_linear_workspace_bytes", "mx_linear_fwd", "mx_linear_fwd_noalloc", "mx_linear_bwd",
             "mx_linear_saved_bytes", "mx_linear_fwd_save", "mx_linear_bwd_saved", "mx_strerror",
+            "mx_act8_codes_bytes", "mx_act8_sf_bytes", "mx_act8_save", "mx_act8_restore", "mx_norm_fwd",
+            "mx_norm_bwd_workspace_bytes", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd",
             "mx_last_device_status", "mx_selftest_bounded_wait", "mx_launch_count",
             "mx_debug_divide", "mx_debug_set_quant_impl", "mx_debug_set_tile_fail_at", "mx_debug_set_bwd_fork", "mx_debug_set_gemm_variant",
             "mx_debug_last_gemm_variant")
@@ -48,6 +51,10 @@ class _CTensor(C.Structure):
                 ("tensor_scale", C.c_void_p), ("rows", C.c_int64), ("k", C.c_int64),
                 ("fmt", C.c_int32), ("block", C.c_int32), ("hadamard", C.c_int32),
                 ("reserved", C.c_int32)]
+
+
+class _CAct8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("sf", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64)]
 
 
 class _CBwdOpts(C.Structure):
@@ -120,6 +127,20 @@ def lib():
             L.mx_linear_bwd_saved.restype = i32
             L.mx_linear_bwd_saved.argtypes = [p, i64, i64, i64, i32, p, C.POINTER(_CBwdOpts), p, sz, p, i32, p, i32,
                                               p, sz, p]
+            a8 = C.POINTER(_CAct8)
+            for name in ("mx_act8_codes_bytes", "mx_act8_sf_bytes", "mx_norm_bwd_workspace_bytes"):
+                getattr(L, name).restype = sz
+                getattr(L, name).argtypes = [i64, i64]
+            L.mx_act8_save.argtypes = [p, i64, i32, a8, p]
+            L.mx_act8_restore.argtypes = [a8, p, i64, i32, p]
+            L.mx_norm_fwd.argtypes = [p, i64, p, i64, i32, i64, i64, i32, p, p, i32, C.c_float, p, i64, p, i64, i32,
+                                      p, p, a8, p, p]
+            L.mx_norm_bwd.argtypes = [p, i64, i32, p, i64, a8, p, p, p, i32, i64, i64, i32, p, i64, p, i64, i32, p,
+                                      p, p, p, sz, p]
+            L.mx_act_fwd.argtypes = [p, i64, p, i64, i64, i64, i32, i32, p, i64, a8, a8, p, p]
+            L.mx_act_bwd.argtypes = [p, i64, p, i64, p, i64, a8, a8, i64, i64, i32, i32, p, i64, p, i64, p, p]
+            for name in ("mx_act8_save", "mx_act8_restore", "mx_norm_fwd", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd"):
+                getattr(L, name).restype = i32
             L.mx_strerror.restype = C.c_char_p
             L.mx_strerror.argtypes = [i32]
             L.mx_last_device_status.restype = i32
@@ -432,6 +453,319 @@ def linear_bwd_saved(dY: torch.Tensor, saved: torch.Tensor, Kin: int, fmt: str,
                                    _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "mx_linear_bwd_saved")
     return dX, dW
+
+
+# ---------------------------------------------------------------- norm, activation, 8-bit checkpoints
+NORMS = {"layer": 0, "rms": 1}
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+class Act8:
+    """An 8-bit checkpoint of a matrix [rows, cols] (G = ceil(cols / 32)): E4M3
+    codes uint8 [rows, 32 G] and exponent bytes uint8 [rows, G]; a value stands
+    for code * 2^(byte - 127).  Made by act8_save, norm_fwd and act_fwd."""
+
+    __slots__ = ("codes", "sf", "cols")
+
+    def __init__(self, codes: torch.Tensor, sf: torch.Tensor, cols: int):
+        self.codes, self.sf, self.cols = codes, sf, cols
+
+    @staticmethod
+    def empty(rows: int, cols: int, device=None) -> "Act8":
+        device = device or torch.device("cuda")
+        G = -(-cols // 32)
+        return Act8(torch.empty((rows, 32 * G), dtype=torch.uint8, device=device),
+                    torch.empty((rows, G), dtype=torch.uint8, device=device), cols)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    def _c(self, dev, rows=None, cols=None) -> _CAct8:
+        c, f = self.codes, self.sf
+        G = -(-self.cols // 32)
+        if (c.dtype != torch.uint8 or f.dtype != torch.uint8 or c.shape != (c.shape[0], 32 * G)
+                or f.shape != (c.shape[0], G) or not c.is_contiguous() or not f.is_contiguous()):
+            raise MXError(MX_ERR_INVALID_ARG, "a checkpoint holds contiguous uint8 codes [rows, 32 G] and sf [rows, G]")
+        if c.device != dev or f.device != dev:
+            raise MXError(MX_ERR_INVALID_ARG, f"checkpoint on {c.device}, expected {dev}")
+        if rows is not None and (c.shape[0] != rows or self.cols != cols):
+            raise MXError(MX_ERR_INVALID_ARG, f"checkpoint of [{c.shape[0]}, {self.cols}], expected [{rows}, {cols}]")
+        return _CAct8(c.data_ptr(), f.data_ptr(), c.shape[0], self.cols)
+
+
+class NormOut(NamedTuple):
+    """norm_fwd's results: y; sum (the residual stream after the addition, or x
+    itself); mean and rstd [rows] (None where not asked for; rms has no mean);
+    saved (the checkpoint of sum, or None)."""
+    y: torch.Tensor
+    sum: torch.Tensor
+    mean: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+    saved: Optional[Act8]
+
+
+class ActOut(NamedTuple):
+    """act_fwd's results: h and the checkpoints of gate and up (or None)."""
+    h: torch.Tensor
+    gate: Optional[Act8]
+    up: Optional[Act8]
+
+
+def _first(t, what):
+    """Shape and device of the matrix that a call goes by."""
+    if t.dim() != 2:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must be a matrix, not of shape {tuple(t.shape)}")
+    _on_gpu(t)
+    return t.shape[0], t.shape[1], t.device
+
+
+def _mat(t, rows, cols, dev, what, dtype=None):
+    """(pointer, row stride) of a matrix after checking it."""
+    if t.shape != (rows, cols):
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    dt = t.dtype
+    if dt is not dtype and (dtype is not None or dt not in OUT):
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} has type {dt}, expected {dtype or 'bfloat16 or float32'}")
+    if t.device != dev:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} is on {t.device}, expected {dev}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must have unit column stride")
+    return t.data_ptr(), ld if rows > 1 else cols
+
+
+def _vec(t, n, dev, what, dtype=torch.float32):
+    """Pointer of a contiguous vector of n elements (None: absent)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or t.device != dev or not t.is_contiguous():
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must be {n} contiguous {dtype} values on {dev}")
+    return t.data_ptr()
+
+
+def _params(weight, bias, cols, dev):
+    """(weight pointer, bias pointer, their type's number)."""
+    first = weight if weight is not None else bias
+    if first is None:
+        return None, None, 0
+    if first.dtype not in OUT:
+        raise MXError(MX_ERR_INVALID_ARG, f"weight and bias are bfloat16 or float32, not {first.dtype}")
+    return (_vec(weight, cols, dev, "weight", first.dtype), _vec(bias, cols, dev, "bias", first.dtype),
+            OUT[first.dtype])
+
+
+def _run(dev, what, fn, *args):
+    """One call of the library on the tensors' device and its current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != MX_OK:
+        raise MXError(rc, what)
+
+
+def _look_up(table, key, what):
+    if key not in table:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} {key!r} is none of {', '.join(map(str, table))}")
+    return table[key]
+
+
+def act8_save(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8:
+    """The 8-bit checkpoint of a bf16 or fp32 matrix."""
+    if stream is not None:  # also what is allocated here then belongs to that stream
+        with torch.cuda.stream(stream):
+            return act8_save(x, out)
+    rows, cols, dev = _first(x, "x")
+    px, ldx = _mat(x, rows, cols, dev, "x")
+    out = out if out is not None else Act8.empty(rows, cols, dev)
+    _run(dev, "mx_act8_save", lib().mx_act8_save, px, ldx, OUT[x.dtype], out._c(dev, rows, cols))
+    return out
+
+
+def act8_restore(a: Act8, out_dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values a checkpoint stands for, [rows, cols]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return act8_restore(a, out_dtype, out)
+    _on_gpu(a.codes)
+    rows, cols, dev = a.rows, a.cols, a.codes.device
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    po, ldo = _mat(out, rows, cols, dev, "out")
+    _run(dev, "mx_act8_restore", lib().mx_act8_restore, a._c(dev), po, ldo, OUT[out.dtype])
+    return out
+
+
+def norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+             kind: str = "layer", eps: float = 1e-5, residual: torch.Tensor | None = None,
+             sum_out: torch.Tensor | None = None, save: bool | Act8 = False, amax_out: torch.Tensor | None = None,
+             out_dtype=None, out: torch.Tensor | None = None, need_stats: bool = True,
+             mean: torch.Tensor | None = None, rstd: torch.Tensor | None = None, stream=None) -> NormOut:
+    """Layer norm (or RMS norm) of the rows of x [rows, cols], or of x +
+    residual: y = (s - mean) * rstd * weight + bias.  sum_out may be x or
+    residual itself.  save: True, or an Act8 to fill, keeps the 8-bit checkpoint
+    of s for norm_bwd.  amax_out: one fp32 word that receives max |y|."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_fwd(x, weight, bias, kind, eps, residual, sum_out, save, amax_out, out_dtype, out, need_stats,
+                            mean, rstd)
+    rows, cols, dev = _first(x, "x")
+    px, ldx = _mat(x, rows, cols, dev, "x")
+    dt = x.dtype
+    pr = ps = None
+    ldr = lds = 0
+    if residual is not None:
+        pr, ldr = _mat(residual, rows, cols, dev, "residual", dt)
+        sum_out = sum_out if sum_out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
+        ps, lds = _mat(sum_out, rows, cols, dev, "sum_out", dt)
+    elif sum_out is not None:
+        raise MXError(MX_ERR_INVALID_ARG, "sum_out goes with residual")
+    pw, pb, wt = _params(weight, bias, cols, dev)
+    y = out if out is not None else torch.empty((rows, cols), dtype=out_dtype or dt, device=dev)
+    py, ldy = _mat(y, rows, cols, dev, "out")
+    k = _look_up(NORMS, kind, "kind")
+    if need_stats:
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        if mean is None and k == 0:
+            mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    saved = None
+    if save is not False and save is not None:
+        saved = save if isinstance(save, Act8) else Act8.empty(rows, cols, dev)
+    _run(dev, "mx_norm_fwd", lib().mx_norm_fwd, px, ldx, pr, ldr, OUT[dt], rows, cols, k, pw, pb, wt, eps, ps, lds,
+         py, ldy, OUT[y.dtype], _vec(mean, rows, dev, "mean") if k == 0 else None, _vec(rstd, rows, dev, "rstd"),
+         saved._c(dev, rows, cols) if saved is not None else None, _vec(amax_out, 1, dev, "amax_out"))
+    return NormOut(y, sum_out if residual is not None else x, mean if k == 0 else None, rstd, saved)
+
+
+def norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().mx_norm_bwd_workspace_bytes(rows, cols))
+
+
+def norm_bwd(dy: torch.Tensor, x: torch.Tensor | Act8, rstd: torch.Tensor, mean: torch.Tensor | None = None,
+             weight: torch.Tensor | None = None, kind: str = "layer", dres: torch.Tensor | None = None,
+             need_dw: bool = True, need_db: bool | None = None, dx_dtype=None, dx: torch.Tensor | None = None,
+             dw: torch.Tensor | None = None, db: torch.Tensor | None = None, amax_out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None):
+    """(dx, dw, db) of norm_fwd.  x: the forward's sum, or its checkpoint.  dres:
+    the gradient that reaches the residual stream past the norm, added to dx.
+    need_db defaults to the kind's use of a bias (layer: True, rms: False);
+    dw and db are fp32 (None where not asked for)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_bwd(dy, x, rstd, mean, weight, kind, dres, need_dw, need_db, dx_dtype, dx, dw, db, amax_out,
+                            workspace)
+    rows, cols, dev = _first(dy, "dy")
+    pdy, lddy = _mat(dy, rows, cols, dev, "dy")
+    k = _look_up(NORMS, kind, "kind")
+    if isinstance(x, Act8):
+        px, ldx, x8 = None, 0, x._c(dev, rows, cols)
+        dt = dx.dtype if dx is not None else dx_dtype or (dres.dtype if dres is not None else dy.dtype)
+    else:
+        dt, x8 = x.dtype, None
+        px, ldx = _mat(x, rows, cols, dev, "x")
+        if dx_dtype is not None and dx_dtype is not dt:
+            raise MXError(MX_ERR_UNSUPPORTED, "dx has the type of x")
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=dt, device=dev)
+    pdx, lddx = _mat(dx, rows, cols, dev, "dx", dt)
+    pres, ldres = _mat(dres, rows, cols, dev, "dres", dt) if dres is not None else (None, 0)
+    if rstd is None or (k == 0 and mean is None):
+        raise MXError(MX_ERR_INVALID_ARG, "norm_bwd needs the forward's rstd, and its mean for a layer norm")
+    pw, _, wt = _params(weight, None, cols, dev)
+    if need_db is None:
+        need_db = k == 0
+    L = lib()
+    n = 0
+    if need_dw or need_db:
+        if need_dw and dw is None:
+            dw = torch.empty(cols, dtype=torch.float32, device=dev)
+        if need_db and db is None:
+            db = torch.empty(cols, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(L.mx_norm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise MXError(MX_ERR_INVALID_ARG, f"workspace must be contiguous memory on {dev}")
+        n = workspace.numel() * workspace.element_size()
+    _run(dev, "mx_norm_bwd", L.mx_norm_bwd, pdy, lddy, OUT[dy.dtype], px, ldx, x8,
+         _vec(mean, rows, dev, "mean") if k == 0 else None, _vec(rstd, rows, dev, "rstd"), pw, wt, rows, cols, k, pres,
+         ldres, pdx, lddx, OUT[dt], _vec(dw, cols, dev, "dw") if need_dw else None,
+         _vec(db, cols, dev, "db") if need_db else None, _vec(amax_out, 1, dev, "amax_out"),
+         workspace.data_ptr() if n else None, n)
+    return dx, dw if need_dw else None, db if need_db else None
+
+
+def act_fwd(gate: torch.Tensor, up: torch.Tensor | None = None, act: str = "silu", save: bool = False,
+            gate8: Act8 | None = None, up8: Act8 | None = None, amax_out: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, stream=None) -> ActOut:
+    """h = act(gate) * up, or act(gate) without up; gate and up may be views of
+    the halves of one projection's output.  save (or gate8 / up8 to fill) keeps
+    the 8-bit checkpoints that act_bwd reads.  amax_out: one fp32 word that
+    receives max |h|."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return act_fwd(gate, up, act, save, gate8, up8, amax_out, out)
+    rows, cols, dev = _first(gate, "gate")
+    pg, ldg = _mat(gate, rows, cols, dev, "gate")
+    dt = gate.dtype
+    pu, ldu = _mat(up, rows, cols, dev, "up", dt) if up is not None else (None, 0)
+    h = out if out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
+    ph, ldh = _mat(h, rows, cols, dev, "out", dt)
+    if save:
+        gate8 = gate8 if gate8 is not None else Act8.empty(rows, cols, dev)
+        if up is not None and up8 is None:
+            up8 = Act8.empty(rows, cols, dev)
+    _run(dev, "mx_act_fwd", lib().mx_act_fwd, pg, ldg, pu, ldu, rows, cols, _look_up(ACTS, act, "act"), OUT[dt], ph, ldh,
+         gate8._c(dev, rows, cols) if gate8 is not None else None,
+         up8._c(dev, rows, cols) if up8 is not None else None, _vec(amax_out, 1, dev, "amax_out"))
+    return ActOut(h, gate8, up8)
+
+
+def act_bwd(dh: torch.Tensor, gate: torch.Tensor | Act8, up: torch.Tensor | Act8 | None = None, act: str = "silu",
+            amax_out: torch.Tensor | None = None, dgate: torch.Tensor | None = None,
+            dup: torch.Tensor | None = None, stream=None):
+    """(dgate, dup) of act_fwd from dh and its inputs, both kept or both as
+    checkpoints (dup is None without up).  Without buffers given, dgate and dup
+    are the halves of one [rows, 2 cols] tensor, as the projection's backward
+    pass takes them.  amax_out: max over both."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return act_bwd(dh, gate, up, act, amax_out, dgate, dup)
+    rows, cols, dev = _first(dh, "dh")
+    pdh, ldh = _mat(dh, rows, cols, dev, "dh")
+    dt = dh.dtype
+    gated = up is not None
+    pg = pu = g8 = u8 = None
+    ldg = ldu = lddu = 0
+    if isinstance(gate, Act8):
+        g8 = gate._c(dev, rows, cols)
+        if gated:
+            if not isinstance(up, Act8):
+                raise MXError(MX_ERR_INVALID_ARG, "gate and up are both kept or both checkpoints")
+            u8 = up._c(dev, rows, cols)
+    else:
+        pg, ldg = _mat(gate, rows, cols, dev, "gate", dt)
+        if gated:
+            if isinstance(up, Act8):
+                raise MXError(MX_ERR_INVALID_ARG, "gate and up are both kept or both checkpoints")
+            pu, ldu = _mat(up, rows, cols, dev, "up", dt)
+    if dgate is None and dup is None and gated:
+        both = torch.empty((rows, 2 * cols), dtype=dt, device=dev)
+        dgate, dup = both[:, :cols], both[:, cols:]
+    if dgate is None:
+        dgate = torch.empty((rows, cols), dtype=dt, device=dev)
+    pdg, lddg = _mat(dgate, rows, cols, dev, "dgate", dt)
+    pdu = None
+    if gated:
+        dup = dup if dup is not None else torch.empty((rows, cols), dtype=dt, device=dev)
+        pdu, lddu = _mat(dup, rows, cols, dev, "dup", dt)
+    elif dup is not None:
+        raise MXError(MX_ERR_INVALID_ARG, "dup goes with up")
+    _run(dev, "mx_act_bwd", lib().mx_act_bwd, pdh, ldh, pg, ldg, pu, ldu, g8, u8, rows, cols,
+         _look_up(ACTS, act, "act"), OUT[dt], pdg, lddg, pdu, lddu, _vec(amax_out, 1, dev, "amax_out"))
+    return dgate, dup
 
 
 def last_device_status(stream=None) -> int:

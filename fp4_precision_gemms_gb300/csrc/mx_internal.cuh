@@ -118,4 +118,65 @@ int launch_wait_selftest(uint64_t limit_ns, const Device& d, cudaStream_t s);
 int launch_divide_check(const float* v, const float* dv, int64_t n, float* fast, float* ieee, const Device& d,
                         cudaStream_t s);
 
+// The norm and activation calls (norm.cu, act.cu).  dtypes are mx_out_dtype
+// values; a null codes pointer is an absent checkpoint.
+struct Act8View {
+    uint8_t* codes = nullptr;
+    uint8_t* sf = nullptr;
+};
+struct NormFwdArgs {
+    const void* x;
+    const void* residual;
+    int64_t ldx, ldr, rows, cols;
+    const void* weight;
+    const void* bias;
+    void* sum_out;
+    void* y;
+    int64_t lds, ldy;
+    float* mean;
+    float* rstd;
+    Act8View save;
+    unsigned* amax;
+    float eps;
+    int x_dtype, y_dtype, w_dtype, kind;
+};
+struct NormBwdArgs {
+    const void* dy;
+    const void* x;
+    Act8View x8;
+    int64_t ldy, ldx, rows, cols;
+    const float* mean;
+    const float* rstd;
+    const void* weight;
+    const void* dres;
+    void* dx;
+    int64_t ldres, lddx;
+    float* dw;
+    float* db;
+    float* parts;  // workspace: partial sums of dw, then of db
+    unsigned* amax;
+    int dy_dtype, dx_dtype, w_dtype, kind;
+};
+struct ActArgs {  // forward: h written; backward: h is dh, read
+    const void* gate;
+    const void* up;
+    void* h;
+    void* dgate;
+    void* dup;
+    int64_t ldg, ldu, ldh, lddg, lddu, rows, cols;
+    Act8View gate8, up8;
+    unsigned* amax;
+    int act, dtype;
+    bool gated;
+};
+int64_t norm_bwd_parts(int64_t rows, int64_t cols);  // partial sums of a column in the workspace
+int launch_norm_fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s);
+int launch_norm_bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s);
+int launch_act_fwd(const ActArgs& a, const Device& d, cudaStream_t s);
+int launch_act_bwd(const ActArgs& a, const Device& d, cudaStream_t s);
+int launch_act8_save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8View out, const Device& d,
+                     cudaStream_t s);
+int launch_act8_restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int dtype, const Device& d,
+                        cudaStream_t s);
+
 }  // namespace mx

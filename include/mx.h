@@ -338,6 +338,115 @@ int mx_linear_bwd_saved(const void* dY, int64_t T, int64_t Kin, int64_t Nout, in
                         const mx_bwd_opts* opts, const void* saved, size_t saved_bytes, void* dX, int dx_dtype,
                         void* dW, int dw_dtype, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * What stands between a model's linears in training and serving: the norm
+ * before a projection, the MLP's activation, and the 8-bit checkpoints of
+ * their inputs that the backward pass reads in place of 16- or 32-bit copies
+ * ([COAT]: activations kept in FP8).
+ *
+ * Rules of these calls beyond the shared conventions:
+ *   - Matrices are row-major with unit column stride and a row stride in
+ *     elements >= cols.  Pointers need the alignment of their element only;
+ *     16-byte aligned rows take the wide-access kernels.  dtype arguments are
+ *     mx_out_dtype values.
+ *   - Any rows >= 0 and 0 <= cols <= 2^30.  A call on an empty matrix
+ *     launches no kernel; it zeroes amax_out, dw and db where given.
+ *   - An output may be the same memory as an input of the same shape, element
+ *     size and row stride; any other overlap is the caller's error.
+ *   - Infinities and NaN propagate as the formulas give them.
+ *   - Sums, statistics and the gradients' reductions are fp32; results are
+ *     rounded once, to nearest even.  The same call on the same inputs gives
+ *     the same bits: no reduction depends on the order of atomics.
+ *   - amax_out (optional, one device float) receives max |value| over the
+ *     call's output as written, NaN if any is NaN: the amax_in / x_amax /
+ *     dy_amax of the quantization that follows.
+ *   - Argument errors come before MX_ERR_NO_DEVICE / MX_ERR_UNSUPPORTED for
+ *     the device: MX_ERR_INVALID_ARG for a null pointer, a bad enum or shape,
+ *     MX_ERR_ALIGNMENT for a misaligned pointer, MX_ERR_UNSUPPORTED for a
+ *     combination of types that has no kernel.
+ *   - The calls allocate nothing and may be captured into a CUDA graph. */
+
+/* An 8-bit activation checkpoint of a matrix [rows, cols], G = ceil(cols/32):
+ *   codes  E4M3, row-major [rows, 32 G] (the pad columns hold code 0),
+ *          mx_act8_codes_bytes bytes, 16-byte aligned;
+ *   sf     one byte e + 127 for each 32 columns of a row, row-major [rows, G],
+ *          mx_act8_sf_bytes bytes.
+ * e is the CEIL rule's exponent: the smallest with b 2^-e <= 448, b the
+ * largest |x| of the group's finite values, at least -127, 0 for b = 0; so no
+ * finite value saturates.  code = E4M3(x 2^-e), to nearest even; Inf and NaN
+ * become the NaN code.  A value stands for code * 2^e. */
+typedef struct mx_act8 {
+    uint8_t* codes;
+    uint8_t* sf;
+    int64_t rows;
+    int64_t cols;
+} mx_act8;
+
+/* Byte sizes of a checkpoint's buffers (0 for invalid arguments). */
+size_t mx_act8_codes_bytes(int64_t rows, int64_t cols);
+size_t mx_act8_sf_bytes(int64_t rows, int64_t cols);
+
+/* Checkpoint of x[out->rows, out->cols] (row stride ldx) into out's buffers. */
+int mx_act8_save(const void* x, int64_t ldx, int x_dtype, const mx_act8* out, void* stream);
+
+/* out[rows, cols] = the values a stands for, exact but for bf16 subnormals and
+ * for codes that rounded up to 2^128 (|x| >= 1.9375 * 2^127), which give Inf. */
+int mx_act8_restore(const mx_act8* a, void* out, int64_t ldo, int out_dtype, void* stream);
+
+typedef enum mx_norm_kind { MX_NORM_LAYER = 0, MX_NORM_RMS = 1 } mx_norm_kind;
+
+/* The norm's forward pass over the rows of a residual stream:
+ *   s    = x, or x + residual rounded to x_dtype (written to sum_out)
+ *   mean = sum(s) / cols (MX_NORM_RMS: 0), var = sum((s - mean)^2) / cols
+ *   rstd = 1 / sqrt(var + eps)
+ *   y    = (s - mean) * rstd * weight + bias, in y_dtype
+ * residual (x_dtype) and sum_out come together or not at all.  weight, bias:
+ * [cols] in w_dtype, each may be NULL (1 and 0).  mean, rstd: [rows] fp32,
+ * each may be NULL (mean is not written for MX_NORM_RMS).  save (may be NULL):
+ * the checkpoint of s, rows x cols. */
+int mx_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int x_dtype, int64_t rows,
+                int64_t cols, int kind, const void* weight, const void* bias, int w_dtype, float eps, void* sum_out,
+                int64_t lds, void* y, int64_t ldy, int y_dtype, float* mean, float* rstd, const mx_act8* save,
+                float* amax_out, void* stream);
+
+/* Workspace bytes of mx_norm_bwd when dw or db is asked for (0 for invalid
+ * arguments or an empty matrix). */
+size_t mx_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/* The norm's backward pass from dy (dy_dtype), the forward's mean and rstd,
+ * and its input s: either x (dx_dtype, row stride ldx) or, with x NULL, the
+ * checkpoint x8.  With h = (s - mean) * rstd and g = dy * weight:
+ *   dx = (g - h * mean_cols(g * h) - mean_cols(g)) * rstd + dres
+ * (MX_NORM_RMS: mean is not read and mean_cols(g) is left out)
+ *   dw[cols] = sum over rows of dy * h,   db[cols] = sum over rows of dy (fp32)
+ * dres (may be NULL, dx_dtype): the gradient that reaches s past the norm.
+ * dw and db may be NULL.  workspace: device, 16-byte aligned, needed when dw
+ * or db is given (MX_ERR_WORKSPACE).  amax_out covers dx. */
+int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_t ldx, const mx_act8* x8,
+                const float* mean, const float* rstd, const void* weight, int w_dtype, int64_t rows, int64_t cols,
+                int kind, const void* dres, int64_t ldres, void* dx, int64_t lddx, int dx_dtype, float* dw, float* db,
+                float* amax_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* a(z): SILU z / (1 + exp(-z)); GELU z * (1 + erf(z / sqrt 2)) / 2; GELU_TANH
+ * z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2. */
+typedef enum mx_act_kind { MX_ACT_SILU = 0, MX_ACT_GELU = 1, MX_ACT_GELU_TANH = 2 } mx_act_kind;
+
+/* The MLP's activation h = a(gate) * up, or a(gate) with up NULL; all of one
+ * dtype.  gate and up may be the halves of one projection's rows.  gate8 /
+ * up8 (each may be NULL): checkpoints of gate and up. */
+int mx_act_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu, int64_t rows, int64_t cols, int act,
+               int dtype, void* h, int64_t ldh, const mx_act8* gate8, const mx_act8* up8, float* amax_out,
+               void* stream);
+
+/* Its backward pass from dh and the forward's inputs, each kept (gate, up, in
+ * dtype) or, with gate NULL, as checkpoints (gate8, up8):
+ *   dgate = dh * up * a'(gate),  dup = dh * a(gate)   (dgate = dh * a'(gate))
+ * Ungated when up and up8 are NULL; dup goes with up / up8.  amax_out covers
+ * dgate and dup together. */
+int mx_act_bwd(const void* dh, int64_t ldh, const void* gate, int64_t ldg, const void* up, int64_t ldu,
+               const mx_act8* gate8, const mx_act8* up8, int64_t rows, int64_t cols, int act, int dtype, void* dgate,
+               int64_t lddg, void* dup, int64_t lddu, float* amax_out, void* stream);
+
 /* Human-readable text of an mx_status. */
 const char* mx_strerror(int status);
 
