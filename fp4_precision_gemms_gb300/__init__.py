@@ -75,6 +75,8 @@ def build(force: bool = False) -> str:
 def lib():
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -483,15 +485,15 @@ class Act8:
 
     def _c(self, dev, rows=None, cols=None) -> _CAct8:
         c, f = self.codes, self.sf
-        G = -(-self.cols // 32)
-        if (c.dtype != torch.uint8 or f.dtype != torch.uint8 or c.shape != (c.shape[0], 32 * G)
-                or f.shape != (c.shape[0], G) or not c.is_contiguous() or not f.is_contiguous()):
+        n, G = c.shape[0], -(-self.cols // 32)
+        if (c.dtype is not torch.uint8 or f.dtype is not torch.uint8 or c.shape != (n, 32 * G) or f.shape != (n, G)
+                or not c.is_contiguous() or not f.is_contiguous()):
             raise MXError(MX_ERR_INVALID_ARG, "a checkpoint holds contiguous uint8 codes [rows, 32 G] and sf [rows, G]")
         if c.device != dev or f.device != dev:
             raise MXError(MX_ERR_INVALID_ARG, f"checkpoint on {c.device}, expected {dev}")
-        if rows is not None and (c.shape[0] != rows or self.cols != cols):
-            raise MXError(MX_ERR_INVALID_ARG, f"checkpoint of [{c.shape[0]}, {self.cols}], expected [{rows}, {cols}]")
-        return _CAct8(c.data_ptr(), f.data_ptr(), c.shape[0], self.cols)
+        if rows is not None and (n != rows or self.cols != cols):
+            raise MXError(MX_ERR_INVALID_ARG, f"checkpoint of [{n}, {self.cols}], expected [{rows}, {cols}]")
+        return _CAct8(c.data_ptr(), f.data_ptr(), n, self.cols)
 
 
 class NormOut(NamedTuple):
@@ -514,10 +516,12 @@ class ActOut(NamedTuple):
 
 def _first(t, what):
     """Shape and device of the matrix that a call goes by."""
+    if not t.is_cuda:
+        _on_gpu(t)
     if t.dim() != 2:
         raise MXError(MX_ERR_INVALID_ARG, f"{what} must be a matrix, not of shape {tuple(t.shape)}")
-    _on_gpu(t)
-    return t.shape[0], t.shape[1], t.device
+    rows, cols = t.shape
+    return rows, cols, t.device
 
 
 def _mat(t, rows, cols, dev, what, dtype=None):
@@ -557,11 +561,12 @@ def _params(weight, bias, cols, dev):
 
 def _run(dev, what, fn, *args):
     """One call of the library on the tensors' device and its current stream."""
-    if dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != MX_OK:
         raise MXError(rc, what)
 
