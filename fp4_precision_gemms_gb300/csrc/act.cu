@@ -1,6 +1,8 @@
 // act.cu -- the MLP's activation, forward and backward, and the 8-bit
 // activation checkpoints on their own.
 #include <algorithm>
+#include <cstring>
+#include <type_traits>
 
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
@@ -15,19 +17,29 @@ struct ValueSlope {
     float value, slope;
 };
 
+// 1 / (1 + exp(-z)).  FAST (results that are rounded to bf16): the approximate
+// exponential and reciprocal, whose errors, a few 2^-22 for the arguments that
+// matter and below 2^-16 for all, disappear in the 2^-9 of that rounding.
+template <bool FAST>
+__device__ __forceinline__ float logistic(float z)
+{
+    return FAST ? __fdividef(1.0f, 1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
+}
+
 // a(z) and a'(z).
-template <int ACT>
+template <int ACT, bool FAST>
 __device__ __forceinline__ ValueSlope activate(float z)
 {
     if constexpr (ACT == MX_ACT_SILU) {
-        const float p = 1.0f / (1.0f + expf(-z));
+        const float p = logistic<FAST>(z);
         return {z * p, p + z * p * (1.0f - p)};
     } else if constexpr (ACT == MX_ACT_GELU) {
         const float p = 0.5f * erfcf(z * -0.70710678118654752f);
-        return {z * p, p + z * (0.39894228040143268f * expf(-0.5f * z * z))};
+        const float x = -0.5f * z * z;
+        return {z * p, p + z * (0.39894228040143268f * (FAST ? __expf(x) : expf(x)))};
     } else {  // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t))
         constexpr float k = 0.79788456080286536f;
-        const float zz = z * z, p = 1.0f / (1.0f + expf(-2.0f * k * (z + 0.044715f * z * zz)));
+        const float zz = z * z, p = logistic<FAST>(2.0f * k * (z + 0.044715f * z * zz));
         const float q = p * (1.0f - p);  // 0 where z^2 may have overflowed: the slope is p there
         return {z * p, q == 0.0f ? p : p + z * q * (2.0f * k) * (1.0f + 0.134145f * zz)};
     }
@@ -72,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_any_kernel(ActArgs a)
         const int64_t r = i / G, c = (i - r * G) * kAct8Group + lane;
         const bool in = c < a.cols;
         const float g = in ? load_f(static_cast<const T*>(a.gate) + r * a.ldg + c) : 0.0f;
-        float h = activate<ACT>(g).value, u = 0.0f;
+        float h = activate<ACT, sizeof(T) == 2>(g).value, u = 0.0f;
         if constexpr (GATED) {
             u = in ? load_f(static_cast<const T*>(a.up) + r * a.ldu + c) : 0.0f;
             h *= u;
@@ -104,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_any_kernel(ActArgs a)
             continue;
         const float g = FROM8 ? restored(a.gate8, i, lane) : load_f(static_cast<const T*>(a.gate) + r * a.ldg + c);
         const float dh = load_f(static_cast<const T*>(a.h) + r * a.ldh + c);
-        const ValueSlope f = activate<ACT>(g);
+        const ValueSlope f = activate<ACT, sizeof(T) == 2>(g);
         float dg = dh * f.slope;
         if constexpr (GATED) {
             const float u = FROM8 ? restored(a.up8, i, lane) : load_f(static_cast<const T*>(a.up) + r * a.ldu + c);
@@ -147,6 +159,255 @@ __global__ void __launch_bounds__(kThreads) act8_restore_any_kernel(Act8View a, 
     }
 }
 
+// ------------------------------------------------------------------ wide
+// Rows that start on 16-byte boundaries.  A unit is eight columns of a row, a
+// row has 4 G units (whole groups, so that the four lanes of a group always
+// work together; those past the row's end hold zeros).  Each thread keeps
+// kUnits units' loads in flight; a grid of kCtasPerSm CTAs an SM strides over
+// the units.
+constexpr int kUnits = 2;
+constexpr int kCtasPerSm = 4;
+
+struct UnitMap {
+    FastDiv per_row;
+    uint32_t total;  // < 2^31
+};
+struct Place {
+    int64_t row;
+    uint32_t unit;  // in the row
+    int32_t cols;   // columns of the unit inside the row: 8, fewer at its end, <= 0 past it
+};
+__device__ __forceinline__ Place place(uint32_t i, const UnitMap& m, int64_t cols)
+{
+    const uint32_t r = div_by(i, m.per_row), u = i - r * m.per_row.d;
+    return {r, u, static_cast<int32_t>(min(cols - static_cast<int64_t>(u) * 8, int64_t{8}))};
+}
+
+template <typename T>
+__device__ __forceinline__ void load_unit(RawOct<T>& o, const void* base, int64_t ld, const Place& p)
+{
+    const T* src = static_cast<const T*>(base) + p.row * ld + static_cast<int64_t>(p.unit) * 8;
+    if (p.cols == 8) {
+        o.load(src);
+    } else {  // the row's last columns, one by one
+        T tail[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            tail[c] = c < p.cols ? src[c] : T(0.0f);
+        memcpy(&o, tail, sizeof tail);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& p, Oct& o, uint32_t& top)
+{
+    T* dst = static_cast<T*>(base) + p.row * ld + static_cast<int64_t>(p.unit) * 8;
+    if (p.cols == 8) {
+        store_oct(dst, o, top);
+    } else if (p.cols > 0) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < p.cols) {
+                store_f(dst + c, o.v[c]);
+                fold_top<T>(top, o.v[c]);
+            }
+    }
+}
+
+__device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, bool in, const Oct& o)
+{
+    int e;
+    const uint2 codes = encode_oct(o, e);
+    if (in) {
+        *reinterpret_cast<uint2*>(out.codes + unit * 8) = codes;
+        if ((threadIdx.x & 3) == 0)
+            out.sf[unit >> 2] = static_cast<uint8_t>(e + 127);
+    }
+}
+
+template <typename T, int ACT, bool GATED>
+__global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
+{
+    uint32_t top = 0;
+    for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
+        RawOct<T> g[kUnits], u[kUnits];
+        Place p[kUnits];
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const uint32_t i = base + k * kThreads + threadIdx.x;
+            p[k] = place(i, m, a.cols);
+            if (i >= m.total)
+                p[k].cols = 0;
+            load_unit(g[k], a.gate, a.ldg, p[k]);
+            if constexpr (GATED)
+                load_unit(u[k], a.up, a.ldu, p[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const uint32_t i = base + k * kThreads + threadIdx.x;
+            Oct gv, uv, h;
+            g[k].get(gv);
+            if constexpr (GATED)
+                u[k].get(uv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h.v[j] = activate<ACT, sizeof(T) == 2>(gv.v[j]).value;
+                if constexpr (GATED)
+                    h.v[j] *= uv.v[j];
+            }
+            store_unit<T>(a.h, a.ldh, p[k], h, top);
+            if (a.gate8.codes)
+                save_unit(a.gate8, i, i < m.total, gv);
+            if constexpr (GATED)
+                if (a.up8.codes)
+                    save_unit(a.up8, i, i < m.total, uv);
+        }
+    }
+    if (a.amax)
+        flush_amax(a.amax, oct_top<T>(top));
+}
+
+template <typename T, int ACT, bool GATED, bool FROM8>
+__global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
+{
+    using Raw = std::conditional_t<FROM8, RawCodes, RawOct<T>>;
+    uint32_t top = 0;
+    for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
+        Raw g[kUnits], u[kUnits];
+        RawOct<T> d[kUnits];
+        Place p[kUnits];
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const uint32_t i = base + k * kThreads + threadIdx.x;
+            p[k] = place(i, m, a.cols);
+            if (i >= m.total)
+                p[k].cols = 0;
+            load_unit(d[k], a.h, a.ldh, p[k]);
+            if constexpr (FROM8) {
+                g[k].clear();
+                u[k].clear();
+                if (p[k].cols > 0) {
+                    g[k].load(a.gate8, i);
+                    if constexpr (GATED)
+                        u[k].load(a.up8, i);
+                }
+            } else {
+                load_unit(g[k], a.gate, a.ldg, p[k]);
+                if constexpr (GATED)
+                    load_unit(u[k], a.up, a.ldu, p[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            Oct gv, uv, dv, dg;
+            d[k].get(dv);
+            g[k].get(gv);
+            if constexpr (GATED)
+                u[k].get(uv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const ValueSlope f = activate<ACT, sizeof(T) == 2>(gv.v[j]);
+                dg.v[j] = dv.v[j] * f.slope;
+                if constexpr (GATED) {
+                    dg.v[j] *= uv.v[j];
+                    dv.v[j] *= f.value;
+                }
+            }
+            store_unit<T>(a.dgate, a.lddg, p[k], dg, top);
+            if constexpr (GATED)
+                store_unit<T>(a.dup, a.lddu, p[k], dv, top);
+        }
+    }
+    if (a.amax)
+        flush_amax(a.amax, oct_top<T>(top));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) act8_save_kernel(const void* __restrict__ x, int64_t ldx, int64_t cols,
+                                                             Act8View out, UnitMap m)
+{
+    for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
+        RawOct<T> w[kUnits];
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const uint32_t i = base + k * kThreads + threadIdx.x;
+            Place p = place(i, m, cols);
+            if (i >= m.total)
+                p.cols = 0;
+            load_unit(w[k], x, ldx, p);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const uint32_t i = base + k * kThreads + threadIdx.x;
+            Oct v;
+            w[k].get(v);
+            save_unit(out, i, i < m.total, v);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View a, int64_t cols, void* __restrict__ out,
+                                                                int64_t ldo, UnitMap m)
+{
+    uint32_t unused = 0;
+    for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
+        RawCodes w[kUnits];
+        Place p[kUnits];
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            const uint32_t i = base + k * kThreads + threadIdx.x;
+            p[k] = place(i, m, cols);
+            if (i >= m.total)
+                p[k].cols = 0;
+            w[k].clear();
+            if (p[k].cols > 0)
+                w[k].load(a, i);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+            Oct v;
+            w[k].get(v);
+            store_unit<T>(out, ldo, p[k], v, unused);
+        }
+    }
+}
+
+// Rows that a launch of the wide kernels can take (its unit count is 31 bits).
+int64_t slab_rows(int64_t cols) { return std::max<int64_t>(1, ((int64_t{1} << 31) - (1 << 22)) / (act8_groups(cols) * 4)); }
+UnitMap unit_map(int64_t rows, int64_t cols)
+{
+    const int64_t per_row = act8_groups(cols) * 4;
+    return {fast_div(static_cast<uint32_t>(per_row)), static_cast<uint32_t>(rows * per_row)};
+}
+unsigned unit_grid(const UnitMap& m, const Device& d)
+{
+    const int64_t ctas = (m.total + int64_t{kThreads} * kUnits - 1) / (kThreads * kUnits);
+    return static_cast<unsigned>(std::min<int64_t>(ctas, d.sms * kCtasPerSm));
+}
+
+// Whether every row of a matrix starts on a 16-byte boundary.
+bool wide(const void* p, int64_t ld, int dtype)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * (dtype == MX_OUT_BF16 ? 2 : 4)) % 16 == 0;
+}
+
+// p moved on by `rows` rows of a matrix (null stays null).
+template <typename P>
+P* ahead(P* p, int64_t rows, int64_t ld, int dtype)
+{
+    using B = std::conditional_t<std::is_const_v<P>, const char, char>;
+    return p ? static_cast<P*>(static_cast<B*>(p) + rows * ld * (dtype == MX_OUT_BF16 ? 2 : 4)) : p;
+}
+Act8View ahead(Act8View v, int64_t rows, int64_t cols)
+{
+    if (v.codes) {
+        v.codes += rows * act8_groups(cols) * kAct8Group;
+        v.sf += rows * act8_groups(cols);
+    }
+    return v;
+}
+
 unsigned any_grid(int64_t rows, int64_t cols, const Device& d)
 {
     const int64_t ctas = (rows * act8_groups(cols) + kWarps - 1) / kWarps;
@@ -162,23 +423,101 @@ int launched()
 template <typename T, int ACT>
 int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
 {
-    const unsigned grid = any_grid(a.rows, a.cols, d);
-    if (a.gated)
-        act_fwd_any_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
-    else
-        act_fwd_any_kernel<T, ACT, false><<<grid, kThreads, 0, s>>>(a);
-    return launched();
+    if (!wide(a.gate, a.ldg, a.dtype) || !wide(a.h, a.ldh, a.dtype) || !wide(a.up, a.ldu, a.dtype)) {
+        const unsigned grid = any_grid(a.rows, a.cols, d);
+        if (a.gated)
+            act_fwd_any_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
+        else
+            act_fwd_any_kernel<T, ACT, false><<<grid, kThreads, 0, s>>>(a);
+        return launched();
+    }
+    const int64_t slab = slab_rows(a.cols);
+    for (int64_t r = 0; r < a.rows; r += slab) {
+        ActArgs b = a;
+        b.rows = std::min(slab, a.rows - r);
+        b.gate = ahead(a.gate, r, a.ldg, a.dtype);
+        b.up = ahead(a.up, r, a.ldu, a.dtype);
+        b.h = ahead(a.h, r, a.ldh, a.dtype);
+        b.gate8 = ahead(a.gate8, r, a.cols);
+        b.up8 = ahead(a.up8, r, a.cols);
+        const UnitMap m = unit_map(b.rows, a.cols);
+        if (a.gated)
+            act_fwd_kernel<T, ACT, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        else
+            act_fwd_kernel<T, ACT, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        if (launched() != MX_OK)
+            return MX_ERR_CUDA;
+    }
+    return MX_OK;
 }
 
 template <typename T, int ACT, bool FROM8>
 int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
 {
-    const unsigned grid = any_grid(a.rows, a.cols, d);
-    if (a.gated)
-        act_bwd_any_kernel<T, ACT, true, FROM8><<<grid, kThreads, 0, s>>>(a);
-    else
-        act_bwd_any_kernel<T, ACT, false, FROM8><<<grid, kThreads, 0, s>>>(a);
-    return launched();
+    if (!wide(a.h, a.ldh, a.dtype) || !wide(a.dgate, a.lddg, a.dtype) || !wide(a.dup, a.lddu, a.dtype) ||
+        !wide(a.gate, a.ldg, a.dtype) || !wide(a.up, a.ldu, a.dtype)) {
+        const unsigned grid = any_grid(a.rows, a.cols, d);
+        if (a.gated)
+            act_bwd_any_kernel<T, ACT, true, FROM8><<<grid, kThreads, 0, s>>>(a);
+        else
+            act_bwd_any_kernel<T, ACT, false, FROM8><<<grid, kThreads, 0, s>>>(a);
+        return launched();
+    }
+    const int64_t slab = slab_rows(a.cols);
+    for (int64_t r = 0; r < a.rows; r += slab) {
+        ActArgs b = a;
+        b.rows = std::min(slab, a.rows - r);
+        b.gate = ahead(a.gate, r, a.ldg, a.dtype);
+        b.up = ahead(a.up, r, a.ldu, a.dtype);
+        b.h = ahead(a.h, r, a.ldh, a.dtype);
+        b.dgate = ahead(a.dgate, r, a.lddg, a.dtype);
+        b.dup = ahead(a.dup, r, a.lddu, a.dtype);
+        b.gate8 = ahead(a.gate8, r, a.cols);
+        b.up8 = ahead(a.up8, r, a.cols);
+        const UnitMap m = unit_map(b.rows, a.cols);
+        if (a.gated)
+            act_bwd_kernel<T, ACT, true, FROM8><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        else
+            act_bwd_kernel<T, ACT, false, FROM8><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        if (launched() != MX_OK)
+            return MX_ERR_CUDA;
+    }
+    return MX_OK;
+}
+
+template <typename T>
+int save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8View out, const Device& d,
+         cudaStream_t s)
+{
+    if (!wide(x, ldx, dtype)) {
+        act8_save_any_kernel<<<any_grid(rows, cols, d), kThreads, 0, s>>>(static_cast<const T*>(x), ldx, rows, cols, out);
+        return launched();
+    }
+    const int64_t slab = slab_rows(cols);
+    for (int64_t r = 0; r < rows; r += slab) {
+        const UnitMap m = unit_map(std::min(slab, rows - r), cols);
+        act8_save_kernel<T><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(x, r, ldx, dtype), ldx, cols, ahead(out, r, cols), m);
+        if (launched() != MX_OK)
+            return MX_ERR_CUDA;
+    }
+    return MX_OK;
+}
+
+template <typename T>
+int restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int dtype, const Device& d, cudaStream_t s)
+{
+    if (!wide(out, ldo, dtype)) {
+        act8_restore_any_kernel<<<any_grid(rows, cols, d), kThreads, 0, s>>>(a, rows, cols, static_cast<T*>(out), ldo);
+        return launched();
+    }
+    const int64_t slab = slab_rows(cols);
+    for (int64_t r = 0; r < rows; r += slab) {
+        const UnitMap m = unit_map(std::min(slab, rows - r), cols);
+        act8_restore_kernel<T><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(a, r, cols), cols, ahead(out, r, ldo, dtype), ldo, m);
+        if (launched() != MX_OK)
+            return MX_ERR_CUDA;
+    }
+    return MX_OK;
 }
 
 template <typename T>
@@ -218,23 +557,15 @@ int launch_act_bwd(const ActArgs& a, const Device& d, cudaStream_t s)
 int launch_act8_save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8View out, const Device& d,
                      cudaStream_t s)
 {
-    const unsigned grid = any_grid(rows, cols, d);
-    if (dtype == MX_OUT_BF16)
-        act8_save_any_kernel<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, cols, out);
-    else
-        act8_save_any_kernel<<<grid, kThreads, 0, s>>>(static_cast<const float*>(x), ldx, rows, cols, out);
-    return launched();
+    return dtype == MX_OUT_BF16 ? save<__nv_bfloat16>(x, ldx, dtype, rows, cols, out, d, s)
+                                : save<float>(x, ldx, dtype, rows, cols, out, d, s);
 }
 
 int launch_act8_restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int dtype, const Device& d,
                         cudaStream_t s)
 {
-    const unsigned grid = any_grid(rows, cols, d);
-    if (dtype == MX_OUT_BF16)
-        act8_restore_any_kernel<<<grid, kThreads, 0, s>>>(a, rows, cols, static_cast<__nv_bfloat16*>(out), ldo);
-    else
-        act8_restore_any_kernel<<<grid, kThreads, 0, s>>>(a, rows, cols, static_cast<float*>(out), ldo);
-    return launched();
+    return dtype == MX_OUT_BF16 ? restore<__nv_bfloat16>(a, rows, cols, out, ldo, dtype, d, s)
+                                : restore<float>(a, rows, cols, out, ldo, dtype, d, s);
 }
 
 }  // namespace mx
