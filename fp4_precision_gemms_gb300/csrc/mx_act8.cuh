@@ -128,6 +128,13 @@ struct RawOct<float> {
         o.v[4] = b.x, o.v[5] = b.y, o.v[6] = b.z, o.v[7] = b.w;
     }
 };
+__device__ __forceinline__ void decode_oct(uint2 w, float s, Oct& o)
+{
+    const float2 p = dec_e4m3x2(w.x & 0xFFFFu), q = dec_e4m3x2(w.x >> 16);
+    const float2 t = dec_e4m3x2(w.y & 0xFFFFu), u = dec_e4m3x2(w.y >> 16);
+    o.v[0] = p.x * s, o.v[1] = p.y * s, o.v[2] = q.x * s, o.v[3] = q.y * s;
+    o.v[4] = t.x * s, o.v[5] = t.y * s, o.v[6] = u.x * s, o.v[7] = u.y * s;
+}
 // Eight checkpoint codes and their group's exponent byte.
 struct RawCodes {
     uint2 w;
@@ -138,15 +145,30 @@ struct RawCodes {
         e = a.sf[unit >> 2];
     }
     __device__ __forceinline__ void clear() { w = make_uint2(0, 0), e = 127; }
-    __device__ __forceinline__ void get(Oct& o) const
-    {
-        const float s = act8_scale(e);
-        const float2 p = dec_e4m3x2(w.x & 0xFFFFu), q = dec_e4m3x2(w.x >> 16);
-        const float2 t = dec_e4m3x2(w.y & 0xFFFFu), u = dec_e4m3x2(w.y >> 16);
-        o.v[0] = p.x * s, o.v[1] = p.y * s, o.v[2] = q.x * s, o.v[3] = q.y * s;
-        o.v[4] = t.x * s, o.v[5] = t.y * s, o.v[6] = u.x * s, o.v[7] = u.y * s;
-    }
+    __device__ __forceinline__ void get(Oct& o) const { decode_oct(w, act8_scale(e), o); }
 };
+
+// Asynchronous copies into a thread's own shared-memory words: no other thread
+// reads them, so the thread's own wait is all the synchronisation they need.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `pending` (0, 1 or 2) groups have arrived.
+__device__ __forceinline__ void copy_wait(int pending)
+{
+    if (pending == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (pending == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
 
 // Writes an oct rounded to its type and folds |written values| into `top`:
 // packed bf16 maxima (finish with oct_top), or fp32 bits.

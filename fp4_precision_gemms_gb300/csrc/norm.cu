@@ -4,6 +4,7 @@
 
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
+#include "mx_ptx.cuh"
 
 namespace mx {
 namespace {
@@ -211,9 +212,571 @@ __global__ void __launch_bounds__(kRowThreads) norm_dw_join_kernel(const float* 
     }
 }
 
+// ------------------------------------------------------------------ wide
+// Rows on 16-byte boundaries, cols % 8 == 0, cols <= 16384.  Eight columns
+// (an oct) at a time: thread t of a row's TPR threads owns the octs t, t + TPR,
+// ..., NV of them; octs past the row's end hold zeros, and a group's four octs
+// lie in four neighbouring lanes.  LPR > 0: LPR lanes of a warp per row, the
+// rows of a CTA independent; LPR = 0: the CTA's blockDim.x threads per row.
+//
+// The grid is persistent, and each thread copies its own words of the rows that
+// its CTA takes next into its own slots of a shared-memory ring (`stages` rows
+// deep): the memory system stays busy through the row sums, without a barrier
+// for the ring.
+constexpr int kMaxWide = 16384;
+constexpr int kSubThreads = 256;  // CTA size where several rows share a CTA
+
+template <typename T>
+__device__ __forceinline__ constexpr int chunks() { return sizeof(T) / 2; }  // 16-byte words of an oct
+
+template <int LPR>
+struct RowMap {
+    int tpr, sub, t;
+    int64_t first, step;
+    __device__ __forceinline__ RowMap()
+    {
+        const int tid = threadIdx.x;
+        tpr = LPR ? LPR : blockDim.x;
+        sub = LPR ? tid / LPR : 0;
+        t = LPR ? tid % LPR : tid;
+        const int rows_per_cta = LPR ? kSubThreads / LPR : 1;
+        first = static_cast<int64_t>(blockIdx.x) * rows_per_cta;
+        step = static_cast<int64_t>(gridDim.x) * rows_per_cta;
+    }
+};
+
+// Sums over a row's threads, known to all of them; a CTA's row goes through
+// `part` (32 entries, zero past the CTA's warps; two of them used in turn, so
+// that one barrier per sum is enough).
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float* part)
+{
+#pragma unroll
+    for (int o = (LPR ? LPR : 32) / 2; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if constexpr (LPR == 0) {
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.0f;
+        for (unsigned w = 0; w < blockDim.x / 32; w += 4) {
+            const float4 p = *reinterpret_cast<const float4*>(part + w);
+            v += (p.x + p.y) + (p.z + p.w);
+        }
+    }
+    return v;
+}
+template <int LPR>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* part)
+{
+#pragma unroll
+    for (int o = (LPR ? LPR : 32) / 2; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+    }
+    if constexpr (LPR == 0) {
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = make_float2(0.0f, 0.0f);
+        for (unsigned w = 0; w < blockDim.x / 32; w += 2) {
+            const float4 p = *reinterpret_cast<const float4*>(part + w);
+            v.x += p.x + p.z;
+            v.y += p.y + p.w;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float absent, Oct& o)
+{
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o.v[i] = absent;
+    } else if (dtype == MX_OUT_BF16) {
+        unpack_oct(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), o);
+    } else {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
+        o.v[0] = a.x, o.v[1] = a.y, o.v[2] = a.z, o.v[3] = a.w;
+        o.v[4] = b.x, o.v[5] = b.y, o.v[6] = b.z, o.v[7] = b.w;
+    }
+}
+
+// A thread's slots of one matrix in a ring stage: 16-byte words, a word's slots
+// of all threads side by side.
+template <typename T>
+__device__ __forceinline__ void slot_fill(uint32_t slots, int j, const T* src)
+{
+#pragma unroll
+    for (int h = 0; h < chunks<T>(); ++h)
+        copy_async16(slots + ((j * chunks<T>() + h) * blockDim.x + threadIdx.x) * 16, src + h * (16 / sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ void slot_read(uint32_t slots, int j, Oct& o)
+{
+    if constexpr (sizeof(T) == 2) {
+        unpack_oct(lds128(slots + (j * blockDim.x + threadIdx.x) * 16), o);
+    } else {
+        const uint4 a = lds128(slots + (2 * j * blockDim.x + threadIdx.x) * 16);
+        const uint4 b = lds128(slots + ((2 * j + 1) * blockDim.x + threadIdx.x) * 16);
+        o.v[0] = __uint_as_float(a.x), o.v[1] = __uint_as_float(a.y), o.v[2] = __uint_as_float(a.z);
+        o.v[3] = __uint_as_float(a.w), o.v[4] = __uint_as_float(b.x), o.v[5] = __uint_as_float(b.y);
+        o.v[6] = __uint_as_float(b.z), o.v[7] = __uint_as_float(b.w);
+    }
+}
+
+template <typename T, typename TY, int LPR, int NV>
+__global__ void __launch_bounds__(LPR ? kSubThreads : 1024) norm_fwd_kernel(NormFwdArgs a, int stages)
+{
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ __align__(16) float part[2][32];
+    if (LPR == 0 && threadIdx.x < 64)
+        part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
+    if (LPR == 0)
+        __syncthreads();
+    const RowMap<LPR> map;
+    const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
+    const float inv_c = 1.0f / static_cast<float>(C);
+    const uint32_t slots = smem_u32(ring);
+    const uint32_t one = NV * chunks<T>() * blockDim.x * 16;  // bytes of one matrix in a stage
+    const uint32_t stage_bytes = a.residual ? 2 * one : one;
+
+    auto fill = [&](int64_t r, int stage) {
+        if (r < a.rows) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = 8 * (map.t + map.tpr * j);
+                if (c < C) {
+                    slot_fill(slots + stage * stage_bytes, j, static_cast<const T*>(a.x) + r * a.ldx + c);
+                    if (a.residual)
+                        slot_fill(slots + stage * stage_bytes + one, j, static_cast<const T*>(a.residual) + r * a.ldr + c);
+                }
+            }
+        }
+        copy_commit();
+    };
+
+    uint32_t top = 0, sum_top = 0;
+    for (int i = 0; i < stages - 1; ++i)
+        fill(map.first + map.sub + i * map.step, i);
+    int stage = 0, odd = 0;
+    for (int64_t rb = map.first; rb < a.rows; rb += map.step, odd ^= 1) {
+        const int64_t r = rb + map.sub;
+        fill(r + (stages - 1) * map.step, stage == 0 ? stages - 1 : stage - 1);  // the slots read a row ago
+        copy_wait(stages - 1);
+        const uint32_t here = slots + stage * stage_bytes;
+        Oct v[NV];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = 8 * (map.t + map.tpr * j);
+            if (c < C && r < a.rows) {
+                slot_read<T>(here, j, v[j]);
+                if (a.residual) {
+                    Oct q;
+                    slot_read<T>(here + one, j, q);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[j].v[i] = as_stored<T>(v[j].v[i] + q.v[i]);
+                    store_oct(static_cast<T*>(a.sum_out) + r * a.lds + c, v[j], sum_top);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sum += v[j].v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[j].v[i] = 0.0f;
+            }
+        }
+        const float mean = a.kind == MX_NORM_LAYER ? row_sum<LPR>(sum, part[0]) * inv_c : 0.0f;
+        float sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (8 * (map.t + map.tpr * j) < C)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = v[j].v[i] - mean;
+                    sq += d * d;
+                }
+        // RMS norm has one sum per row: its words alternate with the row
+        float* const words = part[a.kind == MX_NORM_LAYER ? 1 : odd];
+        const float rstd = 1.0f / sqrtf(row_sum<LPR>(sq, words) * inv_c + a.eps);
+        if (map.t == 0 && r < a.rows) {
+            if (a.mean && a.kind == MX_NORM_LAYER)
+                a.mean[r] = mean;
+            if (a.rstd)
+                a.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = 8 * (map.t + map.tpr * j);
+            if (c < C && r < a.rows) {
+                Oct w, b;
+                param_oct(a.weight, a.w_dtype, c, 1.0f, w);
+                param_oct(a.bias, a.w_dtype, c, 0.0f, b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    b.v[i] = (v[j].v[i] - mean) * rstd * w.v[i] + b.v[i];
+                store_oct(static_cast<TY*>(a.y) + r * a.ldy + c, b, top);
+            }
+            if (a.save.codes) {
+                int e;
+                const uint2 codes = encode_oct(v[j], e);
+                if (c < G * kAct8Group && r < a.rows) {
+                    *reinterpret_cast<uint2*>(a.save.codes + r * G * kAct8Group + c) = codes;
+                    if ((threadIdx.x & 3) == 0)
+                        a.save.sf[r * G + c / kAct8Group] = static_cast<uint8_t>(e + 127);
+                }
+            }
+        }
+        stage = stage + 1 == stages ? 0 : stage + 1;
+    }
+    if (a.amax) {
+        top = __reduce_max_sync(0xFFFFFFFFu, oct_top<TY>(top));
+        if ((threadIdx.x & 31) == 0)
+            atomicMax(a.amax, top);
+    }
+}
+
+// dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
+// is the checkpoint.  The column sums stay in registers over all rows of the
+// CTA; dy h and g h come from one reading of the row, dx from a second one out
+// of shared memory (out of registers where a thread has one oct).
+template <typename T, typename TY, bool FROM8, int LPR, int NV>
+__global__ void __launch_bounds__(LPR ? kSubThreads : 1024) norm_bwd_kernel(NormBwdArgs a, int stages)
+{
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ __align__(16) float2 part[2][32];
+    if (LPR == 0 && threadIdx.x < 64)
+        part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.0f, 0.0f);
+    if (LPR == 0)
+        __syncthreads();
+    const RowMap<LPR> map;
+    const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
+    const float inv_c = 1.0f / static_cast<float>(C);
+    const bool layer = a.kind == MX_NORM_LAYER;
+    const uint32_t slots = smem_u32(ring);
+    const uint32_t at_s = NV * chunks<TY>() * blockDim.x * 16;
+    const uint32_t at_r = at_s + (FROM8 ? NV * blockDim.x * 8 : NV * chunks<T>() * blockDim.x * 16);
+    const uint32_t stage_bytes = a.dres ? at_r + NV * chunks<T>() * blockDim.x * 16 : at_r;
+
+    auto fill = [&](int64_t r, int stage) {
+        if (r < a.rows) {
+            const uint32_t here = slots + stage * stage_bytes;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = 8 * (map.t + map.tpr * j);
+                if (c < C) {
+                    slot_fill(here, j, static_cast<const TY*>(a.dy) + r * a.ldy + c);
+                    if constexpr (FROM8)
+                        copy_async8(here + at_s + (j * blockDim.x + threadIdx.x) * 8, a.x8.codes + r * G * kAct8Group + c);
+                    else
+                        slot_fill(here + at_s, j, static_cast<const T*>(a.x) + r * a.ldx + c);
+                    if (a.dres)
+                        slot_fill(here + at_r, j, static_cast<const T*>(a.dres) + r * a.ldres + c);
+                }
+            }
+        }
+        copy_commit();
+    };
+    struct RowWords {  // what a row needs beside its matrices, loaded a row ahead
+        float mean, rstd;
+        uint32_t e[NV];
+    };
+    auto row_words = [&](int64_t r) {
+        RowWords w;
+        const bool in = r < a.rows;
+        w.mean = in && layer ? a.mean[r] : 0.0f;
+        w.rstd = in ? a.rstd[r] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = 8 * (map.t + map.tpr * j);
+            w.e[j] = FROM8 && in && c < C ? a.x8.sf[r * G + c / kAct8Group] : 127u;
+        }
+        return w;
+    };
+
+    float dw[NV][8], db[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dw[j][i] = db[j][i] = 0.0f;
+    uint32_t top = 0;
+    for (int i = 0; i < stages - 1; ++i)
+        fill(map.first + map.sub + i * map.step, i);
+    RowWords next = row_words(map.first + map.sub);
+    int stage = 0, odd = 0;
+    for (int64_t rb = map.first; rb < a.rows; rb += map.step, odd ^= 1) {
+        const int64_t r = rb + map.sub;
+        const RowWords cur = next;
+        next = row_words(r + map.step);
+        fill(r + (stages - 1) * map.step, stage == 0 ? stages - 1 : stage - 1);
+        copy_wait(stages - 1);
+        const uint32_t here = slots + stage * stage_bytes;
+        // g and h of oct j
+        auto load = [&](int j, int c, Oct& dy, Oct& g, Oct& h) {
+            slot_read<TY>(here, j, dy);
+            if constexpr (FROM8) {
+                uint2 w;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(w.x), "=r"(w.y)
+                             : "r"(here + at_s + (j * blockDim.x + threadIdx.x) * 8)
+                             : "memory");
+                decode_oct(w, act8_scale(cur.e[j]), h);
+            } else {
+                slot_read<T>(here + at_s, j, h);
+            }
+            param_oct(a.weight, a.w_dtype, c, 1.0f, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h.v[i] = (h.v[i] - cur.mean) * cur.rstd;
+                g.v[i] *= dy.v[i];
+            }
+        };
+        Oct kg, kh;  // NV == 1: kept for the second pass
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = 8 * (map.t + map.tpr * j);
+            if (c < C && r < a.rows) {
+                Oct dy;
+                load(j, c, dy, kg, kh);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s.x += kg.v[i] * kh.v[i];
+                    s.y += kg.v[i];
+                    dw[j][i] += dy.v[i] * kh.v[i];
+                    db[j][i] += dy.v[i];
+                }
+            }
+        }
+        s = row_sum2<LPR>(s, part[odd]);
+        const float c1 = s.x * inv_c, c2 = layer ? s.y * inv_c : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = 8 * (map.t + map.tpr * j);
+            if (c < C && r < a.rows) {
+                if constexpr (NV > 1) {
+                    Oct dy;
+                    load(j, c, dy, kg, kh);
+                }
+                Oct q;
+                if (a.dres) {
+                    slot_read<T>(here + at_r, j, q);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        q.v[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q.v[i] += (kg.v[i] - kh.v[i] * c1 - c2) * cur.rstd;
+                store_oct(static_cast<T*>(a.dx) + r * a.lddx + c, q, top);
+            }
+        }
+        stage = stage + 1 == stages ? 0 : stage + 1;
+    }
+    if (a.amax) {
+        top = __reduce_max_sync(0xFFFFFFFFu, oct_top<T>(top));
+        if ((threadIdx.x & 31) == 0)
+            atomicMax(a.amax, top);
+    }
+    if (!a.dw && !a.db)
+        return;
+    float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C;
+    const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
+    if constexpr (LPR == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = 8 * (map.t + map.tpr * j);
+            if (c < C) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    *reinterpret_cast<float4*>(out + c + i) = make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
+                    *reinterpret_cast<float4*>(out + to_db + c + i) =
+                        make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
+                }
+            }
+        }
+    } else {
+        // the rows of a warp, then the warps through shared memory, in order
+        constexpr int kWarpCols = NV * LPR * 8;
+        float* const red = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int o = LPR; o < 32; o <<= 1) {
+                    dw[j][i] += __shfl_xor_sync(0xFFFFFFFFu, dw[j][i], o);
+                    db[j][i] += __shfl_xor_sync(0xFFFFFFFFu, db[j][i], o);
+                }
+        copy_wait(0);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+            if ((threadIdx.x & 31) < LPR)
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        red[(threadIdx.x >> 5) * kWarpCols + (j * 8 + i) * LPR + map.t] = which ? db[j][i] : dw[j][i];
+            __syncthreads();
+            for (int k = threadIdx.x; k < kWarpCols; k += kSubThreads) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kSubThreads / 32; ++w)
+                    v += red[w * kWarpCols + k];
+                const int t = k % LPR, ji = k / LPR, c = 8 * (t + LPR * (ji / 8)) + ji % 8;
+                if (c < C)
+                    out[which * to_db + c] = v;
+            }
+        }
+    }
+}
+
+// How a width is spread over threads: octs of whole groups, so that a group's
+// four lanes all exist.
+struct WideShape {
+    int lpr, nv, threads;
+};
+WideShape fwd_shape(int64_t cols)
+{
+    const int octs = static_cast<int>(act8_groups(cols)) * 4;
+    if (octs <= 8)
+        return {8, 1, kSubThreads};
+    if (octs <= 16)
+        return {16, 1, kSubThreads};
+    if (octs <= 128)
+        return {32, octs <= 32 ? 1 : octs <= 64 ? 2 : 4, kSubThreads};
+    return {0, 2, ((octs + 1) / 2 + 31) / 32 * 32};
+}
+// One oct a thread as long as a CTA's threads suffice: the column sums take 16
+// registers for each.
+WideShape bwd_shape(int64_t cols)
+{
+    const WideShape f = fwd_shape(cols);
+    if (f.lpr)
+        return f;
+    const int octs = static_cast<int>(act8_groups(cols)) * 4;
+    const int nv = octs <= 1024 ? 1 : 2;
+    return {0, nv, ((octs + nv - 1) / nv + 31) / 32 * 32};
+}
+
+constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
+// Rows in flight of a CTA and CTAs of an SM, from the bytes of one row's slots:
+// three stages where they fit.
+struct RingPlan {
+    int stages, per_sm;
+};
+RingPlan ring_plan(int64_t stage_bytes, int threads, int most)
+{
+    RingPlan p;
+    p.per_sm = std::max(1, std::min<int>(most, 1024 / threads));
+    while (p.per_sm > 1 && p.per_sm * 3 * stage_bytes > kRingBytes)
+        --p.per_sm;
+    p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, kRingBytes / (p.per_sm * stage_bytes))));
+    return p;
+}
+
+bool wide_rows(const void* p, int64_t ld, int bytes)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * bytes) % 16 == 0;
+}
+bool wide_cols(int64_t cols) { return cols % 8 == 0 && cols <= kMaxWide; }
+
+template <typename K, typename A>
+int launch_ring(K kernel, const A& a, unsigned grid, int threads, int stages, size_t smem, cudaStream_t s)
+{
+    if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
+       
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return MX_ERR_CUDA;
+    kernel<<<grid, threads, smem, s>>>(a, stages);
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+template <typename T, typename TY>
+int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+{
+    const WideShape w = fwd_shape(a.cols);
+    const int64_t bytes = static_cast<int64_t>(w.nv) * w.threads * 8 * sizeof(T) * (a.residual ? 2 : 1);
+    const RingPlan p = ring_plan(bytes, w.threads, 16);
+    const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a.rows + per_cta - 1) / per_cta, int64_t{d.sms} * p.per_sm));
+    const size_t smem = static_cast<size_t>(bytes) * p.stages;
+    if (w.lpr == 8)
+        return launch_ring(norm_fwd_kernel<T, TY, 8, 1>, a, grid, w.threads, p.stages, smem, s);
+    if (w.lpr == 16)
+        return launch_ring(norm_fwd_kernel<T, TY, 16, 1>, a, grid, w.threads, p.stages, smem, s);
+    if (w.lpr == 32 && w.nv == 1)
+        return launch_ring(norm_fwd_kernel<T, TY, 32, 1>, a, grid, w.threads, p.stages, smem, s);
+    if (w.lpr == 32 && w.nv == 2)
+        return launch_ring(norm_fwd_kernel<T, TY, 32, 2>, a, grid, w.threads, p.stages, smem, s);
+    if (w.lpr == 32)
+        return launch_ring(norm_fwd_kernel<T, TY, 32, 4>, a, grid, w.threads, p.stages, smem, s);
+    return launch_ring(norm_fwd_kernel<T, TY, 0, 2>, a, grid, w.threads, p.stages, smem, s);
+}
+
+// CTAs of the backward kernel, each with its partial sums: at most four an SM
+// (152 SMs).  A pure function of the shape: the workspace is sized by it.
+constexpr int kPartSms = 152;
+int64_t bwd_ctas(int64_t rows, int64_t cols)
+{
+    const WideShape w = bwd_shape(cols);
+    const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
+    const int64_t per_sm = w.lpr ? 2 : std::max(1, std::min(4, 1024 / w.threads));
+    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * per_sm);
+}
+
+template <typename T, typename TY, bool FROM8>
+int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
+{
+    const WideShape w = bwd_shape(a.cols);
+    const int64_t oct = static_cast<int64_t>(w.nv) * w.threads * 8;
+    const int64_t bytes = oct * (sizeof(TY) + (FROM8 ? 1 : sizeof(T)) + (a.dres ? sizeof(T) : 0));
+    const RingPlan p = ring_plan(bytes, w.threads, w.lpr ? 2 : 4);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(bwd_ctas(a.rows, a.cols), int64_t{d.sms} * p.per_sm));
+    // the column sums of a warp-per-row CTA pass through the ring's memory
+    const size_t smem = std::max<size_t>(static_cast<size_t>(bytes) * p.stages, w.lpr ? w.nv * w.lpr * 8 * 4 * (w.threads / 32) : 0);
+    int rc;
+    if (w.lpr == 8)
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 8, 1>, a, grid, w.threads, p.stages, smem, s);
+    else if (w.lpr == 16)
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 16, 1>, a, grid, w.threads, p.stages, smem, s);
+    else if (w.lpr == 32 && w.nv == 1)
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 1>, a, grid, w.threads, p.stages, smem, s);
+    else if (w.lpr == 32 && w.nv == 2)
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 2>, a, grid, w.threads, p.stages, smem, s);
+    else if (w.lpr == 32)
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 4>, a, grid, w.threads, p.stages, smem, s);
+    else if (w.nv == 1)
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 1>, a, grid, w.threads, p.stages, smem, s);
+    else
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 2>, a, grid, w.threads, p.stages, smem, s);
+    if (rc != MX_OK || (!a.dw && !a.db))
+        return rc;
+    norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kRowThreads, 0, s>>>(
+        a.parts, a.cols, static_cast<int>(grid), a.dw, a.db);
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+int64_t any_parts(int64_t rows) { return std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, 64); }
+
 template <typename T, typename TY>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
+    const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
+    if (wide_cols(a.cols) && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
+        wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) && wide_rows(a.weight, 8, wb) &&
+        wide_rows(a.bias, 8, wb))
+        return fwd_wide<T, TY>(a, d, s);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
     norm_fwd_any_kernel<T, TY><<<grid, kRowThreads, 0, s>>>(a);
     count_launch();
@@ -223,8 +786,12 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 template <typename T, typename TY>
 int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
+    const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
+    if (wide_cols(a.cols) && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
+        wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) && wide_rows(a.weight, 8, wb))
+        return a.x8.codes ? bwd_wide<T, TY, true>(a, d, s) : bwd_wide<T, TY, false>(a, d, s);
     if (a.dw || a.db) {  // before dx, which may be dy's memory
-        const int parts = static_cast<int>(norm_bwd_parts(a.rows, a.cols));
+        const int parts = static_cast<int>(any_parts(a.rows));
         const unsigned cols32 = static_cast<unsigned>((a.cols + 31) / 32);
         norm_dw_any_kernel<T, TY><<<dim3(cols32, parts), kRowThreads, 0, s>>>(a);
         norm_dw_join_kernel<<<dim3(cols32, 2), kRowThreads, 0, s>>>(a.parts, a.cols, parts, a.dw, a.db);
@@ -241,8 +808,7 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 
 int64_t norm_bwd_parts(int64_t rows, int64_t cols)
 {
-    (void)cols;
-    return std::max<int64_t>(1, std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, 64));
+    return std::max(any_parts(rows), wide_cols(cols) ? bwd_ctas(rows, cols) : int64_t{1});
 }
 
 int launch_norm_fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
