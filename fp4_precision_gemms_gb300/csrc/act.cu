@@ -45,13 +45,6 @@ __device__ __forceinline__ ValueSlope activate(float z)
     }
 }
 
-__device__ __forceinline__ void flush_amax(unsigned* out, uint32_t top)
-{
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if ((threadIdx.x & 31) == 0)
-        atomicMax(out, top);  // a maximum does not depend on the order
-}
-
 // The warp's 32 lanes hold one group (0 past the row's end).
 __device__ __forceinline__ void save_group(float v, const Act8View& out, int64_t group)
 {
@@ -78,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_any_kernel(ActArgs a)
 {
     const int lane = threadIdx.x & 31;
     const int64_t G = act8_groups(a.cols), total = a.rows * G;
-    uint32_t top = 0;
+    Top<T> top;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); i < total;
          i += static_cast<int64_t>(gridDim.x) * kWarps) {
         const int64_t r = i / G, c = (i - r * G) * kAct8Group + lane;
@@ -92,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_any_kernel(ActArgs a)
         if (in) {
             h = as_stored<T>(h);
             store_f(static_cast<T*>(a.h) + r * a.ldh + c, h);
-            top = max(top, abs_bits(h));
+            top.value(h);
         }
         if (a.gate8.codes)
             save_group(g, a.gate8, i);
@@ -100,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_any_kernel(ActArgs a)
             save_group(u, a.up8, i);
     }
     if (a.amax)
-        flush_amax(a.amax, top);
+        flush_top(a.amax, top);
 }
 
 template <typename T, int ACT, bool GATED, bool FROM8>
@@ -108,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_any_kernel(ActArgs a)
 {
     const int lane = threadIdx.x & 31;
     const int64_t G = act8_groups(a.cols), total = a.rows * G;
-    uint32_t top = 0;
+    Top<T> top;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); i < total;
          i += static_cast<int64_t>(gridDim.x) * kWarps) {
         const int64_t r = i / G, c = (i - r * G) * kAct8Group + lane;
@@ -123,14 +116,14 @@ __global__ void __launch_bounds__(kThreads) act_bwd_any_kernel(ActArgs a)
             dg *= u;
             const float du = as_stored<T>(dh * f.value);
             store_f(static_cast<T*>(a.dup) + r * a.lddu + c, du);
-            top = max(top, abs_bits(du));
+            top.value(du);
         }
         dg = as_stored<T>(dg);
         store_f(static_cast<T*>(a.dgate) + r * a.lddg + c, dg);
-        top = max(top, abs_bits(dg));
+        top.value(dg);
     }
     if (a.amax)
-        flush_amax(a.amax, top);
+        flush_top(a.amax, top);
 }
 
 template <typename T>
@@ -199,7 +192,7 @@ __device__ __forceinline__ void load_unit(RawOct<T>& o, const void* base, int64_
 }
 
 template <typename T>
-__device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& p, Oct& o, uint32_t& top)
+__device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& p, const Oct& o, Top<T>& top)
 {
     T* dst = static_cast<T*>(base) + p.row * ld + static_cast<int64_t>(p.unit) * 8;
     if (p.cols == 8) {
@@ -208,8 +201,8 @@ __device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& 
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             if (c < p.cols) {
-                store_f(dst + c, o.v[c]);
-                fold_top<T>(top, o.v[c]);
+                store_f(dst + c, o[c]);
+                top.value(o[c]);
             }
     }
 }
@@ -228,7 +221,7 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 template <typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 {
-    uint32_t top = 0;
+    Top<T> top;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         RawOct<T> g[kUnits], u[kUnits];
         Place p[kUnits];
@@ -251,9 +244,9 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
                 u[k].get(uv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                h.v[j] = activate<ACT, sizeof(T) == 2>(gv.v[j]).value;
+                h[j] = activate<ACT, sizeof(T) == 2>(gv[j]).value;
                 if constexpr (GATED)
-                    h.v[j] *= uv.v[j];
+                    h[j] *= uv[j];
             }
             store_unit<T>(a.h, a.ldh, p[k], h, top);
             if (a.gate8.codes)
@@ -264,14 +257,14 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
         }
     }
     if (a.amax)
-        flush_amax(a.amax, oct_top<T>(top));
+        flush_top(a.amax, top);
 }
 
 template <typename T, int ACT, bool GATED, bool FROM8>
 __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
 {
     using Raw = std::conditional_t<FROM8, RawCodes, RawOct<T>>;
-    uint32_t top = 0;
+    Top<T> top;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         Raw g[kUnits], u[kUnits];
         RawOct<T> d[kUnits];
@@ -306,11 +299,11 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
                 u[k].get(uv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const ValueSlope f = activate<ACT, sizeof(T) == 2>(gv.v[j]);
-                dg.v[j] = dv.v[j] * f.slope;
+                const ValueSlope f = activate<ACT, sizeof(T) == 2>(gv[j]);
+                dg[j] = dv[j] * f.slope;
                 if constexpr (GATED) {
-                    dg.v[j] *= uv.v[j];
-                    dv.v[j] *= f.value;
+                    dg[j] *= uv[j];
+                    dv[j] *= f.value;
                 }
             }
             store_unit<T>(a.dgate, a.lddg, p[k], dg, top);
@@ -319,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
         }
     }
     if (a.amax)
-        flush_amax(a.amax, oct_top<T>(top));
+        flush_top(a.amax, top);
 }
 
 template <typename T>
@@ -350,7 +343,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View a, int64_t cols, void* __restrict__ out,
                                                                 int64_t ldo, UnitMap m)
 {
-    uint32_t unused = 0;
+    Top<T> unused;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         RawCodes w[kUnits];
         Place p[kUnits];

@@ -65,31 +65,38 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) { retur
 // 16 bytes of bf16 or 32 bytes of fp32, 16-byte aligned.  The loads stay before
 // the stores that follow them in the source: an output may be an input's memory.
 struct Oct {
-    float v[8];
+    float2 p[4];  // pairs, as the two-wide fp32 instructions take them
+    __device__ __forceinline__ float& operator[](int i) { return i & 1 ? p[i >> 1].y : p[i >> 1].x; }
+    __device__ __forceinline__ float operator[](int i) const { return i & 1 ? p[i >> 1].y : p[i >> 1].x; }
+    __device__ __forceinline__ void fill(float v)
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            p[k] = make_float2(v, v);
+    }
 };
 
-__device__ __forceinline__ void unpack_bf16x2(uint32_t w, float& lo, float& hi)
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t w)
 {
-    lo = __uint_as_float(w << 16);
-    hi = __uint_as_float(w & 0xFFFF0000u);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 __device__ __forceinline__ void unpack_oct(uint4 w, Oct& o)
 {
-    unpack_bf16x2(w.x, o.v[0], o.v[1]);
-    unpack_bf16x2(w.y, o.v[2], o.v[3]);
-    unpack_bf16x2(w.z, o.v[4], o.v[5]);
-    unpack_bf16x2(w.w, o.v[6], o.v[7]);
+    o.p[0] = unpack_bf16x2(w.x);
+    o.p[1] = unpack_bf16x2(w.y);
+    o.p[2] = unpack_bf16x2(w.z);
+    o.p[3] = unpack_bf16x2(w.w);
 }
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+__device__ __forceinline__ uint32_t pack_bf16x2(float2 v)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint4 pack_oct(const Oct& o)
 {
-    return make_uint4(pack_bf16x2(o.v[0], o.v[1]), pack_bf16x2(o.v[2], o.v[3]), pack_bf16x2(o.v[4], o.v[5]),
-                      pack_bf16x2(o.v[6], o.v[7]));
+    return make_uint4(pack_bf16x2(o.p[0]), pack_bf16x2(o.p[1]), pack_bf16x2(o.p[2]), pack_bf16x2(o.p[3]));
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // The words of an oct as loaded, so that several loads can be in flight.
 template <typename T>
@@ -124,16 +131,15 @@ struct RawOct<float> {
     __device__ __forceinline__ void clear() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ void get(Oct& o) const
     {
-        o.v[0] = a.x, o.v[1] = a.y, o.v[2] = a.z, o.v[3] = a.w;
-        o.v[4] = b.x, o.v[5] = b.y, o.v[6] = b.z, o.v[7] = b.w;
+        o.p[0] = make_float2(a.x, a.y), o.p[1] = make_float2(a.z, a.w);
+        o.p[2] = make_float2(b.x, b.y), o.p[3] = make_float2(b.z, b.w);
     }
 };
-__device__ __forceinline__ void decode_oct(uint2 w, float s, Oct& o)
+// The codes' own values; times 2^e they are the checkpoint's.
+__device__ __forceinline__ void decode_oct(uint2 w, Oct& o)
 {
-    const float2 p = dec_e4m3x2(w.x & 0xFFFFu), q = dec_e4m3x2(w.x >> 16);
-    const float2 t = dec_e4m3x2(w.y & 0xFFFFu), u = dec_e4m3x2(w.y >> 16);
-    o.v[0] = p.x * s, o.v[1] = p.y * s, o.v[2] = q.x * s, o.v[3] = q.y * s;
-    o.v[4] = t.x * s, o.v[5] = t.y * s, o.v[6] = u.x * s, o.v[7] = u.y * s;
+    o.p[0] = dec_e4m3x2(w.x & 0xFFFFu), o.p[1] = dec_e4m3x2(w.x >> 16);
+    o.p[2] = dec_e4m3x2(w.y & 0xFFFFu), o.p[3] = dec_e4m3x2(w.y >> 16);
 }
 // Eight checkpoint codes and their group's exponent byte.
 struct RawCodes {
@@ -145,7 +151,14 @@ struct RawCodes {
         e = a.sf[unit >> 2];
     }
     __device__ __forceinline__ void clear() { w = make_uint2(0, 0), e = 127; }
-    __device__ __forceinline__ void get(Oct& o) const { decode_oct(w, act8_scale(e), o); }
+    __device__ __forceinline__ void get(Oct& o) const
+    {
+        decode_oct(w, o);
+        const float2 s = both(act8_scale(e));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o.p[k] = __fmul2_rn(o.p[k], s);
+    }
 };
 
 // Asynchronous copies into a thread's own shared-memory words: no other thread
@@ -170,59 +183,78 @@ __device__ __forceinline__ void copy_wait(int pending)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Writes an oct rounded to its type and folds |written values| into `top`:
-// packed bf16 maxima (finish with oct_top), or fp32 bits.
-__device__ __forceinline__ void store_oct(__nv_bfloat16* p, const Oct& o, uint32_t& top)
-{
-    const uint4 w = pack_oct(o);
-    *reinterpret_cast<uint4*>(p) = w;
-    top = __vmaxu2(top, w.x & 0x7FFF7FFFu);
-    top = __vmaxu2(top, w.y & 0x7FFF7FFFu);
-    top = __vmaxu2(top, w.z & 0x7FFF7FFFu);
-    top = __vmaxu2(top, w.w & 0x7FFF7FFFu);
-}
-__device__ __forceinline__ void store_oct(float* p, const Oct& o, uint32_t& top)
-{
-    *reinterpret_cast<float4*>(p) = make_float4(o.v[0], o.v[1], o.v[2], o.v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(o.v[4], o.v[5], o.v[6], o.v[7]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        top = max(top, __float_as_uint(o.v[i]) & 0x7FFFFFFFu);
-}
-// One value of type T folded the same way.
-template <typename T>
-__device__ __forceinline__ void fold_top(uint32_t& top, float v)
-{
-    const uint32_t u = __float_as_uint(as_stored<T>(v)) & 0x7FFFFFFFu;
-    top = sizeof(T) == 2 ? __vmaxu2(top, u >> 16) : max(top, u);
-}
-// The folded maximum as fp32 bits.
-template <typename T>
-__device__ __forceinline__ uint32_t oct_top(uint32_t top)
-{
-    return sizeof(T) == 2 ? max(top & 0xFFFFu, top >> 16) << 16 : top;
-}
-
 __device__ __forceinline__ float max_nan(float a, float b)
 {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_abs(float m, float2 v) { return max_nan(m, fabsf(v.x), fabsf(v.y)); }
+
+// Running maximum of |written value|, NaN once there was one: two packed bf16
+// maxima, or one of fp32.
+template <typename T>
+struct Top;
+template <>
+struct Top<__nv_bfloat16> {
+    __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+    __device__ __forceinline__ void word(uint32_t w)
+    {
+        m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    }
+    __device__ __forceinline__ void value(float v) { word(pack_bf16x2(make_float2(v, 0.0f))); }
+    __device__ __forceinline__ uint32_t bits() const
+    {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&m) & 0x7FFF7FFFu;
+        return max(w & 0xFFFFu, w >> 16) << 16;
+    }
+};
+template <>
+struct Top<float> {
+    float m = 0.0f;
+    __device__ __forceinline__ void pair(float2 v) { m = max_abs(m, v); }
+    __device__ __forceinline__ void value(float v) { m = max_nan(m, fabsf(v)); }
+    __device__ __forceinline__ uint32_t bits() const { return __float_as_uint(m) & 0x7FFFFFFFu; }
+};
+// Folds the CTA's maxima into *out; a maximum does not depend on the order, and
+// most warps find theirs already covered.
+template <typename T>
+__device__ __forceinline__ void flush_top(unsigned* out, const Top<T>& top)
+{
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, top.bits());
+    if ((threadIdx.x & 31) == 0 && m > *static_cast<volatile unsigned*>(out))
+        atomicMax(out, m);
+}
+
+// Writes an oct rounded to its type.
+__device__ __forceinline__ void store_oct(__nv_bfloat16* p, const Oct& o, Top<__nv_bfloat16>& top)
+{
+    const uint4 w = pack_oct(o);
+    *reinterpret_cast<uint4*>(p) = w;
+    top.word(w.x), top.word(w.y), top.word(w.z), top.word(w.w);
+}
+__device__ __forceinline__ void store_oct(float* p, const Oct& o, Top<float>& top)
+{
+    *reinterpret_cast<float4*>(p) = make_float4(o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y);
+    top.pair(o.p[0]), top.pair(o.p[1]), top.pair(o.p[2]), top.pair(o.p[3]);
+}
+
 __device__ __forceinline__ bool non_finite(float v) { return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u; }
 
 // The checkpoint of a group that four consecutive lanes hold, eight columns
 // each (0 past the row's end).  Executed by whole warps.  Groups without Inf
 // and NaN take one maximum and one product per value; a warp that has one of
 // the others repeats the maximum over the finite values.
-__device__ __forceinline__ uint2 encode_oct(const Oct& o, int& e)
+__device__ __forceinline__ uint2 encode_oct(Oct z, int& e)
 {
-    float z[8], m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        z[i] = o.v[i];
-        m = max_nan(m, fabsf(z[i]));
-    }
+    float m = max_abs(max_abs(max_abs(max_abs(0.0f, z.p[0]), z.p[1]), z.p[2]), z.p[3]);
     m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     if (__any_sync(0xFFFFFFFFu, non_finite(m))) {
@@ -236,9 +268,12 @@ __device__ __forceinline__ uint2 encode_oct(const Oct& o, int& e)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     }
     e = act8_exponent(m);
-    const float s = exp2_neg(e);
-    return make_uint2(cvt_e4m3x2(z[0] * s, z[1] * s) | cvt_e4m3x2(z[2] * s, z[3] * s) << 16,
-                      cvt_e4m3x2(z[4] * s, z[5] * s) | cvt_e4m3x2(z[6] * s, z[7] * s) << 16);
+    const float2 s = both(exp2_neg(e));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        z.p[k] = __fmul2_rn(z.p[k], s);
+    return make_uint2(cvt_e4m3x2(z.p[0].x, z.p[0].y) | cvt_e4m3x2(z.p[1].x, z.p[1].y) << 16,
+                      cvt_e4m3x2(z.p[2].x, z.p[2].y) | cvt_e4m3x2(z.p[3].x, z.p[3].y) << 16);
 }
 
 // |v| as the bits that a maximum over unsigned words orders (NaN above all).

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_fwd_any_kernel(NormFwdArgs a
     const int lane = threadIdx.x & 31;
     const int64_t C = a.cols, G = act8_groups(C);
     const float inv_c = 1.0f / static_cast<float>(C);
-    uint32_t top = 0;
+    Top<TY> top;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T* x = static_cast<const T*>(a.x) + r * a.ldx;
         float sum = 0.0f;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_fwd_any_kernel(NormFwdArgs a
                 const float o = as_stored<TY>((v - mean) * rstd * param(a.weight, a.w_dtype, c, 1.0f) +
                                               param(a.bias, a.w_dtype, c, 0.0f));
                 store_f(y + c, o);
-                top = max(top, abs_bits(o));
+                top.value(o);
             }
             if (a.save.codes) {
                 const float z = finite_or_nan(v);
@@ -104,11 +104,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_fwd_any_kernel(NormFwdArgs a
             }
         }
     }
-    if (a.amax) {
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (lane == 0)
-            atomicMax(a.amax, top);  // a maximum does not depend on the order
-    }
+    if (a.amax)
+        flush_top(a.amax, top);
 }
 
 // s of row r, column c: the kept tensor or the checkpoint.
@@ -126,7 +123,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_dx_any_kernel(NormBwdArgs a)
     __shared__ float part[kRowWarps];
     const int64_t C = a.cols, G = act8_groups(C);
     const float inv_c = 1.0f / static_cast<float>(C);
-    uint32_t top = 0;
+    Top<T> top;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const TY* dy = static_cast<const TY*>(a.dy) + r * a.ldy;
         const float rstd = a.rstd[r], mean = a.kind == MX_NORM_LAYER ? a.mean[r] : 0.0f;
@@ -148,14 +145,11 @@ __global__ void __launch_bounds__(kRowThreads) norm_dx_any_kernel(NormBwdArgs a)
                 v += load_f(dres + c);
             v = as_stored<T>(v);
             store_f(dx + c, v);
-            top = max(top, abs_bits(v));
+            top.value(v);
         }
     }
-    if (a.amax) {
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if ((threadIdx.x & 31) == 0)
-            atomicMax(a.amax, top);
-    }
+    if (a.amax)
+        flush_top(a.amax, top);
 }
 
 // Partial column sums: CTA (x, y) adds 32 columns of every gridDim.y-th row.
@@ -188,25 +182,31 @@ __global__ void __launch_bounds__(kRowThreads) norm_dw_any_kernel(NormBwdArgs a)
     }
 }
 
-// dw and db from `parts` partial sums of each column (rows of parts: dw's, then db's).
-__global__ void __launch_bounds__(kRowThreads) norm_dw_join_kernel(const float* __restrict__ src, int64_t C, int parts,
-                                                                   float* __restrict__ dw, float* __restrict__ db)
+// dw and db from `parts` partial sums of each column (rows of parts: dw's, then
+// db's), 32 columns and up to 32 runs of parts a CTA.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const float* __restrict__ src, int64_t C,
+                                                                       int parts, float* __restrict__ dw,
+                                                                       float* __restrict__ db)
 {
-    __shared__ float p[kRowWarps][32];
+    __shared__ float p[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = blockIdx.x * 32ll + lane;
     float* out = blockIdx.y ? db : dw;
     if (!out)
         return;
     float v = 0.0f;
-    if (c < C)
-        for (int i = warp; i < parts; i += kRowWarps)
-            v += src[(static_cast<int64_t>(blockIdx.y) * parts + i) * C + c];
+    if (c < C) {
+        const float* from = src + (static_cast<int64_t>(blockIdx.y) * parts + warp) * C + c;
+#pragma unroll 8
+        for (int i = warp; i < parts; i += kJoinWarps, from += kJoinWarps * C)
+            v += *from;
+    }
     p[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < kRowWarps; ++i)
+        const int n = min(parts, kJoinWarps);
+        for (int i = 1; i < n; ++i)
             v += p[i][lane];
         out[c] = v;
     }
@@ -225,23 +225,26 @@ __global__ void __launch_bounds__(kRowThreads) norm_dw_join_kernel(const float* 
 // for the ring.
 constexpr int kMaxWide = 16384;
 constexpr int kSubThreads = 256;  // CTA size where several rows share a CTA
+constexpr int kBwdThreads = 512;  // most threads of a backward CTA: 128 registers each
 
 template <typename T>
 __device__ __forceinline__ constexpr int chunks() { return sizeof(T) / 2; }  // 16-byte words of an oct
 
 template <int LPR>
 struct RowMap {
-    int tpr, sub, t;
-    int64_t first, step;
-    __device__ __forceinline__ RowMap()
+    int tpr, t;          // threads of a row, this one's place among them
+    int64_t first, step; // this thread's first row, rows from one to the next
+    int mine, all;       // rows of this thread, iterations of the CTA
+    __device__ __forceinline__ explicit RowMap(int64_t rows)
     {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, per_cta = LPR ? kSubThreads / LPR : 1;
         tpr = LPR ? LPR : blockDim.x;
-        sub = LPR ? tid / LPR : 0;
         t = LPR ? tid % LPR : tid;
-        const int rows_per_cta = LPR ? kSubThreads / LPR : 1;
-        first = static_cast<int64_t>(blockIdx.x) * rows_per_cta;
-        step = static_cast<int64_t>(gridDim.x) * rows_per_cta;
+        const int64_t cta = static_cast<int64_t>(blockIdx.x) * per_cta;
+        step = static_cast<int64_t>(gridDim.x) * per_cta;
+        first = cta + (LPR ? tid / LPR : 0);
+        all = static_cast<int>((rows - cta + step - 1) / step);
+        mine = first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
     }
 };
 
@@ -258,350 +261,397 @@ __device__ __forceinline__ float row_sum(float v, float* part)
         if ((threadIdx.x & 31) == 0)
             part[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = 0.0f;
+        float2 s = make_float2(0.0f, 0.0f);
         for (unsigned w = 0; w < blockDim.x / 32; w += 4) {
             const float4 p = *reinterpret_cast<const float4*>(part + w);
-            v += (p.x + p.y) + (p.z + p.w);
+            s = __fadd2_rn(s, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
         }
+        v = s.x + s.y;
     }
     return v;
 }
+// Two sums.  Where a warp belongs to one row its halves exchange the sums, so
+// that each half finishes one of them.
 template <int LPR>
 __device__ __forceinline__ float2 row_sum2(float2 v, float2* part)
 {
+    if constexpr (LPR != 0 && LPR < 32) {
 #pragma unroll
-    for (int o = (LPR ? LPR : 32) / 2; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-    }
-    if constexpr (LPR == 0) {
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x >> 5] = v;
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+        }
+        return v;
+    } else {
+        const bool second = threadIdx.x & 16;
+        float s = second ? v.y : v.x;
+        s += __shfl_xor_sync(0xFFFFFFFFu, second ? v.x : v.y, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if constexpr (LPR == 32)
+            return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
+        if ((threadIdx.x & 15) == 0)
+            reinterpret_cast<float*>(part)[(threadIdx.x >> 5) * 2 + (second ? 1 : 0)] = s;
         __syncthreads();
-        v = make_float2(0.0f, 0.0f);
+        float2 sum = make_float2(0.0f, 0.0f);
         for (unsigned w = 0; w < blockDim.x / 32; w += 2) {
             const float4 p = *reinterpret_cast<const float4*>(part + w);
-            v.x += p.x + p.z;
-            v.y += p.y + p.w;
+            sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
         }
+        return sum;
     }
-    return v;
 }
 
+// Eight of the weights or biases.
 __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float absent, Oct& o)
 {
     if (!p) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o.v[i] = absent;
+        o.fill(absent);
     } else if (dtype == MX_OUT_BF16) {
         unpack_oct(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), o);
     } else {
         const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
         const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
-        o.v[0] = a.x, o.v[1] = a.y, o.v[2] = a.z, o.v[3] = a.w;
-        o.v[4] = b.x, o.v[5] = b.y, o.v[6] = b.z, o.v[7] = b.w;
+        o.p[0] = make_float2(a.x, a.y), o.p[1] = make_float2(a.z, a.w);
+        o.p[2] = make_float2(b.x, b.y), o.p[3] = make_float2(b.z, b.w);
     }
 }
 
 // A thread's slots of one matrix in a ring stage: 16-byte words, a word's slots
-// of all threads side by side.
+// of all threads side by side.  `slots` is the thread's first.
 template <typename T>
 __device__ __forceinline__ void slot_fill(uint32_t slots, int j, const T* src)
 {
 #pragma unroll
     for (int h = 0; h < chunks<T>(); ++h)
-        copy_async16(slots + ((j * chunks<T>() + h) * blockDim.x + threadIdx.x) * 16, src + h * (16 / sizeof(T)));
+        copy_async16(slots + (j * chunks<T>() + h) * blockDim.x * 16, src + h * (16 / sizeof(T)));
 }
 template <typename T>
 __device__ __forceinline__ void slot_read(uint32_t slots, int j, Oct& o)
 {
     if constexpr (sizeof(T) == 2) {
-        unpack_oct(lds128(slots + (j * blockDim.x + threadIdx.x) * 16), o);
+        unpack_oct(lds128(slots + j * blockDim.x * 16), o);
     } else {
-        const uint4 a = lds128(slots + (2 * j * blockDim.x + threadIdx.x) * 16);
-        const uint4 b = lds128(slots + ((2 * j + 1) * blockDim.x + threadIdx.x) * 16);
-        o.v[0] = __uint_as_float(a.x), o.v[1] = __uint_as_float(a.y), o.v[2] = __uint_as_float(a.z);
-        o.v[3] = __uint_as_float(a.w), o.v[4] = __uint_as_float(b.x), o.v[5] = __uint_as_float(b.y);
-        o.v[6] = __uint_as_float(b.z), o.v[7] = __uint_as_float(b.w);
+        const uint4 a = lds128(slots + 2 * j * blockDim.x * 16);
+        const uint4 b = lds128(slots + (2 * j + 1) * blockDim.x * 16);
+        o.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+        o.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+        o.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+        o.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
     }
 }
 
 template <typename T, typename TY, int LPR, int NV>
-__global__ void __launch_bounds__(LPR ? kSubThreads : 1024) norm_fwd_kernel(NormFwdArgs a, int stages)
+__global__ void __launch_bounds__(LPR ? kSubThreads : 1024, LPR ? 4 : 1) norm_fwd_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float part[2][32];
-    if (LPR == 0 && threadIdx.x < 64)
-        part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
-    if (LPR == 0)
+    if (LPR == 0) {
+        if (threadIdx.x < 64)
+            part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
         __syncthreads();
-    const RowMap<LPR> map;
+    }
+    const RowMap<LPR> map(a.rows);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
+    const int c0 = 8 * map.t, dc = 8 * map.tpr;  // columns of oct j: c0 + j dc ..
     const float inv_c = 1.0f / static_cast<float>(C);
-    const uint32_t slots = smem_u32(ring);
+    const bool layer = a.kind == MX_NORM_LAYER, add = a.residual != nullptr;
     const uint32_t one = NV * chunks<T>() * blockDim.x * 16;  // bytes of one matrix in a stage
-    const uint32_t stage_bytes = a.residual ? 2 * one : one;
+    const uint32_t stage_bytes = add ? 2 * one : one;
+    const uint32_t slots = smem_u32(ring) + threadIdx.x * 16;
 
-    auto fill = [&](int64_t r, int stage) {
-        if (r < a.rows) {
+    const T* from_x = static_cast<const T*>(a.x) + map.first * a.ldx + c0;
+    const T* from_r = static_cast<const T*>(a.residual) + map.first * a.ldr + c0;
+    int filled = 0;
+    auto fill = [&](uint32_t at) {
+        if (filled < map.mine) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = 8 * (map.t + map.tpr * j);
-                if (c < C) {
-                    slot_fill(slots + stage * stage_bytes, j, static_cast<const T*>(a.x) + r * a.ldx + c);
-                    if (a.residual)
-                        slot_fill(slots + stage * stage_bytes + one, j, static_cast<const T*>(a.residual) + r * a.ldr + c);
+            for (int j = 0; j < NV; ++j)
+                if (c0 + j * dc < C) {
+                    slot_fill(at, j, from_x + j * dc);
+                    if (add)
+                        slot_fill(at + one, j, from_r + j * dc);
                 }
-            }
         }
+        ++filled;
+        from_x += map.step * a.ldx;
+        from_r += map.step * a.ldr;
         copy_commit();
     };
 
-    uint32_t top = 0, sum_top = 0;
+    Top<TY> top;
+    Top<T> sum_top;
+    T* to_sum = static_cast<T*>(a.sum_out) + map.first * a.lds + c0;
+    TY* to_y = static_cast<TY*>(a.y) + map.first * a.ldy + c0;
+    uint8_t* to_codes = a.save.codes + map.first * (G * kAct8Group) + c0;
+    uint8_t* to_sf = a.save.sf + map.first * G + c0 / kAct8Group;
     for (int i = 0; i < stages - 1; ++i)
-        fill(map.first + map.sub + i * map.step, i);
-    int stage = 0, odd = 0;
-    for (int64_t rb = map.first; rb < a.rows; rb += map.step, odd ^= 1) {
-        const int64_t r = rb + map.sub;
-        fill(r + (stages - 1) * map.step, stage == 0 ? stages - 1 : stage - 1);  // the slots read a row ago
+        fill(slots + i * stage_bytes);
+    int stage = 0;
+    for (int it = 0; it < map.all; ++it) {
+        fill(slots + (stage == 0 ? stages - 1 : stage - 1) * stage_bytes);  // the slots read a row ago
         copy_wait(stages - 1);
         const uint32_t here = slots + stage * stage_bytes;
+        const bool in = it < map.mine;
         Oct v[NV];
-        float sum = 0.0f;
+        float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (map.t + map.tpr * j);
-            if (c < C && r < a.rows) {
+            v[j].fill(0.0f);
+            if (in && c0 + j * dc < C) {
                 slot_read<T>(here, j, v[j]);
-                if (a.residual) {
+                if (add) {
                     Oct q;
                     slot_read<T>(here + one, j, q);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[j].v[i] = as_stored<T>(v[j].v[i] + q.v[i]);
-                    store_oct(static_cast<T*>(a.sum_out) + r * a.lds + c, v[j], sum_top);
+                    for (int k = 0; k < 4; ++k)
+                        q.p[k] = __fadd2_rn(v[j].p[k], q.p[k]);
+                    store_oct(to_sum + j * dc, q, sum_top);
+                    if constexpr (sizeof(T) == 2)
+                        unpack_oct(pack_oct(q), v[j]);  // as it was stored
+                    else
+                        v[j] = q;
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sum += v[j].v[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[j].v[i] = 0.0f;
+                for (int k = 0; k < 4; ++k)
+                    sum2 = __fadd2_rn(sum2, v[j].p[k]);
             }
         }
-        const float mean = a.kind == MX_NORM_LAYER ? row_sum<LPR>(sum, part[0]) * inv_c : 0.0f;
-        float sq = 0.0f;
+        const float mean = layer ? row_sum<LPR>(sum2.x + sum2.y, part[0]) * inv_c : 0.0f;
+        float2 sq2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (8 * (map.t + map.tpr * j) < C)
+            if (c0 + j * dc < C)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = v[j].v[i] - mean;
-                    sq += d * d;
+                for (int k = 0; k < 4; ++k) {
+                    const float2 d = __fadd2_rn(v[j].p[k], both(-mean));
+                    sq2 = __ffma2_rn(d, d, sq2);
                 }
         // RMS norm has one sum per row: its words alternate with the row
-        float* const words = part[a.kind == MX_NORM_LAYER ? 1 : odd];
-        const float rstd = 1.0f / sqrtf(row_sum<LPR>(sq, words) * inv_c + a.eps);
-        if (map.t == 0 && r < a.rows) {
-            if (a.mean && a.kind == MX_NORM_LAYER)
+        const float rstd = 1.0f / sqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1]) * inv_c + a.eps);
+        if (map.t == 0 && in) {
+            const int64_t r = map.first + it * map.step;
+            if (a.mean && layer)
                 a.mean[r] = mean;
             if (a.rstd)
                 a.rstd[r] = rstd;
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (map.t + map.tpr * j);
-            if (c < C && r < a.rows) {
+            if (in && c0 + j * dc < C) {
                 Oct w, b;
-                param_oct(a.weight, a.w_dtype, c, 1.0f, w);
-                param_oct(a.bias, a.w_dtype, c, 0.0f, b);
+                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, w);
+                param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    b.v[i] = (v[j].v[i] - mean) * rstd * w.v[i] + b.v[i];
-                store_oct(static_cast<TY*>(a.y) + r * a.ldy + c, b, top);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 h = __fmul2_rn(__fadd2_rn(v[j].p[k], both(-mean)), both(rstd));
+                    b.p[k] = __ffma2_rn(h, w.p[k], b.p[k]);
+                }
+                store_oct(to_y + j * dc, b, top);
             }
             if (a.save.codes) {
                 int e;
                 const uint2 codes = encode_oct(v[j], e);
-                if (c < G * kAct8Group && r < a.rows) {
-                    *reinterpret_cast<uint2*>(a.save.codes + r * G * kAct8Group + c) = codes;
+                if (in && c0 + j * dc < G * kAct8Group) {
+                    *reinterpret_cast<uint2*>(to_codes + j * dc) = codes;
                     if ((threadIdx.x & 3) == 0)
-                        a.save.sf[r * G + c / kAct8Group] = static_cast<uint8_t>(e + 127);
+                        to_sf[j * dc / kAct8Group] = static_cast<uint8_t>(e + 127);
                 }
             }
         }
+        to_sum += map.step * a.lds;
+        to_y += map.step * a.ldy;
+        to_codes += map.step * (G * kAct8Group);
+        to_sf += map.step * G;
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
-    if (a.amax) {
-        top = __reduce_max_sync(0xFFFFFFFFu, oct_top<TY>(top));
-        if ((threadIdx.x & 31) == 0)
-            atomicMax(a.amax, top);
-    }
+    if (a.amax)
+        flush_top(a.amax, top);
 }
 
 // dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
 // is the checkpoint.  The column sums stay in registers over all rows of the
-// CTA; dy h and g h come from one reading of the row, dx from a second one out
-// of shared memory (out of registers where a thread has one oct).
+// CTA; dy h and g h come from one reading of the row, dx from what was kept of
+// it in registers (up to two octs a thread) or from a second reading of shared
+// memory.
 template <typename T, typename TY, bool FROM8, int LPR, int NV>
-__global__ void __launch_bounds__(LPR ? kSubThreads : 1024) norm_bwd_kernel(NormBwdArgs a, int stages)
+__global__ void __launch_bounds__(LPR ? kSubThreads : kBwdThreads, LPR ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, int stages)
 {
+    constexpr bool KEEP = NV <= 2;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float2 part[2][32];
-    if (LPR == 0 && threadIdx.x < 64)
-        part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.0f, 0.0f);
-    if (LPR == 0)
+    if (LPR == 0) {
+        if (threadIdx.x < 64)
+            part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.0f, 0.0f);
         __syncthreads();
-    const RowMap<LPR> map;
+    }
+    const RowMap<LPR> map(a.rows);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
+    const int c0 = 8 * map.t, dc = 8 * map.tpr;
     const float inv_c = 1.0f / static_cast<float>(C);
-    const bool layer = a.kind == MX_NORM_LAYER;
-    const uint32_t slots = smem_u32(ring);
+    const bool layer = a.kind == MX_NORM_LAYER, add = a.dres != nullptr;
     const uint32_t at_s = NV * chunks<TY>() * blockDim.x * 16;
     const uint32_t at_r = at_s + (FROM8 ? NV * blockDim.x * 8 : NV * chunks<T>() * blockDim.x * 16);
-    const uint32_t stage_bytes = a.dres ? at_r + NV * chunks<T>() * blockDim.x * 16 : at_r;
+    const uint32_t stage_bytes = add ? at_r + NV * chunks<T>() * blockDim.x * 16 : at_r;
+    const uint32_t slots = smem_u32(ring) + threadIdx.x * 16;
 
-    auto fill = [&](int64_t r, int stage) {
-        if (r < a.rows) {
-            const uint32_t here = slots + stage * stage_bytes;
+    const TY* from_dy = static_cast<const TY*>(a.dy) + map.first * a.ldy + c0;
+    const T* from_x = static_cast<const T*>(a.x) + map.first * a.ldx + c0;
+    const uint8_t* from_codes = a.x8.codes + map.first * (G * kAct8Group) + c0;
+    const T* from_r = static_cast<const T*>(a.dres) + map.first * a.ldres + c0;
+    int filled = 0;
+    auto fill = [&](uint32_t at) {
+        if (filled < map.mine) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = 8 * (map.t + map.tpr * j);
-                if (c < C) {
-                    slot_fill(here, j, static_cast<const TY*>(a.dy) + r * a.ldy + c);
+            for (int j = 0; j < NV; ++j)
+                if (c0 + j * dc < C) {
+                    slot_fill(at, j, from_dy + j * dc);
                     if constexpr (FROM8)
-                        copy_async8(here + at_s + (j * blockDim.x + threadIdx.x) * 8, a.x8.codes + r * G * kAct8Group + c);
+                        copy_async8(at + at_s + j * blockDim.x * 8 - threadIdx.x * 8, from_codes + j * dc);
                     else
-                        slot_fill(here + at_s, j, static_cast<const T*>(a.x) + r * a.ldx + c);
-                    if (a.dres)
-                        slot_fill(here + at_r, j, static_cast<const T*>(a.dres) + r * a.ldres + c);
+                        slot_fill(at + at_s, j, from_x + j * dc);
+                    if (add)
+                        slot_fill(at + at_r, j, from_r + j * dc);
                 }
-            }
         }
+        ++filled;
+        from_dy += map.step * a.ldy;
+        if constexpr (FROM8)
+            from_codes += map.step * (G * kAct8Group);
+        else
+            from_x += map.step * a.ldx;
+        from_r += map.step * a.ldres;
         copy_commit();
     };
     struct RowWords {  // what a row needs beside its matrices, loaded a row ahead
         float mean, rstd;
         uint32_t e[NV];
     };
-    auto row_words = [&](int64_t r) {
+    const float* from_mean = a.mean + map.first;
+    const float* from_rstd = a.rstd + map.first;
+    const uint8_t* from_sf = a.x8.sf + map.first * G + c0 / kAct8Group;
+    auto row_words = [&](bool in) {
         RowWords w;
-        const bool in = r < a.rows;
-        w.mean = in && layer ? a.mean[r] : 0.0f;
-        w.rstd = in ? a.rstd[r] : 0.0f;
+        w.mean = in && layer ? *from_mean : 0.0f;
+        w.rstd = in ? *from_rstd : 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (map.t + map.tpr * j);
-            w.e[j] = FROM8 && in && c < C ? a.x8.sf[r * G + c / kAct8Group] : 127u;
-        }
+        for (int j = 0; j < NV; ++j)
+            w.e[j] = FROM8 && in && c0 + j * dc < C ? from_sf[j * dc / kAct8Group] : 127u;
+        from_mean += map.step;
+        from_rstd += map.step;
+        from_sf += map.step * G;
         return w;
     };
 
-    float dw[NV][8], db[NV][8];
+    Oct wt[KEEP ? NV : 1];
+    if constexpr (KEEP)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
+            if (c0 + j * dc < C)
+                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
+    Oct dw[NV], db[NV];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            dw[j][i] = db[j][i] = 0.0f;
-    uint32_t top = 0;
+    for (int j = 0; j < NV; ++j) {
+        dw[j].fill(0.0f);
+        db[j].fill(0.0f);
+    }
+    Top<T> top;
+    T* to_dx = static_cast<T*>(a.dx) + map.first * a.lddx + c0;
     for (int i = 0; i < stages - 1; ++i)
-        fill(map.first + map.sub + i * map.step, i);
-    RowWords next = row_words(map.first + map.sub);
-    int stage = 0, odd = 0;
-    for (int64_t rb = map.first; rb < a.rows; rb += map.step, odd ^= 1) {
-        const int64_t r = rb + map.sub;
+        fill(slots + i * stage_bytes);
+    RowWords next = row_words(0 < map.mine);
+    int stage = 0;
+    for (int it = 0; it < map.all; ++it) {
+        const bool in = it < map.mine;
         const RowWords cur = next;
-        next = row_words(r + map.step);
-        fill(r + (stages - 1) * map.step, stage == 0 ? stages - 1 : stage - 1);
+        next = row_words(it + 1 < map.mine);
+        fill(slots + (stage == 0 ? stages - 1 : stage - 1) * stage_bytes);
         copy_wait(stages - 1);
         const uint32_t here = slots + stage * stage_bytes;
-        // g and h of oct j
-        auto load = [&](int j, int c, Oct& dy, Oct& g, Oct& h) {
+        // dy, and g and h of oct j
+        auto load = [&](int j, Oct& dy, Oct& g, Oct& h) {
             slot_read<TY>(here, j, dy);
             if constexpr (FROM8) {
                 uint2 w;
                 asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                              : "=r"(w.x), "=r"(w.y)
-                             : "r"(here + at_s + (j * blockDim.x + threadIdx.x) * 8)
+                             : "r"(here + at_s + j * blockDim.x * 8 - threadIdx.x * 8)
                              : "memory");
-                decode_oct(w, act8_scale(cur.e[j]), h);
+                decode_oct(w, h);
+                const float2 scale = both(act8_scale(cur.e[j]));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // the product is exact
+                    h.p[k] = __ffma2_rn(h.p[k], scale, both(-cur.mean));
             } else {
                 slot_read<T>(here + at_s, j, h);
-            }
-            param_oct(a.weight, a.w_dtype, c, 1.0f, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h.v[i] = (h.v[i] - cur.mean) * cur.rstd;
-                g.v[i] *= dy.v[i];
+                for (int k = 0; k < 4; ++k)
+                    h.p[k] = __fadd2_rn(h.p[k], both(-cur.mean));
+            }
+            if constexpr (KEEP)
+                g = wt[j];
+            else
+                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, g);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h.p[k] = __fmul2_rn(h.p[k], both(cur.rstd));
+                g.p[k] = __fmul2_rn(g.p[k], dy.p[k]);
             }
         };
-        Oct kg, kh;  // NV == 1: kept for the second pass
-        float2 s = make_float2(0.0f, 0.0f);
+        Oct kg[KEEP ? NV : 1], kh[KEEP ? NV : 1];
+        float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (map.t + map.tpr * j);
-            if (c < C && r < a.rows) {
-                Oct dy;
-                load(j, c, dy, kg, kh);
+        for (int j = 0; j < NV; ++j)
+            if (in && c0 + j * dc < C) {
+                Oct dy, &g = kg[KEEP ? j : 0], &h = kh[KEEP ? j : 0];
+                load(j, dy, g, h);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s.x += kg.v[i] * kh.v[i];
-                    s.y += kg.v[i];
-                    dw[j][i] += dy.v[i] * kh.v[i];
-                    db[j][i] += dy.v[i];
+                for (int k = 0; k < 4; ++k) {
+                    sgh = __ffma2_rn(g.p[k], h.p[k], sgh);
+                    sg = __fadd2_rn(sg, g.p[k]);
+                    dw[j].p[k] = __ffma2_rn(dy.p[k], h.p[k], dw[j].p[k]);
+                    db[j].p[k] = __fadd2_rn(db[j].p[k], dy.p[k]);
                 }
             }
-        }
-        s = row_sum2<LPR>(s, part[odd]);
-        const float c1 = s.x * inv_c, c2 = layer ? s.y * inv_c : 0.0f;
+        const float2 s = row_sum2<LPR>(make_float2(sgh.x + sgh.y, sg.x + sg.y), part[it & 1]);
+        const float2 c1 = both(-s.x * inv_c), c2 = both(layer ? -s.y * inv_c : 0.0f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (map.t + map.tpr * j);
-            if (c < C && r < a.rows) {
-                if constexpr (NV > 1) {
-                    Oct dy;
-                    load(j, c, dy, kg, kh);
-                }
-                Oct q;
-                if (a.dres) {
+        for (int j = 0; j < NV; ++j)
+            if (in && c0 + j * dc < C) {
+                Oct dy, q, &g = kg[KEEP ? j : 0], &h = kh[KEEP ? j : 0];
+                if constexpr (!KEEP)
+                    load(j, dy, g, h);
+                if (add)
                     slot_read<T>(here + at_r, j, q);
-                } else {
+                else
+                    q.fill(0.0f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        q.v[i] = 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    q.v[i] += (kg.v[i] - kh.v[i] * c1 - c2) * cur.rstd;
-                store_oct(static_cast<T*>(a.dx) + r * a.lddx + c, q, top);
+                for (int k = 0; k < 4; ++k)
+                    q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h.p[k], c1, g.p[k]), c2), both(cur.rstd), q.p[k]);
+                store_oct(to_dx + j * dc, q, top);
             }
-        }
+        to_dx += map.step * a.lddx;
         stage = stage + 1 == stages ? 0 : stage + 1;
     }
-    if (a.amax) {
-        top = __reduce_max_sync(0xFFFFFFFFu, oct_top<T>(top));
-        if ((threadIdx.x & 31) == 0)
-            atomicMax(a.amax, top);
-    }
+    if (a.amax)
+        flush_top(a.amax, top);
     if (!a.dw && !a.db)
         return;
     float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C;
     const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
     if constexpr (LPR == 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = 8 * (map.t + map.tpr * j);
-            if (c < C) {
+        for (int j = 0; j < NV; ++j)
+            if (c0 + j * dc < C)
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    *reinterpret_cast<float4*>(out + c + i) = make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
-                    *reinterpret_cast<float4*>(out + to_db + c + i) =
-                        make_float4(db[j][i], db[j][i + 1], db[j][i + 2], db[j][i + 3]);
+                for (int k = 0; k < 4; k += 2) {
+                    float* const to = out + c0 + j * dc + 2 * k;
+                    *reinterpret_cast<float4*>(to) =
+                        make_float4(dw[j].p[k].x, dw[j].p[k].y, dw[j].p[k + 1].x, dw[j].p[k + 1].y);
+                    *reinterpret_cast<float4*>(to + to_db) =
+                        make_float4(db[j].p[k].x, db[j].p[k].y, db[j].p[k + 1].x, db[j].p[k + 1].y);
                 }
-            }
-        }
     } else {
         // the rows of a warp, then the warps through shared memory, in order
         constexpr int kWarpCols = NV * LPR * 8;
@@ -655,16 +705,12 @@ WideShape fwd_shape(int64_t cols)
         return {32, octs <= 32 ? 1 : octs <= 64 ? 2 : 4, kSubThreads};
     return {0, 2, ((octs + 1) / 2 + 31) / 32 * 32};
 }
-// One oct a thread as long as a CTA's threads suffice: the column sums take 16
-// registers for each.
+// At most 512 threads, so that each may use 128 registers: they hold the column
+// sums and, up to two octs a thread, the weights and a row's g and h.
 WideShape bwd_shape(int64_t cols)
 {
     const WideShape f = fwd_shape(cols);
-    if (f.lpr)
-        return f;
-    const int octs = static_cast<int>(act8_groups(cols)) * 4;
-    const int nv = octs <= 1024 ? 1 : 2;
-    return {0, nv, ((octs + nv - 1) / nv + 31) / 32 * 32};
+    return f.threads <= kBwdThreads ? f : WideShape{0, 4, (f.threads / 2 + 31) / 32 * 32};
 }
 
 constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
@@ -673,10 +719,10 @@ constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTA
 struct RingPlan {
     int stages, per_sm;
 };
-RingPlan ring_plan(int64_t stage_bytes, int threads, int most)
+RingPlan ring_plan(int64_t stage_bytes, int most)
 {
     RingPlan p;
-    p.per_sm = std::max(1, std::min<int>(most, 1024 / threads));
+    p.per_sm = std::max(1, most);
     while (p.per_sm > 1 && p.per_sm * 3 * stage_bytes > kRingBytes)
         --p.per_sm;
     p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, kRingBytes / (p.per_sm * stage_bytes))));
@@ -706,7 +752,7 @@ int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     const WideShape w = fwd_shape(a.cols);
     const int64_t bytes = static_cast<int64_t>(w.nv) * w.threads * 8 * sizeof(T) * (a.residual ? 2 : 1);
-    const RingPlan p = ring_plan(bytes, w.threads, 16);
+    const RingPlan p = ring_plan(bytes, std::min(16, 1024 / w.threads));
     const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a.rows + per_cta - 1) / per_cta, int64_t{d.sms} * p.per_sm));
     const size_t smem = static_cast<size_t>(bytes) * p.stages;
@@ -723,6 +769,8 @@ int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     return launch_ring(norm_fwd_kernel<T, TY, 0, 2>, a, grid, w.threads, p.stages, smem, s);
 }
 
+int bwd_per_sm(const WideShape& w) { return std::min(4, kBwdThreads / w.threads); }
+
 // CTAs of the backward kernel, each with its partial sums: at most four an SM
 // (152 SMs).  A pure function of the shape: the workspace is sized by it.
 constexpr int kPartSms = 152;
@@ -730,8 +778,7 @@ int64_t bwd_ctas(int64_t rows, int64_t cols)
 {
     const WideShape w = bwd_shape(cols);
     const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
-    const int64_t per_sm = w.lpr ? 2 : std::max(1, std::min(4, 1024 / w.threads));
-    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * per_sm);
+    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * bwd_per_sm(w));
 }
 
 template <typename T, typename TY, bool FROM8>
@@ -740,7 +787,7 @@ int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
     const WideShape w = bwd_shape(a.cols);
     const int64_t oct = static_cast<int64_t>(w.nv) * w.threads * 8;
     const int64_t bytes = oct * (sizeof(TY) + (FROM8 ? 1 : sizeof(T)) + (a.dres ? sizeof(T) : 0));
-    const RingPlan p = ring_plan(bytes, w.threads, w.lpr ? 2 : 4);
+    const RingPlan p = ring_plan(bytes, bwd_per_sm(w));
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(bwd_ctas(a.rows, a.cols), int64_t{d.sms} * p.per_sm));
     // the column sums of a warp-per-row CTA pass through the ring's memory
     const size_t smem = std::max<size_t>(static_cast<size_t>(bytes) * p.stages, w.lpr ? w.nv * w.lpr * 8 * 4 * (w.threads / 32) : 0);
@@ -755,13 +802,13 @@ int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
         rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 2>, a, grid, w.threads, p.stages, smem, s);
     else if (w.lpr == 32)
         rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 4>, a, grid, w.threads, p.stages, smem, s);
-    else if (w.nv == 1)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 1>, a, grid, w.threads, p.stages, smem, s);
-    else
+    else if (w.nv == 2)
         rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 2>, a, grid, w.threads, p.stages, smem, s);
+    else
+        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 4>, a, grid, w.threads, p.stages, smem, s);
     if (rc != MX_OK || (!a.dw && !a.db))
         return rc;
-    norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kRowThreads, 0, s>>>(
+    norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kJoinWarps * 32, 0, s>>>(
         a.parts, a.cols, static_cast<int>(grid), a.dw, a.db);
     count_launch();
     return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
@@ -794,7 +841,7 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
         const int parts = static_cast<int>(any_parts(a.rows));
         const unsigned cols32 = static_cast<unsigned>((a.cols + 31) / 32);
         norm_dw_any_kernel<T, TY><<<dim3(cols32, parts), kRowThreads, 0, s>>>(a);
-        norm_dw_join_kernel<<<dim3(cols32, 2), kRowThreads, 0, s>>>(a.parts, a.cols, parts, a.dw, a.db);
+        norm_dw_join_kernel<<<dim3(cols32, 2), kJoinWarps * 32, 0, s>>>(a.parts, a.cols, parts, a.dw, a.db);
         count_launch();
         count_launch();
     }
