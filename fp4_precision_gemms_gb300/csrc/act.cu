@@ -51,10 +51,10 @@ __device__ __forceinline__ void save_group(float v, const Act8View& out, int64_t
     const int lane = threadIdx.x & 31;
     const float z = finite_or_nan(v);
     const float b = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(z), 0.0f))));
-    const int e = act8_exponent(b);
-    out.codes[group * kAct8Group + lane] = static_cast<uint8_t>(cvt_e4m3x2(z * exp2_neg(e), 0.0f));
+    const uint32_t e = act8_byte(b);
+    out.codes[group * kAct8Group + lane] = static_cast<uint8_t>(cvt_e4m3x2(z * act8_inverse(e), 0.0f));
     if (lane == 0)
-        out.sf[group] = static_cast<uint8_t>(e + 127);
+        out.sf[group] = static_cast<uint8_t>(e);
 }
 
 __device__ __forceinline__ float restored(const Act8View& a, int64_t group, int lane)
@@ -209,12 +209,12 @@ __device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& 
 
 __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, bool in, const Oct& o)
 {
-    int e;
+    uint8_t e;
     const uint2 codes = encode_oct(o, e);
     if (in) {
         *reinterpret_cast<uint2*>(out.codes + unit * 8) = codes;
         if ((threadIdx.x & 3) == 0)
-            out.sf[unit >> 2] = static_cast<uint8_t>(e + 127);
+            out.sf[unit >> 2] = e;
     }
 }
 

@@ -31,8 +31,19 @@ __device__ __forceinline__ float as_stored(float v)
 // the conversion turns it into the NaN code.
 __device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.0f, x); }
 
-// Exponent of a group whose largest finite |x| is b, and 2^-e.
-__device__ __forceinline__ int act8_exponent(float b) { return pow2_exponent<kElemE4M3>(b, MX_SCALE_CEIL); }
+// Exponent byte e + 127 of a group whose largest finite |x| is b, the CEIL rule
+// in four integer operations: 448 = 1.75 * 2^8, so e + 127 is b's exponent field
+// less 8, and one more when its fraction is above 0.75, which is when adding
+// 2^21 - 1 to it carries.  Subnormal b fall below the byte's lower end like the
+// smallest normal ones; b = 0 has e = 0.
+__device__ __forceinline__ uint32_t act8_byte(float b)
+{
+    const uint32_t u = __float_as_uint(b);
+    const int byte = max(static_cast<int>((u + 0x1FFFFFu) >> 23) - 8, 0);
+    return u == 0 ? 127u : static_cast<uint32_t>(byte);
+}
+// 2^-e = 2^(127 - byte), for the bytes that act8_byte gives (0 to 247)
+__device__ __forceinline__ float act8_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
 // Two E4M3 codes (low byte first) as floats; both conversions are exact.
 __device__ __forceinline__ float2 dec_e4m3x2(uint32_t two)
@@ -252,7 +263,7 @@ __device__ __forceinline__ bool non_finite(float v) { return (__float_as_uint(v)
 // each (0 past the row's end).  Executed by whole warps.  Groups without Inf
 // and NaN take one maximum and one product per value; a warp that has one of
 // the others repeats the maximum over the finite values.
-__device__ __forceinline__ uint2 encode_oct(Oct z, int& e)
+__device__ __forceinline__ uint2 encode_oct(Oct z, uint8_t& byte)
 {
     float m = max_abs(max_abs(max_abs(max_abs(0.0f, z.p[0]), z.p[1]), z.p[2]), z.p[3]);
     m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
@@ -267,8 +278,9 @@ __device__ __forceinline__ uint2 encode_oct(Oct z, int& e)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     }
-    e = act8_exponent(m);
-    const float2 s = both(exp2_neg(e));
+    const uint32_t e = act8_byte(m);
+    byte = static_cast<uint8_t>(e);
+    const float2 s = both(act8_inverse(e));
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         z.p[k] = __fmul2_rn(z.p[k], s);

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_fwd_any_kernel(NormFwdArgs a
             const float d = load_f(x + c) - mean;
             sq += d * d;
         }
-        const float rstd = 1.0f / sqrtf(cta_sum(sq, part) * inv_c + a.eps);
+        const float rstd = rsqrtf(cta_sum(sq, part) * inv_c + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean && a.kind == MX_NORM_LAYER)
                 a.mean[r] = mean;
@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kRowThreads) norm_fwd_any_kernel(NormFwdArgs a
             if (a.save.codes) {
                 const float z = finite_or_nan(v);
                 const float b = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(z), 0.0f))));
-                const int e = act8_exponent(b);
+                const uint32_t e = act8_byte(b);
                 a.save.codes[(r * G + g) * kAct8Group + lane] =
-                    static_cast<uint8_t>(cvt_e4m3x2(z * exp2_neg(e), 0.0f));
+                    static_cast<uint8_t>(cvt_e4m3x2(z * act8_inverse(e), 0.0f));
                 if (lane == 0)
-                    a.save.sf[r * G + g] = static_cast<uint8_t>(e + 127);
+                    a.save.sf[r * G + g] = static_cast<uint8_t>(e);
             }
         }
     }
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const flo
 // for the ring.
 constexpr int kMaxWide = 16384;
 constexpr int kSubThreads = 256;  // CTA size where several rows share a CTA
-constexpr int kBwdThreads = 512;  // most threads of a backward CTA: 128 registers each
+constexpr int kMaxThreads = 512;  // of a CTA: 128 registers each
 
 template <typename T>
 __device__ __forceinline__ constexpr int chunks() { return sizeof(T) / 2; }  // 16-byte words of an oct
@@ -249,7 +249,7 @@ struct RowMap {
 };
 
 // Sums over a row's threads, known to all of them; a CTA's row goes through
-// `part` (32 entries, zero past the CTA's warps; two of them used in turn, so
+// `part` (one entry a warp, zero past the CTA's; two of them used in turn, so
 // that one barrier per sum is enough).
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v, float* part)
@@ -261,10 +261,13 @@ __device__ __forceinline__ float row_sum(float v, float* part)
         if ((threadIdx.x & 31) == 0)
             part[threadIdx.x >> 5] = v;
         __syncthreads();
-        float2 s = make_float2(0.0f, 0.0f);
-        for (unsigned w = 0; w < blockDim.x / 32; w += 4) {
-            const float4 p = *reinterpret_cast<const float4*>(part + w);
-            s = __fadd2_rn(s, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
+        const float4 p = *reinterpret_cast<const float4*>(part), q = *reinterpret_cast<const float4*>(part + 4);
+        float2 s = __fadd2_rn(__fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)),
+                              __fadd2_rn(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+        if (blockDim.x > 256) {
+            const float4 t = *reinterpret_cast<const float4*>(part + 8), u = *reinterpret_cast<const float4*>(part + 12);
+            s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(make_float2(t.x, t.y), make_float2(t.z, t.w)),
+                                         __fadd2_rn(make_float2(u.x, u.y), make_float2(u.z, u.w))));
         }
         v = s.x + s.y;
     }
@@ -295,10 +298,17 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* part)
             reinterpret_cast<float*>(part)[(threadIdx.x >> 5) * 2 + (second ? 1 : 0)] = s;
         __syncthreads();
         float2 sum = make_float2(0.0f, 0.0f);
-        for (unsigned w = 0; w < blockDim.x / 32; w += 2) {
+#pragma unroll
+        for (int w = 0; w < 8; w += 2) {
             const float4 p = *reinterpret_cast<const float4*>(part + w);
             sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
         }
+        if (blockDim.x > 256)
+#pragma unroll
+            for (int w = 8; w < 16; w += 2) {
+                const float4 p = *reinterpret_cast<const float4*>(part + w);
+                sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
+            }
         return sum;
     }
 }
@@ -343,13 +353,13 @@ __device__ __forceinline__ void slot_read(uint32_t slots, int j, Oct& o)
 }
 
 template <typename T, typename TY, int LPR, int NV>
-__global__ void __launch_bounds__(LPR ? kSubThreads : 1024, LPR ? 4 : 1) norm_fwd_kernel(NormFwdArgs a, int stages)
+__global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_fwd_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float part[2][32];
+    __shared__ __align__(16) float part[2][kMaxThreads / 32];
     if (LPR == 0) {
-        if (threadIdx.x < 64)
-            part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
+        if (threadIdx.x < kMaxThreads / 32)
+            part[0][threadIdx.x] = part[1][threadIdx.x] = 0.0f;
         __syncthreads();
     }
     const RowMap<LPR> map(a.rows);
@@ -380,6 +390,15 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : 1024, LPR ? 4 : 1) norm_fw
         copy_commit();
     };
 
+    constexpr bool KEEP = NV <= 2;  // weights and biases stay in registers
+    Oct wt[KEEP ? NV : 1], bi[KEEP ? NV : 1];
+    if constexpr (KEEP)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (c0 + j * dc < C) {
+                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
+                param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, bi[j]);
+            }
     Top<TY> top;
     Top<T> sum_top;
     T* to_sum = static_cast<T*>(a.sum_out) + map.first * a.lds + c0;
@@ -429,7 +448,7 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : 1024, LPR ? 4 : 1) norm_fw
                     sq2 = __ffma2_rn(d, d, sq2);
                 }
         // RMS norm has one sum per row: its words alternate with the row
-        const float rstd = 1.0f / sqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1]) * inv_c + a.eps);
+        const float rstd = rsqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1]) * inv_c + a.eps);
         if (map.t == 0 && in) {
             const int64_t r = map.first + it * map.step;
             if (a.mean && layer)
@@ -440,23 +459,25 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : 1024, LPR ? 4 : 1) norm_fw
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (in && c0 + j * dc < C) {
-                Oct w, b;
-                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, w);
-                param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, b);
+                Oct &w = wt[KEEP ? j : 0], &b = bi[KEEP ? j : 0], y;
+                if constexpr (!KEEP) {
+                    param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, w);
+                    param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, b);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 h = __fmul2_rn(__fadd2_rn(v[j].p[k], both(-mean)), both(rstd));
-                    b.p[k] = __ffma2_rn(h, w.p[k], b.p[k]);
+                    y.p[k] = __ffma2_rn(h, w.p[k], b.p[k]);
                 }
-                store_oct(to_y + j * dc, b, top);
+                store_oct(to_y + j * dc, y, top);
             }
             if (a.save.codes) {
-                int e;
+                uint8_t e;
                 const uint2 codes = encode_oct(v[j], e);
                 if (in && c0 + j * dc < G * kAct8Group) {
                     *reinterpret_cast<uint2*>(to_codes + j * dc) = codes;
                     if ((threadIdx.x & 3) == 0)
-                        to_sf[j * dc / kAct8Group] = static_cast<uint8_t>(e + 127);
+                        to_sf[j * dc / kAct8Group] = e;
                 }
             }
         }
@@ -476,14 +497,14 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : 1024, LPR ? 4 : 1) norm_fw
 // it in registers (up to two octs a thread) or from a second reading of shared
 // memory.
 template <typename T, typename TY, bool FROM8, int LPR, int NV>
-__global__ void __launch_bounds__(LPR ? kSubThreads : kBwdThreads, LPR ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, int stages)
+__global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, int stages)
 {
     constexpr bool KEEP = NV <= 2;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float2 part[2][32];
+    __shared__ __align__(16) float2 part[2][kMaxThreads / 32];
     if (LPR == 0) {
-        if (threadIdx.x < 64)
-            part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.0f, 0.0f);
+        if (threadIdx.x < kMaxThreads / 32)
+            part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
         __syncthreads();
     }
     const RowMap<LPR> map(a.rows);
@@ -690,40 +711,35 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kBwdThreads, LPR ? 2 : 1) 
 }
 
 // How a width is spread over threads: octs of whole groups, so that a group's
-// four lanes all exist.
+// four lanes all exist.  Two octs a thread as long as 512 threads suffice (the
+// weights, the column sums and a row's values then fit 128 registers), four
+// above 8192 columns.  Up to 512 columns a warp, or a part of one, takes a row.
 struct WideShape {
     int lpr, nv, threads;
 };
-WideShape fwd_shape(int64_t cols)
+WideShape wide_shape(int64_t cols)
 {
     const int octs = static_cast<int>(act8_groups(cols)) * 4;
-    if (octs <= 8)
-        return {8, 1, kSubThreads};
     if (octs <= 16)
-        return {16, 1, kSubThreads};
-    if (octs <= 128)
-        return {32, octs <= 32 ? 1 : octs <= 64 ? 2 : 4, kSubThreads};
-    return {0, 2, ((octs + 1) / 2 + 31) / 32 * 32};
-}
-// At most 512 threads, so that each may use 128 registers: they hold the column
-// sums and, up to two octs a thread, the weights and a row's g and h.
-WideShape bwd_shape(int64_t cols)
-{
-    const WideShape f = fwd_shape(cols);
-    return f.threads <= kBwdThreads ? f : WideShape{0, 4, (f.threads / 2 + 31) / 32 * 32};
+        return {octs <= 8 ? 8 : 16, 1, kSubThreads};
+    if (octs <= 64)
+        return {32, octs <= 32 ? 1 : 2, kSubThreads};
+    const int nv = octs <= 2 * kMaxThreads ? 2 : 4;
+    return {0, nv, ((octs + nv - 1) / nv + 31) / 32 * 32};
 }
 
 constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
-// Rows in flight of a CTA and CTAs of an SM, from the bytes of one row's slots:
-// three stages where they fit.
+// CTAs of an SM and rows in flight of each, from the bytes of one row's slots:
+// as many CTAs as registers allow, with three stages where they fit.
 struct RingPlan {
-    int stages, per_sm;
+    int per_sm, stages;
 };
-RingPlan ring_plan(int64_t stage_bytes, int most)
+RingPlan ring_plan(int64_t stage_bytes, int threads, int registers)
 {
     RingPlan p;
-    p.per_sm = std::max(1, most);
-    while (p.per_sm > 1 && p.per_sm * 3 * stage_bytes > kRingBytes)
+    p.per_sm = std::min(32, std::min(65536 / ((registers + 7) / 8 * 8 * threads), 2048 / threads));
+    p.per_sm = std::max(1, p.per_sm);
+    while (p.per_sm > 1 && p.per_sm * 2 * stage_bytes > kRingBytes)
         --p.per_sm;
     p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, kRingBytes / (p.per_sm * stage_bytes))));
     return p;
@@ -735,83 +751,105 @@ bool wide_rows(const void* p, int64_t ld, int bytes)
 }
 bool wide_cols(int64_t cols) { return cols % 8 == 0 && cols <= kMaxWide; }
 
-template <typename K, typename A>
-int launch_ring(K kernel, const A& a, unsigned grid, int threads, int stages, size_t smem, cudaStream_t s)
+int launched()
 {
-    if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
-       
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return MX_ERR_CUDA;
-    kernel<<<grid, threads, smem, s>>>(a, stages);
     count_launch();
     return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+// Launches a ring kernel: its grid fills the GPU, or covers the rows, and has
+// at most `most` CTAs.  `grid` returns it.
+template <void (*KERNEL)(NormFwdArgs, int)>
+int registers_of()
+{
+    static const int n = [] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
+    }();
+    return n;
+}
+template <void (*KERNEL)(NormBwdArgs, int)>
+int registers_of()
+{
+    static const int n = [] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
+    }();
+    return n;
+}
+template <auto KERNEL, typename A>
+int launch_ring(const A& a, const WideShape& w, int64_t stage_bytes, size_t least_smem, int64_t most, unsigned* grid,
+                const Device& d, cudaStream_t s)
+{
+    const RingPlan p = ring_plan(stage_bytes, w.threads, registers_of<KERNEL>());
+    const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1, ctas = (a.rows + per_cta - 1) / per_cta;
+    *grid = static_cast<unsigned>(std::min(most, std::min<int64_t>(ctas, int64_t{d.sms} * p.per_sm)));
+    const size_t smem = std::max(static_cast<size_t>(stage_bytes) * p.stages, least_smem);
+    if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
+        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return MX_ERR_CUDA;
+    KERNEL<<<*grid, w.threads, smem, s>>>(a, p.stages);
+    return launched();
 }
 
 template <typename T, typename TY>
 int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
-    const WideShape w = fwd_shape(a.cols);
+    const WideShape w = wide_shape(a.cols);
     const int64_t bytes = static_cast<int64_t>(w.nv) * w.threads * 8 * sizeof(T) * (a.residual ? 2 : 1);
-    const RingPlan p = ring_plan(bytes, std::min(16, 1024 / w.threads));
-    const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a.rows + per_cta - 1) / per_cta, int64_t{d.sms} * p.per_sm));
-    const size_t smem = static_cast<size_t>(bytes) * p.stages;
+    const int64_t most = INT32_MAX;
+    unsigned grid;
     if (w.lpr == 8)
-        return launch_ring(norm_fwd_kernel<T, TY, 8, 1>, a, grid, w.threads, p.stages, smem, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 8, 1>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.lpr == 16)
-        return launch_ring(norm_fwd_kernel<T, TY, 16, 1>, a, grid, w.threads, p.stages, smem, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 16, 1>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.lpr == 32 && w.nv == 1)
-        return launch_ring(norm_fwd_kernel<T, TY, 32, 1>, a, grid, w.threads, p.stages, smem, s);
-    if (w.lpr == 32 && w.nv == 2)
-        return launch_ring(norm_fwd_kernel<T, TY, 32, 2>, a, grid, w.threads, p.stages, smem, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 32, 1>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.lpr == 32)
-        return launch_ring(norm_fwd_kernel<T, TY, 32, 4>, a, grid, w.threads, p.stages, smem, s);
-    return launch_ring(norm_fwd_kernel<T, TY, 0, 2>, a, grid, w.threads, p.stages, smem, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 32, 2>>(a, w, bytes, 0, most, &grid, d, s);
+    if (w.nv == 2)
+        return launch_ring<norm_fwd_kernel<T, TY, 0, 2>>(a, w, bytes, 0, most, &grid, d, s);
+    return launch_ring<norm_fwd_kernel<T, TY, 0, 4>>(a, w, bytes, 0, most, &grid, d, s);
 }
 
-int bwd_per_sm(const WideShape& w) { return std::min(4, kBwdThreads / w.threads); }
-
-// CTAs of the backward kernel, each with its partial sums: at most four an SM
-// (152 SMs).  A pure function of the shape: the workspace is sized by it.
+// Most CTAs of the backward kernel, each with its partial sums: 512 threads an
+// SM, 152 SMs.  A pure function of the shape: the workspace is sized by it.
 constexpr int kPartSms = 152;
 int64_t bwd_ctas(int64_t rows, int64_t cols)
 {
-    const WideShape w = bwd_shape(cols);
+    const WideShape w = wide_shape(cols);
     const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
-    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * bwd_per_sm(w));
+    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * std::min(8, kMaxThreads / w.threads));
 }
 
 template <typename T, typename TY, bool FROM8>
 int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
-    const WideShape w = bwd_shape(a.cols);
-    const int64_t oct = static_cast<int64_t>(w.nv) * w.threads * 8;
-    const int64_t bytes = oct * (sizeof(TY) + (FROM8 ? 1 : sizeof(T)) + (a.dres ? sizeof(T) : 0));
-    const RingPlan p = ring_plan(bytes, bwd_per_sm(w));
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(bwd_ctas(a.rows, a.cols), int64_t{d.sms} * p.per_sm));
+    const WideShape w = wide_shape(a.cols);
+    const int64_t bytes =
+        static_cast<int64_t>(w.nv) * w.threads * 8 * (sizeof(TY) + (FROM8 ? 1 : sizeof(T)) + (a.dres ? sizeof(T) : 0));
+    const int64_t most = bwd_ctas(a.rows, a.cols);
     // the column sums of a warp-per-row CTA pass through the ring's memory
-    const size_t smem = std::max<size_t>(static_cast<size_t>(bytes) * p.stages, w.lpr ? w.nv * w.lpr * 8 * 4 * (w.threads / 32) : 0);
+    const size_t least = w.lpr ? static_cast<size_t>(w.nv) * w.lpr * 8 * sizeof(float) * (w.threads / 32) : 0;
+    unsigned grid;
     int rc;
     if (w.lpr == 8)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 8, 1>, a, grid, w.threads, p.stages, smem, s);
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 8, 1>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 16)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 16, 1>, a, grid, w.threads, p.stages, smem, s);
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 16, 1>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 32 && w.nv == 1)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 1>, a, grid, w.threads, p.stages, smem, s);
-    else if (w.lpr == 32 && w.nv == 2)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 2>, a, grid, w.threads, p.stages, smem, s);
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 1>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 32)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 32, 4>, a, grid, w.threads, p.stages, smem, s);
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 2>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.nv == 2)
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 2>, a, grid, w.threads, p.stages, smem, s);
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 2>>(a, w, bytes, least, most, &grid, d, s);
     else
-        rc = launch_ring(norm_bwd_kernel<T, TY, FROM8, 0, 4>, a, grid, w.threads, p.stages, smem, s);
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 4>>(a, w, bytes, least, most, &grid, d, s);
     if (rc != MX_OK || (!a.dw && !a.db))
         return rc;
     norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kJoinWarps * 32, 0, s>>>(
         a.parts, a.cols, static_cast<int>(grid), a.dw, a.db);
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    return launched();
 }
 
 int64_t any_parts(int64_t rows) { return std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, 64); }
