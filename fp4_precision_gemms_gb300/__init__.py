@@ -36,7 +36,7 @@ EXPORTED = ("mx_codes_bytes", "mx_sf_bytes", "mx_scale_count", "mx_amax", "mx_qu
             "mx_act8_codes_bytes", "mx_act8_sf_bytes", "mx_act8_save", "mx_act8_restore", "mx_norm_fwd",
             "mx_norm_bwd_workspace_bytes", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd",
             "mx_last_device_status", "mx_selftest_bounded_wait", "mx_launch_count",
-            "mx_debug_divide", "mx_debug_set_quant_impl", "mx_debug_set_tile_fail_at", "mx_debug_set_bwd_fork", "mx_debug_set_gemm_variant",
+            "mx_debug_divide", "mx_debug_set_quant_impl", "mx_debug_set_tile_fail_at", "mx_debug_set_norm_fail_at", "mx_debug_set_bwd_fork", "mx_debug_set_gemm_variant",
             "mx_debug_last_gemm_variant")
 
 
@@ -101,6 +101,8 @@ def lib():
             L.mx_debug_set_quant_impl.argtypes = [i32]
             L.mx_debug_set_tile_fail_at.restype = None
             L.mx_debug_set_tile_fail_at.argtypes = [i64]
+            L.mx_debug_set_norm_fail_at.restype = None
+            L.mx_debug_set_norm_fail_at.argtypes = [i64]
             L.mx_debug_set_bwd_fork.restype = None
             L.mx_debug_set_bwd_fork.argtypes = [i32]
             L.mx_dequantize.restype = i32
@@ -291,6 +293,11 @@ def set_quant_impl(impl: str) -> None:
 def set_tile_fail_at(tile: int) -> None:
     """Test hook: the tile producer gives up its wait on this tile of each CTA (-1: off)."""
     lib().mx_debug_set_tile_fail_at(int(tile))
+
+
+def set_norm_fail_at(row: int) -> None:
+    """Test hook: the norm kernels give up their wait for this row of each CTA (-1: off)."""
+    lib().mx_debug_set_norm_fail_at(int(row))
 
 
 def set_bwd_fork(on: bool) -> None:

@@ -139,6 +139,9 @@ struct NormFwdArgs {
     unsigned* amax;
     float eps;
     int x_dtype, y_dtype, w_dtype, kind;
+    int* status;
+    uint64_t wait_ns;
+    int64_t fail_at;  // test hook: in this row of each CTA a wait counts as run out; -1 never
 };
 struct NormBwdArgs {
     const void* dy;
@@ -156,6 +159,9 @@ struct NormBwdArgs {
     float* parts;  // workspace: partial sums of dw, then of db
     unsigned* amax;
     int dy_dtype, dx_dtype, w_dtype, kind;
+    int* status;
+    uint64_t wait_ns;
+    int64_t fail_at;
 };
 struct ActArgs {  // forward: h written; backward: h is dh, read
     const void* gate;

@@ -68,9 +68,13 @@ int zero(void* p, size_t bytes, cudaStream_t s)
     return !p || bytes == 0 || cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
 }
 
+thread_local int64_t g_norm_fail_at = -1;  // test hook: the norm kernels' forced wait failure
+
 }  // namespace
 
 extern "C" {
+
+void mx_debug_set_norm_fail_at(int64_t row) { g_norm_fail_at = row; }
 
 size_t mx_act8_codes_bytes(int64_t rows, int64_t cols)
 {
@@ -162,6 +166,9 @@ int mx_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, i
     a.y_dtype = y_dtype;
     a.w_dtype = w_dtype;
     a.kind = kind;
+    a.status = d.status;
+    a.wait_ns = kWaitLimitNs;
+    a.fail_at = g_norm_fail_at;
     return launch_norm_fwd(a, d, s);
 }
 
@@ -230,6 +237,9 @@ int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_
     a.dx_dtype = dx_dtype;
     a.w_dtype = w_dtype;
     a.kind = kind;
+    a.status = d.status;
+    a.wait_ns = kWaitLimitNs;
+    a.fail_at = g_norm_fail_at;
     return launch_norm_bwd(a, d, s);
 }
 

@@ -219,13 +219,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const flo
 // lie in four neighbouring lanes.  LPR > 0: LPR lanes of a warp per row, the
 // rows of a CTA independent; LPR = 0: the CTA's blockDim.x threads per row.
 //
-// The grid is persistent, and each thread copies its own words of the rows that
-// its CTA takes next into its own slots of a shared-memory ring (`stages` rows
-// deep): the memory system stays busy through the row sums, without a barrier
-// for the ring.
+// The grid is persistent, and a shared-memory ring holds the rows that a CTA
+// takes next, so that the memory system stays busy through the row sums.
+//
+// LPR = 0: one thread issues a bulk copy per matrix and row, which costs the
+// other threads nothing (per-thread copies took about 60 of a warp's 470
+// instructions a row); a stage's mbarrier says when it has arrived, and the
+// barrier of the row sums that a row ago's stage may be filled again.
+// LPR > 0: each thread copies its own words into its own slots, which needs no
+// barrier between the warps' rows.
 constexpr int kMaxWide = 16384;
 constexpr int kSubThreads = 256;  // CTA size where several rows share a CTA
 constexpr int kMaxThreads = 512;  // of a CTA: 128 registers each
+constexpr int kMaxStages = 6;
+constexpr int kBarBytes = (kMaxStages * 8 + 15) / 16 * 16;
 
 template <typename T>
 __device__ __forceinline__ constexpr int chunks() { return sizeof(T) / 2; }  // 16-byte words of an oct
@@ -252,7 +259,7 @@ struct RowMap {
 // `part` (one entry a warp, zero past the CTA's; two of them used in turn, so
 // that one barrier per sum is enough).
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v, float* part)
+__device__ __forceinline__ float row_sum(float v, float* part, bool& bad)
 {
 #pragma unroll
     for (int o = (LPR ? LPR : 32) / 2; o > 0; o >>= 1)
@@ -260,7 +267,7 @@ __device__ __forceinline__ float row_sum(float v, float* part)
     if constexpr (LPR == 0) {
         if ((threadIdx.x & 31) == 0)
             part[threadIdx.x >> 5] = v;
-        __syncthreads();
+        bad = __syncthreads_or(bad);
         const float4 p = *reinterpret_cast<const float4*>(part), q = *reinterpret_cast<const float4*>(part + 4);
         float2 s = __fadd2_rn(__fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)),
                               __fadd2_rn(make_float2(q.x, q.y), make_float2(q.z, q.w)));
@@ -276,7 +283,7 @@ __device__ __forceinline__ float row_sum(float v, float* part)
 // Two sums.  Where a warp belongs to one row its halves exchange the sums, so
 // that each half finishes one of them.
 template <int LPR>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* part)
+__device__ __forceinline__ float2 row_sum2(float2 v, float2* part, bool& bad)
 {
     if constexpr (LPR != 0 && LPR < 32) {
 #pragma unroll
@@ -296,7 +303,7 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* part)
             return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
         if ((threadIdx.x & 15) == 0)
             reinterpret_cast<float*>(part)[(threadIdx.x >> 5) * 2 + (second ? 1 : 0)] = s;
-        __syncthreads();
+        bad = __syncthreads_or(bad);
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < 8; w += 2) {
@@ -328,29 +335,179 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
     }
 }
 
-// A thread's slots of one matrix in a ring stage: 16-byte words, a word's slots
-// of all threads side by side.  `slots` is the thread's first.
-template <typename T>
-__device__ __forceinline__ void slot_fill(uint32_t slots, int j, const T* src)
-{
+// The ring of PARTS matrices.  A matrix may be absent (null).  Its octs take
+// OB bytes: 16 (bf16), 32 (fp32) or 8 (codes).
+struct RingPart {
+    const char* src;    // row 0
+    int64_t row_bytes;  // from one row to the next
+    int oct;            // bytes of an oct
+    uint32_t at;        // in a stage
+};
+template <int LPR, int NV, int PARTS>
+struct RowRing {
+    RingPart part[PARTS];
+    uint32_t base, stage_bytes, bars;
+    int stages, stage = 0, octs;
+    uint32_t phase = 0;
+
+    // `octs` of a row to copy.  A stage's parts lie one after the other; LPR > 0:
+    // words of NV octs for every thread of the CTA.
+    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int octs_)
+    {
+        stages = stages_;
+        octs = octs_;
+        bars = smem_u32(smem);
+        base = bars + (LPR == 0 ? kBarBytes : 0);
+        uint32_t at = 0;
 #pragma unroll
-    for (int h = 0; h < chunks<T>(); ++h)
-        copy_async16(slots + (j * chunks<T>() + h) * blockDim.x * 16, src + h * (16 / sizeof(T)));
-}
-template <typename T>
-__device__ __forceinline__ void slot_read(uint32_t slots, int j, Oct& o)
-{
-    if constexpr (sizeof(T) == 2) {
-        unpack_oct(lds128(slots + j * blockDim.x * 16), o);
-    } else {
-        const uint4 a = lds128(slots + 2 * j * blockDim.x * 16);
-        const uint4 b = lds128(slots + (2 * j + 1) * blockDim.x * 16);
-        o.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-        o.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
-        o.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-        o.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+        for (int m = 0; m < PARTS; ++m) {
+            part[m].at = at;
+            if (part[m].src)
+                at += (LPR == 0 ? (octs * part[m].oct + 15) / 16 * 16 : NV * blockDim.x * part[m].oct);
+        }
+        stage_bytes = at;
     }
-}
+
+    // ---- LPR = 0
+    // Row r into stage st (one thread).
+    __device__ __forceinline__ void fill(int64_t r, int st)
+    {
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int m = 0; m < PARTS; ++m)
+            if (part[m].src)
+                bytes += (octs * part[m].oct + 15) / 16 * 16;
+        mbar_arrive_expect_tx(bars + st * 8, bytes);
+#pragma unroll
+        for (int m = 0; m < PARTS; ++m)
+            if (part[m].src)
+                bulk_load(base + st * stage_bytes + part[m].at, part[m].src + r * part[m].row_bytes,
+                          (octs * part[m].oct + 15) / 16 * 16, bars + st * 8);
+    }
+    __device__ __forceinline__ bool wait(uint64_t limit_ns) { return mbar_wait_bounded(bars + stage * 8, phase, limit_ns); }
+
+    // ---- both
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    // Thread's word h of oct j of matrix m in the current stage.
+    __device__ __forceinline__ uint32_t word(int m, int j, int h) const
+    {
+        const uint32_t at = base + stage * stage_bytes + part[m].at;
+        if constexpr (LPR == 0)
+            return at + (threadIdx.x + j * blockDim.x) * part[m].oct + h * 16;
+        const int w = min(part[m].oct, 16);
+        return at + ((j * (part[m].oct / w) + h) * blockDim.x + threadIdx.x) * w;
+    }
+    template <typename T>
+    __device__ __forceinline__ void read(int m, int j, Oct& o) const
+    {
+        if constexpr (sizeof(T) == 2) {
+            unpack_oct(lds128(word(m, j, 0)), o);
+        } else {
+            const uint4 a = lds128(word(m, j, 0)), b = lds128(word(m, j, 1));
+            o.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+            o.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+            o.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+            o.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+        }
+    }
+    __device__ __forceinline__ uint2 read_codes(int m, int j) const
+    {
+        uint2 w;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(word(m, j, 0)) : "memory");
+        return w;
+    }
+
+    // ---- LPR > 0
+    // The thread's octs of row r into the stage `ahead` rows on.
+    __device__ __forceinline__ void copy(int64_t r, bool in, int ahead, int t)
+    {
+        if (in) {
+            int st = stage + ahead;
+            st -= st >= stages ? stages : 0;
+            const uint32_t to = base + st * stage_bytes;
+#pragma unroll
+            for (int m = 0; m < PARTS; ++m)
+                if (part[m].src) {
+                    const char* row = part[m].src + r * part[m].row_bytes;
+                    const int w = min(part[m].oct, 16);
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+                        if (t + j * LPR < octs)
+#pragma unroll
+                            for (int h = 0; h < part[m].oct / w; ++h) {
+                                const uint32_t dst =
+                                    to + part[m].at + ((j * (part[m].oct / w) + h) * blockDim.x + threadIdx.x) * w;
+                                const char* from = row + (t + j * LPR) * part[m].oct + h * 16;
+                                if (w == 16)
+                                    copy_async16(dst, from);
+                                else
+                                    copy_async8(dst, from);
+                            }
+                }
+        }
+        copy_commit();
+    }
+
+    // The first rows.
+    __device__ __forceinline__ void start(const RowMap<LPR>& map)
+    {
+        if constexpr (LPR == 0) {
+            if (threadIdx.x == 0) {
+                for (int i = 0; i < stages; ++i)
+                    mbar_init(bars + i * 8, 1);
+                fence_mbar_init();
+            }
+            __syncthreads();
+            if (threadIdx.x == 0)
+                for (int i = 0; i < stages && i < map.all; ++i)
+                    fill(map.first + i * map.step, i);
+        } else {
+            for (int i = 0; i < stages - 1; ++i)
+                copy(map.first + i * map.step, i < map.mine, i, map.t);
+        }
+    }
+    // Row `it` has arrived (false: the wait gave up).
+    __device__ __forceinline__ bool arrive(const RowMap<LPR>& map, int it, uint64_t limit_ns)
+    {
+        if constexpr (LPR == 0)
+            return wait(limit_ns);
+        copy(map.first + (it + stages - 1) * map.step, it + stages - 1 < map.mine, stages - 1, map.t);
+        copy_wait(stages - 1);
+        return true;
+    }
+    // LPR = 0, after a barrier in row `it`: nobody reads row it - 1 any more.
+    __device__ __forceinline__ void refill(const RowMap<LPR>& map, int it)
+    {
+        if (LPR == 0 && stages > 1 && threadIdx.x == 0 && it > 0 && it - 1 + stages < map.all)
+            fill(map.first + (it - 1 + stages) * map.step, stage == 0 ? stages - 1 : stage - 1);
+    }
+    // The end of row `it`.
+    __device__ __forceinline__ void done(const RowMap<LPR>& map, int it)
+    {
+        if (LPR == 0 && stages == 1) {
+            __syncthreads();
+            if (threadIdx.x == 0 && it + 1 < map.all)
+                fill(map.first + (it + 1) * map.step, 0);
+        }
+        next();
+    }
+    // Gave up in row `it`, before its refill: the copies in flight are waited
+    // for before the CTA's memory goes back.
+    __device__ __forceinline__ void abandon(const RowMap<LPR>& map, int it, uint64_t limit_ns)
+    {
+        if (LPR == 0 && threadIdx.x == 0)
+            for (int i = it; i < map.all && i < (it > 0 && stages > 1 ? it - 1 : it) + stages; ++i) {
+                wait(limit_ns);
+                next();
+            }
+    }
+};
 
 template <typename T, typename TY, int LPR, int NV>
 __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_fwd_kernel(NormFwdArgs a, int stages)
@@ -367,28 +524,10 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     const int c0 = 8 * map.t, dc = 8 * map.tpr;  // columns of oct j: c0 + j dc ..
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER, add = a.residual != nullptr;
-    const uint32_t one = NV * chunks<T>() * blockDim.x * 16;  // bytes of one matrix in a stage
-    const uint32_t stage_bytes = add ? 2 * one : one;
-    const uint32_t slots = smem_u32(ring) + threadIdx.x * 16;
-
-    const T* from_x = static_cast<const T*>(a.x) + map.first * a.ldx + c0;
-    const T* from_r = static_cast<const T*>(a.residual) + map.first * a.ldr + c0;
-    int filled = 0;
-    auto fill = [&](uint32_t at) {
-        if (filled < map.mine) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (c0 + j * dc < C) {
-                    slot_fill(at, j, from_x + j * dc);
-                    if (add)
-                        slot_fill(at + one, j, from_r + j * dc);
-                }
-        }
-        ++filled;
-        from_x += map.step * a.ldx;
-        from_r += map.step * a.ldr;
-        copy_commit();
-    };
+    RowRing<LPR, NV, 2> ring_;
+    ring_.part[0] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring_.part[1] = {static_cast<const char*>(a.residual), a.ldr * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring_.layout(ring, stages, C / 8);
 
     constexpr bool KEEP = NV <= 2;  // weights and biases stay in registers
     Oct wt[KEEP ? NV : 1], bi[KEEP ? NV : 1];
@@ -405,13 +544,11 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     TY* to_y = static_cast<TY*>(a.y) + map.first * a.ldy + c0;
     uint8_t* to_codes = a.save.codes + map.first * (G * kAct8Group) + c0;
     uint8_t* to_sf = a.save.sf + map.first * G + c0 / kAct8Group;
-    for (int i = 0; i < stages - 1; ++i)
-        fill(slots + i * stage_bytes);
-    int stage = 0;
-    for (int it = 0; it < map.all; ++it) {
-        fill(slots + (stage == 0 ? stages - 1 : stage - 1) * stage_bytes);  // the slots read a row ago
-        copy_wait(stages - 1);
-        const uint32_t here = slots + stage * stage_bytes;
+    ring_.start(map);
+    bool bad = false;
+    int it = 0;
+    for (; it < map.all; ++it) {
+        bad = !ring_.arrive(map, it, a.wait_ns) || (it == a.fail_at && threadIdx.x == blockDim.x - 1);
         const bool in = it < map.mine;
         Oct v[NV];
         float2 sum2 = make_float2(0.0f, 0.0f);
@@ -419,10 +556,10 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         for (int j = 0; j < NV; ++j) {
             v[j].fill(0.0f);
             if (in && c0 + j * dc < C) {
-                slot_read<T>(here, j, v[j]);
+                ring_.template read<T>(0, j, v[j]);
                 if (add) {
                     Oct q;
-                    slot_read<T>(here + one, j, q);
+                    ring_.template read<T>(1, j, q);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         q.p[k] = __fadd2_rn(v[j].p[k], q.p[k]);
@@ -437,7 +574,12 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
                     sum2 = __fadd2_rn(sum2, v[j].p[k]);
             }
         }
-        const float mean = layer ? row_sum<LPR>(sum2.x + sum2.y, part[0]) * inv_c : 0.0f;
+        float mean = 0.0f;
+        if (layer) {
+            mean = row_sum<LPR>(sum2.x + sum2.y, part[0], bad) * inv_c;
+            if (LPR == 0 && bad)
+                break;
+        }
         float2 sq2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -448,7 +590,10 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
                     sq2 = __ffma2_rn(d, d, sq2);
                 }
         // RMS norm has one sum per row: its words alternate with the row
-        const float rstd = rsqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1]) * inv_c + a.eps);
+        const float rstd = rsqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1], bad) * inv_c + a.eps);
+        if (LPR == 0 && bad)
+            break;
+        ring_.refill(map, it);
         if (map.t == 0 && in) {
             const int64_t r = map.first + it * map.step;
             if (a.mean && layer)
@@ -485,7 +630,13 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         to_y += map.step * a.ldy;
         to_codes += map.step * (G * kAct8Group);
         to_sf += map.step * G;
-        stage = stage + 1 == stages ? 0 : stage + 1;
+        ring_.done(map, it);
+    }
+    if (LPR == 0 && bad) {
+        if (threadIdx.x == 0)
+            atomicExch(a.status, MX_ERR_TIMEOUT);
+        ring_.abandon(map, it, a.wait_ns);
+        return;
     }
     if (a.amax)
         flush_top(a.amax, top);
@@ -512,39 +663,15 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     const int c0 = 8 * map.t, dc = 8 * map.tpr;
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER, add = a.dres != nullptr;
-    const uint32_t at_s = NV * chunks<TY>() * blockDim.x * 16;
-    const uint32_t at_r = at_s + (FROM8 ? NV * blockDim.x * 8 : NV * chunks<T>() * blockDim.x * 16);
-    const uint32_t stage_bytes = add ? at_r + NV * chunks<T>() * blockDim.x * 16 : at_r;
-    const uint32_t slots = smem_u32(ring) + threadIdx.x * 16;
+    RowRing<LPR, NV, 3> ring_;
+    ring_.part[0] = {static_cast<const char*>(a.dy), a.ldy * static_cast<int64_t>(sizeof(TY)), 8 * sizeof(TY), 0};
+    if constexpr (FROM8)
+        ring_.part[1] = {reinterpret_cast<const char*>(a.x8.codes), G * int64_t{kAct8Group}, 8, 0};
+    else
+        ring_.part[1] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring_.part[2] = {static_cast<const char*>(a.dres), a.ldres * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring_.layout(ring, stages, C / 8);
 
-    const TY* from_dy = static_cast<const TY*>(a.dy) + map.first * a.ldy + c0;
-    const T* from_x = static_cast<const T*>(a.x) + map.first * a.ldx + c0;
-    const uint8_t* from_codes = a.x8.codes + map.first * (G * kAct8Group) + c0;
-    const T* from_r = static_cast<const T*>(a.dres) + map.first * a.ldres + c0;
-    int filled = 0;
-    auto fill = [&](uint32_t at) {
-        if (filled < map.mine) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (c0 + j * dc < C) {
-                    slot_fill(at, j, from_dy + j * dc);
-                    if constexpr (FROM8)
-                        copy_async8(at + at_s + j * blockDim.x * 8 - threadIdx.x * 8, from_codes + j * dc);
-                    else
-                        slot_fill(at + at_s, j, from_x + j * dc);
-                    if (add)
-                        slot_fill(at + at_r, j, from_r + j * dc);
-                }
-        }
-        ++filled;
-        from_dy += map.step * a.ldy;
-        if constexpr (FROM8)
-            from_codes += map.step * (G * kAct8Group);
-        else
-            from_x += map.step * a.ldx;
-        from_r += map.step * a.ldres;
-        copy_commit();
-    };
     struct RowWords {  // what a row needs beside its matrices, loaded a row ahead
         float mean, rstd;
         uint32_t e[NV];
@@ -579,33 +706,26 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     }
     Top<T> top;
     T* to_dx = static_cast<T*>(a.dx) + map.first * a.lddx + c0;
-    for (int i = 0; i < stages - 1; ++i)
-        fill(slots + i * stage_bytes);
+    ring_.start(map);
     RowWords next = row_words(0 < map.mine);
-    int stage = 0;
-    for (int it = 0; it < map.all; ++it) {
+    bool bad = false;
+    int it = 0;
+    for (; it < map.all; ++it) {
         const bool in = it < map.mine;
         const RowWords cur = next;
         next = row_words(it + 1 < map.mine);
-        fill(slots + (stage == 0 ? stages - 1 : stage - 1) * stage_bytes);
-        copy_wait(stages - 1);
-        const uint32_t here = slots + stage * stage_bytes;
+        bad = !ring_.arrive(map, it, a.wait_ns) || (it == a.fail_at && threadIdx.x == blockDim.x - 1);
         // dy, and g and h of oct j
         auto load = [&](int j, Oct& dy, Oct& g, Oct& h) {
-            slot_read<TY>(here, j, dy);
+            ring_.template read<TY>(0, j, dy);
             if constexpr (FROM8) {
-                uint2 w;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                             : "=r"(w.x), "=r"(w.y)
-                             : "r"(here + at_s + j * blockDim.x * 8 - threadIdx.x * 8)
-                             : "memory");
-                decode_oct(w, h);
+                decode_oct(ring_.read_codes(1, j), h);
                 const float2 scale = both(act8_scale(cur.e[j]));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // the product is exact
                     h.p[k] = __ffma2_rn(h.p[k], scale, both(-cur.mean));
             } else {
-                slot_read<T>(here + at_s, j, h);
+                ring_.template read<T>(1, j, h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     h.p[k] = __fadd2_rn(h.p[k], both(-cur.mean));
@@ -635,7 +755,10 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
                     db[j].p[k] = __fadd2_rn(db[j].p[k], dy.p[k]);
                 }
             }
-        const float2 s = row_sum2<LPR>(make_float2(sgh.x + sgh.y, sg.x + sg.y), part[it & 1]);
+        const float2 s = row_sum2<LPR>(make_float2(sgh.x + sgh.y, sg.x + sg.y), part[it & 1], bad);
+        if (LPR == 0 && bad)
+            break;
+        ring_.refill(map, it);
         const float2 c1 = both(-s.x * inv_c), c2 = both(layer ? -s.y * inv_c : 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -644,7 +767,7 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
                 if constexpr (!KEEP)
                     load(j, dy, g, h);
                 if (add)
-                    slot_read<T>(here + at_r, j, q);
+                    ring_.template read<T>(2, j, q);
                 else
                     q.fill(0.0f);
 #pragma unroll
@@ -653,7 +776,13 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
                 store_oct(to_dx + j * dc, q, top);
             }
         to_dx += map.step * a.lddx;
-        stage = stage + 1 == stages ? 0 : stage + 1;
+        ring_.done(map, it);
+    }
+    if (LPR == 0 && bad) {
+        if (threadIdx.x == 0)
+            atomicExch(a.status, MX_ERR_TIMEOUT);
+        ring_.abandon(map, it, a.wait_ns);
+        return;
     }
     if (a.amax)
         flush_top(a.amax, top);
@@ -730,18 +859,19 @@ WideShape wide_shape(int64_t cols)
 
 constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
 // CTAs of an SM and rows in flight of each, from the bytes of one row's slots:
-// as many CTAs as registers allow, with three stages where they fit.
+// as many CTAs as registers allow (with at least two stages each), then the
+// stages that fit.
 struct RingPlan {
     int per_sm, stages;
 };
-RingPlan ring_plan(int64_t stage_bytes, int threads, int registers)
+RingPlan ring_plan(int64_t stage_bytes, int threads, int registers, int most)
 {
     RingPlan p;
     p.per_sm = std::min(32, std::min(65536 / ((registers + 7) / 8 * 8 * threads), 2048 / threads));
     p.per_sm = std::max(1, p.per_sm);
     while (p.per_sm > 1 && p.per_sm * 2 * stage_bytes > kRingBytes)
         --p.per_sm;
-    p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, kRingBytes / (p.per_sm * stage_bytes))));
+    p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, kRingBytes / (p.per_sm * stage_bytes))));
     return p;
 }
 
@@ -781,10 +911,11 @@ template <auto KERNEL, typename A>
 int launch_ring(const A& a, const WideShape& w, int64_t stage_bytes, size_t least_smem, int64_t most, unsigned* grid,
                 const Device& d, cudaStream_t s)
 {
-    const RingPlan p = ring_plan(stage_bytes, w.threads, registers_of<KERNEL>());
+    const RingPlan p = ring_plan(stage_bytes, w.threads, registers_of<KERNEL>(),
+                                 w.lpr ? 3 : kMaxStages);
     const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1, ctas = (a.rows + per_cta - 1) / per_cta;
     *grid = static_cast<unsigned>(std::min(most, std::min<int64_t>(ctas, int64_t{d.sms} * p.per_sm)));
-    const size_t smem = std::max(static_cast<size_t>(stage_bytes) * p.stages, least_smem);
+    const size_t smem = std::max(static_cast<size_t>(stage_bytes) * p.stages + (w.lpr ? 0 : kBarBytes), least_smem);
     if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
         cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MX_ERR_CUDA;

@@ -250,3 +250,26 @@ def test_training_without_affine_rows_independent(mx):
     part = mx.norm_fwd(x[13:14], save=True)
     assert torch.equal(whole.y[13:14], part.y) and torch.equal(whole.rstd[13:14], part.rstd)
     assert torch.equal(whole.saved.codes[13:14], part.saved.codes)
+
+
+@pytest.mark.parametrize("row", [0, 1, 3])
+@pytest.mark.parametrize("types", [(BF, 4096), (F32, 16384)])
+def test_a_wait_that_runs_out_is_reported(mx, types, row):
+    """The hook lets one thread of every CTA give up; the status word says so,
+    nothing hangs, and the next calls are right."""
+    dtype, cols = types
+    x = _x(2000, cols, dtype, 50)
+    good = mx.norm_fwd(x)
+    want = mx.norm_bwd(x, x, good.rstd, good.mean, dres=x)
+    for call in (lambda: mx.norm_fwd(x, residual=x), lambda: mx.norm_fwd(x, kind="rms"),
+                 lambda: mx.norm_bwd(x, x, good.rstd, good.mean, dres=x)):
+        mx.set_norm_fail_at(row)
+        try:
+            call()
+        finally:
+            mx.set_norm_fail_at(-1)
+        assert mx.last_device_status() == mx.MX_ERR_TIMEOUT
+    assert torch.equal(mx.norm_fwd(x).y, good.y)
+    got = mx.norm_bwd(x, x, good.rstd, good.mean, dres=x)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert mx.last_device_status() == mx.MX_OK
