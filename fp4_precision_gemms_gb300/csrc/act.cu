@@ -11,7 +11,6 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
 struct ValueSlope {
     float value, slope;
@@ -45,119 +44,11 @@ __device__ __forceinline__ ValueSlope activate(float z)
     }
 }
 
-// The warp's 32 lanes hold one group (0 past the row's end).
-__device__ __forceinline__ void save_group(float v, const Act8View& out, int64_t group)
-{
-    const int lane = threadIdx.x & 31;
-    const float z = finite_or_nan(v);
-    const float b = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, abs_bits(fmaxf(fabsf(z), 0.0f))));
-    const uint32_t e = act8_byte(b);
-    out.codes[group * kAct8Group + lane] = static_cast<uint8_t>(cvt_e4m3x2(z * act8_inverse(e), 0.0f));
-    if (lane == 0)
-        out.sf[group] = static_cast<uint8_t>(e);
-}
-
-__device__ __forceinline__ float restored(const Act8View& a, int64_t group, int lane)
-{
-    return dec_e4m3x2(a.codes[group * kAct8Group + lane]).x * act8_scale(a.sf[group]);
-}
-
-// ------------------------------------------------------------------ any width
-// A warp per group of 32 columns of a row, one column a lane.  Serves every
-// width and alignment.
-
-template <typename T, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads) act_fwd_any_kernel(ActArgs a)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t G = act8_groups(a.cols), total = a.rows * G;
-    Top<T> top;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); i < total;
-         i += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t r = i / G, c = (i - r * G) * kAct8Group + lane;
-        const bool in = c < a.cols;
-        const float g = in ? load_f(static_cast<const T*>(a.gate) + r * a.ldg + c) : 0.0f;
-        float h = activate<ACT, sizeof(T) == 2>(g).value, u = 0.0f;
-        if constexpr (GATED) {
-            u = in ? load_f(static_cast<const T*>(a.up) + r * a.ldu + c) : 0.0f;
-            h *= u;
-        }
-        if (in) {
-            h = as_stored<T>(h);
-            store_f(static_cast<T*>(a.h) + r * a.ldh + c, h);
-            top.value(h);
-        }
-        if (a.gate8.codes)
-            save_group(g, a.gate8, i);
-        if (GATED && a.up8.codes)
-            save_group(u, a.up8, i);
-    }
-    if (a.amax)
-        flush_top(a.amax, top);
-}
-
-template <typename T, int ACT, bool GATED, bool FROM8>
-__global__ void __launch_bounds__(kThreads) act_bwd_any_kernel(ActArgs a)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t G = act8_groups(a.cols), total = a.rows * G;
-    Top<T> top;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); i < total;
-         i += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t r = i / G, c = (i - r * G) * kAct8Group + lane;
-        if (c >= a.cols)
-            continue;
-        const float g = FROM8 ? restored(a.gate8, i, lane) : load_f(static_cast<const T*>(a.gate) + r * a.ldg + c);
-        const float dh = load_f(static_cast<const T*>(a.h) + r * a.ldh + c);
-        const ValueSlope f = activate<ACT, sizeof(T) == 2>(g);
-        float dg = dh * f.slope;
-        if constexpr (GATED) {
-            const float u = FROM8 ? restored(a.up8, i, lane) : load_f(static_cast<const T*>(a.up) + r * a.ldu + c);
-            dg *= u;
-            const float du = as_stored<T>(dh * f.value);
-            store_f(static_cast<T*>(a.dup) + r * a.lddu + c, du);
-            top.value(du);
-        }
-        dg = as_stored<T>(dg);
-        store_f(static_cast<T*>(a.dgate) + r * a.lddg + c, dg);
-        top.value(dg);
-    }
-    if (a.amax)
-        flush_top(a.amax, top);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) act8_save_any_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows,
-                                                                 int64_t cols, Act8View out)
-{
-    const int64_t G = act8_groups(cols), total = rows * G;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); i < total;
-         i += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t r = i / G, c = (i - r * G) * kAct8Group + (threadIdx.x & 31);
-        save_group(c < cols ? load_f(x + r * ldx + c) : 0.0f, out, i);
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) act8_restore_any_kernel(Act8View a, int64_t rows, int64_t cols,
-                                                                    T* __restrict__ out, int64_t ldo)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t G = act8_groups(cols), total = rows * G;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); i < total;
-         i += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t r = i / G, c = (i - r * G) * kAct8Group + lane;
-        if (c < cols)
-            store_f(out + r * ldo + c, restored(a, i, lane));
-    }
-}
-
-// ------------------------------------------------------------------ wide
-// Rows that start on 16-byte boundaries.  A unit is eight columns of a row, a
-// row has 4 G units (whole groups, so that the four lanes of a group always
-// work together; those past the row's end hold zeros).  Each thread keeps
-// kUnits units' loads in flight; a grid of kCtasPerSm CTAs an SM strides over
-// the units.
+// A unit is eight columns of a row, a row has 4 G units (whole groups, so that
+// the four lanes of a group always work together; those past the row's end hold
+// zeros).  Each thread keeps kUnits units' loads in flight; a grid of kCtasPerSm
+// CTAs an SM strides over the units.  ANY: rows of any address and length; else
+// they start on 16-byte boundaries and their length is a multiple of eight.
 constexpr int kUnits = 2;
 constexpr int kCtasPerSm = 4;
 
@@ -173,37 +64,82 @@ struct Place {
 __device__ __forceinline__ Place place(uint32_t i, const UnitMap& m, int64_t cols)
 {
     const uint32_t r = div_by(i, m.per_row), u = i - r * m.per_row.d;
-    return {r, u, static_cast<int32_t>(min(cols - static_cast<int64_t>(u) * 8, int64_t{8}))};
+    Place p = {r, u, static_cast<int32_t>(min(cols - static_cast<int64_t>(u) * 8, int64_t{8}))};
+    if (i >= m.total)
+        p.cols = 0;
+    return p;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_unit(RawOct<T>& o, const void* base, int64_t ld, const Place& p)
-{
-    const T* src = static_cast<const T*>(base) + p.row * ld + static_cast<int64_t>(p.unit) * 8;
-    if (p.cols == 8) {
-        o.load(src);
-    } else {  // the row's last columns, one by one
-        T tail[8];
+// A unit's words.  ANY: the aligned words that it lies in; they may hold a
+// neighbouring row's elements, but nothing before the matrix's first element or
+// after its last one is touched.
+template <typename T, bool ANY>
+struct Unit {
+    RawOct<T> w;
+    uint4 more;
+    int s;
+
+    __device__ __forceinline__ void load(const void* base, int64_t ld, const Place& p, int64_t rows, int64_t cols)
+    {
+        const T* src = static_cast<const T*>(base) + p.row * ld + static_cast<int64_t>(p.unit) * 8;
+        if constexpr (!ANY) {
+            if (p.cols > 0)
+                w.load(src);
+            else
+                w.clear();
+        } else {
+            s = misaligned(src, sizeof(T));
+            const int64_t at = p.row * ld + static_cast<int64_t>(p.unit) * 8, end = (rows - 1) * ld + cols;
+            w.clear();
+            more = make_uint4(0, 0, 0, 0);
+            if (p.cols <= 0)
+                return;
+            if (at < 8 || at + 16 > end) {  // the aligned words may reach past the matrix
+                T v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            tail[c] = c < p.cols ? src[c] : T(0.0f);
-        memcpy(&o, tail, sizeof tail);
+                for (int c = 0; c < 8; ++c)
+                    v[c] = c < p.cols ? src[c] : T(0.0f);
+                memcpy(&w, v, sizeof v);
+                s = 0;
+                return;
+            }
+            w.load(src - s);
+            if (s + p.cols > 8) {
+                RawOct<__nv_bfloat16> m;
+                m.load(reinterpret_cast<const __nv_bfloat16*>(src - s + 8));
+                more = m.w;
+            }
+        }
     }
-}
+    __device__ __forceinline__ void get(Oct& o, int n) const
+    {
+        if constexpr (!ANY) {
+            w.get(o);
+        } else {
+            if constexpr (sizeof(T) == 2) {
+                unpack_oct(shifted(w.w, more, s), o);
+            } else {
+                uint4 a, b, lo, hi;
+                memcpy(&a, &w.a, 16);
+                memcpy(&b, &w.b, 16);
+                shifted(a, b, more, s, lo, hi);
+                words_to_oct(lo, hi, o);
+            }
+            keep_first(o, n);
+        }
+    }
+};
 
-template <typename T>
-__device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& p, const Oct& o, Top<T>& top)
+template <typename T, bool ANY>
+__device__ __forceinline__ void store_unit(void* base, int64_t ld, const Place& p, const Oct& o, int64_t cols, Top<T>& top)
 {
     T* dst = static_cast<T*>(base) + p.row * ld + static_cast<int64_t>(p.unit) * 8;
-    if (p.cols == 8) {
-        store_oct(dst, o, top);
-    } else if (p.cols > 0) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c < p.cols) {
-                store_f(dst + c, o[c]);
-                top.value(o[c]);
-            }
+    if constexpr (!ANY) {
+        if (p.cols > 0)
+            store_oct(dst, o, top);
+    } else {
+        const int lane = threadIdx.x & 31;
+        store_ragged(dst, o, p.cols, lane > 0 && p.unit > 0, lane < 31 && static_cast<int64_t>(p.unit) * 8 + 8 < cols, top);
     }
 }
 
@@ -218,37 +154,35 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
     }
 }
 
-template <typename T, int ACT, bool GATED>
+template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 {
     Top<T> top;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
-        RawOct<T> g[kUnits], u[kUnits];
+        Unit<T, ANY> g[kUnits], u[kUnits];
         Place p[kUnits];
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const uint32_t i = base + k * kThreads + threadIdx.x;
             p[k] = place(i, m, a.cols);
-            if (i >= m.total)
-                p[k].cols = 0;
-            load_unit(g[k], a.gate, a.ldg, p[k]);
+            g[k].load(a.gate, a.ldg, p[k], a.rows, a.cols);
             if constexpr (GATED)
-                load_unit(u[k], a.up, a.ldu, p[k]);
+                u[k].load(a.up, a.ldu, p[k], a.rows, a.cols);
         }
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const uint32_t i = base + k * kThreads + threadIdx.x;
             Oct gv, uv, h;
-            g[k].get(gv);
+            g[k].get(gv, p[k].cols);
             if constexpr (GATED)
-                u[k].get(uv);
+                u[k].get(uv, p[k].cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 h[j] = activate<ACT, sizeof(T) == 2>(gv[j]).value;
                 if constexpr (GATED)
                     h[j] *= uv[j];
             }
-            store_unit<T>(a.h, a.ldh, p[k], h, top);
+            store_unit<T, ANY>(a.h, a.ldh, p[k], h, a.cols, top);
             if (a.gate8.codes)
                 save_unit(a.gate8, i, i < m.total, gv);
             if constexpr (GATED)
@@ -260,22 +194,20 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
         flush_top(a.amax, top);
 }
 
-template <typename T, int ACT, bool GATED, bool FROM8>
+template <typename T, int ACT, bool GATED, bool FROM8, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
 {
-    using Raw = std::conditional_t<FROM8, RawCodes, RawOct<T>>;
+    using Raw = std::conditional_t<FROM8, RawCodes, Unit<T, ANY>>;
     Top<T> top;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         Raw g[kUnits], u[kUnits];
-        RawOct<T> d[kUnits];
+        Unit<T, ANY> d[kUnits];
         Place p[kUnits];
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const uint32_t i = base + k * kThreads + threadIdx.x;
             p[k] = place(i, m, a.cols);
-            if (i >= m.total)
-                p[k].cols = 0;
-            load_unit(d[k], a.h, a.ldh, p[k]);
+            d[k].load(a.h, a.ldh, p[k], a.rows, a.cols);
             if constexpr (FROM8) {
                 g[k].clear();
                 u[k].clear();
@@ -285,18 +217,18 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
                         u[k].load(a.up8, i);
                 }
             } else {
-                load_unit(g[k], a.gate, a.ldg, p[k]);
+                g[k].load(a.gate, a.ldg, p[k], a.rows, a.cols);
                 if constexpr (GATED)
-                    load_unit(u[k], a.up, a.ldu, p[k]);
+                    u[k].load(a.up, a.ldu, p[k], a.rows, a.cols);
             }
         }
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             Oct gv, uv, dv, dg;
-            d[k].get(dv);
-            g[k].get(gv);
+            d[k].get(dv, p[k].cols);
+            g[k].get(gv, p[k].cols);
             if constexpr (GATED)
-                u[k].get(uv);
+                u[k].get(uv, p[k].cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const ValueSlope f = activate<ACT, sizeof(T) == 2>(gv[j]);
@@ -306,40 +238,38 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
                     dv[j] *= f.value;
                 }
             }
-            store_unit<T>(a.dgate, a.lddg, p[k], dg, top);
+            store_unit<T, ANY>(a.dgate, a.lddg, p[k], dg, a.cols, top);
             if constexpr (GATED)
-                store_unit<T>(a.dup, a.lddu, p[k], dv, top);
+                store_unit<T, ANY>(a.dup, a.lddu, p[k], dv, a.cols, top);
         }
     }
     if (a.amax)
         flush_top(a.amax, top);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) act8_save_kernel(const void* __restrict__ x, int64_t ldx, int64_t cols,
-                                                             Act8View out, UnitMap m)
+template <typename T, bool ANY>
+__global__ void __launch_bounds__(kThreads) act8_save_kernel(const void* __restrict__ x, int64_t ldx, int64_t rows,
+                                                             int64_t cols, Act8View out, UnitMap m)
 {
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
-        RawOct<T> w[kUnits];
+        Unit<T, ANY> w[kUnits];
+        Place p[kUnits];
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
-            const uint32_t i = base + k * kThreads + threadIdx.x;
-            Place p = place(i, m, cols);
-            if (i >= m.total)
-                p.cols = 0;
-            load_unit(w[k], x, ldx, p);
+            p[k] = place(base + k * kThreads + threadIdx.x, m, cols);
+            w[k].load(x, ldx, p[k], rows, cols);
         }
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const uint32_t i = base + k * kThreads + threadIdx.x;
             Oct v;
-            w[k].get(v);
+            w[k].get(v, p[k].cols);
             save_unit(out, i, i < m.total, v);
         }
     }
 }
 
-template <typename T>
+template <typename T, bool ANY>
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View a, int64_t cols, void* __restrict__ out,
                                                                 int64_t ldo, UnitMap m)
 {
@@ -351,8 +281,6 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View a, int6
         for (int k = 0; k < kUnits; ++k) {
             const uint32_t i = base + k * kThreads + threadIdx.x;
             p[k] = place(i, m, cols);
-            if (i >= m.total)
-                p[k].cols = 0;
             w[k].clear();
             if (p[k].cols > 0)
                 w[k].load(a, i);
@@ -360,13 +288,13 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View a, int6
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             Oct v;
-            w[k].get(v);
-            store_unit<T>(out, ldo, p[k], v, unused);
+            w[k].get(v, p[k].cols);
+            store_unit<T, ANY>(out, ldo, p[k], v, cols, unused);
         }
     }
 }
 
-// Rows that a launch of the wide kernels can take (its unit count is 31 bits).
+// Rows that one launch can take (its unit count is 31 bits).
 int64_t slab_rows(int64_t cols) { return std::max<int64_t>(1, ((int64_t{1} << 31) - (1 << 22)) / (act8_groups(cols) * 4)); }
 UnitMap unit_map(int64_t rows, int64_t cols)
 {
@@ -401,12 +329,6 @@ Act8View ahead(Act8View v, int64_t rows, int64_t cols)
     return v;
 }
 
-unsigned any_grid(int64_t rows, int64_t cols, const Device& d)
-{
-    const int64_t ctas = (rows * act8_groups(cols) + kWarps - 1) / kWarps;
-    return static_cast<unsigned>(std::min<int64_t>(ctas, d.sms * 8));
-}
-
 int launched()
 {
     count_launch();
@@ -416,14 +338,7 @@ int launched()
 template <typename T, int ACT>
 int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
 {
-    if (!wide(a.gate, a.ldg, a.dtype) || !wide(a.h, a.ldh, a.dtype) || !wide(a.up, a.ldu, a.dtype)) {
-        const unsigned grid = any_grid(a.rows, a.cols, d);
-        if (a.gated)
-            act_fwd_any_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
-        else
-            act_fwd_any_kernel<T, ACT, false><<<grid, kThreads, 0, s>>>(a);
-        return launched();
-    }
+    const bool aligned = a.cols % 8 == 0 && wide(a.gate, a.ldg, a.dtype) && wide(a.h, a.ldh, a.dtype) && wide(a.up, a.ldu, a.dtype);
     const int64_t slab = slab_rows(a.cols);
     for (int64_t r = 0; r < a.rows; r += slab) {
         ActArgs b = a;
@@ -434,10 +349,14 @@ int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.gate8 = ahead(a.gate8, r, a.cols);
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
-        if (a.gated)
-            act_fwd_kernel<T, ACT, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        if (aligned && a.gated)
+            act_fwd_kernel<T, ACT, true, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        else if (aligned)
+            act_fwd_kernel<T, ACT, false, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        else if (a.gated)
+            act_fwd_kernel<T, ACT, true, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
         else
-            act_fwd_kernel<T, ACT, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            act_fwd_kernel<T, ACT, false, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
         if (launched() != MX_OK)
             return MX_ERR_CUDA;
     }
@@ -447,15 +366,8 @@ int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
 template <typename T, int ACT, bool FROM8>
 int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
 {
-    if (!wide(a.h, a.ldh, a.dtype) || !wide(a.dgate, a.lddg, a.dtype) || !wide(a.dup, a.lddu, a.dtype) ||
-        !wide(a.gate, a.ldg, a.dtype) || !wide(a.up, a.ldu, a.dtype)) {
-        const unsigned grid = any_grid(a.rows, a.cols, d);
-        if (a.gated)
-            act_bwd_any_kernel<T, ACT, true, FROM8><<<grid, kThreads, 0, s>>>(a);
-        else
-            act_bwd_any_kernel<T, ACT, false, FROM8><<<grid, kThreads, 0, s>>>(a);
-        return launched();
-    }
+    const bool aligned = a.cols % 8 == 0 && wide(a.h, a.ldh, a.dtype) && wide(a.dgate, a.lddg, a.dtype) && wide(a.dup, a.lddu, a.dtype) &&
+                         wide(a.gate, a.ldg, a.dtype) && wide(a.up, a.ldu, a.dtype);
     const int64_t slab = slab_rows(a.cols);
     for (int64_t r = 0; r < a.rows; r += slab) {
         ActArgs b = a;
@@ -468,10 +380,14 @@ int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.gate8 = ahead(a.gate8, r, a.cols);
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
-        if (a.gated)
-            act_bwd_kernel<T, ACT, true, FROM8><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        if (aligned && a.gated)
+            act_bwd_kernel<T, ACT, true, FROM8, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        else if (aligned)
+            act_bwd_kernel<T, ACT, false, FROM8, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+        else if (a.gated)
+            act_bwd_kernel<T, ACT, true, FROM8, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
         else
-            act_bwd_kernel<T, ACT, false, FROM8><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            act_bwd_kernel<T, ACT, false, FROM8, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
         if (launched() != MX_OK)
             return MX_ERR_CUDA;
     }
@@ -482,14 +398,16 @@ template <typename T>
 int save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8View out, const Device& d,
          cudaStream_t s)
 {
-    if (!wide(x, ldx, dtype)) {
-        act8_save_any_kernel<<<any_grid(rows, cols, d), kThreads, 0, s>>>(static_cast<const T*>(x), ldx, rows, cols, out);
-        return launched();
-    }
+    const bool aligned = cols % 8 == 0 && wide(x, ldx, dtype);
     const int64_t slab = slab_rows(cols);
     for (int64_t r = 0; r < rows; r += slab) {
-        const UnitMap m = unit_map(std::min(slab, rows - r), cols);
-        act8_save_kernel<T><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(x, r, ldx, dtype), ldx, cols, ahead(out, r, cols), m);
+        const int64_t n = std::min(slab, rows - r);
+        const UnitMap m = unit_map(n, cols);
+        const void* from = ahead(x, r, ldx, dtype);
+        if (aligned)
+            act8_save_kernel<T, false><<<unit_grid(m, d), kThreads, 0, s>>>(from, ldx, n, cols, ahead(out, r, cols), m);
+        else
+            act8_save_kernel<T, true><<<unit_grid(m, d), kThreads, 0, s>>>(from, ldx, n, cols, ahead(out, r, cols), m);
         if (launched() != MX_OK)
             return MX_ERR_CUDA;
     }
@@ -499,14 +417,16 @@ int save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8
 template <typename T>
 int restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int dtype, const Device& d, cudaStream_t s)
 {
-    if (!wide(out, ldo, dtype)) {
-        act8_restore_any_kernel<<<any_grid(rows, cols, d), kThreads, 0, s>>>(a, rows, cols, static_cast<T*>(out), ldo);
-        return launched();
-    }
+    const bool aligned = cols % 8 == 0 && wide(out, ldo, dtype);
     const int64_t slab = slab_rows(cols);
     for (int64_t r = 0; r < rows; r += slab) {
-        const UnitMap m = unit_map(std::min(slab, rows - r), cols);
-        act8_restore_kernel<T><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(a, r, cols), cols, ahead(out, r, ldo, dtype), ldo, m);
+        const int64_t n = std::min(slab, rows - r);
+        const UnitMap m = unit_map(n, cols);
+        void* to = ahead(out, r, ldo, dtype);
+        if (aligned)
+            act8_restore_kernel<T, false><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(a, r, cols), cols, to, ldo, m);
+        else
+            act8_restore_kernel<T, true><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(a, r, cols), cols, to, ldo, m);
         if (launched() != MX_OK)
             return MX_ERR_CUDA;
     }

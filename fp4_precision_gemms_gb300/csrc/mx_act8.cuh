@@ -162,7 +162,7 @@ struct RawCodes {
         e = a.sf[unit >> 2];
     }
     __device__ __forceinline__ void clear() { w = make_uint2(0, 0), e = 127; }
-    __device__ __forceinline__ void get(Oct& o) const
+    __device__ __forceinline__ void get(Oct& o, int = 8) const
     {
         decode_oct(w, o);
         const float2 s = both(act8_scale(e));
@@ -255,6 +255,134 @@ __device__ __forceinline__ void store_oct(float* p, const Oct& o, Top<float>& to
     *reinterpret_cast<float4*>(p) = make_float4(o.p[0].x, o.p[0].y, o.p[1].x, o.p[1].y);
     *reinterpret_cast<float4*>(p + 4) = make_float4(o.p[2].x, o.p[2].y, o.p[3].x, o.p[3].y);
     top.pair(o.p[0]), top.pair(o.p[1]), top.pair(o.p[2]), top.pair(o.p[3]);
+}
+
+// ------------------------------------------------------ rows at any address
+// A row that does not start on a 16-byte boundary is still read and written in
+// aligned 16-byte words: an oct lies in two of them (three of fp32) and is
+// shifted into place, and on the way out each lane joins its neighbour's last
+// values to its own.  Elements that share an aligned word with another warp's,
+// and the row's ragged end, go one by one.
+__device__ __forceinline__ int misaligned(const void* p, int bytes)  // elements past the boundary
+{
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / bytes;
+}
+
+// Elements s .. s + 7 of the 16 bf16 in (lo, hi), s <= 7.
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, int s)
+{
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t a[6], b[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+        a[i] = s & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        b[i] = s & 2 ? a[i + 1] : a[i];
+    const int bits = (s & 1) * 16;
+    return make_uint4(__funnelshift_r(b[0], b[1], bits), __funnelshift_r(b[1], b[2], bits),
+                      __funnelshift_r(b[2], b[3], bits), __funnelshift_r(b[3], b[4], bits));
+}
+// Words s .. s + 7 of the twelve in (x, y, z), s <= 3.
+__device__ __forceinline__ void shifted(uint4 x, uint4 y, uint4 z, int s, uint4& lo, uint4& hi)
+{
+    const uint32_t w[12] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+    uint32_t a[9], b[8];
+#pragma unroll
+    for (int i = 0; i < 9; ++i)
+        a[i] = s & 2 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        b[i] = s & 1 ? a[i + 1] : a[i];
+    lo = make_uint4(b[0], b[1], b[2], b[3]);
+    hi = make_uint4(b[4], b[5], b[6], b[7]);
+}
+__device__ __forceinline__ void words_to_oct(uint4 a, uint4 b, Oct& o)
+{
+    o.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+    o.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    o.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+    o.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+}
+// Zeros in place of what lies past the first n values.
+__device__ __forceinline__ void keep_first(Oct& o, int n)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= n)
+            o[i] = 0.0f;
+}
+__device__ __forceinline__ uint4 shfl_up1(uint4 v)
+{
+    return make_uint4(__shfl_up_sync(0xFFFFFFFFu, v.x, 1), __shfl_up_sync(0xFFFFFFFFu, v.y, 1),
+                      __shfl_up_sync(0xFFFFFFFFu, v.z, 1), __shfl_up_sync(0xFFFFFFFFu, v.w, 1));
+}
+
+// Writes an oct (its first n values, n may be <= 0) at any address p; executed
+// by whole warps.  prev / next: the neighbouring lane holds the oct before /
+// after this one in the same row, the latter with at least one value.  With s
+// elements between the aligned word and p, a lane's word holds the s last values
+// of the lane before it and its own first 8 - s.
+template <typename T, typename W>
+__device__ __forceinline__ void store_rest(T* p, const W (&own)[8], const W (&left)[8], int n, int s, bool whole,
+                                           bool prev, bool next)
+{
+    W* const to = reinterpret_cast<W*>(p);
+    // one by one: the first 8 - s where no lane's word takes them, the last s
+    // where the next lane does not
+    const int from = whole ? 8 - s : 0, end = next ? min(n, 8 - s) : n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= from && i < end)
+            to[i] = own[i];
+    if (!whole && prev && n > 0)  // a row's end that does not fill its word: the lane before leaves it its last s
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (i >= 8 - s)
+                to[i - 8] = left[i];
+}
+__device__ __forceinline__ void store_ragged(__nv_bfloat16* p, Oct o, int n, bool prev, bool next, Top<__nv_bfloat16>& top)
+{
+    keep_first(o, n);
+    const uint4 own = pack_oct(o), left = shfl_up1(own);
+    const int s = misaligned(p, 2);
+    top.word(own.x), top.word(own.y), top.word(own.z), top.word(own.w);
+    const bool whole = n == 8 && (prev || s == 0);
+    if (whole)
+        *reinterpret_cast<uint4*>(p - s) = s == 0 ? own : shifted(left, own, 8 - s);
+    if (!whole || (!next && s != 0)) {
+        const uint32_t a[4] = {own.x, own.y, own.z, own.w}, b[4] = {left.x, left.y, left.z, left.w};
+        uint16_t v[8], l[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = static_cast<uint16_t>(a[i >> 1] >> ((i & 1) * 16));
+            l[i] = static_cast<uint16_t>(b[i >> 1] >> ((i & 1) * 16));
+        }
+        store_rest(p, v, l, n, s, whole, prev, next);
+    }
+}
+__device__ __forceinline__ void store_ragged(float* p, Oct o, int n, bool prev, bool next, Top<float>& top)
+{
+    keep_first(o, n);
+    const uint4 a = make_uint4(__float_as_uint(o.p[0].x), __float_as_uint(o.p[0].y), __float_as_uint(o.p[1].x),
+                               __float_as_uint(o.p[1].y));
+    const uint4 b = make_uint4(__float_as_uint(o.p[2].x), __float_as_uint(o.p[2].y), __float_as_uint(o.p[3].x),
+                               __float_as_uint(o.p[3].y));
+    const uint4 left = shfl_up1(b);
+    const int s = misaligned(p, 4);
+    top.pair(o.p[0]), top.pair(o.p[1]), top.pair(o.p[2]), top.pair(o.p[3]);
+    const bool whole = n == 8 && (prev || s == 0);
+    if (whole) {
+        uint4 lo = a, hi = b;
+        if (s != 0)
+            shifted(left, a, b, 4 - s, lo, hi);
+        reinterpret_cast<uint4*>(p - s)[0] = lo;
+        reinterpret_cast<uint4*>(p - s)[1] = hi;
+    }
+    if (!whole || (!next && s != 0)) {
+        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, l[8] = {0, 0, 0, 0, left.x, left.y, left.z, left.w};
+        store_rest(p, v, l, n, s, whole, prev, next);
+    }
 }
 
 __device__ __forceinline__ bool non_finite(float v) { return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u; }

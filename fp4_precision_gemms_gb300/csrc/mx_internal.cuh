@@ -141,7 +141,7 @@ struct NormFwdArgs {
     int x_dtype, y_dtype, w_dtype, kind;
     int* status;
     uint64_t wait_ns;
-    int64_t fail_at;  // test hook: in this row of each CTA a wait counts as run out; -1 never
+    int fail_at;  // test hook: in this row of each CTA a wait counts as run out; -1 never
 };
 struct NormBwdArgs {
     const void* dy;
@@ -161,7 +161,7 @@ struct NormBwdArgs {
     int dy_dtype, dx_dtype, w_dtype, kind;
     int* status;
     uint64_t wait_ns;
-    int64_t fail_at;
+    int fail_at;
 };
 struct ActArgs {  // forward: h written; backward: h is dh, read
     const void* gate;

@@ -68,13 +68,13 @@ int zero(void* p, size_t bytes, cudaStream_t s)
     return !p || bytes == 0 || cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
 }
 
-thread_local int64_t g_norm_fail_at = -1;  // test hook: the norm kernels' forced wait failure
+thread_local int g_norm_fail_at = -1;  // test hook: the norm kernels' forced wait failure
 
 }  // namespace
 
 extern "C" {
 
-void mx_debug_set_norm_fail_at(int64_t row) { g_norm_fail_at = row; }
+void mx_debug_set_norm_fail_at(int64_t row) { g_norm_fail_at = row < 0 || row > INT32_MAX ? -1 : static_cast<int>(row); }
 
 size_t mx_act8_codes_bytes(int64_t rows, int64_t cols)
 {

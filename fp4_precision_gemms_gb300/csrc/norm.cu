@@ -1,6 +1,7 @@
 // norm.cu -- layer norm and RMS norm over the rows of a residual stream,
 // forward and backward.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
@@ -213,8 +214,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const flo
 }
 
 // ------------------------------------------------------------------ wide
-// Rows on 16-byte boundaries, cols % 8 == 0, cols <= 16384.  Eight columns
-// (an oct) at a time: thread t of a row's TPR threads owns the octs t, t + TPR,
+// Up to 16384 columns.  Eight columns (an oct) at a time: thread t of a row's TPR threads owns the octs t, t + TPR,
 // ..., NV of them; octs past the row's end hold zeros, and a group's four octs
 // lie in four neighbouring lanes.  LPR > 0: LPR lanes of a warp per row, the
 // rows of a CTA independent; LPR = 0: the CTA's blockDim.x threads per row.
@@ -321,10 +321,15 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* part, bool& bad)
 }
 
 // Eight of the weights or biases.
-__device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float absent, Oct& o)
+template <bool ANY>
+__device__ __forceinline__ void param_oct(const void* p, int dtype, int c, int C, float absent, Oct& o)
 {
     if (!p) {
         o.fill(absent);
+    } else if (ANY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = c + i < C ? param(p, dtype, c + i, absent) : 0.0f;
     } else if (dtype == MX_OUT_BF16) {
         unpack_oct(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), o);
     } else {
@@ -336,119 +341,120 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
 }
 
 // The ring of PARTS matrices.  A matrix may be absent (null).  Its octs take
-// OB bytes: 16 (bf16), 32 (fp32) or 8 (codes).
+// 16 (bf16), 32 (fp32) or 8 (codes) bytes.  ANY: rows at any address: a stage
+// holds the aligned 16-byte words that a row lies in, one more than its octs
+// fill, and an oct is shifted into place when it is read (codes always start on
+// a boundary).  The words may hold a neighbouring row's elements; the first and
+// the last rows (`edge` of them), whose words would reach past the matrix, are
+// not copied but read where they are.
 struct RingPart {
     const char* src;    // row 0
-    int64_t row_bytes;  // from one row to the next
+    int64_t next_row;   // bytes from one row to the next
     int oct;            // bytes of an oct
     uint32_t at;        // in a stage
 };
-template <int LPR, int NV, int PARTS>
+__host__ __device__ constexpr uint32_t region_bytes(int octs, int oct, bool any)
+{
+    return (octs * oct + 15) / 16 * 16 + (any && oct != 8 ? 16 : 0);
+}
+template <int LPR, int NV, int PARTS, bool ANY>
 struct RowRing {
+    static constexpr int kLanes = LPR ? LPR : 1;
     RingPart part[PARTS];
-    uint32_t base, stage_bytes, bars;
+    uint32_t base, stage_bytes, bars, at_stage = 0;
     int stages, stage = 0, octs;
     uint32_t phase = 0;
+    int64_t rows, row = 0, edge = 1;
+    bool direct = false;  // ANY: the current row is read from where it is
 
-    // `octs` of a row to copy.  A stage's parts lie one after the other; LPR > 0:
-    // words of NV octs for every thread of the CTA.
-    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int octs_)
+    __device__ __forceinline__ uint32_t region(int m) const { return region_bytes(octs, part[m].oct, ANY); }
+    __device__ __forceinline__ uint32_t shift(int m, int64_t r) const  // bytes past a boundary
+    {
+        return ANY ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(part[m].src + r * part[m].next_row)) & 15u : 0u;
+    }
+    __device__ __forceinline__ bool at_edge(int64_t r) const { return ANY && (r < edge || r >= rows - edge); }
+
+    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int cols, int64_t rows_)
     {
         stages = stages_;
-        octs = octs_;
+        octs = (cols + 7) / 8;
+        rows = rows_;
         bars = smem_u32(smem);
         base = bars + (LPR == 0 ? kBarBytes : 0);
         uint32_t at = 0;
 #pragma unroll
         for (int m = 0; m < PARTS; ++m) {
             part[m].at = at;
-            if (part[m].src)
-                at += (LPR == 0 ? (octs * part[m].oct + 15) / 16 * 16 : NV * blockDim.x * part[m].oct);
+            if (part[m].src) {
+                at += LPR == 0 ? region(m) : ANY ? kSubThreads / kLanes * region(m) : NV * kSubThreads * part[m].oct;
+                if (ANY && part[m].next_row < 16)
+                    edge = 16;
+            }
         }
         stage_bytes = at;
     }
 
-    // ---- LPR = 0
-    // Row r into stage st (one thread).
+    // Row r into stage st: LPR = 0, one thread.
     __device__ __forceinline__ void fill(int64_t r, int st)
     {
+        const uint32_t bar = bars + st * 8, to = base + st * stage_bytes;
+        if (at_edge(r)) {
+            mbar_arrive(bar);
+            return;
+        }
         uint32_t bytes = 0;
 #pragma unroll
         for (int m = 0; m < PARTS; ++m)
             if (part[m].src)
-                bytes += (octs * part[m].oct + 15) / 16 * 16;
-        mbar_arrive_expect_tx(bars + st * 8, bytes);
+                bytes += copied(m, r);
+        mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
         for (int m = 0; m < PARTS; ++m)
             if (part[m].src)
-                bulk_load(base + st * stage_bytes + part[m].at, part[m].src + r * part[m].row_bytes,
-                          (octs * part[m].oct + 15) / 16 * 16, bars + st * 8);
+                bulk_load(to + part[m].at, part[m].src + r * part[m].next_row - shift(m, r), copied(m, r), bar);
     }
-    __device__ __forceinline__ bool wait(uint64_t limit_ns) { return mbar_wait_bounded(bars + stage * 8, phase, limit_ns); }
+    // Bytes of the words that row r lies in.
+    __device__ __forceinline__ uint32_t copied(int m, int64_t r) const
+    {
+        if constexpr (!ANY)
+            return region(m);
+        return part[m].oct == 8 ? region(m) : (shift(m, r) + row_bytes(m) + 15) / 16 * 16;
+    }
+    int cols_ = 0;
+    __device__ __forceinline__ uint32_t row_bytes(int m) const { return static_cast<uint32_t>(cols_) * (part[m].oct / 8); }
 
-    // ---- both
-    __device__ __forceinline__ void next()
-    {
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-    // Thread's word h of oct j of matrix m in the current stage.
-    __device__ __forceinline__ uint32_t word(int m, int j, int h) const
-    {
-        const uint32_t at = base + stage * stage_bytes + part[m].at;
-        if constexpr (LPR == 0)
-            return at + (threadIdx.x + j * blockDim.x) * part[m].oct + h * 16;
-        const int w = min(part[m].oct, 16);
-        return at + ((j * (part[m].oct / w) + h) * blockDim.x + threadIdx.x) * w;
-    }
-    template <typename T>
-    __device__ __forceinline__ void read(int m, int j, Oct& o) const
-    {
-        if constexpr (sizeof(T) == 2) {
-            unpack_oct(lds128(word(m, j, 0)), o);
-        } else {
-            const uint4 a = lds128(word(m, j, 0)), b = lds128(word(m, j, 1));
-            o.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-            o.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
-            o.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-            o.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
-        }
-    }
-    __device__ __forceinline__ uint2 read_codes(int m, int j) const
-    {
-        uint2 w;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(word(m, j, 0)) : "memory");
-        return w;
-    }
-
-    // ---- LPR > 0
-    // The thread's octs of row r into the stage `ahead` rows on.
+    // LPR > 0: this thread's share of its row r into the stage `ahead` rows on.
     __device__ __forceinline__ void copy(int64_t r, bool in, int ahead, int t)
     {
-        if (in) {
-            int st = stage + ahead;
-            st -= st >= stages ? stages : 0;
-            const uint32_t to = base + st * stage_bytes;
+        if (in && !at_edge(r)) {
+            const int st = stage + ahead;
+            const uint32_t to = base + (st >= stages ? st - stages : st) * stage_bytes;
 #pragma unroll
             for (int m = 0; m < PARTS; ++m)
                 if (part[m].src) {
-                    const char* row = part[m].src + r * part[m].row_bytes;
-                    const int w = min(part[m].oct, 16);
+                    const char* row_at = part[m].src + r * part[m].next_row;
+                    if constexpr (ANY) {  // the row's words over its lanes
+                        const uint32_t dst = to + part[m].at + (threadIdx.x / kLanes) * region(m);
+                        const uint32_t n = copied(m, r);
+                        row_at -= shift(m, r);
+                        for (uint32_t w = t * 16; w < n; w += kLanes * 16)
+                            copy_async16(dst + w, row_at + w);
+                    } else {  // a thread's own octs
+                        const int w = min(part[m].oct, 16);
 #pragma unroll
-                    for (int j = 0; j < NV; ++j)
-                        if (t + j * LPR < octs)
+                        for (int j = 0; j < NV; ++j)
+                            if (t + j * kLanes < octs)
 #pragma unroll
-                            for (int h = 0; h < part[m].oct / w; ++h) {
-                                const uint32_t dst =
-                                    to + part[m].at + ((j * (part[m].oct / w) + h) * blockDim.x + threadIdx.x) * w;
-                                const char* from = row + (t + j * LPR) * part[m].oct + h * 16;
-                                if (w == 16)
-                                    copy_async16(dst, from);
-                                else
-                                    copy_async8(dst, from);
-                            }
+                                for (int h = 0; h < part[m].oct / w; ++h) {
+                                    const uint32_t dst =
+                                        to + part[m].at + ((j * (part[m].oct / w) + h) * kSubThreads + threadIdx.x) * w;
+                                    const char* from = row_at + (t + j * kLanes) * part[m].oct + h * 16;
+                                    if (w == 16)
+                                        copy_async16(dst, from);
+                                    else
+                                        copy_async8(dst, from);
+                                }
+                    }
                 }
         }
         copy_commit();
@@ -457,16 +463,16 @@ struct RowRing {
     // The first rows.
     __device__ __forceinline__ void start(const RowMap<LPR>& map)
     {
+        row = map.first;
         if constexpr (LPR == 0) {
             if (threadIdx.x == 0) {
                 for (int i = 0; i < stages; ++i)
                     mbar_init(bars + i * 8, 1);
                 fence_mbar_init();
-            }
-            __syncthreads();
-            if (threadIdx.x == 0)
                 for (int i = 0; i < stages && i < map.all; ++i)
                     fill(map.first + i * map.step, i);
+            }
+            __syncthreads();
         } else {
             for (int i = 0; i < stages - 1; ++i)
                 copy(map.first + i * map.step, i < map.mine, i, map.t);
@@ -475,16 +481,19 @@ struct RowRing {
     // Row `it` has arrived (false: the wait gave up).
     __device__ __forceinline__ bool arrive(const RowMap<LPR>& map, int it, uint64_t limit_ns)
     {
+        direct = at_edge(row);
         if constexpr (LPR == 0)
-            return wait(limit_ns);
+            return mbar_wait_bounded(bars + stage * 8, phase, limit_ns);
         copy(map.first + (it + stages - 1) * map.step, it + stages - 1 < map.mine, stages - 1, map.t);
         copy_wait(stages - 1);
+        if (ANY)
+            __syncwarp();
         return true;
     }
     // LPR = 0, after a barrier in row `it`: nobody reads row it - 1 any more.
     __device__ __forceinline__ void refill(const RowMap<LPR>& map, int it)
     {
-        if (LPR == 0 && stages > 1 && threadIdx.x == 0 && it > 0 && it - 1 + stages < map.all)
+        if (LPR == 0 && threadIdx.x == 0 && stages > 1 && it > 0 && it - 1 + stages < map.all)
             fill(map.first + (it - 1 + stages) * map.step, stage == 0 ? stages - 1 : stage - 1);
     }
     // The end of row `it`.
@@ -495,7 +504,15 @@ struct RowRing {
             if (threadIdx.x == 0 && it + 1 < map.all)
                 fill(map.first + (it + 1) * map.step, 0);
         }
-        next();
+        if (LPR != 0 && ANY)
+            __syncwarp();  // the stage's next words may come from another lane
+        row += map.step;
+        at_stage += stage_bytes;
+        if (++stage == stages) {
+            stage = 0;
+            at_stage = 0;
+            phase ^= 1;
+        }
     }
     // Gave up in row `it`, before its refill: the copies in flight are waited
     // for before the CTA's memory goes back.
@@ -503,14 +520,79 @@ struct RowRing {
     {
         if (LPR == 0 && threadIdx.x == 0)
             for (int i = it; i < map.all && i < (it > 0 && stages > 1 ? it - 1 : it) + stages; ++i) {
-                wait(limit_ns);
-                next();
+                mbar_wait_bounded(bars + stage * 8, phase, limit_ns);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
+    }
+
+    // Address of word h of oct j of matrix m in the current stage.
+    __device__ __forceinline__ uint32_t word(int m, int j, int h) const
+    {
+        const uint32_t at = base + at_stage + part[m].at;
+        if constexpr (LPR == 0)
+            return at + (threadIdx.x + j * blockDim.x) * part[m].oct + h * 16;
+        if constexpr (ANY)
+            return at + threadIdx.x / kLanes * region(m) + (threadIdx.x % kLanes + j * kLanes) * part[m].oct + h * 16;
+        const int w = min(part[m].oct, 16);
+        return at + ((j * (part[m].oct / w) + h) * kSubThreads + threadIdx.x) * w;
+    }
+    // Oct j, at column c, with n > 0 values inside the row.
+    template <typename T>
+    __device__ __forceinline__ void read(int m, int j, int c, int n, Oct& o) const
+    {
+        if constexpr (!ANY) {
+            if constexpr (sizeof(T) == 2)
+                unpack_oct(lds128(word(m, j, 0)), o);
+            else
+                words_to_oct(lds128(word(m, j, 0)), lds128(word(m, j, 1)), o);
+        } else {
+            if (direct) {
+                const T* from = reinterpret_cast<const T*>(part[m].src + row * part[m].next_row) + c;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = i < n ? load_f(from + i) : 0.0f;
+                return;
+            }
+            const int s = static_cast<int>(shift(m, row) / sizeof(T));
+            if constexpr (sizeof(T) == 2) {
+                unpack_oct(shifted(lds128(word(m, j, 0)), lds128(word(m, j, 1)), s), o);
+            } else {
+                uint4 lo, hi;
+                shifted(lds128(word(m, j, 0)), lds128(word(m, j, 1)), lds128(word(m, j, 2)), s, lo, hi);
+                words_to_oct(lo, hi, o);
+            }
+            keep_first(o, n);
+        }
+    }
+    // A checkpoint's codes, as their own values (the pad columns' are zero).
+    __device__ __forceinline__ void read_codes(int m, int j, int c, Oct& o) const
+    {
+        uint2 w;
+        if (ANY && direct)
+            w = *reinterpret_cast<const uint2*>(part[m].src + row * part[m].next_row + c);
+        else
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(word(m, j, 0)) : "memory");
+        decode_oct(w, o);
     }
 };
 
-template <typename T, typename TY, int LPR, int NV>
-__global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_fwd_kernel(NormFwdArgs a, int stages)
+// Writes an oct at column c: n of its values, none of them for n <= 0.
+template <bool ANY, typename T>
+__device__ __forceinline__ void put_oct(T* p, const Oct& o, int n, int c, int C, Top<T>& top)
+{
+    if constexpr (ANY) {
+        const int lane = threadIdx.x & 31;
+        store_ragged(p, o, n, lane > 0 && c > 0, lane < 31 && c + 8 < C && n > 0, top);
+    } else if (n > 0) {
+        store_oct(p, o, top);
+    }
+}
+
+template <typename T, typename TY, int LPR, int NV, bool ANY>
+__global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float part[2][kMaxThreads / 32];
@@ -524,10 +606,12 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     const int c0 = 8 * map.t, dc = 8 * map.tpr;  // columns of oct j: c0 + j dc ..
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER, add = a.residual != nullptr;
-    RowRing<LPR, NV, 2> ring_;
+    RowRing<LPR, NV, 2, ANY> ring_;
     ring_.part[0] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
     ring_.part[1] = {static_cast<const char*>(a.residual), a.ldr * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
-    ring_.layout(ring, stages, C / 8);
+    ring_.cols_ = C;
+    ring_.layout(ring, stages, C, a.rows);
+    auto count = [&](bool in, int j) { return in ? min(C - c0 - j * dc, 8) : 0; };  // an oct's values
 
     constexpr bool KEEP = NV <= 2;  // weights and biases stay in registers
     Oct wt[KEEP ? NV : 1], bi[KEEP ? NV : 1];
@@ -535,8 +619,8 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (c0 + j * dc < C) {
-                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
-                param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, bi[j]);
+                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, wt[j]);
+                param_oct<ANY>(a.bias, a.w_dtype, c0 + j * dc, C, 0.0f, bi[j]);
             }
     Top<TY> top;
     Top<T> sum_top;
@@ -544,35 +628,40 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     TY* to_y = static_cast<TY*>(a.y) + map.first * a.ldy + c0;
     uint8_t* to_codes = a.save.codes + map.first * (G * kAct8Group) + c0;
     uint8_t* to_sf = a.save.sf + map.first * G + c0 / kAct8Group;
+    const int64_t sum_step = map.step * a.lds, y_step = map.step * a.ldy;
+    const int64_t codes_step = map.step * (G * kAct8Group), sf_step = map.step * G;
+    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
     ring_.start(map);
     bool bad = false;
     int it = 0;
     for (; it < map.all; ++it) {
-        bad = !ring_.arrive(map, it, a.wait_ns) || (it == a.fail_at && threadIdx.x == blockDim.x - 1);
+        bad = !ring_.arrive(map, it, a.wait_ns) || it == fail_at;
         const bool in = it < map.mine;
         Oct v[NV];
         float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            const int n = count(in, j);
             v[j].fill(0.0f);
-            if (in && c0 + j * dc < C) {
-                ring_.template read<T>(0, j, v[j]);
-                if (add) {
-                    Oct q;
-                    ring_.template read<T>(1, j, q);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        q.p[k] = __fadd2_rn(v[j].p[k], q.p[k]);
-                    store_oct(to_sum + j * dc, q, sum_top);
-                    if constexpr (sizeof(T) == 2)
-                        unpack_oct(pack_oct(q), v[j]);  // as it was stored
-                    else
-                        v[j] = q;
-                }
+            if (n > 0)
+                ring_.template read<T>(0, j, c0 + j * dc, n, v[j]);
+            if (add) {
+                Oct q;
+                q.fill(0.0f);
+                if (n > 0)
+                    ring_.template read<T>(1, j, c0 + j * dc, n, q);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    sum2 = __fadd2_rn(sum2, v[j].p[k]);
+                    q.p[k] = __fadd2_rn(v[j].p[k], q.p[k]);
+                put_oct<ANY>(to_sum + j * dc, q, n, c0 + j * dc, C, sum_top);
+                if constexpr (sizeof(T) == 2)
+                    unpack_oct(pack_oct(q), v[j]);  // as it was stored
+                else
+                    v[j] = q;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sum2 = __fadd2_rn(sum2, v[j].p[k]);
         }
         float mean = 0.0f;
         if (layer) {
@@ -583,12 +672,17 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         float2 sq2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (c0 + j * dc < C)
+            if (c0 + j * dc < C) {
+                Oct d;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 d = __fadd2_rn(v[j].p[k], both(-mean));
-                    sq2 = __ffma2_rn(d, d, sq2);
-                }
+                for (int k = 0; k < 4; ++k)
+                    d.p[k] = __fadd2_rn(v[j].p[k], both(-mean));
+                if constexpr (ANY)
+                    keep_first(d, C - c0 - j * dc);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sq2 = __ffma2_rn(d.p[k], d.p[k], sq2);
+            }
         // RMS norm has one sum per row: its words alternate with the row
         const float rstd = rsqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1], bad) * inv_c + a.eps);
         if (LPR == 0 && bad)
@@ -603,18 +697,19 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (in && c0 + j * dc < C) {
-                Oct &w = wt[KEEP ? j : 0], &b = bi[KEEP ? j : 0], y;
-                if constexpr (!KEEP) {
-                    param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, w);
-                    param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, b);
-                }
+            const int n = count(in, j);
+            Oct &w = wt[KEEP ? j : 0], &b = bi[KEEP ? j : 0], y;
+            if (!KEEP && n > 0) {
+                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, w);
+                param_oct<ANY>(a.bias, a.w_dtype, c0 + j * dc, C, 0.0f, b);
+            }
+            if (ANY || n > 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 h = __fmul2_rn(__fadd2_rn(v[j].p[k], both(-mean)), both(rstd));
                     y.p[k] = __ffma2_rn(h, w.p[k], b.p[k]);
                 }
-                store_oct(to_y + j * dc, y, top);
+                put_oct<ANY>(to_y + j * dc, y, n, c0 + j * dc, C, top);
             }
             if (a.save.codes) {
                 uint8_t e;
@@ -626,10 +721,10 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
                 }
             }
         }
-        to_sum += map.step * a.lds;
-        to_y += map.step * a.ldy;
-        to_codes += map.step * (G * kAct8Group);
-        to_sf += map.step * G;
+        to_sum += sum_step;
+        to_y += y_step;
+        to_codes += codes_step;
+        to_sf += sf_step;
         ring_.done(map, it);
     }
     if (LPR == 0 && bad) {
@@ -647,7 +742,7 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
 // CTA; dy h and g h come from one reading of the row, dx from what was kept of
 // it in registers (up to two octs a thread) or from a second reading of shared
 // memory.
-template <typename T, typename TY, bool FROM8, int LPR, int NV>
+template <typename T, typename TY, bool FROM8, int LPR, int NV, bool ANY>
 __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, int stages)
 {
     constexpr bool KEEP = NV <= 2;
@@ -663,14 +758,16 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     const int c0 = 8 * map.t, dc = 8 * map.tpr;
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER, add = a.dres != nullptr;
-    RowRing<LPR, NV, 3> ring_;
+    RowRing<LPR, NV, 3, ANY> ring_;
     ring_.part[0] = {static_cast<const char*>(a.dy), a.ldy * static_cast<int64_t>(sizeof(TY)), 8 * sizeof(TY), 0};
     if constexpr (FROM8)
         ring_.part[1] = {reinterpret_cast<const char*>(a.x8.codes), G * int64_t{kAct8Group}, 8, 0};
     else
         ring_.part[1] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
     ring_.part[2] = {static_cast<const char*>(a.dres), a.ldres * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
-    ring_.layout(ring, stages, C / 8);
+    ring_.cols_ = C;
+    ring_.layout(ring, stages, C, a.rows);
+    auto count = [&](bool in, int j) { return in ? min(C - c0 - j * dc, 8) : 0; };  // an oct's values
 
     struct RowWords {  // what a row needs beside its matrices, loaded a row ahead
         float mean, rstd;
@@ -697,7 +794,7 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (c0 + j * dc < C)
-                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
+                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, wt[j]);
     Oct dw[NV], db[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -706,6 +803,8 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     }
     Top<T> top;
     T* to_dx = static_cast<T*>(a.dx) + map.first * a.lddx + c0;
+    const int64_t dx_step = map.step * a.lddx;
+    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
     ring_.start(map);
     RowWords next = row_words(0 < map.mine);
     bool bad = false;
@@ -714,18 +813,18 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         const bool in = it < map.mine;
         const RowWords cur = next;
         next = row_words(it + 1 < map.mine);
-        bad = !ring_.arrive(map, it, a.wait_ns) || (it == a.fail_at && threadIdx.x == blockDim.x - 1);
+        bad = !ring_.arrive(map, it, a.wait_ns) || it == fail_at;
         // dy, and g and h of oct j
-        auto load = [&](int j, Oct& dy, Oct& g, Oct& h) {
-            ring_.template read<TY>(0, j, dy);
+        auto load = [&](int j, int n, Oct& dy, Oct& g, Oct& h) {
+            ring_.template read<TY>(0, j, c0 + j * dc, n, dy);
             if constexpr (FROM8) {
-                decode_oct(ring_.read_codes(1, j), h);
+                ring_.read_codes(1, j, c0 + j * dc, h);
                 const float2 scale = both(act8_scale(cur.e[j]));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // the product is exact
                     h.p[k] = __ffma2_rn(h.p[k], scale, both(-cur.mean));
             } else {
-                ring_.template read<T>(1, j, h);
+                ring_.template read<T>(1, j, c0 + j * dc, n, h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     h.p[k] = __fadd2_rn(h.p[k], both(-cur.mean));
@@ -733,20 +832,20 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
             if constexpr (KEEP)
                 g = wt[j];
             else
-                param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, g);
+                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, g);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 h.p[k] = __fmul2_rn(h.p[k], both(cur.rstd));
-                g.p[k] = __fmul2_rn(g.p[k], dy.p[k]);
+                g.p[k] = __fmul2_rn(g.p[k], dy.p[k]);  // zero past the row's end, as dy
             }
         };
         Oct kg[KEEP ? NV : 1], kh[KEEP ? NV : 1];
         float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (in && c0 + j * dc < C) {
+            if (const int n = count(in, j); n > 0) {
                 Oct dy, &g = kg[KEEP ? j : 0], &h = kh[KEEP ? j : 0];
-                load(j, dy, g, h);
+                load(j, n, dy, g, h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     sgh = __ffma2_rn(g.p[k], h.p[k], sgh);
@@ -762,20 +861,21 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         const float2 c1 = both(-s.x * inv_c), c2 = both(layer ? -s.y * inv_c : 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (in && c0 + j * dc < C) {
+            if (const int n = count(in, j); ANY || n > 0) {
                 Oct dy, q, &g = kg[KEEP ? j : 0], &h = kh[KEEP ? j : 0];
-                if constexpr (!KEEP)
-                    load(j, dy, g, h);
-                if (add)
-                    ring_.template read<T>(2, j, q);
-                else
-                    q.fill(0.0f);
+                q.fill(0.0f);
+                if (n > 0) {
+                    if constexpr (!KEEP)
+                        load(j, n, dy, g, h);
+                    if (add)
+                        ring_.template read<T>(2, j, c0 + j * dc, n, q);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h.p[k], c1, g.p[k]), c2), both(cur.rstd), q.p[k]);
-                store_oct(to_dx + j * dc, q, top);
+                put_oct<ANY>(to_dx + j * dc, q, n, c0 + j * dc, C, top);
             }
-        to_dx += map.step * a.lddx;
+        to_dx += dx_step;
         ring_.done(map, it);
     }
     if (LPR == 0 && bad) {
@@ -793,7 +893,14 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     if constexpr (LPR == 0) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (c0 + j * dc < C)
+            if (ANY) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c0 + j * dc + i < C) {
+                        out[c0 + j * dc + i] = dw[j][i];
+                        out[to_db + c0 + j * dc + i] = db[j][i];
+                    }
+            } else if (c0 + j * dc < C)
 #pragma unroll
                 for (int k = 0; k < 4; k += 2) {
                     float* const to = out + c0 + j * dc + 2 * k;
@@ -842,14 +949,15 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
 // How a width is spread over threads: octs of whole groups, so that a group's
 // four lanes all exist.  Two octs a thread as long as 512 threads suffice (the
 // weights, the column sums and a row's values then fit 128 registers), four
-// above 8192 columns.  Up to 512 columns a warp, or a part of one, takes a row.
+// above 8192 columns.  Up to 512 columns a warp, or a part of one, takes a row
+// (`any`: rows at any address: a whole warp).
 struct WideShape {
     int lpr, nv, threads;
 };
-WideShape wide_shape(int64_t cols)
+WideShape wide_shape(int64_t cols, bool any)
 {
     const int octs = static_cast<int>(act8_groups(cols)) * 4;
-    if (octs <= 16)
+    if (octs <= 16 && !any)
         return {octs <= 8 ? 8 : 16, 1, kSubThreads};
     if (octs <= 64)
         return {32, octs <= 32 ? 1 : 2, kSubThreads};
@@ -869,6 +977,8 @@ RingPlan ring_plan(int64_t stage_bytes, int threads, int registers, int most)
     RingPlan p;
     p.per_sm = std::min(32, std::min(65536 / ((registers + 7) / 8 * 8 * threads), 2048 / threads));
     p.per_sm = std::max(1, p.per_sm);
+    if (stage_bytes == 0)  // no ring
+        return {p.per_sm, 0};
     while (p.per_sm > 1 && p.per_sm * 2 * stage_bytes > kRingBytes)
         --p.per_sm;
     p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, kRingBytes / (p.per_sm * stage_bytes))));
@@ -879,7 +989,7 @@ bool wide_rows(const void* p, int64_t ld, int bytes)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * bytes) % 16 == 0;
 }
-bool wide_cols(int64_t cols) { return cols % 8 == 0 && cols <= kMaxWide; }
+bool wide_cols(int64_t cols) { return cols <= kMaxWide; }
 
 int launched()
 {
@@ -923,64 +1033,81 @@ int launch_ring(const A& a, const WideShape& w, int64_t stage_bytes, size_t leas
     return launched();
 }
 
-template <typename T, typename TY>
+// Bytes of a stage's share of one matrix.
+int64_t stage_part(const WideShape& w, int64_t cols, int oct, bool any)
+{
+    const int64_t region = region_bytes(static_cast<int>((cols + 7) / 8), oct, any);
+    return w.lpr == 0 ? region : any ? w.threads / w.lpr * region : static_cast<int64_t>(w.nv) * w.threads * oct;
+}
+
+template <typename T, typename TY, bool ANY>
 int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
-    const WideShape w = wide_shape(a.cols);
-    const int64_t bytes = static_cast<int64_t>(w.nv) * w.threads * 8 * sizeof(T) * (a.residual ? 2 : 1);
+    const WideShape w = wide_shape(a.cols, ANY);
+    const int64_t bytes = stage_part(w, a.cols, 8 * sizeof(T), ANY) * (a.residual ? 2 : 1);
     const int64_t most = INT32_MAX;
     unsigned grid;
-    if (w.lpr == 8)
-        return launch_ring<norm_fwd_kernel<T, TY, 8, 1>>(a, w, bytes, 0, most, &grid, d, s);
-    if (w.lpr == 16)
-        return launch_ring<norm_fwd_kernel<T, TY, 16, 1>>(a, w, bytes, 0, most, &grid, d, s);
+    if constexpr (!ANY) {
+        if (w.lpr == 8)
+            return launch_ring<norm_fwd_kernel<T, TY, 8, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+        if (w.lpr == 16)
+            return launch_ring<norm_fwd_kernel<T, TY, 16, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+    }
     if (w.lpr == 32 && w.nv == 1)
-        return launch_ring<norm_fwd_kernel<T, TY, 32, 1>>(a, w, bytes, 0, most, &grid, d, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 32, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.lpr == 32)
-        return launch_ring<norm_fwd_kernel<T, TY, 32, 2>>(a, w, bytes, 0, most, &grid, d, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 32, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.nv == 2)
-        return launch_ring<norm_fwd_kernel<T, TY, 0, 2>>(a, w, bytes, 0, most, &grid, d, s);
-    return launch_ring<norm_fwd_kernel<T, TY, 0, 4>>(a, w, bytes, 0, most, &grid, d, s);
+        return launch_ring<norm_fwd_kernel<T, TY, 0, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+    return launch_ring<norm_fwd_kernel<T, TY, 0, 4, ANY>>(a, w, bytes, 0, most, &grid, d, s);
 }
 
-// Most CTAs of the backward kernel, each with its partial sums: 512 threads an
-// SM, 152 SMs.  A pure function of the shape: the workspace is sized by it.
+// Most CTAs of a backward kernel, each with its partial sums: 768 threads an SM
+// at most, 152 SMs.  A pure function of the shape: the workspace is sized by it.
 constexpr int kPartSms = 152;
-int64_t bwd_ctas(int64_t rows, int64_t cols)
+int64_t ctas_of(const WideShape& w, int64_t rows)
 {
-    const WideShape w = wide_shape(cols);
     const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
-    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * std::min(8, kMaxThreads / w.threads));
+    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * std::min(8, std::max(1, 768 / w.threads)));
 }
 
-template <typename T, typename TY, bool FROM8>
+// dw and db from `parts` partial sums of each column, where they are asked for.
+int join(const NormBwdArgs& a, int parts, cudaStream_t s)
+{
+    if (!a.dw && !a.db)
+        return MX_OK;
+    norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kJoinWarps * 32, 0, s>>>(
+        a.parts, a.cols, parts, a.dw, a.db);
+    return launched();
+}
+
+template <typename T, typename TY, bool FROM8, bool ANY>
 int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
-    const WideShape w = wide_shape(a.cols);
-    const int64_t bytes =
-        static_cast<int64_t>(w.nv) * w.threads * 8 * (sizeof(TY) + (FROM8 ? 1 : sizeof(T)) + (a.dres ? sizeof(T) : 0));
-    const int64_t most = bwd_ctas(a.rows, a.cols);
+    const WideShape w = wide_shape(a.cols, ANY);
+    const int64_t bytes = stage_part(w, a.cols, 8 * sizeof(TY), ANY) +
+                          stage_part(w, a.cols, FROM8 ? 8 : 8 * sizeof(T), ANY) +
+                          (a.dres ? stage_part(w, a.cols, 8 * sizeof(T), ANY) : 0);
+    const int64_t most = ctas_of(w, a.rows);
     // the column sums of a warp-per-row CTA pass through the ring's memory
     const size_t least = w.lpr ? static_cast<size_t>(w.nv) * w.lpr * 8 * sizeof(float) * (w.threads / 32) : 0;
     unsigned grid;
-    int rc;
-    if (w.lpr == 8)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 8, 1>>(a, w, bytes, least, most, &grid, d, s);
-    else if (w.lpr == 16)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 16, 1>>(a, w, bytes, least, most, &grid, d, s);
-    else if (w.lpr == 32 && w.nv == 1)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 1>>(a, w, bytes, least, most, &grid, d, s);
+    int rc = MX_ERR_UNSUPPORTED;
+    if constexpr (!ANY) {
+        if (w.lpr == 8)
+            rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 8, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
+        else if (w.lpr == 16)
+            rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 16, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
+    }
+    if (w.lpr == 32 && w.nv == 1)
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 32)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 2>>(a, w, bytes, least, most, &grid, d, s);
-    else if (w.nv == 2)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 2>>(a, w, bytes, least, most, &grid, d, s);
-    else
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 4>>(a, w, bytes, least, most, &grid, d, s);
-    if (rc != MX_OK || (!a.dw && !a.db))
-        return rc;
-    norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kJoinWarps * 32, 0, s>>>(
-        a.parts, a.cols, static_cast<int>(grid), a.dw, a.db);
-    return launched();
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
+    else if (w.lpr == 0 && w.nv == 2)
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
+    else if (w.lpr == 0)
+        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 4, ANY>>(a, w, bytes, least, most, &grid, d, s);
+    return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
 }
 
 int64_t any_parts(int64_t rows) { return std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, 64); }
@@ -989,42 +1116,48 @@ template <typename T, typename TY>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
-    if (wide_cols(a.cols) && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
-        wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) && wide_rows(a.weight, 8, wb) &&
-        wide_rows(a.bias, 8, wb))
-        return fwd_wide<T, TY>(a, d, s);
+    if (wide_cols(a.cols)) {
+        const bool aligned = a.cols % 8 == 0 && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
+                             wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) &&
+                             wide_rows(a.weight, 8, wb) && wide_rows(a.bias, 8, wb);
+        return aligned ? fwd_wide<T, TY, false>(a, d, s) : fwd_wide<T, TY, true>(a, d, s);
+    }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
     norm_fwd_any_kernel<T, TY><<<grid, kRowThreads, 0, s>>>(a);
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    return launched();
 }
 
 template <typename T, typename TY>
 int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
     const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
-    if (wide_cols(a.cols) && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
-        wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) && wide_rows(a.weight, 8, wb))
-        return a.x8.codes ? bwd_wide<T, TY, true>(a, d, s) : bwd_wide<T, TY, false>(a, d, s);
+    if (wide_cols(a.cols)) {
+        const bool aligned = a.cols % 8 == 0 && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
+                             wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) &&
+                             wide_rows(a.weight, 8, wb);
+        if (a.x8.codes)
+            return aligned ? bwd_wide<T, TY, true, false>(a, d, s) : bwd_wide<T, TY, true, true>(a, d, s);
+        return aligned ? bwd_wide<T, TY, false, false>(a, d, s) : bwd_wide<T, TY, false, true>(a, d, s);
+    }
     if (a.dw || a.db) {  // before dx, which may be dy's memory
         const int parts = static_cast<int>(any_parts(a.rows));
-        const unsigned cols32 = static_cast<unsigned>((a.cols + 31) / 32);
-        norm_dw_any_kernel<T, TY><<<dim3(cols32, parts), kRowThreads, 0, s>>>(a);
-        norm_dw_join_kernel<<<dim3(cols32, 2), kJoinWarps * 32, 0, s>>>(a.parts, a.cols, parts, a.dw, a.db);
-        count_launch();
-        count_launch();
+        norm_dw_any_kernel<T, TY><<<dim3(static_cast<unsigned>((a.cols + 31) / 32), parts), kRowThreads, 0, s>>>(a);
+        int rc = launched();
+        if (rc != MX_OK || (rc = join(a, parts, s)) != MX_OK)
+            return rc;
     }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
     norm_dx_any_kernel<T, TY><<<grid, kRowThreads, 0, s>>>(a);
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    return launched();
 }
 
 }  // namespace
 
 int64_t norm_bwd_parts(int64_t rows, int64_t cols)
 {
-    return std::max(any_parts(rows), wide_cols(cols) ? bwd_ctas(rows, cols) : int64_t{1});
+    if (!wide_cols(cols))
+        return any_parts(rows);
+    return std::max(ctas_of(wide_shape(cols, false), rows), ctas_of(wide_shape(cols, true), rows));
 }
 
 int launch_norm_fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
