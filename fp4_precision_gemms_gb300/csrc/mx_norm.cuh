@@ -1,0 +1,43 @@
+// mx_norm.cuh -- what the norm's translation units share.
+#pragma once
+#include "mx_act8.cuh"
+#include "mx_internal.cuh"
+
+namespace mx {
+
+// Weight or bias c (`absent` without one).
+__device__ __forceinline__ float param(const void* p, int dtype, int64_t c, float absent)
+{
+    if (!p)
+        return absent;
+    return dtype == MX_OUT_BF16 ? load_f(static_cast<const __nv_bfloat16*>(p) + c) : static_cast<const float*>(p)[c];
+}
+// Eight of them, from a 16-byte boundary.
+__device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float absent, Oct& o)
+{
+    if (!p) {
+        o.fill(absent);
+    } else if (dtype == MX_OUT_BF16) {
+        unpack_oct(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), o);
+    } else {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + c);
+        words_to_oct(__ldg(q), __ldg(q + 1), o);
+    }
+}
+
+inline int launched()
+{
+    count_launch();
+    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+// The kernels of norm_cta.cu: columns they take, and their threads (two octs
+// each, whole checkpoint groups).
+constexpr int64_t kCtaMinCols = 513, kCtaMaxCols = 8192;
+inline int cta_threads(int64_t cols) { return static_cast<int>((act8_groups(cols) * 2 + 31) / 32 * 32); }
+int launch_norm_fwd_cta(const NormFwdArgs& a, const Device& d, cudaStream_t s);
+// At most `most` CTAs; *grid returns their number, each of which leaves a row of
+// partial sums.
+int launch_norm_bwd_cta(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid);
+
+}  // namespace mx

@@ -5,6 +5,7 @@
 
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
+#include "mx_norm.cuh"
 #include "mx_ptx.cuh"
 
 namespace mx {
@@ -34,13 +35,6 @@ __device__ __forceinline__ float cta_sum(float v, float* part)
     for (int w = 0; w < kRowWarps; ++w)
         v += part[w];
     return v;
-}
-
-__device__ __forceinline__ float param(const void* p, int dtype, int64_t c, float absent)
-{
-    if (!p)
-        return absent;
-    return dtype == MX_OUT_BF16 ? load_f(static_cast<const __nv_bfloat16*>(p) + c) : static_cast<const float*>(p)[c];
 }
 
 // ------------------------------------------------------------------ any width
@@ -320,23 +314,16 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2* part, bool& bad)
     }
 }
 
-// Eight of the weights or biases.
+// Eight of the weights or biases.  ANY: at any address, those inside the row.
 template <bool ANY>
 __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, int C, float absent, Oct& o)
 {
-    if (!p) {
-        o.fill(absent);
-    } else if (ANY) {
+    if constexpr (ANY) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             o[i] = c + i < C ? param(p, dtype, c + i, absent) : 0.0f;
-    } else if (dtype == MX_OUT_BF16) {
-        unpack_oct(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), o);
     } else {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + 1);
-        o.p[0] = make_float2(a.x, a.y), o.p[1] = make_float2(a.z, a.w);
-        o.p[2] = make_float2(b.x, b.y), o.p[3] = make_float2(b.z, b.w);
+        mx::param_oct(p, dtype, c, absent, o);
     }
 }
 
@@ -991,12 +978,6 @@ bool wide_rows(const void* p, int64_t ld, int bytes)
 }
 bool wide_cols(int64_t cols) { return cols <= kMaxWide; }
 
-int launched()
-{
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
-}
-
 // Launches a ring kernel: its grid fills the GPU, or covers the rows, and has
 // at most `most` CTAs.  `grid` returns it.
 template <void (*KERNEL)(NormFwdArgs, int)>
@@ -1057,8 +1038,9 @@ int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
         return launch_ring<norm_fwd_kernel<T, TY, 32, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.lpr == 32)
         return launch_ring<norm_fwd_kernel<T, TY, 32, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
-    if (w.nv == 2)
-        return launch_ring<norm_fwd_kernel<T, TY, 0, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+    if constexpr (ANY)
+        if (w.nv == 2)
+            return launch_ring<norm_fwd_kernel<T, TY, 0, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     return launch_ring<norm_fwd_kernel<T, TY, 0, 4, ANY>>(a, w, bytes, 0, most, &grid, d, s);
 }
 
@@ -1103,10 +1085,12 @@ int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
         rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 32)
         rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
-    else if (w.lpr == 0 && w.nv == 2)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
-    else if (w.lpr == 0)
+    else if (w.lpr == 0 && w.nv == 4)
         rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 4, ANY>>(a, w, bytes, least, most, &grid, d, s);
+    if constexpr (ANY) {
+        if (w.lpr == 0 && w.nv == 2)
+            rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
+    }
     return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
 }
 
@@ -1120,6 +1104,8 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
         const bool aligned = a.cols % 8 == 0 && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
                              wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) &&
                              wide_rows(a.weight, 8, wb) && wide_rows(a.bias, 8, wb);
+        if (aligned && a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols)
+            return launch_norm_fwd_cta(a, d, s);
         return aligned ? fwd_wide<T, TY, false>(a, d, s) : fwd_wide<T, TY, true>(a, d, s);
     }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
@@ -1135,6 +1121,11 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
         const bool aligned = a.cols % 8 == 0 && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
                              wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) &&
                              wide_rows(a.weight, 8, wb);
+        if (aligned && a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols) {
+            unsigned grid;
+            const int rc = launch_norm_bwd_cta(a, static_cast<int>(ctas_of(wide_shape(a.cols, false), a.rows)), d, s, &grid);
+            return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
+        }
         if (a.x8.codes)
             return aligned ? bwd_wide<T, TY, true, false>(a, d, s) : bwd_wide<T, TY, true, true>(a, d, s);
         return aligned ? bwd_wide<T, TY, false, false>(a, d, s) : bwd_wide<T, TY, false, true>(a, d, s);

@@ -1,0 +1,560 @@
+// norm_cta.cu -- the norm's kernels for rows of 520 to 8192 columns on 16-byte
+// boundaries (a multiple of eight): the widths and layouts of model training.
+//
+// A CTA takes a row at a time (forward: two, where enough rows are there), two
+// octs (eight columns) a thread, with the weights, the biases and the backward
+// pass's column sums in registers over all of its rows.  One thread copies the
+// rows to come into a ring of shared-memory stages by bulk copies, an mbarrier
+// says when a stage is there, and the row sums' barrier that the stage before it
+// may be filled again.
+//
+// What bounds them: with the ring the memory system is never idle, and what is
+// left is the number of instructions a row takes.  The options are therefore
+// compile-time, fp32 arithmetic is two-wide, and the forward kernel's two rows
+// share one barrier and one exchange per sum.
+#include <algorithm>
+
+#include "mx_act8.cuh"
+#include "mx_internal.cuh"
+#include "mx_norm.cuh"
+#include "mx_ptx.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kMaxThreads = 512;  // 128 registers each
+constexpr int kMaxStages = 6;
+constexpr int kBarBytes = 64;
+constexpr int kWarps = kMaxThreads / 32;
+
+// The ring: PARTS matrices, R rows of each in a stage.
+template <int PARTS, int R>
+struct Pipe {
+    const char* src[PARTS];     // row 0
+    int64_t next_row[PARTS];    // bytes
+    uint32_t row_bytes[PARTS];  // to copy
+    uint32_t at[PARTS];         // in a stage
+    uint32_t bars, base, stage_bytes, here;  // here: the current stage
+    int stages, stage = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ void layout(uint8_t* smem, int stages_)
+    {
+        stages = stages_;
+        bars = smem_u32(smem);
+        here = base = bars + kBarBytes;
+        uint32_t n = 0;
+#pragma unroll
+        for (int m = 0; m < PARTS; ++m) {
+            at[m] = n;
+            n += R * row_bytes[m];
+        }
+        stage_bytes = n;
+    }
+    // Rows r, r + 1 .. of the tile into stage st (one thread).
+    __device__ __forceinline__ void fill(int64_t r, int64_t rows, int st)
+    {
+        const int n = static_cast<int>(min(static_cast<int64_t>(R), rows - r));
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int m = 0; m < PARTS; ++m)
+            bytes += n * row_bytes[m];
+        mbar_arrive_expect_tx(bars + st * 8, bytes);
+#pragma unroll
+        for (int m = 0; m < PARTS; ++m)
+            for (int i = 0; i < n; ++i)
+                bulk_load(base + st * stage_bytes + at[m] + i * row_bytes[m], src[m] + (r + i) * next_row[m], row_bytes[m],
+                          bars + st * 8);
+    }
+    // Barriers and the first tiles; ends with a CTA barrier.
+    __device__ __forceinline__ void start(int64_t rows, int tiles)
+    {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < stages; ++i)
+                mbar_init(bars + i * 8, 1);
+            fence_mbar_init();
+            for (int i = 0; i < stages && i < tiles; ++i)
+                fill((blockIdx.x + static_cast<int64_t>(i) * gridDim.x) * R, rows, i);
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ bool wait(uint64_t limit_ns) { return mbar_wait_bounded(bars + stage * 8, phase, limit_ns); }
+    // After a barrier that follows every thread's last reading of tile it's stage.
+    __device__ __forceinline__ void refill(int it, int64_t rows, int tiles, int st)
+    {
+        if (threadIdx.x == 0 && it >= 0 && it + stages < tiles)
+            fill((blockIdx.x + static_cast<int64_t>(it + stages) * gridDim.x) * R, rows, st);
+    }
+    __device__ __forceinline__ int before() const { return stage == 0 ? stages - 1 : stage - 1; }
+    __device__ __forceinline__ void next()
+    {
+        here += stage_bytes;
+        if (++stage == stages) {
+            stage = 0;
+            here = base;
+            phase ^= 1;
+        }
+    }
+    // A wait of tile `it` ran out: those in flight (the newest is tile
+    // last - 1) are waited for before the CTA's memory goes back.
+    __device__ __forceinline__ void abandon(int it, int last, uint64_t limit_ns, int* status)
+    {
+        if (threadIdx.x != 0)
+            return;
+        atomicExch(status, MX_ERR_TIMEOUT);
+        for (; it < last; ++it) {
+            wait(limit_ns);
+            next();
+        }
+    }
+};
+
+// A thread's oct j of a row at `row` in shared memory.
+template <typename T>
+__device__ __forceinline__ void oct_from(uint32_t row, int j, Oct& o)
+{
+    const uint32_t at = row + (threadIdx.x + j * blockDim.x) * (8 * sizeof(T));
+    if constexpr (sizeof(T) == 2)
+        unpack_oct(lds128(at), o);
+    else
+        words_to_oct(lds128(at), lds128(at + 16), o);
+}
+
+// Two sums over the CTA, in a fixed order, known to every thread.  The halves of
+// a warp exchange them, so that each half finishes one; `part` has an entry a
+// warp, zero past the CTA's.  The barrier also collects `bad`.
+__device__ __forceinline__ float2 cta_sum2(float x, float y, float2* part, bool& bad)
+{
+    const bool second = threadIdx.x & 16;
+    float s = second ? y : x;
+    s += __shfl_xor_sync(0xFFFFFFFFu, second ? x : y, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if ((threadIdx.x & 15) == 0)
+        reinterpret_cast<float*>(part)[threadIdx.x >> 4] = s;
+    bad = __syncthreads_or(bad);
+    const float4* p = reinterpret_cast<const float4*>(part);
+    float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p[w].x, p[w].y), make_float2(p[w].z, p[w].w)));
+    if (blockDim.x > 256)
+#pragma unroll
+        for (int w = 4; w < 8; ++w)
+            sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p[w].x, p[w].y), make_float2(p[w].z, p[w].w)));
+    return sum;
+}
+
+// ADD: the residual is added; SAVE: the checkpoint is kept; R rows at a time.
+template <typename T, typename TY, bool ADD, bool SAVE, int R>
+__global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float2 part[2][kWarps];
+    if (threadIdx.x < kWarps)
+        part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
+    const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
+    const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
+    const bool own[2] = {c0 < C, c0 + dc < C};
+    const float inv_c = 1.0f / static_cast<float>(C);
+    const bool layer = a.kind == MX_NORM_LAYER;
+    const int64_t tiles_of_all = (a.rows + R - 1) / R;
+    const int tiles = static_cast<int>((tiles_of_all - blockIdx.x + gridDim.x - 1) / gridDim.x);
+
+    Pipe<ADD ? 2 : 1, R> pipe;
+    pipe.src[0] = static_cast<const char*>(a.x);
+    pipe.next_row[0] = a.ldx * static_cast<int64_t>(sizeof(T));
+    pipe.row_bytes[0] = C * sizeof(T);
+    if constexpr (ADD) {
+        pipe.src[1] = static_cast<const char*>(a.residual);
+        pipe.next_row[1] = a.ldr * static_cast<int64_t>(sizeof(T));
+        pipe.row_bytes[1] = C * sizeof(T);
+    }
+    pipe.layout(smem, stages);
+    pipe.start(a.rows, tiles);
+
+    Oct wt[2], bi[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        wt[j].fill(0.0f);
+        bi[j].fill(0.0f);
+        if (own[j]) {
+            param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
+            param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, bi[j]);
+        }
+    }
+    int64_t r = static_cast<int64_t>(blockIdx.x) * R;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+    TY* to_y = static_cast<TY*>(a.y) + r * a.ldy + c0;
+    T* to_sum = ADD ? static_cast<T*>(a.sum_out) + r * a.lds + c0 : nullptr;
+    uint8_t* to_codes = SAVE ? a.save.codes + r * (G * kAct8Group) + c0 : nullptr;
+    const int64_t y_step = step * a.ldy, sum_step = step * a.lds, codes_step = step * (G * kAct8Group);
+    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
+
+    Top<TY> top;
+    Top<T> unused;
+    bool bad = false;
+    int it = 0;
+    for (; it < tiles; ++it) {
+        bad = !pipe.wait(a.wait_ns) || it == fail_at;
+        const bool two = R == 2 && r + 1 < a.rows;  // the last tile may have one row
+        Oct v[R][2];
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                v[q][j].fill(0.0f);
+                if (own[j]) {
+                    oct_from<T>(pipe.here + q * pipe.row_bytes[0], j, v[q][j]);
+                    if constexpr (ADD) {
+                        Oct o;
+                        oct_from<T>(pipe.here + pipe.at[1] + q * pipe.row_bytes[1], j, o);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o.p[k] = __fadd2_rn(v[q][j].p[k], o.p[k]);
+                        if (q == 0 || two)
+                            store_oct(to_sum + q * a.lds + j * dc, o, unused);
+                        if constexpr (sizeof(T) == 2)
+                            unpack_oct(pack_oct(o), v[q][j]);  // as it was stored
+                        else
+                            v[q][j] = o;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s2 = __fadd2_rn(s2, v[q][j].p[k]);
+            }
+            sum[q] = s2.x + s2.y;
+        }
+        float2 mean = make_float2(0.0f, 0.0f);
+        if (layer) {
+            mean = cta_sum2(sum[0], sum[1], part[0], bad);
+            if (bad)
+                break;
+            mean.x *= inv_c;
+            mean.y *= inv_c;
+        }
+        if constexpr (SAVE) {
+#pragma unroll
+            for (int q = 0; q < R; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint8_t e;
+                    const uint2 codes = encode_oct(v[q][j], e);
+                    if (c0 + j * dc < G * kAct8Group && (q == 0 || two)) {
+                        *reinterpret_cast<uint2*>(to_codes + q * (G * kAct8Group) + j * dc) = codes;
+                        if ((threadIdx.x & 3) == 0)
+                            a.save.sf[(r + q) * G + (c0 + j * dc) / kAct8Group] = e;
+                    }
+                }
+        }
+        float sq[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const float2 m = both(q == 0 ? -mean.x : -mean.y);
+            float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (own[j])
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        v[q][j].p[k] = __fadd2_rn(v[q][j].p[k], m);
+                        s2 = __ffma2_rn(v[q][j].p[k], v[q][j].p[k], s2);
+                    }
+            sq[q] = s2.x + s2.y;
+        }
+        // RMS norm has one barrier per tile: its words alternate
+        const float2 var = cta_sum2(sq[0], sq[1], part[layer ? 1 : it & 1], bad);
+        if (bad)
+            break;
+        pipe.refill(it, a.rows, tiles, pipe.stage);  // the tile's rows are in registers
+        const float2 rstd = make_float2(rsqrtf(var.x * inv_c + a.eps), rsqrtf(var.y * inv_c + a.eps));
+        if (threadIdx.x < R && (threadIdx.x == 0 || two)) {
+            const bool first = threadIdx.x == 0;
+            if (a.mean && layer)
+                a.mean[r + threadIdx.x] = first ? mean.x : mean.y;
+            if (a.rstd)
+                a.rstd[r + threadIdx.x] = first ? rstd.x : rstd.y;
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (q == 0 || two) {
+                const float2 s = both(q == 0 ? rstd.x : rstd.y);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (own[j]) {
+                        Oct y;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y.p[k] = __ffma2_rn(__fmul2_rn(v[q][j].p[k], s), wt[j].p[k], bi[j].p[k]);
+                        store_oct(to_y + q * a.ldy + j * dc, y, top);
+                    }
+            }
+        r += step;
+        to_y += y_step;
+        if constexpr (ADD)
+            to_sum += sum_step;
+        if constexpr (SAVE)
+            to_codes += codes_step;
+        pipe.next();
+    }
+    if (bad) {
+        pipe.abandon(it, min(tiles, it + stages), a.wait_ns, a.status);
+        return;
+    }
+    if (a.amax)
+        flush_top(a.amax, top);
+}
+
+// dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
+// is the checkpoint.  ADD: the residual path's gradient joins dx.
+template <typename T, typename TY, bool FROM8, bool ADD>
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a, int stages)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float2 part[2][kWarps];
+    if (threadIdx.x < kWarps)
+        part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
+    const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
+    const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
+    const bool own[2] = {c0 < C, c0 + dc < C};
+    const float inv_c = 1.0f / static_cast<float>(C);
+    const bool layer = a.kind == MX_NORM_LAYER;
+    const int tiles = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
+
+    Pipe<ADD ? 3 : 2, 1> pipe;
+    pipe.src[0] = static_cast<const char*>(a.dy);
+    pipe.next_row[0] = a.ldy * static_cast<int64_t>(sizeof(TY));
+    pipe.row_bytes[0] = C * sizeof(TY);
+    pipe.src[1] = FROM8 ? reinterpret_cast<const char*>(a.x8.codes) : static_cast<const char*>(a.x);
+    pipe.next_row[1] = FROM8 ? G * int64_t{kAct8Group} : a.ldx * static_cast<int64_t>(sizeof(T));
+    pipe.row_bytes[1] = FROM8 ? G * kAct8Group : C * sizeof(T);
+    if constexpr (ADD) {
+        pipe.src[2] = static_cast<const char*>(a.dres);
+        pipe.next_row[2] = a.ldres * static_cast<int64_t>(sizeof(T));
+        pipe.row_bytes[2] = C * sizeof(T);
+    }
+    pipe.layout(smem, stages);
+    pipe.start(a.rows, tiles);
+
+    Oct wt[2], dw[2], db[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        wt[j].fill(0.0f);
+        dw[j].fill(0.0f);
+        db[j].fill(0.0f);
+        if (own[j])
+            param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
+    }
+    int64_t r = blockIdx.x;
+    const int64_t step = gridDim.x;
+    T* to_dx = static_cast<T*>(a.dx) + r * a.lddx + c0;
+    const int64_t dx_step = step * a.lddx;
+    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
+    // what a row needs beside its matrices, loaded a row ahead
+    const int last_group = G - 1, g0 = min(c0 / kAct8Group, last_group), g1 = min((c0 + dc) / kAct8Group, last_group);
+    float mean = 0.0f, rstd = a.rstd[r];
+    if (layer)
+        mean = a.mean[r];
+    uint32_t e0 = 127, e1 = 127;
+    if constexpr (FROM8) {
+        e0 = a.x8.sf[r * G + g0];
+        e1 = a.x8.sf[r * G + g1];
+    }
+
+    Top<T> top;
+    bool bad = false;
+    int it = 0;
+    for (; it < tiles; ++it) {
+        const float2 m = both(-mean), s = both(rstd);
+        const float2 scale[2] = {both(act8_scale(e0)), both(act8_scale(e1))};
+        r += step;
+        if (it + 1 < tiles) {
+            rstd = a.rstd[r];
+            if (layer)
+                mean = a.mean[r];
+            if constexpr (FROM8) {
+                e0 = a.x8.sf[r * G + g0];
+                e1 = a.x8.sf[r * G + g1];
+            }
+        }
+        bad = !pipe.wait(a.wait_ns) || it == fail_at;
+        Oct g[2], h[2];
+        float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (own[j]) {
+                Oct dy;
+                oct_from<TY>(pipe.here, j, dy);
+                if constexpr (FROM8) {
+                    uint2 w;
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(w.x), "=r"(w.y)
+                                 : "r"(pipe.here + pipe.at[1] + c0 + j * dc)
+                                 : "memory");
+                    decode_oct(w, h[j]);
+                } else {
+                    oct_from<T>(pipe.here + pipe.at[1], j, h[j]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // the code's product with its scale is exact
+                    h[j].p[k] = FROM8 ? __ffma2_rn(h[j].p[k], scale[j], m) : __fadd2_rn(h[j].p[k], m);
+                    h[j].p[k] = __fmul2_rn(h[j].p[k], s);
+                    g[j].p[k] = __fmul2_rn(dy.p[k], wt[j].p[k]);
+                    sgh = __ffma2_rn(g[j].p[k], h[j].p[k], sgh);
+                    sg = __fadd2_rn(sg, g[j].p[k]);
+                    dw[j].p[k] = __ffma2_rn(dy.p[k], h[j].p[k], dw[j].p[k]);
+                    db[j].p[k] = __fadd2_rn(db[j].p[k], dy.p[k]);
+                }
+            }
+        const float2 sums = cta_sum2(sgh.x + sgh.y, sg.x + sg.y, part[it & 1], bad);
+        if (bad)
+            break;
+        if (stages > 1)
+            pipe.refill(it - 1, a.rows, tiles, pipe.before());  // nobody reads the row before any more
+        const float2 c1 = both(-sums.x * inv_c), c2 = both(layer ? -sums.y * inv_c : 0.0f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (own[j]) {
+                Oct q;
+                if constexpr (ADD)
+                    oct_from<T>(pipe.here + pipe.at[2], j, q);
+                else
+                    q.fill(0.0f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h[j].p[k], c1, g[j].p[k]), c2), s, q.p[k]);
+                store_oct(to_dx + j * dc, q, top);
+            }
+        to_dx += dx_step;
+        if (stages == 1) {
+            __syncthreads();
+            pipe.refill(it, a.rows, tiles, 0);
+        }
+        pipe.next();
+    }
+    if (bad) {
+        pipe.abandon(it, min(tiles, stages > 1 ? max(it - 1, 0) + stages : it + 1), a.wait_ns, a.status);
+        return;
+    }
+    if (a.amax)
+        flush_top(a.amax, top);
+    if (!a.dw && !a.db)
+        return;
+    float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C + c0;
+    const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (own[j])
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                float* const to = out + j * dc + 2 * k;
+                *reinterpret_cast<float4*>(to) = make_float4(dw[j].p[k].x, dw[j].p[k].y, dw[j].p[k + 1].x, dw[j].p[k + 1].y);
+                *reinterpret_cast<float4*>(to + to_db) =
+                    make_float4(db[j].p[k].x, db[j].p[k].y, db[j].p[k + 1].x, db[j].p[k + 1].y);
+            }
+}
+
+template <typename A, void (*KERNEL)(A, int)>
+int registers_of()
+{
+    static const int n = [] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
+    }();
+    return n;
+}
+constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
+
+// CTAs an SM that registers allow, with at least two stages each where that can be.
+template <typename A, void (*KERNEL)(A, int)>
+int ctas_per_sm(int threads, int64_t stage_bytes)
+{
+    int n = std::max(1, std::min(16, 65536 / ((registers_of<A, KERNEL>() + 7) / 8 * 8 * threads)));
+    while (n > 1 && n * 2 * stage_bytes > kRingBytes)
+        --n;
+    return n;
+}
+template <typename A, void (*KERNEL)(A, int)>
+int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned grid, cudaStream_t s)
+{
+    const int stages =
+        static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxStages, kRingBytes / (per_sm * stage_bytes))));
+    const size_t smem = static_cast<size_t>(stage_bytes) * stages + kBarBytes;
+    if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
+        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return MX_ERR_CUDA;
+    KERNEL<<<grid, threads, smem, s>>>(a, stages);
+    return launched();
+}
+
+template <typename T, typename TY, bool ADD, bool SAVE>
+int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+{
+    const int threads = cta_threads(a.cols);
+    const int64_t row = a.cols * static_cast<int64_t>(sizeof(T)) * (ADD ? 2 : 1);
+    using A = NormFwdArgs;
+    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1>;
+    constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2>;
+    // Two rows at a time where every CTA still has several tiles and a ring of
+    // three stages fits; a row at a time spreads few rows over more SMs.
+    const int n2 = ctas_per_sm<A, two>(threads, 2 * row);
+    if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
+        return launch<A, two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
+    const int n1 = ctas_per_sm<A, one>(threads, row);
+    return launch<A, one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
+}
+
+template <typename T, typename TY>
+int fwd_options(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+{
+    if (a.residual)
+        return a.save.codes ? fwd<T, TY, true, true>(a, d, s) : fwd<T, TY, true, false>(a, d, s);
+    return a.save.codes ? fwd<T, TY, false, true>(a, d, s) : fwd<T, TY, false, false>(a, d, s);
+}
+
+template <typename T, typename TY, bool FROM8, bool ADD>
+int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
+{
+    const int threads = cta_threads(a.cols);
+    const int64_t row = a.cols * static_cast<int64_t>(sizeof(TY) + (FROM8 ? 0 : sizeof(T)) + (ADD ? sizeof(T) : 0)) +
+                        (FROM8 ? act8_groups(a.cols) * kAct8Group : 0);
+    using A = NormBwdArgs;
+    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD>;
+    const int n = ctas_per_sm<A, kernel>(threads, row);
+    *grid = static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(a.rows, most), int64_t{n} * d.sms));
+    return launch<A, kernel>(a, threads, row, n, *grid, s);
+}
+
+template <typename T, typename TY>
+int bwd_options(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
+{
+    if (a.x8.codes)
+        return a.dres ? bwd<T, TY, true, true>(a, most, d, s, grid) : bwd<T, TY, true, false>(a, most, d, s, grid);
+    return a.dres ? bwd<T, TY, false, true>(a, most, d, s, grid) : bwd<T, TY, false, false>(a, most, d, s, grid);
+}
+
+}  // namespace
+
+int launch_norm_fwd_cta(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+{
+    using bf = __nv_bfloat16;
+    if (a.x_dtype == MX_OUT_BF16)
+        return a.y_dtype == MX_OUT_BF16 ? fwd_options<bf, bf>(a, d, s) : fwd_options<bf, float>(a, d, s);
+    return a.y_dtype == MX_OUT_BF16 ? fwd_options<float, bf>(a, d, s) : fwd_options<float, float>(a, d, s);
+}
+
+int launch_norm_bwd_cta(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
+{
+    using bf = __nv_bfloat16;
+    if (a.dx_dtype == MX_OUT_BF16)
+        return a.dy_dtype == MX_OUT_BF16 ? bwd_options<bf, bf>(a, most, d, s, grid) : bwd_options<bf, float>(a, most, d, s, grid);
+    return a.dy_dtype == MX_OUT_BF16 ? bwd_options<float, bf>(a, most, d, s, grid)
+                                     : bwd_options<float, float>(a, most, d, s, grid);
+}
+
+}  // namespace mx
