@@ -141,7 +141,7 @@ struct NormFwdArgs {
     int x_dtype, y_dtype, w_dtype, kind;
     int* status;
     uint64_t wait_ns;
-    int fail_at;  // test hook: in this row of each CTA a wait counts as run out; -1 never
+    int fail_at;  // test hook: this tile of each CTA is never copied, so that its wait runs out; -1 none
 };
 struct NormBwdArgs {
     const void* dy;

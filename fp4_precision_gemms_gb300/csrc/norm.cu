@@ -349,7 +349,7 @@ struct RowRing {
     static constexpr int kLanes = LPR ? LPR : 1;
     RingPart part[PARTS];
     uint32_t base, stage_bytes, bars, at_stage = 0;
-    int stages, stage = 0, octs;
+    int stages, stage = 0, octs, skip = -1;  // skip: test hook, a row that is never copied
     uint32_t phase = 0;
     int64_t rows, row = 0, edge = 1;
     bool direct = false;  // ANY: the current row is read from where it is
@@ -381,9 +381,12 @@ struct RowRing {
         stage_bytes = at;
     }
 
-    // Row r into stage st: LPR = 0, one thread.
-    __device__ __forceinline__ void fill(int64_t r, int st)
+    // The CTA's row number `it` into stage st: LPR = 0, one thread.
+    __device__ __forceinline__ void fill(const RowMap<LPR>& map, int it, int st)
     {
+        if (it == skip)
+            return;
+        const int64_t r = map.first + it * map.step;
         const uint32_t bar = bars + st * 8, to = base + st * stage_bytes;
         if (at_edge(r)) {
             mbar_arrive(bar);
@@ -457,7 +460,7 @@ struct RowRing {
                     mbar_init(bars + i * 8, 1);
                 fence_mbar_init();
                 for (int i = 0; i < stages && i < map.all; ++i)
-                    fill(map.first + i * map.step, i);
+                    fill(map, i, i);
             }
             __syncthreads();
         } else {
@@ -481,7 +484,7 @@ struct RowRing {
     __device__ __forceinline__ void refill(const RowMap<LPR>& map, int it)
     {
         if (LPR == 0 && threadIdx.x == 0 && stages > 1 && it > 0 && it - 1 + stages < map.all)
-            fill(map.first + (it - 1 + stages) * map.step, stage == 0 ? stages - 1 : stage - 1);
+            fill(map, it - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
     }
     // The end of row `it`.
     __device__ __forceinline__ void done(const RowMap<LPR>& map, int it)
@@ -489,7 +492,7 @@ struct RowRing {
         if (LPR == 0 && stages == 1) {
             __syncthreads();
             if (threadIdx.x == 0 && it + 1 < map.all)
-                fill(map.first + (it + 1) * map.step, 0);
+                fill(map, it + 1, 0);
         }
         if (LPR != 0 && ANY)
             __syncwarp();  // the stage's next words may come from another lane
@@ -617,12 +620,12 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
     uint8_t* to_sf = a.save.sf + map.first * G + c0 / kAct8Group;
     const int64_t sum_step = map.step * a.lds, y_step = map.step * a.ldy;
     const int64_t codes_step = map.step * (G * kAct8Group), sf_step = map.step * G;
-    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
+    ring_.skip = a.fail_at;
     ring_.start(map);
     bool bad = false;
     int it = 0;
     for (; it < map.all; ++it) {
-        bad = !ring_.arrive(map, it, a.wait_ns) || it == fail_at;
+        bad = !ring_.arrive(map, it, a.wait_ns);
         const bool in = it < map.mine;
         Oct v[NV];
         float2 sum2 = make_float2(0.0f, 0.0f);
@@ -791,7 +794,7 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
     Top<T> top;
     T* to_dx = static_cast<T*>(a.dx) + map.first * a.lddx + c0;
     const int64_t dx_step = map.step * a.lddx;
-    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
+    ring_.skip = a.fail_at;
     ring_.start(map);
     RowWords next = row_words(0 < map.mine);
     bool bad = false;
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         const bool in = it < map.mine;
         const RowWords cur = next;
         next = row_words(it + 1 < map.mine);
-        bad = !ring_.arrive(map, it, a.wait_ns) || it == fail_at;
+        bad = !ring_.arrive(map, it, a.wait_ns);
         // dy, and g and h of oct j
         auto load = [&](int j, int n, Oct& dy, Oct& g, Oct& h) {
             ring_.template read<TY>(0, j, c0 + j * dc, n, dy);

@@ -35,12 +35,13 @@ struct Pipe {
     uint32_t row_bytes[PARTS];  // to copy
     uint32_t at[PARTS];         // in a stage
     uint32_t bars, base, stage_bytes, here;  // here: the current stage
-    int stages, stage = 0;
+    int stages, stage = 0, skip;  // skip: test hook, a tile that is never copied
     uint32_t phase = 0;
 
-    __device__ __forceinline__ void layout(uint8_t* smem, int stages_)
+    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int skip_)
     {
         stages = stages_;
+        skip = skip_;
         bars = smem_u32(smem);
         here = base = bars + kBarBytes;
         uint32_t n = 0;
@@ -51,9 +52,12 @@ struct Pipe {
         }
         stage_bytes = n;
     }
-    // Rows r, r + 1 .. of the tile into stage st (one thread).
-    __device__ __forceinline__ void fill(int64_t r, int64_t rows, int st)
+    // Tile `it` (rows r, r + 1 ..) of the CTA into stage st (one thread).
+    __device__ __forceinline__ void fill(int it, int64_t rows, int st)
     {
+        if (it == skip)
+            return;
+        const int64_t r = (blockIdx.x + static_cast<int64_t>(it) * gridDim.x) * R;
         const int n = static_cast<int>(min(static_cast<int64_t>(R), rows - r));
         uint32_t bytes = 0;
 #pragma unroll
@@ -74,7 +78,7 @@ struct Pipe {
                 mbar_init(bars + i * 8, 1);
             fence_mbar_init();
             for (int i = 0; i < stages && i < tiles; ++i)
-                fill((blockIdx.x + static_cast<int64_t>(i) * gridDim.x) * R, rows, i);
+                fill(i, rows, i);
         }
         __syncthreads();
     }
@@ -83,7 +87,7 @@ struct Pipe {
     __device__ __forceinline__ void refill(int it, int64_t rows, int tiles, int st)
     {
         if (threadIdx.x == 0 && it >= 0 && it + stages < tiles)
-            fill((blockIdx.x + static_cast<int64_t>(it + stages) * gridDim.x) * R, rows, st);
+            fill(it + stages, rows, st);
     }
     __device__ __forceinline__ int before() const { return stage == 0 ? stages - 1 : stage - 1; }
     __device__ __forceinline__ void next()
@@ -146,8 +150,10 @@ __device__ __forceinline__ float2 cta_sum2(float x, float y, float2* part, bool&
     return sum;
 }
 
-// ADD: the residual is added; SAVE: the checkpoint is kept; R rows at a time.
-template <typename T, typename TY, bool ADD, bool SAVE, int R>
+// ADD: the residual is added; SAVE: the checkpoint is kept; R rows at a time;
+// FULL: every thread's octs lie inside the row (cols a multiple of 512), which
+// saves a tenth of the instructions.
+template <typename T, typename TY, bool ADD, bool SAVE, int R, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
     const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
-    const bool own[2] = {c0 < C, c0 + dc < C};
+    const bool own[2] = {FULL || c0 < C, FULL || c0 + dc < C};
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER;
     const int64_t tiles_of_all = (a.rows + R - 1) / R;
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
         pipe.next_row[1] = a.ldr * static_cast<int64_t>(sizeof(T));
         pipe.row_bytes[1] = C * sizeof(T);
     }
-    pipe.layout(smem, stages);
+    pipe.layout(smem, stages, a.fail_at);
     pipe.start(a.rows, tiles);
 
     Oct wt[2], bi[2];
@@ -190,14 +196,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
     T* to_sum = ADD ? static_cast<T*>(a.sum_out) + r * a.lds + c0 : nullptr;
     uint8_t* to_codes = SAVE ? a.save.codes + r * (G * kAct8Group) + c0 : nullptr;
     const int64_t y_step = step * a.ldy, sum_step = step * a.lds, codes_step = step * (G * kAct8Group);
-    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
 
     Top<TY> top;
     Top<T> unused;
     bool bad = false;
     int it = 0;
     for (; it < tiles; ++it) {
-        bad = !pipe.wait(a.wait_ns) || it == fail_at;
+        bad = !pipe.wait(a.wait_ns);
         const bool two = R == 2 && r + 1 < a.rows;  // the last tile may have one row
         Oct v[R][2];
         float sum[2] = {0.0f, 0.0f};
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
                 for (int j = 0; j < 2; ++j) {
                     uint8_t e;
                     const uint2 codes = encode_oct(v[q][j], e);
-                    if (c0 + j * dc < G * kAct8Group && (q == 0 || two)) {
+                    if ((FULL || c0 + j * dc < G * kAct8Group) && (q == 0 || two)) {
                         *reinterpret_cast<uint2*>(to_codes + q * (G * kAct8Group) + j * dc) = codes;
                         if ((threadIdx.x & 3) == 0)
                             a.save.sf[(r + q) * G + (c0 + j * dc) / kAct8Group] = e;
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
 
 // dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
 // is the checkpoint.  ADD: the residual path's gradient joins dx.
-template <typename T, typename TY, bool FROM8, bool ADD>
+template <typename T, typename TY, bool FROM8, bool ADD, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
     const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
-    const bool own[2] = {c0 < C, c0 + dc < C};
+    const bool own[2] = {FULL || c0 < C, FULL || c0 + dc < C};
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER;
     const int tiles = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         pipe.next_row[2] = a.ldres * static_cast<int64_t>(sizeof(T));
         pipe.row_bytes[2] = C * sizeof(T);
     }
-    pipe.layout(smem, stages);
+    pipe.layout(smem, stages, a.fail_at);
     pipe.start(a.rows, tiles);
 
     Oct wt[2], dw[2], db[2];
@@ -353,7 +358,6 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
     const int64_t step = gridDim.x;
     T* to_dx = static_cast<T*>(a.dx) + r * a.lddx + c0;
     const int64_t dx_step = step * a.lddx;
-    const int fail_at = threadIdx.x == blockDim.x - 1 ? a.fail_at : -1;
     // what a row needs beside its matrices, loaded a row ahead
     const int last_group = G - 1, g0 = min(c0 / kAct8Group, last_group), g1 = min((c0 + dc) / kAct8Group, last_group);
     float mean = 0.0f, rstd = a.rstd[r];
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
                 e1 = a.x8.sf[r * G + g1];
             }
         }
-        bad = !pipe.wait(a.wait_ns) || it == fail_at;
+        bad = !pipe.wait(a.wait_ns);
         Oct g[2], h[2];
         float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
 #pragma unroll
@@ -492,14 +496,14 @@ int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned gr
     return launched();
 }
 
-template <typename T, typename TY, bool ADD, bool SAVE>
+template <typename T, typename TY, bool ADD, bool SAVE, bool FULL>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     const int threads = cta_threads(a.cols);
     const int64_t row = a.cols * static_cast<int64_t>(sizeof(T)) * (ADD ? 2 : 1);
     using A = NormFwdArgs;
-    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1>;
-    constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2>;
+    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, FULL>;
+    constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL>;
     // Two rows at a time where every CTA still has several tiles and a ring of
     // three stages fits; a row at a time spreads few rows over more SMs.
     const int n2 = ctas_per_sm<A, two>(threads, 2 * row);
@@ -509,33 +513,46 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     return launch<A, one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
 }
 
-template <typename T, typename TY>
+bool full_rows(int64_t cols) { return cols == 16 * cta_threads(cols); }
+
+template <typename T, typename TY, bool FULL>
 int fwd_options(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     if (a.residual)
-        return a.save.codes ? fwd<T, TY, true, true>(a, d, s) : fwd<T, TY, true, false>(a, d, s);
-    return a.save.codes ? fwd<T, TY, false, true>(a, d, s) : fwd<T, TY, false, false>(a, d, s);
+        return a.save.codes ? fwd<T, TY, true, true, FULL>(a, d, s) : fwd<T, TY, true, false, FULL>(a, d, s);
+    return a.save.codes ? fwd<T, TY, false, true, FULL>(a, d, s) : fwd<T, TY, false, false, FULL>(a, d, s);
+}
+template <typename T, typename TY>
+int fwd_any(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+{
+    return full_rows(a.cols) ? fwd_options<T, TY, true>(a, d, s) : fwd_options<T, TY, false>(a, d, s);
 }
 
-template <typename T, typename TY, bool FROM8, bool ADD>
+template <typename T, typename TY, bool FROM8, bool ADD, bool FULL>
 int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     const int threads = cta_threads(a.cols);
     const int64_t row = a.cols * static_cast<int64_t>(sizeof(TY) + (FROM8 ? 0 : sizeof(T)) + (ADD ? sizeof(T) : 0)) +
                         (FROM8 ? act8_groups(a.cols) * kAct8Group : 0);
     using A = NormBwdArgs;
-    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD>;
+    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, FULL>;
     const int n = ctas_per_sm<A, kernel>(threads, row);
     *grid = static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(a.rows, most), int64_t{n} * d.sms));
     return launch<A, kernel>(a, threads, row, n, *grid, s);
 }
 
-template <typename T, typename TY>
+template <typename T, typename TY, bool FULL>
 int bwd_options(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     if (a.x8.codes)
-        return a.dres ? bwd<T, TY, true, true>(a, most, d, s, grid) : bwd<T, TY, true, false>(a, most, d, s, grid);
-    return a.dres ? bwd<T, TY, false, true>(a, most, d, s, grid) : bwd<T, TY, false, false>(a, most, d, s, grid);
+        return a.dres ? bwd<T, TY, true, true, FULL>(a, most, d, s, grid) : bwd<T, TY, true, false, FULL>(a, most, d, s, grid);
+    return a.dres ? bwd<T, TY, false, true, FULL>(a, most, d, s, grid) : bwd<T, TY, false, false, FULL>(a, most, d, s, grid);
+}
+
+template <typename T, typename TY>
+int bwd_any(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
+{
+    return full_rows(a.cols) ? bwd_options<T, TY, true>(a, most, d, s, grid) : bwd_options<T, TY, false>(a, most, d, s, grid);
 }
 
 }  // namespace
@@ -544,17 +561,17 @@ int launch_norm_fwd_cta(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     using bf = __nv_bfloat16;
     if (a.x_dtype == MX_OUT_BF16)
-        return a.y_dtype == MX_OUT_BF16 ? fwd_options<bf, bf>(a, d, s) : fwd_options<bf, float>(a, d, s);
-    return a.y_dtype == MX_OUT_BF16 ? fwd_options<float, bf>(a, d, s) : fwd_options<float, float>(a, d, s);
+        return a.y_dtype == MX_OUT_BF16 ? fwd_any<bf, bf>(a, d, s) : fwd_any<bf, float>(a, d, s);
+    return a.y_dtype == MX_OUT_BF16 ? fwd_any<float, bf>(a, d, s) : fwd_any<float, float>(a, d, s);
 }
 
 int launch_norm_bwd_cta(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     using bf = __nv_bfloat16;
     if (a.dx_dtype == MX_OUT_BF16)
-        return a.dy_dtype == MX_OUT_BF16 ? bwd_options<bf, bf>(a, most, d, s, grid) : bwd_options<bf, float>(a, most, d, s, grid);
-    return a.dy_dtype == MX_OUT_BF16 ? bwd_options<float, bf>(a, most, d, s, grid)
-                                     : bwd_options<float, float>(a, most, d, s, grid);
+        return a.dy_dtype == MX_OUT_BF16 ? bwd_any<bf, bf>(a, most, d, s, grid) : bwd_any<bf, float>(a, most, d, s, grid);
+    return a.dy_dtype == MX_OUT_BF16 ? bwd_any<float, bf>(a, most, d, s, grid)
+                                     : bwd_any<float, float>(a, most, d, s, grid);
 }
 
 }  // namespace mx

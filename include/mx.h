@@ -485,13 +485,13 @@ void mx_debug_set_quant_impl(int impl);
  * initial value) turns it off.  Nothing faults or hangs. */
 void mx_debug_set_tile_fail_at(int64_t tile);
 
-/* Test hook for the bounded waits of mx_norm_fwd / mx_norm_bwd (16-byte aligned
- * rows of 520 to 16384 columns): for later calls made by the calling host
- * thread, the last thread of every CTA treats its wait for that CTA's row
- * number `row` (0-based, in the CTA's own order) as timed out.  The kernel then
- * waits for its own copies in flight, stops and reports MX_ERR_TIMEOUT through
- * the status word; outputs of such a call are unspecified.  -1 (the initial
- * value) turns it off.  Nothing faults or hangs. */
+/* Test hook for the bounded waits of mx_norm_fwd / mx_norm_bwd (rows of more
+ * than 512 columns): for later calls made by the calling host thread, the copy
+ * of every CTA's row (or pair of rows) number `row`, 0-based in the CTA's own
+ * order, is left out and the limit of the waits is 2 ms.  The wait for it runs
+ * out; the kernel then waits for its other copies in flight, stops and reports
+ * MX_ERR_TIMEOUT through the status word; outputs of such a call are
+ * unspecified.  -1 (the initial value) turns it off.  Nothing faults or hangs. */
 void mx_debug_set_norm_fail_at(int64_t row);
 
 /* Test and tuning hook: 0 runs both gradients of mx_linear_bwd /
