@@ -329,18 +329,16 @@ Act8View ahead(Act8View v, int64_t rows, int64_t cols)
     return v;
 }
 
-int launched()
-{
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
-}
-
 template <typename T, int ACT>
 int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
 {
     const bool aligned = a.cols % 8 == 0 && wide(a.gate, a.ldg, a.dtype) && wide(a.h, a.ldh, a.dtype) && wide(a.up, a.ldu, a.dtype);
     const int64_t slab = slab_rows(a.cols);
+    int rc = launch_zero(a.amax, s);
+    if (rc != MX_OK)
+        return rc;
     for (int64_t r = 0; r < a.rows; r += slab) {
+        const bool early = a.amax && r == 0;
         ActArgs b = a;
         b.rows = std::min(slab, a.rows - r);
         b.gate = ahead(a.gate, r, a.ldg, a.dtype);
@@ -350,15 +348,15 @@ int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
         if (aligned && a.gated)
-            act_fwd_kernel<T, ACT, true, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, true, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
         else if (aligned)
-            act_fwd_kernel<T, ACT, false, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, false, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
         else if (a.gated)
-            act_fwd_kernel<T, ACT, true, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, true, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
         else
-            act_fwd_kernel<T, ACT, false, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
-        if (launched() != MX_OK)
-            return MX_ERR_CUDA;
+            rc = launch_kernel(act_fwd_kernel<T, ACT, false, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+        if (rc != MX_OK)
+            return rc;
     }
     return MX_OK;
 }
@@ -369,7 +367,11 @@ int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
     const bool aligned = a.cols % 8 == 0 && wide(a.h, a.ldh, a.dtype) && wide(a.dgate, a.lddg, a.dtype) && wide(a.dup, a.lddu, a.dtype) &&
                          wide(a.gate, a.ldg, a.dtype) && wide(a.up, a.ldu, a.dtype);
     const int64_t slab = slab_rows(a.cols);
+    int rc = launch_zero(a.amax, s);
+    if (rc != MX_OK)
+        return rc;
     for (int64_t r = 0; r < a.rows; r += slab) {
+        const bool early = a.amax && r == 0;
         ActArgs b = a;
         b.rows = std::min(slab, a.rows - r);
         b.gate = ahead(a.gate, r, a.ldg, a.dtype);
@@ -381,15 +383,15 @@ int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
         if (aligned && a.gated)
-            act_bwd_kernel<T, ACT, true, FROM8, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, true, FROM8, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
         else if (aligned)
-            act_bwd_kernel<T, ACT, false, FROM8, false><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, false, FROM8, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
         else if (a.gated)
-            act_bwd_kernel<T, ACT, true, FROM8, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, true, FROM8, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
         else
-            act_bwd_kernel<T, ACT, false, FROM8, true><<<unit_grid(m, d), kThreads, 0, s>>>(b, m);
-        if (launched() != MX_OK)
-            return MX_ERR_CUDA;
+            rc = launch_kernel(act_bwd_kernel<T, ACT, false, FROM8, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+        if (rc != MX_OK)
+            return rc;
     }
     return MX_OK;
 }
@@ -400,16 +402,17 @@ int save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8
 {
     const bool aligned = cols % 8 == 0 && wide(x, ldx, dtype);
     const int64_t slab = slab_rows(cols);
+    int rc = MX_OK;
     for (int64_t r = 0; r < rows; r += slab) {
         const int64_t n = std::min(slab, rows - r);
         const UnitMap m = unit_map(n, cols);
         const void* from = ahead(x, r, ldx, dtype);
         if (aligned)
-            act8_save_kernel<T, false><<<unit_grid(m, d), kThreads, 0, s>>>(from, ldx, n, cols, ahead(out, r, cols), m);
+            rc = launch_kernel(act8_save_kernel<T, false>, unit_grid(m, d), 1, kThreads, 0, false, s, from, ldx, n, cols, ahead(out, r, cols), m);
         else
-            act8_save_kernel<T, true><<<unit_grid(m, d), kThreads, 0, s>>>(from, ldx, n, cols, ahead(out, r, cols), m);
-        if (launched() != MX_OK)
-            return MX_ERR_CUDA;
+            rc = launch_kernel(act8_save_kernel<T, true>, unit_grid(m, d), 1, kThreads, 0, false, s, from, ldx, n, cols, ahead(out, r, cols), m);
+        if (rc != MX_OK)
+            return rc;
     }
     return MX_OK;
 }
@@ -419,16 +422,17 @@ int restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int 
 {
     const bool aligned = cols % 8 == 0 && wide(out, ldo, dtype);
     const int64_t slab = slab_rows(cols);
+    int rc = MX_OK;
     for (int64_t r = 0; r < rows; r += slab) {
         const int64_t n = std::min(slab, rows - r);
         const UnitMap m = unit_map(n, cols);
         void* to = ahead(out, r, ldo, dtype);
         if (aligned)
-            act8_restore_kernel<T, false><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(a, r, cols), cols, to, ldo, m);
+            rc = launch_kernel(act8_restore_kernel<T, false>, unit_grid(m, d), 1, kThreads, 0, false, s, ahead(a, r, cols), cols, to, ldo, m);
         else
-            act8_restore_kernel<T, true><<<unit_grid(m, d), kThreads, 0, s>>>(ahead(a, r, cols), cols, to, ldo, m);
-        if (launched() != MX_OK)
-            return MX_ERR_CUDA;
+            rc = launch_kernel(act8_restore_kernel<T, true>, unit_grid(m, d), 1, kThreads, 0, false, s, ahead(a, r, cols), cols, to, ldo, m);
+        if (rc != MX_OK)
+            return rc;
     }
     return MX_OK;
 }
@@ -453,7 +457,18 @@ int bwd_by_act(const ActArgs& a, const Device& d, cudaStream_t s)
     }
 }
 
+__global__ void zero_word_kernel(unsigned* word)
+{
+    let_next_launch_start();
+    *word = 0;
+}
+
 }  // namespace
+
+int launch_zero(unsigned* word, cudaStream_t s)
+{
+    return word ? launch_kernel(zero_word_kernel, 1, 1, 1, 0, false, s, word) : MX_OK;
+}
 
 int launch_act_fwd(const ActArgs& a, const Device& d, cudaStream_t s)
 {

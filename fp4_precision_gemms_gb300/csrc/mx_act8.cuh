@@ -10,6 +10,37 @@
 
 namespace mx {
 
+// Programmatic dependent launch: a kernel launched early may start while the
+// kernel before it in the stream still runs, and waits here for that kernel's
+// end and its writes (nothing to wait for in an ordinary launch).  The kernel
+// before says at its start that this may happen.
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// `early`: the launch may overlap the end of the one before.
+template <typename... P, typename... A>
+int launch_kernel(void (*kernel)(P...), unsigned grid_x, unsigned grid_y, int threads, size_t smem, bool early, cudaStream_t s,
+                  A... args)
+{
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid_x, grid_y);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = early ? 1 : 0;
+    count_launch();
+    if (cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...) == cudaSuccess)
+        return MX_OK;
+    (void)cudaGetLastError();
+    return MX_ERR_CUDA;
+}
+// Sets the word that flush_top folds into to zero (none: nothing is launched).
+int launch_zero(unsigned* word, cudaStream_t s);
+
 constexpr int kAct8Group = 32;  // columns that share one scale byte
 __host__ __device__ inline int64_t act8_groups(int64_t cols) { return (cols + kAct8Group - 1) / kAct8Group; }
 
@@ -233,11 +264,13 @@ struct Top<float> {
     __device__ __forceinline__ void value(float v) { m = max_nan(m, fabsf(v)); }
     __device__ __forceinline__ uint32_t bits() const { return __float_as_uint(m) & 0x7FFFFFFFu; }
 };
-// Folds the CTA's maxima into *out; a maximum does not depend on the order, and
-// most warps find theirs already covered.
+// Folds the CTA's maxima into *out, which the launch before this one sets to zero
+// (launch_zero); a maximum does not depend on the order, and most warps find
+// theirs already covered.
 template <typename T>
 __device__ __forceinline__ void flush_top(unsigned* out, const Top<T>& top)
 {
+    wait_for_launch_before();
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, top.bits());
     if ((threadIdx.x & 31) == 0 && m > *static_cast<volatile unsigned*>(out))
         atomicMax(out, m);

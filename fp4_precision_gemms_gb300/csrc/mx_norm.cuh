@@ -25,12 +25,6 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
     }
 }
 
-inline int launched()
-{
-    count_launch();
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
-}
-
 // The kernels of norm_cta.cu: columns they take, and their threads (two octs
 // each, whole checkpoint groups).
 constexpr int64_t kCtaMinCols = 513, kCtaMaxCols = 8192;

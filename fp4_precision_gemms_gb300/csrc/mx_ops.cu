@@ -142,8 +142,8 @@ int mx_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, i
     if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
         return ok.rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (ok(zero(amax_out, sizeof(float), s)).rc != MX_OK || empty(rows, cols))
-        return ok.rc;
+    if (empty(rows, cols))
+        return zero(amax_out, sizeof(float), s);
     NormFwdArgs a = {};
     a.x = x;
     a.residual = residual;
@@ -209,11 +209,8 @@ int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_
     if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
         return ok.rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ok(zero(amax_out, sizeof(float), s));
     if (empty(rows, cols))
-        return ok(zero(dw, cols * sizeof(float), s))(zero(db, cols * sizeof(float), s)).rc;
-    if (ok.rc != MX_OK)
-        return ok.rc;
+        return ok(zero(amax_out, sizeof(float), s))(zero(dw, cols * sizeof(float), s))(zero(db, cols * sizeof(float), s)).rc;
     NormBwdArgs a = {};
     a.dy = dy;
     a.x = x;
@@ -264,8 +261,8 @@ int mx_act_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu, int64
     if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
         return ok.rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (ok(zero(amax_out, sizeof(float), s)).rc != MX_OK || empty(rows, cols))
-        return ok.rc;
+    if (empty(rows, cols))
+        return zero(amax_out, sizeof(float), s);
     ActArgs a = {};
     a.gate = gate;
     a.up = up;
@@ -313,8 +310,8 @@ int mx_act_bwd(const void* dh, int64_t ldh, const void* gate, int64_t ldg, const
     if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
         return ok.rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (ok(zero(amax_out, sizeof(float), s)).rc != MX_OK || empty(rows, cols))
-        return ok.rc;
+    if (empty(rows, cols))
+        return zero(amax_out, sizeof(float), s);
     ActArgs a = {};
     a.gate = gate;
     a.up = up;

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_dx_any_kernel(NormBwdArgs a)
 template <typename T, typename TY>
 __global__ void __launch_bounds__(kRowThreads) norm_dw_any_kernel(NormBwdArgs a)
 {
+    let_next_launch_start();  // the join
     __shared__ float pw[kRowWarps][32], pb[kRowWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t C = a.cols, G = act8_groups(C), c = blockIdx.x * 32ll + lane;
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const flo
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = blockIdx.x * 32ll + lane;
     float* out = blockIdx.y ? db : dw;
+    wait_for_launch_before();
     if (!out)
         return;
     float v = 0.0f;
@@ -735,6 +737,7 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
 template <typename T, typename TY, bool FROM8, int LPR, int NV, bool ANY>
 __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, int stages)
 {
+    let_next_launch_start();  // the join of the partial sums
     constexpr bool KEEP = NV <= 2;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float2 part[2][kMaxThreads / 32];
@@ -1013,8 +1016,7 @@ int launch_ring(const A& a, const WideShape& w, int64_t stage_bytes, size_t leas
     if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
         cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MX_ERR_CUDA;
-    KERNEL<<<*grid, w.threads, smem, s>>>(a, p.stages);
-    return launched();
+    return launch_kernel(KERNEL, *grid, 1, w.threads, smem, a.amax != nullptr, s, a, p.stages);
 }
 
 // Bytes of a stage's share of one matrix.
@@ -1061,9 +1063,8 @@ int join(const NormBwdArgs& a, int parts, cudaStream_t s)
 {
     if (!a.dw && !a.db)
         return MX_OK;
-    norm_dw_join_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), kJoinWarps * 32, 0, s>>>(
-        a.parts, a.cols, parts, a.dw, a.db);
-    return launched();
+    return launch_kernel(norm_dw_join_kernel, static_cast<unsigned>((a.cols + 31) / 32), 2, kJoinWarps * 32, 0, true, s,
+                         a.parts, a.cols, parts, a.dw, a.db);
 }
 
 template <typename T, typename TY, bool FROM8, bool ANY>
@@ -1112,8 +1113,7 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
         return aligned ? fwd_wide<T, TY, false>(a, d, s) : fwd_wide<T, TY, true>(a, d, s);
     }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
-    norm_fwd_any_kernel<T, TY><<<grid, kRowThreads, 0, s>>>(a);
-    return launched();
+    return launch_kernel(norm_fwd_any_kernel<T, TY>, grid, 1, kRowThreads, 0, a.amax != nullptr, s, a);
 }
 
 template <typename T, typename TY>
@@ -1135,14 +1135,13 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
     }
     if (a.dw || a.db) {  // before dx, which may be dy's memory
         const int parts = static_cast<int>(any_parts(a.rows));
-        norm_dw_any_kernel<T, TY><<<dim3(static_cast<unsigned>((a.cols + 31) / 32), parts), kRowThreads, 0, s>>>(a);
-        int rc = launched();
+        int rc = launch_kernel(norm_dw_any_kernel<T, TY>, static_cast<unsigned>((a.cols + 31) / 32), parts, kRowThreads, 0,
+                               false, s, a);
         if (rc != MX_OK || (rc = join(a, parts, s)) != MX_OK)
             return rc;
     }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
-    norm_dx_any_kernel<T, TY><<<grid, kRowThreads, 0, s>>>(a);
-    return launched();
+    return launch_kernel(norm_dx_any_kernel<T, TY>, grid, 1, kRowThreads, 0, false, s, a);
 }
 
 }  // namespace
@@ -1156,6 +1155,9 @@ int64_t norm_bwd_parts(int64_t rows, int64_t cols)
 
 int launch_norm_fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
+    const int rc = launch_zero(a.amax, s);
+    if (rc != MX_OK)
+        return rc;
     using bf = __nv_bfloat16;
     if (a.x_dtype == MX_OUT_BF16)
         return a.y_dtype == MX_OUT_BF16 ? fwd<bf, bf>(a, d, s) : fwd<bf, float>(a, d, s);
@@ -1164,6 +1166,9 @@ int launch_norm_fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 
 int launch_norm_bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
+    const int rc = launch_zero(a.amax, s);
+    if (rc != MX_OK)
+        return rc;
     using bf = __nv_bfloat16;
     if (a.dx_dtype == MX_OUT_BF16)
         return a.dy_dtype == MX_OUT_BF16 ? bwd<bf, bf>(a, d, s) : bwd<bf, float>(a, d, s);

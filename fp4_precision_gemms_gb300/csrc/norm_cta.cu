@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float2 part[2][kWarps];
+    let_next_launch_start();  // the join of the partial sums
     if (threadIdx.x < kWarps)
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
@@ -492,8 +493,7 @@ int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned gr
     if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
         cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MX_ERR_CUDA;
-    KERNEL<<<grid, threads, smem, s>>>(a, stages);
-    return launched();
+    return launch_kernel(KERNEL, grid, 1, threads, smem, a.amax != nullptr, s, a, stages);
 }
 
 template <typename T, typename TY, bool ADD, bool SAVE, bool FULL>
