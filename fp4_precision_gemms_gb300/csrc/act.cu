@@ -46,11 +46,15 @@ __device__ __forceinline__ ValueSlope activate(float z)
 
 // A unit is eight columns of a row, a row has 4 G units (whole groups, so that
 // the four lanes of a group always work together; those past the row's end hold
-// zeros).  Each thread keeps kUnits units' loads in flight; a grid of kCtasPerSm
-// CTAs an SM strides over the units.  ANY: rows of any address and length; else
+// zeros).  A thread keeps units_in_flight() units' loads in flight, and a grid of
+// kFwdCtas, kBwdCtas or k8Ctas CTAs an SM strides over the units; 8192x14336 bf16
+// gated from or with checkpoints measured, in us, at 3 / 4 / 5 / 8 CTAs: forward
+// 158 / 150 / 160 / 159, backward 175 / 159 / 147 / 168; 4096x11008 saved and
+// restored 50 / 46 / 44 / 42.  One unit in place of two: 169, 162 and 55, but at
+// any address, where the shifts take the registers, 1023x11009 fp32 49 -> 40.  ANY: rows of any address and length; else
 // they start on 16-byte boundaries and their length is a multiple of eight.
-constexpr int kUnits = 2;
-constexpr int kCtasPerSm = 4;
+constexpr int kFwdCtas = 4, kBwdCtas = 5, k8Ctas = 8;
+__host__ __device__ constexpr int units_in_flight(bool any) { return any ? 1 : 2; }
 
 struct UnitMap {
     FastDiv per_row;
@@ -157,6 +161,7 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 {
+    constexpr int kUnits = units_in_flight(ANY);
     Top<T> top;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         Unit<T, ANY> g[kUnits], u[kUnits];
@@ -197,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 template <typename T, int ACT, bool GATED, bool FROM8, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
 {
+    constexpr int kUnits = units_in_flight(ANY);
     using Raw = std::conditional_t<FROM8, RawCodes, Unit<T, ANY>>;
     Top<T> top;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
@@ -251,6 +257,7 @@ template <typename T, bool ANY>
 __global__ void __launch_bounds__(kThreads) act8_save_kernel(const void* __restrict__ x, int64_t ldx, int64_t rows,
                                                              int64_t cols, Act8View out, UnitMap m)
 {
+    constexpr int kUnits = units_in_flight(ANY);
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         Unit<T, ANY> w[kUnits];
         Place p[kUnits];
@@ -273,6 +280,7 @@ template <typename T, bool ANY>
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(Act8View a, int64_t cols, void* __restrict__ out,
                                                                 int64_t ldo, UnitMap m)
 {
+    constexpr int kUnits = units_in_flight(ANY);
     Top<T> unused;
     for (uint32_t base = blockIdx.x * (kThreads * kUnits); base < m.total; base += gridDim.x * (kThreads * kUnits)) {
         RawCodes w[kUnits];
@@ -301,10 +309,10 @@ UnitMap unit_map(int64_t rows, int64_t cols)
     const int64_t per_row = act8_groups(cols) * 4;
     return {fast_div(static_cast<uint32_t>(per_row)), static_cast<uint32_t>(rows * per_row)};
 }
-unsigned unit_grid(const UnitMap& m, const Device& d)
+unsigned unit_grid(const UnitMap& m, bool any, int per_sm, const Device& d)
 {
-    const int64_t ctas = (m.total + int64_t{kThreads} * kUnits - 1) / (kThreads * kUnits);
-    return static_cast<unsigned>(std::min<int64_t>(ctas, d.sms * kCtasPerSm));
+    const int64_t per_cta = int64_t{kThreads} * units_in_flight(any);
+    return static_cast<unsigned>(std::min<int64_t>((m.total + per_cta - 1) / per_cta, d.sms * per_sm));
 }
 
 // Whether every row of a matrix starts on a 16-byte boundary.
@@ -348,13 +356,13 @@ int fwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
         if (aligned && a.gated)
-            rc = launch_kernel(act_fwd_kernel<T, ACT, true, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, true, false>, unit_grid(m, !aligned, kFwdCtas, d), 1, kThreads, 0, early, s, b, m);
         else if (aligned)
-            rc = launch_kernel(act_fwd_kernel<T, ACT, false, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, false, false>, unit_grid(m, !aligned, kFwdCtas, d), 1, kThreads, 0, early, s, b, m);
         else if (a.gated)
-            rc = launch_kernel(act_fwd_kernel<T, ACT, true, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, true, true>, unit_grid(m, !aligned, kFwdCtas, d), 1, kThreads, 0, early, s, b, m);
         else
-            rc = launch_kernel(act_fwd_kernel<T, ACT, false, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_fwd_kernel<T, ACT, false, true>, unit_grid(m, !aligned, kFwdCtas, d), 1, kThreads, 0, early, s, b, m);
         if (rc != MX_OK)
             return rc;
     }
@@ -383,13 +391,13 @@ int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
         if (aligned && a.gated)
-            rc = launch_kernel(act_bwd_kernel<T, ACT, true, FROM8, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, true, FROM8, false>, unit_grid(m, !aligned, kBwdCtas, d), 1, kThreads, 0, early, s, b, m);
         else if (aligned)
-            rc = launch_kernel(act_bwd_kernel<T, ACT, false, FROM8, false>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, false, FROM8, false>, unit_grid(m, !aligned, kBwdCtas, d), 1, kThreads, 0, early, s, b, m);
         else if (a.gated)
-            rc = launch_kernel(act_bwd_kernel<T, ACT, true, FROM8, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, true, FROM8, true>, unit_grid(m, !aligned, kBwdCtas, d), 1, kThreads, 0, early, s, b, m);
         else
-            rc = launch_kernel(act_bwd_kernel<T, ACT, false, FROM8, true>, unit_grid(m, d), 1, kThreads, 0, early, s, b, m);
+            rc = launch_kernel(act_bwd_kernel<T, ACT, false, FROM8, true>, unit_grid(m, !aligned, kBwdCtas, d), 1, kThreads, 0, early, s, b, m);
         if (rc != MX_OK)
             return rc;
     }
@@ -408,9 +416,9 @@ int save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols, Act8
         const UnitMap m = unit_map(n, cols);
         const void* from = ahead(x, r, ldx, dtype);
         if (aligned)
-            rc = launch_kernel(act8_save_kernel<T, false>, unit_grid(m, d), 1, kThreads, 0, false, s, from, ldx, n, cols, ahead(out, r, cols), m);
+            rc = launch_kernel(act8_save_kernel<T, false>, unit_grid(m, !aligned, k8Ctas, d), 1, kThreads, 0, false, s, from, ldx, n, cols, ahead(out, r, cols), m);
         else
-            rc = launch_kernel(act8_save_kernel<T, true>, unit_grid(m, d), 1, kThreads, 0, false, s, from, ldx, n, cols, ahead(out, r, cols), m);
+            rc = launch_kernel(act8_save_kernel<T, true>, unit_grid(m, !aligned, k8Ctas, d), 1, kThreads, 0, false, s, from, ldx, n, cols, ahead(out, r, cols), m);
         if (rc != MX_OK)
             return rc;
     }
@@ -428,9 +436,9 @@ int restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int 
         const UnitMap m = unit_map(n, cols);
         void* to = ahead(out, r, ldo, dtype);
         if (aligned)
-            rc = launch_kernel(act8_restore_kernel<T, false>, unit_grid(m, d), 1, kThreads, 0, false, s, ahead(a, r, cols), cols, to, ldo, m);
+            rc = launch_kernel(act8_restore_kernel<T, false>, unit_grid(m, !aligned, k8Ctas, d), 1, kThreads, 0, false, s, ahead(a, r, cols), cols, to, ldo, m);
         else
-            rc = launch_kernel(act8_restore_kernel<T, true>, unit_grid(m, d), 1, kThreads, 0, false, s, ahead(a, r, cols), cols, to, ldo, m);
+            rc = launch_kernel(act8_restore_kernel<T, true>, unit_grid(m, !aligned, k8Ctas, d), 1, kThreads, 0, false, s, ahead(a, r, cols), cols, to, ldo, m);
         if (rc != MX_OK)
             return rc;
     }

@@ -1,8 +1,8 @@
 // norm_cta.cu -- the norm's kernels for rows of 520 to 8192 columns on 16-byte
 // boundaries (a multiple of eight): the widths and layouts of model training.
 //
-// A CTA takes a row at a time (forward: two, where enough rows are there), two
-// octs (eight columns) a thread, with the weights, the biases and the backward
+// A CTA takes a row at a time (forward without a residual: two), two octs
+// (eight columns) a thread, with the weights, the biases and the backward
 // pass's column sums in registers over all of its rows.  One thread copies the
 // rows to come into a ring of shared-memory stages by bulk copies, an mbarrier
 // says when a stage is there, and the row sums' barrier that the stage before it
@@ -10,7 +10,7 @@
 //
 // What bounds them: with the ring the memory system is never idle, and what is
 // left is the number of instructions a row takes.  The options are therefore
-// compile-time, fp32 arithmetic is two-wide, and the forward kernel's two rows
+// compile-time and fp32 arithmetic is two-wide; two rows of the forward kernel
 // share one barrier and one exchange per sum.
 #include <algorithm>
 
@@ -503,12 +503,16 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     const int64_t row = a.cols * static_cast<int64_t>(sizeof(T)) * (ADD ? 2 : 1);
     using A = NormFwdArgs;
     constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, FULL>;
-    constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL>;
-    // Two rows at a time where every CTA still has several tiles and a ring of
-    // three stages fits; a row at a time spreads few rows over more SMs.
-    const int n2 = ctas_per_sm<A, two>(threads, 2 * row);
-    if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
-        return launch<A, two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
+    // Two rows at a time for the norm without a residual, whose few bytes a row
+    // leave it bound by instructions (32768x4096 bf16: 125 -> 90 us), where every
+    // CTA still has several tiles and a ring of three stages fits.  With the
+    // addition one row is faster (8192x4096: 42.6 us, 45.9 for two).
+    if constexpr (!ADD) {
+        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL>;
+        const int n2 = ctas_per_sm<A, two>(threads, 2 * row);
+        if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
+            return launch<A, two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
+    }
     const int n1 = ctas_per_sm<A, one>(threads, row);
     return launch<A, one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
 }
