@@ -1,6 +1,7 @@
 // mx_act8.cuh -- device pieces shared by the norm and activation kernels:
 // element access in bf16 / fp32, and the 8-bit checkpoint's group codec.
 #pragma once
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,6 +39,23 @@ int launch_kernel(void (*kernel)(P...), unsigned grid_x, unsigned grid_y, int th
     (void)cudaGetLastError();
     return MX_ERR_CUDA;
 }
+// Registers a thread of a kernel, and the CTAs of an SM that they allow.
+template <auto KERNEL>
+int registers_of()
+{
+    static const int n = [] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
+    }();
+    return n;
+}
+template <auto KERNEL>
+int resident_ctas(int threads)
+{
+    const int n = std::min(65536 / ((registers_of<KERNEL>() + 7) / 8 * 8 * threads), 2048 / threads);
+    return std::max(1, std::min(32, n));
+}
+
 // Sets the word that flush_top folds into to zero (none: nothing is launched).
 int launch_zero(unsigned* word, cudaStream_t s);
 

@@ -965,13 +965,10 @@ constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTA
 struct RingPlan {
     int per_sm, stages;
 };
-RingPlan ring_plan(int64_t stage_bytes, int threads, int registers, int most)
+RingPlan ring_plan(int64_t stage_bytes, int resident, int most)
 {
     RingPlan p;
-    p.per_sm = std::min(32, std::min(65536 / ((registers + 7) / 8 * 8 * threads), 2048 / threads));
-    p.per_sm = std::max(1, p.per_sm);
-    if (stage_bytes == 0)  // no ring
-        return {p.per_sm, 0};
+    p.per_sm = resident;
     while (p.per_sm > 1 && p.per_sm * 2 * stage_bytes > kRingBytes)
         --p.per_sm;
     p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, kRingBytes / (p.per_sm * stage_bytes))));
@@ -986,29 +983,11 @@ bool wide_cols(int64_t cols) { return cols <= kMaxWide; }
 
 // Launches a ring kernel: its grid fills the GPU, or covers the rows, and has
 // at most `most` CTAs.  `grid` returns it.
-template <void (*KERNEL)(NormFwdArgs, int)>
-int registers_of()
-{
-    static const int n = [] {
-        cudaFuncAttributes f = {};
-        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
-    }();
-    return n;
-}
-template <void (*KERNEL)(NormBwdArgs, int)>
-int registers_of()
-{
-    static const int n = [] {
-        cudaFuncAttributes f = {};
-        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
-    }();
-    return n;
-}
 template <auto KERNEL, typename A>
 int launch_ring(const A& a, const WideShape& w, int64_t stage_bytes, size_t least_smem, int64_t most, unsigned* grid,
                 const Device& d, cudaStream_t s)
 {
-    const RingPlan p = ring_plan(stage_bytes, w.threads, registers_of<KERNEL>(),
+    const RingPlan p = ring_plan(stage_bytes, resident_ctas<KERNEL>(w.threads),
                                  w.lpr ? 3 : kMaxStages);
     const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1, ctas = (a.rows + per_cta - 1) / per_cta;
     *grid = static_cast<unsigned>(std::min(most, std::min<int64_t>(ctas, int64_t{d.sms} * p.per_sm)));

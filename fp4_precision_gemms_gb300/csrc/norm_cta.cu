@@ -464,27 +464,18 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
             }
 }
 
-template <typename A, void (*KERNEL)(A, int)>
-int registers_of()
-{
-    static const int n = [] {
-        cudaFuncAttributes f = {};
-        return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 128;
-    }();
-    return n;
-}
 constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
 
 // CTAs an SM that registers allow, with at least two stages each where that can be.
-template <typename A, void (*KERNEL)(A, int)>
+template <auto KERNEL>
 int ctas_per_sm(int threads, int64_t stage_bytes)
 {
-    int n = std::max(1, std::min(16, 65536 / ((registers_of<A, KERNEL>() + 7) / 8 * 8 * threads)));
+    int n = resident_ctas<KERNEL>(threads);
     while (n > 1 && n * 2 * stage_bytes > kRingBytes)
         --n;
     return n;
 }
-template <typename A, void (*KERNEL)(A, int)>
+template <auto KERNEL, typename A>
 int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned grid, cudaStream_t s)
 {
     const int stages =
@@ -501,7 +492,6 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     const int threads = cta_threads(a.cols);
     const int64_t row = a.cols * static_cast<int64_t>(sizeof(T)) * (ADD ? 2 : 1);
-    using A = NormFwdArgs;
     constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, FULL>;
     // Two rows at a time for the norm without a residual, whose few bytes a row
     // leave it bound by instructions (32768x4096 bf16: 125 -> 90 us), where every
@@ -509,12 +499,12 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     // addition one row is faster (8192x4096: 42.6 us, 45.9 for two).
     if constexpr (!ADD) {
         constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL>;
-        const int n2 = ctas_per_sm<A, two>(threads, 2 * row);
+        const int n2 = ctas_per_sm<two>(threads, 2 * row);
         if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
-            return launch<A, two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
+            return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
     }
-    const int n1 = ctas_per_sm<A, one>(threads, row);
-    return launch<A, one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
+    const int n1 = ctas_per_sm<one>(threads, row);
+    return launch<one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
 }
 
 bool full_rows(int64_t cols) { return cols == 16 * cta_threads(cols); }
@@ -538,11 +528,10 @@ int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigne
     const int threads = cta_threads(a.cols);
     const int64_t row = a.cols * static_cast<int64_t>(sizeof(TY) + (FROM8 ? 0 : sizeof(T)) + (ADD ? sizeof(T) : 0)) +
                         (FROM8 ? act8_groups(a.cols) * kAct8Group : 0);
-    using A = NormBwdArgs;
     constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, FULL>;
-    const int n = ctas_per_sm<A, kernel>(threads, row);
+    const int n = ctas_per_sm<kernel>(threads, row);
     *grid = static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(a.rows, most), int64_t{n} * d.sms));
-    return launch<A, kernel>(a, threads, row, n, *grid, s);
+    return launch<kernel>(a, threads, row, n, *grid, s);
 }
 
 template <typename T, typename TY, bool FULL>
