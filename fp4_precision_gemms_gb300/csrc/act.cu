@@ -172,7 +172,8 @@ struct Unit {
                 shifted(a, b, more, s, lo, hi);
                 words_to_oct(lo, hi, o);
             }
-            keep_first(o, n);
+            if (n < 8)
+                keep_first(o, n);
         }
     }
 };

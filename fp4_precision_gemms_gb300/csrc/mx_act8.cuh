@@ -392,12 +392,36 @@ __device__ __forceinline__ void store_rest(T* p, const W (&own)[8], const W (&le
             if (i >= 8 - s)
                 to[i - 8] = left[i];
 }
+// A warp whose 32 octs are whole and follow one another: every lane but the
+// first writes its word, and eight lanes write the first lane's values before
+// its word and the last lane's after it.
+__device__ __forceinline__ bool whole_warp(int n, bool prev)
+{
+    return __all_sync(0xFFFFFFFFu, n == 8 && (prev || (threadIdx.x & 31) == 0));
+}
 __device__ __forceinline__ void store_ragged(__nv_bfloat16* p, Oct o, int n, bool prev, bool next, Top<__nv_bfloat16>& top)
 {
-    keep_first(o, n);
+    if (n < 8)
+        keep_first(o, n);
     const uint4 own = pack_oct(o), left = shfl_up1(own);
     const int s = misaligned(p, 2);
     top.word(own.x), top.word(own.y), top.word(own.z), top.word(own.w);
+    if (whole_warp(n, prev)) {
+        const int lane = threadIdx.x & 31;
+        if (s == 0) {
+            *reinterpret_cast<uint4*>(p) = own;
+            return;
+        }
+        if (lane > 0)
+            *reinterpret_cast<uint4*>(p - s) = shifted(left, own, 8 - s);
+        const int from = lane < 8 - s ? 0 : 31;  // lane i < 8: value i of lane 0, or of lane 31
+        const uint32_t a = __shfl_sync(0xFFFFFFFFu, own.x, from), b = __shfl_sync(0xFFFFFFFFu, own.y, from);
+        const uint32_t c = __shfl_sync(0xFFFFFFFFu, own.z, from), d = __shfl_sync(0xFFFFFFFFu, own.w, from);
+        const uint32_t w = lane & 4 ? (lane & 2 ? d : c) : (lane & 2 ? b : a);
+        if (lane < 8)
+            reinterpret_cast<uint16_t*>(p - 8 * lane)[8 * from + lane] = static_cast<uint16_t>(w >> ((lane & 1) * 16));
+        return;
+    }
     const bool whole = n == 8 && (prev || s == 0);
     if (whole)
         *reinterpret_cast<uint4*>(p - s) = s == 0 ? own : shifted(left, own, 8 - s);
@@ -414,7 +438,8 @@ __device__ __forceinline__ void store_ragged(__nv_bfloat16* p, Oct o, int n, boo
 }
 __device__ __forceinline__ void store_ragged(float* p, Oct o, int n, bool prev, bool next, Top<float>& top)
 {
-    keep_first(o, n);
+    if (n < 8)
+        keep_first(o, n);
     const uint4 a = make_uint4(__float_as_uint(o.p[0].x), __float_as_uint(o.p[0].y), __float_as_uint(o.p[1].x),
                                __float_as_uint(o.p[1].y));
     const uint4 b = make_uint4(__float_as_uint(o.p[2].x), __float_as_uint(o.p[2].y), __float_as_uint(o.p[3].x),
@@ -422,6 +447,26 @@ __device__ __forceinline__ void store_ragged(float* p, Oct o, int n, bool prev, 
     const uint4 left = shfl_up1(b);
     const int s = misaligned(p, 4);
     top.pair(o.p[0]), top.pair(o.p[1]), top.pair(o.p[2]), top.pair(o.p[3]);
+    if (whole_warp(n, prev)) {
+        const int lane = threadIdx.x & 31;
+        uint4 lo = a, hi = b;
+        if (s != 0)
+            shifted(left, a, b, 4 - s, lo, hi);
+        if (lane > 0 || s == 0)
+            reinterpret_cast<uint4*>(p - s)[0] = lo;
+        reinterpret_cast<uint4*>(p - s)[1] = hi;
+        if (s != 0) {  // lane i < 4: value i of lane 0, or value 4 + i of lane 31
+            const bool head = lane < 4 - s;
+            const uint32_t x = __shfl_sync(0xFFFFFFFFu, a.x, 0), y = __shfl_sync(0xFFFFFFFFu, a.y, 0);
+            const uint32_t z = __shfl_sync(0xFFFFFFFFu, a.z, 0);
+            const uint32_t u = __shfl_sync(0xFFFFFFFFu, b.y, 31), v = __shfl_sync(0xFFFFFFFFu, b.z, 31);
+            const uint32_t w = __shfl_sync(0xFFFFFFFFu, b.w, 31);
+            const uint32_t first = lane == 0 ? x : lane == 1 ? y : z, last = lane == 1 ? u : lane == 2 ? v : w;
+            if (lane < 4)
+                reinterpret_cast<uint32_t*>(p - 8 * lane)[head ? lane : 31 * 8 + 4 + lane] = head ? first : last;
+        }
+        return;
+    }
     const bool whole = n == 8 && (prev || s == 0);
     if (whole) {
         uint4 lo = a, hi = b;

@@ -355,6 +355,7 @@ struct RowRing {
     uint32_t phase = 0;
     int64_t rows, row = 0, edge = 1;
     bool direct = false;  // ANY: the current row is read from where it is
+    uint32_t here_shift[PARTS], shift_step[PARTS];  // ANY: bytes past a boundary, the current row's and a step's
 
     __device__ __forceinline__ uint32_t region(int m) const { return region_bytes(octs, part[m].oct, ANY); }
     __device__ __forceinline__ uint32_t shift(int m, int64_t r) const  // bytes past a boundary
@@ -456,6 +457,12 @@ struct RowRing {
     __device__ __forceinline__ void start(const RowMap<LPR>& map)
     {
         row = map.first;
+        if constexpr (ANY)
+#pragma unroll
+            for (int m = 0; m < PARTS; ++m) {
+                here_shift[m] = shift(m, row);
+                shift_step[m] = static_cast<uint32_t>(map.step * part[m].next_row) & 15u;
+            }
         if constexpr (LPR == 0) {
             if (threadIdx.x == 0) {
                 for (int i = 0; i < stages; ++i)
@@ -499,6 +506,10 @@ struct RowRing {
         if (LPR != 0 && ANY)
             __syncwarp();  // the stage's next words may come from another lane
         row += map.step;
+        if constexpr (ANY)
+#pragma unroll
+            for (int m = 0; m < PARTS; ++m)
+                here_shift[m] = (here_shift[m] + shift_step[m]) & 15u;
         at_stage += stage_bytes;
         if (++stage == stages) {
             stage = 0;
@@ -548,7 +559,7 @@ struct RowRing {
                     o[i] = i < n ? load_f(from + i) : 0.0f;
                 return;
             }
-            const int s = static_cast<int>(shift(m, row) / sizeof(T));
+            const int s = static_cast<int>(here_shift[m] / sizeof(T));
             if constexpr (sizeof(T) == 2) {
                 unpack_oct(shifted(lds128(word(m, j, 0)), lds128(word(m, j, 1)), s), o);
             } else {
@@ -556,7 +567,8 @@ struct RowRing {
                 shifted(lds128(word(m, j, 0)), lds128(word(m, j, 1)), lds128(word(m, j, 2)), s, lo, hi);
                 words_to_oct(lo, hi, o);
             }
-            keep_first(o, n);
+            if (n < 8)
+                keep_first(o, n);
         }
     }
     // A checkpoint's codes, as their own values (the pad columns' are zero).
@@ -669,7 +681,7 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     d.p[k] = __fadd2_rn(v[j].p[k], both(-mean));
-                if constexpr (ANY)
+                if (ANY && C - c0 - j * dc < 8)
                     keep_first(d, C - c0 - j * dc);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
