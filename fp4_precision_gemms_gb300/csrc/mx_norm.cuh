@@ -29,9 +29,10 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
 // each, whole checkpoint groups).
 constexpr int64_t kCtaMinCols = 513, kCtaMaxCols = 8192;
 inline int cta_threads(int64_t cols) { return static_cast<int>((act8_groups(cols) * 2 + 31) / 32 * 32); }
-int launch_norm_fwd_cta(const NormFwdArgs& a, const Device& d, cudaStream_t s);
+// aligned: rows on 16-byte boundaries of a multiple of eight columns.
+int launch_norm_fwd_cta(const NormFwdArgs& a, bool aligned, const Device& d, cudaStream_t s);
 // At most `most` CTAs; *grid returns their number, each of which leaves a row of
 // partial sums.
-int launch_norm_bwd_cta(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid);
+int launch_norm_bwd_cta(const NormBwdArgs& a, bool aligned, int most, const Device& d, cudaStream_t s, unsigned* grid);
 
 }  // namespace mx

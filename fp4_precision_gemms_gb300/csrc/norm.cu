@@ -1034,9 +1034,6 @@ int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
         return launch_ring<norm_fwd_kernel<T, TY, 32, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     if (w.lpr == 32)
         return launch_ring<norm_fwd_kernel<T, TY, 32, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
-    if constexpr (ANY)
-        if (w.nv == 2)
-            return launch_ring<norm_fwd_kernel<T, TY, 0, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     return launch_ring<norm_fwd_kernel<T, TY, 0, 4, ANY>>(a, w, bytes, 0, most, &grid, d, s);
 }
 
@@ -1082,10 +1079,6 @@ int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
         rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 0 && w.nv == 4)
         rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 4, ANY>>(a, w, bytes, least, most, &grid, d, s);
-    if constexpr (ANY) {
-        if (w.lpr == 0 && w.nv == 2)
-            rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
-    }
     return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
 }
 
@@ -1099,8 +1092,8 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
         const bool aligned = a.cols % 8 == 0 && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
                              wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) &&
                              wide_rows(a.weight, 8, wb) && wide_rows(a.bias, 8, wb);
-        if (aligned && a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols)
-            return launch_norm_fwd_cta(a, d, s);
+        if (a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols)
+            return launch_norm_fwd_cta(a, aligned, d, s);
         return aligned ? fwd_wide<T, TY, false>(a, d, s) : fwd_wide<T, TY, true>(a, d, s);
     }
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
@@ -1115,9 +1108,9 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
         const bool aligned = a.cols % 8 == 0 && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
                              wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) &&
                              wide_rows(a.weight, 8, wb);
-        if (aligned && a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols) {
+        if (a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols) {
             unsigned grid;
-            const int rc = launch_norm_bwd_cta(a, static_cast<int>(ctas_of(wide_shape(a.cols, false), a.rows)), d, s, &grid);
+            const int rc = launch_norm_bwd_cta(a, aligned, static_cast<int>(ctas_of(wide_shape(a.cols, false), a.rows)), d, s, &grid);
             return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
         }
         if (a.x8.codes)

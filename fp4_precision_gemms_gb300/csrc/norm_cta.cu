@@ -1,5 +1,5 @@
-// norm_cta.cu -- the norm's kernels for rows of 520 to 8192 columns on 16-byte
-// boundaries (a multiple of eight): the widths and layouts of model training.
+// norm_cta.cu -- the norm's kernels for rows of 513 to 8192 columns: the widths
+// of model training.
 //
 // A CTA takes a row at a time (forward without a residual: two), two octs
 // (eight columns) a thread, with the weights, the biases and the backward
@@ -27,18 +27,44 @@ constexpr int kMaxStages = 6;
 constexpr int kBarBytes = 64;
 constexpr int kWarps = kMaxThreads / 32;
 
-// The ring: PARTS matrices, R rows of each in a stage.
-template <int PARTS, int R>
+// The ring: PARTS matrices, R rows of each in a stage.  ANY: rows at any address,
+// one to a stage.  A stage then holds the aligned 16-byte words that a row lies
+// in, and an oct is shifted into place when it is read.  The words may hold a
+// neighbouring row's elements; the first and the last rows, whose words would
+// reach past the matrix, are not copied but read where they are.
+template <int PARTS, int R, bool ANY>
 struct Pipe {
+    static_assert(!ANY || R == 1, "rows at any address come one at a time");
     const char* src[PARTS];     // row 0
     int64_t next_row[PARTS];    // bytes
-    uint32_t row_bytes[PARTS];  // to copy
+    uint32_t row_bytes[PARTS];  // of a row, or of its words' room (ANY)
+    uint32_t length[PARTS];     // ANY: bytes of a row
     uint32_t at[PARTS];         // in a stage
-    uint32_t bars, base, stage_bytes, here;  // here: the current stage
-    int stages, stage = 0, skip;  // skip: test hook, a tile that is never copied
+    uint32_t shift[PARTS], shift_step[PARTS];  // ANY: the row's bytes past a boundary; what a step adds
+    uint32_t bars, base, stage_bytes, here;    // here: the current stage
+    int stages, stage = 0, skip;               // skip: test hook, a tile that is never copied
     uint32_t phase = 0;
+    int64_t edge = 1;     // ANY: rows at either end that are not copied
+    bool direct = false;  // ANY: this row is one of them
 
-    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int skip_)
+    // A matrix of rows of n bytes; words: they start on 16-byte boundaries.
+    __device__ __forceinline__ void matrix(int m, const void* p, int64_t row, uint32_t n, bool words)
+    {
+        src[m] = static_cast<const char*>(p);
+        next_row[m] = row;
+        length[m] = n;
+        row_bytes[m] = room(n, ANY && !words);
+        if (ANY && row < 16)
+            edge = 16;
+    }
+    __host__ __device__ static constexpr uint32_t room(uint32_t n, bool any) { return any ? (n + 15) / 16 * 16 + 32 : n; }
+    __device__ __forceinline__ uint32_t shift_of(int m, int64_t r) const
+    {
+        return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src[m]) + r * next_row[m]) & 15u;
+    }
+    __device__ __forceinline__ bool at_edge(int64_t r, int64_t rows) const { return ANY && (r < edge || r >= rows - edge); }
+
+    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int skip_, int64_t rows)
     {
         stages = stages_;
         skip = skip_;
@@ -49,8 +75,13 @@ struct Pipe {
         for (int m = 0; m < PARTS; ++m) {
             at[m] = n;
             n += R * row_bytes[m];
+            if constexpr (ANY) {
+                shift[m] = shift_of(m, blockIdx.x);
+                shift_step[m] = static_cast<uint32_t>(gridDim.x * next_row[m]) & 15u;
+            }
         }
         stage_bytes = n;
+        direct = at_edge(blockIdx.x, rows);
     }
     // Tile `it` (rows r, r + 1 ..) of the CTA into stage st (one thread).
     __device__ __forceinline__ void fill(int it, int64_t rows, int st)
@@ -58,17 +89,32 @@ struct Pipe {
         if (it == skip)
             return;
         const int64_t r = (blockIdx.x + static_cast<int64_t>(it) * gridDim.x) * R;
-        const int n = static_cast<int>(min(static_cast<int64_t>(R), rows - r));
-        uint32_t bytes = 0;
+        const uint32_t bar = bars + st * 8, to = base + st * stage_bytes;
+        if constexpr (ANY) {
+            if (at_edge(r, rows)) {
+                mbar_arrive(bar);
+                return;
+            }
+            uint32_t bytes = 0;
 #pragma unroll
-        for (int m = 0; m < PARTS; ++m)
-            bytes += n * row_bytes[m];
-        mbar_arrive_expect_tx(bars + st * 8, bytes);
+            for (int m = 0; m < PARTS; ++m)
+                bytes += (shift_of(m, r) + length[m] + 15) / 16 * 16;
+            mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-        for (int m = 0; m < PARTS; ++m)
-            for (int i = 0; i < n; ++i)
-                bulk_load(base + st * stage_bytes + at[m] + i * row_bytes[m], src[m] + (r + i) * next_row[m], row_bytes[m],
-                          bars + st * 8);
+            for (int m = 0; m < PARTS; ++m)
+                bulk_load(to + at[m], src[m] + r * next_row[m] - shift_of(m, r), (shift_of(m, r) + length[m] + 15) / 16 * 16, bar);
+        } else {
+            const int n = static_cast<int>(min(static_cast<int64_t>(R), rows - r));
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int m = 0; m < PARTS; ++m)
+                bytes += n * row_bytes[m];
+            mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+            for (int m = 0; m < PARTS; ++m)
+                for (int i = 0; i < n; ++i)
+                    bulk_load(to + at[m] + i * row_bytes[m], src[m] + (r + i) * next_row[m], row_bytes[m], bar);
+        }
     }
     // Barriers and the first tiles; ends with a CTA barrier.
     __device__ __forceinline__ void start(int64_t rows, int tiles)
@@ -90,8 +136,15 @@ struct Pipe {
             fill(it + stages, rows, st);
     }
     __device__ __forceinline__ int before() const { return stage == 0 ? stages - 1 : stage - 1; }
-    __device__ __forceinline__ void next()
+    // On to the tile that begins with row r.
+    __device__ __forceinline__ void next(int64_t r, int64_t rows)
     {
+        if constexpr (ANY) {
+#pragma unroll
+            for (int m = 0; m < PARTS; ++m)
+                shift[m] = (shift[m] + shift_step[m]) & 15u;
+            direct = at_edge(r, rows);
+        }
         here += stage_bytes;
         if (++stage == stages) {
             stage = 0;
@@ -108,20 +161,77 @@ struct Pipe {
         atomicExch(status, MX_ERR_TIMEOUT);
         for (; it < last; ++it) {
             wait(limit_ns);
-            next();
+            next(0, 0);
         }
+    }
+
+    // Oct j of row r (number q of its tile) of matrix m, whose first n values
+    // (n > 0) are inside the row.
+    template <typename T>
+    __device__ __forceinline__ void oct(int m, int q, int j, int64_t r, int n, Oct& o) const
+    {
+        const uint32_t from = here + at[m] + q * row_bytes[m] + (threadIdx.x + j * blockDim.x) * (8 * sizeof(T));
+        if constexpr (!ANY) {
+            if constexpr (sizeof(T) == 2)
+                unpack_oct(lds128(from), o);
+            else
+                words_to_oct(lds128(from), lds128(from + 16), o);
+        } else {
+            if (direct) {
+                const T* p = reinterpret_cast<const T*>(src[m] + r * next_row[m]) + (threadIdx.x + j * blockDim.x) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = i < n ? load_f(p + i) : 0.0f;
+                return;
+            }
+            const int s = static_cast<int>(shift[m] / sizeof(T));
+            if constexpr (sizeof(T) == 2) {
+                unpack_oct(shifted(lds128(from), lds128(from + 16), s), o);
+            } else {
+                uint4 lo, hi;
+                shifted(lds128(from), lds128(from + 16), lds128(from + 32), s, lo, hi);
+                words_to_oct(lo, hi, o);
+            }
+            if (n < 8)
+                keep_first(o, n);
+        }
+    }
+    // Oct j of a checkpoint's codes, as their own values.
+    __device__ __forceinline__ void codes(int m, int j, int64_t r, Oct& o) const
+    {
+        const uint32_t c = (threadIdx.x + j * blockDim.x) * 8;
+        uint2 w;
+        if (ANY && direct)
+            w = *reinterpret_cast<const uint2*>(src[m] + r * next_row[m] + c);
+        else
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(here + at[m] + c) : "memory");
+        decode_oct(w, o);
     }
 };
 
-// A thread's oct j of a row at `row` in shared memory.
-template <typename T>
-__device__ __forceinline__ void oct_from(uint32_t row, int j, Oct& o)
+// Writes n values of an oct (ANY: by whole warps).
+template <bool ANY, typename T>
+__device__ __forceinline__ void put(T* p, const Oct& o, int n, int c, int C, Top<T>& top)
 {
-    const uint32_t at = row + (threadIdx.x + j * blockDim.x) * (8 * sizeof(T));
-    if constexpr (sizeof(T) == 2)
-        unpack_oct(lds128(at), o);
-    else
-        words_to_oct(lds128(at), lds128(at + 16), o);
+    if constexpr (ANY) {
+        const int lane = threadIdx.x & 31;
+        store_ragged(p, o, n, lane > 0, lane < 31 && c + 8 < C, top);
+    } else if (n > 0) {
+        store_oct(p, o, top);
+    }
+}
+template <bool ANY>
+__device__ __forceinline__ void params(const void* p, int dtype, int c, int n, float absent, Oct& o)
+{
+    o.fill(0.0f);
+    if constexpr (ANY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                o[i] = param(p, dtype, c + i, absent);
+    } else if (n > 0) {
+        param_oct(p, dtype, c, absent, o);
+    }
 }
 
 // Two sums over the CTA, in a fixed order, known to every thread.  The halves of
@@ -153,7 +263,7 @@ __device__ __forceinline__ float2 cta_sum2(float x, float y, float2* part, bool&
 // ADD: the residual is added; SAVE: the checkpoint is kept; R rows at a time;
 // FULL: every thread's octs lie inside the row (cols a multiple of 512), which
 // saves a tenth of the instructions.
-template <typename T, typename TY, bool ADD, bool SAVE, int R, bool FULL>
+template <typename T, typename TY, bool ADD, bool SAVE, int R, bool FULL, bool ANY>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -162,33 +272,24 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
     const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
-    const bool own[2] = {FULL || c0 < C, FULL || c0 + dc < C};
+    const int own[2] = {FULL ? 8 : min(C - c0, 8), FULL ? 8 : min(C - c0 - dc, 8)};  // values of each oct, <= 0: none
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER;
     const int64_t tiles_of_all = (a.rows + R - 1) / R;
     const int tiles = static_cast<int>((tiles_of_all - blockIdx.x + gridDim.x - 1) / gridDim.x);
 
-    Pipe<ADD ? 2 : 1, R> pipe;
-    pipe.src[0] = static_cast<const char*>(a.x);
-    pipe.next_row[0] = a.ldx * static_cast<int64_t>(sizeof(T));
-    pipe.row_bytes[0] = C * sizeof(T);
-    if constexpr (ADD) {
-        pipe.src[1] = static_cast<const char*>(a.residual);
-        pipe.next_row[1] = a.ldr * static_cast<int64_t>(sizeof(T));
-        pipe.row_bytes[1] = C * sizeof(T);
-    }
-    pipe.layout(smem, stages, a.fail_at);
+    Pipe<ADD ? 2 : 1, R, ANY> pipe;
+    pipe.matrix(0, a.x, a.ldx * static_cast<int64_t>(sizeof(T)), C * sizeof(T), false);
+    if constexpr (ADD)
+        pipe.matrix(1, a.residual, a.ldr * static_cast<int64_t>(sizeof(T)), C * sizeof(T), false);
+    pipe.layout(smem, stages, a.fail_at, a.rows);
     pipe.start(a.rows, tiles);
 
     Oct wt[2], bi[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        wt[j].fill(0.0f);
-        bi[j].fill(0.0f);
-        if (own[j]) {
-            param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
-            param_oct(a.bias, a.w_dtype, c0 + j * dc, 0.0f, bi[j]);
-        }
+        params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, wt[j]);
+        params<ANY>(a.bias, a.w_dtype, c0 + j * dc, own[j], 0.0f, bi[j]);
     }
     int64_t r = static_cast<int64_t>(blockIdx.x) * R;
     const int64_t step = static_cast<int64_t>(gridDim.x) * R;
@@ -212,21 +313,22 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 v[q][j].fill(0.0f);
-                if (own[j]) {
-                    oct_from<T>(pipe.here + q * pipe.row_bytes[0], j, v[q][j]);
-                    if constexpr (ADD) {
-                        Oct o;
-                        oct_from<T>(pipe.here + pipe.at[1] + q * pipe.row_bytes[1], j, o);
+                if (own[j] > 0)
+                    pipe.template oct<T>(0, q, j, r + q, own[j], v[q][j]);
+                if constexpr (ADD) {
+                    Oct o;
+                    o.fill(0.0f);
+                    if (own[j] > 0)
+                        pipe.template oct<T>(1, q, j, r + q, own[j], o);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o.p[k] = __fadd2_rn(v[q][j].p[k], o.p[k]);
-                        if (q == 0 || two)
-                            store_oct(to_sum + q * a.lds + j * dc, o, unused);
-                        if constexpr (sizeof(T) == 2)
-                            unpack_oct(pack_oct(o), v[q][j]);  // as it was stored
-                        else
-                            v[q][j] = o;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        o.p[k] = __fadd2_rn(v[q][j].p[k], o.p[k]);
+                    if (q == 0 || two)
+                        put<ANY>(to_sum + q * a.lds + j * dc, o, own[j], c0 + j * dc, C, unused);
+                    if constexpr (sizeof(T) == 2)
+                        unpack_oct(pack_oct(o), v[q][j]);  // as it was stored
+                    else
+                        v[q][j] = o;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -263,12 +365,16 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
             float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (own[j])
+                if (own[j] > 0) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 4; ++k)
                         v[q][j].p[k] = __fadd2_rn(v[q][j].p[k], m);
+                    if (ANY && own[j] < 8)
+                        keep_first(v[q][j], own[j]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
                         s2 = __ffma2_rn(v[q][j].p[k], v[q][j].p[k], s2);
-                    }
+                }
             sq[q] = s2.x + s2.y;
         }
         // RMS norm has one barrier per tile: its words alternate
@@ -289,14 +395,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
             if (q == 0 || two) {
                 const float2 s = both(q == 0 ? rstd.x : rstd.y);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (own[j]) {
-                        Oct y;
+                for (int j = 0; j < 2; ++j) {
+                    Oct y;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y.p[k] = __ffma2_rn(__fmul2_rn(v[q][j].p[k], s), wt[j].p[k], bi[j].p[k]);
-                        store_oct(to_y + q * a.ldy + j * dc, y, top);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        y.p[k] = __ffma2_rn(__fmul2_rn(v[q][j].p[k], s), wt[j].p[k], bi[j].p[k]);
+                    put<ANY>(to_y + q * a.ldy + j * dc, y, own[j], c0 + j * dc, C, top);
+                }
             }
         r += step;
         to_y += y_step;
@@ -304,7 +409,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
             to_sum += sum_step;
         if constexpr (SAVE)
             to_codes += codes_step;
-        pipe.next();
+        pipe.next(r, a.rows);
     }
     if (bad) {
         pipe.abandon(it, min(tiles, it + stages), a.wait_ns, a.status);
@@ -316,7 +421,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
 
 // dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
 // is the checkpoint.  ADD: the residual path's gradient joins dx.
-template <typename T, typename TY, bool FROM8, bool ADD, bool FULL>
+template <typename T, typename TY, bool FROM8, bool ADD, bool FULL, bool ANY>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -326,34 +431,28 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
     const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
-    const bool own[2] = {FULL || c0 < C, FULL || c0 + dc < C};
+    const int own[2] = {FULL ? 8 : min(C - c0, 8), FULL ? 8 : min(C - c0 - dc, 8)};  // values of each oct, <= 0: none
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER;
     const int tiles = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
 
-    Pipe<ADD ? 3 : 2, 1> pipe;
-    pipe.src[0] = static_cast<const char*>(a.dy);
-    pipe.next_row[0] = a.ldy * static_cast<int64_t>(sizeof(TY));
-    pipe.row_bytes[0] = C * sizeof(TY);
-    pipe.src[1] = FROM8 ? reinterpret_cast<const char*>(a.x8.codes) : static_cast<const char*>(a.x);
-    pipe.next_row[1] = FROM8 ? G * int64_t{kAct8Group} : a.ldx * static_cast<int64_t>(sizeof(T));
-    pipe.row_bytes[1] = FROM8 ? G * kAct8Group : C * sizeof(T);
-    if constexpr (ADD) {
-        pipe.src[2] = static_cast<const char*>(a.dres);
-        pipe.next_row[2] = a.ldres * static_cast<int64_t>(sizeof(T));
-        pipe.row_bytes[2] = C * sizeof(T);
-    }
-    pipe.layout(smem, stages, a.fail_at);
+    Pipe<ADD ? 3 : 2, 1, ANY> pipe;
+    pipe.matrix(0, a.dy, a.ldy * static_cast<int64_t>(sizeof(TY)), C * sizeof(TY), false);
+    if constexpr (FROM8)
+        pipe.matrix(1, a.x8.codes, G * int64_t{kAct8Group}, G * kAct8Group, true);
+    else
+        pipe.matrix(1, a.x, a.ldx * static_cast<int64_t>(sizeof(T)), C * sizeof(T), false);
+    if constexpr (ADD)
+        pipe.matrix(2, a.dres, a.ldres * static_cast<int64_t>(sizeof(T)), C * sizeof(T), false);
+    pipe.layout(smem, stages, a.fail_at, a.rows);
     pipe.start(a.rows, tiles);
 
     Oct wt[2], dw[2], db[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        wt[j].fill(0.0f);
+        params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, wt[j]);
         dw[j].fill(0.0f);
         db[j].fill(0.0f);
-        if (own[j])
-            param_oct(a.weight, a.w_dtype, c0 + j * dc, 1.0f, wt[j]);
     }
     int64_t r = blockIdx.x;
     const int64_t step = gridDim.x;
@@ -376,6 +475,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
     for (; it < tiles; ++it) {
         const float2 m = both(-mean), s = both(rstd);
         const float2 scale[2] = {both(act8_scale(e0)), both(act8_scale(e1))};
+        const int64_t row = r;
         r += step;
         if (it + 1 < tiles) {
             rstd = a.rstd[r];
@@ -391,19 +491,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            if (own[j]) {
+            if (own[j] > 0) {
                 Oct dy;
-                oct_from<TY>(pipe.here, j, dy);
-                if constexpr (FROM8) {
-                    uint2 w;
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                 : "=r"(w.x), "=r"(w.y)
-                                 : "r"(pipe.here + pipe.at[1] + c0 + j * dc)
-                                 : "memory");
-                    decode_oct(w, h[j]);
-                } else {
-                    oct_from<T>(pipe.here + pipe.at[1], j, h[j]);
-                }
+                pipe.template oct<TY>(0, 0, j, row, own[j], dy);
+                if constexpr (FROM8)
+                    pipe.codes(1, j, row, h[j]);
+                else
+                    pipe.template oct<T>(1, 0, j, row, own[j], h[j]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     // the code's product with its scale is exact
@@ -424,23 +518,22 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         const float2 c1 = both(-sums.x * inv_c), c2 = both(layer ? -sums.y * inv_c : 0.0f);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            if (own[j]) {
+            if (ANY || own[j] > 0) {
                 Oct q;
-                if constexpr (ADD)
-                    oct_from<T>(pipe.here + pipe.at[2], j, q);
-                else
-                    q.fill(0.0f);
+                q.fill(0.0f);
+                if (ADD && own[j] > 0)
+                    pipe.template oct<T>(2, 0, j, row, own[j], q);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h[j].p[k], c1, g[j].p[k]), c2), s, q.p[k]);
-                store_oct(to_dx + j * dc, q, top);
+                put<ANY>(to_dx + j * dc, q, own[j], c0 + j * dc, C, top);
             }
         to_dx += dx_step;
         if (stages == 1) {
             __syncthreads();
             pipe.refill(it, a.rows, tiles, 0);
         }
-        pipe.next();
+        pipe.next(r, a.rows);
     }
     if (bad) {
         pipe.abandon(it, min(tiles, stages > 1 ? max(it - 1, 0) + stages : it + 1), a.wait_ns, a.status);
@@ -453,15 +546,25 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
     float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C + c0;
     const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (own[j])
+    for (int j = 0; j < 2; ++j) {
+        float* const to = out + j * dc;
+        if constexpr (ANY) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < own[j]) {
+                    to[i] = dw[j][i];
+                    to[to_db + i] = db[j][i];
+                }
+        } else if (own[j] > 0) {
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
-                float* const to = out + j * dc + 2 * k;
-                *reinterpret_cast<float4*>(to) = make_float4(dw[j].p[k].x, dw[j].p[k].y, dw[j].p[k + 1].x, dw[j].p[k + 1].y);
-                *reinterpret_cast<float4*>(to + to_db) =
+                *reinterpret_cast<float4*>(to + 2 * k) =
+                    make_float4(dw[j].p[k].x, dw[j].p[k].y, dw[j].p[k + 1].x, dw[j].p[k + 1].y);
+                *reinterpret_cast<float4*>(to + to_db + 2 * k) =
                     make_float4(db[j].p[k].x, db[j].p[k].y, db[j].p[k + 1].x, db[j].p[k + 1].y);
             }
+        }
+    }
 }
 
 constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
@@ -487,84 +590,95 @@ int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned gr
     return launch_kernel(KERNEL, grid, 1, threads, smem, a.amax != nullptr, s, a, stages);
 }
 
-template <typename T, typename TY, bool ADD, bool SAVE, bool FULL>
+// How the rows of a call lie: every thread's octs inside the row, some past it,
+// or rows at any address.
+enum Rows { kFull, kPart, kAny };
+
+template <typename T, typename TY, bool ADD, bool SAVE, Rows ROWS>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
+    constexpr bool FULL = ROWS == kFull, ANY = ROWS == kAny;
     const int threads = cta_threads(a.cols);
-    const int64_t row = a.cols * static_cast<int64_t>(sizeof(T)) * (ADD ? 2 : 1);
-    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, FULL>;
+    const int64_t row = int64_t{Pipe<1, 1, ANY>::room(static_cast<uint32_t>(a.cols * sizeof(T)), ANY)} * (ADD ? 2 : 1);
     // Two rows at a time for the norm without a residual, whose few bytes a row
     // leave it bound by instructions (32768x4096 bf16: 125 -> 90 us), where every
     // CTA still has several tiles and a ring of three stages fits.  With the
     // addition one row is faster (8192x4096: 42.6 us, 45.9 for two).
-    if constexpr (!ADD) {
-        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL>;
+    if constexpr (!ADD && !ANY) {
+        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL, false>;
         const int n2 = ctas_per_sm<two>(threads, 2 * row);
         if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
             return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
     }
+    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, FULL, ANY>;
     const int n1 = ctas_per_sm<one>(threads, row);
     return launch<one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
+}
+template <typename T, typename TY, Rows ROWS>
+int fwd_options(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+{
+    if (a.residual)
+        return a.save.codes ? fwd<T, TY, true, true, ROWS>(a, d, s) : fwd<T, TY, true, false, ROWS>(a, d, s);
+    return a.save.codes ? fwd<T, TY, false, true, ROWS>(a, d, s) : fwd<T, TY, false, false, ROWS>(a, d, s);
 }
 
 bool full_rows(int64_t cols) { return cols == 16 * cta_threads(cols); }
 
-template <typename T, typename TY, bool FULL>
-int fwd_options(const NormFwdArgs& a, const Device& d, cudaStream_t s)
-{
-    if (a.residual)
-        return a.save.codes ? fwd<T, TY, true, true, FULL>(a, d, s) : fwd<T, TY, true, false, FULL>(a, d, s);
-    return a.save.codes ? fwd<T, TY, false, true, FULL>(a, d, s) : fwd<T, TY, false, false, FULL>(a, d, s);
-}
 template <typename T, typename TY>
-int fwd_any(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+int fwd_rows(const NormFwdArgs& a, bool aligned, const Device& d, cudaStream_t s)
 {
-    return full_rows(a.cols) ? fwd_options<T, TY, true>(a, d, s) : fwd_options<T, TY, false>(a, d, s);
+    if (!aligned)
+        return fwd_options<T, TY, kAny>(a, d, s);
+    return full_rows(a.cols) ? fwd_options<T, TY, kFull>(a, d, s) : fwd_options<T, TY, kPart>(a, d, s);
 }
 
-template <typename T, typename TY, bool FROM8, bool ADD, bool FULL>
+template <typename T, typename TY, bool FROM8, bool ADD, Rows ROWS>
 int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
+    constexpr bool ANY = ROWS == kAny;
     const int threads = cta_threads(a.cols);
-    const int64_t row = a.cols * static_cast<int64_t>(sizeof(TY) + (FROM8 ? 0 : sizeof(T)) + (ADD ? sizeof(T) : 0)) +
-                        (FROM8 ? act8_groups(a.cols) * kAct8Group : 0);
-    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, FULL>;
+    auto room = [&](size_t bytes) { return int64_t{Pipe<2, 1, ANY>::room(static_cast<uint32_t>(a.cols * bytes), ANY)}; };
+    const int64_t row =
+        room(sizeof(TY)) + (FROM8 ? act8_groups(a.cols) * kAct8Group : room(sizeof(T))) + (ADD ? room(sizeof(T)) : 0);
+    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, ROWS == kFull, ANY>;
     const int n = ctas_per_sm<kernel>(threads, row);
     *grid = static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(a.rows, most), int64_t{n} * d.sms));
     return launch<kernel>(a, threads, row, n, *grid, s);
 }
-
-template <typename T, typename TY, bool FULL>
+template <typename T, typename TY, Rows ROWS>
 int bwd_options(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     if (a.x8.codes)
-        return a.dres ? bwd<T, TY, true, true, FULL>(a, most, d, s, grid) : bwd<T, TY, true, false, FULL>(a, most, d, s, grid);
-    return a.dres ? bwd<T, TY, false, true, FULL>(a, most, d, s, grid) : bwd<T, TY, false, false, FULL>(a, most, d, s, grid);
+        return a.dres ? bwd<T, TY, true, true, ROWS>(a, most, d, s, grid) : bwd<T, TY, true, false, ROWS>(a, most, d, s, grid);
+    return a.dres ? bwd<T, TY, false, true, ROWS>(a, most, d, s, grid) : bwd<T, TY, false, false, ROWS>(a, most, d, s, grid);
 }
-
 template <typename T, typename TY>
-int bwd_any(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
+int bwd_rows(const NormBwdArgs& a, bool aligned, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
-    return full_rows(a.cols) ? bwd_options<T, TY, true>(a, most, d, s, grid) : bwd_options<T, TY, false>(a, most, d, s, grid);
+    if (!aligned)
+        return bwd_options<T, TY, kAny>(a, most, d, s, grid);
+    return full_rows(a.cols) ? bwd_options<T, TY, kFull>(a, most, d, s, grid)
+                             : bwd_options<T, TY, kPart>(a, most, d, s, grid);
 }
 
 }  // namespace
 
-int launch_norm_fwd_cta(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+int launch_norm_fwd_cta(const NormFwdArgs& a, bool aligned, const Device& d, cudaStream_t s)
 {
     using bf = __nv_bfloat16;
     if (a.x_dtype == MX_OUT_BF16)
-        return a.y_dtype == MX_OUT_BF16 ? fwd_any<bf, bf>(a, d, s) : fwd_any<bf, float>(a, d, s);
-    return a.y_dtype == MX_OUT_BF16 ? fwd_any<float, bf>(a, d, s) : fwd_any<float, float>(a, d, s);
+        return a.y_dtype == MX_OUT_BF16 ? fwd_rows<bf, bf>(a, aligned, d, s) : fwd_rows<bf, float>(a, aligned, d, s);
+    return a.y_dtype == MX_OUT_BF16 ? fwd_rows<float, bf>(a, aligned, d, s) : fwd_rows<float, float>(a, aligned, d, s);
 }
 
-int launch_norm_bwd_cta(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
+int launch_norm_bwd_cta(const NormBwdArgs& a, bool aligned, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     using bf = __nv_bfloat16;
     if (a.dx_dtype == MX_OUT_BF16)
-        return a.dy_dtype == MX_OUT_BF16 ? bwd_any<bf, bf>(a, most, d, s, grid) : bwd_any<bf, float>(a, most, d, s, grid);
-    return a.dy_dtype == MX_OUT_BF16 ? bwd_any<float, bf>(a, most, d, s, grid)
-                                     : bwd_any<float, float>(a, most, d, s, grid);
+        return a.dy_dtype == MX_OUT_BF16 ? bwd_rows<bf, bf>(a, aligned, most, d, s, grid)
+                                         : bwd_rows<bf, float>(a, aligned, most, d, s, grid);
+    return a.dy_dtype == MX_OUT_BF16 ? bwd_rows<float, bf>(a, aligned, most, d, s, grid)
+                                     : bwd_rows<float, float>(a, aligned, most, d, s, grid);
 }
 
 }  // namespace mx
