@@ -465,6 +465,10 @@ def linear_bwd_saved(dY: torch.Tensor, saved: torch.Tensor, Kin: int, fmt: str,
 
 
 # ---------------------------------------------------------------- norm, activation, 8-bit checkpoints
+_device_index = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (device index) -> cudaStream_t of its current stream
+_U8, _F32 = torch.uint8, torch.float32
+
 NORMS = {"layer": 0, "rms": 1}
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
@@ -522,13 +526,19 @@ class ActOut(NamedTuple):
 
 
 def _first(t, what):
-    """Shape and device of the matrix that a call goes by."""
+    """(pointer, row stride, rows, columns, device, type) of the matrix that a call goes by."""
     if not t.is_cuda:
         _on_gpu(t)
     if t.dim() != 2:
         raise MXError(MX_ERR_INVALID_ARG, f"{what} must be a matrix, not of shape {tuple(t.shape)}")
+    dt = t.dtype
+    if dt not in OUT:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} has type {dt}, expected bfloat16 or float32")
     rows, cols = t.shape
-    return rows, cols, t.device
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must have unit column stride")
+    return t.data_ptr(), ld if rows > 1 else cols, rows, cols, t.device, dt
 
 
 def _mat(t, rows, cols, dev, what, dtype=None):
@@ -544,6 +554,16 @@ def _mat(t, rows, cols, dev, what, dtype=None):
     if unit != 1 and cols > 1:
         raise MXError(MX_ERR_INVALID_ARG, f"{what} must have unit column stride")
     return t.data_ptr(), ld if rows > 1 else cols
+
+
+def _save_to(out, rows, cols, dev):
+    """(checkpoint, its C form): a new one, or the one given after checking it."""
+    if isinstance(out, Act8):
+        return out, out._c(dev, rows, cols)
+    G = (cols + 31) >> 5
+    codes = torch.empty((rows, 32 * G), dtype=_U8, device=dev)
+    sf = torch.empty((rows, G), dtype=_U8, device=dev)
+    return Act8(codes, sf, cols), _CAct8(codes.data_ptr(), sf.data_ptr(), rows, cols)
 
 
 def _vec(t, n, dev, what, dtype=torch.float32):
@@ -569,11 +589,11 @@ def _params(weight, bias, cols, dev):
 def _run(dev, what, fn, *args):
     """One call of the library on the tensors' device and its current stream."""
     index = dev.index
-    if index != torch._C._cuda_getDevice():
+    if index != _device_index():
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            rc = fn(*args, _raw_stream(index))
     else:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        rc = fn(*args, _raw_stream(index))
     if rc != MX_OK:
         raise MXError(rc, what)
 
@@ -589,10 +609,9 @@ def act8_save(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8:
     if stream is not None:  # also what is allocated here then belongs to that stream
         with torch.cuda.stream(stream):
             return act8_save(x, out)
-    rows, cols, dev = _first(x, "x")
-    px, ldx = _mat(x, rows, cols, dev, "x")
-    out = out if out is not None else Act8.empty(rows, cols, dev)
-    _run(dev, "mx_act8_save", lib().mx_act8_save, px, ldx, OUT[x.dtype], out._c(dev, rows, cols))
+    px, ldx, rows, cols, dev, dt = _first(x, "x")
+    out, c = _save_to(out, rows, cols, dev)
+    _run(dev, "mx_act8_save", lib().mx_act8_save, px, ldx, OUT[dt], c)
     return out
 
 
@@ -601,12 +620,18 @@ def act8_restore(a: Act8, out_dtype=torch.bfloat16, out: torch.Tensor | None = N
     if stream is not None:
         with torch.cuda.stream(stream):
             return act8_restore(a, out_dtype, out)
-    _on_gpu(a.codes)
-    rows, cols, dev = a.rows, a.cols, a.codes.device
+    if not a.codes.is_cuda:
+        _on_gpu(a.codes)
+    rows, cols, dev = a.codes.shape[0], a.cols, a.codes.device
+    c = a._c(dev)
     if out is None:
+        number = _look_up(OUT, out_dtype, "out_dtype")
         out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-    po, ldo = _mat(out, rows, cols, dev, "out")
-    _run(dev, "mx_act8_restore", lib().mx_act8_restore, a._c(dev), po, ldo, OUT[out.dtype])
+        po, ldo = out.data_ptr(), cols
+    else:
+        po, ldo = _mat(out, rows, cols, dev, "out")
+        number = OUT[out.dtype]
+    _run(dev, "mx_act8_restore", lib().mx_act8_restore, c, po, ldo, number)
     return out
 
 
@@ -623,33 +648,44 @@ def norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Te
         with torch.cuda.stream(stream):
             return norm_fwd(x, weight, bias, kind, eps, residual, sum_out, save, amax_out, out_dtype, out, need_stats,
                             mean, rstd)
-    rows, cols, dev = _first(x, "x")
-    px, ldx = _mat(x, rows, cols, dev, "x")
-    dt = x.dtype
-    pr = ps = None
+    px, ldx, rows, cols, dev, dt = _first(x, "x")
+    k = _look_up(NORMS, kind, "kind")
+    pr = ps = pm = pt = saved = csaved = None
     ldr = lds = 0
     if residual is not None:
         pr, ldr = _mat(residual, rows, cols, dev, "residual", dt)
-        sum_out = sum_out if sum_out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
-        ps, lds = _mat(sum_out, rows, cols, dev, "sum_out", dt)
+        if sum_out is None:
+            sum_out = torch.empty((rows, cols), dtype=dt, device=dev)
+            ps, lds = sum_out.data_ptr(), cols
+        else:
+            ps, lds = _mat(sum_out, rows, cols, dev, "sum_out", dt)
     elif sum_out is not None:
         raise MXError(MX_ERR_INVALID_ARG, "sum_out goes with residual")
     pw, pb, wt = _params(weight, bias, cols, dev)
-    y = out if out is not None else torch.empty((rows, cols), dtype=out_dtype or dt, device=dev)
-    py, ldy = _mat(y, rows, cols, dev, "out")
-    k = _look_up(NORMS, kind, "kind")
+    if out is None:
+        ydt = out_dtype or dt
+        yt = _look_up(OUT, ydt, "out_dtype")
+        out = torch.empty((rows, cols), dtype=ydt, device=dev)
+        py, ldy = out.data_ptr(), cols
+    else:
+        py, ldy = _mat(out, rows, cols, dev, "out")
+        yt = OUT[out.dtype]
     if need_stats:
         if rstd is None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+            rstd = torch.empty(rows, dtype=_F32, device=dev)
         if mean is None and k == 0:
-            mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    saved = None
+            mean = torch.empty(rows, dtype=_F32, device=dev)
+    if rstd is not None:
+        pt = _vec(rstd, rows, dev, "rstd")
+    if k != 0:
+        mean = None
+    elif mean is not None:
+        pm = _vec(mean, rows, dev, "mean")
     if save is not False and save is not None:
-        saved = save if isinstance(save, Act8) else Act8.empty(rows, cols, dev)
+        saved, csaved = _save_to(save, rows, cols, dev)
     _run(dev, "mx_norm_fwd", lib().mx_norm_fwd, px, ldx, pr, ldr, OUT[dt], rows, cols, k, pw, pb, wt, eps, ps, lds,
-         py, ldy, OUT[y.dtype], _vec(mean, rows, dev, "mean") if k == 0 else None, _vec(rstd, rows, dev, "rstd"),
-         saved._c(dev, rows, cols) if saved is not None else None, _vec(amax_out, 1, dev, "amax_out"))
-    return NormOut(y, sum_out if residual is not None else x, mean if k == 0 else None, rstd, saved)
+         py, ldy, yt, pm, pt, csaved, _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None)
+    return NormOut(out, sum_out if residual is not None else x, mean, rstd, saved)
 
 
 def norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -669,43 +705,54 @@ def norm_bwd(dy: torch.Tensor, x: torch.Tensor | Act8, rstd: torch.Tensor, mean:
         with torch.cuda.stream(stream):
             return norm_bwd(dy, x, rstd, mean, weight, kind, dres, need_dw, need_db, dx_dtype, dx, dw, db, amax_out,
                             workspace)
-    rows, cols, dev = _first(dy, "dy")
-    pdy, lddy = _mat(dy, rows, cols, dev, "dy")
+    pdy, lddy, rows, cols, dev, ydt = _first(dy, "dy")
     k = _look_up(NORMS, kind, "kind")
+    px = x8 = pres = pm = pdw = pdb = pws = None
+    ldx = ldres = n = 0
     if isinstance(x, Act8):
-        px, ldx, x8 = None, 0, x._c(dev, rows, cols)
-        dt = dx.dtype if dx is not None else dx_dtype or (dres.dtype if dres is not None else dy.dtype)
+        x8 = x._c(dev, rows, cols)
+        dt = dx.dtype if dx is not None else dx_dtype or (dres.dtype if dres is not None else ydt)
     else:
-        dt, x8 = x.dtype, None
+        dt = x.dtype
         px, ldx = _mat(x, rows, cols, dev, "x")
         if dx_dtype is not None and dx_dtype is not dt:
             raise MXError(MX_ERR_UNSUPPORTED, "dx has the type of x")
+    number = _look_up(OUT, dt, "dx's type")
     if dx is None:
         dx = torch.empty((rows, cols), dtype=dt, device=dev)
-    pdx, lddx = _mat(dx, rows, cols, dev, "dx", dt)
-    pres, ldres = _mat(dres, rows, cols, dev, "dres", dt) if dres is not None else (None, 0)
+        pdx, lddx = dx.data_ptr(), cols
+    else:
+        pdx, lddx = _mat(dx, rows, cols, dev, "dx", dt)
+    if dres is not None:
+        pres, ldres = _mat(dres, rows, cols, dev, "dres", dt)
     if rstd is None or (k == 0 and mean is None):
         raise MXError(MX_ERR_INVALID_ARG, "norm_bwd needs the forward's rstd, and its mean for a layer norm")
+    if k == 0:
+        pm = _vec(mean, rows, dev, "mean")
     pw, _, wt = _params(weight, None, cols, dev)
     if need_db is None:
         need_db = k == 0
     L = lib()
-    n = 0
     if need_dw or need_db:
-        if need_dw and dw is None:
-            dw = torch.empty(cols, dtype=torch.float32, device=dev)
-        if need_db and db is None:
-            db = torch.empty(cols, dtype=torch.float32, device=dev)
+        if need_dw:
+            if dw is None:
+                dw = torch.empty(cols, dtype=_F32, device=dev)
+            pdw = _vec(dw, cols, dev, "dw")
+        if need_db:
+            if db is None:
+                db = torch.empty(cols, dtype=_F32, device=dev)
+            pdb = _vec(db, cols, dev, "db")
         if workspace is None:
-            workspace = torch.empty(L.mx_norm_bwd_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+            n = L.mx_norm_bwd_workspace_bytes(rows, cols)
+            workspace = torch.empty(n, dtype=_U8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise MXError(MX_ERR_INVALID_ARG, f"workspace must be contiguous memory on {dev}")
-        n = workspace.numel() * workspace.element_size()
-    _run(dev, "mx_norm_bwd", L.mx_norm_bwd, pdy, lddy, OUT[dy.dtype], px, ldx, x8,
-         _vec(mean, rows, dev, "mean") if k == 0 else None, _vec(rstd, rows, dev, "rstd"), pw, wt, rows, cols, k, pres,
-         ldres, pdx, lddx, OUT[dt], _vec(dw, cols, dev, "dw") if need_dw else None,
-         _vec(db, cols, dev, "db") if need_db else None, _vec(amax_out, 1, dev, "amax_out"),
-         workspace.data_ptr() if n else None, n)
+        else:
+            n = workspace.numel() * workspace.element_size()
+        pws = workspace.data_ptr() if n else None
+    _run(dev, "mx_norm_bwd", L.mx_norm_bwd, pdy, lddy, OUT[ydt], px, ldx, x8, pm, _vec(rstd, rows, dev, "rstd"), pw, wt,
+         rows, cols, k, pres, ldres, pdx, lddx, number, pdw, pdb,
+         _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None, pws, n)
     return dx, dw if need_dw else None, db if need_db else None
 
 
@@ -719,20 +766,23 @@ def act_fwd(gate: torch.Tensor, up: torch.Tensor | None = None, act: str = "silu
     if stream is not None:
         with torch.cuda.stream(stream):
             return act_fwd(gate, up, act, save, gate8, up8, amax_out, out)
-    rows, cols, dev = _first(gate, "gate")
-    pg, ldg = _mat(gate, rows, cols, dev, "gate")
-    dt = gate.dtype
-    pu, ldu = _mat(up, rows, cols, dev, "up", dt) if up is not None else (None, 0)
-    h = out if out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
-    ph, ldh = _mat(h, rows, cols, dev, "out", dt)
-    if save:
-        gate8 = gate8 if gate8 is not None else Act8.empty(rows, cols, dev)
-        if up is not None and up8 is None:
-            up8 = Act8.empty(rows, cols, dev)
+    pg, ldg, rows, cols, dev, dt = _first(gate, "gate")
+    pu = c8 = cu8 = None
+    ldu = 0
+    if up is not None:
+        pu, ldu = _mat(up, rows, cols, dev, "up", dt)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dt, device=dev)
+        ph, ldh = out.data_ptr(), cols
+    else:
+        ph, ldh = _mat(out, rows, cols, dev, "out", dt)
+    if save or gate8 is not None:
+        gate8, c8 = _save_to(gate8, rows, cols, dev)
+    if up8 is not None or (save and up is not None):
+        up8, cu8 = _save_to(up8, rows, cols, dev)
     _run(dev, "mx_act_fwd", lib().mx_act_fwd, pg, ldg, pu, ldu, rows, cols, _look_up(ACTS, act, "act"), OUT[dt], ph, ldh,
-         gate8._c(dev, rows, cols) if gate8 is not None else None,
-         up8._c(dev, rows, cols) if up8 is not None else None, _vec(amax_out, 1, dev, "amax_out"))
-    return ActOut(h, gate8, up8)
+         c8, cu8, _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None)
+    return ActOut(out, gate8, up8)
 
 
 def act_bwd(dh: torch.Tensor, gate: torch.Tensor | Act8, up: torch.Tensor | Act8 | None = None, act: str = "silu",
@@ -745,9 +795,7 @@ def act_bwd(dh: torch.Tensor, gate: torch.Tensor | Act8, up: torch.Tensor | Act8
     if stream is not None:
         with torch.cuda.stream(stream):
             return act_bwd(dh, gate, up, act, amax_out, dgate, dup)
-    rows, cols, dev = _first(dh, "dh")
-    pdh, ldh = _mat(dh, rows, cols, dev, "dh")
-    dt = dh.dtype
+    pdh, ldh, rows, cols, dev, dt = _first(dh, "dh")
     gated = up is not None
     pg = pu = g8 = u8 = None
     ldg = ldu = lddu = 0
@@ -763,20 +811,25 @@ def act_bwd(dh: torch.Tensor, gate: torch.Tensor | Act8, up: torch.Tensor | Act8
             if isinstance(up, Act8):
                 raise MXError(MX_ERR_INVALID_ARG, "gate and up are both kept or both checkpoints")
             pu, ldu = _mat(up, rows, cols, dev, "up", dt)
+    pdu = None
     if dgate is None and dup is None and gated:
         both = torch.empty((rows, 2 * cols), dtype=dt, device=dev)
         dgate, dup = both[:, :cols], both[:, cols:]
-    if dgate is None:
-        dgate = torch.empty((rows, cols), dtype=dt, device=dev)
-    pdg, lddg = _mat(dgate, rows, cols, dev, "dgate", dt)
-    pdu = None
-    if gated:
-        dup = dup if dup is not None else torch.empty((rows, cols), dtype=dt, device=dev)
-        pdu, lddu = _mat(dup, rows, cols, dev, "dup", dt)
-    elif dup is not None:
-        raise MXError(MX_ERR_INVALID_ARG, "dup goes with up")
+        pdg = both.data_ptr()
+        pdu = pdg + cols * both.element_size()
+        lddg = lddu = 2 * cols
+    else:
+        if dgate is None:
+            dgate = torch.empty((rows, cols), dtype=dt, device=dev)
+        pdg, lddg = _mat(dgate, rows, cols, dev, "dgate", dt)
+        if gated:
+            dup = dup if dup is not None else torch.empty((rows, cols), dtype=dt, device=dev)
+            pdu, lddu = _mat(dup, rows, cols, dev, "dup", dt)
+        elif dup is not None:
+            raise MXError(MX_ERR_INVALID_ARG, "dup goes with up")
     _run(dev, "mx_act_bwd", lib().mx_act_bwd, pdh, ldh, pg, ldg, pu, ldu, g8, u8, rows, cols,
-         _look_up(ACTS, act, "act"), OUT[dt], pdg, lddg, pdu, lddu, _vec(amax_out, 1, dev, "amax_out"))
+         _look_up(ACTS, act, "act"), OUT[dt], pdg, lddg, pdu, lddu,
+         _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None)
     return dgate, dup
 
 
