@@ -201,7 +201,8 @@ int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_
         ok(aligned(weight, dtype_bytes(w_dtype)) ? MX_OK : MX_ERR_ALIGNMENT);
         ok.words(mean).words(rstd).words(dw).words(db).words(amax_out);
         if ((dw || db) && !none) {
-            ok(workspace && ws_bytes >= mx_norm_bwd_workspace_bytes(rows, cols) ? MX_OK : MX_ERR_WORKSPACE);
+            const size_t need = mx_norm_bwd_workspace_bytes(rows, cols);
+            ok(need == 0 || (workspace && ws_bytes >= need) ? MX_OK : MX_ERR_WORKSPACE);
             ok(aligned(workspace, 16) ? MX_OK : MX_ERR_ALIGNMENT);
         }
     }

@@ -112,69 +112,116 @@ __device__ __forceinline__ float kept(const NormBwdArgs& a, int64_t r, int64_t c
     return load_f(static_cast<const T*>(a.x) + r * a.ldx + c);
 }
 
+// dx of row r.
+template <typename T, typename TY>
+__device__ __forceinline__ void dx_row(const NormBwdArgs& a, int64_t r, float* part, Top<T>& top)
+{
+    const int64_t C = a.cols, G = act8_groups(C);
+    const float inv_c = 1.0f / static_cast<float>(C);
+    const TY* dy = static_cast<const TY*>(a.dy) + r * a.ldy;
+    const float rstd = a.rstd[r], mean = a.kind == MX_NORM_LAYER ? a.mean[r] : 0.0f;
+    float sgh = 0.0f, sg = 0.0f;
+#pragma unroll 4
+    for (int64_t c = threadIdx.x; c < C; c += kRowThreads) {
+        const float g = load_f(dy + c) * param(a.weight, a.w_dtype, c, 1.0f);
+        sgh += g * ((kept<T>(a, r, c, G) - mean) * rstd);
+        sg += g;
+    }
+    const float c1 = cta_sum(sgh, part) * inv_c;
+    const float c2 = a.kind == MX_NORM_LAYER ? cta_sum(sg, part) * inv_c : 0.0f;
+    const T* dres = static_cast<const T*>(a.dres) + r * a.ldres;
+    T* dx = static_cast<T*>(a.dx) + r * a.lddx;
+#pragma unroll 4
+    for (int64_t c = threadIdx.x; c < C; c += kRowThreads) {
+        const float g = load_f(dy + c) * param(a.weight, a.w_dtype, c, 1.0f);
+        const float h = (kept<T>(a, r, c, G) - mean) * rstd;
+        float v = (g - h * c1 - c2) * rstd;
+        if (a.dres)
+            v += load_f(dres + c);
+        v = as_stored<T>(v);
+        store_f(dx + c, v);
+        top.value(v);
+    }
+}
+
+// Sums over rows first, first + step .. of column c of the lane, this warp's
+// share of them joined with the other warps' (in warp 0).
+struct ColumnSums {
+    float w, b;
+};
+template <typename T, typename TY>
+__device__ __forceinline__ ColumnSums column_sums(const NormBwdArgs& a, int64_t c, int64_t first, int64_t step)
+{
+    __shared__ float pw[kRowWarps][32], pb[kRowWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t G = act8_groups(a.cols);
+    ColumnSums s = {0.0f, 0.0f};
+    if (c < a.cols)
+#pragma unroll 4
+        for (int64_t r = first + warp; r < a.rows; r += step) {
+            const float dy = load_f(static_cast<const TY*>(a.dy) + r * a.ldy + c);
+            const float mean = a.kind == MX_NORM_LAYER ? a.mean[r] : 0.0f;
+            s.w += dy * ((kept<T>(a, r, c, G) - mean) * a.rstd[r]);
+            s.b += dy;
+        }
+    pw[warp][lane] = s.w;
+    pb[warp][lane] = s.b;
+    __syncthreads();
+    if (warp == 0)
+#pragma unroll
+        for (int i = 1; i < kRowWarps; ++i) {
+            s.w += pw[i][lane];
+            s.b += pb[i][lane];
+        }
+    return s;
+}
+
 template <typename T, typename TY>
 __global__ void __launch_bounds__(kRowThreads) norm_dx_any_kernel(NormBwdArgs a)
 {
     __shared__ float part[kRowWarps];
-    const int64_t C = a.cols, G = act8_groups(C);
-    const float inv_c = 1.0f / static_cast<float>(C);
     Top<T> top;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const TY* dy = static_cast<const TY*>(a.dy) + r * a.ldy;
-        const float rstd = a.rstd[r], mean = a.kind == MX_NORM_LAYER ? a.mean[r] : 0.0f;
-        float sgh = 0.0f, sg = 0.0f;
-        for (int64_t c = threadIdx.x; c < C; c += kRowThreads) {
-            const float g = load_f(dy + c) * param(a.weight, a.w_dtype, c, 1.0f);
-            sgh += g * ((kept<T>(a, r, c, G) - mean) * rstd);
-            sg += g;
-        }
-        const float c1 = cta_sum(sgh, part) * inv_c;
-        const float c2 = a.kind == MX_NORM_LAYER ? cta_sum(sg, part) * inv_c : 0.0f;
-        const T* dres = static_cast<const T*>(a.dres) + r * a.ldres;
-        T* dx = static_cast<T*>(a.dx) + r * a.lddx;
-        for (int64_t c = threadIdx.x; c < C; c += kRowThreads) {
-            const float g = load_f(dy + c) * param(a.weight, a.w_dtype, c, 1.0f);
-            const float h = (kept<T>(a, r, c, G) - mean) * rstd;
-            float v = (g - h * c1 - c2) * rstd;
-            if (a.dres)
-                v += load_f(dres + c);
-            v = as_stored<T>(v);
-            store_f(dx + c, v);
-            top.value(v);
-        }
-    }
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x)
+        dx_row<T, TY>(a, r, part, top);
     if (a.amax)
         flush_top(a.amax, top);
 }
 
-// Partial column sums: CTA (x, y) adds 32 columns of every gridDim.y-th row.
+// Partial column sums: CTA (x, y) adds 32 columns of every gridDim.y-th eight rows.
 template <typename T, typename TY>
 __global__ void __launch_bounds__(kRowThreads) norm_dw_any_kernel(NormBwdArgs a)
 {
     let_next_launch_start();  // the join
-    __shared__ float pw[kRowWarps][32], pb[kRowWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t C = a.cols, G = act8_groups(C), c = blockIdx.x * 32ll + lane;
-    float w = 0.0f, b = 0.0f;
-    if (c < C) {
-        for (int64_t r = blockIdx.y * kRowWarps + warp; r < a.rows; r += static_cast<int64_t>(gridDim.y) * kRowWarps) {
-            const float dy = load_f(static_cast<const TY*>(a.dy) + r * a.ldy + c);
-            const float mean = a.kind == MX_NORM_LAYER ? a.mean[r] : 0.0f;
-            w += dy * ((kept<T>(a, r, c, G) - mean) * a.rstd[r]);
-            b += dy;
-        }
+    const int64_t C = a.cols, c = blockIdx.x * 32ll + (threadIdx.x & 31);
+    const ColumnSums s = column_sums<T, TY>(a, c, blockIdx.y * kRowWarps, static_cast<int64_t>(gridDim.y) * kRowWarps);
+    if (threadIdx.x < 32 && c < C) {
+        a.parts[blockIdx.y * C + c] = s.w;
+        a.parts[(gridDim.y + blockIdx.y) * C + c] = s.b;
     }
-    pw[warp][lane] = w;
-    pb[warp][lane] = b;
-    __syncthreads();
-    if (warp == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < kRowWarps; ++i) {
-            w += pw[i][lane];
-            b += pb[i][lane];
-        }
-        a.parts[blockIdx.y * C + c] = w;
-        a.parts[(gridDim.y + blockIdx.y) * C + c] = b;
+}
+
+// Few short rows: dx by the CTAs first_cta .. a.rows - 1 and the finished column
+// sums by those from a.rows on, without a workspace and, unless dx is the memory
+// of dy or x, which both read, in one launch.
+template <typename T, typename TY>
+__global__ void __launch_bounds__(kRowThreads) norm_bwd_few_kernel(NormBwdArgs a, unsigned first_cta)
+{
+    __shared__ float part[kRowWarps];
+    const int64_t cta = static_cast<int64_t>(blockIdx.x) + first_cta;
+    if (cta < a.rows) {
+        Top<T> top;
+        dx_row<T, TY>(a, cta, part, top);
+        if (a.amax)
+            flush_top(a.amax, top);
+        return;
+    }
+    const int64_t c = (cta - a.rows) * 32 + (threadIdx.x & 31);
+    const ColumnSums s = column_sums<T, TY>(a, c, 0, kRowWarps);
+    if (threadIdx.x < 32 && c < a.cols) {
+        if (a.dw)
+            a.dw[c] = s.w;
+        if (a.db)
+            a.db[c] = s.b;
     }
 }
 
@@ -1100,9 +1147,28 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     return launch_kernel(norm_fwd_any_kernel<T, TY>, grid, 1, kRowThreads, 0, a.amax != nullptr, s, a);
 }
 
+// Calls of up to 64 rows and 2048 columns: one launch, 3.1 us at
+// 32x1024 fp32 where the row kernel and the join take 4.4 us; from 4096 columns
+// on, where a row is long for its CTA's scalar accesses, it is the other way
+// round (64x4096 bf16 from a checkpoint 9.9 us to 6.2).
+bool few_rows(int64_t rows, int64_t cols) { return rows <= 64 && cols <= 2048; }
+
+template <typename T, typename TY>
+int bwd_few(const NormBwdArgs& a, cudaStream_t s)
+{
+    const unsigned rows = static_cast<unsigned>(a.rows);
+    const unsigned columns = a.dw || a.db ? static_cast<unsigned>((a.cols + 31) / 32) : 0;
+    if (columns == 0 || (a.dx != a.dy && a.dx != a.x))
+        return launch_kernel(norm_bwd_few_kernel<T, TY>, rows + columns, 1, kRowThreads, 0, a.amax != nullptr, s, a, 0u);
+    const int rc = launch_kernel(norm_bwd_few_kernel<T, TY>, columns, 1, kRowThreads, 0, false, s, a, rows);
+    return rc != MX_OK ? rc : launch_kernel(norm_bwd_few_kernel<T, TY>, rows, 1, kRowThreads, 0, false, s, a, 0u);
+}
+
 template <typename T, typename TY>
 int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
+    if (few_rows(a.rows, a.cols))
+        return bwd_few<T, TY>(a, s);
     const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
     if (wide_cols(a.cols)) {
         const bool aligned = a.cols % 8 == 0 && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
@@ -1132,6 +1198,8 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 
 int64_t norm_bwd_parts(int64_t rows, int64_t cols)
 {
+    if (few_rows(rows, cols))
+        return 0;
     if (!wide_cols(cols))
         return any_parts(rows);
     return std::max(ctas_of(wide_shape(cols, false), rows), ctas_of(wide_shape(cols, true), rows));

@@ -409,8 +409,8 @@ int mx_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, i
                 int64_t lds, void* y, int64_t ldy, int y_dtype, float* mean, float* rstd, const mx_act8* save,
                 float* amax_out, void* stream);
 
-/* Workspace bytes of mx_norm_bwd when dw or db is asked for (0 for invalid
- * arguments or an empty matrix). */
+/* Workspace bytes of mx_norm_bwd when dw or db is asked for (0 where it needs
+ * none, for invalid arguments and for an empty matrix). */
 size_t mx_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 
 /* The norm's backward pass from dy (dy_dtype), the forward's mean and rstd,
@@ -420,8 +420,9 @@ size_t mx_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  * (MX_NORM_RMS: mean is not read and mean_cols(g) is left out)
  *   dw[cols] = sum over rows of dy * h,   db[cols] = sum over rows of dy (fp32)
  * dres (may be NULL, dx_dtype): the gradient that reaches s past the norm.
- * dw and db may be NULL.  workspace: device, 16-byte aligned, needed when dw
- * or db is given (MX_ERR_WORKSPACE).  amax_out covers dx. */
+ * dw and db may be NULL.  workspace: device, 16-byte aligned, at least
+ * mx_norm_bwd_workspace_bytes when dw or db is given (MX_ERR_WORKSPACE), else
+ * not used.  amax_out covers dx. */
 int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_t ldx, const mx_act8* x8,
                 const float* mean, const float* rstd, const void* weight, int w_dtype, int64_t rows, int64_t cols,
                 int kind, const void* dres, int64_t ldres, void* dx, int64_t lddx, int dx_dtype, float* dw, float* db,

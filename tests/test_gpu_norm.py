@@ -201,6 +201,27 @@ def test_backward_layouts_and_in_place(mx, cols, how):
     assert torch.equal(dy, apart[0]) and torch.equal(got2[1], apart[1]) and torch.equal(got2[2], apart[2])
 
 
+@pytest.mark.parametrize("shape", [(64, 2048), (65, 2048), (64, 2056), (3, 9), (64, 31)])
+@pytest.mark.parametrize("over", ["dy", "x", None])
+def test_backward_around_the_few_row_rule(mx, shape, over):
+    """Both sides of the rule that picks the one-launch kernel, dx apart from,
+    over dy and over x, from the input and from the checkpoint."""
+    rows, cols = shape
+    s, dy = _x(rows, cols, BF, 60), workloads.draw("student_t3", (rows, cols), 61, 1e-3, device="cuda")
+    w, _ = _wb(cols, F32, 62)
+    _, mean, rstd = ref.norm_fwd(s, w, None, "layer", 1e-5)
+    mean, rstd = mean.float(), rstd.float()
+    for kept in (s.clone(), mx.act8_save(s)):
+        sv = s if torch.is_tensor(kept) else ref.decode(kept.codes, kept.sf, cols)
+        d = dy.clone()
+        dx = d if over == "dy" else kept if over == "x" and torch.is_tensor(kept) else None
+        got = mx.norm_bwd(d, kept, rstd, mean, w, dx=dx, dx_dtype=BF)
+        want = ref.norm_bwd(dy, sv, mean, rstd, w, "layer", None)
+        bound = ref.norm_bwd_bounds(dy, sv, mean, rstd, w, "layer", None, BF)
+        for g, v, b, n in zip(got, want, bound, ("dx", "dw", "db")):
+            ref.assert_within(g, v, b, n)
+
+
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("cols", [5, 40])
 def test_gradients_against_differences(mx, cols, kind):

@@ -30,6 +30,7 @@ def test_sizes(L):
     for rows, cols in ((0, 64), (64, 0), (-1, 64), (64, -1), (1, 2 ** 31), (2 ** 60, 64)):
         assert L.mx_act8_codes_bytes(rows, cols) == 0
         assert L.mx_norm_bwd_workspace_bytes(rows, cols) == 0
+    assert L.mx_norm_bwd_workspace_bytes(64, 2048) == 0  # few short rows need none
     for rows in (1, 100, 10 ** 6):
         n = L.mx_norm_bwd_workspace_bytes(rows, 4096)
         assert n >= 2 * 4096 * 4 and n <= 1 << 28
@@ -87,10 +88,15 @@ def test_norm_fwd_refuses(L, why, code, args):
     ("bad kind", BAD, dict(kind=-1)), ("bad type", BAD, dict(xt=7)), ("short stride", BAD, dict(ldx=2)),
     ("short dres", BAD, dict(dres=P, ldres=1)), ("another checkpoint", BAD, dict(x=None, x8=a8(rows=5))),
     ("misaligned dx", ALIGN, dict(dx=P + 1)), ("misaligned dw", ALIGN, dict(dw=P + 2)),
-    ("misaligned workspace", ALIGN, dict(ws=P + 4)), ("no workspace", WS, dict(ws=None)),
-    ("short workspace", WS, dict(n=16))])
+    ("misaligned workspace", ALIGN, dict(ws=P + 4)), ("no workspace", WS, dict(ws=None, rows=100)),
+    ("short workspace", WS, dict(n=16, rows=100))])
 def test_norm_bwd_refuses(L, why, code, args):
     assert norm_bwd(L, **args) == code, why
+
+
+def test_norm_bwd_takes_no_workspace_a_byte_short(L):
+    n = L.mx_norm_bwd_workspace_bytes(100, 64)
+    assert n > 0 and norm_bwd(L, rows=100, n=n - 1) == WS
 
 
 @pytest.mark.parametrize("why,code,args", [
@@ -140,6 +146,7 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
     v, rs = torch.ones(64, device="cuda"), torch.ones(4, device="cuda")
     g = mx.act8_save(x)
+    y, ry = torch.zeros(100, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(100, device="cuda")
     calls = [
         lambda: mx.norm_fwd(x[0]), lambda: mx.norm_fwd(x.half()), lambda: mx.norm_fwd(x.t()),
         lambda: mx.norm_fwd(x[:1].expand(4, 64)),  # rows that share memory have no row stride
@@ -147,7 +154,7 @@ def test_the_binding_refuses_tensors_that_do_not_fit():
         lambda: mx.norm_fwd(x, residual=x.float()), lambda: mx.norm_fwd(x, sum_out=x), lambda: mx.norm_fwd(x, v.cpu()),
         lambda: mx.norm_fwd(x, amax_out=v), lambda: mx.norm_fwd(x, save=mx.Act8.empty(4, 32)),
         lambda: mx.norm_bwd(x, x, rs), lambda: mx.norm_bwd(x, x, rs[:3], rs), lambda: mx.norm_bwd(x, x.float(), rs, rs, dx=x),
-        lambda: mx.norm_bwd(x, x, rs, rs, workspace=torch.empty(4, dtype=torch.uint8, device="cuda")),
+        lambda: mx.norm_bwd(y, y, ry, ry, workspace=torch.empty(4, dtype=torch.uint8, device="cuda")),
         lambda: mx.norm_bwd(x, mx.Act8(g.codes, g.sf, 65), rs, rs),
         lambda: mx.act_fwd(x, x[:, :32]), lambda: mx.act_fwd(x, act="relu"), lambda: mx.act_fwd(x, x.float()),
         lambda: mx.act_bwd(x, g, x), lambda: mx.act_bwd(x, x, g), lambda: mx.act_bwd(x, x, dup=x),
