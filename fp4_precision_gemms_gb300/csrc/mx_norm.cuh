@@ -25,10 +25,14 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
     }
 }
 
-// The kernels of norm_cta.cu: columns they take, and their threads (two octs
-// each, whole checkpoint groups).
-constexpr int64_t kCtaMinCols = 513, kCtaMaxCols = 8192;
-inline int cta_threads(int64_t cols) { return static_cast<int>((act8_groups(cols) * 2 + 31) / 32 * 32); }
+// The kernels of norm_cta.cu: columns they take, and a CTA's threads, two octs
+// each up to kCtaTwoOcts columns and four above, whole checkpoint groups.
+constexpr int64_t kCtaMinCols = 513, kCtaTwoOcts = 8192, kCtaMaxCols = 16384;
+inline int cta_threads(int64_t cols)
+{
+    const int64_t octs = act8_groups(cols) * 4, nv = cols <= kCtaTwoOcts ? 2 : 4;
+    return static_cast<int>(((octs + nv - 1) / nv + 31) / 32 * 32);
+}
 // aligned: rows on 16-byte boundaries of a multiple of eight columns.
 int launch_norm_fwd_cta(const NormFwdArgs& a, bool aligned, const Device& d, cudaStream_t s);
 // At most `most` CTAs; *grid returns their number, each of which leaves a row of

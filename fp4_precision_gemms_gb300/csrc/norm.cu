@@ -1,7 +1,8 @@
-// norm.cu -- layer norm and RMS norm over the rows of a residual stream,
-// forward and backward.
+// norm.cu -- layer norm and RMS norm over the rows of a residual stream, forward
+// and backward: the choice of the kernel, the kernels for narrow rows (up to 512
+// columns), for few short rows and for rows above 16384 columns, and the join of
+// the column sums.  The rows between are norm_cta.cu's.
 #include <algorithm>
-#include <type_traits>
 
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
@@ -38,8 +39,8 @@ __device__ __forceinline__ float cta_sum(float v, float* part)
 }
 
 // ------------------------------------------------------------------ any width
-// One CTA per row, a warp per 32 columns at a time, the row read once per sum.
-// Serves every width and alignment.
+// One CTA per row, a warp per 32 columns at a time, the row read once per sum:
+// right for every width and alignment, and what rows above 16384 columns take.
 
 template <typename T, typename TY>
 __global__ void __launch_bounds__(kRowThreads) norm_fwd_any_kernel(NormFwdArgs a)
@@ -256,111 +257,45 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const flo
     }
 }
 
-// ------------------------------------------------------------------ wide
-// Up to 16384 columns.  Eight columns (an oct) at a time: thread t of a row's TPR threads owns the octs t, t + TPR,
-// ..., NV of them; octs past the row's end hold zeros, and a group's four octs
-// lie in four neighbouring lanes.  LPR > 0: LPR lanes of a warp per row, the
-// rows of a CTA independent; LPR = 0: the CTA's blockDim.x threads per row.
+// ------------------------------------------------------------------ narrow
+// Rows of up to 512 columns, several to a CTA: LPR lanes of a warp (8, 16 or 32)
+// take a row, NV octs (eight columns) each, oct t + j LPR for lane t, so that a
+// checkpoint group's four octs lie in four neighbouring lanes.  Rows that start on
+// 16-byte boundaries, of a multiple of eight columns, take as few lanes as hold
+// them; rows at any address (ANY) a whole warp.
 //
-// The grid is persistent, and a shared-memory ring holds the rows that a CTA
-// takes next, so that the memory system stays busy through the row sums.
-//
-// LPR = 0: one thread issues a bulk copy per matrix and row, which costs the
-// other threads nothing (per-thread copies took about 60 of a warp's 470
-// instructions a row); a stage's mbarrier says when it has arrived, and the
-// barrier of the row sums that a row ago's stage may be filled again.
-// LPR > 0: each thread copies its own words into its own slots, which needs no
-// barrier between the warps' rows.
-constexpr int kMaxWide = 16384;
-constexpr int kSubThreads = 256;  // CTA size where several rows share a CTA
-constexpr int kMaxThreads = 512;  // of a CTA: 128 registers each
-constexpr int kMaxStages = 6;
-constexpr int kBarBytes = (kMaxStages * 8 + 15) / 16 * 16;
-
-template <typename T>
-__device__ __forceinline__ constexpr int chunks() { return sizeof(T) / 2; }  // 16-byte words of an oct
+// The grid is persistent.  A warp copies the rows that it takes next into a ring
+// of shared-memory stages asynchronously, so that the memory system stays busy
+// through the row sums; nothing but the warp's own wait synchronises them.
+// 262144x128 bf16 measured: forward with residual, checkpoint and maximum 55 us
+// (5.5 TB/s), backward from the checkpoint 65 us (3.7 TB/s), 65536x512 57 and 49.
+constexpr int kMaxNarrow = 512;
+constexpr int kThreads = 256;
 
 template <int LPR>
 struct RowMap {
-    int tpr, t;          // threads of a row, this one's place among them
-    int64_t first, step; // this thread's first row, rows from one to the next
-    int mine, all;       // rows of this thread, iterations of the CTA
+    int t;               // this lane's place among a row's lanes
+    int64_t first, step; // its first row, rows from one to the next
+    int mine, all;       // rows of this lane, iterations of the CTA
     __device__ __forceinline__ explicit RowMap(int64_t rows)
     {
-        const int tid = threadIdx.x, per_cta = LPR ? kSubThreads / LPR : 1;
-        tpr = LPR ? LPR : blockDim.x;
-        t = LPR ? tid % LPR : tid;
-        const int64_t cta = static_cast<int64_t>(blockIdx.x) * per_cta;
-        step = static_cast<int64_t>(gridDim.x) * per_cta;
-        first = cta + (LPR ? tid / LPR : 0);
+        constexpr int kRows = kThreads / LPR;
+        t = threadIdx.x % LPR;
+        const int64_t cta = static_cast<int64_t>(blockIdx.x) * kRows;
+        step = static_cast<int64_t>(gridDim.x) * kRows;
+        first = cta + threadIdx.x / LPR;
         all = static_cast<int>((rows - cta + step - 1) / step);
         mine = first < rows ? static_cast<int>((rows - first + step - 1) / step) : 0;
     }
 };
 
-// Sums over a row's threads, known to all of them; a CTA's row goes through
-// `part` (one entry a warp, zero past the CTA's; two of them used in turn, so
-// that one barrier per sum is enough).
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v, float* part, bool& bad)
+__device__ __forceinline__ float row_sum(float v)
 {
 #pragma unroll
-    for (int o = (LPR ? LPR : 32) / 2; o > 0; o >>= 1)
+    for (int o = LPR / 2; o > 0; o >>= 1)
         v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if constexpr (LPR == 0) {
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x >> 5] = v;
-        bad = __syncthreads_or(bad);
-        const float4 p = *reinterpret_cast<const float4*>(part), q = *reinterpret_cast<const float4*>(part + 4);
-        float2 s = __fadd2_rn(__fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)),
-                              __fadd2_rn(make_float2(q.x, q.y), make_float2(q.z, q.w)));
-        if (blockDim.x > 256) {
-            const float4 t = *reinterpret_cast<const float4*>(part + 8), u = *reinterpret_cast<const float4*>(part + 12);
-            s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(make_float2(t.x, t.y), make_float2(t.z, t.w)),
-                                         __fadd2_rn(make_float2(u.x, u.y), make_float2(u.z, u.w))));
-        }
-        v = s.x + s.y;
-    }
     return v;
-}
-// Two sums.  Where a warp belongs to one row its halves exchange the sums, so
-// that each half finishes one of them.
-template <int LPR>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* part, bool& bad)
-{
-    if constexpr (LPR != 0 && LPR < 32) {
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-        }
-        return v;
-    } else {
-        const bool second = threadIdx.x & 16;
-        float s = second ? v.y : v.x;
-        s += __shfl_xor_sync(0xFFFFFFFFu, second ? v.x : v.y, 16);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if constexpr (LPR == 32)
-            return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
-        if ((threadIdx.x & 15) == 0)
-            reinterpret_cast<float*>(part)[(threadIdx.x >> 5) * 2 + (second ? 1 : 0)] = s;
-        bad = __syncthreads_or(bad);
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < 8; w += 2) {
-            const float4 p = *reinterpret_cast<const float4*>(part + w);
-            sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
-        }
-        if (blockDim.x > 256)
-#pragma unroll
-            for (int w = 8; w < 16; w += 2) {
-                const float4 p = *reinterpret_cast<const float4*>(part + w);
-                sum = __fadd2_rn(sum, __fadd2_rn(make_float2(p.x, p.y), make_float2(p.z, p.w)));
-            }
-        return sum;
-    }
 }
 
 // Eight of the weights or biases.  ANY: at any address, those inside the row.
@@ -377,17 +312,17 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, int C
 }
 
 // The ring of PARTS matrices.  A matrix may be absent (null).  Its octs take
-// 16 (bf16), 32 (fp32) or 8 (codes) bytes.  ANY: rows at any address: a stage
-// holds the aligned 16-byte words that a row lies in, one more than its octs
-// fill, and an oct is shifted into place when it is read (codes always start on
-// a boundary).  The words may hold a neighbouring row's elements; the first and
-// the last rows (`edge` of them), whose words would reach past the matrix, are
-// not copied but read where they are.
+// 16 (bf16), 32 (fp32) or 8 (codes) bytes.  ANY: a stage holds the aligned
+// 16-byte words that a row lies in, one more than its octs fill, and an oct is
+// shifted into place when it is read (codes always start on a boundary).  The
+// words may hold a neighbouring row's elements; the first and the last rows
+// (`edge` of them), whose words would reach past the matrix, are not copied but
+// read where they are.
 struct RingPart {
-    const char* src;    // row 0
-    int64_t next_row;   // bytes from one row to the next
-    int oct;            // bytes of an oct
-    uint32_t at;        // in a stage
+    const char* src;   // row 0
+    int64_t next_row;  // bytes from one row to the next
+    int oct;           // bytes of an oct
+    uint32_t at;       // in a stage
 };
 __host__ __device__ constexpr uint32_t region_bytes(int octs, int oct, bool any)
 {
@@ -395,11 +330,9 @@ __host__ __device__ constexpr uint32_t region_bytes(int octs, int oct, bool any)
 }
 template <int LPR, int NV, int PARTS, bool ANY>
 struct RowRing {
-    static constexpr int kLanes = LPR ? LPR : 1;
     RingPart part[PARTS];
-    uint32_t base, stage_bytes, bars, at_stage = 0;
-    int stages, stage = 0, octs, skip = -1;  // skip: test hook, a row that is never copied
-    uint32_t phase = 0;
+    uint32_t base, stage_bytes, at_stage = 0;
+    int stages, stage = 0, cols, octs;
     int64_t rows, row = 0, edge = 1;
     bool direct = false;  // ANY: the current row is read from where it is
     uint32_t here_shift[PARTS], shift_step[PARTS];  // ANY: bytes past a boundary, the current row's and a step's
@@ -411,59 +344,31 @@ struct RowRing {
     }
     __device__ __forceinline__ bool at_edge(int64_t r) const { return ANY && (r < edge || r >= rows - edge); }
 
-    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int cols, int64_t rows_)
+    __device__ __forceinline__ void layout(uint8_t* smem, int stages_, int cols_, int64_t rows_)
     {
         stages = stages_;
+        cols = cols_;
         octs = (cols + 7) / 8;
         rows = rows_;
-        bars = smem_u32(smem);
-        base = bars + (LPR == 0 ? kBarBytes : 0);
+        base = smem_u32(smem);
         uint32_t at = 0;
 #pragma unroll
         for (int m = 0; m < PARTS; ++m) {
             part[m].at = at;
             if (part[m].src) {
-                at += LPR == 0 ? region(m) : ANY ? kSubThreads / kLanes * region(m) : NV * kSubThreads * part[m].oct;
+                at += ANY ? kThreads / LPR * region(m) : NV * kThreads * part[m].oct;
                 if (ANY && part[m].next_row < 16)
                     edge = 16;
             }
         }
         stage_bytes = at;
     }
-
-    // The CTA's row number `it` into stage st: LPR = 0, one thread.
-    __device__ __forceinline__ void fill(const RowMap<LPR>& map, int it, int st)
-    {
-        if (it == skip)
-            return;
-        const int64_t r = map.first + it * map.step;
-        const uint32_t bar = bars + st * 8, to = base + st * stage_bytes;
-        if (at_edge(r)) {
-            mbar_arrive(bar);
-            return;
-        }
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int m = 0; m < PARTS; ++m)
-            if (part[m].src)
-                bytes += copied(m, r);
-        mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-        for (int m = 0; m < PARTS; ++m)
-            if (part[m].src)
-                bulk_load(to + part[m].at, part[m].src + r * part[m].next_row - shift(m, r), copied(m, r), bar);
-    }
     // Bytes of the words that row r lies in.
     __device__ __forceinline__ uint32_t copied(int m, int64_t r) const
     {
-        if constexpr (!ANY)
-            return region(m);
-        return part[m].oct == 8 ? region(m) : (shift(m, r) + row_bytes(m) + 15) / 16 * 16;
+        return part[m].oct == 8 ? region(m) : (shift(m, r) + static_cast<uint32_t>(cols * (part[m].oct / 8)) + 15) / 16 * 16;
     }
-    int cols_ = 0;
-    __device__ __forceinline__ uint32_t row_bytes(int m) const { return static_cast<uint32_t>(cols_) * (part[m].oct / 8); }
-
-    // LPR > 0: this thread's share of its row r into the stage `ahead` rows on.
+    // This lane's share of its row r into the stage `ahead` rows on.
     __device__ __forceinline__ void copy(int64_t r, bool in, int ahead, int t)
     {
         if (in && !at_edge(r)) {
@@ -474,21 +379,21 @@ struct RowRing {
                 if (part[m].src) {
                     const char* row_at = part[m].src + r * part[m].next_row;
                     if constexpr (ANY) {  // the row's words over its lanes
-                        const uint32_t dst = to + part[m].at + (threadIdx.x / kLanes) * region(m);
+                        const uint32_t dst = to + part[m].at + (threadIdx.x / LPR) * region(m);
                         const uint32_t n = copied(m, r);
                         row_at -= shift(m, r);
-                        for (uint32_t w = t * 16; w < n; w += kLanes * 16)
+                        for (uint32_t w = t * 16; w < n; w += LPR * 16)
                             copy_async16(dst + w, row_at + w);
-                    } else {  // a thread's own octs
+                    } else {  // a lane's own octs
                         const int w = min(part[m].oct, 16);
 #pragma unroll
                         for (int j = 0; j < NV; ++j)
-                            if (t + j * kLanes < octs)
+                            if (t + j * LPR < octs)
 #pragma unroll
                                 for (int h = 0; h < part[m].oct / w; ++h) {
                                     const uint32_t dst =
-                                        to + part[m].at + ((j * (part[m].oct / w) + h) * kSubThreads + threadIdx.x) * w;
-                                    const char* from = row_at + (t + j * kLanes) * part[m].oct + h * 16;
+                                        to + part[m].at + ((j * (part[m].oct / w) + h) * kThreads + threadIdx.x) * w;
+                                    const char* from = row_at + (t + j * LPR) * part[m].oct + h * 16;
                                     if (w == 16)
                                         copy_async16(dst, from);
                                     else
@@ -510,47 +415,22 @@ struct RowRing {
                 here_shift[m] = shift(m, row);
                 shift_step[m] = static_cast<uint32_t>(map.step * part[m].next_row) & 15u;
             }
-        if constexpr (LPR == 0) {
-            if (threadIdx.x == 0) {
-                for (int i = 0; i < stages; ++i)
-                    mbar_init(bars + i * 8, 1);
-                fence_mbar_init();
-                for (int i = 0; i < stages && i < map.all; ++i)
-                    fill(map, i, i);
-            }
-            __syncthreads();
-        } else {
-            for (int i = 0; i < stages - 1; ++i)
-                copy(map.first + i * map.step, i < map.mine, i, map.t);
-        }
+        for (int i = 0; i < stages - 1; ++i)
+            copy(map.first + i * map.step, i < map.mine, i, map.t);
     }
-    // Row `it` has arrived (false: the wait gave up).
-    __device__ __forceinline__ bool arrive(const RowMap<LPR>& map, int it, uint64_t limit_ns)
+    // Row `it` has arrived.
+    __device__ __forceinline__ void arrive(const RowMap<LPR>& map, int it)
     {
         direct = at_edge(row);
-        if constexpr (LPR == 0)
-            return mbar_wait_bounded(bars + stage * 8, phase, limit_ns);
         copy(map.first + (it + stages - 1) * map.step, it + stages - 1 < map.mine, stages - 1, map.t);
         copy_wait(stages - 1);
         if (ANY)
-            __syncwarp();
-        return true;
+            __syncwarp();  // words that other lanes copied
     }
-    // LPR = 0, after a barrier in row `it`: nobody reads row it - 1 any more.
-    __device__ __forceinline__ void refill(const RowMap<LPR>& map, int it)
+    // The end of a row.
+    __device__ __forceinline__ void done(const RowMap<LPR>& map)
     {
-        if (LPR == 0 && threadIdx.x == 0 && stages > 1 && it > 0 && it - 1 + stages < map.all)
-            fill(map, it - 1 + stages, stage == 0 ? stages - 1 : stage - 1);
-    }
-    // The end of row `it`.
-    __device__ __forceinline__ void done(const RowMap<LPR>& map, int it)
-    {
-        if (LPR == 0 && stages == 1) {
-            __syncthreads();
-            if (threadIdx.x == 0 && it + 1 < map.all)
-                fill(map, it + 1, 0);
-        }
-        if (LPR != 0 && ANY)
+        if (ANY)
             __syncwarp();  // the stage's next words may come from another lane
         row += map.step;
         if constexpr (ANY)
@@ -561,33 +441,17 @@ struct RowRing {
         if (++stage == stages) {
             stage = 0;
             at_stage = 0;
-            phase ^= 1;
         }
-    }
-    // Gave up in row `it`, before its refill: the copies in flight are waited
-    // for before the CTA's memory goes back.
-    __device__ __forceinline__ void abandon(const RowMap<LPR>& map, int it, uint64_t limit_ns)
-    {
-        if (LPR == 0 && threadIdx.x == 0)
-            for (int i = it; i < map.all && i < (it > 0 && stages > 1 ? it - 1 : it) + stages; ++i) {
-                mbar_wait_bounded(bars + stage * 8, phase, limit_ns);
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
     }
 
     // Address of word h of oct j of matrix m in the current stage.
     __device__ __forceinline__ uint32_t word(int m, int j, int h) const
     {
         const uint32_t at = base + at_stage + part[m].at;
-        if constexpr (LPR == 0)
-            return at + (threadIdx.x + j * blockDim.x) * part[m].oct + h * 16;
         if constexpr (ANY)
-            return at + threadIdx.x / kLanes * region(m) + (threadIdx.x % kLanes + j * kLanes) * part[m].oct + h * 16;
+            return at + threadIdx.x / LPR * region(m) + (threadIdx.x % LPR + j * LPR) * part[m].oct + h * 16;
         const int w = min(part[m].oct, 16);
-        return at + ((j * (part[m].oct / w) + h) * kSubThreads + threadIdx.x) * w;
+        return at + ((j * (part[m].oct / w) + h) * kThreads + threadIdx.x) * w;
     }
     // Oct j, at column c, with n > 0 values inside the row.
     template <typename T>
@@ -636,43 +500,36 @@ __device__ __forceinline__ void put_oct(T* p, const Oct& o, int n, int c, int C,
 {
     if constexpr (ANY) {
         const int lane = threadIdx.x & 31;
-        store_ragged(p, o, n, lane > 0 && c > 0, lane < 31 && c + 8 < C && n > 0, top);
+        store_ragged(p, o, n, lane > 0, lane < 31 && c + 8 < C && n > 0, top);
     } else if (n > 0) {
         store_oct(p, o, top);
     }
 }
 
 template <typename T, typename TY, int LPR, int NV, bool ANY>
-__global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArgs a, int stages)
+__global__ void __launch_bounds__(kThreads, 2) norm_fwd_narrow_kernel(NormFwdArgs a, int stages)
 {
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float part[2][kMaxThreads / 32];
-    if (LPR == 0) {
-        if (threadIdx.x < kMaxThreads / 32)
-            part[0][threadIdx.x] = part[1][threadIdx.x] = 0.0f;
-        __syncthreads();
-    }
+    static_assert(!ANY || LPR == 32, "rows at any address take whole warps");
+    extern __shared__ __align__(16) uint8_t smem[];
     const RowMap<LPR> map(a.rows);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
-    const int c0 = 8 * map.t, dc = 8 * map.tpr;  // columns of oct j: c0 + j dc ..
+    const int c0 = 8 * map.t;
+    constexpr int dc = 8 * LPR;  // columns of oct j: c0 + j dc ..
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER, add = a.residual != nullptr;
-    RowRing<LPR, NV, 2, ANY> ring_;
-    ring_.part[0] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
-    ring_.part[1] = {static_cast<const char*>(a.residual), a.ldr * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
-    ring_.cols_ = C;
-    ring_.layout(ring, stages, C, a.rows);
+    RowRing<LPR, NV, 2, ANY> ring;
+    ring.part[0] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring.part[1] = {static_cast<const char*>(a.residual), a.ldr * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring.layout(smem, stages, C, a.rows);
     auto count = [&](bool in, int j) { return in ? min(C - c0 - j * dc, 8) : 0; };  // an oct's values
 
-    constexpr bool KEEP = NV <= 2;  // weights and biases stay in registers
-    Oct wt[KEEP ? NV : 1], bi[KEEP ? NV : 1];
-    if constexpr (KEEP)
+    Oct wt[NV], bi[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (c0 + j * dc < C) {
-                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, wt[j]);
-                param_oct<ANY>(a.bias, a.w_dtype, c0 + j * dc, C, 0.0f, bi[j]);
-            }
+    for (int j = 0; j < NV; ++j)
+        if (c0 + j * dc < C) {
+            param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, wt[j]);
+            param_oct<ANY>(a.bias, a.w_dtype, c0 + j * dc, C, 0.0f, bi[j]);
+        }
     Top<TY> top;
     Top<T> sum_top;
     T* to_sum = static_cast<T*>(a.sum_out) + map.first * a.lds + c0;
@@ -681,12 +538,9 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
     uint8_t* to_sf = a.save.sf + map.first * G + c0 / kAct8Group;
     const int64_t sum_step = map.step * a.lds, y_step = map.step * a.ldy;
     const int64_t codes_step = map.step * (G * kAct8Group), sf_step = map.step * G;
-    ring_.skip = a.fail_at;
-    ring_.start(map);
-    bool bad = false;
-    int it = 0;
-    for (; it < map.all; ++it) {
-        bad = !ring_.arrive(map, it, a.wait_ns);
+    ring.start(map);
+    for (int it = 0; it < map.all; ++it) {
+        ring.arrive(map, it);
         const bool in = it < map.mine;
         Oct v[NV];
         float2 sum2 = make_float2(0.0f, 0.0f);
@@ -695,12 +549,12 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
             const int n = count(in, j);
             v[j].fill(0.0f);
             if (n > 0)
-                ring_.template read<T>(0, j, c0 + j * dc, n, v[j]);
+                ring.template read<T>(0, j, c0 + j * dc, n, v[j]);
             if (add) {
                 Oct q;
                 q.fill(0.0f);
                 if (n > 0)
-                    ring_.template read<T>(1, j, c0 + j * dc, n, q);
+                    ring.template read<T>(1, j, c0 + j * dc, n, q);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     q.p[k] = __fadd2_rn(v[j].p[k], q.p[k]);
@@ -714,12 +568,7 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
             for (int k = 0; k < 4; ++k)
                 sum2 = __fadd2_rn(sum2, v[j].p[k]);
         }
-        float mean = 0.0f;
-        if (layer) {
-            mean = row_sum<LPR>(sum2.x + sum2.y, part[0], bad) * inv_c;
-            if (LPR == 0 && bad)
-                break;
-        }
+        const float mean = layer ? row_sum<LPR>(sum2.x + sum2.y) * inv_c : 0.0f;
         float2 sq2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -734,11 +583,7 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
                 for (int k = 0; k < 4; ++k)
                     sq2 = __ffma2_rn(d.p[k], d.p[k], sq2);
             }
-        // RMS norm has one sum per row: its words alternate with the row
-        const float rstd = rsqrtf(row_sum<LPR>(sq2.x + sq2.y, part[layer ? 1 : it & 1], bad) * inv_c + a.eps);
-        if (LPR == 0 && bad)
-            break;
-        ring_.refill(map, it);
+        const float rstd = rsqrtf(row_sum<LPR>(sq2.x + sq2.y) * inv_c + a.eps);
         if (map.t == 0 && in) {
             const int64_t r = map.first + it * map.step;
             if (a.mean && layer)
@@ -749,16 +594,12 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int n = count(in, j);
-            Oct &w = wt[KEEP ? j : 0], &b = bi[KEEP ? j : 0], y;
-            if (!KEEP && n > 0) {
-                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, w);
-                param_oct<ANY>(a.bias, a.w_dtype, c0 + j * dc, C, 0.0f, b);
-            }
             if (ANY || n > 0) {
+                Oct y;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 h = __fmul2_rn(__fadd2_rn(v[j].p[k], both(-mean)), both(rstd));
-                    y.p[k] = __ffma2_rn(h, w.p[k], b.p[k]);
+                    y.p[k] = __ffma2_rn(h, wt[j].p[k], bi[j].p[k]);
                 }
                 put_oct<ANY>(to_y + j * dc, y, n, c0 + j * dc, C, top);
             }
@@ -776,50 +617,36 @@ __global__ void __maxnreg__(ANY || NV > 2 ? 112 : 96) norm_fwd_kernel(NormFwdArg
         to_y += y_step;
         to_codes += codes_step;
         to_sf += sf_step;
-        ring_.done(map, it);
-    }
-    if (LPR == 0 && bad) {
-        if (threadIdx.x == 0)
-            atomicExch(a.status, MX_ERR_TIMEOUT);
-        ring_.abandon(map, it, a.wait_ns);
-        return;
+        ring.done(map);
     }
     if (a.amax)
         flush_top(a.amax, top);
 }
 
 // dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
-// is the checkpoint.  The column sums stay in registers over all rows of the
-// CTA; dy h and g h come from one reading of the row, dx from what was kept of
-// it in registers (up to two octs a thread) or from a second reading of shared
-// memory.
+// is the checkpoint.  The column sums stay in registers over all of a lane's rows;
+// at the end the rows of a warp and the warps join them, in a fixed order.
 template <typename T, typename TY, bool FROM8, int LPR, int NV, bool ANY>
-__global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) norm_bwd_kernel(NormBwdArgs a, int stages)
+__global__ void __launch_bounds__(kThreads, 2) norm_bwd_narrow_kernel(NormBwdArgs a, int stages)
 {
+    static_assert(!ANY || LPR == 32, "rows at any address take whole warps");
     let_next_launch_start();  // the join of the partial sums
-    constexpr bool KEEP = NV <= 2;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float2 part[2][kMaxThreads / 32];
-    if (LPR == 0) {
-        if (threadIdx.x < kMaxThreads / 32)
-            part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
-        __syncthreads();
-    }
+    extern __shared__ __align__(16) uint8_t smem[];
     const RowMap<LPR> map(a.rows);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
-    const int c0 = 8 * map.t, dc = 8 * map.tpr;
+    const int c0 = 8 * map.t;
+    constexpr int dc = 8 * LPR;
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER, add = a.dres != nullptr;
-    RowRing<LPR, NV, 3, ANY> ring_;
-    ring_.part[0] = {static_cast<const char*>(a.dy), a.ldy * static_cast<int64_t>(sizeof(TY)), 8 * sizeof(TY), 0};
+    RowRing<LPR, NV, 3, ANY> ring;
+    ring.part[0] = {static_cast<const char*>(a.dy), a.ldy * static_cast<int64_t>(sizeof(TY)), 8 * sizeof(TY), 0};
     if constexpr (FROM8)
-        ring_.part[1] = {reinterpret_cast<const char*>(a.x8.codes), G * int64_t{kAct8Group}, 8, 0};
+        ring.part[1] = {reinterpret_cast<const char*>(a.x8.codes), G * int64_t{kAct8Group}, 8, 0};
     else
-        ring_.part[1] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
-    ring_.part[2] = {static_cast<const char*>(a.dres), a.ldres * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
-    ring_.cols_ = C;
-    ring_.layout(ring, stages, C, a.rows);
-    auto count = [&](bool in, int j) { return in ? min(C - c0 - j * dc, 8) : 0; };  // an oct's values
+        ring.part[1] = {static_cast<const char*>(a.x), a.ldx * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring.part[2] = {static_cast<const char*>(a.dres), a.ldres * static_cast<int64_t>(sizeof(T)), 8 * sizeof(T), 0};
+    ring.layout(smem, stages, C, a.rows);
+    auto count = [&](bool in, int j) { return in ? min(C - c0 - j * dc, 8) : 0; };
 
     struct RowWords {  // what a row needs beside its matrices, loaded a row ahead
         float mean, rstd;
@@ -841,100 +668,64 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         return w;
     };
 
-    Oct wt[KEEP ? NV : 1];
-    if constexpr (KEEP)
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (c0 + j * dc < C)
-                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, wt[j]);
-    Oct dw[NV], db[NV];
+    Oct wt[NV], dw[NV], db[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+        if (c0 + j * dc < C)
+            param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, wt[j]);
         dw[j].fill(0.0f);
         db[j].fill(0.0f);
     }
     Top<T> top;
     T* to_dx = static_cast<T*>(a.dx) + map.first * a.lddx + c0;
     const int64_t dx_step = map.step * a.lddx;
-    ring_.skip = a.fail_at;
-    ring_.start(map);
+    ring.start(map);
     RowWords next = row_words(0 < map.mine);
-    bool bad = false;
-    int it = 0;
-    for (; it < map.all; ++it) {
+    for (int it = 0; it < map.all; ++it) {
         const bool in = it < map.mine;
         const RowWords cur = next;
         next = row_words(it + 1 < map.mine);
-        bad = !ring_.arrive(map, it, a.wait_ns);
-        // dy, and g and h of oct j
-        auto load = [&](int j, int n, Oct& dy, Oct& g, Oct& h) {
-            ring_.template read<TY>(0, j, c0 + j * dc, n, dy);
-            if constexpr (FROM8) {
-                ring_.read_codes(1, j, c0 + j * dc, h);
-                const float2 scale = both(act8_scale(cur.e[j]));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)  // the product is exact
-                    h.p[k] = __ffma2_rn(h.p[k], scale, both(-cur.mean));
-            } else {
-                ring_.template read<T>(1, j, c0 + j * dc, n, h);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h.p[k] = __fadd2_rn(h.p[k], both(-cur.mean));
-            }
-            if constexpr (KEEP)
-                g = wt[j];
-            else
-                param_oct<ANY>(a.weight, a.w_dtype, c0 + j * dc, C, 1.0f, g);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h.p[k] = __fmul2_rn(h.p[k], both(cur.rstd));
-                g.p[k] = __fmul2_rn(g.p[k], dy.p[k]);  // zero past the row's end, as dy
-            }
-        };
-        Oct kg[KEEP ? NV : 1], kh[KEEP ? NV : 1];
+        ring.arrive(map, it);
+        Oct g[NV], h[NV];
         float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (const int n = count(in, j); n > 0) {
-                Oct dy, &g = kg[KEEP ? j : 0], &h = kh[KEEP ? j : 0];
-                load(j, n, dy, g, h);
+                Oct dy;
+                ring.template read<TY>(0, j, c0 + j * dc, n, dy);
+                if constexpr (FROM8)
+                    ring.read_codes(1, j, c0 + j * dc, h[j]);
+                else
+                    ring.template read<T>(1, j, c0 + j * dc, n, h[j]);
+                const float2 scale = both(act8_scale(cur.e[j]));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    sgh = __ffma2_rn(g.p[k], h.p[k], sgh);
-                    sg = __fadd2_rn(sg, g.p[k]);
-                    dw[j].p[k] = __ffma2_rn(dy.p[k], h.p[k], dw[j].p[k]);
+                    // the code's product with its scale is exact
+                    h[j].p[k] = FROM8 ? __ffma2_rn(h[j].p[k], scale, both(-cur.mean)) : __fadd2_rn(h[j].p[k], both(-cur.mean));
+                    h[j].p[k] = __fmul2_rn(h[j].p[k], both(cur.rstd));
+                    g[j].p[k] = __fmul2_rn(wt[j].p[k], dy.p[k]);  // zero past the row's end, as dy
+                    sgh = __ffma2_rn(g[j].p[k], h[j].p[k], sgh);
+                    sg = __fadd2_rn(sg, g[j].p[k]);
+                    dw[j].p[k] = __ffma2_rn(dy.p[k], h[j].p[k], dw[j].p[k]);
                     db[j].p[k] = __fadd2_rn(db[j].p[k], dy.p[k]);
                 }
             }
-        const float2 s = row_sum2<LPR>(make_float2(sgh.x + sgh.y, sg.x + sg.y), part[it & 1], bad);
-        if (LPR == 0 && bad)
-            break;
-        ring_.refill(map, it);
-        const float2 c1 = both(-s.x * inv_c), c2 = both(layer ? -s.y * inv_c : 0.0f);
+        const float c1s = row_sum<LPR>(sgh.x + sgh.y) * inv_c, c2s = row_sum<LPR>(sg.x + sg.y) * inv_c;
+        const float2 c1 = both(-c1s), c2 = both(layer ? -c2s : 0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (const int n = count(in, j); ANY || n > 0) {
-                Oct dy, q, &g = kg[KEEP ? j : 0], &h = kh[KEEP ? j : 0];
+                Oct q;
                 q.fill(0.0f);
-                if (n > 0) {
-                    if constexpr (!KEEP)
-                        load(j, n, dy, g, h);
-                    if (add)
-                        ring_.template read<T>(2, j, c0 + j * dc, n, q);
-                }
+                if (add && n > 0)
+                    ring.template read<T>(2, j, c0 + j * dc, n, q);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h.p[k], c1, g.p[k]), c2), both(cur.rstd), q.p[k]);
+                    q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h[j].p[k], c1, g[j].p[k]), c2), both(cur.rstd), q.p[k]);
                 put_oct<ANY>(to_dx + j * dc, q, n, c0 + j * dc, C, top);
             }
         to_dx += dx_step;
-        ring_.done(map, it);
-    }
-    if (LPR == 0 && bad) {
-        if (threadIdx.x == 0)
-            atomicExch(a.status, MX_ERR_TIMEOUT);
-        ring_.abandon(map, it, a.wait_ns);
-        return;
+        ring.done(map);
     }
     if (a.amax)
         flush_top(a.amax, top);
@@ -942,155 +733,112 @@ __global__ void __launch_bounds__(LPR ? kSubThreads : kMaxThreads, LPR ? 2 : 1) 
         return;
     float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C;
     const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
-    if constexpr (LPR == 0) {
+    constexpr int kWarpCols = NV * LPR * 8;
+    float* const red = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (ANY) {
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int o = LPR; o < 32; o <<= 1) {
+                dw[j][i] += __shfl_xor_sync(0xFFFFFFFFu, dw[j][i], o);
+                db[j][i] += __shfl_xor_sync(0xFFFFFFFFu, db[j][i], o);
+            }
+    copy_wait(0);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+        if ((threadIdx.x & 31) < LPR)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (c0 + j * dc + i < C) {
-                        out[c0 + j * dc + i] = dw[j][i];
-                        out[to_db + c0 + j * dc + i] = db[j][i];
-                    }
-            } else if (c0 + j * dc < C)
+                    red[(threadIdx.x >> 5) * kWarpCols + (j * 8 + i) * LPR + map.t] = which ? db[j][i] : dw[j][i];
+        __syncthreads();
+        for (int k = threadIdx.x; k < kWarpCols; k += kThreads) {
+            float v = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    float* const to = out + c0 + j * dc + 2 * k;
-                    *reinterpret_cast<float4*>(to) =
-                        make_float4(dw[j].p[k].x, dw[j].p[k].y, dw[j].p[k + 1].x, dw[j].p[k + 1].y);
-                    *reinterpret_cast<float4*>(to + to_db) =
-                        make_float4(db[j].p[k].x, db[j].p[k].y, db[j].p[k + 1].x, db[j].p[k + 1].y);
-                }
-    } else {
-        // the rows of a warp, then the warps through shared memory, in order
-        constexpr int kWarpCols = NV * LPR * 8;
-        float* const red = reinterpret_cast<float*>(ring);
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int o = LPR; o < 32; o <<= 1) {
-                    dw[j][i] += __shfl_xor_sync(0xFFFFFFFFu, dw[j][i], o);
-                    db[j][i] += __shfl_xor_sync(0xFFFFFFFFu, db[j][i], o);
-                }
-        copy_wait(0);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
-            if ((threadIdx.x & 31) < LPR)
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        red[(threadIdx.x >> 5) * kWarpCols + (j * 8 + i) * LPR + map.t] = which ? db[j][i] : dw[j][i];
-            __syncthreads();
-            for (int k = threadIdx.x; k < kWarpCols; k += kSubThreads) {
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kSubThreads / 32; ++w)
-                    v += red[w * kWarpCols + k];
-                const int t = k % LPR, ji = k / LPR, c = 8 * (t + LPR * (ji / 8)) + ji % 8;
-                if (c < C)
-                    out[which * to_db + c] = v;
-            }
+            for (int w = 0; w < kThreads / 32; ++w)
+                v += red[w * kWarpCols + k];
+            const int t = k % LPR, ji = k / LPR, c = 8 * (t + LPR * (ji / 8)) + ji % 8;
+            if (c < C)
+                out[which * to_db + c] = v;
         }
     }
 }
 
-// How a width is spread over threads: octs of whole groups, so that a group's
-// four lanes all exist.  Two octs a thread as long as 512 threads suffice (the
-// weights, the column sums and a row's values then fit 128 registers), four
-// above 8192 columns.  Up to 512 columns a warp, or a part of one, takes a row
-// (`any`: rows at any address: a whole warp).
-struct WideShape {
-    int lpr, nv, threads;
+// Lanes of a narrow row and octs of each: whole checkpoint groups.
+struct NarrowShape {
+    int lpr, nv;
 };
-WideShape wide_shape(int64_t cols, bool any)
+NarrowShape narrow_shape(int64_t cols, bool any)
 {
     const int octs = static_cast<int>(act8_groups(cols)) * 4;
     if (octs <= 16 && !any)
-        return {octs <= 8 ? 8 : 16, 1, kSubThreads};
-    if (octs <= 64)
-        return {32, octs <= 32 ? 1 : 2, kSubThreads};
-    const int nv = octs <= 2 * kMaxThreads ? 2 : 4;
-    return {0, nv, ((octs + nv - 1) / nv + 31) / 32 * 32};
+        return {octs <= 8 ? 8 : 16, 1};
+    return {32, octs <= 32 ? 1 : 2};
 }
-
-constexpr int kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
-// CTAs of an SM and rows in flight of each, from the bytes of one row's slots:
-// as many CTAs as registers allow (with at least two stages each), then the
-// stages that fit.
-struct RingPlan {
-    int per_sm, stages;
-};
-RingPlan ring_plan(int64_t stage_bytes, int resident, int most)
+// Bytes of a stage's share of one matrix.
+int64_t stage_part(const NarrowShape& w, int64_t cols, int oct, bool any)
 {
-    RingPlan p;
-    p.per_sm = resident;
-    while (p.per_sm > 1 && p.per_sm * 2 * stage_bytes > kRingBytes)
-        --p.per_sm;
-    p.stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, kRingBytes / (p.per_sm * stage_bytes))));
-    return p;
+    return any ? int64_t{kThreads / w.lpr} * region_bytes(static_cast<int>((cols + 7) / 8), oct, true)
+               : int64_t{w.nv} * kThreads * oct;
 }
-
 bool wide_rows(const void* p, int64_t ld, int bytes)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * bytes) % 16 == 0;
 }
-bool wide_cols(int64_t cols) { return cols <= kMaxWide; }
 
-// Launches a ring kernel: its grid fills the GPU, or covers the rows, and has
-// at most `most` CTAs.  `grid` returns it.
+// Launches a ring kernel: up to three rows in flight for each of the CTAs that
+// an SM holds, a grid that fills the GPU or covers the rows, with at most `most`
+// CTAs.  *grid returns it.
+constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
 template <auto KERNEL, typename A>
-int launch_ring(const A& a, const WideShape& w, int64_t stage_bytes, size_t least_smem, int64_t most, unsigned* grid,
-                const Device& d, cudaStream_t s)
+int launch_narrow(const A& a, const NarrowShape& w, int64_t stage_bytes, size_t least_smem, int64_t most, unsigned* grid,
+                  const Device& d, cudaStream_t s)
 {
-    const RingPlan p = ring_plan(stage_bytes, resident_ctas<KERNEL>(w.threads),
-                                 w.lpr ? 3 : kMaxStages);
-    const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1, ctas = (a.rows + per_cta - 1) / per_cta;
-    *grid = static_cast<unsigned>(std::min(most, std::min<int64_t>(ctas, int64_t{d.sms} * p.per_sm)));
-    const size_t smem = std::max(static_cast<size_t>(stage_bytes) * p.stages + (w.lpr ? 0 : kBarBytes), least_smem);
-    if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
+    int per_sm = resident_ctas<KERNEL>(kThreads);
+    while (per_sm > 1 && per_sm * 2 * stage_bytes > kRingBytes)
+        --per_sm;
+    const int stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, kRingBytes / (per_sm * stage_bytes))));
+    const int64_t per_cta = kThreads / w.lpr, ctas = (a.rows + per_cta - 1) / per_cta;
+    *grid = static_cast<unsigned>(std::min(most, std::min<int64_t>(ctas, int64_t{d.sms} * per_sm)));
+    const size_t smem = std::max(static_cast<size_t>(stage_bytes) * stages, least_smem);
+    if (smem > 40 * 1024 &&  // 48 KiB without asking
         cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return MX_ERR_CUDA;
-    return launch_kernel(KERNEL, *grid, 1, w.threads, smem, a.amax != nullptr, s, a, p.stages);
-}
-
-// Bytes of a stage's share of one matrix.
-int64_t stage_part(const WideShape& w, int64_t cols, int oct, bool any)
-{
-    const int64_t region = region_bytes(static_cast<int>((cols + 7) / 8), oct, any);
-    return w.lpr == 0 ? region : any ? w.threads / w.lpr * region : static_cast<int64_t>(w.nv) * w.threads * oct;
+    return launch_kernel(KERNEL, *grid, 1, kThreads, smem, a.amax != nullptr, s, a, stages);
 }
 
 template <typename T, typename TY, bool ANY>
-int fwd_wide(const NormFwdArgs& a, const Device& d, cudaStream_t s)
+int fwd_narrow(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
-    const WideShape w = wide_shape(a.cols, ANY);
+    const NarrowShape w = narrow_shape(a.cols, ANY);
     const int64_t bytes = stage_part(w, a.cols, 8 * sizeof(T), ANY) * (a.residual ? 2 : 1);
     const int64_t most = INT32_MAX;
     unsigned grid;
     if constexpr (!ANY) {
         if (w.lpr == 8)
-            return launch_ring<norm_fwd_kernel<T, TY, 8, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+            return launch_narrow<norm_fwd_narrow_kernel<T, TY, 8, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
         if (w.lpr == 16)
-            return launch_ring<norm_fwd_kernel<T, TY, 16, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+            return launch_narrow<norm_fwd_narrow_kernel<T, TY, 16, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
     }
-    if (w.lpr == 32 && w.nv == 1)
-        return launch_ring<norm_fwd_kernel<T, TY, 32, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
-    if (w.lpr == 32)
-        return launch_ring<norm_fwd_kernel<T, TY, 32, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
-    return launch_ring<norm_fwd_kernel<T, TY, 0, 4, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+    if (w.nv == 1)
+        return launch_narrow<norm_fwd_narrow_kernel<T, TY, 32, 1, ANY>>(a, w, bytes, 0, most, &grid, d, s);
+    return launch_narrow<norm_fwd_narrow_kernel<T, TY, 32, 2, ANY>>(a, w, bytes, 0, most, &grid, d, s);
 }
 
 // Most CTAs of a backward kernel, each with its partial sums: 768 threads an SM
 // at most, 152 SMs.  A pure function of the shape: the workspace is sized by it.
 constexpr int kPartSms = 152;
-int64_t ctas_of(const WideShape& w, int64_t rows)
+int64_t cta_parts(int64_t rows, int64_t cols)
 {
-    const int64_t per_cta = w.lpr ? w.threads / w.lpr : 1;
-    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * std::min(8, std::max(1, 768 / w.threads)));
+    return std::min<int64_t>(rows, kPartSms * std::min(8, std::max(1, 768 / cta_threads(cols))));
+}
+int64_t narrow_parts(int64_t rows, int64_t cols, bool any)
+{
+    const int64_t per_cta = kThreads / narrow_shape(cols, any).lpr;
+    return std::min<int64_t>((rows + per_cta - 1) / per_cta, kPartSms * (768 / kThreads));
 }
 
 // dw and db from `parts` partial sums of each column, where they are asked for.
@@ -1103,29 +851,27 @@ int join(const NormBwdArgs& a, int parts, cudaStream_t s)
 }
 
 template <typename T, typename TY, bool FROM8, bool ANY>
-int bwd_wide(const NormBwdArgs& a, const Device& d, cudaStream_t s)
+int bwd_narrow(const NormBwdArgs& a, const Device& d, cudaStream_t s)
 {
-    const WideShape w = wide_shape(a.cols, ANY);
+    const NarrowShape w = narrow_shape(a.cols, ANY);
     const int64_t bytes = stage_part(w, a.cols, 8 * sizeof(TY), ANY) +
                           stage_part(w, a.cols, FROM8 ? 8 : 8 * sizeof(T), ANY) +
                           (a.dres ? stage_part(w, a.cols, 8 * sizeof(T), ANY) : 0);
-    const int64_t most = ctas_of(w, a.rows);
-    // the column sums of a warp-per-row CTA pass through the ring's memory
-    const size_t least = w.lpr ? static_cast<size_t>(w.nv) * w.lpr * 8 * sizeof(float) * (w.threads / 32) : 0;
+    const int64_t most = narrow_parts(a.rows, a.cols, ANY);
+    // the warps' column sums pass through the ring's memory
+    const size_t least = static_cast<size_t>(w.nv) * w.lpr * 8 * sizeof(float) * (kThreads / 32);
     unsigned grid;
     int rc = MX_ERR_UNSUPPORTED;
     if constexpr (!ANY) {
         if (w.lpr == 8)
-            rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 8, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
+            rc = launch_narrow<norm_bwd_narrow_kernel<T, TY, FROM8, 8, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
         else if (w.lpr == 16)
-            rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 16, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
+            rc = launch_narrow<norm_bwd_narrow_kernel<T, TY, FROM8, 16, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
     }
     if (w.lpr == 32 && w.nv == 1)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
+        rc = launch_narrow<norm_bwd_narrow_kernel<T, TY, FROM8, 32, 1, ANY>>(a, w, bytes, least, most, &grid, d, s);
     else if (w.lpr == 32)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 32, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
-    else if (w.lpr == 0 && w.nv == 4)
-        rc = launch_ring<norm_bwd_kernel<T, TY, FROM8, 0, 4, ANY>>(a, w, bytes, least, most, &grid, d, s);
+        rc = launch_narrow<norm_bwd_narrow_kernel<T, TY, FROM8, 32, 2, ANY>>(a, w, bytes, least, most, &grid, d, s);
     return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
 }
 
@@ -1135,14 +881,13 @@ template <typename T, typename TY>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
-    if (wide_cols(a.cols)) {
-        const bool aligned = a.cols % 8 == 0 && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
-                             wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) &&
-                             wide_rows(a.weight, 8, wb) && wide_rows(a.bias, 8, wb);
-        if (a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols)
-            return launch_norm_fwd_cta(a, aligned, d, s);
-        return aligned ? fwd_wide<T, TY, false>(a, d, s) : fwd_wide<T, TY, true>(a, d, s);
-    }
+    const bool aligned = a.cols % 8 == 0 && wide_rows(a.x, a.ldx, sizeof(T)) && wide_rows(a.residual, a.ldr, sizeof(T)) &&
+                         wide_rows(a.sum_out, a.lds, sizeof(T)) && wide_rows(a.y, a.ldy, sizeof(TY)) &&
+                         wide_rows(a.weight, 8, wb) && wide_rows(a.bias, 8, wb);
+    if (a.cols <= kMaxNarrow)
+        return aligned ? fwd_narrow<T, TY, false>(a, d, s) : fwd_narrow<T, TY, true>(a, d, s);
+    if (a.cols <= kCtaMaxCols)
+        return launch_norm_fwd_cta(a, aligned, d, s);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, d.sms * 8));
     return launch_kernel(norm_fwd_any_kernel<T, TY>, grid, 1, kRowThreads, 0, a.amax != nullptr, s, a);
 }
@@ -1170,18 +915,18 @@ int bwd(const NormBwdArgs& a, const Device& d, cudaStream_t s)
     if (few_rows(a.rows, a.cols))
         return bwd_few<T, TY>(a, s);
     const int wb = a.w_dtype == MX_OUT_BF16 ? 2 : 4;
-    if (wide_cols(a.cols)) {
-        const bool aligned = a.cols % 8 == 0 && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
-                             wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) &&
-                             wide_rows(a.weight, 8, wb);
-        if (a.cols >= kCtaMinCols && a.cols <= kCtaMaxCols) {
-            unsigned grid;
-            const int rc = launch_norm_bwd_cta(a, aligned, static_cast<int>(ctas_of(wide_shape(a.cols, false), a.rows)), d, s, &grid);
-            return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
-        }
+    const bool aligned = a.cols % 8 == 0 && wide_rows(a.dy, a.ldy, sizeof(TY)) && wide_rows(a.x, a.ldx, sizeof(T)) &&
+                         wide_rows(a.dres, a.ldres, sizeof(T)) && wide_rows(a.dx, a.lddx, sizeof(T)) &&
+                         wide_rows(a.weight, 8, wb);
+    if (a.cols <= kMaxNarrow) {
         if (a.x8.codes)
-            return aligned ? bwd_wide<T, TY, true, false>(a, d, s) : bwd_wide<T, TY, true, true>(a, d, s);
-        return aligned ? bwd_wide<T, TY, false, false>(a, d, s) : bwd_wide<T, TY, false, true>(a, d, s);
+            return aligned ? bwd_narrow<T, TY, true, false>(a, d, s) : bwd_narrow<T, TY, true, true>(a, d, s);
+        return aligned ? bwd_narrow<T, TY, false, false>(a, d, s) : bwd_narrow<T, TY, false, true>(a, d, s);
+    }
+    if (a.cols <= kCtaMaxCols) {
+        unsigned grid;
+        const int rc = launch_norm_bwd_cta(a, aligned, static_cast<int>(cta_parts(a.rows, a.cols)), d, s, &grid);
+        return rc == MX_OK ? join(a, static_cast<int>(grid), s) : rc;
     }
     if (a.dw || a.db) {  // before dx, which may be dy's memory
         const int parts = static_cast<int>(any_parts(a.rows));
@@ -1200,9 +945,9 @@ int64_t norm_bwd_parts(int64_t rows, int64_t cols)
 {
     if (few_rows(rows, cols))
         return 0;
-    if (!wide_cols(cols))
-        return any_parts(rows);
-    return std::max(ctas_of(wide_shape(cols, false), rows), ctas_of(wide_shape(cols, true), rows));
+    if (cols <= kMaxNarrow)
+        return std::max(narrow_parts(rows, cols, false), narrow_parts(rows, cols, true));
+    return cols <= kCtaMaxCols ? cta_parts(rows, cols) : any_parts(rows);
 }
 
 int launch_norm_fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)

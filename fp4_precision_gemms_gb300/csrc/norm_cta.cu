@@ -1,17 +1,23 @@
-// norm_cta.cu -- the norm's kernels for rows of 513 to 8192 columns: the widths
-// of model training.
+// norm_cta.cu -- the norm's kernels for rows of 513 to 16384 columns.
 //
-// A CTA takes a row at a time (forward without a residual: two), two octs
-// (eight columns) a thread, with the weights, the biases and the backward
-// pass's column sums in registers over all of its rows.  One thread copies the
-// rows to come into a ring of shared-memory stages by bulk copies, an mbarrier
-// says when a stage is there, and the row sums' barrier that the stage before it
-// may be filled again.
+// A CTA takes a row at a time (forward without a residual: two), NV octs (eight
+// columns) a thread, with the column sums of the backward pass in registers over
+// all of its rows.  Two octs up to 8192 columns: the weights, the biases and a
+// row's g and h stay in registers too.  Four above: those are read again.  One
+// thread copies the rows to come into a ring of shared-memory stages by bulk
+// copies, an mbarrier says when a stage is there, and the row sums' barrier that
+// the stage before it may be filled again.
 //
 // What bounds them: with the ring the memory system is never idle, and what is
 // left is the number of instructions a row takes.  The options are therefore
 // compile-time and fp32 arithmetic is two-wide; two rows of the forward kernel
-// share one barrier and one exchange per sum.
+// share one barrier and one exchange per sum.  8192x4096 bf16 measured: forward
+// with residual, checkpoint and maximum 55 us (303 MB, 5.5 TB/s; 65536 rows 6.0),
+// backward from the checkpoint with the residual's gradient 45.5 us (236 MB, 5.2
+// TB/s; 65536 rows 6.8), of which the partial sums and their join take 5; layer
+// norm alone at 32768 rows 90 us (537 MB, 5.9 TB/s).  At odd addresses the
+// shifts double the instructions: 8192x4099 fp32 in, bf16 out 88 us, where
+// 8192x4096 takes 34.
 #include <algorithm>
 
 #include "mx_act8.cuh"
@@ -263,7 +269,7 @@ __device__ __forceinline__ float2 cta_sum2(float x, float y, float2* part, bool&
 // ADD: the residual is added; SAVE: the checkpoint is kept; R rows at a time;
 // FULL: every thread's octs lie inside the row (cols a multiple of 512), which
 // saves a tenth of the instructions.
-template <typename T, typename TY, bool ADD, bool SAVE, int R, bool FULL, bool ANY>
+template <typename T, typename TY, bool ADD, bool SAVE, int R, int NV, bool FULL, bool ANY>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -272,7 +278,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
     const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
-    const int own[2] = {FULL ? 8 : min(C - c0, 8), FULL ? 8 : min(C - c0 - dc, 8)};  // values of each oct, <= 0: none
+    constexpr bool KEEP = NV <= 2;
+    int own[NV];  // values of each oct, <= 0: none
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        own[j] = FULL ? 8 : min(C - c0 - j * dc, 8);
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER;
     const int64_t tiles_of_all = (a.rows + R - 1) / R;
@@ -285,9 +295,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
     pipe.layout(smem, stages, a.fail_at, a.rows);
     pipe.start(a.rows, tiles);
 
-    Oct wt[2], bi[2];
+    Oct wt[KEEP ? NV : 1], bi[KEEP ? NV : 1];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < (KEEP ? NV : 0); ++j) {
         params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, wt[j]);
         params<ANY>(a.bias, a.w_dtype, c0 + j * dc, own[j], 0.0f, bi[j]);
     }
@@ -305,13 +315,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
     for (; it < tiles; ++it) {
         bad = !pipe.wait(a.wait_ns);
         const bool two = R == 2 && r + 1 < a.rows;  // the last tile may have one row
-        Oct v[R][2];
+        Oct v[R][NV];
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < NV; ++j) {
                 v[q][j].fill(0.0f);
                 if (own[j] > 0)
                     pipe.template oct<T>(0, q, j, r + q, own[j], v[q][j]);
@@ -348,7 +358,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
 #pragma unroll
             for (int q = 0; q < R; ++q)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < NV; ++j) {
                     uint8_t e;
                     const uint2 codes = encode_oct(v[q][j], e);
                     if ((FULL || c0 + j * dc < G * kAct8Group) && (q == 0 || two)) {
@@ -364,7 +374,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
             const float2 m = both(q == 0 ? -mean.x : -mean.y);
             float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NV; ++j)
                 if (own[j] > 0) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -395,11 +405,15 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
             if (q == 0 || two) {
                 const float2 s = both(q == 0 ? rstd.x : rstd.y);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    Oct y;
+                for (int j = 0; j < NV; ++j) {
+                    Oct y, &w = wt[KEEP ? j : 0], &b = bi[KEEP ? j : 0];
+                    if constexpr (!KEEP) {
+                        params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, w);
+                        params<ANY>(a.bias, a.w_dtype, c0 + j * dc, own[j], 0.0f, b);
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        y.p[k] = __ffma2_rn(__fmul2_rn(v[q][j].p[k], s), wt[j].p[k], bi[j].p[k]);
+                        y.p[k] = __ffma2_rn(__fmul2_rn(v[q][j].p[k], s), w.p[k], b.p[k]);
                     put<ANY>(to_y + q * a.ldy + j * dc, y, own[j], c0 + j * dc, C, top);
                 }
             }
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a
 
 // dx of each row and the CTA's partial sums of dw and db.  FROM8: the kept input
 // is the checkpoint.  ADD: the residual path's gradient joins dx.
-template <typename T, typename TY, bool FROM8, bool ADD, bool FULL, bool ANY>
+template <typename T, typename TY, bool FROM8, bool ADD, int NV, bool FULL, bool ANY>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -431,7 +445,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         part[0][threadIdx.x] = part[1][threadIdx.x] = make_float2(0.0f, 0.0f);
     const int C = static_cast<int>(a.cols), G = (C + kAct8Group - 1) / kAct8Group;
     const int c0 = 8 * threadIdx.x, dc = 8 * blockDim.x;
-    const int own[2] = {FULL ? 8 : min(C - c0, 8), FULL ? 8 : min(C - c0 - dc, 8)};  // values of each oct, <= 0: none
+    constexpr bool KEEP = NV <= 2;
+    int own[NV];  // values of each oct, <= 0: none
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        own[j] = FULL ? 8 : min(C - c0 - j * dc, 8);
     const float inv_c = 1.0f / static_cast<float>(C);
     const bool layer = a.kind == MX_NORM_LAYER;
     const int tiles = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
@@ -447,10 +465,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
     pipe.layout(smem, stages, a.fail_at, a.rows);
     pipe.start(a.rows, tiles);
 
-    Oct wt[2], dw[2], db[2];
+    Oct wt[KEEP ? NV : 1], dw[NV], db[NV];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, wt[j]);
+    for (int j = 0; j < NV; ++j) {
+        if constexpr (KEEP)
+            params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, wt[j]);
         dw[j].fill(0.0f);
         db[j].fill(0.0f);
     }
@@ -459,54 +478,63 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
     T* to_dx = static_cast<T*>(a.dx) + r * a.lddx + c0;
     const int64_t dx_step = step * a.lddx;
     // what a row needs beside its matrices, loaded a row ahead
-    const int last_group = G - 1, g0 = min(c0 / kAct8Group, last_group), g1 = min((c0 + dc) / kAct8Group, last_group);
-    float mean = 0.0f, rstd = a.rstd[r];
-    if (layer)
-        mean = a.mean[r];
-    uint32_t e0 = 127, e1 = 127;
-    if constexpr (FROM8) {
-        e0 = a.x8.sf[r * G + g0];
-        e1 = a.x8.sf[r * G + g1];
-    }
+    float mean = 0.0f, rstd = 0.0f;
+    uint32_t e[NV];
+    auto row_words = [&] {
+        rstd = a.rstd[r];
+        if (layer)
+            mean = a.mean[r];
+        if constexpr (FROM8)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                e[j] = a.x8.sf[r * G + min((c0 + j * dc) / kAct8Group, G - 1)];
+    };
+    row_words();
 
     Top<T> top;
     bool bad = false;
     int it = 0;
     for (; it < tiles; ++it) {
         const float2 m = both(-mean), s = both(rstd);
-        const float2 scale[2] = {both(act8_scale(e0)), both(act8_scale(e1))};
+        float2 scale[NV];
+#pragma unroll
+        for (int j = 0; j < (FROM8 ? NV : 0); ++j)
+            scale[j] = both(act8_scale(e[j]));
         const int64_t row = r;
         r += step;
-        if (it + 1 < tiles) {
-            rstd = a.rstd[r];
-            if (layer)
-                mean = a.mean[r];
-            if constexpr (FROM8) {
-                e0 = a.x8.sf[r * G + g0];
-                e1 = a.x8.sf[r * G + g1];
-            }
-        }
+        if (it + 1 < tiles)
+            row_words();
         bad = !pipe.wait(a.wait_ns);
-        Oct g[2], h[2];
+        // g and h of oct j
+        auto load = [&](int j, Oct& dy, Oct& g, Oct& h) {
+            pipe.template oct<TY>(0, 0, j, row, own[j], dy);
+            if constexpr (FROM8)
+                pipe.codes(1, j, row, h);
+            else
+                pipe.template oct<T>(1, 0, j, row, own[j], h);
+            Oct& w = wt[KEEP ? j : 0];
+            if constexpr (!KEEP)
+                params<ANY>(a.weight, a.w_dtype, c0 + j * dc, own[j], 1.0f, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // the code's product with its scale is exact
+                h.p[k] = FROM8 ? __ffma2_rn(h.p[k], scale[j], m) : __fadd2_rn(h.p[k], m);
+                h.p[k] = __fmul2_rn(h.p[k], s);
+                g.p[k] = __fmul2_rn(dy.p[k], w.p[k]);
+            }
+        };
+        Oct keep_g[KEEP ? NV : 1], keep_h[KEEP ? NV : 1];
         float2 sgh = make_float2(0.0f, 0.0f), sg = sgh;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NV; ++j)
             if (own[j] > 0) {
-                Oct dy;
-                pipe.template oct<TY>(0, 0, j, row, own[j], dy);
-                if constexpr (FROM8)
-                    pipe.codes(1, j, row, h[j]);
-                else
-                    pipe.template oct<T>(1, 0, j, row, own[j], h[j]);
+                Oct dy, &g = keep_g[KEEP ? j : 0], &h = keep_h[KEEP ? j : 0];
+                load(j, dy, g, h);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    // the code's product with its scale is exact
-                    h[j].p[k] = FROM8 ? __ffma2_rn(h[j].p[k], scale[j], m) : __fadd2_rn(h[j].p[k], m);
-                    h[j].p[k] = __fmul2_rn(h[j].p[k], s);
-                    g[j].p[k] = __fmul2_rn(dy.p[k], wt[j].p[k]);
-                    sgh = __ffma2_rn(g[j].p[k], h[j].p[k], sgh);
-                    sg = __fadd2_rn(sg, g[j].p[k]);
-                    dw[j].p[k] = __ffma2_rn(dy.p[k], h[j].p[k], dw[j].p[k]);
+                    sgh = __ffma2_rn(g.p[k], h.p[k], sgh);
+                    sg = __fadd2_rn(sg, g.p[k]);
+                    dw[j].p[k] = __ffma2_rn(dy.p[k], h.p[k], dw[j].p[k]);
                     db[j].p[k] = __fadd2_rn(db[j].p[k], dy.p[k]);
                 }
             }
@@ -517,15 +545,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
             pipe.refill(it - 1, a.rows, tiles, pipe.before());  // nobody reads the row before any more
         const float2 c1 = both(-sums.x * inv_c), c2 = both(layer ? -sums.y * inv_c : 0.0f);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NV; ++j)
             if (ANY || own[j] > 0) {
-                Oct q;
+                Oct dy, q, &g = keep_g[KEEP ? j : 0], &h = keep_h[KEEP ? j : 0];
+                if (!KEEP && own[j] > 0)
+                    load(j, dy, g, h);
                 q.fill(0.0f);
                 if (ADD && own[j] > 0)
                     pipe.template oct<T>(2, 0, j, row, own[j], q);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h[j].p[k], c1, g[j].p[k]), c2), s, q.p[k]);
+                    q.p[k] = __ffma2_rn(__fadd2_rn(__ffma2_rn(h.p[k], c1, g.p[k]), c2), s, q.p[k]);
                 put<ANY>(to_dx + j * dc, q, own[j], c0 + j * dc, C, top);
             }
         to_dx += dx_step;
@@ -546,7 +576,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
     float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C + c0;
     const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NV; ++j) {
         float* const to = out + j * dc;
         if constexpr (ANY) {
 #pragma unroll
@@ -594,7 +624,7 @@ int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned gr
 // or rows at any address.
 enum Rows { kFull, kPart, kAny };
 
-template <typename T, typename TY, bool ADD, bool SAVE, Rows ROWS>
+template <typename T, typename TY, bool ADD, bool SAVE, Rows ROWS, int NV>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     constexpr bool FULL = ROWS == kFull, ANY = ROWS == kAny;
@@ -604,35 +634,39 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     // leave it bound by instructions (32768x4096 bf16: 125 -> 90 us), where every
     // CTA still has several tiles and a ring of three stages fits.  With the
     // addition one row is faster (8192x4096: 42.6 us, 45.9 for two).
-    if constexpr (!ADD && !ANY) {
-        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, FULL, false>;
+    if constexpr (!ADD && !ANY && NV == 2) {
+        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, NV, FULL, false>;
         const int n2 = ctas_per_sm<two>(threads, 2 * row);
         if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
             return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
     }
-    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, FULL, ANY>;
+    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, NV, FULL, ANY>;
     const int n1 = ctas_per_sm<one>(threads, row);
     return launch<one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
 }
-template <typename T, typename TY, Rows ROWS>
+template <typename T, typename TY, Rows ROWS, int NV>
 int fwd_options(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     if (a.residual)
-        return a.save.codes ? fwd<T, TY, true, true, ROWS>(a, d, s) : fwd<T, TY, true, false, ROWS>(a, d, s);
-    return a.save.codes ? fwd<T, TY, false, true, ROWS>(a, d, s) : fwd<T, TY, false, false, ROWS>(a, d, s);
+        return a.save.codes ? fwd<T, TY, true, true, ROWS, NV>(a, d, s) : fwd<T, TY, true, false, ROWS, NV>(a, d, s);
+    return a.save.codes ? fwd<T, TY, false, true, ROWS, NV>(a, d, s) : fwd<T, TY, false, false, ROWS, NV>(a, d, s);
 }
 
+// Above 8192 columns the rows may always end before a thread's octs do (as
+// kPart), which halves the kernels there.
 bool full_rows(int64_t cols) { return cols == 16 * cta_threads(cols); }
 
 template <typename T, typename TY>
 int fwd_rows(const NormFwdArgs& a, bool aligned, const Device& d, cudaStream_t s)
 {
+    if (a.cols > kCtaTwoOcts)
+        return aligned ? fwd_options<T, TY, kPart, 4>(a, d, s) : fwd_options<T, TY, kAny, 4>(a, d, s);
     if (!aligned)
-        return fwd_options<T, TY, kAny>(a, d, s);
-    return full_rows(a.cols) ? fwd_options<T, TY, kFull>(a, d, s) : fwd_options<T, TY, kPart>(a, d, s);
+        return fwd_options<T, TY, kAny, 2>(a, d, s);
+    return full_rows(a.cols) ? fwd_options<T, TY, kFull, 2>(a, d, s) : fwd_options<T, TY, kPart, 2>(a, d, s);
 }
 
-template <typename T, typename TY, bool FROM8, bool ADD, Rows ROWS>
+template <typename T, typename TY, bool FROM8, bool ADD, Rows ROWS, int NV>
 int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     constexpr bool ANY = ROWS == kAny;
@@ -640,25 +674,27 @@ int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigne
     auto room = [&](size_t bytes) { return int64_t{Pipe<2, 1, ANY>::room(static_cast<uint32_t>(a.cols * bytes), ANY)}; };
     const int64_t row =
         room(sizeof(TY)) + (FROM8 ? act8_groups(a.cols) * kAct8Group : room(sizeof(T))) + (ADD ? room(sizeof(T)) : 0);
-    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, ROWS == kFull, ANY>;
+    constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, NV, ROWS == kFull, ANY>;
     const int n = ctas_per_sm<kernel>(threads, row);
     *grid = static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(a.rows, most), int64_t{n} * d.sms));
     return launch<kernel>(a, threads, row, n, *grid, s);
 }
-template <typename T, typename TY, Rows ROWS>
+template <typename T, typename TY, Rows ROWS, int NV>
 int bwd_options(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
     if (a.x8.codes)
-        return a.dres ? bwd<T, TY, true, true, ROWS>(a, most, d, s, grid) : bwd<T, TY, true, false, ROWS>(a, most, d, s, grid);
-    return a.dres ? bwd<T, TY, false, true, ROWS>(a, most, d, s, grid) : bwd<T, TY, false, false, ROWS>(a, most, d, s, grid);
+        return a.dres ? bwd<T, TY, true, true, ROWS, NV>(a, most, d, s, grid) : bwd<T, TY, true, false, ROWS, NV>(a, most, d, s, grid);
+    return a.dres ? bwd<T, TY, false, true, ROWS, NV>(a, most, d, s, grid) : bwd<T, TY, false, false, ROWS, NV>(a, most, d, s, grid);
 }
 template <typename T, typename TY>
 int bwd_rows(const NormBwdArgs& a, bool aligned, int most, const Device& d, cudaStream_t s, unsigned* grid)
 {
+    if (a.cols > kCtaTwoOcts)
+        return aligned ? bwd_options<T, TY, kPart, 4>(a, most, d, s, grid) : bwd_options<T, TY, kAny, 4>(a, most, d, s, grid);
     if (!aligned)
-        return bwd_options<T, TY, kAny>(a, most, d, s, grid);
-    return full_rows(a.cols) ? bwd_options<T, TY, kFull>(a, most, d, s, grid)
-                             : bwd_options<T, TY, kPart>(a, most, d, s, grid);
+        return bwd_options<T, TY, kAny, 2>(a, most, d, s, grid);
+    return full_rows(a.cols) ? bwd_options<T, TY, kFull, 2>(a, most, d, s, grid)
+                             : bwd_options<T, TY, kPart, 2>(a, most, d, s, grid);
 }
 
 }  // namespace

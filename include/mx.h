@@ -486,8 +486,8 @@ void mx_debug_set_quant_impl(int impl);
  * initial value) turns it off.  Nothing faults or hangs. */
 void mx_debug_set_tile_fail_at(int64_t tile);
 
-/* Test hook for the bounded waits of mx_norm_fwd / mx_norm_bwd (rows of more
- * than 512 columns): for later calls made by the calling host thread, the copy
+/* Test hook for the bounded waits of mx_norm_fwd / mx_norm_bwd (rows of 513
+ * to 16384 columns): for later calls made by the calling host thread, the copy
  * of every CTA's row (or pair of rows) number `row`, 0-based in the CTA's own
  * order, is left out and the limit of the waits is 2 ms.  The wait for it runs
  * out; the kernel then waits for its other copies in flight, stops and reports
