@@ -25,7 +25,7 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
     }
 }
 
-// The kernels of norm_cta.cu: columns they take, and a CTA's threads, two octs
+// The kernels of norm_cta_fwd.cu and norm_cta_bwd.cu: columns they take, and a CTA's threads, two octs
 // each up to kCtaTwoOcts columns and four above, whole checkpoint groups.
 constexpr int64_t kCtaMinCols = 513, kCtaTwoOcts = 8192, kCtaMaxCols = 16384;
 inline int cta_threads(int64_t cols)

@@ -1,7 +1,8 @@
 // norm.cu -- layer norm and RMS norm over the rows of a residual stream, forward
 // and backward: the choice of the kernel, the kernels for narrow rows (up to 512
 // columns), for few short rows and for rows above 16384 columns, and the join of
-// the column sums.  The rows between are norm_cta.cu's.
+// the column sums.  The rows between are norm_cta_fwd.cu's and
+// norm_cta_bwd.cu's.
 #include <algorithm>
 
 #include "mx_act8.cuh"
