@@ -25,6 +25,10 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
     }
 }
 
+// Floats from one row of partial sums to the next: rows of any width are written
+// eight columns at a time.
+__host__ __device__ inline int64_t part_stride(int64_t cols) { return (cols + 7) / 8 * 8; }
+
 // The kernels of norm_cta_fwd.cu and norm_cta_bwd.cu: columns they take, and a CTA's threads, two octs
 // each up to kCtaTwoOcts columns and four above, whole checkpoint groups.
 constexpr int64_t kCtaMinCols = 513, kCtaTwoOcts = 8192, kCtaMaxCols = 16384;

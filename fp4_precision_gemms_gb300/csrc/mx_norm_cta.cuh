@@ -232,7 +232,7 @@ template <bool ANY>
 __device__ __forceinline__ void params(const void* p, int dtype, int c, int n, float absent, Oct& o)
 {
     o.fill(0.0f);
-    if constexpr (ANY) {
+    if (ANY && (n < 8 || (reinterpret_cast<uintptr_t>(p) & 15) != 0)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n)

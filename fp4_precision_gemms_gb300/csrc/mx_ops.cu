@@ -3,6 +3,7 @@
 // and the launches.
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
+#include "mx_norm.cuh"
 
 using namespace mx;
 
@@ -176,7 +177,7 @@ size_t mx_norm_bwd_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (check_shape(rows, cols) != MX_OK || empty(rows, cols))
         return 0;
-    return static_cast<size_t>(norm_bwd_parts(rows, cols)) * cols * 2 * sizeof(float);
+    return static_cast<size_t>(norm_bwd_parts(rows, cols) * part_stride(cols)) * 2 * sizeof(float);
 }
 
 int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_t ldx, const mx_act8* x8,

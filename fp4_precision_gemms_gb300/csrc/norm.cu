@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_dw_any_kernel(NormBwdArgs a)
     const int64_t C = a.cols, c = blockIdx.x * 32ll + (threadIdx.x & 31);
     const ColumnSums s = column_sums<T, TY>(a, c, blockIdx.y * kRowWarps, static_cast<int64_t>(gridDim.y) * kRowWarps);
     if (threadIdx.x < 32 && c < C) {
-        a.parts[blockIdx.y * C + c] = s.w;
-        a.parts[(gridDim.y + blockIdx.y) * C + c] = s.b;
+        a.parts[blockIdx.y * part_stride(C) + c] = s.w;
+        a.parts[(gridDim.y + blockIdx.y) * part_stride(C) + c] = s.b;
     }
 }
 
@@ -243,9 +243,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_dw_join_kernel(const flo
         return;
     float v = 0.0f;
     if (c < C) {
-        const float* from = src + (static_cast<int64_t>(blockIdx.y) * parts + warp) * C + c;
+        const int64_t stride = part_stride(C);
+        const float* from = src + (static_cast<int64_t>(blockIdx.y) * parts + warp) * stride + c;
 #pragma unroll 8
-        for (int i = warp; i < parts; i += kJoinWarps, from += kJoinWarps * C)
+        for (int i = warp; i < parts; i += kJoinWarps, from += kJoinWarps * stride)
             v += *from;
     }
     p[warp][lane] = v;
@@ -732,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_bwd_narrow_kernel(NormBwdArg
         flush_top(a.amax, top);
     if (!a.dw && !a.db)
         return;
-    float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C;
-    const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
+    float* const out = a.parts + blockIdx.x * part_stride(C);
+    const int64_t to_db = gridDim.x * part_stride(C);
     constexpr int kWarpCols = NV * LPR * 8;
     float* const red = reinterpret_cast<float*>(smem);
 #pragma unroll

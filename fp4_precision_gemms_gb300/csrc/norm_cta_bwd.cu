@@ -144,19 +144,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
         flush_top(a.amax, top);
     if (!a.dw && !a.db)
         return;
-    float* const out = a.parts + static_cast<int64_t>(blockIdx.x) * C + c0;
-    const int64_t to_db = static_cast<int64_t>(gridDim.x) * C;
+    float* const out = a.parts + blockIdx.x * part_stride(C) + c0;
+    const int64_t to_db = gridDim.x * part_stride(C);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        float* const to = out + j * dc;
-        if constexpr (ANY) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < own[j]) {
-                    to[i] = dw[j][i];
-                    to[to_db + i] = db[j][i];
-                }
-        } else if (own[j] > 0) {
+    for (int j = 0; j < NV; ++j)
+        if (own[j] > 0) {  // zeros past the row's end, up to the stride
+            float* const to = out + j * dc;
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
                 *reinterpret_cast<float4*>(to + 2 * k) =
@@ -165,7 +158,6 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_cta_kernel(NormBwdArgs a
                     make_float4(db[j].p[k].x, db[j].p[k].y, db[j].p[k + 1].x, db[j].p[k + 1].y);
             }
         }
-    }
 }
 
 template <typename T, typename TY, bool FROM8, bool ADD, Rows ROWS, int NV>
