@@ -6,7 +6,9 @@ namespace {
 
 // ADD: the residual is added; SAVE: the checkpoint is kept; R rows at a time;
 // FULL: every thread's octs lie inside the row (cols a multiple of 512), which
-// saves a tenth of the instructions.
+// saves a tenth of the instructions.  The mean is summed first and the variance
+// around it, from the values in registers: a second barrier, but no cancellation.
+// Figures stand in mx_norm_cta.cuh.
 template <typename T, typename TY, bool ADD, bool SAVE, int R, int NV, bool FULL, bool ANY>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
 {
