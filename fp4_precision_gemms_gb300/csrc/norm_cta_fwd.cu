@@ -9,8 +9,22 @@ namespace {
 // saves a tenth of the instructions.  The mean is summed first and the variance
 // around it, from the values in registers: a second barrier, but no cancellation.
 // Figures stand in mx_norm_cta.cuh.
+// Registers: 96 a thread, by a bound of 640 threads, for rows at any address, for a
+// sum that is also saved in 8 bits and for one row at a time without a residual;
+// 128 elsewhere.  Two CTAs of 257 to 341 threads then lie on an SM in place of one,
+// and at other sizes the tighter schedule is the faster one but at 8192 columns.
+// 8192 rows, 128 against 96: saved bf16 sum of 4096 columns 55.5 and 51.8 us, 5120
+// 70 and 64, fp32 4099 columns 88 and 62; 4096 rows of 8193 96 and 71, but the saved
+// sum of 8192 51 and 56.  The sum alone and two rows at a time lose (43 and 46, 34
+// and 42).
+constexpr int fwd_bound(bool add, bool save, int r, int nv, bool any)
+{
+    return any || (nv == 2 && r == 1 && (save || !add)) ? 640 : kMaxThreads;
+}
+
 template <typename T, typename TY, bool ADD, bool SAVE, int R, int NV, bool FULL, bool ANY>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
+__global__ void __launch_bounds__(fwd_bound(ADD, SAVE, R, NV, ANY))
+    norm_fwd_cta_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float2 part[2][kWarps];
@@ -179,18 +193,20 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     constexpr bool FULL = ROWS == kFull, ANY = ROWS == kAny;
     const int threads = cta_threads(a.cols);
     const int64_t row = int64_t{Pipe<1, 1, ANY>::room(static_cast<uint32_t>(a.cols * sizeof(T)), ANY)} * (ADD ? 2 : 1);
+    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, NV, FULL, ANY>;
+    const int n1 = ctas_per_sm<one>(threads, row);
     // Two rows at a time for the norm without a residual, whose few bytes a row
     // leave it bound by instructions (32768x4096 bf16: 125 -> 90 us), where every
-    // CTA still has several tiles and a ring of three stages fits.  With the
-    // addition one row is faster (8192x4096: 42.6 us, 45.9 for two).
+    // CTA still has several tiles and a ring of three stages fits, unless that
+    // leaves an SM one CTA where one row leaves it two (257 to 341 threads; 8192x5120
+    // 38.0 us and 35.8, with the checkpoint 53.3 and 46.8).  With the addition one
+    // row is faster (8192x4096: 42.6 us, 45.9 for two).
     if constexpr (!ADD && !ANY && NV == 2) {
         constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, NV, FULL, false>;
         const int n2 = ctas_per_sm<two>(threads, 2 * row);
-        if (a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
+        if ((n2 > 1 || n1 == 1) && a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
             return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
     }
-    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, NV, FULL, ANY>;
-    const int n1 = ctas_per_sm<one>(threads, row);
     return launch<one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
 }
 template <typename T, typename TY, Rows ROWS, int NV>
