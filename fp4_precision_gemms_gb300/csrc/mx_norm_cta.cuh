@@ -17,7 +17,7 @@
 // backward from the checkpoint with the residual's gradient 45.5 us (236 MB, 5.2
 // TB/s; 65536 rows 6.8), of which the partial sums and their join take 5; layer
 // norm alone at 32768 rows 90 us (537 MB, 5.9 TB/s).  At odd addresses the
-// shifts double the instructions: 8192x4099 fp32 in, bf16 out 62 us, where
+// shifts double the instructions: 8192x4099 fp32 in, bf16 out 61 us, where
 // 8192x4096 takes 34.
 #pragma once
 #include <algorithm>

@@ -9,22 +9,10 @@ namespace {
 // saves a tenth of the instructions.  The mean is summed first and the variance
 // around it, from the values in registers: a second barrier, but no cancellation.
 // Figures stand in mx_norm_cta.cuh.
-// Registers: 96 a thread, by a bound of 640 threads, for rows at any address, for a
-// sum that is also saved in 8 bits and for one row at a time without a residual;
-// 128 elsewhere.  Two CTAs of 257 to 341 threads then lie on an SM in place of one,
-// and at other sizes the tighter schedule is the faster one but at 8192 columns.
-// 8192 rows, 128 against 96: saved bf16 sum of 4096 columns 55.5 and 51.8 us, 5120
-// 70 and 64, fp32 4099 columns 88 and 62; 4096 rows of 8193 96 and 71, but the saved
-// sum of 8192 51 and 56.  The sum alone and two rows at a time lose (43 and 46, 34
-// and 42).
-constexpr int fwd_bound(bool add, bool save, int r, int nv, bool any)
-{
-    return any || (nv == 2 && r == 1 && (save || !add)) ? 640 : kMaxThreads;
-}
-
-template <typename T, typename TY, bool ADD, bool SAVE, int R, int NV, bool FULL, bool ANY>
-__global__ void __launch_bounds__(fwd_bound(ADD, SAVE, R, NV, ANY))
-    norm_fwd_cta_kernel(NormFwdArgs a, int stages)
+// BOUND: the threads that the compiler limits registers for, 512: 128 a thread, 544
+// to 640: 96.
+template <typename T, typename TY, bool ADD, bool SAVE, int R, int NV, bool FULL, bool ANY, int BOUND>
+__global__ void __launch_bounds__(BOUND) norm_fwd_cta_kernel(NormFwdArgs a, int stages)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float2 part[2][kWarps];
@@ -187,13 +175,37 @@ __global__ void __launch_bounds__(fwd_bound(ADD, SAVE, R, NV, ANY))
         flush_top(a.amax, top);
 }
 
+template <auto KERNEL>
+int fwd_one(const NormFwdArgs& a, int threads, int64_t row, int n, const Device& d, cudaStream_t s)
+{
+    return launch<KERNEL>(a, threads, row, n, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n} * d.sms)), s);
+}
+
+// Registers.  Where 96 a thread leave an SM two CTAs, up to 341 threads, a sum that
+// is also saved takes 96 and above 128; the sum alone takes 128 up to there and 96
+// above.  The CTAs' number is not all: the compiler's schedule is another one, as it
+// is between bounds of 576 and 640, which allow the same 96 (saved sum 8192x4096 50.2
+// and 51.7 us, but 65536x4096 396 and 365; sum alone 4096x8192 43.5 and 45).  Measured over 2^25 bf16 values,
+// columns: us at 128 | 96 registers:
+//   saved sum     768: 92 | 70   4096: 54.9 | 51.7   5120: 58 | 52   8192: 50.9 | 56.6
+//   sum alone     768: 47 | 51   4096: 43.3 | 46.9   5120: 46 | 48   8192: 47 | 43.5
+// Rows at any address take 96 (2^24 values fp32, 2049 columns 34 | 31, 4099 48 | 34,
+// 8191 33.7 | 34.2; bf16 8193 columns 96 | 71), one row at a time without a residual
+// too, for the second CTA; two rows take 128 (8192x4096 34, at 96 42).
 template <typename T, typename TY, bool ADD, bool SAVE, Rows ROWS, int NV>
 int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
 {
     constexpr bool FULL = ROWS == kFull, ANY = ROWS == kAny;
+    constexpr int tight = ANY || (ADD && !SAVE && NV == 2) ? 576 : NV == 2 ? 640 : kMaxThreads;
     const int threads = cta_threads(a.cols);
     const int64_t row = int64_t{Pipe<1, 1, ANY>::room(static_cast<uint32_t>(a.cols * sizeof(T)), ANY)} * (ADD ? 2 : 1);
-    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, NV, FULL, ANY>;
+    if constexpr (ADD && !ANY && NV == 2) {
+        if (SAVE != (threads <= 65536 / (2 * 96))) {
+            constexpr auto loose = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, NV, FULL, false, kMaxThreads>;
+            return fwd_one<loose>(a, threads, row, ctas_per_sm<loose>(threads, row), d, s);
+        }
+    }
+    constexpr auto one = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 1, NV, FULL, ANY, tight>;
     const int n1 = ctas_per_sm<one>(threads, row);
     // Two rows at a time for the norm without a residual, whose few bytes a row
     // leave it bound by instructions (32768x4096 bf16: 125 -> 90 us), where every
@@ -202,12 +214,12 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
     // 38.0 us and 35.8, with the checkpoint 53.3 and 46.8).  With the addition one
     // row is faster (8192x4096: 42.6 us, 45.9 for two).
     if constexpr (!ADD && !ANY && NV == 2) {
-        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, NV, FULL, false>;
+        constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, NV, FULL, false, kMaxThreads>;
         const int n2 = ctas_per_sm<two>(threads, 2 * row);
         if ((n2 > 1 || n1 == 1) && a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
             return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
     }
-    return launch<one>(a, threads, row, n1, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n1} * d.sms)), s);
+    return fwd_one<one>(a, threads, row, n1, d, s);
 }
 template <typename T, typename TY, Rows ROWS, int NV>
 int fwd_options(const NormFwdArgs& a, const Device& d, cudaStream_t s)
