@@ -1,5 +1,7 @@
 // mx_norm.cuh -- what the norm's translation units share.
 #pragma once
+#include <atomic>
+
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
 
@@ -28,6 +30,31 @@ __device__ __forceinline__ void param_oct(const void* p, int dtype, int c, float
 // Floats from one row of partial sums to the next: rows of any width are written
 // eight columns at a time.
 __host__ __device__ inline int64_t part_stride(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+// The rings of rows in flight: bytes of an SM's shared memory that they take, all
+// its CTAs together, and the words beside one.
+constexpr int64_t kRingBytes = 220 * 1024;
+constexpr int kRingExtra = 64;
+
+// Lets KERNEL be launched with `bytes` of dynamic shared memory.  The limit is one
+// of the kernel, not of the launch, and other host threads launch it with rings of
+// other sizes: it is set once on a device, to the most that a ring can be.  Two
+// threads that both come first set the same value.
+template <auto KERNEL>
+int allow_ring(size_t bytes, const Device& d)
+{
+    static std::atomic<uint64_t> set{0};  // a bit for each of the first 64 devices
+    const uint64_t bit = d.id < 64 ? uint64_t{1} << d.id : 0;
+    if (bytes <= 40 * 1024 || (set.load(std::memory_order_acquire) & bit))  // 48 KiB without asking, static words included
+        return MX_OK;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes) + kRingExtra) !=
+        cudaSuccess) {
+        (void)cudaGetLastError();
+        return MX_ERR_CUDA;
+    }
+    set.fetch_or(bit, std::memory_order_release);
+    return MX_OK;
+}
 
 // The kernels of norm_cta_fwd.cu and norm_cta_bwd.cu: columns they take, and a CTA's threads, two octs
 // each up to kCtaTwoOcts columns and four above, whole checkpoint groups.

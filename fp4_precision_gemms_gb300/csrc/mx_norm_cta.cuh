@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kMaxThreads = 512;  // 128 registers each
 constexpr int kMaxStages = 6;
-constexpr int kBarBytes = 64;
+constexpr int kBarBytes = kRingExtra;
 constexpr int kWarps = kMaxThreads / 32;
 
 // The ring: PARTS matrices, R rows of each in a stage.  ANY: rows at any address,
@@ -268,8 +268,6 @@ __device__ __forceinline__ float2 cta_sum2(float x, float y, float2* part, bool&
     return sum;
 }
 
-constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
-
 // CTAs an SM that registers allow, with at least two stages each where that can be.
 template <auto KERNEL>
 int ctas_per_sm(int threads, int64_t stage_bytes)
@@ -280,14 +278,13 @@ int ctas_per_sm(int threads, int64_t stage_bytes)
     return n;
 }
 template <auto KERNEL, typename A>
-int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned grid, cudaStream_t s)
+int launch(const A& a, int threads, int64_t stage_bytes, int per_sm, unsigned grid, const Device& d, cudaStream_t s)
 {
     const int stages =
         static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxStages, kRingBytes / (per_sm * stage_bytes))));
     const size_t smem = static_cast<size_t>(stage_bytes) * stages + kBarBytes;
-    if (smem > 40 * 1024 &&  // 48 KiB without asking, the kernels' static words included
-        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return MX_ERR_CUDA;
+    if (const int rc = allow_ring<KERNEL>(smem, d); rc != MX_OK)
+        return rc;
     return launch_kernel(KERNEL, grid, 1, threads, smem, a.amax != nullptr, s, a, stages);
 }
 

@@ -794,7 +794,6 @@ bool wide_rows(const void* p, int64_t ld, int bytes)
 // Launches a ring kernel: up to three rows in flight for each of the CTAs that
 // an SM holds, a grid that fills the GPU or covers the rows, with at most `most`
 // CTAs.  *grid returns it.
-constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory, all its CTAs together
 template <auto KERNEL, typename A>
 int launch_narrow(const A& a, const NarrowShape& w, int64_t stage_bytes, size_t least_smem, int64_t most, unsigned* grid,
                   const Device& d, cudaStream_t s)
@@ -806,9 +805,8 @@ int launch_narrow(const A& a, const NarrowShape& w, int64_t stage_bytes, size_t 
     const int64_t per_cta = kThreads / w.lpr, ctas = (a.rows + per_cta - 1) / per_cta;
     *grid = static_cast<unsigned>(std::min(most, std::min<int64_t>(ctas, int64_t{d.sms} * per_sm)));
     const size_t smem = std::max(static_cast<size_t>(stage_bytes) * stages, least_smem);
-    if (smem > 40 * 1024 &&  // 48 KiB without asking
-        cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return MX_ERR_CUDA;
+    if (const int rc = allow_ring<KERNEL>(smem, d); rc != MX_OK)
+        return rc;
     return launch_kernel(KERNEL, *grid, 1, kThreads, smem, a.amax != nullptr, s, a, stages);
 }
 

@@ -171,7 +171,7 @@ int bwd(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigne
     constexpr auto kernel = norm_bwd_cta_kernel<T, TY, FROM8, ADD, NV, ROWS == kFull, ANY>;
     const int n = ctas_per_sm<kernel>(threads, row);
     *grid = static_cast<unsigned>(std::min<int64_t>(std::min<int64_t>(a.rows, most), int64_t{n} * d.sms));
-    return launch<kernel>(a, threads, row, n, *grid, s);
+    return launch<kernel>(a, threads, row, n, *grid, d, s);
 }
 template <typename T, typename TY, Rows ROWS, int NV>
 int bwd_options(const NormBwdArgs& a, int most, const Device& d, cudaStream_t s, unsigned* grid)

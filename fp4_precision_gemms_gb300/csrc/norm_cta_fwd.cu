@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(BOUND) norm_fwd_cta_kernel(NormFwdArgs a, int 
 template <auto KERNEL>
 int fwd_one(const NormFwdArgs& a, int threads, int64_t row, int n, const Device& d, cudaStream_t s)
 {
-    return launch<KERNEL>(a, threads, row, n, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n} * d.sms)), s);
+    return launch<KERNEL>(a, threads, row, n, static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{n} * d.sms)), d, s);
 }
 
 // Registers.  Where 96 a thread leave an SM two CTAs, up to 341 threads, a sum that
@@ -217,7 +217,7 @@ int fwd(const NormFwdArgs& a, const Device& d, cudaStream_t s)
         constexpr auto two = norm_fwd_cta_kernel<T, TY, ADD, SAVE, 2, NV, FULL, false, kMaxThreads>;
         const int n2 = ctas_per_sm<two>(threads, 2 * row);
         if ((n2 > 1 || n1 == 1) && a.rows >= 4ll * n2 * d.sms && n2 * 3 * 2 * row <= kRingBytes)
-            return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), s);
+            return launch<two>(a, threads, 2 * row, n2, static_cast<unsigned>(n2 * d.sms), d, s);
     }
     return fwd_one<one>(a, threads, row, n1, d, s);
 }
