@@ -465,8 +465,15 @@ def linear_bwd_saved(dY: torch.Tensor, saved: torch.Tensor, Kin: int, fmt: str,
 
 
 # ---------------------------------------------------------------- norm, activation, 8-bit checkpoints
-_device_index = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream  # (device index) -> cudaStream_t of its current stream
+def _cuda_calls(c):
+    """(() -> the current device's index, (device index) -> cudaStream_t of its current
+    stream) by torch's own short cuts in module c, or in public calls where it has none:
+    those need CUDA only when they are made, so a torch without it can import this."""
+    return (getattr(c, "_cuda_getDevice", torch.cuda.current_device),
+            getattr(c, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream))
+
+
+_device_index, _raw_stream = _cuda_calls(torch._C)
 _U8, _F32 = torch.uint8, torch.float32
 
 NORMS = {"layer": 0, "rms": 1}
