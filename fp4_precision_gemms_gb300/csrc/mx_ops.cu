@@ -5,6 +5,8 @@
 #include "mx_internal.cuh"
 #include "mx_norm.cuh"
 
+#include <initializer_list>
+
 using namespace mx;
 
 namespace {
@@ -63,6 +65,30 @@ struct Checks {
     Checks& require(bool ok) { return (*this)(ok ? MX_OK : MX_ERR_INVALID_ARG); }
     Checks& words(const void* p) { return (*this)(aligned(p, 4) ? MX_OK : MX_ERR_ALIGNMENT); }
 };
+
+// A call's vectors: none that it writes overlaps another that it writes or reads.
+// The kernels read weights and statistics while, or after, other CTAs write these.
+struct Vector {
+    const void* p;
+    int64_t bytes;
+    bool overlaps(const Vector& v) const
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(v.p);
+        return p && v.p && a < b + v.bytes && b < a + bytes;
+    }
+};
+int check_apart(std::initializer_list<Vector> written, std::initializer_list<Vector> read)
+{
+    for (const Vector* w = written.begin(); w != written.end(); ++w) {
+        for (const Vector* v = w + 1; v != written.end(); ++v)
+            if (w->overlaps(*v))
+                return MX_ERR_INVALID_ARG;
+        for (const Vector& v : read)
+            if (w->overlaps(v))
+                return MX_ERR_INVALID_ARG;
+    }
+    return MX_OK;
+}
 
 int zero(void* p, size_t bytes, cudaStream_t s)
 {
@@ -142,6 +168,10 @@ int mx_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, i
     Device d;
     if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
         return ok.rc;
+    const int64_t param = cols * dtype_bytes(w_dtype), stat = rows * static_cast<int64_t>(sizeof(float));
+    if (ok(check_apart({{kind == MX_NORM_LAYER ? mean : nullptr, stat}, {rstd, stat}, {amax_out, sizeof(float)}},
+                       {{weight, param}, {bias, param}})).rc != MX_OK)
+        return ok.rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (empty(rows, cols))
         return zero(amax_out, sizeof(float), s);
@@ -209,6 +239,11 @@ int mx_norm_bwd(const void* dy, int64_t ldy, int dy_dtype, const void* x, int64_
     }
     Device d;
     if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
+        return ok.rc;
+    const int64_t stat = rows * static_cast<int64_t>(sizeof(float)), grad = cols * static_cast<int64_t>(sizeof(float));
+    if (ok(check_apart({{dw, grad}, {db, grad}, {amax_out, sizeof(float)}},
+                       {{weight, cols * dtype_bytes(w_dtype)}, {kind == MX_NORM_LAYER ? mean : nullptr, stat}, {rstd, stat}}))
+            .rc != MX_OK)
         return ok.rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (empty(rows, cols))

@@ -351,8 +351,11 @@ int mx_linear_bwd_saved(const void* dY, int64_t T, int64_t Kin, int64_t Nout, in
  *     mx_out_dtype values.
  *   - Any rows >= 0 and 0 <= cols <= 2^30.  A call on an empty matrix
  *     launches no kernel; it zeroes amax_out, dw and db where given.
- *   - An output may be the same memory as an input of the same shape, element
- *     size and row stride; any other overlap is the caller's error.
+ *   - A matrix output may be the same memory as a matrix input of the same
+ *     shape, element size and row stride.  The vectors that a call writes
+ *     (mean, rstd, dw, db, amax_out) overlap neither one another nor the
+ *     vectors that it reads (weight, bias, mean, rstd): MX_ERR_INVALID_ARG.
+ *     Any other overlap is the caller's error.
  *   - Infinities and NaN propagate as the formulas give them.
  *   - Sums, statistics and the gradients' reductions are fp32; results are
  *     rounded once, to nearest even.  The same call on the same inputs gives
@@ -360,8 +363,8 @@ int mx_linear_bwd_saved(const void* dY, int64_t T, int64_t Kin, int64_t Nout, in
  *   - amax_out (optional, one device float) receives max |value| over the
  *     call's output as written, NaN if any is NaN: the amax_in / x_amax /
  *     dy_amax of the quantization that follows.
- *   - Argument errors come before MX_ERR_NO_DEVICE / MX_ERR_UNSUPPORTED for
- *     the device: MX_ERR_INVALID_ARG for a null pointer, a bad enum or shape,
+ *   - Argument errors, all but overlapping vectors, come before
+ *     MX_ERR_NO_DEVICE / MX_ERR_UNSUPPORTED for the device: MX_ERR_INVALID_ARG for a null pointer, a bad enum or shape,
  *     MX_ERR_ALIGNMENT for a misaligned pointer, MX_ERR_UNSUPPORTED for a
  *     combination of types that has no kernel.
  *   - The calls allocate nothing and may be captured into a CUDA graph. */
