@@ -16,19 +16,35 @@ struct ValueSlope {
     float value, slope;
 };
 
-// exp(x).  FAST (results that are rounded to bf16): the approximate exponential,
-// off by a few 2^-22 for the arguments that matter and below 2^-16 for all,
-// which disappears in the 2^-9 of that rounding.
+// FAST: results that are rounded to bf16.
+//
+// exp(x), x <= 0: the approximate exponential is off by 2 + 1.2 |x| last places,
+// so by 2^-22 of the result for the arguments that matter and below 2^-16 for all.
 template <bool FAST>
 __device__ __forceinline__ float exponential(float x)
 {
     return FAST ? __expf(x) : expf(x);
 }
-// 1 / (1 + exp(-z)); the division is within 2 last places.
+// 1 / d for 1 <= d <= 8: within 2 last places, or to nearest.
 template <bool FAST>
-__device__ __forceinline__ float logistic(float z)
+__device__ __forceinline__ float reciprocal(float d)
 {
-    return __fdividef(1.0f, 1.0f + exponential<FAST>(-z));
+    return FAST ? __fdividef(1.0f, d) : 1.0f / d;
+}
+
+// p = 1 / (1 + exp(-t)) and its slope q = p (1 - p).  From exp(-|t|) nothing
+// overflows, and p keeps its precision down to the last subnormal exponential (t =
+// -103).  Nor does anything cancel in q = e r^2; FAST takes p (1 - p), off by 2^-24
+// where q is small beside p, for 3 us of the backward pass of 8192x14336.
+struct Logistic {
+    float p, q;
+};
+template <bool FAST>
+__device__ __forceinline__ Logistic logistic(float t)
+{
+    const float e = exponential<FAST>(-fabsf(t)), r = reciprocal<FAST>(1.0f + e), er = e * r;
+    const float p = t < 0.0f ? er : r;
+    return {p, FAST ? p * (1.0f - p) : er * r};
 }
 
 struct NormalTail {
@@ -73,30 +89,33 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ ValueSlope activate(float z)
 {
     if constexpr (ACT == MX_ACT_SILU) {
-        const float p = logistic<FAST>(z);
-        return {z * p, p + z * p * (1.0f - p)};
+        const Logistic f = logistic<FAST>(z);
+        return {z * f.p, f.p + z * f.q};
     } else if constexpr (ACT == MX_ACT_GELU) {
         const NormalTail n = normal_tail<FAST>(fabsf(z));
         const float p = z > 0.0f ? 1.0f - n.tail : n.tail;
         return {z * p, p + z * (0.39894228040143268f * n.gauss)};
     } else {  // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t))
         constexpr float k = 0.79788456080286536f;
-        const float zz = z * z, p = logistic<FAST>(2.0f * k * (z + 0.044715f * z * zz));
-        const float q = p * (1.0f - p);  // 0 where z^2 may have overflowed: the slope is p there
-        return {z * p, q == 0.0f ? p : p + z * q * (2.0f * k) * (1.0f + 0.134145f * zz)};
+        const float zz = z * z;
+        const Logistic f = logistic<FAST>(2.0f * k * (z + 0.044715f * z * zz));
+        // q is 0 where z^2 may have overflowed: the slope is p there
+        return {z * f.p, f.q == 0.0f ? f.p : f.p + z * f.q * (2.0f * k) * (1.0f + 0.134145f * zz)};
     }
 }
 
 // A unit is eight columns of a row, a row has 4 G units (whole groups, so that
 // the four lanes of a group always work together; those past the row's end hold
 // zeros).  A thread keeps units_in_flight() units' loads in flight, and a grid of
-// kFwdCtas, kBwdCtas or k8Ctas CTAs an SM strides over the units; 8192x14336 bf16
-// gated from or with checkpoints measured, in us, at 3 / 4 / 5 / 8 CTAs: forward
-// 158 / 150 / 160 / 159, backward 175 / 159 / 147 / 168; 4096x11008 saved and
-// restored 50 / 46 / 44 / 42.  One unit in place of two: 169, 162 and 55, but at
+// kFwdCtas, kBwdCtas (from the kept inputs), kBwd8Ctas (from checkpoints) or k8Ctas
+// CTAs an SM strides over the units, or as many as registers allow.  8192x14336
+// bf16 gated SiLU measured, in us, at 3 / 4 / 5 / 6 CTAs: forward with checkpoints
+// 161 / 150 and no more fit, backward 194 / 179 / 181 / 187 from the kept inputs
+// (GELU 215 / 196 / 185 / 185), 179 / 163 / 151 / 148 from checkpoints; 4096x11008
+// saved and restored at 3 / 4 / 5 / 8 50 / 46 / 44 / 42.  One unit in place of two: 169, 162 and 55, but at
 // any address, where the shifts take the registers, 1023x11009 fp32 49 -> 40.  ANY: rows of any address and length; else
 // they start on 16-byte boundaries and their length is a multiple of eight.
-constexpr int kFwdCtas = 4, kBwdCtas = 5, k8Ctas = 8;
+constexpr int kFwdCtas = 4, kBwdCtas = 5, kBwd8Ctas = 6, k8Ctas = 8;
 __host__ __device__ constexpr int units_in_flight(bool any) { return any ? 1 : 2; }
 
 struct UnitMap {
@@ -203,9 +222,9 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 }
 
 // h = a(gate) up, the checkpoints of both inputs and the maximum from one reading.
-// Bound by DRAM: 8192x14336 bf16 SiLU with checkpoints 150 us (946 MB, 6.3 TB/s,
-// 63 % of the issue slots); GELU 181 us, where the instructions show; fp32 279 us
-// (1651 MB, 5.9 TB/s); 14335 columns 233 us.
+// Bound by DRAM: 8192x14336 bf16 SiLU with checkpoints 150 us (946 MB, 6.3 TB/s);
+// GELU 181 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
+// columns 243 us.
 template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 {
@@ -248,8 +267,8 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 }
 
 // dgate = dh up a'(gate), dup = dh a(gate): one exponential gives value and slope.
-// Bound by DRAM: 8192x14336 bf16 SiLU from checkpoints 147 us (946 MB, 6.4 TB/s),
-// from the kept inputs 182 us (1175 MB, 6.5 TB/s); GELU 179 us.
+// Bound by DRAM: 8192x14336 bf16 SiLU from checkpoints 148 us (946 MB, 6.4 TB/s),
+// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 179 us.
 template <typename T, int ACT, bool GATED, bool FROM8, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
 {
@@ -448,13 +467,13 @@ int bwd(const ActArgs& a, const Device& d, cudaStream_t s)
         b.up8 = ahead(a.up8, r, a.cols);
         const UnitMap m = unit_map(b.rows, a.cols);
         if (aligned && a.gated)
-            rc = launch_units<act_bwd_kernel<T, ACT, true, FROM8, false>>(m, !aligned, kBwdCtas, early, d, s, b);
+            rc = launch_units<act_bwd_kernel<T, ACT, true, FROM8, false>>(m, !aligned, FROM8 ? kBwd8Ctas : kBwdCtas, early, d, s, b);
         else if (aligned)
-            rc = launch_units<act_bwd_kernel<T, ACT, false, FROM8, false>>(m, !aligned, kBwdCtas, early, d, s, b);
+            rc = launch_units<act_bwd_kernel<T, ACT, false, FROM8, false>>(m, !aligned, FROM8 ? kBwd8Ctas : kBwdCtas, early, d, s, b);
         else if (a.gated)
-            rc = launch_units<act_bwd_kernel<T, ACT, true, FROM8, true>>(m, !aligned, kBwdCtas, early, d, s, b);
+            rc = launch_units<act_bwd_kernel<T, ACT, true, FROM8, true>>(m, !aligned, FROM8 ? kBwd8Ctas : kBwdCtas, early, d, s, b);
         else
-            rc = launch_units<act_bwd_kernel<T, ACT, false, FROM8, true>>(m, !aligned, kBwdCtas, early, d, s, b);
+            rc = launch_units<act_bwd_kernel<T, ACT, false, FROM8, true>>(m, !aligned, FROM8 ? kBwd8Ctas : kBwdCtas, early, d, s, b);
         if (rc != MX_OK)
             return rc;
     }

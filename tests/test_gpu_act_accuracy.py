@@ -1,0 +1,57 @@
+"""The activation's arithmetic where a coarser one shows: the far negative side,
+where the value is small but a normal number, and the slopes' zeros, where two
+terms cancel.
+
+Bounds: u = 2^-24.  CUDA's expf is within 1 last place (2 u), __expf within 2 +
+1.173 |x| of them, an fp32 division within u, the approximate one within 2 last
+places (4 u); each sum and product adds u, each subnormal intermediate 2^-149 at
+most."""
+import pytest
+import torch
+
+import ops_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = ref.U
+
+
+@pytest.fixture(scope="module")
+def mx():
+    import fp4_precision_gemms_gb300 as m
+    m.build()
+    return m
+
+
+def _half_place(v, dtype):
+    """Half a last place of v in dtype."""
+    bits = 8 if dtype is BF else 24
+    _, ex = torch.frexp(v.abs())
+    return torch.exp2((ex - bits - 1).double()).clamp_min(2.0 ** (-134 if dtype is BF else -150))
+
+
+def _both(mx, z, act):
+    dz, _ = mx.act_bwd(torch.ones_like(z), z, act=act)
+    return mx.act_fwd(z, act=act).h, dz
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_where_the_exponential_leaves_the_normal_numbers(mx, act, dtype):
+    """p = e / (1 + e), e = exp(-t), t to beyond the last subnormal e (t = 104): e's own
+    error and that of t (up to 6 u t: five operations of tanh GELU's argument, none of
+    SiLU's), 4 u after it."""
+    lo, hi = (-106.0, -80.0) if act == "silu" else (-10.9, -9.3)
+    z = torch.linspace(lo, hi, 4096, device="cuda").to(dtype).view(1, -1)
+    h, dz = _both(mx, z, act)
+    a, s, p, t = ref.activation(z, act)
+    t = t.abs()
+    e = 2 * (2 + 1.173 * t) * U if dtype is BF else 2 * U + 0 * t
+    rel = torch.expm1(e + (6 * t * U if act == "gelu_tanh" else 0) + 8 * U)
+    zd, tiny = z.double().abs(), 2.0 ** -147
+    ref.assert_within(h, a, a.abs() * rel + zd * tiny + _half_place(a, dtype), "value")
+    inner = zd * (2 * ref.K_TANH * (1 + 3 * ref.C_TANH * zd ** 2) if act == "gelu_tanh" else 1.0)
+    ref.assert_within(dz, s, (p + inner * p) * (rel + 4 * U) + (1 + inner) * tiny + _half_place(s, dtype), "slope")
+    normal = a.abs() > 2.0 ** -126
+    assert normal.any() and (h[normal] != 0).all()
