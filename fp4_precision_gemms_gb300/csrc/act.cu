@@ -33,18 +33,16 @@ __device__ __forceinline__ float reciprocal(float d)
 }
 
 // p = 1 / (1 + exp(-t)) and its slope q = p (1 - p).  From exp(-|t|) nothing
-// overflows, and p keeps its precision down to the last subnormal exponential (t =
-// -103).  Nor does anything cancel in q = e r^2; FAST takes p (1 - p), off by 2^-24
-// where q is small beside p, for 3 us of the backward pass of 8192x14336.
+// overflows, and the smaller of p and 1 - p keeps its precision down to the last
+// subnormal exponential (|t| = 103); from that one nothing cancels in q.
 struct Logistic {
     float p, q;
 };
 template <bool FAST>
 __device__ __forceinline__ Logistic logistic(float t)
 {
-    const float e = exponential<FAST>(-fabsf(t)), r = reciprocal<FAST>(1.0f + e), er = e * r;
-    const float p = t < 0.0f ? er : r;
-    return {p, FAST ? p * (1.0f - p) : er * r};
+    const float e = exponential<FAST>(-fabsf(t)), r = reciprocal<FAST>(1.0f + e), least = e * r;
+    return {t < 0.0f ? least : r, fmaf(-least, least, least)};
 }
 
 struct NormalTail {
