@@ -12,8 +12,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Of two arguments.
 struct ValueSlope {
-    float value, slope;
+    float2 value, slope;
 };
 
 // FAST: results that are rounded to bf16.
@@ -46,59 +47,83 @@ __device__ __forceinline__ Logistic logistic(float t)
 }
 
 struct NormalTail {
-    float tail, gauss;  // Phi(-y) and exp(-y^2 / 2)
+    float2 tail, gauss;  // Phi(-y) and exp(-y^2 / 2)
 };
-// The normal distribution's tail at y >= 0 as exp(-y^2 / 2) t P(t), t = 1 / (1 + k
-// y): what the Gaussian leaves is smooth on (0, 1], and a polynomial fitted to it
-// there (least squares reweighted to an even relative error, y up to 14.5) is off
-// by 9e-6 at degree 5 (FAST) and by 3.2e-8 at degree 8, relative to the tail
-// itself, so that the far negative side keeps its precision.  One exponential
-// serves the value and the slope; with the library's erfc and a second one the
-// bf16 backward pass of 8192x14336 took 287 us.
+// The normal distribution's tail at y >= 0 in the form of Hastings, "Approximations
+// for Digital Computers" (1955; Abramowitz and Stegun 26.2.17): exp(-y^2 / 2) times
+// a polynomial in t = 1 / (1 + k y).  One exponential serves the value and the
+// slope; with the library's erfc and a second one the bf16 backward pass of
+// 8192x14336 took 287 us.
+//
+// fp32: t (1/2 + w Q(w)), w = k y t = 1 - t.  Near y = 0, where most arguments lie, w
+// is small and Q's rounding with it, and on the far side the tail keeps its
+// precision.  Q is a least squares fit, reweighted to an even relative error over 0 <=
+// y <= 14.5: 2e-8, 4e-8 with its coefficients rounded (tests/test_normal_tail_fit.py
+// has the fit).  What y^2 loses to rounding goes into the exponential as a factor.
+// With every operation rounded the tail is off by 4e-7 of itself at most, and the
+// slope's root mean square error is that of its plain form by erf.  Of t's two last
+// places (a division to nearest: 33 us in place of 29.7 for 1023x11009 backward) that
+// shows nothing.
+//
+// bf16 (FAST): t P(t), P of degree 5 fitted to 9e-6.
 template <bool FAST>
-__device__ __forceinline__ NormalTail normal_tail(float y)
+__device__ __forceinline__ NormalTail normal_tail(float2 y)
 {
-    float p;
-    const float t = __fdividef(1.0f, fmaf(FAST ? 0.3f : 0.35f, y, 1.0f));
     if constexpr (FAST) {
-        p = -0.0767005980f;
-        p = fmaf(p, t, 0.214848995f);
-        p = fmaf(p, t, -0.0155976024f);
-        p = fmaf(p, t, 0.143473402f);
-        p = fmaf(p, t, 0.113922819f);
-        p = fmaf(p, t, 0.120057419f);
+        const float2 d = __ffma2_rn(both(0.3f), y, both(1.0f));
+        const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
+        constexpr float c[] = {0.120057419f, 0.113922819f, 0.143473402f, -0.0155976024f, 0.214848995f, -0.0767005980f};
+        float2 p = both(c[5]);
+#pragma unroll
+        for (int i = 4; i >= 0; --i)
+            p = __ffma2_rn(p, t, both(c[i]));
+        const float2 a = __fmul2_rn(__fmul2_rn(y, both(-0.5f)), y);
+        const float2 e = make_float2(exponential<true>(a.x), exponential<true>(a.y));
+        return {__fmul2_rn(e, __fmul2_rn(t, p)), e};
     } else {
-        p = -0.0291578863f;
-        p = fmaf(p, t, 0.144030914f);
-        p = fmaf(p, t, -0.255838990f);
-        p = fmaf(p, t, 0.159319699f);
-        p = fmaf(p, t, -0.0232123509f);
-        p = fmaf(p, t, 0.105552502f);
-        p = fmaf(p, t, 0.119821288f);
-        p = fmaf(p, t, 0.139863521f);
-        p = fmaf(p, t, 0.139621302f);
+        constexpr float k = 0.4f;
+        constexpr float full[] = {-0.497356862f,  0.0678424835f, 0.116752833f, 0.0223698318f, -0.0597253218f,
+                                  0.0548196249f, -0.12487451f,   0.11158748f,  -0.0318392329f};
+        const float2 ky = __fmul2_rn(y, both(k)), d = __fadd2_rn(ky, both(1.0f));
+        const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y)), w = __fmul2_rn(ky, t);
+        float2 q = both(full[8]);
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+            q = __ffma2_rn(q, w, both(full[i]));
+        const float2 half = __fmul2_rn(y, both(-0.5f)), a = __fmul2_rn(half, y);
+        float2 e = make_float2(exponential<false>(a.x), exponential<false>(a.y));
+        e = __ffma2_rn(e, __ffma2_rn(half, y, make_float2(-a.x, -a.y)), e);
+        return {__fmul2_rn(e, __fmul2_rn(t, __ffma2_rn(w, q, both(0.5f)))), e};
     }
-    const float e = exponential<FAST>(-0.5f * y * y);
-    return {e * (t * p), e};
 }
 
 // a(z) and a'(z).
 template <int ACT, bool FAST>
-__device__ __forceinline__ ValueSlope activate(float z)
+__device__ __forceinline__ ValueSlope activate(float2 z)
 {
     if constexpr (ACT == MX_ACT_SILU) {
-        const Logistic f = logistic<FAST>(z);
-        return {z * f.p, f.p + z * f.q};
+        const Logistic f = logistic<FAST>(z.x), g = logistic<FAST>(z.y);
+        return {make_float2(z.x * f.p, z.y * g.p), make_float2(f.p + z.x * f.q, g.p + z.y * g.q)};
     } else if constexpr (ACT == MX_ACT_GELU) {
-        const NormalTail n = normal_tail<FAST>(fabsf(z));
-        const float p = z > 0.0f ? 1.0f - n.tail : n.tail;
-        return {z * p, p + z * (0.39894228040143268f * n.gauss)};
+        float2 y = make_float2(fabsf(z.x), fabsf(z.y));
+        if constexpr (!FAST)  // the tail is 0 from 14.5 on, and y^2 stays finite
+            y = make_float2(fminf(y.x, 16.0f), fminf(y.y, 16.0f));
+        const NormalTail n = normal_tail<FAST>(y);
+        const float2 p = make_float2(z.x > 0.0f ? 1.0f - n.tail.x : n.tail.x, z.y > 0.0f ? 1.0f - n.tail.y : n.tail.y);
+        return {__fmul2_rn(z, p), __ffma2_rn(z, __fmul2_rn(n.gauss, both(0.39894228040143268f)), p)};
     } else {  // (1 + tanh t) / 2 = 1 / (1 + exp(-2 t))
         constexpr float k = 0.79788456080286536f;
-        const float zz = z * z;
-        const Logistic f = logistic<FAST>(2.0f * k * (z + 0.044715f * z * zz));
-        // q is 0 where z^2 may have overflowed: the slope is p there
-        return {z * f.p, f.q == 0.0f ? f.p : f.p + z * f.q * (2.0f * k) * (1.0f + 0.134145f * zz)};
+        auto one = [](float v, float& value, float& slope) {
+            const float vv = v * v;
+            const Logistic f = logistic<FAST>(2.0f * k * (v + 0.044715f * v * vv));
+            value = v * f.p;
+            // q is 0 where v^2 may have overflowed: the slope is p there
+            slope = f.q == 0.0f ? f.p : f.p + v * f.q * (2.0f * k) * (1.0f + 0.134145f * vv);
+        };
+        ValueSlope r;
+        one(z.x, r.value.x, r.slope.x);
+        one(z.y, r.value.y, r.slope.y);
+        return r;
     }
 }
 
@@ -109,7 +134,7 @@ __device__ __forceinline__ ValueSlope activate(float z)
 // CTAs an SM strides over the units, or as many as registers allow.  8192x14336
 // bf16 gated SiLU measured, in us, at 3 / 4 / 5 / 6 CTAs: forward with checkpoints
 // 161 / 150 and no more fit, backward 194 / 179 / 181 / 187 from the kept inputs
-// (GELU 215 / 196 / 185 / 185), 179 / 163 / 151 / 148 from checkpoints; 4096x11008
+// (GELU 5: 182), 179 / 163 / 151 / 148 from checkpoints; 4096x11008
 // saved and restored at 3 / 4 / 5 / 8 50 / 46 / 44 / 42.  One unit in place of two: 169, 162 and 55, but at
 // any address, where the shifts take the registers, 1023x11009 fp32 49 -> 40.  ANY: rows of any address and length; else
 // they start on 16-byte boundaries and their length is a multiple of eight.
@@ -221,7 +246,7 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 
 // h = a(gate) up, the checkpoints of both inputs and the maximum from one reading.
 // Bound by DRAM: 8192x14336 bf16 SiLU with checkpoints 150 us (946 MB, 6.3 TB/s);
-// GELU 181 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
+// GELU 166 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
 // columns 243 us.
 template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
@@ -247,10 +272,10 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
             if constexpr (GATED)
                 u[k].get(uv, p[k].cols);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                h[j] = activate<ACT, sizeof(T) == 2>(gv[j]).value;
+            for (int j = 0; j < 4; ++j) {
+                h.p[j] = activate<ACT, sizeof(T) == 2>(gv.p[j]).value;
                 if constexpr (GATED)
-                    h[j] *= uv[j];
+                    h.p[j].x *= uv.p[j].x, h.p[j].y *= uv.p[j].y;
             }
             store_unit<T, ANY>(a.h, a.ldh, p[k], h, a.cols, top);
             if (a.gate8.codes)
@@ -266,9 +291,11 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 
 // dgate = dh up a'(gate), dup = dh a(gate): one exponential gives value and slope.
 // Bound by DRAM: 8192x14336 bf16 SiLU from checkpoints 148 us (946 MB, 6.4 TB/s),
-// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 179 us.
+// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 170 and 182 us, the latter
+// with registers held to 48 for the fifth CTA (0: the compiler's own choice).
 template <typename T, int ACT, bool GATED, bool FROM8, bool ANY>
-__global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
+__global__ void __launch_bounds__(kThreads, !ANY && !FROM8 && sizeof(T) == 2 && ACT == MX_ACT_GELU ? kBwdCtas : 0)
+    act_bwd_kernel(ActArgs a, UnitMap m)
 {
     constexpr int kUnits = units_in_flight(ANY);
     using Raw = std::conditional_t<FROM8, RawCodes, Unit<T, ANY>>;
@@ -304,12 +331,12 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(ActArgs a, UnitMap m)
             if constexpr (GATED)
                 u[k].get(uv, p[k].cols);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const ValueSlope f = activate<ACT, sizeof(T) == 2>(gv[j]);
-                dg[j] = dv[j] * f.slope;
+            for (int j = 0; j < 4; ++j) {
+                const ValueSlope f = activate<ACT, sizeof(T) == 2>(gv.p[j]);
+                dg.p[j].x = dv.p[j].x * f.slope.x, dg.p[j].y = dv.p[j].y * f.slope.y;
                 if constexpr (GATED) {
-                    dg[j] *= uv[j];
-                    dv[j] *= f.value;
+                    dg.p[j].x *= uv.p[j].x, dg.p[j].y *= uv.p[j].y;
+                    dv.p[j].x *= f.value.x, dv.p[j].y *= f.value.y;
                 }
             }
             store_unit<T, ANY>(a.dgate, a.lddg, p[k], dg, a.cols, top);

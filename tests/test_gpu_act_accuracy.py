@@ -57,7 +57,7 @@ def test_where_the_exponential_leaves_the_normal_numbers(mx, act, dtype):
     assert normal.any() and (h[normal] != 0).all()
 
 
-@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_gradients_in_fp32_are_as_near_as_the_plain_form(mx, act):
     """Root mean square error of the slope over normal arguments, beside that of the plain
     form's single operations: no more than 1.1 times."""
@@ -68,8 +68,31 @@ def test_gradients_in_fp32_are_as_near_as_the_plain_form(mx, act):
     if act == "silu":
         p = 1 / (1 + torch.exp(-z))
         plain = p + z * p * (1 - p)
+    elif act == "gelu":
+        plain = 0.5 * (1 + torch.erf(z * 0.5 ** 0.5)) + z * (torch.exp(-0.5 * z * z) * 0.3989422804014327)
     else:
         th = torch.tanh(ref.K_TANH * (z + ref.C_TANH * z ** 3))
         plain = 0.5 * (1 + th) + 0.5 * z * (1 - th * th) * ref.K_TANH * (1 + 3 * ref.C_TANH * z * z)
     rms = lambda v: (v.double() - s).square().mean().sqrt().item()  # noqa: E731
     assert rms(dz) <= 1.1 * rms(plain), (rms(dz), rms(plain))
+
+
+def _gelu_rel(dtype):
+    """GELU's tail e t g(t): the exponential (fp32: 2 u and u for its argument's rest), t
+    = 1 / (1 + k y) (fp32 2 u: less than the approximate division's documented 4 u, so that
+    not everything may be at its worst at once; what the tail makes of it is no more), the
+    polynomial's own 0.1 u and its sums, at most 6 u of g, the two products and z's: 14 u;
+    bf16: t 5 u and the polynomial 3 u, and beside them the exponential's (2 + 1.173 y^2 / 2)
+    places and 2 u y^2 / 2 of its argument."""
+    return 14 * U if dtype is F32 else 19 * U
+
+
+@pytest.mark.parametrize("lo,hi", [(0.0, 1.0), (1.0, 3.0), (3.0, 5.0), (5.0, 8.0), (8.0, 12.9)])
+def test_gelu_in_fp32_keeps_its_precision_on_the_negative_side(mx, lo, hi):
+    z = -torch.linspace(lo, hi, 100001, device="cuda").view(1, -1)
+    h, dz = _both(mx, z, "gelu")
+    a, s, p, _ = ref.activation(z, "gelu")
+    rel, zd = _gelu_rel(F32), z.double().abs()
+    gauss = torch.exp(-zd ** 2 / 2) / (2 * torch.pi) ** 0.5
+    ref.assert_within(h, a, a.abs() * rel + 2.0 ** -126, "value")
+    ref.assert_within(dz, s, p * rel + zd * gauss * 6 * U + U * s.abs() + 2.0 ** -120, "slope")
