@@ -17,7 +17,11 @@ struct ValueSlope {
     float2 value, slope;
 };
 
-// FAST: results that are rounded to bf16.
+// FAST: results that are rounded to bf16.  The value and the slope are off by less
+// than 2^-20 of their terms for the arguments that matter.  Beside half a bf16 place,
+// 2^-9, that is nothing but where a slope's terms cancel: at the bf16 argument next to
+// a slope's zero, 1/200 to 1/360 of a term remains, and the error is up to a fifth of
+// half a place there.
 //
 // exp(x), x <= 0: the approximate exponential is off by 2 + 1.2 |x| last places,
 // so by 2^-22 of the result for the arguments that matter and below 2^-16 for all.
@@ -26,7 +30,7 @@ __device__ __forceinline__ float exponential(float x)
 {
     return FAST ? __expf(x) : expf(x);
 }
-// 1 / d for 1 <= d <= 8: within 2 last places, or to nearest.
+// 1 / d for 1 <= d <= 2: within 2 last places, or to nearest.
 template <bool FAST>
 __device__ __forceinline__ float reciprocal(float d)
 {
@@ -55,46 +59,36 @@ struct NormalTail {
 // slope; with the library's erfc and a second one the bf16 backward pass of
 // 8192x14336 took 287 us.
 //
-// fp32: t (1/2 + w Q(w)), w = k y t = 1 - t.  Near y = 0, where most arguments lie, w
+// It is t (1/2 + w Q(w)), w = k y t = 1 - t: near y = 0, where most arguments lie, w
 // is small and Q's rounding with it, and on the far side the tail keeps its
 // precision.  Q is a least squares fit, reweighted to an even relative error over 0 <=
-// y <= 14.5: 2e-8, 4e-8 with its coefficients rounded (tests/test_normal_tail_fit.py
-// has the fit).  What y^2 loses to rounding goes into the exponential as a factor.
-// With every operation rounded the tail is off by 4e-7 of itself at most, and the
-// slope's root mean square error is that of its plain form by erf.  Of t's two last
-// places (a division to nearest: 33 us in place of 29.7 for 1023x11009 backward) that
-// shows nothing.
+// y <= 14.5 (tests/test_normal_tail_fit.py has the fit): 2e-8, 4e-8 with its
+// coefficients rounded; FAST two degrees less and 3e-7, 3e-7.
 //
-// bf16 (FAST): t P(t), P of degree 5 fitted to 9e-6.
+// fp32: what y^2 loses to rounding goes into the exponential as a factor.  With every
+// operation rounded the tail is off by 4e-7 of itself at most, and the slope's root
+// mean square error is that of its plain form by erf.  Of t's two last places (a
+// division to nearest: 33 us in place of 29.7 for 1023x11009 backward) that shows
+// nothing.
 template <bool FAST>
 __device__ __forceinline__ NormalTail normal_tail(float2 y)
 {
-    if constexpr (FAST) {
-        const float2 d = __ffma2_rn(both(0.3f), y, both(1.0f));
-        const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
-        constexpr float c[] = {0.120057419f, 0.113922819f, 0.143473402f, -0.0155976024f, 0.214848995f, -0.0767005980f};
-        float2 p = both(c[5]);
+    constexpr float k = FAST ? 0.42f : 0.4f;
+    constexpr float fast[] = {-0.449849814f, 0.0171071552f, 0.111512974f, 0.0109572522f,
+                              0.0409163237f, -0.107324116f, 0.0442672148f};
+    constexpr float full[] = {-0.497356862f,  0.0678424835f, 0.116752833f, 0.0223698318f, -0.0597253218f,
+                              0.0548196249f, -0.12487451f,   0.11158748f,  -0.0318392329f};
+    const float2 ky = __fmul2_rn(y, both(k)), d = __fadd2_rn(ky, both(1.0f));
+    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y)), w = __fmul2_rn(ky, t);
+    float2 q = both(FAST ? fast[6] : full[8]);
 #pragma unroll
-        for (int i = 4; i >= 0; --i)
-            p = __ffma2_rn(p, t, both(c[i]));
-        const float2 a = __fmul2_rn(__fmul2_rn(y, both(-0.5f)), y);
-        const float2 e = make_float2(exponential<true>(a.x), exponential<true>(a.y));
-        return {__fmul2_rn(e, __fmul2_rn(t, p)), e};
-    } else {
-        constexpr float k = 0.4f;
-        constexpr float full[] = {-0.497356862f,  0.0678424835f, 0.116752833f, 0.0223698318f, -0.0597253218f,
-                                  0.0548196249f, -0.12487451f,   0.11158748f,  -0.0318392329f};
-        const float2 ky = __fmul2_rn(y, both(k)), d = __fadd2_rn(ky, both(1.0f));
-        const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y)), w = __fmul2_rn(ky, t);
-        float2 q = both(full[8]);
-#pragma unroll
-        for (int i = 7; i >= 0; --i)
-            q = __ffma2_rn(q, w, both(full[i]));
-        const float2 half = __fmul2_rn(y, both(-0.5f)), a = __fmul2_rn(half, y);
-        float2 e = make_float2(exponential<false>(a.x), exponential<false>(a.y));
+    for (int i = FAST ? 5 : 7; i >= 0; --i)
+        q = __ffma2_rn(q, w, both(FAST ? fast[i] : full[i]));
+    const float2 half = __fmul2_rn(y, both(-0.5f)), a = __fmul2_rn(half, y);
+    float2 e = make_float2(exponential<FAST>(a.x), exponential<FAST>(a.y));
+    if constexpr (!FAST)
         e = __ffma2_rn(e, __ffma2_rn(half, y, make_float2(-a.x, -a.y)), e);
-        return {__fmul2_rn(e, __fmul2_rn(t, __ffma2_rn(w, q, both(0.5f)))), e};
-    }
+    return {__fmul2_rn(e, __fmul2_rn(t, __ffma2_rn(w, q, both(0.5f)))), e};
 }
 
 // a(z) and a'(z).
@@ -134,7 +128,7 @@ __device__ __forceinline__ ValueSlope activate(float2 z)
 // CTAs an SM strides over the units, or as many as registers allow.  8192x14336
 // bf16 gated SiLU measured, in us, at 3 / 4 / 5 / 6 CTAs: forward with checkpoints
 // 161 / 150 and no more fit, backward 194 / 179 / 181 / 187 from the kept inputs
-// (GELU 5: 182), 179 / 163 / 151 / 148 from checkpoints; 4096x11008
+// (GELU 5: 184), 179 / 163 / 151 / 148 from checkpoints; 4096x11008
 // saved and restored at 3 / 4 / 5 / 8 50 / 46 / 44 / 42.  One unit in place of two: 169, 162 and 55, but at
 // any address, where the shifts take the registers, 1023x11009 fp32 49 -> 40.  ANY: rows of any address and length; else
 // they start on 16-byte boundaries and their length is a multiple of eight.
@@ -246,7 +240,7 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 
 // h = a(gate) up, the checkpoints of both inputs and the maximum from one reading.
 // Bound by DRAM: 8192x14336 bf16 SiLU with checkpoints 150 us (946 MB, 6.3 TB/s);
-// GELU 166 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
+// GELU 176 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
 // columns 243 us.
 template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
@@ -291,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 
 // dgate = dh up a'(gate), dup = dh a(gate): one exponential gives value and slope.
 // Bound by DRAM: 8192x14336 bf16 SiLU from checkpoints 148 us (946 MB, 6.4 TB/s),
-// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 170 and 182 us, the latter
-// with registers held to 48 for the fifth CTA (0: the compiler's own choice).
+// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 181 and 184 us, the latter
+// with registers held to 48 for the fifth CTA (54 without: 200 us; 0: the compiler's own choice).
 template <typename T, int ACT, bool GATED, bool FROM8, bool ANY>
 __global__ void __launch_bounds__(kThreads, !ANY && !FROM8 && sizeof(T) == 2 && ACT == MX_ACT_GELU ? kBwdCtas : 0)
     act_bwd_kernel(ActArgs a, UnitMap m)

@@ -96,3 +96,24 @@ def test_gelu_in_fp32_keeps_its_precision_on_the_negative_side(mx, lo, hi):
     gauss = torch.exp(-zd ** 2 / 2) / (2 * torch.pi) ** 0.5
     ref.assert_within(h, a, a.abs() * rel + 2.0 ** -126, "value")
     ref.assert_within(dz, s, p * rel + zd * gauss * 6 * U + U * s.abs() + 2.0 ** -120, "slope")
+
+
+@pytest.mark.parametrize("act,at", [("silu", -1.28125), ("gelu", -0.75), ("gelu_tanh", -0.75)])
+def test_bf16_slopes_at_their_zero(mx, act, at):
+    """dgate = dh up a'(gate) at the bf16 gate next to the slope's zero, over all fractions
+    of dh and up: off by half a place and the error of the two terms that cancel."""
+    f = (1 + torch.arange(128, device="cuda") / 128).to(BF)
+    dh, up = f.view(-1, 1).expand(128, 128).contiguous(), f.view(1, -1).expand(128, 128).contiguous()
+    gate = torch.full_like(dh, at)
+    dg, _ = mx.act_bwd(dh, gate, up, act=act)
+    _, s, p, t = ref.activation(gate, act)
+    z = gate.double().abs()
+    if act == "gelu":
+        e = 2 * (2 + 1.173 * z * z / 2) * U + z * z * U
+        terms = p * (_gelu_rel(BF) + z * z * U) + z * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5 * (e + 3 * U)
+    else:
+        e = 2 * (2 + 1.173 * t.abs()) * U + 6 * t.abs() * U
+        inner = z * (2 * ref.K_TANH * (1 + 3 * ref.C_TANH * z ** 2) if act == "gelu_tanh" else 1.0)
+        terms = p * (e + 8 * U) + inner * p * (1 - p) * (e + 14 * U)
+    d = dh.double() * up.double()
+    ref.assert_within(dg, d * s, d * (terms + 3 * U * s.abs()) + _half_place(d * s.abs() * (1 + 2.0 ** -9), BF), "dgate")

@@ -48,7 +48,7 @@ def fit(k, degree, points=4000, rounds=400):
     return best
 
 
-CASES = [("fp32", 8, 2e-8, 4e-8, 4e-7)]  # polynomial's degree, its error, with rounded coefficients, the tail's
+CASES = [("fp32", 8, 2e-8, 4e-8, 4e-7), ("bf16", 6, 3e-7, 3e-7, 5e-6)]  # polynomial's degree, its error, with rounded coefficients, the tail's
 
 
 @pytest.mark.parametrize("which,degree,fitted,rounded,whole", CASES)
