@@ -79,7 +79,9 @@ __device__ __forceinline__ NormalTail normal_tail(float2 y)
     constexpr float full[] = {-0.497356862f,  0.0678424835f, 0.116752833f, 0.0223698318f, -0.0597253218f,
                               0.0548196249f, -0.12487451f,   0.11158748f,  -0.0318392329f};
     const float2 ky = __fmul2_rn(y, both(k)), d = __fadd2_rn(ky, both(1.0f));
-    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y)), w = __fmul2_rn(ky, t);
+    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
+    // k y t is the more precise; 1 - t holds for infinite y too
+    const float2 w = FAST ? __ffma2_rn(t, both(-1.0f), both(1.0f)) : __fmul2_rn(ky, t);
     float2 q = both(FAST ? fast[6] : full[8]);
 #pragma unroll
     for (int i = FAST ? 5 : 7; i >= 0; --i)
@@ -127,11 +129,13 @@ __device__ __forceinline__ ValueSlope activate(float2 z)
 // kFwdCtas, kBwdCtas (from the kept inputs), kBwd8Ctas (from checkpoints) or k8Ctas
 // CTAs an SM strides over the units, or as many as registers allow.  8192x14336
 // bf16 gated SiLU measured, in us, at 3 / 4 / 5 / 6 CTAs: forward with checkpoints
-// 161 / 150 and no more fit, backward 194 / 179 / 181 / 187 from the kept inputs
-// (GELU 5: 184), 179 / 163 / 151 / 148 from checkpoints; 4096x11008
-// saved and restored at 3 / 4 / 5 / 8 50 / 46 / 44 / 42.  One unit in place of two: 169, 162 and 55, but at
-// any address, where the shifts take the registers, 1023x11009 fp32 49 -> 40.  ANY: rows of any address and length; else
-// they start on 16-byte boundaries and their length is a multiple of eight.
+// 161 / 150 and no more fit, backward from the kept inputs 194 / 179 / 181 / 187 (GELU
+// 215 / 196 / 185 / 185), from checkpoints 179 / 163 / 151 / 148; 4096x11008 saved and
+// restored at 3 / 4 / 5 / 8 50 / 46 / 44 / 42.  One unit in place of two: 170, 149 and
+// 45, but at any address, where the shifts take the registers, 1023x11009 fp32 32.5
+// -> 29.7, 8192x14335 248 -> 243, 4096x11007 saved and restored 67.5 -> 64.7.
+// ANY: rows of any address and length; else they start on 16-byte boundaries and their
+// length is a multiple of eight.
 constexpr int kFwdCtas = 4, kBwdCtas = 5, kBwd8Ctas = 6, k8Ctas = 8;
 __host__ __device__ constexpr int units_in_flight(bool any) { return any ? 1 : 2; }
 
@@ -240,7 +244,7 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 
 // h = a(gate) up, the checkpoints of both inputs and the maximum from one reading.
 // Bound by DRAM: 8192x14336 bf16 SiLU with checkpoints 150 us (946 MB, 6.3 TB/s);
-// GELU 176 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
+// GELU 173 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
 // columns 243 us.
 template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
@@ -285,10 +289,11 @@ __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)
 
 // dgate = dh up a'(gate), dup = dh a(gate): one exponential gives value and slope.
 // Bound by DRAM: 8192x14336 bf16 SiLU from checkpoints 148 us (946 MB, 6.4 TB/s),
-// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 181 and 184 us, the latter
-// with registers held to 48 for the fifth CTA (54 without: 200 us; 0: the compiler's own choice).
+// from the kept inputs 181 us (1175 MB, 6.5 TB/s); GELU 181 and 185 us, where the
+// registers are held to what lets its CTAs be resident (without: 188 and 200 us; 0
+// leaves them to the compiler); 14335 columns, SiLU, 238 us.
 template <typename T, int ACT, bool GATED, bool FROM8, bool ANY>
-__global__ void __launch_bounds__(kThreads, !ANY && !FROM8 && sizeof(T) == 2 && ACT == MX_ACT_GELU ? kBwdCtas : 0)
+__global__ void __launch_bounds__(kThreads, !ANY && sizeof(T) == 2 && ACT == MX_ACT_GELU ? (FROM8 ? kBwd8Ctas : kBwdCtas) : 0)
     act_bwd_kernel(ActArgs a, UnitMap m)
 {
     constexpr int kUnits = units_in_flight(ANY);

@@ -117,3 +117,23 @@ def test_bf16_slopes_at_their_zero(mx, act, at):
         terms = p * (e + 8 * U) + inner * p * (1 - p) * (e + 14 * U)
     d = dh.double() * up.double()
     ref.assert_within(dg, d * s, d * (terms + 3 * U * s.abs()) + _half_place(d * s.abs() * (1 + 2.0 ** -9), BF), "dgate")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_infinities_and_nan(mx, act, dtype):
+    """As the formulas give them: the value at Inf is Inf, at -Inf -Inf times 0, at NaN NaN;
+    the slope of tanh GELU has its limits at the infinities, the others' an Inf times 0.
+    What stands beside them is as it is alone."""
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([[1.0, inf, -inf, nan, -2.0, 3e38, -3e38, 0.5]], device="cuda").to(dtype)
+    h, dz = _both(mx, z, act)
+    assert h[0, 1] == inf and torch.isnan(h[0, 2:4]).all() and torch.isnan(dz[0, 3])
+    if act == "gelu_tanh":
+        assert dz[0, 1] == 1 and dz[0, 2] == 0
+    else:
+        assert torch.isnan(dz[0, 1:3]).all()
+    assert h[0, 5] == z[0, 5] and h[0, 6] == 0 and dz[0, 5] == 1 and dz[0, 6] == 0
+    keep = [0, 4, 7]
+    alone, dalone = _both(mx, z[:, keep].contiguous(), act)
+    assert torch.equal(h[:, keep], alone) and torch.equal(dz[:, keep], dalone)
