@@ -30,11 +30,15 @@ __device__ __forceinline__ float exponential(float x)
 {
     return FAST ? __expf(x) : expf(x);
 }
-// 1 / d for 1 <= d <= 2: within 2 last places, or to nearest.
+// 1 / d for 1 <= d <= 2.  FAST: within 2 last places.  fp32: one step of Newton's
+// iteration from there, r + r (1 - d r), whose error is the square of r's, so that its
+// own rounding is what is left.  (The operator's division takes care of every d, in a
+// subroutine: 3x192 forward 3.4 us in place of 2.4, 1023x11009 32.6 in place of 30.9.)
 template <bool FAST>
 __device__ __forceinline__ float reciprocal(float d)
 {
-    return FAST ? __fdividef(1.0f, d) : 1.0f / d;
+    const float r = __fdividef(1.0f, d);
+    return FAST ? r : fmaf(r, fmaf(-d, r, 1.0f), r);
 }
 
 // p = 1 / (1 + exp(-t)) and its slope q = p (1 - p).  From exp(-|t|) nothing
@@ -130,7 +134,7 @@ __device__ __forceinline__ ValueSlope activate(float2 z)
 // CTAs an SM strides over the units, or as many as registers allow.  8192x14336
 // bf16 gated SiLU measured, in us, at 3 / 4 / 5 / 6 CTAs: forward with checkpoints
 // 161 / 150 and no more fit, backward from the kept inputs 194 / 179 / 181 / 187 (GELU
-// 215 / 196 / 185 / 185), from checkpoints 179 / 163 / 151 / 148; 4096x11008 saved and
+// 196 / 185 at 4 / 5), from checkpoints 179 / 163 / 151 / 148; 4096x11008 saved and
 // restored at 3 / 4 / 5 / 8 50 / 46 / 44 / 42.  One unit in place of two: 170, 149 and
 // 45, but at any address, where the shifts take the registers, 1023x11009 fp32 32.5
 // -> 29.7, 8192x14335 248 -> 243, 4096x11007 saved and restored 67.5 -> 64.7.
@@ -244,7 +248,7 @@ __device__ __forceinline__ void save_unit(const Act8View& out, int64_t unit, boo
 
 // h = a(gate) up, the checkpoints of both inputs and the maximum from one reading.
 // Bound by DRAM: 8192x14336 bf16 SiLU with checkpoints 150 us (946 MB, 6.3 TB/s);
-// GELU 173 us, where the instructions show; fp32 280 us (1651 MB, 5.9 TB/s); 14335
+// GELU 173 us, where the instructions show; fp32 279 us (1651 MB, 5.9 TB/s); 14335
 // columns 243 us.
 template <typename T, int ACT, bool GATED, bool ANY>
 __global__ void __launch_bounds__(kThreads) act_fwd_kernel(ActArgs a, UnitMap m)

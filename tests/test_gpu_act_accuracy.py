@@ -77,13 +77,23 @@ def test_gradients_in_fp32_are_as_near_as_the_plain_form(mx, act):
     assert rms(dz) <= 1.1 * rms(plain), (rms(dz), rms(plain))
 
 
+def test_silu_in_fp32_adds_few_roundings(mx):
+    """z / (1 + e), e = exp(-z): e's 2 u, of which 1 - p reaches the value, the sum's u, the
+    reciprocal's 2 u (a last place) and the product's u; below 0 e / (1 + e) has e's 2 u
+    whole and a product more."""
+    z = torch.linspace(-80, 30, 1000003, device="cuda").view(1, -1)
+    h = mx.act_fwd(z, act="silu").h
+    a, _, p, _ = ref.activation(z, "silu")
+    ref.assert_within(h, a, a.abs() * torch.where(z >= 0, 2 * (1 - p) + 4, 7.0) * U, "value")
+
+
 def _gelu_rel(dtype):
     """GELU's tail e t g(t): the exponential (fp32: 2 u and u for its argument's rest), t
     = 1 / (1 + k y) (fp32 2 u: less than the approximate division's documented 4 u, so that
     not everything may be at its worst at once; what the tail makes of it is no more), the
     polynomial's own 0.1 u and its sums, at most 6 u of g, the two products and z's: 14 u;
-    bf16: t 5 u and the polynomial 3 u, and beside them the exponential's (2 + 1.173 y^2 / 2)
-    places and 2 u y^2 / 2 of its argument."""
+    bf16: t 5 u, the polynomial 5 u, its sums, the products and z's 9 u: 19 u, and beside
+    them the exponential's (2 + 1.173 y^2 / 2) places and 2 u y^2 / 2 of its argument."""
     return 14 * U if dtype is F32 else 19 * U
 
 
