@@ -35,6 +35,7 @@ EXPORTED = ("mx_codes_bytes", "mx_sf_bytes", "mx_scale_count", "mx_amax", "mx_qu
             "mx_linear_saved_bytes", "mx_linear_fwd_save", "mx_linear_bwd_saved", "mx_strerror",
             "mx_act8_codes_bytes", "mx_act8_sf_bytes", "mx_act8_save", "mx_act8_restore", "mx_norm_fwd",
             "mx_norm_bwd_workspace_bytes", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd",
+            "mx_grad_norm_workspace_bytes", "mx_grad_norm", "mx_adamw_step",
             "mx_last_device_status", "mx_selftest_bounded_wait", "mx_launch_count",
             "mx_debug_divide", "mx_debug_set_quant_impl", "mx_debug_set_tile_fail_at", "mx_debug_set_norm_fail_at", "mx_debug_set_bwd_fork", "mx_debug_set_gemm_variant",
             "mx_debug_last_gemm_variant")
@@ -55,6 +56,23 @@ class _CTensor(C.Structure):
 
 class _CAct8(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("sf", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64)]
+
+
+class _CGrad(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class _CAdamwTensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_sf", C.c_void_p), ("v_sf", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_int64),
+                ("weight_decay", C.c_double), ("p_dtype", C.c_int32), ("g_dtype", C.c_int32), ("bits", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class _CAdamwOpts(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double),
+                ("t", C.c_int64), ("lr_at", C.c_void_p), ("t_at", C.c_void_p), ("seed", C.c_uint64),
+                ("rounding", C.c_int32), ("reserved", C.c_int32)]
 
 
 class _CBwdOpts(C.Structure):
@@ -145,6 +163,12 @@ def lib():
             L.mx_act_bwd.argtypes = [p, i64, p, i64, p, i64, a8, a8, i64, i64, i32, i32, p, i64, p, i64, p, p]
             for name in ("mx_act8_save", "mx_act8_restore", "mx_norm_fwd", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd"):
                 getattr(L, name).restype = i32
+            L.mx_grad_norm_workspace_bytes.restype = sz
+            L.mx_grad_norm_workspace_bytes.argtypes = [i64]
+            L.mx_grad_norm.restype = i32
+            L.mx_grad_norm.argtypes = [C.POINTER(_CGrad), i64, C.c_double, p, p, sz, p]
+            L.mx_adamw_step.restype = i32
+            L.mx_adamw_step.argtypes = [C.POINTER(_CAdamwTensor), i64, C.POINTER(_CAdamwOpts), p, p, p]
             L.mx_strerror.restype = C.c_char_p
             L.mx_strerror.argtypes = [i32]
             L.mx_last_device_status.restype = i32
@@ -838,6 +862,192 @@ def act_bwd(dh: torch.Tensor, gate: torch.Tensor | Act8, up: torch.Tensor | Act8
          _look_up(ACTS, act, "act"), OUT[dt], pdg, lddg, pdu, lddu,
          _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None)
     return dgate, dup
+
+
+# ---------------------------------------------------------------- gradient norm and optimizer step
+def _flat(t, what, dev=None):
+    """(pointer, values, type's number) of one of many tensors after checking it."""
+    if not t.is_cuda:
+        _on_gpu(t)
+    if t.dtype not in OUT:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} has type {t.dtype}, expected bfloat16 or float32")
+    if not t.is_contiguous():
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must be contiguous")
+    if dev is not None and t.device != dev:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} is on {t.device}, expected {dev}")
+    return t.data_ptr(), t.numel(), OUT[t.dtype]
+
+
+def grad_norm(grads, max_norm: float | None = None, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """fp32 [norm, factor] of the gradients' values taken together, on the device:
+    factor = min(1, max_norm / (norm + 1e-6)) (1 without max_norm), NaN when the
+    norm is not finite.  out[1:] is what AdamW.step takes as grad_scale.  None
+    among the gradients counts as zeros."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return grad_norm(grads, max_norm, out, workspace)
+    given = [g for g in grads if g is not None]
+    if not given and out is None:
+        raise MXError(MX_ERR_INVALID_ARG, "grad_norm needs a gradient, or out")
+    dev = (given[0] if given else out).device
+    table = (_CGrad * len(given))()
+    for row, g in zip(table, given):
+        row.data, row.n, row.dtype = _flat(g, "a gradient", dev)
+    L = lib()
+    if out is None:
+        out = torch.empty(2, dtype=_F32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(L.mx_grad_norm_workspace_bytes(len(given)), dtype=_U8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise MXError(MX_ERR_INVALID_ARG, f"workspace must be contiguous memory on {dev}")
+    _run(dev, "mx_grad_norm", L.mx_grad_norm, table, len(given), float("inf") if max_norm is None else max_norm,
+         _vec(out, 2, dev, "out"), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+class AdamW:
+    """AdamW over a list of tensors, one launch a step for those of a kind.
+
+    params: contiguous bfloat16 or float32 tensors on one device, updated in place.
+    weight_decay: one number, or one for each tensor.  state: "fp32", or "8bit"
+    for moments in the checkpoints' format (m, and the root of v; 1.03 bytes each).
+    copies: bfloat16 tensors (or None) beside float32 params, which a step fills
+    with the rounded weights.  rounding: "rne", or "sr" for stochastic rounding of
+    8-bit moments and of bfloat16 params by seed and step number.  capturable: the
+    step number lives on the device, so that a step captured into a CUDA graph
+    counts at each replay.
+
+    m, v: the moments, one for each tensor (float32 views, or Act8 with one row;
+    v holds roots there); m_all, v_all: the memory that holds them, each tensor's
+    from the next multiple of 32 values.  t: steps made (with capturable: issued).
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
+                 state: str = "fp32", copies=None, rounding: str = "rne", seed: int = 0, capturable: bool = False):
+        self.params = list(params)
+        if not self.params:
+            raise MXError(MX_ERR_INVALID_ARG, "AdamW needs a tensor")
+        n = len(self.params)
+        self.lr, self.betas, self.eps, self.seed = lr, tuple(betas), eps, int(seed)
+        self.state = state
+        bits = _look_up({"fp32": 32, "8bit": 8}, state, "state")
+        self._rounding = _look_up(ROUNDING, rounding, "rounding")
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        self.copies = list(copies) if copies is not None else [None] * n
+        if len(decay) != n or len(self.copies) != n:
+            raise MXError(MX_ERR_INVALID_ARG, f"weight_decay and copies have one entry for each of the {n} tensors")
+        self.t = 0
+        dev = self.device = self.params[0].device
+        self._table = (_CAdamwTensor * n)()
+        self._opts = _CAdamwOpts()
+        groups = []
+        for row, p, wd in zip(self._table, self.params, decay):
+            row.param, row.n, row.p_dtype = _flat(p, "a parameter", dev)
+            row.weight_decay, row.bits = wd, bits
+            groups.append(-(-row.n // 32))
+        G = sum(groups)
+        if bits == 8:
+            self.m_all, self.v_all = (Act8(torch.zeros((1, 32 * G), dtype=_U8, device=dev),
+                                           torch.zeros((1, G), dtype=_U8, device=dev), 32 * G) for _ in range(2))
+        else:
+            self.m_all, self.v_all = (torch.zeros(32 * G, dtype=_F32, device=dev) for _ in range(2))
+        self.m, self.v = [], []
+        first = 0
+        for row, p, g in zip(self._table, self.params, groups):
+            for mine, everything, name in ((self.m, self.m_all, "m"), (self.v, self.v_all, "v")):
+                if bits == 8:
+                    a = Act8(everything.codes[:, 32 * first:32 * (first + g)], everything.sf[:, first:first + g], row.n)
+                    setattr(row, name, a.codes.data_ptr())
+                    setattr(row, name + "_sf", a.sf.data_ptr())
+                else:
+                    a = everything[32 * first:32 * first + row.n].view(p.shape)
+                    setattr(row, name, a.data_ptr())
+                mine.append(a)
+            first += g
+        self._t_dev = torch.zeros(1, dtype=torch.int64, device=dev) if capturable else None
+        self._where = None
+        self._check_written()
+
+    def _check_written(self):
+        """Takes the parameters' and copies' places; no two of what a step writes may share memory."""
+        spans = []
+        for row, p, c in zip(self._table, self.params, self.copies):
+            at, n, dtype = _flat(p, "a parameter", self.device)
+            if n != row.n or dtype != row.p_dtype:
+                raise MXError(MX_ERR_INVALID_ARG, "a parameter changed its size or type")
+            row.param = at
+            spans.append((at, at + n * p.element_size()))
+            row.copy = None
+            if c is not None:
+                if dtype != OUT[torch.float32]:
+                    raise MXError(MX_ERR_UNSUPPORTED, "a copy goes with a float32 parameter")
+                at, m, dtype = _flat(c, "a copy", self.device)
+                if m != n or dtype != OUT[torch.bfloat16]:
+                    raise MXError(MX_ERR_INVALID_ARG, "a copy is bfloat16 and has its parameter's size")
+                row.copy = at
+                spans.append((at, at + 2 * n))
+        spans = sorted(s for s in spans if s[1] > s[0])
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise MXError(MX_ERR_INVALID_ARG, "parameters and copies must not share memory")
+        self._where = self._places()
+
+    def _places(self):
+        return [p.data_ptr() for p in self.params], [c is not None and c.data_ptr() for c in self.copies]
+
+    def step(self, grads, grad_scale: torch.Tensor | None = None, amax_out: torch.Tensor | None = None, lr=None,
+             t: int | None = None, stream=None) -> None:
+        """One step.  grads: one for each tensor, of its size (None: the tensor stays
+        as it is).  grad_scale: one fp32 value on the device that multiplies them; NaN
+        leaves every tensor as it is.  amax_out: fp32 [tensors], max |weight| of each
+        copy (of the parameter without one), for its next quantization.  lr: a number,
+        or one fp32 value on the device; the default is the optimizer's.  t: this
+        step's number (from 1), in place of the count."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.step(grads, grad_scale, amax_out, lr, t)
+        dev = self.device
+        grads = list(grads)
+        n = len(self.params)
+        if len(grads) != n:
+            raise MXError(MX_ERR_INVALID_ARG, f"{len(grads)} gradients for {n} tensors")
+        if self._places() != self._where:
+            self._check_written()
+        for row, g in zip(self._table, grads):
+            if g is None:
+                row.grad = None
+                continue
+            row.grad, m, row.g_dtype = _flat(g, "a gradient", dev)
+            if m != row.n:
+                raise MXError(MX_ERR_INVALID_ARG, f"a gradient of {m} values for a tensor of {row.n}")
+        o = self._opts
+        lr = self.lr if lr is None else lr
+        o.lr_at = None
+        if isinstance(lr, torch.Tensor):
+            o.lr, o.lr_at = 0.0, _vec(lr, 1, dev, "lr")
+        else:
+            o.lr = lr
+        o.beta1, o.beta2 = self.betas
+        o.eps, o.seed, o.rounding = self.eps, self.seed, self._rounding
+        count = self.t + 1 if t is None else int(t)
+        if count < 1:
+            raise MXError(MX_ERR_INVALID_ARG, "steps are numbered from 1")
+        scale = _vec(grad_scale, 1, dev, "grad_scale") if grad_scale is not None else None
+        top = _vec(amax_out, n, dev, "amax_out") if amax_out is not None else None
+        if self._t_dev is not None:
+            if t is None:
+                self._t_dev.add_(1)
+            else:
+                self._t_dev.fill_(count)
+            o.t_at = self._t_dev.data_ptr()
+        o.t = count
+        try:
+            _run(dev, "mx_adamw_step", lib().mx_adamw_step, self._table, n, o, scale, top)
+        except MXError:
+            if self._t_dev is not None and t is None:
+                self._t_dev.sub_(1)
+            raise
+        self.t = count
 
 
 def last_device_status(stream=None) -> int:

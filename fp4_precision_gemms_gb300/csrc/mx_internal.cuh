@@ -185,4 +185,12 @@ int launch_act8_save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_
 int launch_act8_restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int dtype, const Device& d,
                         cudaStream_t s);
 
+// The optimizer's step and the gradients' norm (optim.cu), after mx_ops.cu's checks.
+constexpr int kGradNormCtas = 1024;        // partial sums that one launch leaves at most
+int64_t grad_norm_parts(int64_t count);    // partial sums in the workspace
+int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_opts& o, const float* scale, float* amax,
+                 const Device& d, cudaStream_t s);
+int launch_grad_norm(const mx_grad* grads, int64_t count, double max_norm, float* out, double* parts, const Device& d,
+                     cudaStream_t s);
+
 }  // namespace mx

@@ -1,10 +1,11 @@
-// mx_ops.cu -- the extern "C" entry points of the norm, activation and 8-bit
-// checkpoint calls declared in include/mx.h: argument validation on the host
-// and the launches.
+// mx_ops.cu -- the extern "C" entry points of the norm, activation, 8-bit
+// checkpoint, gradient norm and optimizer calls declared in include/mx.h:
+// argument validation on the host and the launches.
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
 #include "mx_norm.cuh"
 
+#include <cmath>
 #include <initializer_list>
 
 using namespace mx;
@@ -12,6 +13,8 @@ using namespace mx;
 namespace {
 
 constexpr int64_t kMaxCols = int64_t(1) << 30;
+constexpr int64_t kMaxFlat = int64_t(1) << 34;  // values of one of many tensors: 32-bit units of eight
+constexpr int64_t kMaxTensors = int64_t(1) << 24;
 constexpr int64_t kMaxElems = int64_t(1) << 60;  // rows x stride: byte offsets fit 64 bits
 
 bool valid_dtype(int t) { return t == MX_OUT_F32 || t == MX_OUT_BF16; }
@@ -369,6 +372,69 @@ int mx_act_bwd(const void* dh, int64_t ldh, const void* gate, int64_t ldg, const
     a.dtype = dtype;
     a.gated = up || up8;
     return launch_act_bwd(a, d, s);
+}
+
+size_t mx_grad_norm_workspace_bytes(int64_t count)
+{
+    return count < 0 || count > kMaxTensors ? 0 : static_cast<size_t>(grad_norm_parts(count)) * sizeof(double);
+}
+
+int mx_grad_norm(const mx_grad* grads, int64_t count, double max_norm, float* out, void* workspace, size_t ws_bytes,
+                 void* stream)
+{
+    Checks ok;
+    ok.require(count >= 0 && count <= kMaxTensors && (grads || count == 0) && out && max_norm > 0.0);
+    ok.words(out);
+    for (int64_t i = 0; ok.rc == MX_OK && i < count; ++i) {
+        const mx_grad& g = grads[i];
+        ok.require(g.n >= 0 && g.n <= kMaxFlat && valid_dtype(g.dtype) && (g.data || g.n == 0));
+        if (ok.rc == MX_OK)
+            ok(aligned(g.data, dtype_bytes(g.dtype)) ? MX_OK : MX_ERR_ALIGNMENT);
+    }
+    if (ok.rc == MX_OK) {
+        ok(workspace && ws_bytes >= mx_grad_norm_workspace_bytes(count) ? MX_OK : MX_ERR_WORKSPACE);
+        ok(aligned(workspace, 8) ? MX_OK : MX_ERR_ALIGNMENT);
+    }
+    Device d;
+    if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
+        return ok.rc;
+    return launch_grad_norm(grads, count, max_norm, out, static_cast<double*>(workspace), d,
+                            static_cast<cudaStream_t>(stream));
+}
+
+int mx_adamw_step(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_opts* opts, const float* grad_scale,
+                  float* amax_out, void* stream)
+{
+    Checks ok;
+    ok.require(count >= 0 && count <= kMaxTensors && (tensors || count == 0) && opts);
+    if (ok.rc != MX_OK)
+        return ok.rc;
+    const mx_adamw_opts& o = *opts;
+    ok.require(std::isfinite(o.lr) && o.beta1 >= 0.0 && o.beta1 < 1.0 && o.beta2 >= 0.0 && o.beta2 < 1.0);
+    ok.require(o.eps >= 0.0 && std::isfinite(o.eps) && (o.t >= 1 || o.t_at));
+    ok.require(o.rounding == MX_ROUND_RNE || o.rounding == MX_ROUND_SR);
+    ok.words(o.lr_at)(aligned(o.t_at, 8) ? MX_OK : MX_ERR_ALIGNMENT).words(grad_scale).words(amax_out);
+    for (int64_t i = 0; ok.rc == MX_OK && i < count; ++i) {
+        const mx_adamw_tensor& t = tensors[i];
+        ok.require(t.n >= 0 && t.n <= kMaxFlat && valid_dtype(t.p_dtype) && valid_dtype(t.g_dtype));
+        ok.require((t.bits == 8 || t.bits == 32) && std::isfinite(t.weight_decay));
+        if (ok.rc != MX_OK)
+            break;
+        ok(t.copy && t.p_dtype != MX_OUT_F32 ? MX_ERR_UNSUPPORTED : MX_OK);
+        ok.require(t.n == 0 || (t.param && t.m && t.v && (t.bits == 32 || (t.m_sf && t.v_sf))));
+        const int state = t.bits == 8 ? 16 : 4;
+        ok(aligned(t.param, dtype_bytes(t.p_dtype)) && aligned(t.grad, dtype_bytes(t.g_dtype)) && aligned(t.m, state) &&
+                   aligned(t.v, state) && aligned(t.copy, 2)
+               ? MX_OK
+               : MX_ERR_ALIGNMENT);
+    }
+    Device d;
+    if (ok.rc != MX_OK || ok(current_device(&d)).rc != MX_OK)
+        return ok.rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (ok(zero(amax_out, static_cast<size_t>(count) * sizeof(float), s)).rc != MX_OK)
+        return ok.rc;
+    return launch_adamw(tensors, count, o, grad_scale, amax_out, d, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,562 @@
+// optim.cu -- the optimizer's step and the gradients' norm over many tensors in
+// one launch each.
+#include <algorithm>
+#include <cmath>
+
+#include "mx_act8.cuh"
+#include "mx_internal.cuh"
+#include "mx_units.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnitsPerTile = kThreads;  // a tile: eight consecutive values a thread
+
+// ---------------------------------------------------------------- AdamW
+// The tensors of one launch, in its parameters: no table to copy to the device
+// before it and nothing that a captured graph would have to keep alive.
+constexpr int kAdamwEntries = 128;
+struct AdamwEntry {
+    void* p;
+    const void* g;  // null: the tensor has no gradient and stays as it is
+    void* m;
+    void* v;
+    uint8_t* m_sf;
+    uint8_t* v_sf;
+    __nv_bfloat16* copy;
+    int64_t n;
+    uint32_t first;  // the launch's tile at which the tensor starts
+    uint32_t index;  // in the call
+    float wd, decay;
+};
+struct AdamwTable {
+    AdamwEntry e[kAdamwEntries];
+    int count;
+    uint32_t tiles;
+    float b1, c1, b2, c2;    // beta, 1 - beta
+    float eps, lr;
+    float step, root;        // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    float log_b1, log_b2;
+    const float* lr_at;      // these two replace lr, t and what follows from them
+    const int64_t* t_at;
+    const float* scale;
+    unsigned* amax;
+    uint32_t t, k0, k1;
+};
+
+// The entry that holds tile i.
+__device__ __forceinline__ int entry_of(const AdamwTable& t, uint32_t i)
+{
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.e[mid].first <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sqrt_approx(float x)
+{
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Philox4x32-10 (Salmon et al., SC'11) for values 8 unit .. 8 unit + 7: u[k] holds
+// the number of value 2 k in its low half and that of value 2 k + 1 in its high one.
+__device__ __forceinline__ void random8(const AdamwTable& a, uint32_t t, uint32_t unit, uint32_t word, uint32_t (&u)[4])
+{
+    uint32_t c0 = unit, c1 = 0, c2 = t, c3 = word, k0 = a.k0, k1 = a.k1;
+#pragma unroll
+    for (int round = 0; round < 10; ++round) {
+        const uint64_t x = uint64_t{0xD2511F53u} * c0, y = uint64_t{0xCD9E8D57u} * c2;
+        c0 = static_cast<uint32_t>(y >> 32) ^ c1 ^ k0;
+        c2 = static_cast<uint32_t>(x >> 32) ^ c3 ^ k1;
+        c1 = static_cast<uint32_t>(y);
+        c3 = static_cast<uint32_t>(x);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    u[0] = c0, u[1] = c1, u[2] = c2, u[3] = c3;
+}
+__device__ __forceinline__ uint32_t half_of(const uint32_t (&u)[4], int i) { return i & 1 ? u[i >> 1] >> 16 : u[i >> 1] & 0xFFFFu; }
+
+// The E4M3 code of |y| <= 448, up iff u16 < p 2^16.  From 2^-6 on a float's upper bits
+// are the code, and the 20 that go are p.  Below, adding 2^-6 brings the value to the
+// same spacing of 2^-9, one exponent up; rounding that sum up keeps the comparison,
+// whose left side is whole, what it is on the exact p.
+__device__ __forceinline__ uint32_t e4m3_sr(float y, uint32_t u16)
+{
+    const float a = fabsf(y);
+    const bool low = a < 0.015625f;
+    const uint32_t b = __float_as_uint(low ? __fadd_ru(a, 0.015625f) : a);
+    const uint32_t code = (b >> 20) - (low ? 968u : 960u) + ((u16 << 4) < (b & 0xFFFFFu) ? 1u : 0u);
+    return code | (__float_as_uint(y) >> 31) << 7;
+}
+
+// A moment in the 8-bit checkpoint's format: like encode_oct, but rounded
+// stochastically where SR, and with ROOT a value that is not zero keeps at least
+// the smallest code: a root that vanished would divide its first moment by eps.
+template <bool ROOT, bool SR>
+__device__ __forceinline__ uint2 encode_moment(Oct z, uint8_t& byte, const uint32_t (&u)[4])
+{
+    if constexpr (!ROOT && !SR)
+        return encode_oct(z, byte);
+    float m = max_abs(max_abs(max_abs(max_abs(0.0f, z.p[0]), z.p[1]), z.p[2]), z.p[3]);
+    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const bool odd = __any_sync(0xFFFFFFFFu, non_finite(m));
+    if (odd) {
+        m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[i] = finite_or_nan(z[i]);
+            m = fmaxf(m, fabsf(z[i]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    }
+    const uint32_t e = act8_byte(m);
+    byte = static_cast<uint8_t>(e);
+    const float s = act8_inverse(e);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = __fmul_rn(z[i], s);
+        if constexpr (ROOT)
+            y[i] = z[i] == 0.0f ? 0.0f : max_nan(y[i], 0.001953125f);
+    }
+    uint32_t w[2] = {0u, 0u};
+    if constexpr (SR) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i >> 2] |= (odd && y[i] != y[i] ? 0x7Fu : e4m3_sr(y[i], half_of(u, i))) << (8 * (i & 3));
+    } else {
+        w[0] = cvt_e4m3x2(y[0], y[1]) | cvt_e4m3x2(y[2], y[3]) << 16;
+        w[1] = cvt_e4m3x2(y[4], y[5]) | cvt_e4m3x2(y[6], y[7]) << 16;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// bf16 values by 16-bit numbers: up where the number is below the 16 bits that go.
+__device__ __forceinline__ void round_bf16_sr(Oct& p, const uint32_t (&u)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t b = __float_as_uint(p[i]);
+        if ((b & 0x7F800000u) != 0x7F800000u)
+            b += half_of(u, i) < (b & 0xFFFFu) ? 0x10000u : 0u;
+        else if (b & 0x7FFFFFu)
+            b |= 0x400000u;  // a NaN stays one
+        p[i] = __uint_as_float(b & 0xFFFF0000u);
+    }
+}
+
+// Each operation of the moments is rounded on its own, so that the codes of 8-bit ones
+// are a function of the formula alone.  The scalar intrinsics: the compiler fuses the
+// two-wide product and sum.
+__device__ __forceinline__ float first_moment(const AdamwTable& a, float m, float g)
+{
+    return __fadd_rn(__fmul_rn(m, a.b1), __fmul_rn(g, a.c1));
+}
+__device__ __forceinline__ float second_moment(const AdamwTable& a, float v, float g)
+{
+    return __fadd_rn(__fmul_rn(v, a.b2), __fmul_rn(__fmul_rn(g, g), a.c2));
+}
+
+// m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2, and the weight's step, which divides
+// by approximation (2^-21 of the step).
+// Of 8-bit moments the second one's root is kept: it spans half the octaves, and
+// E4M3's 18 then hold 36 of the moment's.
+template <typename P, typename G, int BITS, bool SR, bool ANY>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwTable a)
+{
+    const float scale = a.scale ? *a.scale : 1.0f;
+    float step = a.step, root = a.root, lr = a.lr;
+    uint32_t t = a.t;
+    if (a.lr_at || a.t_at) {
+        if (a.lr_at)
+            lr = *a.lr_at;
+        float n = static_cast<float>(a.t);
+        if (a.t_at) {
+            t = static_cast<uint32_t>(*a.t_at);
+            n = static_cast<float>(*a.t_at);
+        }
+        step = lr / -expm1f(n * a.log_b1);
+        root = 1.0f / sqrtf(-expm1f(n * a.log_b2));
+    }
+    const bool skip = scale != scale;
+    Top<P> top;
+    Top<__nv_bfloat16> top16;
+    int cur = -1;
+    auto flush = [&](int i, bool copied) {
+        if (a.amax)
+            copied ? flush_top(a.amax + a.e[i].index, top16) : flush_top(a.amax + a.e[i].index, top);
+        top = Top<P>();
+        top16 = Top<__nv_bfloat16>();
+    };
+    for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const int i = entry_of(a, tile);
+        const AdamwEntry& e = a.e[i];
+        if (cur >= 0 && i != cur)
+            flush(cur, a.e[cur].copy != nullptr);
+        cur = i;
+        const uint32_t unit = (tile - e.first) * kUnitsPerTile + threadIdx.x;
+        const Place at = {0, unit, static_cast<int32_t>(max(min(e.n - static_cast<int64_t>(unit) * 8, int64_t{8}), int64_t{0}))};
+        Unit<P, ANY> rp;
+        rp.load(e.p, 0, at, 1, e.n);
+        Oct p;
+        if (skip || !e.g) {
+            rp.get(p, at.cols);
+        } else {
+            Unit<G, ANY> rg;
+            rg.load(e.g, 0, at, 1, e.n);
+            Oct g, m, v;
+            if constexpr (BITS == 8) {
+                RawCodes cm, cv;
+                cm.clear(), cv.clear();
+                if (at.cols > 0) {
+                    cm.load({static_cast<uint8_t*>(e.m), e.m_sf}, unit);
+                    cv.load({static_cast<uint8_t*>(e.v), e.v_sf}, unit);
+                }
+                cm.get(m);
+                cv.get(v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v.p[k] = __fmul2_rn(v.p[k], v.p[k]);
+            } else {
+                Unit<float, ANY> rm, rv;
+                rm.load(e.m, 0, at, 1, e.n);
+                rv.load(e.v, 0, at, 1, e.n);
+                rm.get(m, at.cols);
+                rv.get(v, at.cols);
+            }
+            rp.get(p, at.cols);
+            rg.get(g, at.cols);
+            const float decay = a.lr_at ? 1.0f - lr * e.wd : e.decay;
+            Oct r;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float x = __fmul_rn(g.p[k].x, scale), y = __fmul_rn(g.p[k].y, scale);
+                m.p[k] = make_float2(first_moment(a, m.p[k].x, x), first_moment(a, m.p[k].y, y));
+                v.p[k] = make_float2(second_moment(a, v.p[k].x, x), second_moment(a, v.p[k].y, y));
+                if constexpr (BITS == 8)
+                    r.p[k] = make_float2(__fsqrt_rn(v.p[k].x), __fsqrt_rn(v.p[k].y));
+                else
+                    r.p[k] = make_float2(sqrt_approx(v.p[k].x), sqrt_approx(v.p[k].y));
+                const float2 d = __ffma2_rn(r.p[k], both(root), both(a.eps));
+                const float2 q = __fmul2_rn(m.p[k], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+                p.p[k] = __ffma2_rn(q, both(-step), __fmul2_rn(p.p[k], both(decay)));
+            }
+            uint32_t u[4] = {};
+            if constexpr (BITS == 8) {
+                if (at.cols < 8) {
+                    keep_first(m, at.cols);
+                    keep_first(r, at.cols);
+                }
+                uint8_t bm, bv;
+                if constexpr (SR)
+                    random8(a, t, unit, 4 * e.index, u);
+                const uint2 cm = encode_moment<false, SR>(m, bm, u);
+                if constexpr (SR)
+                    random8(a, t, unit, 4 * e.index + 1, u);
+                const uint2 cv = encode_moment<true, SR>(r, bv, u);
+                // whole groups: a tensor's last one is padded with zeros
+                if (static_cast<int64_t>(unit) * 8 < (e.n + 31) / 32 * 32) {
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + static_cast<int64_t>(unit) * 8) = cm;
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + static_cast<int64_t>(unit) * 8) = cv;
+                    if ((threadIdx.x & 3) == 0) {
+                        e.m_sf[unit >> 2] = bm;
+                        e.v_sf[unit >> 2] = bv;
+                    }
+                }
+            } else {
+                Top<float> unused;
+                store_unit<float, ANY>(e.m, 0, at, m, e.n, unused);
+                store_unit<float, ANY>(e.v, 0, at, v, e.n, unused);
+            }
+            if constexpr (SR && sizeof(P) == 2) {
+                random8(a, t, unit, 4 * e.index + 2, u);
+                round_bf16_sr(p, u);
+            }
+        }
+        store_unit<P, ANY>(e.p, 0, at, p, e.n, top);
+        if constexpr (sizeof(P) == 4)
+            if (e.copy)
+                store_unit<__nv_bfloat16, ANY>(e.copy, 0, at, p, e.n, top16);
+    }
+    if (cur >= 0)
+        flush(cur, a.e[cur].copy != nullptr);
+}
+
+template <typename P, typename G, int BITS, bool SR, bool ANY>
+int launch_adamw(const AdamwTable& t, const Device& d, cudaStream_t s)
+{
+    constexpr auto kernel = adamw_kernel<P, G, BITS, SR, ANY>;
+    const unsigned most = static_cast<unsigned>(d.sms * resident_ctas<kernel>(kThreads));
+    return launch_kernel(kernel, std::min(t.tiles, most), 1, kThreads, 0, false, s, t);
+}
+template <typename P, typename G, int BITS, bool SR>
+int launch_adamw(const AdamwTable& t, bool any, const Device& d, cudaStream_t s)
+{
+    return any ? launch_adamw<P, G, BITS, SR, true>(t, d, s) : launch_adamw<P, G, BITS, SR, false>(t, d, s);
+}
+template <typename P, typename G>
+int launch_adamw(const AdamwTable& t, int bits, bool sr, bool any, const Device& d, cudaStream_t s)
+{
+    if (bits == 8)
+        return sr ? launch_adamw<P, G, 8, true>(t, any, d, s) : launch_adamw<P, G, 8, false>(t, any, d, s);
+    if constexpr (sizeof(P) == 2)
+        if (sr)
+            return launch_adamw<P, G, 32, true>(t, any, d, s);
+    return launch_adamw<P, G, 32, false>(t, any, d, s);
+}
+
+bool at_16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+uint32_t tiles_of(int64_t n) { return static_cast<uint32_t>((n + 8 * kUnitsPerTile - 1) / (8 * kUnitsPerTile)); }
+
+}  // namespace
+
+int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_opts& o, const float* scale, float* amax,
+                 const Device& d, cudaStream_t s)
+{
+    AdamwTable t;
+    t.b1 = static_cast<float>(o.beta1);
+    t.c1 = static_cast<float>(1.0 - o.beta1);
+    t.b2 = static_cast<float>(o.beta2);
+    t.c2 = static_cast<float>(1.0 - o.beta2);
+    t.eps = static_cast<float>(o.eps);
+    t.lr = static_cast<float>(o.lr);
+    t.step = static_cast<float>(o.lr / -std::expm1(static_cast<double>(o.t) * std::log(o.beta1)));
+    t.root = static_cast<float>(1.0 / std::sqrt(-std::expm1(static_cast<double>(o.t) * std::log(o.beta2))));
+    t.log_b1 = static_cast<float>(std::log(o.beta1));
+    t.log_b2 = static_cast<float>(std::log(o.beta2));
+    t.lr_at = o.lr_at;
+    t.t_at = o.t_at;
+    t.scale = scale;
+    t.amax = reinterpret_cast<unsigned*>(amax);
+    t.t = static_cast<uint32_t>(o.t);
+    t.k0 = static_cast<uint32_t>(o.seed);
+    t.k1 = static_cast<uint32_t>(o.seed >> 32);
+    // one launch for each kind of tensor (types, 8-bit moments, alignment) and 128 of them
+    for (int kind = 0; kind < 16; ++kind) {
+        const bool p16 = kind & 1, g16 = kind & 2, eight = kind & 4, any = kind & 8;
+        t.count = 0;
+        t.tiles = 0;
+        auto flush = [&]() -> int {
+            if (t.count == 0)
+                return MX_OK;
+            const int bits = eight ? 8 : 32;
+            const bool sr = o.rounding == MX_ROUND_SR;
+            const int rc = p16 ? (g16 ? launch_adamw<__nv_bfloat16, __nv_bfloat16>(t, bits, sr, any, d, s)
+                                      : launch_adamw<__nv_bfloat16, float>(t, bits, sr, any, d, s))
+                               : (g16 ? launch_adamw<float, __nv_bfloat16>(t, bits, sr, any, d, s)
+                                      : launch_adamw<float, float>(t, bits, sr, any, d, s));
+            t.count = 0;
+            t.tiles = 0;
+            return rc;
+        };
+        for (int64_t i = 0; i < count; ++i) {
+            const mx_adamw_tensor& x = tensors[i];
+            const bool whole = x.n % 8 == 0 && at_16(x.param) && at_16(x.grad) && at_16(x.copy) &&
+                               (x.bits == 8 || (at_16(x.m) && at_16(x.v)));
+            if (x.n == 0 || (x.p_dtype == MX_OUT_BF16) != p16 || (x.g_dtype == MX_OUT_BF16) != g16 ||
+                (x.bits == 8) != eight || whole == any)
+                continue;
+            const uint32_t tiles = tiles_of(x.n);
+            if (t.count == kAdamwEntries || t.tiles + static_cast<uint64_t>(tiles) > 0x7FFFFFFFu) {
+                const int rc = flush();
+                if (rc != MX_OK)
+                    return rc;
+            }
+            AdamwEntry& e = t.e[t.count++];
+            e.p = x.param;
+            e.g = x.grad;
+            e.m = x.m;
+            e.v = x.v;
+            e.m_sf = x.m_sf;
+            e.v_sf = x.v_sf;
+            e.copy = static_cast<__nv_bfloat16*>(x.copy);
+            e.n = x.n;
+            e.first = t.tiles;
+            e.index = static_cast<uint32_t>(i);
+            e.wd = static_cast<float>(x.weight_decay);
+            e.decay = static_cast<float>(1.0 - o.lr * x.weight_decay);
+            t.tiles += tiles;
+        }
+        const int rc = flush();
+        if (rc != MX_OK)
+            return rc;
+    }
+    return MX_OK;
+}
+
+// ---------------------------------------------------------------- gradient norm
+namespace {
+
+constexpr int kNormEntries = 512;
+constexpr int kNormUnits = 4;  // octs a thread in flight
+struct NormEntry {
+    const void* g;
+    int64_t n;
+    uint32_t first, bf16;
+};
+struct NormTable {
+    NormEntry e[kNormEntries];
+    int count;
+    uint32_t tiles;
+    double* parts;
+};
+
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double of_warp[kThreads / 32];
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, k);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        of_warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int k = 0; k < kThreads / 32; ++k)
+        v += of_warp[k];
+    return v;
+}
+
+template <typename G>
+__device__ __forceinline__ float squares(const NormEntry& e, uint32_t tile)
+{
+    const bool any = !((reinterpret_cast<uintptr_t>(e.g) & 15) == 0 && e.n % 8 == 0);
+    const int64_t first = static_cast<int64_t>(tile - e.first) * (kThreads * kNormUnits) + threadIdx.x;
+    float2 sum = both(0.0f);
+    auto add = [&](const Oct& o) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sum = __ffma2_rn(o.p[j], o.p[j], sum);
+    };
+    auto place = [&](int k) {
+        const int64_t unit = first + k * kThreads;
+        return Place{0, static_cast<uint32_t>(unit), static_cast<int32_t>(max(min(e.n - unit * 8, int64_t{8}), int64_t{0}))};
+    };
+    if (!any) {
+        Unit<G, false> w[kNormUnits];
+#pragma unroll
+        for (int k = 0; k < kNormUnits; ++k)
+            w[k].load(e.g, 0, place(k), 1, e.n);
+#pragma unroll
+        for (int k = 0; k < kNormUnits; ++k) {
+            Oct o;
+            w[k].get(o, 8);
+            add(o);
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < kNormUnits; ++k) {
+            const Place at = place(k);
+            Unit<G, true> w;
+            w.load(e.g, 0, at, 1, e.n);
+            Oct o;
+            w.get(o, at.cols);
+            add(o);
+        }
+    }
+    return sum.x + sum.y;
+}
+
+// Squares and the sums of a thread's 32 values in fp32, everything above in fp64:
+// no chain of fp32 additions grows with the tensors.  Partial sums by tile order and
+// CTA, which the shapes alone fix.
+__global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ NormTable a)
+{
+    let_next_launch_start();
+    double sum = 0.0;
+    for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        int lo = 0, hi = a.count;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.e[mid].first <= tile)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const NormEntry& e = a.e[lo];
+        sum += e.bf16 ? squares<__nv_bfloat16>(e, tile) : squares<float>(e, tile);
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0)
+        a.parts[blockIdx.x] = sum;
+}
+
+// out[0] = the norm, out[1] = min(1, max_norm / (norm + 1e-6)), NaN for a norm that is
+// not finite.
+__global__ void __launch_bounds__(kThreads) norm_join_kernel(const double* parts, int count, double max_norm, float* out)
+{
+    wait_for_launch_before();
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < count; i += kThreads)
+        sum += parts[i];
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sum);
+        out[0] = static_cast<float>(norm);
+        const double f = max_norm / (norm + 1e-6);
+        out[1] = isfinite(norm) ? static_cast<float>(f < 1.0 ? f : 1.0) : __int_as_float(0x7FC00000);
+    }
+}
+
+}  // namespace
+
+int64_t grad_norm_parts(int64_t count) { return (count / kNormEntries + 1) * kGradNormCtas; }
+
+int launch_grad_norm(const mx_grad* grads, int64_t count, double max_norm, float* out, double* parts, const Device& d,
+                     cudaStream_t s)
+{
+    NormTable t;
+    t.count = 0;
+    t.tiles = 0;
+    int used = 0;
+    auto flush = [&]() -> int {
+        const unsigned most =
+            std::min<unsigned>(kGradNormCtas, d.sms * resident_ctas<square_sum_kernel>(kThreads));
+        const unsigned ctas = std::min(t.tiles, most);
+        t.parts = parts + used;
+        used += static_cast<int>(ctas);
+        const int rc = ctas ? launch_kernel(square_sum_kernel, ctas, 1, kThreads, 0, false, s, t) : MX_OK;
+        t.count = 0;
+        t.tiles = 0;
+        return rc;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        if (grads[i].n == 0)
+            continue;
+        if (t.count == kNormEntries) {
+            const int rc = flush();
+            if (rc != MX_OK)
+                return rc;
+        }
+        NormEntry& e = t.e[t.count++];
+        e.g = grads[i].data;
+        e.n = grads[i].n;
+        e.first = t.tiles;
+        e.bf16 = grads[i].dtype == MX_OUT_BF16;
+        t.tiles += static_cast<uint32_t>((e.n + 8 * kThreads * kNormUnits - 1) / (8 * kThreads * kNormUnits));
+    }
+    int rc = flush();
+    if (rc == MX_OK)
+        rc = launch_kernel(norm_join_kernel, 1, 1, kThreads, 0, used > 0, s, static_cast<const double*>(parts), used, max_norm,
+                           out);
+    return rc;
+}
+
+}  // namespace mx

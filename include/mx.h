@@ -451,6 +451,91 @@ int mx_act_bwd(const void* dh, int64_t ldh, const void* gate, int64_t ldg, const
                const mx_act8* gate8, const mx_act8* up8, int64_t rows, int64_t cols, int act, int dtype, void* dgate,
                int64_t lddg, void* dup, int64_t lddu, float* amax_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The weights' update after the backward calls: the gradients' norm and the
+ * optimizer's step, over many tensors at once.  The rules of the calls above
+ * hold where they apply: stream order, no allocation, no reduction whose
+ * result depends on the order of atomics, capture into CUDA graphs.  Arrays of
+ * descriptors are host memory, read before the call returns; the tensors are
+ * contiguous device memory that needs the alignment of its elements only
+ * (16-byte aligned tensors of a multiple of eight values take wide accesses). */
+
+typedef struct mx_grad {
+    const void* data;
+    int64_t n;       /* 0 <= n <= 2^34 */
+    int32_t dtype;   /* mx_out_dtype */
+    int32_t reserved;
+} mx_grad;
+
+/* Workspace bytes of mx_grad_norm (0 for a negative count). */
+size_t mx_grad_norm_workspace_bytes(int64_t count);
+
+/* out[0] = sqrt(sum of the squares of all values), out[1] = the factor that
+ * brings the norm down to max_norm, min(1, max_norm / (out[0] + 1e-6)), or NaN
+ * when the norm is not finite: as grad_scale it makes mx_adamw_step leave the
+ * weights alone.  Squares are fp32 (values above 1.8e19 have none, those below
+ * 2^-75 count as 0), sums of more than 32 of them fp64.  max_norm > 0; +Inf
+ * gives the factor 1.  out: two device floats, 4-byte aligned; workspace:
+ * device, 8-byte aligned. */
+int mx_grad_norm(const mx_grad* grads, int64_t count, double max_norm, float* out, void* workspace, size_t ws_bytes,
+                 void* stream);
+
+/* One tensor of mx_adamw_step.
+ *   bits 32: m and v are fp32 [n].
+ *   bits 8:  m and v are checkpoints (mx_act8, one row of n columns) of the
+ *            first moment and of the second one's square root: codes
+ *            [32 ceil(n / 32)], 16-byte aligned, and bytes m_sf / v_sf
+ *            [ceil(n / 32)].  Zeros are a valid start. */
+typedef struct mx_adamw_tensor {
+    void* param;            /* [n], p_dtype, updated in place */
+    const void* grad;       /* [n], g_dtype; NULL: param, m and v stay as they are */
+    void* m;
+    void* v;
+    uint8_t* m_sf;          /* bits 8 only */
+    uint8_t* v_sf;
+    void* copy;             /* bf16 [n] or NULL; with p_dtype F32 only: param rounded to nearest even */
+    int64_t n;              /* 0 <= n <= 2^34 */
+    double weight_decay;
+    int32_t p_dtype, g_dtype;
+    int32_t bits;
+    int32_t reserved;
+} mx_adamw_tensor;
+
+typedef struct mx_adamw_opts {
+    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps >= 0 */
+    int64_t t;                     /* this step's number, from 1 */
+    const float* lr_at;            /* optional device words that replace lr and t, */
+    const int64_t* t_at;           /* read when the kernel runs (captured graphs) */
+    uint64_t seed;                 /* MX_ROUND_SR */
+    int32_t rounding;              /* mx_rounding of 8-bit moments and of bf16 params */
+    int32_t reserved;
+} mx_adamw_opts;
+
+/* AdamW, for every tensor i and value:
+ *   g = grad_scale * grad
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32; the step takes m and v as computed, before 8-bit moments are rounded.
+ * m and v round after each product and sum, so that the codes of 8-bit moments
+ * follow from the formula alone.  A root that is not zero keeps at least its
+ * group's smallest code, 2^-9 2^e; Inf and NaN become the NaN code.  MX_ROUND_SR:
+ * value L of tensor i rounds up iff u16 < p 2^16 as in mx_rounding, the numbers
+ * from Philox4x32-10(counter = {L >> 3, L >> 35, t, 4 i + k}, key = {seed, seed >> 32}),
+ * k = 0 for m, 1 for the root, 2 for a bf16 param.  (With beta2 = 0.999 a step
+ * changes a root by 0.05 %, far less than a code's distance to the next, 6 to
+ * 12 %: rounded to nearest, 8-bit roots only ever follow large gradients up.)
+ *   grad_scale  optional device float (NULL: 1).  NaN: params, m and v stay as
+ *               they are (copies and amax_out are written all the same).
+ *   amax_out    optional device floats [count]: max |value| of each tensor's
+ *               copy, or param without one, as written; the w_amax / amax_in of
+ *               its next quantization.  NaN if any is NaN.
+ * No two of the written tensors may overlap.  Errors: MX_ERR_INVALID_ARG for
+ * null pointers, sizes, enums and numbers out of range, MX_ERR_ALIGNMENT,
+ * MX_ERR_UNSUPPORTED for a copy of a bf16 param. */
+int mx_adamw_step(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_opts* opts, const float* grad_scale,
+                  float* amax_out, void* stream);
+
 /* Human-readable text of an mx_status. */
 const char* mx_strerror(int status);
 
