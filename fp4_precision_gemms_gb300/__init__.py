@@ -35,6 +35,7 @@ EXPORTED = ("mx_codes_bytes", "mx_sf_bytes", "mx_scale_count", "mx_amax", "mx_qu
             "mx_linear_saved_bytes", "mx_linear_fwd_save", "mx_linear_bwd_saved", "mx_strerror",
             "mx_act8_codes_bytes", "mx_act8_sf_bytes", "mx_act8_save", "mx_act8_restore", "mx_norm_fwd",
             "mx_norm_bwd_workspace_bytes", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd",
+            "mx_gemm_gated", "mx_gated_workspace_bytes", "mx_gated_fwd", "mx_gated_fwd_save", "mx_gated_bwd",
             "mx_grad_norm_workspace_bytes", "mx_grad_norm", "mx_adamw_step",
             "mx_last_device_status", "mx_selftest_bounded_wait", "mx_launch_count",
             "mx_debug_divide", "mx_debug_set_quant_impl", "mx_debug_set_tile_fail_at", "mx_debug_set_norm_fail_at", "mx_debug_set_bwd_fork", "mx_debug_set_gemm_variant",
@@ -162,6 +163,17 @@ def lib():
             L.mx_act_fwd.argtypes = [p, i64, p, i64, i64, i64, i32, i32, p, i64, a8, a8, p, p]
             L.mx_act_bwd.argtypes = [p, i64, p, i64, p, i64, a8, a8, i64, i64, i32, i32, p, i64, p, i64, p, p]
             for name in ("mx_act8_save", "mx_act8_restore", "mx_norm_fwd", "mx_norm_bwd", "mx_act_fwd", "mx_act_bwd"):
+                getattr(L, name).restype = i32
+            t8 = C.POINTER(_CTensor)
+            L.mx_gated_workspace_bytes.restype = sz
+            L.mx_gated_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+            L.mx_gemm_gated.argtypes = [t8, t8, t8, i32, p, i64, a8, a8, p, p]
+            L.mx_gated_fwd.argtypes = [p, i64, i64, i64, i64, i32, i32, p, t8, t8, p, i64, p, p, sz, p]
+            L.mx_gated_fwd_save.argtypes = [p, i64, p, i64, i64, i64, i32, i32, p, p, C.POINTER(_CBwdOpts), p, i64, a8, a8,
+                                            p, p, sz, p, sz, p]
+            L.mx_gated_bwd.argtypes = [p, i64, i64, i64, i64, i32, i32, a8, a8, C.POINTER(_CBwdOpts), p, sz, p, i32, p,
+                                       i32, p, sz, p]
+            for name in ("mx_gemm_gated", "mx_gated_fwd", "mx_gated_fwd_save", "mx_gated_bwd"):
                 getattr(L, name).restype = i32
             L.mx_grad_norm_workspace_bytes.restype = sz
             L.mx_grad_norm_workspace_bytes.argtypes = [i64]
@@ -862,6 +874,195 @@ def act_bwd(dh: torch.Tensor, gate: torch.Tensor | Act8, up: torch.Tensor | Act8
          _look_up(ACTS, act, "act"), OUT[dt], pdg, lddg, pdu, lddu,
          _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None)
     return dgate, dup
+
+
+# ---------------------------------------------------------------- gated feed-forward block
+class GatedOut(NamedTuple):
+    """gated_fwd_save's results: h; saved (the X^T and W^T operands) and the
+    checkpoints of both projections' outputs, which gated_bwd reads."""
+    h: torch.Tensor
+    saved: torch.Tensor
+    gate: Act8
+    up: Act8
+
+
+_BF16 = torch.bfloat16
+_GATED_PASSES = {"fwd": 0, "bwd": 1, "fwd_quantized": 2}
+
+
+def gated_workspace_bytes(T: int, Kin: int, F: int, fmt: str, pass_: str = "fwd") -> int:
+    """Workspace of gated_fwd from W and gated_fwd_save ("fwd"), gated_bwd ("bwd") and
+    gated_fwd from quantized weights ("fwd_quantized")."""
+    return int(lib().mx_gated_workspace_bytes(T, Kin, F, _look_up(FORMATS, fmt, "fmt"),
+                                              _look_up(_GATED_PASSES, pass_, "pass_")))
+
+
+def _memory(t, n, dev, what):
+    """(tensor, pointer, bytes) of a buffer of at least n bytes: a new one, or the one given."""
+    if t is None:
+        t = torch.empty(n, dtype=_U8, device=dev)
+    elif t.device != dev or not t.is_contiguous():
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must be contiguous memory on {dev}")
+    return t, t.data_ptr(), t.numel() * t.element_size()
+
+
+def _bf16_rows(t, what):
+    px, ld, rows, cols, dev, dt = _first(t, what)
+    if dt is not _BF16:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} has type {dt}, expected bfloat16")
+    return px, ld, rows, cols, dev
+
+
+def _gate_up(W, cols, dev):
+    """(pointer of W [2 F, cols], F)."""
+    if W.dim() != 2 or W.shape[0] % 2 or W.shape[1] != cols:
+        raise MXError(MX_ERR_INVALID_ARG, f"W has shape {tuple(W.shape)}, expected (2 F, {cols})")
+    if W.dtype is not _BF16 or W.device != dev or not W.is_contiguous():
+        raise MXError(MX_ERR_INVALID_ARG, f"W must be contiguous bfloat16 on {dev}")
+    return W.data_ptr(), W.shape[0] // 2
+
+
+def _operand(q, fmt, cols, dev, what):
+    if not isinstance(q, MXTensor) or q.fmt != fmt or q.k != cols or q.codes.device != dev:
+        raise MXError(MX_ERR_INVALID_ARG, f"{what} must be an MXTensor of {fmt} with k = {cols} on {dev}")
+    return q._c()
+
+
+def gated_weights(W: torch.Tensor, fmt: str, stream=None):
+    """(gate, up): the two halves of W [2 F, Kin] (gate rows first) quantized once, for
+    gated_fwd, under one tensor scale where the format has one."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_weights(W, fmt)
+    _look_up(FORMATS, fmt, "fmt")
+    if not W.is_cuda:
+        _on_gpu(W)
+    if W.dim() != 2:
+        raise MXError(MX_ERR_INVALID_ARG, f"W must be a matrix, not of shape {tuple(W.shape)}")
+    _, F = _gate_up(W, W.shape[1], W.device)
+    with torch.cuda.device(W.device):
+        top = amax(W) if fmt in ("nvfp4", "moss") else None
+        return quantize(W[:F], fmt, amax_in=top), quantize(W[F:], fmt, amax_in=top)
+
+
+def gemm_gated(a: MXTensor, gate: MXTensor, up: MXTensor, act: str = "silu", save: bool = False,
+               amax_out: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> ActOut:
+    """h = act(dq(a) dq(gate)^T) * (dq(a) dq(up)^T) in bfloat16, one kernel.  save keeps
+    the 8-bit checkpoints of both products; amax_out: one fp32 word, max |h|."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gemm_gated(a, gate, up, act, save, amax_out, out)
+    dev = a.codes.device
+    ca, cg, cu = a._c(), _operand(gate, a.fmt, a.k, dev, "gate"), _operand(up, a.fmt, a.k, dev, "up")
+    rows, F = a.rows, gate.rows
+    if out is None:
+        out = torch.empty((rows, -(-F // 8) * 8), dtype=_BF16, device=dev)[:, :F]
+    ph, ldh = _mat(out, rows, F, dev, "out", _BF16)
+    g8, c8 = _save_to(None, rows, F, dev) if save else (None, None)
+    u8, cu8 = _save_to(None, rows, F, dev) if save else (None, None)
+    _run(dev, "mx_gemm_gated", lib().mx_gemm_gated, ca, cg, cu, _look_up(ACTS, act, "act"), ph, -(-ldh // 8) * 8 if rows <= 1 else ldh,
+         c8, cu8, _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None)
+    return ActOut(out, g8, u8)
+
+
+def gated_fwd(X: torch.Tensor, W, fmt: str, act: str = "silu", amax_out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h [T, F] = act(X Wg^T) * (X Wu^T), X [T, Kin] bfloat16 quantized within the call.
+    W: [2 F, Kin] bfloat16 (gate rows first), quantized within the call too, or
+    gated_weights(W, fmt).  amax_out: one fp32 word, max |h| (the x_amax of the next
+    linear).  The rows of h start at multiples of eight values."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_fwd(X, W, fmt, act, amax_out, workspace, out)
+    px, ldx, T, Kin, dev = _bf16_rows(X, "X")
+    number, kind = _look_up(FORMATS, fmt, "fmt"), _look_up(ACTS, act, "act")
+    pw = cg = cu = None
+    if isinstance(W, torch.Tensor):
+        pw, F = _gate_up(W, Kin, dev)
+    else:
+        gate, up = W
+        cg, cu = _operand(gate, fmt, Kin, dev, "gate"), _operand(up, fmt, Kin, dev, "up")
+        F = gate.rows
+    if out is None:
+        out = torch.empty((T, -(-F // 8) * 8), dtype=_BF16, device=dev)
+        if F % 8:
+            out = out[:, :F]
+    ph, ldh = _mat(out, T, F, dev, "out", _BF16)
+    L = lib()
+    workspace, pws, n = _memory(workspace, L.mx_gated_workspace_bytes(T, Kin, F, number, 2 if pw is None else 0), dev,
+                                "workspace")
+    _run(dev, "mx_gated_fwd", L.mx_gated_fwd, px, ldx, T, Kin, F, number, kind, pw, cg, cu, ph,
+         -(-ldh // 8) * 8 if T <= 1 else ldh, _vec(amax_out, 1, dev, "amax_out") if amax_out is not None else None, pws, n)
+    return out
+
+
+def gated_fwd_save(X: torch.Tensor, W: torch.Tensor, fmt: str, act: str = "silu", wgrad_hadamard: bool = False,
+                   wgrad_dy_rounding: str = "rne", seed: int = 0, stream_id: int = 0,
+                   x_amax: torch.Tensor | None = None, w_amax: torch.Tensor | None = None,
+                   amax_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   saved: torch.Tensor | None = None, gate8: Act8 | None = None, up8: Act8 | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> GatedOut:
+    """gated_fwd from W [2 F, Kin], keeping what gated_bwd reads: the X^T and W^T
+    operands (as linear_fwd_save does) and 8-bit checkpoints of both projections'
+    outputs.  Pass the same backward options to gated_bwd."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_fwd_save(X, W, fmt, act, wgrad_hadamard, wgrad_dy_rounding, seed, stream_id, x_amax, w_amax,
+                                  amax_out, workspace, saved, gate8, up8, out)
+    px, ldx, T, Kin, dev = _bf16_rows(X, "X")
+    number, kind = _look_up(FORMATS, fmt, "fmt"), _look_up(ACTS, act, "act")
+    pw, F = _gate_up(W, Kin, dev)
+    if out is None:
+        out = torch.empty((T, F), dtype=_BF16, device=dev)
+    ph, ldh = _mat(out, T, F, dev, "out", _BF16)
+    L = lib()
+    workspace, pws, n = _memory(workspace, L.mx_gated_workspace_bytes(T, Kin, F, number, 0), dev, "workspace")
+    saved, psv, ns = _memory(saved, L.mx_linear_saved_bytes(T, Kin, 2 * F, number), dev, "saved")
+    gate8, cg = _save_to(gate8, T, F, dev)
+    up8, cu = _save_to(up8, T, F, dev)
+    o = _CBwdOpts(int(bool(wgrad_hadamard)), _look_up(ROUNDING, wgrad_dy_rounding, "wgrad_dy_rounding"), seed, stream_id, 0)
+    one = lambda t, what: _vec(t, 1, dev, what) if t is not None else None  # noqa: E731
+    _run(dev, "mx_gated_fwd_save", L.mx_gated_fwd_save, px, ldx, pw, T, Kin, F, number, kind, one(x_amax, "x_amax"),
+         one(w_amax, "w_amax"), o, ph, ldh, cg, cu, one(amax_out, "amax_out"), pws, n, psv, ns)
+    return GatedOut(out, saved, gate8, up8)
+
+
+def gated_bwd(dH: torch.Tensor, kept: GatedOut, Kin: int, fmt: str, act: str = "silu", wgrad_hadamard: bool = False,
+              wgrad_dy_rounding: str = "rne", seed: int = 0, stream_id: int = 0, dx_dtype=torch.bfloat16,
+              dw_dtype=torch.float32, need_dx: bool = True, need_dw: bool = True,
+              workspace: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+              dW: torch.Tensor | None = None, stream=None):
+    """(dX [T, Kin], dW [2 F, Kin]) of gated_fwd_save from dH [T, F] (bfloat16) and what
+    it kept (kept.h is not read)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_bwd(dH, kept, Kin, fmt, act, wgrad_hadamard, wgrad_dy_rounding, seed, stream_id, dx_dtype, dw_dtype,
+                             need_dx, need_dw, workspace, dX, dW)
+    pd, ldd, T, F, dev = _bf16_rows(dH, "dH")
+    number, kind = _look_up(FORMATS, fmt, "fmt"), _look_up(ACTS, act, "act")
+    cg, cu = kept.gate._c(dev, T, F), kept.up._c(dev, T, F)
+    pdx = pdw = None
+    if need_dx:
+        if dX is None:
+            _look_up(OUT, dx_dtype, "dx_dtype")
+            dX = torch.empty((T, Kin), dtype=dx_dtype, device=dev)
+        pdx, ld = _mat(dX, T, Kin, dev, "dX")
+        if ld != Kin:
+            raise MXError(MX_ERR_INVALID_ARG, "dX must be contiguous")
+    if need_dw:
+        if dW is None:
+            _look_up(OUT, dw_dtype, "dw_dtype")
+            dW = torch.empty((2 * F, Kin), dtype=dw_dtype, device=dev)
+        pdw, ld = _mat(dW, 2 * F, Kin, dev, "dW")
+        if ld != Kin:
+            raise MXError(MX_ERR_INVALID_ARG, "dW must be contiguous")
+    L = lib()
+    workspace, pws, n = _memory(workspace, L.mx_gated_workspace_bytes(T, Kin, F, number, 1), dev, "workspace")
+    _, psv, ns = _memory(kept.saved, 0, dev, "saved")
+    o = _CBwdOpts(int(bool(wgrad_hadamard)), _look_up(ROUNDING, wgrad_dy_rounding, "wgrad_dy_rounding"), seed, stream_id, 0)
+    _run(dev, "mx_gated_bwd", L.mx_gated_bwd, pd, ldd, T, Kin, F, number, kind, cg, cu, o, psv, ns, pdx,
+         OUT[dX.dtype] if need_dx else 0, pdw, OUT[dW.dtype] if need_dw else 0, pws, n)
+    return (dX if need_dx else None), (dW if need_dw else None)
 
 
 # ---------------------------------------------------------------- gradient norm and optimizer step

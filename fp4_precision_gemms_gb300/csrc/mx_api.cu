@@ -3,6 +3,7 @@
 // quantize + GEMM into a linear layer's forward, data-gradient and
 // weight-gradient passes.
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "mx_internal.cuh"
@@ -815,6 +816,310 @@ int mx_linear_bwd_saved(const void* dY, int64_t T, int64_t Kin, int64_t Nout, in
             rc = rj;
     }
     return rc;
+}
+
+namespace {
+
+// The backward options' default (RNE, no Hadamard) where none are given.
+mx_bwd_opts bwd_opts_or_default(const mx_bwd_opts* opts)
+{
+    mx_bwd_opts o;
+    std::memset(&o, 0, sizeof o);
+    return opts ? *opts : o;
+}
+
+bool valid_act(int act) { return act >= MX_ACT_SILU && act <= MX_ACT_GELU_TANH; }
+
+bool gated_shape(int64_t T, int64_t Kin, int64_t F, int fmt)
+{
+    return valid_fmt(fmt) && T >= 0 && Kin >= 0 && F >= 0 && T <= INT32_MAX && Kin <= INT32_MAX && F <= INT32_MAX / 2;
+}
+
+int check_checkpoint(const mx_act8* a, int64_t rows, int64_t cols)
+{
+    if (a->rows != rows || a->cols != cols || (rows > 0 && cols > 0 && (!a->codes || !a->sf)))
+        return MX_ERR_INVALID_ARG;
+    return aligned16(a->codes) ? MX_OK : MX_ERR_ALIGNMENT;
+}
+
+Act8View checkpoint_view(const mx_act8* a) { return a ? Act8View{a->codes, a->sf} : Act8View{}; }
+
+// Rows from .. from + rows - 1 of an operand, from a multiple of 128: they start a
+// row tile of the scale layout.
+mx_tensor operand_rows(const mx_tensor& t, int64_t from, int64_t rows)
+{
+    mx_tensor v = t;
+    v.codes = static_cast<uint8_t*>(t.codes) + from * codes_row_bytes(t.fmt, t.k);
+    v.sf = t.sf + sf_layout_bytes(from, t.k / t.block);
+    if (fmt_is_local(t.fmt)) {
+        v.amax = t.amax + from / kLocalRegion;
+        v.tensor_scale = t.tensor_scale + from / kLocalRegion;
+    }
+    v.rows = rows;
+    return v;
+}
+
+int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const float* amax_out)
+{
+    if (reinterpret_cast<uintptr_t>(amax_out) % 4 != 0)
+        return MX_ERR_ALIGNMENT;
+    if (T == 0 || F == 0)
+        return MX_OK;
+    if (!h || ldh < F)
+        return MX_ERR_INVALID_ARG;
+    return ldh % 8 == 0 && aligned16(h) ? MX_OK : MX_ERR_ALIGNMENT;
+}
+
+int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
+                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, const Device& d, cudaStream_t s)
+{
+    for (const mx_tensor* t : {A, gate, up}) {
+        const int rc = check_operand(t);
+        if (rc != MX_OK)
+            return rc;
+        if (t->fmt != A->fmt || t->k != A->k)
+            return MX_ERR_INVALID_ARG;
+        if (t->hadamard)
+            return MX_ERR_UNSUPPORTED;
+    }
+    const int64_t T = A->rows, F = gate->rows, K = A->k;
+    if (up->rows != F || !valid_act(act) || !gate8 != !up8)
+        return MX_ERR_INVALID_ARG;
+    if (T > INT32_MAX || F > INT32_MAX / 2 || K > INT32_MAX || K == 0)
+        return MX_ERR_UNSUPPORTED;
+    if (K % gemm_k_multiple(A->fmt) != 0)
+        return MX_ERR_ALIGNMENT;
+    int rc = check_gated_output(h, ldh, T, F, amax_out);
+    for (const mx_act8* c : {gate8, up8})
+        if (c && rc == MX_OK)
+            rc = check_checkpoint(c, T, F);
+    if (rc != MX_OK)
+        return rc;
+    if (amax_out && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess)
+        return MX_ERR_CUDA;
+    if (T == 0 || F == 0)
+        return MX_OK;
+    GatedArgs a;
+    a.x = A;
+    a.gate = gate;
+    a.up = up;
+    a.act = act;
+    a.h = h;
+    a.ldh = ldh;
+    a.gate8 = checkpoint_view(gate8);
+    a.up8 = checkpoint_view(up8);
+    a.amax = reinterpret_cast<unsigned*>(amax_out);
+    return launch_gated(a, d, s);
+}
+
+// The weights' two halves as operands of their own under W's tensor scale.
+int quantize_halves(const void* W, int64_t Kin, int64_t F, int fmt, const float* amax, mx_tensor* gate, mx_tensor* up,
+                    const Device& d, cudaStream_t s)
+{
+    const uint16_t* w = static_cast<const uint16_t*>(W);
+    for (int half = 0; half < 2; ++half) {
+        const int rc = quantize_impl(w + half * F * Kin, F, Kin, Kin, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE,
+                                     MX_SCALE_DEFAULT, 0, 0, 0, amax, half ? up : gate, d, s);
+        if (rc != MX_OK)
+            return rc;
+    }
+    return MX_OK;
+}
+
+// Bytes of the quantized weights in a workspace: one operand of 2F rows, or two of F.
+size_t carve_gated_weights(uint8_t* ws, int fmt, int64_t Kin, int64_t F, mx_tensor* w, mx_tensor* gate, mx_tensor* up)
+{
+    if (F % 128 == 0)
+        return carve(ws, fmt, 2 * F, Kin, w);
+    const size_t off = carve(ws, fmt, F, Kin, gate);
+    return off + carve(ws ? ws + off : nullptr, fmt, F, Kin, up);
+}
+
+}  // namespace
+
+int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
+                  const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* stream)
+{
+    Device d;
+    const int rc = current_device(&d);
+    if (rc != MX_OK)
+        return rc;
+    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, d, static_cast<cudaStream_t>(stream));
+}
+
+size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int pass)
+{
+    if (!gated_shape(T, Kin, F, fmt))
+        return 0;
+    if (pass == 0)
+        return carve(nullptr, fmt, T, Kin, nullptr) + carve_gated_weights(nullptr, fmt, Kin, F, nullptr, nullptr, nullptr);
+    if (pass == 1)  // D, its maximum, and the linear layer's backward
+        return round_up(static_cast<size_t>(T) * static_cast<size_t>(F) * 4, 256) + 256 +
+               mx_linear_workspace_bytes(T, Kin, 2 * F, fmt, 2);
+    return pass == 2 ? carve(nullptr, fmt, T, Kin, nullptr) : 0;
+}
+
+int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, int fmt, int act, const void* W,
+                 const mx_tensor* gate, const mx_tensor* up, void* h, int64_t ldh, float* amax_out, void* workspace,
+                 size_t ws_bytes, void* stream)
+{
+    if (!gated_shape(T, Kin, F, fmt) || !valid_act(act) || (W ? gate || up : F > 0 && (!gate || !up)))
+        return MX_ERR_INVALID_ARG;
+    if (Kin == 0 || Kin % gemm_k_multiple(fmt) != 0 || !aligned16(W))
+        return MX_ERR_ALIGNMENT;
+    int rc = check_quantize_args(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT);
+    if (rc == MX_OK)
+        rc = check_gated_output(h, ldh, T, F, amax_out);
+    if (rc == MX_OK && T > 0 && F > 0 && (!workspace || ws_bytes < mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2)))
+        rc = MX_ERR_WORKSPACE;
+    if (rc == MX_OK && gate)
+        for (const mx_tensor* t : {gate, up})
+            if (rc == MX_OK && (rc = check_operand(t)) == MX_OK && (t->fmt != fmt || t->k != Kin || t->rows != F))
+                rc = MX_ERR_INVALID_ARG;
+    Device d;
+    if (rc != MX_OK || (rc = current_device(&d)) != MX_OK)
+        return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0 || F == 0)
+        return !amax_out || cudaMemsetAsync(amax_out, 0, sizeof(float), s) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    mx_tensor xq, wq, gq, uq;
+    const size_t off = carve(ws, fmt, T, Kin, &xq);
+    rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
+                       &xq, d, s);
+    if (rc != MX_OK)
+        return rc;
+    if (!W)
+        return gemm_gated_impl(&xq, gate, up, act, h, ldh, nullptr, nullptr, amax_out, d, s);
+    carve_gated_weights(ws + off, fmt, Kin, F, &wq, &gq, &uq);
+    if (F % 128 == 0) {
+        rc = quantize_impl(W, 2 * F, Kin, Kin, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0,
+                           nullptr, &wq, d, s);
+        gq = operand_rows(wq, 0, F);
+        uq = operand_rows(wq, F, F);
+    } else {
+        const bool one_scale = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt);
+        if (one_scale)
+            rc = launch_amax(W, 2 * F, Kin, Kin, gq.amax, d, s);
+        if (rc == MX_OK)
+            rc = quantize_halves(W, Kin, F, fmt, one_scale ? gq.amax : nullptr, &gq, &uq, d, s);
+    }
+    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, nullptr, nullptr, amax_out, d, s);
+}
+
+int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
+                      const float* x_amax, const float* w_amax, const mx_bwd_opts* opts, void* h, int64_t ldh,
+                      const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* workspace, size_t ws_bytes,
+                      void* saved, size_t saved_bytes, void* stream)
+{
+    if (!gated_shape(T, Kin, F, fmt) || !valid_act(act) || !gate8 || !up8 || (!W && F > 0))
+        return MX_ERR_INVALID_ARG;
+    const mx_bwd_opts o = bwd_opts_or_default(opts);
+    if (Kin == 0 || Kin % gemm_k_multiple(fmt) != 0 || T % 32 != 0 || F % 16 != 0 || !aligned16(W))
+        return MX_ERR_ALIGNMENT;
+    int rc = check_quantize_args(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT);
+    if (rc == MX_OK)
+        rc = check_direction(fmt, MX_ROUND_RNE, o.wgrad_hadamard);
+    if (rc == MX_OK)
+        rc = check_gated_output(h, ldh, T, F, amax_out);
+    for (const mx_act8* c : {gate8, up8})
+        if (rc == MX_OK)
+            rc = check_checkpoint(c, T, F);
+    if (rc != MX_OK)
+        return rc;
+    if (!workspace || ws_bytes < mx_gated_workspace_bytes(T, Kin, F, fmt, 0) || !saved ||
+        saved_bytes < mx_linear_saved_bytes(T, Kin, 2 * F, fmt))
+        return MX_ERR_WORKSPACE;
+    if ((fmt_is_local(fmt) && (x_amax || w_amax)) || (fmt == MX_FMT_NVFP4 && o.wgrad_hadamard && x_amax))
+        return MX_ERR_UNSUPPORTED;
+    Device d;
+    if ((rc = current_device(&d)) != MX_OK)
+        return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0 || F == 0)
+        return !amax_out || cudaMemsetAsync(amax_out, 0, sizeof(float), s) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    mx_tensor xq, wq, gq, uq, xt, wt;
+    const size_t off = carve(ws, fmt, T, Kin, &xq);
+    carve_gated_weights(ws + off, fmt, Kin, F, &wq, &gq, &uq);
+    carve_saved(static_cast<uint8_t*>(saved), T, Kin, 2 * F, fmt, o.wgrad_hadamard, &xt, &wt);
+    const int block = fmt_block(fmt);
+    rc = quantize_dual_impl(X, T, Kin, ldx, fmt, block, MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE,
+                            o.wgrad_hadamard, x_amax, &xq, &xt, d, s);
+    if (rc != MX_OK)
+        return rc;
+    if (F % 128 == 0) {
+        rc = quantize_dual_impl(W, 2 * F, Kin, Kin, fmt, block, MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE, 0,
+                                w_amax, &wq, &wt, d, s);
+        gq = operand_rows(wq, 0, F);
+        uq = operand_rows(wq, F, F);
+    } else {
+        rc = quantize_impl(W, 2 * F, Kin, Kin, MX_COLWISE, fmt, block, MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, w_amax, &wt,
+                           d, s);
+        const bool one_scale = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt);
+        if (rc == MX_OK)
+            rc = quantize_halves(W, Kin, F, fmt, one_scale ? wt.amax : nullptr, &gq, &uq, d, s);
+    }
+    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, gate8, up8, amax_out, d, s);
+}
+
+int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
+                 const mx_act8* gate8, const mx_act8* up8, const mx_bwd_opts* opts, const void* saved,
+                 size_t saved_bytes, void* dX, int dx_dtype, void* dW, int dw_dtype, void* workspace,
+                 size_t ws_bytes, void* stream)
+{
+    if (!gated_shape(T, Kin, F, fmt) || !valid_act(act) || !gate8 || !up8 || lddh < F || (T > 0 && F > 0 && !dH))
+        return MX_ERR_INVALID_ARG;
+    const mx_bwd_opts o = bwd_opts_or_default(opts);
+    for (const int t : {dx_dtype, dw_dtype})
+        if (t != MX_OUT_F32 && t != MX_OUT_BF16)
+            return MX_ERR_INVALID_ARG;
+    const int64_t km = gemm_k_multiple(fmt);
+    if (Kin == 0 || Kin % km != 0 || T % 32 != 0 || F % 16 != 0 || (dX && 2 * F % km != 0) || (dW && T % km != 0))
+        return MX_ERR_ALIGNMENT;
+    if (reinterpret_cast<uintptr_t>(dH) % 2 != 0 || !aligned16(dX) || !aligned16(dW) || !aligned16(workspace))
+        return MX_ERR_ALIGNMENT;
+    int rc = check_direction(fmt, o.wgrad_dy_rounding, o.wgrad_hadamard);
+    for (const mx_act8* c : {gate8, up8})
+        if (rc == MX_OK)
+            rc = check_checkpoint(c, T, F);
+    if (rc == MX_OK && (!workspace || ws_bytes < mx_gated_workspace_bytes(T, Kin, F, fmt, 1) || !saved ||
+                        saved_bytes < mx_linear_saved_bytes(T, Kin, 2 * F, fmt)))
+        rc = MX_ERR_WORKSPACE;
+    Device d;
+    if (rc != MX_OK || (rc = current_device(&d)) != MX_OK)
+        return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0 || F == 0) {  // no tokens, or no features: zero gradients
+        if (dX && T > 0 && cudaMemsetAsync(dX, 0, T * Kin * (dx_dtype == MX_OUT_BF16 ? 2 : 4), s) != cudaSuccess)
+            return MX_ERR_CUDA;
+        if (dW && F > 0 && cudaMemsetAsync(dW, 0, 2 * F * Kin * (dw_dtype == MX_OUT_BF16 ? 2 : 4), s) != cudaSuccess)
+            return MX_ERR_CUDA;
+        return MX_OK;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const size_t d_bytes = round_up(static_cast<size_t>(T) * static_cast<size_t>(F) * 4, 256);
+    float* word = reinterpret_cast<float*>(ws + d_bytes);
+    // the formats whose tensor scale is that of D itself take its maximum from the pass that makes it
+    const bool takes_amax = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt) && !o.wgrad_hadamard;
+    ActArgs a = {};
+    a.h = const_cast<void*>(dH);  // read only in the backward kernels
+    a.ldh = lddh;
+    a.gate8 = checkpoint_view(gate8);
+    a.up8 = checkpoint_view(up8);
+    a.rows = T;
+    a.cols = F;
+    a.act = act;
+    a.dtype = MX_OUT_BF16;
+    a.gated = true;
+    a.dgate = ws;
+    a.dup = ws + 2 * F;
+    a.lddg = a.lddu = 2 * F;
+    a.amax = takes_amax ? reinterpret_cast<unsigned*>(word) : nullptr;
+    if ((rc = launch_act_bwd(a, d, s)) != MX_OK)
+        return rc;
+    return mx_linear_bwd_saved(ws, T, Kin, 2 * F, fmt, takes_amax ? word : nullptr, &o, saved, saved_bytes, dX, dx_dtype,
+                               dW, dw_dtype, ws + d_bytes + 256, ws_bytes - d_bytes - 256, stream);
 }
 
 const char* mx_strerror(int status)

@@ -185,6 +185,19 @@ int launch_act8_save(const void* x, int64_t ldx, int dtype, int64_t rows, int64_
 int launch_act8_restore(Act8View a, int64_t rows, int64_t cols, void* out, int64_t ldo, int dtype, const Device& d,
                         cudaStream_t s);
 
+// h = act(x gate^T) * (x up^T), bf16 (gated.cu); amax zeroed by the caller.
+struct GatedArgs {
+    const mx_tensor* x;
+    const mx_tensor* gate;
+    const mx_tensor* up;
+    int act;
+    void* h;
+    int64_t ldh;
+    Act8View gate8, up8;  // both or neither
+    unsigned* amax;
+};
+int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s);
+
 // The optimizer's step and the gradients' norm (optim.cu), after mx_ops.cu's checks.
 constexpr int kGradNormCtas = 1024;        // partial sums that one launch leaves at most
 int64_t grad_norm_parts(int64_t count);    // partial sums in the workspace

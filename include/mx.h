@@ -452,6 +452,58 @@ int mx_act_bwd(const void* dh, int64_t ldh, const void* gate, int64_t ldg, const
                int64_t lddg, void* dup, int64_t lddu, float* amax_out, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The gated feed-forward block's first half: both projections, the activation
+ * and the product in one kernel, whose only writes are h and, for training, the
+ * 8-bit checkpoints of the projections' outputs.  The rules of the activation
+ * calls hold; X, dH and h are bf16, all operands of one format. */
+
+/* h[T, F] = act(g) * u, g = dq(A) dq(gate)^T, u = dq(A) dq(up)^T, with T = A->rows,
+ * F = gate->rows = up->rows, K = A->k: the products as mx_gemm forms them (fp32
+ * accumulators times the tensor scales), act and the product in fp32, one rounding
+ * to bf16.  ldh >= F, ldh % 8 == 0, h 16-byte aligned.  gate8 / up8: checkpoints of
+ * g and u (from fp32), both or neither.  amax_out (may be NULL): max |h|.
+ * Operands carry no Hadamard transform (MX_ERR_UNSUPPORTED); other rules as
+ * mx_gemm, and K > 0. */
+int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
+                  const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* stream);
+
+/* Workspace bytes: pass 0 mx_gated_fwd from W and mx_gated_fwd_save, pass 1
+ * mx_gated_bwd, pass 2 mx_gated_fwd from quantized weights; 0 for another pass or
+ * invalid arguments. */
+size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int pass);
+
+/* The block from X[T, Kin] (bf16, row stride ldx, ldx % 8 == 0, 16-byte aligned),
+ * quantized rowwise with RNE and the format's default rule.  The weights are W[2F,
+ * Kin] (bf16, row stride Kin, the gate's rows first; quantized likewise, as one
+ * tensor under one tensor scale), or with W NULL the operands gate and up [F, Kin].
+ * NVFP4_LOCAL: where F % 128 != 0 the regions of 128 rows start anew at the up rows. */
+int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, int fmt, int act, const void* W,
+                 const mx_tensor* gate, const mx_tensor* up, void* h, int64_t ldh, float* amax_out, void* workspace,
+                 size_t ws_bytes, void* stream);
+
+/* mx_gated_fwd from W, keeping what the backward pass needs: gate8 and up8, and in
+ * `saved` (mx_linear_saved_bytes(T, Kin, 2F, fmt) bytes) the operands X^T and W^T as
+ * mx_linear_fwd_save keeps them.  x_amax, w_amax, opts as there.  T % 32 == 0 and
+ * F % 16 == 0.  One pass over W emits both of its operands where F % 128 == 0, so
+ * that the up rows start a row tile of the scale layout; else the rowwise halves
+ * take passes of their own. */
+int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
+                      const float* x_amax, const float* w_amax, const mx_bwd_opts* opts, void* h, int64_t ldh,
+                      const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* workspace, size_t ws_bytes,
+                      void* saved, size_t saved_bytes, void* stream);
+
+/* Its backward pass from dH[T, F] (bf16, row stride lddh) and what it kept:
+ *   D[T, 2F] = [dH u act'(g), dH act(g)] in bf16, g and u the checkpoints' values
+ *   dX[T, Kin] = D W, dW[2F, Kin] = D^T X as mx_linear_bwd_saved forms them
+ * dX or dW may be NULL.  Exactly mx_act_bwd into one matrix followed by
+ * mx_linear_bwd_saved (with D's maximum as dy_amax where the format takes one).
+ * 2F (for dX) and T (for dW) are multiples of 128 (FP8 formats) or 256 (FP4). */
+int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
+                 const mx_act8* gate8, const mx_act8* up8, const mx_bwd_opts* opts, const void* saved,
+                 size_t saved_bytes, void* dX, int dx_dtype, void* dW, int dw_dtype, void* workspace,
+                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * The weights' update after the backward calls: the gradients' norm and the
  * optimizer's step, over many tensors at once.  The rules of the calls above
  * hold where they apply: stream order, no allocation, no reduction whose
