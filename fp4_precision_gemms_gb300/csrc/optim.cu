@@ -2,6 +2,7 @@
 // one launch each.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "mx_act8.cuh"
 #include "mx_internal.cuh"
@@ -11,7 +12,66 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnitsPerTile = kThreads;  // a tile: eight consecutive values a thread
+// Octs (eight consecutive values) that a thread takes of a tile.  8-bit moments: four, 32
+// apart, so that a warp has 32 whole groups and reads and writes their exponent bytes as
+// one sector each (a quarter of a sector at a time: 602 us in place of 545 for a layer).
+__host__ __device__ constexpr int octs_of(int bits) { return bits == 8 ? 4 : 1; }
+
+// Eight values of a flat tensor.  ANY as in mx_units.cuh, but fp32 tensors that are not
+// ANY start on 32-byte boundaries: eight fp32 values are one access.  (In two of 16
+// bytes each, a warp's access touches every sector of its kilobyte twice.)
+template <typename T, bool ANY>
+struct Values {
+    Unit<T, ANY> w;
+    __device__ __forceinline__ void load(const void* base, const Place& at, int64_t n) { w.load(base, 0, at, 1, n); }
+    __device__ __forceinline__ void get(Oct& o, int n) const { w.get(o, n); }
+    static __device__ __forceinline__ void store(void* base, const Place& at, const Oct& o, int64_t n)
+    {
+        Top<T> unused;
+        store_unit<T, ANY>(base, 0, at, o, n, unused);
+    }
+};
+template <>
+struct Values<float, false> {
+    float v[8];
+    __device__ __forceinline__ void load(const void* base, const Place& at, int64_t)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = 0.0f;
+        if (at.cols > 0)
+            asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                         : "l"(static_cast<const float*>(base) + static_cast<int64_t>(at.unit) * 8)
+                         : "memory");
+    }
+    __device__ __forceinline__ void get(Oct& o, int) const
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o.p[k] = make_float2(v[2 * k], v[2 * k + 1]);
+    }
+    static __device__ __forceinline__ void store(void* base, const Place& at, const Oct& o, int64_t)
+    {
+        if (at.cols <= 0)
+            return;
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         static_cast<float*>(base) + static_cast<int64_t>(at.unit) * 8),
+                     "f"(o.p[0].x), "f"(o.p[0].y), "f"(o.p[1].x), "f"(o.p[1].y), "f"(o.p[2].x), "f"(o.p[2].y),
+                     "f"(o.p[3].x), "f"(o.p[3].y)
+                     : "memory");
+    }
+};
+__device__ __forceinline__ void fold(Top<float>& top, const Oct& o)
+{
+    top.pair(o.p[0]), top.pair(o.p[1]), top.pair(o.p[2]), top.pair(o.p[3]);
+}
+__device__ __forceinline__ void fold(Top<__nv_bfloat16>& top, const Oct& o)
+{
+    const uint4 w = pack_oct(o);
+    top.word(w.x), top.word(w.y), top.word(w.z), top.word(w.w);
+}
+bool whole(const void* p, int64_t n, int bytes) { return n % 8 == 0 && reinterpret_cast<uintptr_t>(p) % (8 * bytes) == 0; }
 
 // ---------------------------------------------------------------- AdamW
 // The tensors of one launch, in its parameters: no table to copy to the device
@@ -59,10 +119,11 @@ __device__ __forceinline__ int entry_of(const AdamwTable& t, uint32_t i)
     return lo;
 }
 
+// 1 / x for x >= 0; below 2^-126 that number's.
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(max_nan(x, 1.17549435e-38f)));
     return r;
 }
 __device__ __forceinline__ float sqrt_approx(float x)
@@ -91,17 +152,33 @@ __device__ __forceinline__ void random8(const AdamwTable& a, uint32_t t, uint32_
 }
 __device__ __forceinline__ uint32_t half_of(const uint32_t (&u)[4], int i) { return i & 1 ? u[i >> 1] >> 16 : u[i >> 1] & 0xFFFFu; }
 
-// The E4M3 code of |y| <= 448, up iff u16 < p 2^16.  From 2^-6 on a float's upper bits
-// are the code, and the 20 that go are p.  Below, adding 2^-6 brings the value to the
-// same spacing of 2^-9, one exponent up; rounding that sum up keeps the comparison,
-// whose left side is whole, what it is on the exact p.
-__device__ __forceinline__ uint32_t e4m3_sr(float y, uint32_t u16)
+// The E4M3 codes of four values |y| <= 448, each up iff u16 < p 2^16; u as random8 gives
+// it.  From 2^-6 on a float's upper bits are the code (less 960), and the 20 that go are
+// p 2^20: adding 2^20 - 1 - 16 u16 carries into the code where they are above 16 u16.
+// Below 2^-6, adding 2^-6 brings the value to the same spacing of 2^-9, eight codes up;
+// rounding that sum up keeps the comparison, whose other side is whole, what it is on the
+// exact p.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t e4m3_sr4(const float (&y)[4], uint32_t u01, uint32_t u23)
 {
-    const float a = fabsf(y);
-    const bool low = a < 0.015625f;
-    const uint32_t b = __float_as_uint(low ? __fadd_ru(a, 0.015625f) : a);
-    const uint32_t code = (b >> 20) - (low ? 968u : 960u) + ((u16 << 4) < (b & 0xFFFFFu) ? 1u : 0u);
-    return code | (__float_as_uint(y) >> 31) << 7;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = SIGNED ? fabsf(y[i]) : y[i];
+        const uint32_t u = i < 2 ? u01 : u23;
+        const uint32_t r = ((i & 1 ? u >> 12 : u << 4) & 0xFFFF0u) ^ 0xFFFFFu;
+        const uint32_t b = a < 0.015625f ? __float_as_uint(__fadd_ru(a, 0.015625f)) - (8u << 20) : __float_as_uint(a);
+        w[i] = (b + r) << 4;  // the code + 0xC0 in the top byte
+    }
+    const uint32_t four = __byte_perm(__byte_perm(w[0], w[1], 0x0073), __byte_perm(w[2], w[3], 0x0073), 0x5410);
+    // less 0xC0 again: a byte's upper bits are 11 for codes below 0x40 and 00 (carried) above
+    uint32_t codes = (four & 0x3F3F3F3Fu) | (~four & 0x40404040u);
+    if constexpr (SIGNED) {
+        const uint32_t s = __byte_perm(__byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0073),
+                                       __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0073), 0x5410);
+        codes |= s & 0x80808080u;
+    }
+    return codes;
 }
 
 // A moment in the 8-bit checkpoint's format: like encode_oct, but rounded
@@ -136,11 +213,15 @@ __device__ __forceinline__ uint2 encode_moment(Oct z, uint8_t& byte, const uint3
         if constexpr (ROOT)
             y[i] = z[i] == 0.0f ? 0.0f : max_nan(y[i], 0.001953125f);
     }
-    uint32_t w[2] = {0u, 0u};
+    uint32_t w[2];
     if constexpr (SR) {
+        w[0] = e4m3_sr4<!ROOT>({y[0], y[1], y[2], y[3]}, u[0], u[1]);
+        w[1] = e4m3_sr4<!ROOT>({y[4], y[5], y[6], y[7]}, u[2], u[3]);
+        if (odd)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i >> 2] |= (odd && y[i] != y[i] ? 0x7Fu : e4m3_sr(y[i], half_of(u, i))) << (8 * (i & 3));
+            for (int i = 0; i < 8; ++i)
+                if (y[i] != y[i])
+                    w[i >> 2] |= 0x7Fu << (8 * (i & 3));
     } else {
         w[0] = cvt_e4m3x2(y[0], y[1]) | cvt_e4m3x2(y[2], y[3]) << 16;
         w[1] = cvt_e4m3x2(y[4], y[5]) | cvt_e4m3x2(y[6], y[7]) << 16;
@@ -174,13 +255,55 @@ __device__ __forceinline__ float second_moment(const AdamwTable& a, float v, flo
     return __fadd_rn(__fmul_rn(v, a.b2), __fmul_rn(__fmul_rn(g, g), a.c2));
 }
 
+// Eight codes of an 8-bit moment.
+struct Codes {
+    uint2 w;
+    __device__ __forceinline__ void load(const void* codes, const Place& at)
+    {
+        w = make_uint2(0u, 0u);
+        if (at.cols > 0)
+            asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(w.x), "=r"(w.y)
+                         : "l"(static_cast<const uint8_t*>(codes) + static_cast<int64_t>(at.unit) * 8)
+                         : "memory");
+    }
+    __device__ __forceinline__ void get(Oct& o, uint32_t byte) const
+    {
+        decode_oct(w, o);
+        const float2 s = both(act8_scale(byte));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o.p[k] = __fmul2_rn(o.p[k], s);
+    }
+};
+// A tensor's values as one thread takes them from memory.
+template <typename P, typename G, int BITS, bool ANY>
+struct Loaded {
+    Place at;
+    Values<P, ANY> p;
+    Values<G, ANY> g;
+    std::conditional_t<BITS == 8, Codes, Values<float, ANY>> m, v;
+};
+
 // m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2, and the weight's step, which divides
-// by approximation (2^-21 of the step).
+// by approximation (2^-21 of the step; a divisor below 2^-126 counts as that).
 // Of 8-bit moments the second one's root is kept: it spans half the octaves, and
 // E4M3's 18 then hold 36 of the moment's.
+//
+// Bound by DRAM: a layer of 218e6 values, fp32 with bf16 copies and maxima, 990 us (6.54
+// GB, 6.6 TB/s; 1408 with fp32 accesses of 16 bytes), 8-bit moments and bf16 gradients
+// 564 us (3.52 GB, 6.2 TB/s).  Stochastic rounding at odd addresses by instructions: 7.7e6
+// bf16 values 45 us, three sets of random numbers and the shifts.
 template <typename P, typename G, int BITS, bool SR, bool ANY>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwTable a)
 {
+    constexpr int kOcts = octs_of(BITS);
+    // octs whose loads are in flight together (a layer with 8-bit moments: one 573 us, two
+    // 562, four 589), and how often the loop over them is unrolled: at any address its body
+    // is long, and unrolled it takes the registers of a CTA an SM
+    constexpr int kBatch = ANY || kOcts == 1 ? 1 : 2;
+    constexpr int kUnroll = ANY ? 1 : kOcts / kBatch;
+    const int lane = threadIdx.x & 31;
     const float scale = a.scale ? *a.scale : 1.0f;
     float step = a.step, root = a.root, lr = a.lr;
     uint32_t t = a.t;
@@ -199,9 +322,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     Top<P> top;
     Top<__nv_bfloat16> top16;
     int cur = -1;
-    auto flush = [&](int i, bool copied) {
-        if (a.amax)
-            copied ? flush_top(a.amax + a.e[i].index, top16) : flush_top(a.amax + a.e[i].index, top);
+    auto flush = [&](int i) {
+        if (!a.amax)
+            return;
+        if (sizeof(P) == 4 && a.e[i].copy)
+            flush_top(a.amax + a.e[i].index, top16);
+        else
+            flush_top(a.amax + a.e[i].index, top);
         top = Top<P>();
         top16 = Top<__nv_bfloat16>();
     };
@@ -209,94 +336,124 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         const int i = entry_of(a, tile);
         const AdamwEntry& e = a.e[i];
         if (cur >= 0 && i != cur)
-            flush(cur, a.e[cur].copy != nullptr);
+            flush(cur);
         cur = i;
-        const uint32_t unit = (tile - e.first) * kUnitsPerTile + threadIdx.x;
-        const Place at = {0, unit, static_cast<int32_t>(max(min(e.n - static_cast<int64_t>(unit) * 8, int64_t{8}), int64_t{0}))};
-        Unit<P, ANY> rp;
-        rp.load(e.p, 0, at, 1, e.n);
-        Oct p;
-        if (skip || !e.g) {
-            rp.get(p, at.cols);
-        } else {
-            Unit<G, ANY> rg;
-            rg.load(e.g, 0, at, 1, e.n);
-            Oct g, m, v;
-            if constexpr (BITS == 8) {
-                RawCodes cm, cv;
-                cm.clear(), cv.clear();
-                if (at.cols > 0) {
-                    cm.load({static_cast<uint8_t*>(e.m), e.m_sf}, unit);
-                    cv.load({static_cast<uint8_t*>(e.v), e.v_sf}, unit);
-                }
-                cm.get(m);
-                cv.get(v);
+        const bool still = skip || !e.g;
+        const float decay = a.lr_at ? 1.0f - lr * e.wd : e.decay;
+        // this lane's first oct of the warp's 32 kOcts
+        const uint32_t first = (tile - e.first) * (kThreads * kOcts) + (threadIdx.x - lane) * kOcts + lane;
+        uint32_t bytes_m = 127, bytes_v = 127;  // 8-bit moments: of the warp's group `lane`
+        uint8_t new_m = 0, new_v = 0;
+        const int64_t group = static_cast<int64_t>(first - lane) / 4 + lane;
+        const bool has_group = BITS == 8 && group * kAct8Group < e.n;
+        if (has_group && !still) {
+            bytes_m = e.m_sf[group];
+            bytes_v = e.v_sf[group];
+        }
+#pragma unroll kUnroll
+        for (int batch = 0; batch < kOcts; batch += kBatch) {
+            Loaded<P, G, BITS, ANY> w[kBatch];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v.p[k] = __fmul2_rn(v.p[k], v.p[k]);
-            } else {
-                Unit<float, ANY> rm, rv;
-                rm.load(e.m, 0, at, 1, e.n);
-                rv.load(e.v, 0, at, 1, e.n);
-                rm.get(m, at.cols);
-                rv.get(v, at.cols);
-            }
-            rp.get(p, at.cols);
-            rg.get(g, at.cols);
-            const float decay = a.lr_at ? 1.0f - lr * e.wd : e.decay;
-            Oct r;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float x = __fmul_rn(g.p[k].x, scale), y = __fmul_rn(g.p[k].y, scale);
-                m.p[k] = make_float2(first_moment(a, m.p[k].x, x), first_moment(a, m.p[k].y, y));
-                v.p[k] = make_float2(second_moment(a, v.p[k].x, x), second_moment(a, v.p[k].y, y));
-                if constexpr (BITS == 8)
-                    r.p[k] = make_float2(__fsqrt_rn(v.p[k].x), __fsqrt_rn(v.p[k].y));
-                else
-                    r.p[k] = make_float2(sqrt_approx(v.p[k].x), sqrt_approx(v.p[k].y));
-                const float2 d = __ffma2_rn(r.p[k], both(root), both(a.eps));
-                const float2 q = __fmul2_rn(m.p[k], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
-                p.p[k] = __ffma2_rn(q, both(-step), __fmul2_rn(p.p[k], both(decay)));
-            }
-            uint32_t u[4] = {};
-            if constexpr (BITS == 8) {
-                if (at.cols < 8) {
-                    keep_first(m, at.cols);
-                    keep_first(r, at.cols);
+            for (int o = 0; o < kBatch; ++o) {
+                const uint32_t unit = first + (batch + o) * 32;
+                w[o].at = {0, unit, static_cast<int32_t>(max(min(e.n - static_cast<int64_t>(unit) * 8, int64_t{8}), int64_t{0}))};
+                w[o].p.load(e.p, w[o].at, e.n);
+                if (still)
+                    continue;
+                w[o].g.load(e.g, w[o].at, e.n);
+                if constexpr (BITS == 8) {
+                    w[o].m.load(e.m, w[o].at);
+                    w[o].v.load(e.v, w[o].at);
+                } else {
+                    w[o].m.load(e.m, w[o].at, e.n);
+                    w[o].v.load(e.v, w[o].at, e.n);
                 }
-                uint8_t bm, bv;
-                if constexpr (SR)
-                    random8(a, t, unit, 4 * e.index, u);
-                const uint2 cm = encode_moment<false, SR>(m, bm, u);
-                if constexpr (SR)
-                    random8(a, t, unit, 4 * e.index + 1, u);
-                const uint2 cv = encode_moment<true, SR>(r, bv, u);
-                // whole groups: a tensor's last one is padded with zeros
-                if (static_cast<int64_t>(unit) * 8 < (e.n + 31) / 32 * 32) {
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + static_cast<int64_t>(unit) * 8) = cm;
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + static_cast<int64_t>(unit) * 8) = cv;
-                    if ((threadIdx.x & 3) == 0) {
-                        e.m_sf[unit >> 2] = bm;
-                        e.v_sf[unit >> 2] = bv;
+            }
+#pragma unroll
+            for (int o = 0; o < kBatch; ++o) {
+                const Place at = w[o].at;
+                const uint32_t unit = at.unit;
+                Oct p;
+                w[o].p.get(p, at.cols);
+                if (!still) {
+                    Oct g, m, v, r;
+                    w[o].g.get(g, at.cols);
+                    if constexpr (BITS == 8) {
+                        const int from = (batch + o) * 8 + (lane >> 2);
+                        w[o].m.get(m, __shfl_sync(0xFFFFFFFFu, bytes_m, from));
+                        w[o].v.get(v, __shfl_sync(0xFFFFFFFFu, bytes_v, from));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v.p[k] = __fmul2_rn(v.p[k], v.p[k]);
+                    } else {
+                        w[o].m.get(m, at.cols);
+                        w[o].v.get(v, at.cols);
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x = __fmul_rn(g.p[k].x, scale), y = __fmul_rn(g.p[k].y, scale);
+                        m.p[k] = make_float2(first_moment(a, m.p[k].x, x), first_moment(a, m.p[k].y, y));
+                        v.p[k] = make_float2(second_moment(a, v.p[k].x, x), second_moment(a, v.p[k].y, y));
+                        if constexpr (BITS == 8)
+                            r.p[k] = make_float2(__fsqrt_rn(v.p[k].x), __fsqrt_rn(v.p[k].y));
+                        else
+                            r.p[k] = make_float2(sqrt_approx(v.p[k].x), sqrt_approx(v.p[k].y));
+                        const float2 d = __ffma2_rn(r.p[k], both(root), both(a.eps));
+                        const float2 q = __fmul2_rn(m.p[k], make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+                        p.p[k] = __ffma2_rn(q, both(-step), __fmul2_rn(p.p[k], both(decay)));
+                    }
+                    uint32_t u[4] = {};
+                    if constexpr (BITS == 8) {
+                        if (at.cols < 8) {
+                            keep_first(m, at.cols);
+                            keep_first(r, at.cols);
+                        }
+                        uint8_t bm, bv;
+                        if constexpr (SR)
+                            random8(a, t, unit, 4 * e.index, u);
+                        const uint2 cm = encode_moment<false, SR>(m, bm, u);
+                        if constexpr (SR)
+                            random8(a, t, unit, 4 * e.index + 1, u);
+                        const uint2 cv = encode_moment<true, SR>(r, bv, u);
+                        const uint32_t from = (lane & 7) * 4;
+                        const uint32_t both_bytes = __shfl_sync(0xFFFFFFFFu, uint32_t{bm} | uint32_t{bv} << 8, from);
+                        if ((lane >> 3) == batch + o) {
+                            new_m = static_cast<uint8_t>(both_bytes);
+                            new_v = static_cast<uint8_t>(both_bytes >> 8);
+                        }
+                        // whole groups: a tensor's last one is padded with zeros
+                        if (static_cast<int64_t>(unit) * 8 < (e.n + 31) / 32 * 32) {
+                            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.m) + static_cast<int64_t>(unit) * 8) = cm;
+                            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(e.v) + static_cast<int64_t>(unit) * 8) = cv;
+                        }
+                    } else {
+                        Values<float, ANY>::store(e.m, at, m, e.n);
+                        Values<float, ANY>::store(e.v, at, v, e.n);
+                    }
+                    if constexpr (SR && sizeof(P) == 2) {
+                        random8(a, t, unit, 4 * e.index + 2, u);
+                        round_bf16_sr(p, u);
+                    }
+                    Values<P, ANY>::store(e.p, at, p, e.n);
                 }
-            } else {
-                Top<float> unused;
-                store_unit<float, ANY>(e.m, 0, at, m, e.n, unused);
-                store_unit<float, ANY>(e.v, 0, at, v, e.n, unused);
-            }
-            if constexpr (SR && sizeof(P) == 2) {
-                random8(a, t, unit, 4 * e.index + 2, u);
-                round_bf16_sr(p, u);
+                if (at.cols < 8)
+                    keep_first(p, at.cols);
+                if (sizeof(P) == 4 && e.copy) {
+                    Values<__nv_bfloat16, ANY>::store(e.copy, at, p, e.n);
+                    if (a.amax)
+                        fold(top16, p);
+                } else if (a.amax) {
+                    fold(top, p);
+                }
             }
         }
-        store_unit<P, ANY>(e.p, 0, at, p, e.n, top);
-        if constexpr (sizeof(P) == 4)
-            if (e.copy)
-                store_unit<__nv_bfloat16, ANY>(e.copy, 0, at, p, e.n, top16);
+        if (has_group && !still) {
+            e.m_sf[group] = new_m;
+            e.v_sf[group] = new_v;
+        }
     }
     if (cur >= 0)
-        flush(cur, a.e[cur].copy != nullptr);
+        flush(cur);
 }
 
 template <typename P, typename G, int BITS, bool SR, bool ANY>
@@ -322,8 +479,11 @@ int launch_adamw(const AdamwTable& t, int bits, bool sr, bool any, const Device&
     return launch_adamw<P, G, 32, false>(t, any, d, s);
 }
 
-bool at_16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-uint32_t tiles_of(int64_t n) { return static_cast<uint32_t>((n + 8 * kUnitsPerTile - 1) / (8 * kUnitsPerTile)); }
+uint32_t tiles_of(int64_t n, int bits)
+{
+    const int64_t tile = 8 * kThreads * octs_of(bits);
+    return static_cast<uint32_t>((n + tile - 1) / tile);
+}
 
 }  // namespace
 
@@ -368,12 +528,12 @@ int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_o
         };
         for (int64_t i = 0; i < count; ++i) {
             const mx_adamw_tensor& x = tensors[i];
-            const bool whole = x.n % 8 == 0 && at_16(x.param) && at_16(x.grad) && at_16(x.copy) &&
-                               (x.bits == 8 || (at_16(x.m) && at_16(x.v)));
+            const bool wide = whole(x.param, x.n, p16 ? 2 : 4) && whole(x.grad, x.n, g16 ? 2 : 4) && whole(x.copy, x.n, 2) &&
+                              (x.bits == 8 || (whole(x.m, x.n, 4) && whole(x.v, x.n, 4)));
             if (x.n == 0 || (x.p_dtype == MX_OUT_BF16) != p16 || (x.g_dtype == MX_OUT_BF16) != g16 ||
-                (x.bits == 8) != eight || whole == any)
+                (x.bits == 8) != eight || wide == any)
                 continue;
-            const uint32_t tiles = tiles_of(x.n);
+            const uint32_t tiles = tiles_of(x.n, x.bits);
             if (t.count == kAdamwEntries || t.tiles + static_cast<uint64_t>(tiles) > 0x7FFFFFFFu) {
                 const int rc = flush();
                 if (rc != MX_OK)
@@ -437,7 +597,7 @@ __device__ __forceinline__ double block_sum(double v)
 template <typename G>
 __device__ __forceinline__ float squares(const NormEntry& e, uint32_t tile)
 {
-    const bool any = !((reinterpret_cast<uintptr_t>(e.g) & 15) == 0 && e.n % 8 == 0);
+    const bool any = e.n % 8 != 0 || reinterpret_cast<uintptr_t>(e.g) % (8 * sizeof(G)) != 0;
     const int64_t first = static_cast<int64_t>(tile - e.first) * (kThreads * kNormUnits) + threadIdx.x;
     float2 sum = both(0.0f);
     auto add = [&](const Oct& o) {
@@ -450,10 +610,10 @@ __device__ __forceinline__ float squares(const NormEntry& e, uint32_t tile)
         return Place{0, static_cast<uint32_t>(unit), static_cast<int32_t>(max(min(e.n - unit * 8, int64_t{8}), int64_t{0}))};
     };
     if (!any) {
-        Unit<G, false> w[kNormUnits];
+        Values<G, false> w[kNormUnits];
 #pragma unroll
         for (int k = 0; k < kNormUnits; ++k)
-            w[k].load(e.g, 0, place(k), 1, e.n);
+            w[k].load(e.g, place(k), e.n);
 #pragma unroll
         for (int k = 0; k < kNormUnits; ++k) {
             Oct o;

@@ -568,7 +568,8 @@ typedef struct mx_adamw_opts {
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   param = param (1 - lr weight_decay)
  *           - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32; the step takes m and v as computed, before 8-bit moments are rounded.
+ * in fp32 (a divisor below 2^-126 counts as that); the step takes m and v as
+ * computed, before 8-bit moments are rounded.
  * m and v round after each product and sum, so that the codes of 8-bit moments
  * follow from the formula alone.  A root that is not zero keeps at least its
  * group's smallest code, 2^-9 2^e; Inf and NaN become the NaN code.  MX_ROUND_SR:
