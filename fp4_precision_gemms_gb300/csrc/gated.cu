@@ -216,6 +216,8 @@ int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
 int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s)
 {
     const int64_t K = a.x->k;
+    if (a.x->rows <= kGatedFewTokens && !a.gate8.codes)
+        return launch_gated_few(a, a.early, d, s);
     switch (a.x->fmt) {  // stages as the plain GEMM has them
     case MX_FMT_MXFP8_E4M3:
     case MX_FMT_MOSS_FP8:

@@ -870,8 +870,10 @@ int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const f
     return ldh % 8 == 0 && aligned16(h) ? MX_OK : MX_ERR_ALIGNMENT;
 }
 
+// early: A was written by the launch before this one, which waited for all before it, and
+// amax_out is zero already.
 int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
-                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, const Device& d, cudaStream_t s)
+                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, bool early, const Device& d, cudaStream_t s)
 {
     for (const mx_tensor* t : {A, gate, up}) {
         const int rc = check_operand(t);
@@ -895,7 +897,7 @@ int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* 
             rc = check_checkpoint(c, T, F);
     if (rc != MX_OK)
         return rc;
-    if (amax_out && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess)
+    if (!early && amax_out && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess)
         return MX_ERR_CUDA;
     if (T == 0 || F == 0)
         return MX_OK;
@@ -909,6 +911,7 @@ int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* 
     a.gate8 = checkpoint_view(gate8);
     a.up8 = checkpoint_view(up8);
     a.amax = reinterpret_cast<unsigned*>(amax_out);
+    a.early = early;
     return launch_gated(a, d, s);
 }
 
@@ -944,7 +947,7 @@ int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up
     const int rc = current_device(&d);
     if (rc != MX_OK)
         return rc;
-    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, d, static_cast<cudaStream_t>(stream));
+    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, false, d, static_cast<cudaStream_t>(stream));
 }
 
 size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int pass)
@@ -982,29 +985,39 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0 || F == 0)
         return !amax_out || cudaMemsetAsync(amax_out, 0, sizeof(float), s) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    if (amax_out && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess)
+        return MX_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     mx_tensor xq, wq, gq, uq;
     const size_t off = carve(ws, fmt, T, Kin, &xq);
-    rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
-                       &xq, d, s);
-    if (rc != MX_OK)
-        return rc;
-    if (!W)
-        return gemm_gated_impl(&xq, gate, up, act, h, ldh, nullptr, nullptr, amax_out, d, s);
-    carve_gated_weights(ws + off, fmt, Kin, F, &wq, &gq, &uq);
-    if (F % 128 == 0) {
-        rc = quantize_impl(W, 2 * F, Kin, Kin, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0,
-                           nullptr, &wq, d, s);
-        gq = operand_rows(wq, 0, F);
-        uq = operand_rows(wq, F, F);
-    } else {
-        const bool one_scale = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt);
-        if (one_scale)
-            rc = launch_amax(W, 2 * F, Kin, Kin, gq.amax, d, s);
-        if (rc == MX_OK)
-            rc = quantize_halves(W, Kin, F, fmt, one_scale ? gq.amax : nullptr, &gq, &uq, d, s);
+    if (W) {
+        carve_gated_weights(ws + off, fmt, Kin, F, &wq, &gq, &uq);
+        if (F % 128 == 0) {
+            rc = quantize_impl(W, 2 * F, Kin, Kin, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0,
+                               nullptr, &wq, d, s);
+            gq = operand_rows(wq, 0, F);
+            uq = operand_rows(wq, F, F);
+        } else {
+            const bool one_scale = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt);
+            if (one_scale)
+                rc = launch_amax(W, 2 * F, Kin, Kin, gq.amax, d, s);
+            if (rc == MX_OK)
+                rc = quantize_halves(W, Kin, F, fmt, one_scale ? gq.amax : nullptr, &gq, &uq, d, s);
+        }
+        if (rc != MX_OK)
+            return rc;
+        gate = &gq;
+        up = &uq;
     }
-    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, nullptr, nullptr, amax_out, d, s);
+    // the tokens last: the weights are then complete before their quantization starts
+    if (quantize_few_takes(T, Kin)) {
+        fill_meta(&xq, T, Kin, fmt, 0);
+        rc = launch_quantize_few(X, ldx, &xq, d, s);
+    } else {
+        rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
+                           &xq, d, s);
+    }
+    return rc != MX_OK ? rc : gemm_gated_impl(&xq, gate, up, act, h, ldh, nullptr, nullptr, amax_out, true, d, s);
 }
 
 int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
@@ -1060,7 +1073,7 @@ int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int6
         if (rc == MX_OK)
             rc = quantize_halves(W, Kin, F, fmt, one_scale ? wt.amax : nullptr, &gq, &uq, d, s);
     }
-    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, gate8, up8, amax_out, d, s);
+    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, gate8, up8, amax_out, false, d, s);
 }
 
 int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F, int fmt, int act,

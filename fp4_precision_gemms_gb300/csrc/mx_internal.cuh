@@ -195,8 +195,17 @@ struct GatedArgs {
     int64_t ldh;
     Act8View gate8, up8;  // both or neither
     unsigned* amax;
+    // the launch before this one wrote x, and was itself launched after everything before
+    // it had finished: the weights may be read before it has
+    bool early;
 };
+constexpr int kGatedFewTokens = 64;  // up to here launch_gated takes gated_few.cu's kernel
 int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s);
+// Rowwise quantization of a few rows with the default rules (quant_few.cu); out's
+// fields are set.  A launch that follows may start early.
+bool quantize_few_takes(int64_t rows, int64_t k);
+int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, const Device& d, cudaStream_t s);
+int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s);
 
 // The optimizer's step and the gradients' norm (optim.cu), after mx_ops.cu's checks.
 constexpr int kGradNormCtas = 1024;        // partial sums that one launch leaves at most

@@ -57,7 +57,7 @@ def values(mx, q):
 
 
 SHAPES = [(1, 256, 32), (1, 512, 128), (2, 256, 8), (33, 256, 40), (64, 1024, 136), (130, 768, 200), (257, 512, 384), (300, 1280, 96),
-          (700, 256, 20)]
+          (700, 256, 20), (70, 256, 21), (40, 256, 131)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -103,6 +103,46 @@ def test_forms_of_the_weights_agree(mx, fmt, T, K, F):
     assert torch.equal(h, mx.gemm_gated(x, *mx.gated_weights(W, fmt)).h)
     if T % 32 == 0 and F % 16 == 0:
         assert torch.equal(h, mx.gated_fwd_save(X, W, fmt).h)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 3, 15, 16, 17, 31, 33, 48, 64, 65])
+@pytest.mark.parametrize("K,F", [(256, 128), (1280, 300), (4096, 264)])
+def test_few_tokens(mx, fmt, T, K, F):
+    """The kernel for few tokens against the one for many (which keeps checkpoints), and the tokens' quantization
+    within the call against the one on its own: a row that is all zeros and a tensor that is among them."""
+    X, W = data(T, K, F, T)
+    X[T // 2] = 0
+    if T == 3:
+        X.zero_()
+    if T == 15:
+        X *= 2.0 ** -120  # block scales at their lower end
+    gate, up = mx.gated_weights(W, fmt)
+    top = torch.empty(1, device="cuda")
+    for act in ACTS:
+        many = mx.gemm_gated(mx.quantize(X, fmt), gate, up, act=act, save=True).h
+        few = mx.gemm_gated(mx.quantize(X, fmt), gate, up, act=act, amax_out=top).h
+        assert torch.equal(few, many) and float(top) == float(many.float().abs().max())
+        assert torch.equal(mx.gated_fwd(X, (gate, up), fmt, act=act, amax_out=top), many)
+        assert float(top) == float(many.float().abs().max())
+
+
+def test_few_tokens_of_a_wide_matrix(mx):
+    """More values than the small quantization holds, rows of a wider matrix, and both captured."""
+    for T, K in ((64, 8192 + 256), (64, 8192), (5, 512)):
+        X, W = data(T, K + 64, 256, 3)
+        X, W = X[:, 32:K + 32], W[:, :K].contiguous()
+        for fmt in ("nvfp4", "mxfp8"):
+            w = mx.gated_weights(W, fmt)
+            want = mx.gemm_gated(mx.quantize(X.contiguous(), fmt), *w, save=True).h
+            assert torch.equal(mx.gated_fwd(X, w, fmt), want)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                h = mx.gated_fwd(X, w, fmt)
+            for _ in range(2):
+                h.zero_()
+                g.replay()
+                assert torch.equal(h, want)
 
 
 TRAIN = [(256, 256, 128), (256, 512, 384), (512, 768, 128 + 256), (256, 256, 640)]
