@@ -27,6 +27,7 @@ struct GatedParams {
     int ts_region;
     Act8View gate8, up8;
     int64_t groups;   // checkpoint groups of a row
+    int pair_bytes;   // a thread's two exponent bytes are an aligned pair
     int64_t kgroups;
     int m_tiles, n_tiles, group_m;  // 256 x 128 tiles
     unsigned* amax_out;
@@ -34,55 +35,64 @@ struct GatedParams {
     uint64_t wait_ns;
 };
 
-// Eight checkpoint codes' words and the exponent byte of 32 columns of a row that one
-// thread holds (those past n count as zeros).
-__device__ __forceinline__ void save_group(const Act8View& out, int64_t row, int64_t groups, int group, int n,
-                                           const uint32_t (&r)[32], float alpha)
+// 32 values of a row in pairs.
+struct Chunk {
+    float2 v[16];
+};
+
+// A checkpoint group with values that are not finite: these count for nothing but their
+// own codes.
+__device__ __noinline__ uint32_t encode_not_finite(Chunk& x)
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        m = max_nan(m, i < n ? fabsf(__uint_as_float(r[i])) : 0.0f);
-    m = __fmul_rn(m, fabsf(alpha));
-    const bool odd = non_finite(m);
-    if (odd) {
-        m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            m = fmaxf(m, i < n ? fabsf(finite_or_nan(__fmul_rn(__uint_as_float(r[i]), alpha))) : 0.0f);
+    for (int i = 0; i < 16; ++i) {
+        x.v[i] = make_float2(finite_or_nan(x.v[i].x), finite_or_nan(x.v[i].y));
+        m = fmaxf(m, fmaxf(fabsf(x.v[i].x), fabsf(x.v[i].y)));
     }
-    const uint32_t e = act8_byte(m);
-    const float s = act8_inverse(e);
+    return act8_byte(m);
+}
+
+// The checkpoint of 32 columns that one thread holds; returns their exponent byte.
+__device__ __forceinline__ uint32_t save_codes(uint8_t* codes, Chunk x)
+{
+    float m[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        m[i & 1] = max_abs(m[i & 1], x.v[i]);
+    m[0] = max_nan(m[0], m[1]);
+    const uint32_t e = non_finite(m[0]) ? encode_not_finite(x) : act8_byte(m[0]);
+    const float2 s = both(act8_inverse(e));
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = __fmul_rn(__uint_as_float(r[4 * i + k]), alpha);
-            if (odd)
-                v[k] = finite_or_nan(v[k]);
-            v[k] = 4 * i + k < n ? __fmul_rn(v[k], s) : 0.0f;
-        }
-        w[i] = cvt_e4m3x2(v[0], v[1]) | cvt_e4m3x2(v[2], v[3]) << 16;
+        const float2 a = __fmul2_rn(x.v[2 * i], s), b = __fmul2_rn(x.v[2 * i + 1], s);
+        w[i] = cvt_e4m3x2(a.x, a.y) | cvt_e4m3x2(b.x, b.y) << 16;
     }
-    uint4* dst = reinterpret_cast<uint4*>(out.codes + (row * groups + group) * kAct8Group);
+    uint4* dst = reinterpret_cast<uint4*>(codes);
     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    out.sf[row * groups + group] = static_cast<uint8_t>(e);
+    return e;
 }
 
 template <int ACT>
-__device__ __forceinline__ void gated32(const uint32_t (&g)[32], const uint32_t (&u)[32], float ag, float au,
-                                        uint32_t (&pk)[16])
+__device__ __forceinline__ void gated32(const Chunk& g, const Chunk& u, uint32_t (&pk)[16])
 {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float2 z = make_float2(__fmul_rn(__uint_as_float(g[2 * i]), ag), __fmul_rn(__uint_as_float(g[2 * i + 1]), ag));
-        const float2 f = activate<ACT, true>(z).value;
-        pk[i] = pack_bf16x2(make_float2(f.x * __fmul_rn(__uint_as_float(u[2 * i]), au),
-                                        f.y * __fmul_rn(__uint_as_float(u[2 * i + 1]), au)));
-    }
+    for (int i = 0; i < 16; ++i)
+        pk[i] = pack_bf16x2(__fmul2_rn(activate<ACT, true>(g.v[i]).value, u.v[i]));
+}
+
+// Accumulators times their factor, zeros past the first n (most chunks are whole).
+__device__ __forceinline__ void scaled(Chunk& x, const uint32_t (&r)[32], float alpha, int n)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        x.v[i] = __fmul2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), both(alpha));
+    if (n < 32)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x.v[i] = make_float2(2 * i < n ? x.v[i].x : 0.0f, 2 * i + 1 < n ? x.v[i].y : 0.0f);
 }
 
 struct GatedEpilogue {
@@ -107,6 +117,8 @@ struct GatedEpilogue {
         const int row = row0 + lane;
         if (row0 >= p.M)
             return;
+        const int64_t group0 = static_cast<int64_t>(row) * p.groups + nt * 4 + half * 2;
+        uint32_t byte_g = 0, byte_u = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int col0 = nt * 128 + half * 64 + j * 32;
@@ -117,25 +129,24 @@ struct GatedEpilogue {
                 ag = region_alpha(p.tsa, p.tsg, 1.0f, row, col0);
                 au = region_alpha(p.tsa, p.tsu, 1.0f, row, col0);
             }
+            Chunk g, u;
+            scaled(g, r[j], ag, n);
+            scaled(u, r[2 + j], au, n);
             if (p.gate8.codes && row < p.M) {
-                save_group(p.gate8, row, p.groups, col0 / kAct8Group, n, r[j], ag);
-                save_group(p.up8, row, p.groups, col0 / kAct8Group, n, r[2 + j], au);
+                byte_g |= save_codes(p.gate8.codes + (group0 + j) * kAct8Group, g) << (8 * j);
+                byte_u |= save_codes(p.up8.codes + (group0 + j) * kAct8Group, u) << (8 * j);
             }
             uint32_t pk[16];
             if (p.act == MX_ACT_SILU)
-                gated32<MX_ACT_SILU>(r[j], r[2 + j], ag, au, pk);
+                gated32<MX_ACT_SILU>(g, u, pk);
             else if (p.act == MX_ACT_GELU)
-                gated32<MX_ACT_GELU>(r[j], r[2 + j], ag, au, pk);
+                gated32<MX_ACT_GELU>(g, u, pk);
             else
-                gated32<MX_ACT_GELU_TANH>(r[j], r[2 + j], ag, au, pk);
-            if (p.amax_out && row < p.M) {
+                gated32<MX_ACT_GELU_TANH>(g, u, pk);
+            if (p.amax_out && row < p.M)  // what lies past the columns is 0: act(0) * 0
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (2 * i + 1 < n)
-                        top.word(pk[i]);
-                    else if (2 * i < n)
-                        top.word(pk[i] & 0xFFFFu);
-            }
+                    top.word(pk[i]);
             // 64 bytes of a row through the staging box: lane l writes row l, then reads and
             // stores 16 bytes of row 8 i + l / 4
 #pragma unroll
@@ -162,6 +173,21 @@ struct GatedEpilogue {
                 }
             }
             __syncwarp();
+        }
+        if (p.gate8.codes && row < p.M) {  // the thread's two exponent bytes, at once where they are an aligned pair
+            if (p.pair_bytes) {
+                if (nt * 128 + half * 64 < p.N) {
+                    *reinterpret_cast<uint16_t*>(p.gate8.sf + group0) = static_cast<uint16_t>(byte_g);
+                    *reinterpret_cast<uint16_t*>(p.up8.sf + group0) = static_cast<uint16_t>(byte_u);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (nt * 128 + half * 64 + j * 32 < p.N) {
+                        p.gate8.sf[group0 + j] = static_cast<uint8_t>(byte_g >> (8 * j));
+                        p.up8.sf[group0 + j] = static_cast<uint8_t>(byte_u >> (8 * j));
+                    }
+            }
         }
     }
     __device__ __forceinline__ void finish(const GatedParams& p)
@@ -201,6 +227,7 @@ int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
     p.gate8 = a.gate8;
     p.up8 = a.up8;
     p.groups = act8_groups(N);
+    p.pair_bytes = N % 64 == 0 && reinterpret_cast<uintptr_t>(a.gate8.sf) % 2 == 0 && reinterpret_cast<uintptr_t>(a.up8.sf) % 2 == 0;
     p.kgroups = sf_kgroups(K / G::BLOCK);
     p.m_tiles = static_cast<int>((M + 255) / 256);
     p.n_tiles = static_cast<int>((N + 127) / 128);

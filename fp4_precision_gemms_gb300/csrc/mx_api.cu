@@ -859,6 +859,14 @@ mx_tensor operand_rows(const mx_tensor& t, int64_t from, int64_t rows)
     return v;
 }
 
+// The kernel for few tokens: its partial sums and counters, at a workspace's end.
+size_t gated_few_bytes(int64_t T, int64_t F)
+{
+    return T > 0 && T <= kGatedFewTokens
+               ? static_cast<size_t>(gated_few_part_bytes(T)) + round_up(static_cast<size_t>((F + 127) / 128) * sizeof(unsigned), 256)
+               : 0;
+}
+
 int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const float* amax_out)
 {
     if (reinterpret_cast<uintptr_t>(amax_out) % 4 != 0)
@@ -871,9 +879,9 @@ int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const f
 }
 
 // early: A was written by the launch before this one, which waited for all before it, and
-// amax_out is zero already.
+// amax_out is zero already.  parts, counters: as GatedArgs has them.
 int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
-                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, bool early, const Device& d, cudaStream_t s)
+                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, bool early, void* parts, unsigned* counters, const Device& d, cudaStream_t s)
 {
     for (const mx_tensor* t : {A, gate, up}) {
         const int rc = check_operand(t);
@@ -912,6 +920,8 @@ int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* 
     a.up8 = checkpoint_view(up8);
     a.amax = reinterpret_cast<unsigned*>(amax_out);
     a.early = early;
+    a.parts = parts;
+    a.counters = counters;
     return launch_gated(a, d, s);
 }
 
@@ -947,7 +957,7 @@ int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up
     const int rc = current_device(&d);
     if (rc != MX_OK)
         return rc;
-    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, false, d, static_cast<cudaStream_t>(stream));
+    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d, static_cast<cudaStream_t>(stream));
 }
 
 size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int pass)
@@ -955,11 +965,12 @@ size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int 
     if (!gated_shape(T, Kin, F, fmt))
         return 0;
     if (pass == 0)
-        return carve(nullptr, fmt, T, Kin, nullptr) + carve_gated_weights(nullptr, fmt, Kin, F, nullptr, nullptr, nullptr);
+        return carve(nullptr, fmt, T, Kin, nullptr) + carve_gated_weights(nullptr, fmt, Kin, F, nullptr, nullptr, nullptr) +
+               gated_few_bytes(T, F);
     if (pass == 1)  // D, its maximum, and the linear layer's backward
         return round_up(static_cast<size_t>(T) * static_cast<size_t>(F) * 4, 256) + 256 +
                mx_linear_workspace_bytes(T, Kin, 2 * F, fmt, 2);
-    return pass == 2 ? carve(nullptr, fmt, T, Kin, nullptr) : 0;
+    return pass == 2 ? carve(nullptr, fmt, T, Kin, nullptr) + gated_few_bytes(T, F) : 0;
 }
 
 int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, int fmt, int act, const void* W,
@@ -968,7 +979,7 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
 {
     if (!gated_shape(T, Kin, F, fmt) || !valid_act(act) || (W ? gate || up : F > 0 && (!gate || !up)))
         return MX_ERR_INVALID_ARG;
-    if (Kin == 0 || Kin % gemm_k_multiple(fmt) != 0 || !aligned16(W))
+    if (Kin == 0 || Kin % gemm_k_multiple(fmt) != 0 || !aligned16(W) || !aligned16(workspace))
         return MX_ERR_ALIGNMENT;
     int rc = check_quantize_args(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT);
     if (rc == MX_OK)
@@ -1010,14 +1021,19 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
         up = &uq;
     }
     // the tokens last: the weights are then complete before their quantization starts
+    void* parts = nullptr;
+    unsigned* counters = nullptr;
     if (quantize_few_takes(T, Kin)) {
+        uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - gated_few_bytes(T, F);
+        parts = tail;
+        counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T));
         fill_meta(&xq, T, Kin, fmt, 0);
-        rc = launch_quantize_few(X, ldx, &xq, d, s);
+        rc = launch_quantize_few(X, ldx, &xq, counters, static_cast<int>((F + 127) / 128), s);
     } else {
         rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
                            &xq, d, s);
     }
-    return rc != MX_OK ? rc : gemm_gated_impl(&xq, gate, up, act, h, ldh, nullptr, nullptr, amax_out, true, d, s);
+    return rc != MX_OK ? rc : gemm_gated_impl(&xq, gate, up, act, h, ldh, nullptr, nullptr, amax_out, true, parts, counters, d, s);
 }
 
 int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
@@ -1028,7 +1044,8 @@ int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int6
     if (!gated_shape(T, Kin, F, fmt) || !valid_act(act) || !gate8 || !up8 || (!W && F > 0))
         return MX_ERR_INVALID_ARG;
     const mx_bwd_opts o = bwd_opts_or_default(opts);
-    if (Kin == 0 || Kin % gemm_k_multiple(fmt) != 0 || T % 32 != 0 || F % 16 != 0 || !aligned16(W))
+    if (Kin == 0 || Kin % gemm_k_multiple(fmt) != 0 || T % 32 != 0 || F % 16 != 0 || !aligned16(W) ||
+        !aligned16(workspace) || !aligned16(saved))
         return MX_ERR_ALIGNMENT;
     int rc = check_quantize_args(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT);
     if (rc == MX_OK)
@@ -1073,7 +1090,7 @@ int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int6
         if (rc == MX_OK)
             rc = quantize_halves(W, Kin, F, fmt, one_scale ? wt.amax : nullptr, &gq, &uq, d, s);
     }
-    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, gate8, up8, amax_out, false, d, s);
+    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d, s);
 }
 
 int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
@@ -1090,7 +1107,8 @@ int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F
     const int64_t km = gemm_k_multiple(fmt);
     if (Kin == 0 || Kin % km != 0 || T % 32 != 0 || F % 16 != 0 || (dX && 2 * F % km != 0) || (dW && T % km != 0))
         return MX_ERR_ALIGNMENT;
-    if (reinterpret_cast<uintptr_t>(dH) % 2 != 0 || !aligned16(dX) || !aligned16(dW) || !aligned16(workspace))
+    if (reinterpret_cast<uintptr_t>(dH) % 2 != 0 || !aligned16(dX) || !aligned16(dW) || !aligned16(workspace) ||
+        !aligned16(saved))
         return MX_ERR_ALIGNMENT;
     int rc = check_direction(fmt, o.wgrad_dy_rounding, o.wgrad_hadamard);
     for (const mx_act8* c : {gate8, up8})

@@ -198,13 +198,21 @@ struct GatedArgs {
     // the launch before this one wrote x, and was itself launched after everything before
     // it had finished: the weights may be read before it has
     bool early;
+    // few tokens: partial sums (gated_few_part_bytes) and a zero word for each 128 features,
+    // or null for both
+    void* parts;
+    unsigned* counters;
 };
 constexpr int kGatedFewTokens = 64;  // up to here launch_gated takes gated_few.cu's kernel
+constexpr int kGatedFewCtas = 152;   // of that kernel, at most
+// Two slots a CTA of 2 x 128 sums for each token, tokens in fours.
+inline int64_t gated_few_part_bytes(int64_t tokens) { return int64_t{kGatedFewCtas} * 2 * 2 * 128 * ((tokens + 3) / 4) * 16; }
 int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s);
 // Rowwise quantization of a few rows with the default rules (quant_few.cu); out's
-// fields are set.  A launch that follows may start early.
+// fields are set.  Sets `zeros` words from `zero` on to zero.  A launch that follows may
+// start early.
 bool quantize_few_takes(int64_t rows, int64_t k);
-int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, const Device& d, cudaStream_t s);
+int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s);
 int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s);
 
 // The optimizer's step and the gradients' norm (optim.cu), after mx_ops.cu's checks.

@@ -60,9 +60,21 @@ __device__ __forceinline__ void encode(Oct o, float ts, bool in, int64_t oct, in
     if constexpr (fmt_is_nvfp4(FMT)) {
         byte = cvt_e4m3x2(__fdiv_rn(b, __fmul_rn(6.0f, ts)), 0.0f) & 0x7Fu;
         const float d = __fmul_rn(dec_e4m3_pos(byte), ts);
+        if (d > 0x1p-90f && d < 0x1p90f) {
+            // the quotient to nearest from the reciprocal to nearest and one residual (Markstein,
+            // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990);
+            // where x is so small that the residual is not exact the code is 0 either way
+            const float r = __frcp_rn(d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)  // a block whose scale decodes to 0 holds zeros that keep their signs
-            q[i] = d == 0.0f ? copysignf(0.0f, o[i]) : __fdiv_rn(o[i], d);
+            for (int i = 0; i < 8; ++i) {
+                const float a = __fmul_rn(o[i], r);
+                q[i] = fmaf(fmaf(-a, d, o[i]), r, a);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // a block whose scale decodes to 0 holds zeros that keep their signs
+                q[i] = d == 0.0f ? copysignf(0.0f, o[i]) : __fdiv_rn(o[i], d);
+        }
     } else {
         const int e = pow2_exponent<ELEM>(b, FMT == MX_FMT_MOSS_FP8 ? MX_SCALE_CEIL : MX_SCALE_FLOOR);
         byte = static_cast<uint32_t>(e + 127);
@@ -85,10 +97,13 @@ __device__ __forceinline__ void encode(Oct o, float ts, bool in, int64_t oct, in
 
 template <int FMT>
 __global__ void __launch_bounds__(256) quantize_few_kernel(const void* x, int64_t ld, int per_row, int octs, int64_t kgroups,
-                                                           uint8_t* codes, uint8_t* sf)
+                                                           uint8_t* codes, uint8_t* sf, unsigned* zero, int zeros)
 {
+    wait_for_launch_before();  // everything before has finished when the next launch starts
     let_next_launch_start();
     const int oct = blockIdx.x * 256 + threadIdx.x;
+    for (int i = oct; i < zeros; i += gridDim.x * 256)
+        zero[i] = 0;
     const bool in = oct < octs;
     Oct o;
     unpack_oct(in ? load_words(x, ld, oct, per_row) : make_uint4(0, 0, 0, 0), o);
@@ -99,9 +114,12 @@ __global__ void __launch_bounds__(256) quantize_few_kernel(const void* x, int64_
 template <int FMT>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(1024)
     quantize_few_cluster_kernel(const void* x, int64_t ld, int per_row, int octs, int64_t kgroups, uint8_t* codes, uint8_t* sf,
-                                float* amax, float* tensor_scale)
+                                float* amax, float* tensor_scale, unsigned* zero, int zeros)
 {
+    wait_for_launch_before();
     let_next_launch_start();
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < zeros; i += kCluster * 1024)
+        zero[i] = 0;
     __shared__ uint32_t of_warp[32];
     __shared__ uint32_t of_cta[kCluster];
     const int first = blockIdx.x * 1024 + threadIdx.x;
@@ -152,17 +170,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(1024)
 }
 
 template <int FMT>
-int launch_few(const void* x, int64_t ld, const mx_tensor* out, cudaStream_t s)
+int launch_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s)
 {
     const int per_row = static_cast<int>(out->k / 8), octs = static_cast<int>(out->rows) * per_row;
     const int64_t kgroups = sf_kgroups(out->k / fmt_block(FMT));
     uint8_t* codes = static_cast<uint8_t*>(out->codes);
     if constexpr (fmt_has_tensor_scale(FMT))
-        return launch_kernel(quantize_few_cluster_kernel<FMT>, kCluster, 1, 1024, 0, false, s, x, ld, per_row, octs, kgroups,
-                             codes, out->sf, out->amax, out->tensor_scale);
+        return launch_kernel(quantize_few_cluster_kernel<FMT>, kCluster, 1, 1024, 0, true, s, x, ld, per_row, octs, kgroups,
+                             codes, out->sf, out->amax, out->tensor_scale, zero, zeros);
     else
-        return launch_kernel(quantize_few_kernel<FMT>, static_cast<unsigned>((octs + 255) / 256), 1, 256, 0, false, s, x, ld,
-                             per_row, octs, kgroups, codes, out->sf);
+        return launch_kernel(quantize_few_kernel<FMT>, static_cast<unsigned>((octs + 255) / 256), 1, 256, 0, true, s, x, ld,
+                             per_row, octs, kgroups, codes, out->sf, zero, zeros);
 }
 
 }  // namespace
@@ -172,13 +190,13 @@ bool quantize_few_takes(int64_t rows, int64_t k)
     return rows > 0 && rows <= kGatedFewTokens && k % 32 == 0 && rows * k <= int64_t{kCluster} * 1024 * kMaxOcts * 8;
 }
 
-int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, const Device&, cudaStream_t s)
+int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s)
 {
     switch (out->fmt) {
-    case MX_FMT_MXFP8_E4M3: return launch_few<MX_FMT_MXFP8_E4M3>(x, ld, out, s);
-    case MX_FMT_MXFP4_E2M1: return launch_few<MX_FMT_MXFP4_E2M1>(x, ld, out, s);
-    case MX_FMT_MOSS_FP8: return launch_few<MX_FMT_MOSS_FP8>(x, ld, out, s);
-    default: return launch_few<MX_FMT_NVFP4>(x, ld, out, s);  // one region at most: the local scale is the tensor's
+    case MX_FMT_MXFP8_E4M3: return launch_few<MX_FMT_MXFP8_E4M3>(x, ld, out, zero, zeros, s);
+    case MX_FMT_MXFP4_E2M1: return launch_few<MX_FMT_MXFP4_E2M1>(x, ld, out, zero, zeros, s);
+    case MX_FMT_MOSS_FP8: return launch_few<MX_FMT_MOSS_FP8>(x, ld, out, zero, zeros, s);
+    default: return launch_few<MX_FMT_NVFP4>(x, ld, out, zero, zeros, s);  // one region at most: the local scale is the tensor's
     }
 }
 

@@ -35,7 +35,7 @@ COMMON = [(BAD, dict(T=-1)), (BAD, dict(F=-1)), (BAD, dict(Kin=-1)), (BAD, dict(
           (BAD, dict(X=None)), (BAD, dict(ldx=255)), (ALIGN, dict(ldx=260)), (ALIGN, dict(X=P + 8)), (ALIGN, dict(Kin=0)),
           (ALIGN, dict(Kin=192, ldx=192)), (ALIGN, dict(fmt=2, Kin=128, ldx=128)), (BAD, dict(h=None)), (BAD, dict(ldh=56)),
           (ALIGN, dict(ldh=68)), (ALIGN, dict(h=P + 4)), (ALIGN, dict(amax=P + 1)), (ALIGN, dict(W=P + 2)), (WS, dict(ws=None)),
-          (WS, dict(n=100))]
+          (WS, dict(n=100)), (ALIGN, dict(ws=P + 8))]
 
 
 @pytest.mark.parametrize("want,kw", COMMON + [(BAD, dict(W=None)), (BAD, dict(gate=operand(), up=operand())),
@@ -85,7 +85,7 @@ def bwd(L, opts=None, **k):
     (ALIGN, dict(dH=P + 1)), (ALIGN, dict(dX=P + 8)), (ALIGN, dict(dW=P + 2)), (ALIGN, dict(ws=P + 8)), (ALIGN, dict(Kin=192)),
     (ALIGN, dict(T=96, gate8=a8(96), up8=a8(96))), (ALIGN, dict(F=48, gate8=a8(128, 48), up8=a8(128, 48))),
     (ALIGN, dict(fmt=2)), (WS, dict(ws=None)), (WS, dict(n=1000)), (WS, dict(saved=None)), (WS, dict(ns=1000)),
-    (BAD, dict(opts=(0, 2, 0, 0, 0))), (UNSUP, dict(fmt=3, opts=(1, 0, 0, 0, 0)))])
+    (ALIGN, dict(saved=P + 4)), (BAD, dict(opts=(0, 2, 0, 0, 0))), (UNSUP, dict(fmt=3, opts=(1, 0, 0, 0, 0)))])
 def test_bwd_refuses(L, want, kw):
     assert bwd(L, **kw) == want
 

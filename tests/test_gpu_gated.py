@@ -57,7 +57,7 @@ def values(mx, q):
 
 
 SHAPES = [(1, 256, 32), (1, 512, 128), (2, 256, 8), (33, 256, 40), (64, 1024, 136), (130, 768, 200), (257, 512, 384), (300, 1280, 96),
-          (700, 256, 20), (70, 256, 21), (40, 256, 131)]
+          (700, 256, 20), (70, 256, 21), (40, 256, 131), (300, 512, 320), (129, 256, 64)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -95,7 +95,8 @@ def test_h_and_checkpoints(mx, fmt, T, K, F):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,K,F", [(1, 512, 128), (5, 256, 56), (300, 768, 384), (161, 256, 96)])
 def test_forms_of_the_weights_agree(mx, fmt, T, K, F):
-    """Quantized beforehand, within the call, or with the saved state: the same h."""
+    """Quantized beforehand, within the call, or with the saved state: the same h.  (K is too short for few tokens'
+    sums to be cut.)"""
     X, W = data(T, K, F, 1)
     h = mx.gated_fwd(X, mx.gated_weights(W, fmt), fmt)
     assert torch.equal(h, mx.gated_fwd(X, W, fmt))
@@ -123,19 +124,32 @@ def test_few_tokens(mx, fmt, T, K, F):
         many = mx.gemm_gated(mx.quantize(X, fmt), gate, up, act=act, save=True).h
         few = mx.gemm_gated(mx.quantize(X, fmt), gate, up, act=act, amax_out=top).h
         assert torch.equal(few, many) and float(top) == float(many.float().abs().max())
-        assert torch.equal(mx.gated_fwd(X, (gate, up), fmt, act=act, amax_out=top), many)
-        assert float(top) == float(many.float().abs().max())
+        # within the call the sums may be cut along K and joined: fp32 sums in another order, the bound of the 64-bit
+        # test on both, so twice that
+        whole = mx.gated_fwd(X, (gate, up), fmt, act=act, amax_out=top)
+        assert float(top) == float(whole.float().abs().max())
+        assert torch.equal(whole, mx.gated_fwd(X, (gate, up), fmt, act=act))  # one order
+        a, b, c = (values(mx, q) for q in (mx.quantize(X, fmt), gate, up))
+        g, u = a @ b.T, a @ c.T
+        eg, eu = ((a.abs() @ w.abs().T) * (K * 2.0 ** -23) for w in (b, c))
+        want = activation(g, act) * u
+        bound = 1.13 * eg * (u.abs() + eu) + (g.abs() + eg) * eu + (HALF + 2.0 ** -16) * want.abs() + 1e-30
+        assert ((whole.double() - want).abs() <= 1.01 * bound).all()
 
 
 def test_few_tokens_of_a_wide_matrix(mx):
     """More values than the small quantization holds, rows of a wider matrix, and both captured."""
-    for T, K in ((64, 8192 + 256), (64, 8192), (5, 512)):
+    for T, K in ((64, 8192 + 256), (64, 8192), (5, 256)):
         X, W = data(T, K + 64, 256, 3)
         X, W = X[:, 32:K + 32], W[:, :K].contiguous()
         for fmt in ("nvfp4", "mxfp8"):
             w = mx.gated_weights(W, fmt)
-            want = mx.gemm_gated(mx.quantize(X.contiguous(), fmt), *w, save=True).h
-            assert torch.equal(mx.gated_fwd(X, w, fmt), want)
+            many = mx.gemm_gated(mx.quantize(X.contiguous(), fmt), *w, save=True).h.double()
+            want = mx.gated_fwd(X, w, fmt)
+            # sums of K products in another order: their size is at most sqrt(K) here, 2^-23 K of it each
+            assert ((want.double() - many).abs() <= 2 * HALF * many.abs() + K ** 1.5 * 2.0 ** -23 * (1 + many.abs())).all()
+            if K == 256:  # too few steps to cut
+                assert torch.equal(want.double(), many)
             g = torch.cuda.CUDAGraph()
             with torch.cuda.graph(g):
                 h = mx.gated_fwd(X, w, fmt)
@@ -143,6 +157,27 @@ def test_few_tokens_of_a_wide_matrix(mx):
                 h.zero_()
                 g.replay()
                 assert torch.equal(h, want)
+
+
+def test_checkpoint_of_values_that_are_not_finite(mx):
+    """Products that overflow: their codes are NaN, their groups' other values keep their own scale."""
+    T, K, F = 130, 256, 96
+    X, W = data(T, K, F, 12)
+    X[5] *= 2.0 ** 100
+    W[7] *= 2.0 ** 100  # gate feature 7
+    W[F + 40] *= 2.0 ** 100  # up feature 40
+    x, (gate, up) = mx.quantize(X, "mxfp8"), mx.gated_weights(W, "mxfp8")
+    h, g8, u8 = mx.gemm_gated(x, gate, up, save=True)
+    g, u = products(mx, x, gate, up)
+    assert not torch.isfinite(g[5, 7]) and not torch.isfinite(u[5, 40])
+    for got, want in ((g8, mx.act8_save(g)), (u8, mx.act8_save(u))):
+        assert torch.equal(got.codes & 127, want.codes & 127) and torch.equal(got.sf, want.sf)
+    room = torch.full((T, 8, 32), 77, dtype=torch.uint8, device="cuda")
+    sf = torch.full((T * 3 + 1,), 77, dtype=torch.uint8, device="cuda")  # bytes at an odd address
+    odd = mx.Act8(room[:, :3].reshape(T, 96).contiguous(), sf[1:].view(T, 3), F)
+    kept = mx.gated_fwd_save(X[:128], W, "mxfp8", gate8=mx.Act8(odd.codes[:128], odd.sf[:128], F))
+    assert torch.equal(kept.gate.codes & 127, g8.codes[:128] & 127) and torch.equal(kept.gate.sf, g8.sf[:128])
+    assert (sf[0] == 77) and (sf[1 + 128 * 3:] == 77).all()
 
 
 TRAIN = [(256, 256, 128), (256, 512, 384), (512, 768, 128 + 256), (256, 256, 640)]
