@@ -1,0 +1,262 @@
+// gated_bwd.cu -- the gated block's backward activation and the quantization of its
+// result in one pass: from dH and the checkpoints of g and u straight to the MXFP8 /
+// MXFP4 operands of both gradient products.
+//
+//   D[T, 2F] = [dH u act'(g), dH act(g)], rounded to bf16 as mx_act_bwd writes it, then
+//   encoded along its rows (the data gradient's operand) and along its columns (the
+//   weight gradient's, transposed), to nearest with the FLOOR rule
+//
+// A CTA takes 128 tokens x 128 features, the extent of one 512-byte scale chunk in both
+// directions.  First each thread computes eights of a row, encodes them (four lanes share
+// a block's maximum) and leaves the bf16 values in shared memory; then each thread
+// encodes two columns of 32 tokens.  Chunks of scale bytes are gathered in shared memory
+// and written whole.  Bytes: 2 + 2.06 a value of dH read, 4.12 written (FP8); the
+// two passes that this replaces move D's 4 bytes out and in again as well.
+#include <cuda_bf16.h>
+
+#include "mx_act8.cuh"
+#include "mx_activate.cuh"
+#include "mx_codec.cuh"
+#include "mx_internal.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kTile = 128;     // tokens and features
+constexpr int kThreads = 256;
+constexpr int kPitch = kTile * 2 + 16;  // bytes of a staged row
+constexpr int kStage = kTile * kPitch;  // of one operand
+constexpr int kSmem = 2 * kStage + 4 * 512;
+constexpr int kFlight = 2;     // eights of a thread whose loads are in flight together
+
+struct BwdQuantParams {
+    const __nv_bfloat16* dh;
+    int64_t ldh;
+    Act8View g8, u8;
+    int64_t T, F;
+    uint8_t* row_codes;  // [T, 2F]
+    uint8_t* row_sf;
+    uint8_t* col_codes;  // [2F, T]
+    uint8_t* col_sf;
+};
+
+// max(|a|, |b|) by halves; the signs of the result are not cleared.
+__device__ __forceinline__ uint32_t top_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 scaled(uint32_t w, float2 s) { return __fmul2_rn(unpack_bf16x2(w), s); }
+
+// Offset of (row r of 128, block kb of 4) in a chunk of scale bytes.
+__device__ __forceinline__ int chunk_at(int r, int kb) { return (r & 31) * 16 + (r >> 5) * 4 + kb; }
+
+// Eight values of a row whose block four lanes hold: their codes and the block's byte.
+template <int ELEM>
+__device__ __forceinline__ uint32_t encode_row(uint4 w, uint2& codes)
+{
+    uint32_t m = top_bf16x2(top_bf16x2(w.x, w.y), top_bf16x2(w.z, w.w));
+    m = top_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = top_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) & 0x7FFF7FFFu;
+    const int e = pow2_exponent<ELEM>(__uint_as_float(max(m << 16, m & 0xFFFF0000u)), MX_SCALE_FLOOR);
+    const float2 s = both(exp2_neg(e));
+    const float2 a = scaled(w.x, s), b = scaled(w.y, s), c = scaled(w.z, s), d = scaled(w.w, s);
+    if constexpr (ELEM == kElemE4M3) {
+        codes = make_uint2(cvt_e4m3x2(a.x, a.y) | cvt_e4m3x2(b.x, b.y) << 16, cvt_e4m3x2(c.x, c.y) | cvt_e4m3x2(d.x, d.y) << 16);
+    } else {
+        const float q[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+        codes.x = cvt_e2m1x8(q);
+    }
+    return static_cast<uint32_t>(e + 127);
+}
+
+// 32 tokens of two neighbouring columns.
+template <int ELEM>
+__device__ __forceinline__ void encode_columns(const uint32_t (&w)[32], uint8_t* to_a, uint8_t* to_b, uint8_t* byte_a,
+                                               uint8_t* byte_b)
+{
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m[i] = top_bf16x2(top_bf16x2(w[i], w[i + 8]), top_bf16x2(w[i + 16], w[i + 24]));
+#pragma unroll
+    for (int h = 4; h > 0; h >>= 1)
+#pragma unroll
+        for (int i = 0; i < h; ++i)
+            m[i] = top_bf16x2(m[i], m[i + h]);
+    m[0] &= 0x7FFF7FFFu;
+    const int ea = pow2_exponent<ELEM>(__uint_as_float(m[0] << 16), MX_SCALE_FLOOR);
+    const int eb = pow2_exponent<ELEM>(__uint_as_float(m[0] & 0xFFFF0000u), MX_SCALE_FLOOR);
+    const float2 s = make_float2(exp2_neg(ea), exp2_neg(eb));
+    *byte_a = static_cast<uint8_t>(ea + 127);
+    *byte_b = static_cast<uint8_t>(eb + 127);
+    if constexpr (ELEM == kElemE4M3) {
+        uint32_t a[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 p = scaled(w[4 * i], s), q = scaled(w[4 * i + 1], s), r = scaled(w[4 * i + 2], s), t = scaled(w[4 * i + 3], s);
+            a[i] = cvt_e4m3x2(p.x, q.x) | cvt_e4m3x2(r.x, t.x) << 16;
+            b[i] = cvt_e4m3x2(p.y, q.y) | cvt_e4m3x2(r.y, t.y) << 16;
+        }
+        reinterpret_cast<uint4*>(to_a)[0] = make_uint4(a[0], a[1], a[2], a[3]);
+        reinterpret_cast<uint4*>(to_a)[1] = make_uint4(a[4], a[5], a[6], a[7]);
+        reinterpret_cast<uint4*>(to_b)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+        reinterpret_cast<uint4*>(to_b)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+    } else {
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float qa[8], qb[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 p = scaled(w[8 * i + k], s);
+                qa[k] = p.x;
+                qb[k] = p.y;
+            }
+            a[i] = cvt_e2m1x8(qa);
+            b[i] = cvt_e2m1x8(qb);
+        }
+        *reinterpret_cast<uint4*>(to_a) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4*>(to_b) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+}
+
+template <int ACT, int ELEM>
+__global__ void __launch_bounds__(kThreads, 3) gated_bwd_quantize_kernel(const BwdQuantParams p)
+{
+    constexpr int EPB = ELEM == kElemE4M3 ? 1 : 2;  // values a byte
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* chunks = smem + 2 * kStage;  // rowwise gate, up; columnwise gate, up
+    const int f_tiles = static_cast<int>(p.F / kTile);
+    const int tt = blockIdx.x / f_tiles, ft = blockIdx.x - tt * f_tiles;
+    const int64_t t0 = static_cast<int64_t>(tt) * kTile, f0 = static_cast<int64_t>(ft) * kTile;
+    const int64_t groups = p.F / kAct8Group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // rows: a warp takes two at a time, sixteen lanes each
+    const int oct = lane & 15;
+#pragma unroll 1
+    for (int it = 0; it < 8; it += kFlight) {
+        RawOct<__nv_bfloat16> dh[kFlight];
+        uint2 cg[kFlight], cu[kFlight];
+        uint32_t bg[kFlight], bu[kFlight];
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const int64_t t = t0 + (it + k) * 16 + warp * 2 + (lane >> 4);
+            dh[k].load(p.dh + t * p.ldh + f0 + oct * 8);
+            const int64_t at = t * p.F + f0 + oct * 8;  // F is a multiple of 32: the checkpoints' rows have no pads
+            cg[k] = __ldcs(reinterpret_cast<const uint2*>(p.g8.codes + at));
+            cu[k] = __ldcs(reinterpret_cast<const uint2*>(p.u8.codes + at));
+            const int64_t group = t * groups + (f0 >> 5) + (oct >> 2);
+            bg[k] = p.g8.sf[group];
+            bu[k] = p.u8.sf[group];
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const int r = (it + k) * 16 + warp * 2 + (lane >> 4);
+            Oct d, g, u, dg, du;
+            dh[k].get(d);
+            decode_oct(cg[k], g);
+            decode_oct(cu[k], u);
+            const float2 sg = both(act8_scale(bg[k])), su = both(act8_scale(bu[k]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // the order of mx_act_bwd's products
+                const ValueSlope f = activate<ACT, true>(__fmul2_rn(g.p[j], sg));
+                const float2 up = __fmul2_rn(u.p[j], su);
+                dg.p[j].x = d.p[j].x * f.slope.x, dg.p[j].y = d.p[j].y * f.slope.y;
+                dg.p[j].x *= up.x, dg.p[j].y *= up.y;
+                du.p[j].x = d.p[j].x * f.value.x, du.p[j].y = d.p[j].y * f.value.y;
+            }
+            const uint4 wg = pack_oct(dg), wu = pack_oct(du);
+            *reinterpret_cast<uint4*>(smem + r * kPitch + oct * 16) = wg;
+            *reinterpret_cast<uint4*>(smem + kStage + r * kPitch + oct * 16) = wu;
+            uint2 g_codes, u_codes;
+            const uint32_t g_byte = encode_row<ELEM>(wg, g_codes), u_byte = encode_row<ELEM>(wu, u_codes);
+            uint8_t* to = p.row_codes + ((t0 + r) * 2 * p.F + f0 + oct * 8) / EPB;
+            if constexpr (ELEM == kElemE4M3) {
+                *reinterpret_cast<uint2*>(to) = g_codes;
+                *reinterpret_cast<uint2*>(to + p.F) = u_codes;
+            } else {
+                *reinterpret_cast<uint32_t*>(to) = g_codes.x;
+                *reinterpret_cast<uint32_t*>(to + p.F / 2) = u_codes.x;
+            }
+            if ((lane & 3) == 0) {
+                chunks[chunk_at(r, oct >> 2)] = static_cast<uint8_t>(g_byte);
+                chunks[512 + chunk_at(r, oct >> 2)] = static_cast<uint8_t>(u_byte);
+            }
+        }
+    }
+    __syncthreads();
+    // columns: warp w takes 64 features (lane: two) of operand w / 4, halves w % 2, and
+    // every other block of 32 tokens
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int operand = warp >> 2, pair = (warp & 1) * 32 + lane, block = ((warp >> 1) & 1) + 2 * k;
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            w[i] = *reinterpret_cast<const uint32_t*>(smem + operand * kStage + (block * 32 + i) * kPitch + pair * 4);
+        const int64_t f = operand * p.F + f0 + 2 * pair;
+        uint8_t* to = p.col_codes + (f * p.T + t0 + block * 32) / EPB;
+        uint8_t* bytes = chunks + (2 + operand) * 512;
+        encode_columns<ELEM>(w, to, to + p.T / EPB, bytes + chunk_at(2 * pair, block), bytes + chunk_at(2 * pair + 1, block));
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {  // four chunks of 32 x 16 bytes
+        const int c = threadIdx.x >> 5;
+        const int64_t f_chunks = p.F / kTile, t_chunks = p.T / kTile;
+        uint8_t* to = c < 2 ? p.row_sf + (tt * 2 * f_chunks + c * f_chunks + ft) * 512
+                            : p.col_sf + (((c - 2) * f_chunks + ft) * t_chunks + tt) * 512;
+        reinterpret_cast<uint4*>(to)[lane] = reinterpret_cast<const uint4*>(chunks + c * 512)[lane];
+    }
+}
+
+template <int ACT, int ELEM>
+int launch(const BwdQuantParams& p, const Device& d, cudaStream_t s)
+{
+    constexpr auto kernel = gated_bwd_quantize_kernel<ACT, ELEM>;
+    static int configured_device = -1;
+    if (configured_device != d.id) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return MX_ERR_CUDA;
+        configured_device = d.id;
+    }
+    return launch_kernel(kernel, static_cast<unsigned>((p.T / kTile) * (p.F / kTile)), 1, kThreads, kSmem, false, s, p);
+}
+template <int ELEM>
+int launch(int act, const BwdQuantParams& p, const Device& d, cudaStream_t s)
+{
+    switch (act) {
+    case MX_ACT_SILU: return launch<MX_ACT_SILU, ELEM>(p, d, s);
+    case MX_ACT_GELU: return launch<MX_ACT_GELU, ELEM>(p, d, s);
+    default: return launch<MX_ACT_GELU_TANH, ELEM>(p, d, s);
+    }
+}
+
+}  // namespace
+
+bool gated_bwd_quantize_takes(const ActArgs& a, int fmt)
+{
+    return (fmt == MX_FMT_MXFP8_E4M3 || fmt == MX_FMT_MXFP4_E2M1) && a.rows % kTile == 0 && a.cols % kTile == 0 && a.ldh % 8 == 0 &&
+           reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.rows / kTile) * (a.cols / kTile) <= INT32_MAX;
+}
+
+int launch_gated_bwd_quantize(const ActArgs& a, const mx_tensor& rows, const mx_tensor& cols, int fmt, const Device& d,
+                              cudaStream_t s)
+{
+    BwdQuantParams p;
+    p.dh = static_cast<const __nv_bfloat16*>(a.h);
+    p.ldh = a.ldh;
+    p.g8 = a.gate8;
+    p.u8 = a.up8;
+    p.T = a.rows;
+    p.F = a.cols;
+    p.row_codes = static_cast<uint8_t*>(rows.codes);
+    p.row_sf = rows.sf;
+    p.col_codes = static_cast<uint8_t*>(cols.codes);
+    p.col_sf = cols.sf;
+    return fmt == MX_FMT_MXFP8_E4M3 ? launch<kElemE4M3>(a.act, p, d, s) : launch<kElemE2M1>(a.act, p, d, s);
+}
+
+}  // namespace mx

@@ -725,6 +725,25 @@ void carve_saved(uint8_t* saved, int64_t T, int64_t Kin, int64_t Nout, int fmt, 
     fill_meta(wt, Kin, Nout, fmt, 0);
 }
 
+// Both gradients' products: the data gradient on s, the weight gradient on the side
+// stream when both are wanted.
+int gradient_gemms(const mx_tensor& dyr, const mx_tensor& dyt, const mx_tensor& wt, const mx_tensor& xt, int64_t Kin, void* dX,
+                   int dx_dtype, void* dW, int dw_dtype, const Device& d, cudaStream_t s)
+{
+    int rc = MX_OK;
+    cudaStream_t sw = dX && dW ? fork_begin(d, s) : nullptr;
+    if (dX)
+        rc = gemm_impl(&dyr, &wt, 1.0f, dX, Kin, dx_dtype, d, s);
+    if (dW && rc == MX_OK)
+        rc = gemm_impl(&dyt, &xt, 1.0f, dW, Kin, dw_dtype, d, sw ? sw : s);
+    if (sw) {
+        const int rj = fork_end(d, sw, s);
+        if (rc == MX_OK)
+            rc = rj;
+    }
+    return rc;
+}
+
 }  // namespace
 
 int mx_linear_fwd_save(const void* X, const void* W, int64_t T, int64_t Kin, int64_t Nout, int fmt,
@@ -802,20 +821,7 @@ int mx_linear_bwd_saved(const void* dY, int64_t T, int64_t Kin, int64_t Nout, in
         rc = quantize_impl(dY, T, Nout, Nout, MX_COLWISE, fmt, block, o.wgrad_dy_rounding, MX_SCALE_DEFAULT, o.seed,
                            o.stream_id, o.wgrad_hadamard, dy_amax, &dyt, d, s);
     }
-    if (rc != MX_OK)
-        return rc;
-    // data gradient on s, weight gradient on the side stream when both are wanted
-    cudaStream_t sw = dX && dW ? fork_begin(d, s) : nullptr;
-    if (dX)
-        rc = gemm_impl(&dyr, &wt, 1.0f, dX, Kin, dx_dtype, d, s);
-    if (dW && rc == MX_OK)
-        rc = gemm_impl(&dyt, &xt, 1.0f, dW, Kin, dw_dtype, d, sw ? sw : s);
-    if (sw) {
-        const int rj = fork_end(d, sw, s);
-        if (rc == MX_OK)
-            rc = rj;
-    }
-    return rc;
+    return rc != MX_OK ? rc : gradient_gemms(dyr, dyt, wt, xt, Kin, dX, dx_dtype, dW, dw_dtype, d, s);
 }
 
 namespace {
@@ -1147,6 +1153,17 @@ int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F
     a.dup = ws + 2 * F;
     a.lddg = a.lddu = 2 * F;
     a.amax = takes_amax ? reinterpret_cast<unsigned*>(word) : nullptr;
+    if (dX && dW && o.wgrad_dy_rounding == MX_ROUND_RNE && !o.wgrad_hadamard && gated_bwd_quantize_takes(a, fmt)) {
+        mx_tensor dr, dt, xt, wt;  // where mx_linear_bwd_saved would have them
+        uint8_t* at = ws + d_bytes + 256;
+        const size_t off = carve(at, fmt, T, 2 * F, &dr);
+        carve(at + off, fmt, 2 * F, T, &dt);
+        carve_saved(static_cast<uint8_t*>(const_cast<void*>(saved)), T, Kin, 2 * F, fmt, 0, &xt, &wt);
+        fill_meta(&dr, T, 2 * F, fmt, 0);
+        fill_meta(&dt, 2 * F, T, fmt, 0);
+        rc = launch_gated_bwd_quantize(a, dr, dt, fmt, d, s);
+        return rc != MX_OK ? rc : gradient_gemms(dr, dt, wt, xt, Kin, dX, dx_dtype, dW, dw_dtype, d, s);
+    }
     if ((rc = launch_act_bwd(a, d, s)) != MX_OK)
         return rc;
     return mx_linear_bwd_saved(ws, T, Kin, 2 * F, fmt, takes_amax ? word : nullptr, &o, saved, saved_bytes, dX, dx_dtype,

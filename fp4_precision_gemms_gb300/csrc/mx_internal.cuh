@@ -215,6 +215,12 @@ bool quantize_few_takes(int64_t rows, int64_t k);
 int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s);
 int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s);
 
+// The gated block's backward activation with its result encoded at once (gated_bwd.cu):
+// D's rowwise operand [T, 2F] and columnwise one [2F, T] in place of a.dgate and a.dup.
+bool gated_bwd_quantize_takes(const ActArgs& a, int fmt);
+int launch_gated_bwd_quantize(const ActArgs& a, const mx_tensor& rows, const mx_tensor& cols, int fmt, const Device& d,
+                              cudaStream_t s);
+
 // The optimizer's step and the gradients' norm (optim.cu), after mx_ops.cu's checks.
 constexpr int kGradNormCtas = 1024;        // partial sums that one launch leaves at most
 int64_t grad_norm_parts(int64_t count);    // partial sums in the workspace
