@@ -1153,7 +1153,8 @@ int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F
     a.dup = ws + 2 * F;
     a.lddg = a.lddu = 2 * F;
     a.amax = takes_amax ? reinterpret_cast<unsigned*>(word) : nullptr;
-    if (dX && dW && o.wgrad_dy_rounding == MX_ROUND_RNE && !o.wgrad_hadamard && gated_bwd_quantize_takes(a, fmt)) {
+    if (dX && dW && o.wgrad_dy_rounding == MX_ROUND_RNE && !o.wgrad_hadamard && gated_bwd_quantize_takes(a, fmt) &&
+        reinterpret_cast<uintptr_t>(workspace) % 32 == 0) {  // the columns' codes leave by whole sectors
         mx_tensor dr, dt, xt, wt;  // where mx_linear_bwd_saved would have them
         uint8_t* at = ws + d_bytes + 256;
         const size_t off = carve(at, fmt, T, 2 * F, &dr);

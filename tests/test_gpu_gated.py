@@ -280,6 +280,16 @@ def test_given_buffers_and_strides(mx, fmt):
         a = mx.gated_bwd(dh, kept, K, fmt, workspace=ws)
         b = mx.gated_bwd(dh.contiguous(), kept, K, fmt)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    else:  # FP8, whole tiles: rows at odd addresses and a workspace off the sector's grid take the separate passes
+        F = 128
+        X, W = data(T, K, F, 6)
+        kept = mx.gated_fwd_save(X, W, fmt)
+        dh = torch.randn(T, F + 3, device="cuda").to(BF)[:, 1:F + 1]
+        n = mx.gated_workspace_bytes(T, K, F, fmt, "bwd")
+        ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
+        want = mx.gated_bwd(dh.contiguous(), kept, K, fmt)
+        for a in (mx.gated_bwd(dh, kept, K, fmt), mx.gated_bwd(dh.contiguous(), kept, K, fmt, workspace=ws[16:])):
+            assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1])
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
