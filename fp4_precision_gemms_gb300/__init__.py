@@ -1088,10 +1088,10 @@ def _flats(ts, what, dev):
     """(pointers, sizes, types' numbers) of many tensors after checking them; by maps over
     torch's own methods, which for tens of tensors take a third of a loop's time."""
     try:
-        ok = set(map(torch.Tensor.get_device, ts)) <= {dev.index} and all(map(torch.Tensor.is_contiguous, ts))
-        if ok:
-            return (list(map(torch.Tensor.data_ptr, ts)), list(map(torch.Tensor.numel, ts)),
-                    list(map(OUT.__getitem__, map(_dtype_of, ts))))
+        if set(map(torch.Tensor.get_device, ts)) <= {dev.index} and all(map(torch.Tensor.is_contiguous, ts)):
+            kinds = set(map(_dtype_of, ts))
+            types = [OUT[kinds.pop()]] * len(ts) if len(kinds) == 1 else list(map(OUT.__getitem__, map(_dtype_of, ts)))
+            return list(map(torch.Tensor.data_ptr, ts)), list(map(torch.Tensor.numel, ts)), types
     except (KeyError, TypeError):
         pass
     for t in ts:  # names what is wrong
@@ -1161,7 +1161,7 @@ class AdamW:
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
                  state: str = "fp32", copies=None, rounding: str = "rne", seed: int = 0, capturable: bool = False):
-        self.params = list(params)
+        self.params = tuple(params)
         if not self.params:
             raise MXError(MX_ERR_INVALID_ARG, "AdamW needs a tensor")
         n = len(self.params)
@@ -1170,7 +1170,7 @@ class AdamW:
         bits = _look_up({"fp32": 32, "8bit": 8}, state, "state")
         self._rounding = _look_up(ROUNDING, rounding, "rounding")
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
-        self.copies = list(copies) if copies is not None else [None] * n
+        self.copies = tuple(copies) if copies is not None else (None,) * n
         if len(decay) != n or len(self.copies) != n:
             raise MXError(MX_ERR_INVALID_ARG, f"weight_decay and copies have one entry for each of the {n} tensors")
         self.t = 0
@@ -1227,14 +1227,8 @@ class AdamW:
         spans = sorted(s for s in spans if s[1] > s[0])
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise MXError(MX_ERR_INVALID_ARG, "parameters and copies must not share memory")
-        self._written = self.params + [c for c in self.copies if c is not None]
+        self._written = self.params + tuple(c for c in self.copies if c is not None)
         self._where = list(map(torch.Tensor.data_ptr, self._written))
-
-    def _moved(self):
-        """Whether a parameter or copy is another tensor, or elsewhere, than when last checked."""
-        now = self.params + [c for c in self.copies if c is not None]
-        return (len(now) != len(self._written) or any(map(operator.is_not, now, self._written))
-                or list(map(torch.Tensor.data_ptr, now)) != self._where)
 
     def step(self, grads, grad_scale: torch.Tensor | None = None, amax_out: torch.Tensor | None = None, lr=None,
              t: int | None = None, stream=None) -> None:
@@ -1252,7 +1246,7 @@ class AdamW:
         n = len(self.params)
         if len(grads) != n:
             raise MXError(MX_ERR_INVALID_ARG, f"{len(grads)} gradients for {n} tensors")
-        if self._moved():
+        if list(map(torch.Tensor.data_ptr, self._written)) != self._where:  # storage that was replaced
             self._check_written()
         given = [g for g in grads if g is not None]
         at = pointers, sizes, types = _flats(given, "a gradient", dev) if given else ([], [], [])

@@ -71,7 +71,10 @@ __device__ __forceinline__ void fold(Top<__nv_bfloat16>& top, const Oct& o)
     const uint4 w = pack_oct(o);
     top.word(w.x), top.word(w.y), top.word(w.z), top.word(w.w);
 }
-bool whole(const void* p, int64_t n, int bytes) { return n % 8 == 0 && reinterpret_cast<uintptr_t>(p) % (8 * bytes) == 0; }
+bool whole(const void* p, int64_t n, unsigned bytes)  // bytes of a value: 2 or 4
+{
+    return ((n & 7) | static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) & (8 * bytes - 1))) == 0;
+}
 
 // ---------------------------------------------------------------- AdamW
 // The tensors of one launch, in its parameters: no table to copy to the device
@@ -509,15 +512,25 @@ int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_o
     t.k0 = static_cast<uint32_t>(o.seed);
     t.k1 = static_cast<uint32_t>(o.seed >> 32);
     // one launch for each kind of tensor (types, 8-bit moments, alignment) and 128 of them
+    auto kind_of = [](const mx_adamw_tensor& x) {
+        const bool p16 = x.p_dtype == MX_OUT_BF16, g16 = x.g_dtype == MX_OUT_BF16, eight = x.bits == 8;
+        const bool wide = whole(x.param, x.n, p16 ? 2 : 4) && whole(x.grad, x.n, g16 ? 2 : 4) && whole(x.copy, x.n, 2) &&
+                          (eight || (whole(x.m, x.n, 4) && whole(x.v, x.n, 4)));
+        return (p16 ? 1 : 0) | (g16 ? 2 : 0) | (eight ? 4 : 0) | (wide ? 0 : 8);
+    };
+    unsigned kinds = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (tensors[i].n > 0)
+            kinds |= 1u << kind_of(tensors[i]);
     for (int kind = 0; kind < 16; ++kind) {
-        const bool p16 = kind & 1, g16 = kind & 2, eight = kind & 4, any = kind & 8;
+        if (!(kinds >> kind & 1))
+            continue;
+        const bool p16 = kind & 1, g16 = kind & 2, any = kind & 8;
+        const int bits = kind & 4 ? 8 : 32;
+        const bool sr = o.rounding == MX_ROUND_SR;
         t.count = 0;
         t.tiles = 0;
         auto flush = [&]() -> int {
-            if (t.count == 0)
-                return MX_OK;
-            const int bits = eight ? 8 : 32;
-            const bool sr = o.rounding == MX_ROUND_SR;
             const int rc = p16 ? (g16 ? launch_adamw<__nv_bfloat16, __nv_bfloat16>(t, bits, sr, any, d, s)
                                       : launch_adamw<__nv_bfloat16, float>(t, bits, sr, any, d, s))
                                : (g16 ? launch_adamw<float, __nv_bfloat16>(t, bits, sr, any, d, s)
@@ -528,13 +541,9 @@ int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_o
         };
         for (int64_t i = 0; i < count; ++i) {
             const mx_adamw_tensor& x = tensors[i];
-            const bool wide = whole(x.param, x.n, p16 ? 2 : 4) && whole(x.grad, x.n, g16 ? 2 : 4) && whole(x.copy, x.n, 2) &&
-                              (x.bits == 8 || (whole(x.m, x.n, 4) && whole(x.v, x.n, 4)));
-            if (x.n == 0 || (x.p_dtype == MX_OUT_BF16) != p16 || (x.g_dtype == MX_OUT_BF16) != g16 ||
-                (x.bits == 8) != eight || wide == any)
+            if (x.n == 0 || kind_of(x) != kind)
                 continue;
-            const uint32_t tiles = tiles_of(x.n, x.bits);
-            if (t.count == kAdamwEntries || t.tiles + static_cast<uint64_t>(tiles) > 0x7FFFFFFFu) {
+            if (t.count == kAdamwEntries) {
                 const int rc = flush();
                 if (rc != MX_OK)
                     return rc;
@@ -552,7 +561,7 @@ int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_o
             e.index = static_cast<uint32_t>(i);
             e.wd = static_cast<float>(x.weight_decay);
             e.decay = static_cast<float>(1.0 - o.lr * x.weight_decay);
-            t.tiles += tiles;
+            t.tiles += tiles_of(x.n, x.bits);  // at most 2^23 each
         }
         const int rc = flush();
         if (rc != MX_OK)

@@ -100,7 +100,7 @@ def test_python_side_refusals():
         with pytest.raises(mx.MXError):
             opt.step(a, **kw)
     assert opt.t == 0 and not p.any()
-    opt.params[0] = torch.zeros(32, device="cuda")  # another size
+    p.data = torch.zeros(32, device="cuda")  # another size
     with pytest.raises(mx.MXError):
         opt.step([g])
     with pytest.raises(mx.MXError):
