@@ -17,17 +17,17 @@ namespace mx {
 namespace {
 
 struct GatedParams {
+    CUtensorMap map_h;  // h in boxes of 32 rows x 32 columns
     const float* tsa;
     const float* tsg;
     const float* tsu;
-    __nv_bfloat16* h;
-    int64_t ldh;
     int M, N, K;  // N: features
     int act;
     int ts_region;
     Act8View gate8, up8;
     int64_t groups;   // checkpoint groups of a row
     int pair_bytes;   // a thread's two exponent bytes are an aligned pair
+    int sectors;      // the checkpoints' codes start on 32-byte boundaries
     int64_t kgroups;
     int m_tiles, n_tiles, group_m;  // 256 x 128 tiles
     unsigned* amax_out;
@@ -53,8 +53,19 @@ __device__ __noinline__ uint32_t encode_not_finite(Chunk& x)
     return act8_byte(m);
 }
 
-// The checkpoint of 32 columns that one thread holds; returns their exponent byte.
-__device__ __forceinline__ uint32_t save_codes(uint8_t* codes, Chunk x)
+// 32 bytes to a multiple of 32 (sectors) or of 16.
+__device__ __forceinline__ void store32(uint8_t* to, bool sectors, const uint32_t (&w)[8])
+{
+    if (sectors) {
+        store_sector(to, w);
+    } else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// The checkpoint codes of 32 columns that one thread holds; returns their exponent byte.
+__device__ __forceinline__ uint32_t encode_group(Chunk x, uint32_t (&w)[8])
 {
     float m[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -63,15 +74,11 @@ __device__ __forceinline__ uint32_t save_codes(uint8_t* codes, Chunk x)
     m[0] = max_nan(m[0], m[1]);
     const uint32_t e = non_finite(m[0]) ? encode_not_finite(x) : act8_byte(m[0]);
     const float2 s = both(act8_inverse(e));
-    uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float2 a = __fmul2_rn(x.v[2 * i], s), b = __fmul2_rn(x.v[2 * i + 1], s);
         w[i] = cvt_e4m3x2(a.x, a.y) | cvt_e4m3x2(b.x, b.y) << 16;
     }
-    uint4* dst = reinterpret_cast<uint4*>(codes);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     return e;
 }
 
@@ -99,6 +106,7 @@ struct GatedEpilogue {
     using Params = GatedParams;
     static constexpr int kHalves = 2;
     float ag, au;
+    bool busy = false;  // the warp's staging box may still be read by a store
     Top<__nv_bfloat16> top;
 
     __device__ __forceinline__ explicit GatedEpilogue(const GatedParams& p)
@@ -107,6 +115,31 @@ struct GatedEpilogue {
         ag = __fmul_rn(ta, p.tsg ? *p.tsg : 1.0f);
         au = __fmul_rn(ta, p.tsu ? *p.tsu : 1.0f);
     }
+    // 64 bytes of each of the warp's 32 rows to column x on, by a tensor store that clips
+    // what lies outside the matrix.  The box is swizzled (16-byte pieces of a 64-byte row
+    // exchanged by the row's pair number), which keeps the lanes' writes apart in the banks.
+    // The stores that leave the chip then cost the load/store unit nothing, on which the
+    // warps that feed the scales depend.
+    __device__ __forceinline__ void send(const CUtensorMap& map, const uint32_t (&w)[16], int x, int row0, int lane, uint8_t* stg)
+    {
+        if (busy) {  // the previous store has read the box
+            if (lane == 0)
+                bulk_wait_read_all();
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(&map, smem_u32(stg), x, row0);
+            bulk_commit();
+        }
+        busy = true;
+    }
+
     // chunks 0, 1: gate columns, 2, 3: the same up columns
     static __device__ __forceinline__ int column(int half, int j) { return (j >> 1) * 128 + half * 64 + (j & 1) * 32; }
 
@@ -117,11 +150,15 @@ struct GatedEpilogue {
         const int row = row0 + lane;
         if (row0 >= p.M)
             return;
-        const int64_t group0 = static_cast<int64_t>(row) * p.groups + nt * 4 + half * 2;
+        const int col = nt * 128 + half * 64;
+        if (col >= p.N)
+            return;
+        const int64_t group0 = static_cast<int64_t>(row) * p.groups + col / kAct8Group;
+        const bool save = p.gate8.codes && row < p.M;
         uint32_t byte_g = 0, byte_u = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int col0 = nt * 128 + half * 64 + j * 32;
+            const int col0 = col + j * 32;
             const int n = p.N - col0;
             if (n <= 0)
                 break;
@@ -132,9 +169,12 @@ struct GatedEpilogue {
             Chunk g, u;
             scaled(g, r[j], ag, n);
             scaled(u, r[2 + j], au, n);
-            if (p.gate8.codes && row < p.M) {
-                byte_g |= save_codes(p.gate8.codes + (group0 + j) * kAct8Group, g) << (8 * j);
-                byte_u |= save_codes(p.up8.codes + (group0 + j) * kAct8Group, u) << (8 * j);
+            if (save) {
+                uint32_t w[8];
+                byte_g |= encode_group(g, w) << (8 * j);
+                store32(p.gate8.codes + (group0 + j) * kAct8Group, p.sectors, w);
+                byte_u |= encode_group(u, w) << (8 * j);
+                store32(p.up8.codes + (group0 + j) * kAct8Group, p.sectors, w);
             }
             uint32_t pk[16];
             if (p.act == MX_ACT_SILU)
@@ -147,55 +187,45 @@ struct GatedEpilogue {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     top.word(pk[i]);
-            // 64 bytes of a row through the staging box: lane l writes row l, then reads and
-            // stores 16 bytes of row 8 i + l / 4
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                *reinterpret_cast<uint4*>(stg + lane * kStgPitch + w * 16) =
-                    make_uint4(pk[4 * w], pk[4 * w + 1], pk[4 * w + 2], pk[4 * w + 3]);
-            __syncwarp();
-            const int piece = lane & 3, c = col0 + piece * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rr = 8 * i + (lane >> 2);
-                const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * kStgPitch + piece * 16);
-                if (row0 + rr < p.M && c < p.N) {
-                    __nv_bfloat16* dst = p.h + static_cast<int64_t>(row0 + rr) * p.ldh + c;
-                    if (c + 8 <= p.N) {
-                        st_global_v4(dst, v);
-                    } else {
-                        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (c + e < p.N)
-                                reinterpret_cast<uint16_t*>(dst)[e] = static_cast<uint16_t>(w4[e >> 1] >> (16 * (e & 1)));
-                    }
-                }
-            }
-            __syncwarp();
+            send(p.map_h, pk, col0, row0, lane, stg);
         }
-        if (p.gate8.codes && row < p.M) {  // the thread's two exponent bytes, at once where they are an aligned pair
-            if (p.pair_bytes) {
-                if (nt * 128 + half * 64 < p.N) {
-                    *reinterpret_cast<uint16_t*>(p.gate8.sf + group0) = static_cast<uint16_t>(byte_g);
-                    *reinterpret_cast<uint16_t*>(p.up8.sf + group0) = static_cast<uint16_t>(byte_u);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (nt * 128 + half * 64 + j * 32 < p.N) {
-                        p.gate8.sf[group0 + j] = static_cast<uint8_t>(byte_g >> (8 * j));
-                        p.up8.sf[group0 + j] = static_cast<uint8_t>(byte_u >> (8 * j));
-                    }
-            }
+        if (!save)
+            return;
+        if (p.pair_bytes) {  // the thread's two exponent bytes at once
+            *reinterpret_cast<uint16_t*>(p.gate8.sf + group0) = static_cast<uint16_t>(byte_g);
+            *reinterpret_cast<uint16_t*>(p.up8.sf + group0) = static_cast<uint16_t>(byte_u);
+            return;
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (col + j * 32 < p.N) {
+                p.gate8.sf[group0 + j] = static_cast<uint8_t>(byte_g >> (8 * j));
+                p.up8.sf[group0 + j] = static_cast<uint8_t>(byte_u >> (8 * j));
+            }
     }
     __device__ __forceinline__ void finish(const GatedParams& p)
     {
+        if (busy && (threadIdx.x & 31) == 0)
+            bulk_wait_all();
+        __syncwarp();
         if (p.amax_out)
             flush_top(p.amax_out, top);
     }
 };
+
+// 2-D map over h (row stride ld) for stores of 32 x 32 boxes with the 64-byte swizzle.
+bool make_h_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {32u, 32u};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int KIND, int STAGES, int BKB, int SFS>
 int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
@@ -213,12 +243,12 @@ int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
         !make_code_map(&maps.b[1], a.up->codes, N, kbytes, 128) || !make_sf_map(&maps.sfb[1], a.up->sf, sfb, G::NCHUNK))
         return MX_ERR_CUDA;
     GatedParams p;
+    if (!make_h_map(&p.map_h, a.h, M, N, a.ldh))
+        return MX_ERR_CUDA;
     const bool ts = fmt_has_tensor_scale(a.x->fmt);
     p.tsa = ts ? a.x->tensor_scale : nullptr;
     p.tsg = ts ? a.gate->tensor_scale : nullptr;
     p.tsu = ts ? a.up->tensor_scale : nullptr;
-    p.h = static_cast<__nv_bfloat16*>(a.h);
-    p.ldh = a.ldh;
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
     p.K = static_cast<int>(K);
@@ -228,6 +258,7 @@ int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
     p.up8 = a.up8;
     p.groups = act8_groups(N);
     p.pair_bytes = N % 64 == 0 && reinterpret_cast<uintptr_t>(a.gate8.sf) % 2 == 0 && reinterpret_cast<uintptr_t>(a.up8.sf) % 2 == 0;
+    p.sectors = reinterpret_cast<uintptr_t>(a.gate8.codes) % 32 == 0 && reinterpret_cast<uintptr_t>(a.up8.codes) % 32 == 0;
     p.kgroups = sf_kgroups(K / G::BLOCK);
     p.m_tiles = static_cast<int>((M + 255) / 256);
     p.n_tiles = static_cast<int>((N + 127) / 128);

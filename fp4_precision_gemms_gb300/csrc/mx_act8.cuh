@@ -481,6 +481,14 @@ __device__ __forceinline__ void store_ragged(float* p, Oct o, int n, bool prev, 
     }
 }
 
+// 32 bytes at a multiple of 32: a whole sector in one access.
+__device__ __forceinline__ void store_sector(uint8_t* to, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ bool non_finite(float v) { return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u; }
 
 // The checkpoint of a group that four consecutive lanes hold, eight columns

@@ -211,7 +211,7 @@ struct CfgWs {
 
 template <class G, class Epi>
 __global__ void __launch_bounds__(512, 1)
-    bs_gemm_ws_kernel(const __grid_constant__ WsMaps<Epi::kHalves> maps, const typename Epi::Params p)
+    bs_gemm_ws_kernel(const __grid_constant__ WsMaps<Epi::kHalves> maps, const __grid_constant__ typename Epi::Params p)
 {
     constexpr int KIND = G::KIND, STAGES = G::STAGES;
     constexpr int kHalves = Epi::kHalves;  // 2: the tile's two halves of 128 columns come from two operands
