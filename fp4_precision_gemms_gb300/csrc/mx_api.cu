@@ -996,6 +996,8 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
         for (const mx_tensor* t : {gate, up})
             if (rc == MX_OK && (rc = check_operand(t)) == MX_OK && (t->fmt != fmt || t->k != Kin || t->rows != F))
                 rc = MX_ERR_INVALID_ARG;
+            else if (rc == MX_OK && t->hadamard)
+                rc = MX_ERR_UNSUPPORTED;
     Device d;
     if (rc != MX_OK || (rc = current_device(&d)) != MX_OK)
         return rc;

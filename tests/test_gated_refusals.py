@@ -45,7 +45,7 @@ def test_fwd_refuses(L, want, kw):
 
 
 @pytest.mark.parametrize("want,bad", [(BAD, dict(rows=63)), (BAD, dict(k=512)), (BAD, dict(fmt=3)), (BAD, dict(codes=None)),
-                                      (ALIGN, dict(codes=P + 8)), (BAD, dict(block=16))])
+                                      (ALIGN, dict(codes=P + 8)), (BAD, dict(block=16)), (UNSUP, dict(had=1))])
 def test_fwd_refuses_operands(L, want, bad):
     assert fwd(L, W=None, gate=operand(**bad), up=operand()) == want
     assert fwd(L, W=None, gate=operand(), up=operand(**bad)) == want
