@@ -269,7 +269,28 @@ int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
     return ws_launch<G, GatedEpilogue>(maps, p, clusters, s);
 }
 
+__global__ void __launch_bounds__(256) move_scales_kernel(const uint8_t* __restrict__ sf, int64_t from, int64_t rows,
+                                                         int64_t kgroups, uint8_t* __restrict__ to)
+{
+    const int64_t words = (rows + 127) / 128 * 128 * kgroups, stride = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words; i += stride) {
+        // 128 words of a chunk at a time: word i % 128 of its chunk in the order of the layout
+        const int64_t chunk = i >> 7, tile = chunk / kgroups, kg = chunk - tile * kgroups;
+        const int64_t r = tile * 128 + (i & 3) * 32 + ((i & 127) >> 2);
+        if (r < rows)
+            *reinterpret_cast<uint32_t*>(to + sf_offset(r, kg * 4, kgroups)) =
+                *reinterpret_cast<const uint32_t*>(sf + sf_offset(from + r, kg * 4, kgroups));
+    }
+}
+
 }  // namespace
+
+int launch_move_scales(const uint8_t* sf, int64_t from, int64_t rows, int64_t kgroups, uint8_t* to, cudaStream_t s)
+{
+    const int64_t padded = (rows + 127) / 128 * 128;  // whole chunks
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>((padded * kgroups + 255) / 256, 152 * 8));
+    return launch_kernel(move_scales_kernel, ctas, 1, 256, 0, false, s, sf, from, rows, kgroups, to);
+}
 
 int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s)
 {

@@ -10,7 +10,8 @@
 // directions.  First each thread computes eights of a row, encodes them (four lanes share
 // a block's maximum) and leaves the bf16 values in shared memory; then each thread
 // encodes two columns of 32 tokens.  Chunks of scale bytes are gathered in shared memory
-// and written whole.  Bytes: 2 + 2.06 a value of dH read, 4.12 written (FP8); the
+// and written whole.  Where F is an odd multiple of 64, up's columns of D start in the
+// middle of a chunk: tiles of 64 features then, whose scale bytes go out one by one.  Bytes: 2 + 2.06 a value of dH read, 4.12 written (FP8); the
 // two passes that this replaces move D's 4 bytes out and in again as well (149 + 166 us).
 // Bound by issue and latency together: 48 instructions a value of dH, 55 % of the issue
 // slots, two CTAs an SM whose loading and encoding phases overlap only with each other's.
@@ -24,11 +25,16 @@
 namespace mx {
 namespace {
 
-constexpr int kTile = 128;     // tokens and features
-constexpr int kThreads = 512;
-constexpr int kPitch = kTile * 2 + 16;  // bytes of a staged row
-constexpr int kStage = kTile * kPitch;  // of one operand
-constexpr int kSmem = 2 * kStage + 4 * 512;
+constexpr int kTokens = 128;  // of a tile
+template <int FEATURES>
+struct Shape {
+    static constexpr int threads = 4 * FEATURES, ctas = 1024 / threads;
+    static constexpr int pitch = FEATURES * 2 + 16;    // bytes of a staged row
+    static constexpr int stage = kTokens * pitch;      // of one operand
+    static constexpr int smem = 2 * stage + 4 * 512;
+    static constexpr int octs = FEATURES / 8;          // of a row
+    static constexpr int rows = threads / octs;        // that the threads take at once
+};
 // Eights of a thread whose loads are in flight together: all four of a tile.  8192 x 14336
 // SiLU: 234 us (960 MB, 4.1 TB/s); two at a time 248, three CTAs of 256 threads 246.
 constexpr int kFlight = 4;
@@ -77,8 +83,8 @@ __device__ __forceinline__ uint32_t encode_row(uint4 w, uint2& codes)
 
 // 32 tokens of two neighbouring columns.
 template <int ELEM>
-__device__ __forceinline__ void encode_columns(const uint32_t (&w)[32], uint8_t* to_a, uint8_t* to_b, uint8_t* byte_a,
-                                               uint8_t* byte_b)
+__device__ __forceinline__ void encode_columns(const uint32_t (&w)[32], uint8_t* to_a, uint8_t* to_b, uint8_t& byte_a,
+                                               uint8_t& byte_b)
 {
     uint32_t m[8];
 #pragma unroll
@@ -93,8 +99,8 @@ __device__ __forceinline__ void encode_columns(const uint32_t (&w)[32], uint8_t*
     const int ea = pow2_exponent<ELEM>(__uint_as_float(m[0] << 16), MX_SCALE_FLOOR);
     const int eb = pow2_exponent<ELEM>(__uint_as_float(m[0] & 0xFFFF0000u), MX_SCALE_FLOOR);
     const float2 s = make_float2(exp2_neg(ea), exp2_neg(eb));
-    *byte_a = static_cast<uint8_t>(ea + 127);
-    *byte_b = static_cast<uint8_t>(eb + 127);
+    byte_a = static_cast<uint8_t>(ea + 127);
+    byte_b = static_cast<uint8_t>(eb + 127);
     if constexpr (ELEM == kElemE4M3) {
         uint32_t a[8], b[8];
 #pragma unroll
@@ -124,28 +130,32 @@ __device__ __forceinline__ void encode_columns(const uint32_t (&w)[32], uint8_t*
     }
 }
 
-template <int ACT, int ELEM>
-__global__ void __launch_bounds__(kThreads, 2) gated_bwd_quantize_kernel(const BwdQuantParams p)
+template <int ACT, int ELEM, int FEATURES>
+__global__ void __launch_bounds__(Shape<FEATURES>::threads, Shape<FEATURES>::ctas) gated_bwd_quantize_kernel(const BwdQuantParams p)
 {
+    using S = Shape<FEATURES>;
     constexpr int EPB = ELEM == kElemE4M3 ? 1 : 2;  // values a byte
+    constexpr bool CHUNKS = FEATURES == 128;        // a tile's scale bytes are whole chunks
+    constexpr int kStage = S::stage, kPitch = S::pitch;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* chunks = smem + 2 * kStage;  // rowwise gate, up; columnwise gate, up
-    const int f_tiles = static_cast<int>(p.F / kTile);
+    const int f_tiles = static_cast<int>(p.F / FEATURES);
     const int tt = blockIdx.x / f_tiles, ft = blockIdx.x - tt * f_tiles;
-    const int64_t t0 = static_cast<int64_t>(tt) * kTile, f0 = static_cast<int64_t>(ft) * kTile;
+    const int64_t t0 = static_cast<int64_t>(tt) * kTokens, f0 = static_cast<int64_t>(ft) * FEATURES;
+    const int64_t row_kgroups = p.F / 64, col_kgroups = p.T / 128;  // 2F / 32 / 4, T / 32 / 4
     const int64_t groups = p.F / kAct8Group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // rows: a warp takes two at a time, sixteen lanes each
-    const int oct = lane & 15;
+    // rows: a warp takes two or four at a time
+    const int oct = threadIdx.x % S::octs, row = threadIdx.x / S::octs;
 #pragma unroll 1
-    for (int it = 0; it < 2048 / kThreads; it += kFlight) {
+    for (int it = 0; it < kTokens / S::rows; it += kFlight) {
         RawOct<__nv_bfloat16> dh[kFlight];
         uint2 cg[kFlight], cu[kFlight];
         uint32_t bg[kFlight], bu[kFlight];
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-            const int64_t t = t0 + (it + k) * (kThreads / 16) + warp * 2 + (lane >> 4);
+            const int64_t t = t0 + (it + k) * S::rows + row;
             dh[k].load(p.dh + t * p.ldh + f0 + oct * 8);
             const int64_t at = t * p.F + f0 + oct * 8;  // F is a multiple of 32: the checkpoints' rows have no pads
             cg[k] = __ldcs(reinterpret_cast<const uint2*>(p.g8.codes + at));
@@ -156,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_quantize_kernel(const B
         }
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-            const int r = (it + k) * (kThreads / 16) + warp * 2 + (lane >> 4);
+            const int r = (it + k) * S::rows + row;
             Oct d, g, u, dg, du;
             dh[k].get(d);
             decode_oct(cg[k], g);
@@ -184,46 +194,66 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_quantize_kernel(const B
                 *reinterpret_cast<uint32_t*>(to + p.F / 2) = u_codes.x;
             }
             if ((lane & 3) == 0) {
-                chunks[chunk_at(r, oct >> 2)] = static_cast<uint8_t>(g_byte);
-                chunks[512 + chunk_at(r, oct >> 2)] = static_cast<uint8_t>(u_byte);
+                if constexpr (CHUNKS) {
+                    chunks[chunk_at(r, oct >> 2)] = static_cast<uint8_t>(g_byte);
+                    chunks[512 + chunk_at(r, oct >> 2)] = static_cast<uint8_t>(u_byte);
+                } else {
+                    const int64_t kb = (f0 >> 5) + (oct >> 2);
+                    p.row_sf[sf_offset(t0 + r, kb, row_kgroups)] = static_cast<uint8_t>(g_byte);
+                    p.row_sf[sf_offset(t0 + r, kb + (p.F >> 5), row_kgroups)] = static_cast<uint8_t>(u_byte);
+                }
             }
         }
     }
     __syncthreads();
-    // columns: sixteen tasks of a warp, each 64 features (two a lane) of an operand and 32 tokens
-#pragma unroll 1
-    for (int k = warp; k < 16; k += kThreads / 32) {
-        const int operand = k >> 3, pair = (k & 1) * 32 + lane, block = (k >> 1) & 3;
-        uint32_t w[32];
+    // columns: a thread takes two neighbouring features of an operand and 32 tokens, a warp 64
+    // features
+    constexpr int kWarpsOfOperand = S::threads / 64;
+    const int operand = warp / kWarpsOfOperand, pair = (warp % (FEATURES / 64)) * 32 + lane;
+    const int block = (warp % kWarpsOfOperand) / (FEATURES / 64);
+    uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            w[i] = *reinterpret_cast<const uint32_t*>(smem + operand * kStage + (block * 32 + i) * kPitch + pair * 4);
-        const int64_t f = operand * p.F + f0 + 2 * pair;
-        uint8_t* to = p.col_codes + (f * p.T + t0 + block * 32) / EPB;
+    for (int i = 0; i < 32; ++i)
+        w[i] = *reinterpret_cast<const uint32_t*>(smem + operand * kStage + (block * 32 + i) * kPitch + pair * 4);
+    const int64_t f = operand * p.F + f0 + 2 * pair;
+    uint8_t* to = p.col_codes + (f * p.T + t0 + block * 32) / EPB;
+    uint8_t byte_a, byte_b;
+    encode_columns<ELEM>(w, to, to + p.T / EPB, byte_a, byte_b);
+    if constexpr (!CHUNKS) {
+        p.col_sf[sf_offset(f, (t0 >> 5) + block, col_kgroups)] = byte_a;
+        p.col_sf[sf_offset(f + 1, (t0 >> 5) + block, col_kgroups)] = byte_b;
+    } else {
         uint8_t* bytes = chunks + (2 + operand) * 512;
-        encode_columns<ELEM>(w, to, to + p.T / EPB, bytes + chunk_at(2 * pair, block), bytes + chunk_at(2 * pair + 1, block));
-    }
-    __syncthreads();
-    if (threadIdx.x < 128) {  // four chunks of 32 x 16 bytes
-        const int c = threadIdx.x >> 5;
-        const int64_t f_chunks = p.F / kTile, t_chunks = p.T / kTile;
-        uint8_t* to = c < 2 ? p.row_sf + (tt * 2 * f_chunks + c * f_chunks + ft) * 512
-                            : p.col_sf + (((c - 2) * f_chunks + ft) * t_chunks + tt) * 512;
-        reinterpret_cast<uint4*>(to)[lane] = reinterpret_cast<const uint4*>(chunks + c * 512)[lane];
+        bytes[chunk_at(2 * pair, block)] = byte_a;
+        bytes[chunk_at(2 * pair + 1, block)] = byte_b;
+        __syncthreads();
+        if (threadIdx.x < 128) {  // four chunks of 32 x 16 bytes
+            const int c = threadIdx.x >> 5;
+            const int64_t f_chunks = p.F / 128;
+            uint8_t* out = c < 2 ? p.row_sf + (tt * row_kgroups + c * f_chunks + ft) * 512
+                                 : p.col_sf + (((c - 2) * f_chunks + ft) * col_kgroups + tt) * 512;
+            reinterpret_cast<uint4*>(out)[lane] = reinterpret_cast<const uint4*>(chunks + c * 512)[lane];
+        }
     }
 }
 
-template <int ACT, int ELEM>
+template <int ACT, int ELEM, int FEATURES>
 int launch(const BwdQuantParams& p, const Device& d, cudaStream_t s)
 {
-    constexpr auto kernel = gated_bwd_quantize_kernel<ACT, ELEM>;
+    using S = Shape<FEATURES>;
+    constexpr auto kernel = gated_bwd_quantize_kernel<ACT, ELEM, FEATURES>;
     static int configured_device = -1;
     if (configured_device != d.id) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess)
             return MX_ERR_CUDA;
         configured_device = d.id;
     }
-    return launch_kernel(kernel, static_cast<unsigned>((p.T / kTile) * (p.F / kTile)), 1, kThreads, kSmem, false, s, p);
+    return launch_kernel(kernel, static_cast<unsigned>((p.T / kTokens) * (p.F / FEATURES)), 1, S::threads, S::smem, false, s, p);
+}
+template <int ACT, int ELEM>
+int launch(const BwdQuantParams& p, const Device& d, cudaStream_t s)
+{
+    return p.F % 128 == 0 ? launch<ACT, ELEM, 128>(p, d, s) : launch<ACT, ELEM, 64>(p, d, s);
 }
 template <int ELEM>
 int launch(int act, const BwdQuantParams& p, const Device& d, cudaStream_t s)
@@ -239,8 +269,8 @@ int launch(int act, const BwdQuantParams& p, const Device& d, cudaStream_t s)
 
 bool gated_bwd_quantize_takes(const ActArgs& a, int fmt)
 {
-    return (fmt == MX_FMT_MXFP8_E4M3 || fmt == MX_FMT_MXFP4_E2M1) && a.rows % kTile == 0 && a.cols % kTile == 0 && a.ldh % 8 == 0 &&
-           reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.rows / kTile) * (a.cols / kTile) <= INT32_MAX;
+    return (fmt == MX_FMT_MXFP8_E4M3 || fmt == MX_FMT_MXFP4_E2M1) && a.rows % kTokens == 0 && a.cols % 64 == 0 && a.ldh % 8 == 0 &&
+           reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.rows / kTokens) * (a.cols / 64) <= INT32_MAX;
 }
 
 int launch_gated_bwd_quantize(const ActArgs& a, const mx_tensor& rows, const mx_tensor& cols, int fmt, const Device& d,

@@ -850,8 +850,8 @@ int check_checkpoint(const mx_act8* a, int64_t rows, int64_t cols)
 
 Act8View checkpoint_view(const mx_act8* a) { return a ? Act8View{a->codes, a->sf} : Act8View{}; }
 
-// Rows from .. from + rows - 1 of an operand, from a multiple of 128: they start a
-// row tile of the scale layout.
+// Rows from .. from + rows - 1 of an operand; sf is theirs where from is a multiple of
+// 128, so that they start a row tile of the scale layout.
 mx_tensor operand_rows(const mx_tensor& t, int64_t from, int64_t rows)
 {
     mx_tensor v = t;
@@ -931,27 +931,61 @@ int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* 
     return launch_gated(a, d, s);
 }
 
-// The weights' two halves as operands of their own under W's tensor scale.
-int quantize_halves(const void* W, int64_t Kin, int64_t F, int fmt, const float* amax, mx_tensor* gate, mx_tensor* up,
-                    const Device& d, cudaStream_t s)
+// The quantized weights of the gated block: gate's and up's rows of one operand w [2F,
+// Kin].  Where F % 128 != 0 up's rows start within a row tile of the scale layout, and its
+// scale bytes are copied to a layout of their own (3 us); NVFP4_LOCAL, whose regions would
+// straddle the halves too, has two operands from passes of their own there.
+struct GatedWeights {
+    mx_tensor w, gate, up;
+    uint8_t* up_sf;
+    bool halves;
+};
+size_t carve_gated_weights(uint8_t* ws, int fmt, int64_t Kin, int64_t F, GatedWeights* g)
 {
-    const uint16_t* w = static_cast<const uint16_t*>(W);
-    for (int half = 0; half < 2; ++half) {
-        const int rc = quantize_impl(w + half * F * Kin, F, Kin, Kin, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE,
-                                     MX_SCALE_DEFAULT, 0, 0, 0, amax, half ? up : gate, d, s);
-        if (rc != MX_OK)
-            return rc;
+    const bool whole = F % 128 == 0, halves = !whole && fmt_is_local(fmt);
+    size_t off = halves ? carve(ws, fmt, F, Kin, g ? &g->gate : nullptr) : carve(ws, fmt, 2 * F, Kin, g ? &g->w : nullptr);
+    uint8_t* at = ws ? ws + off : nullptr;
+    if (halves)
+        off += carve(at, fmt, F, Kin, g ? &g->up : nullptr);
+    else if (!whole)
+        off += round_up(mx_sf_bytes(fmt, F, Kin), 256);
+    if (g) {
+        g->halves = halves;
+        g->up_sf = whole || halves ? nullptr : at;
     }
-    return MX_OK;
+    return off;
 }
 
-// Bytes of the quantized weights in a workspace: one operand of 2F rows, or two of F.
-size_t carve_gated_weights(uint8_t* ws, int fmt, int64_t Kin, int64_t F, mx_tensor* w, mx_tensor* gate, mx_tensor* up)
+// Quantizes W [2F, Kin] into g's buffers; with wt also W^T from the same pass.
+int quantize_gated_weights(const void* W, int64_t Kin, int64_t F, int fmt, const float* w_amax, GatedWeights* g, mx_tensor* wt,
+                           const Device& d, cudaStream_t s)
 {
-    if (F % 128 == 0)
-        return carve(ws, fmt, 2 * F, Kin, w);
-    const size_t off = carve(ws, fmt, F, Kin, gate);
-    return off + carve(ws ? ws + off : nullptr, fmt, F, Kin, up);
+    const int block = fmt_block(fmt);
+    const uint16_t* w = static_cast<const uint16_t*>(W);
+    int rc = MX_OK;
+    if (g->halves) {
+        if (wt)
+            rc = quantize_impl(W, 2 * F, Kin, Kin, MX_COLWISE, fmt, block, MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr, wt, d,
+                               s);
+        for (int half = 0; half < 2 && rc == MX_OK; ++half)
+            rc = quantize_impl(w + half * F * Kin, F, Kin, Kin, MX_ROWWISE, fmt, block, MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0,
+                               nullptr, half ? &g->up : &g->gate, d, s);
+        return rc;
+    }
+    if (wt)
+        rc = quantize_dual_impl(W, 2 * F, Kin, Kin, fmt, block, MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE, 0, w_amax,
+                                &g->w, wt, d, s);
+    else
+        rc = quantize_impl(W, 2 * F, Kin, Kin, MX_ROWWISE, fmt, block, MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, w_amax, &g->w, d,
+                           s);
+    g->gate = operand_rows(g->w, 0, F);
+    g->up = operand_rows(g->w, F, F);
+    if (g->up_sf) {
+        g->up.sf = g->up_sf;
+        if (rc == MX_OK)
+            rc = launch_move_scales(g->w.sf, F, F, sf_kgroups(Kin / block), g->up_sf, s);
+    }
+    return rc;
 }
 
 }  // namespace
@@ -971,7 +1005,7 @@ size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int 
     if (!gated_shape(T, Kin, F, fmt))
         return 0;
     if (pass == 0)
-        return carve(nullptr, fmt, T, Kin, nullptr) + carve_gated_weights(nullptr, fmt, Kin, F, nullptr, nullptr, nullptr) +
+        return carve(nullptr, fmt, T, Kin, nullptr) + carve_gated_weights(nullptr, fmt, Kin, F, nullptr) +
                gated_few_bytes(T, F);
     if (pass == 1)  // D, its maximum, and the linear layer's backward
         return round_up(static_cast<size_t>(T) * static_cast<size_t>(F) * 4, 256) + 256 +
@@ -1007,26 +1041,15 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
     if (amax_out && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess)
         return MX_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    mx_tensor xq, wq, gq, uq;
+    mx_tensor xq;
     const size_t off = carve(ws, fmt, T, Kin, &xq);
+    GatedWeights g;
     if (W) {
-        carve_gated_weights(ws + off, fmt, Kin, F, &wq, &gq, &uq);
-        if (F % 128 == 0) {
-            rc = quantize_impl(W, 2 * F, Kin, Kin, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0,
-                               nullptr, &wq, d, s);
-            gq = operand_rows(wq, 0, F);
-            uq = operand_rows(wq, F, F);
-        } else {
-            const bool one_scale = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt);
-            if (one_scale)
-                rc = launch_amax(W, 2 * F, Kin, Kin, gq.amax, d, s);
-            if (rc == MX_OK)
-                rc = quantize_halves(W, Kin, F, fmt, one_scale ? gq.amax : nullptr, &gq, &uq, d, s);
-        }
-        if (rc != MX_OK)
+        carve_gated_weights(ws + off, fmt, Kin, F, &g);
+        if ((rc = quantize_gated_weights(W, Kin, F, fmt, nullptr, &g, nullptr, d, s)) != MX_OK)
             return rc;
-        gate = &gq;
-        up = &uq;
+        gate = &g.gate;
+        up = &g.up;
     }
     // the tokens last: the weights are then complete before their quantization starts
     void* parts = nullptr;
@@ -1077,28 +1100,17 @@ int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int6
     if (T == 0 || F == 0)
         return !amax_out || cudaMemsetAsync(amax_out, 0, sizeof(float), s) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    mx_tensor xq, wq, gq, uq, xt, wt;
+    mx_tensor xq, xt, wt;
+    GatedWeights g;
     const size_t off = carve(ws, fmt, T, Kin, &xq);
-    carve_gated_weights(ws + off, fmt, Kin, F, &wq, &gq, &uq);
+    carve_gated_weights(ws + off, fmt, Kin, F, &g);
     carve_saved(static_cast<uint8_t*>(saved), T, Kin, 2 * F, fmt, o.wgrad_hadamard, &xt, &wt);
-    const int block = fmt_block(fmt);
-    rc = quantize_dual_impl(X, T, Kin, ldx, fmt, block, MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE,
+    rc = quantize_dual_impl(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE,
                             o.wgrad_hadamard, x_amax, &xq, &xt, d, s);
-    if (rc != MX_OK)
-        return rc;
-    if (F % 128 == 0) {
-        rc = quantize_dual_impl(W, 2 * F, Kin, Kin, fmt, block, MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE, 0,
-                                w_amax, &wq, &wt, d, s);
-        gq = operand_rows(wq, 0, F);
-        uq = operand_rows(wq, F, F);
-    } else {
-        rc = quantize_impl(W, 2 * F, Kin, Kin, MX_COLWISE, fmt, block, MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, w_amax, &wt,
-                           d, s);
-        const bool one_scale = fmt_has_tensor_scale(fmt) && !fmt_is_local(fmt);
-        if (rc == MX_OK)
-            rc = quantize_halves(W, Kin, F, fmt, one_scale ? wt.amax : nullptr, &gq, &uq, d, s);
-    }
-    return rc != MX_OK ? rc : gemm_gated_impl(&xq, &gq, &uq, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d, s);
+    if (rc == MX_OK)
+        rc = quantize_gated_weights(W, Kin, F, fmt, w_amax, &g, &wt, d, s);
+    return rc != MX_OK ? rc
+                       : gemm_gated_impl(&xq, &g.gate, &g.up, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d, s);
 }
 
 int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F, int fmt, int act,

@@ -215,6 +215,10 @@ bool quantize_few_takes(int64_t rows, int64_t k);
 int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s);
 int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s);
 
+// Scale words (four K-blocks) of rows from .. from + rows - 1 of one scale layout to a
+// layout of their own (gated.cu).
+int launch_move_scales(const uint8_t* sf, int64_t from, int64_t rows, int64_t kgroups, uint8_t* to, cudaStream_t s);
+
 // The gated block's backward activation with its result encoded at once (gated_bwd.cu):
 // D's rowwise operand [T, 2F] and columnwise one [2F, T] in place of a.dgate and a.dup.
 bool gated_bwd_quantize_takes(const ActArgs& a, int fmt);

@@ -484,9 +484,7 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
 /* mx_gated_fwd from W, keeping what the backward pass needs: gate8 and up8, and in
  * `saved` (mx_linear_saved_bytes(T, Kin, 2F, fmt) bytes) the operands X^T and W^T as
  * mx_linear_fwd_save keeps them.  x_amax, w_amax, opts as there.  T % 32 == 0 and
- * F % 16 == 0.  One pass over W emits both of its operands where F % 128 == 0, so
- * that the up rows start a row tile of the scale layout; else the rowwise halves
- * take passes of their own. */
+ * F % 16 == 0. */
 int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int64_t Kin, int64_t F, int fmt, int act,
                       const float* x_amax, const float* w_amax, const mx_bwd_opts* opts, void* h, int64_t ldh,
                       const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* workspace, size_t ws_bytes,

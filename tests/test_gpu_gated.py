@@ -93,7 +93,8 @@ def test_h_and_checkpoints(mx, fmt, T, K, F):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T,K,F", [(1, 512, 128), (5, 256, 56), (300, 768, 384), (161, 256, 96)])
+@pytest.mark.parametrize("T,K,F", [(1, 512, 128), (5, 256, 56), (300, 768, 384), (161, 256, 96), (96, 256, 16), (96, 512, 208),
+                                   (70, 1024, 131)])
 def test_forms_of_the_weights_agree(mx, fmt, T, K, F):
     """Quantized beforehand, within the call, or with the saved state: the same h.  (K is too short for few tokens'
     sums to be cut.)"""
@@ -207,9 +208,9 @@ def test_gradients_are_those_of_the_calls(mx, fmt, T, K, F, act):
     assert torch.equal(only, dW.to(BF)) and none is None
 
 
-@pytest.mark.parametrize("fmt,T,F", [("mxfp8", 128, 64), ("mxfp8", 384, 192), ("moss", 128, 320), ("mxfp8", 128, 3392)])
-def test_gradients_where_the_halves_take_passes_of_their_own(mx, fmt, T, F):
-    K = 256
+@pytest.mark.parametrize("fmt,T,F,K", [("mxfp8", 128, 64, 256), ("mxfp8", 384, 192, 128), ("moss", 128, 320, 256),
+                                       ("mxfp8", 128, 3392, 640), ("nvfp4_local", 256, 128, 256)])
+def test_gradients_where_up_starts_within_a_scale_chunk(mx, fmt, T, F, K):
     X, W = data(T, K, F, 3)
     dH = (torch.randn(T, F, device="cuda") * 1e-2).to(BF)
     kept = mx.gated_fwd_save(X, W, fmt)
