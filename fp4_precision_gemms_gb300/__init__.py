@@ -927,7 +927,11 @@ def _gate_up(W, cols, dev):
 def _operand(q, fmt, cols, dev, what):
     if not isinstance(q, MXTensor) or q.fmt != fmt or q.k != cols or q.codes.device != dev:
         raise MXError(MX_ERR_INVALID_ARG, f"{what} must be an MXTensor of {fmt} with k = {cols} on {dev}")
-    return q._c()
+    if not (q.sf.is_cuda and q.scalars.is_cuda):
+        _on_gpu(q.sf, q.scalars)
+    top = q.scalars.data_ptr()
+    return _CTensor(q.codes.data_ptr(), q.sf.data_ptr(), top, top + 4 * q.nscale, q.rows, cols, FORMATS[fmt], q.block,
+                    int(q.hadamard), 0)
 
 
 def gated_weights(W: torch.Tensor, fmt: str, stream=None):

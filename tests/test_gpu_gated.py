@@ -336,6 +336,26 @@ def test_captured_and_on_other_streams(mx, fmt):
             assert all(torch.equal(a, b) for a, b in zip(out, (kept.h, dX, dW)))
 
 
+@pytest.mark.parametrize("T,K,F", [(1, 4096, 256), (48, 2048, 640), (200, 512, 256)])
+def test_calls_at_once_and_one_behind_another(mx, T, K, F):
+    """Two streams with workspaces of their own, each with many calls behind one another in the same workspace."""
+    W = mx.gated_weights(data(T, K, F, 30)[1], "nvfp4")
+    X = [data(T, K, F, 31 + i)[0] for i in range(4)]
+    want = [mx.gated_fwd(x, W, "nvfp4") for x in X]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    n = mx.gated_workspace_bytes(T, K, F, "nvfp4", "fwd_quantized")
+    spaces = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        for k, s in enumerate(streams):
+            j = (i + k) % 4
+            got.append((j, mx.gated_fwd(X[j], W, "nvfp4", workspace=spaces[k], stream=s)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(h, want[j]) for j, h in got)
+
+
 def test_past_2g_values(mx):
     """h and the checkpoints of more than 2^31 values: the last rows are what the same call makes of them alone."""
     K, F, tail = 128, 14336, 64

@@ -352,6 +352,31 @@ def test_other_stream_and_order(mx):
     assert torch.equal(p[0], q[0])
 
 
+def test_two_optimizers_at_once(mx):
+    """Steps of two optimizers with 8-bit moments on two streams, against the same steps one after another."""
+    sizes = [40000 + 37 * i for i in range(20)]
+
+    def make(seed):
+        return mx.AdamW([values(seed + i, n).cuda() for i, n in enumerate(sizes)], state="8bit", rounding="sr", seed=seed)
+
+    grads = [values(500 + i, n).cuda() for i, n in enumerate(sizes)]
+    a, b, c, d = make(1), make(2), make(1), make(2)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        na = mx.grad_norm(grads, max_norm=1.0, stream=s)
+        a.step(grads, grad_scale=na[1:], stream=s)
+        nb = mx.grad_norm(grads, max_norm=2.0, stream=t)
+        b.step(grads, grad_scale=nb[1:], stream=t)
+        torch.cuda.synchronize()  # na and nb are read on their streams until here
+    for _ in range(5):
+        c.step(grads, grad_scale=mx.grad_norm(grads, max_norm=1.0)[1:])
+        d.step(grads, grad_scale=mx.grad_norm(grads, max_norm=2.0)[1:])
+    for x, y in ((a, c), (b, d)):
+        assert all(torch.equal(p, q) for p, q in zip(x.params, y.params))
+        assert torch.equal(x.v_all.codes, y.v_all.codes) and torch.equal(x.m_all.sf, y.m_all.sf)
+
+
 def test_past_2g_values(mx):
     """The last values of a tensor of more than 2^31 are what the same step makes of them alone."""
     n, tail = (1 << 31) + 64 * 1024 + 8, 1024 + 8
