@@ -17,49 +17,82 @@ constexpr int kThreads = 256;
 // one sector each (a quarter of a sector at a time: 602 us in place of 545 for a layer).
 __host__ __device__ constexpr int octs_of(int bits) { return bits == 8 ? 4 : 1; }
 
-// Eight values of a flat tensor.  ANY as in mx_units.cuh, but fp32 tensors that are not
-// ANY start on 32-byte boundaries: eight fp32 values are one access.  (In two of 16
-// bytes each, a warp's access touches every sector of its kilobyte twice.)
+// Eight fp32 values at a multiple of 32 bytes in one access.  (In two of 16 bytes each, a
+// warp's access touches every sector of its kilobyte twice.)
+__device__ __forceinline__ void load_sector(const float* p, RawOct<float>& w)
+{
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(w.a.x), "=f"(w.a.y), "=f"(w.a.z), "=f"(w.a.w), "=f"(w.b.x), "=f"(w.b.y), "=f"(w.b.z), "=f"(w.b.w)
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store_sector(float* p, const Oct& o)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(o.p[0].x), "f"(o.p[0].y), "f"(o.p[1].x),
+                 "f"(o.p[1].y), "f"(o.p[2].x), "f"(o.p[2].y), "f"(o.p[3].x), "f"(o.p[3].y)
+                 : "memory");
+}
+
+// Eight values of a flat tensor.  Not ANY: the tensor starts on a boundary of eight values
+// and holds a multiple of eight.  ANY: it need not; which of its arrays do is looked at
+// for each, since most start where an allocation does and only their sizes are odd.
 template <typename T, bool ANY>
 struct Values {
-    Unit<T, ANY> w;
-    __device__ __forceinline__ void load(const void* base, const Place& at, int64_t n) { w.load(base, 0, at, 1, n); }
-    __device__ __forceinline__ void get(Oct& o, int n) const { w.get(o, n); }
+    Unit<T, true> u;
+
+    static __device__ __forceinline__ bool on_boundary(const void* base)
+    {
+        return (reinterpret_cast<uintptr_t>(base) & (8 * sizeof(T) - 1)) == 0;
+    }
+    __device__ __forceinline__ void load(const void* base, const Place& at, int64_t n)
+    {
+        const T* src = static_cast<const T*>(base) + static_cast<int64_t>(at.unit) * 8;
+        if (ANY && !on_boundary(base)) {
+            u.load(base, 0, at, 1, n);
+            return;
+        }
+        u.s = 0;
+        u.w.clear();
+        if (at.cols == 8) {
+            if constexpr (sizeof(T) == 4)
+                load_sector(src, u.w);
+            else
+                u.w.load(src);
+        } else if (ANY && at.cols > 0) {
+            T v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[c] = c < at.cols ? src[c] : T(0.0f);
+            memcpy(&u.w, v, sizeof v);
+        }
+    }
+    __device__ __forceinline__ void get(Oct& o, int n) const
+    {
+        if (ANY && u.s != 0)
+            u.get(o, n);
+        else
+            u.w.get(o);
+    }
+    // Executed by whole warps.
     static __device__ __forceinline__ void store(void* base, const Place& at, const Oct& o, int64_t n)
     {
-        Top<T> unused;
-        store_unit<T, ANY>(base, 0, at, o, n, unused);
-    }
-};
-template <>
-struct Values<float, false> {
-    float v[8];
-    __device__ __forceinline__ void load(const void* base, const Place& at, int64_t)
-    {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = 0.0f;
-        if (at.cols > 0)
-            asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                         : "l"(static_cast<const float*>(base) + static_cast<int64_t>(at.unit) * 8)
-                         : "memory");
-    }
-    __device__ __forceinline__ void get(Oct& o, int) const
-    {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o.p[k] = make_float2(v[2 * k], v[2 * k + 1]);
-    }
-    static __device__ __forceinline__ void store(void* base, const Place& at, const Oct& o, int64_t)
-    {
-        if (at.cols <= 0)
+        if (ANY && !on_boundary(base)) {
+            Top<T> unused;
+            store_unit<T, true>(base, 0, at, o, n, unused);
             return;
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                         static_cast<float*>(base) + static_cast<int64_t>(at.unit) * 8),
-                     "f"(o.p[0].x), "f"(o.p[0].y), "f"(o.p[1].x), "f"(o.p[1].y), "f"(o.p[2].x), "f"(o.p[2].y),
-                     "f"(o.p[3].x), "f"(o.p[3].y)
-                     : "memory");
+        }
+        T* dst = static_cast<T*>(base) + static_cast<int64_t>(at.unit) * 8;
+        if (at.cols == 8) {
+            if constexpr (sizeof(T) == 4)
+                store_sector(dst, o);
+            else
+                *reinterpret_cast<uint4*>(dst) = pack_oct(o);
+        } else if (ANY) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < at.cols)
+                    store_f(dst + c, o[c]);
+        }
     }
 };
 __device__ __forceinline__ void fold(Top<float>& top, const Oct& o)
@@ -105,7 +138,8 @@ struct AdamwTable {
     const int64_t* t_at;
     const float* scale;
     unsigned* amax;
-    uint32_t t, k0, k1;
+    uint32_t t;
+    uint32_t keys[20];  // Philox's two, round by round: operands from the constant bank
 };
 
 // The entry that holds tile i.
@@ -140,20 +174,17 @@ __device__ __forceinline__ float sqrt_approx(float x)
 // the number of value 2 k in its low half and that of value 2 k + 1 in its high one.
 __device__ __forceinline__ void random8(const AdamwTable& a, uint32_t t, uint32_t unit, uint32_t word, uint32_t (&u)[4])
 {
-    uint32_t c0 = unit, c1 = 0, c2 = t, c3 = word, k0 = a.k0, k1 = a.k1;
+    uint32_t c0 = unit, c1 = 0, c2 = t, c3 = word;
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
         const uint64_t x = uint64_t{0xD2511F53u} * c0, y = uint64_t{0xCD9E8D57u} * c2;
-        c0 = static_cast<uint32_t>(y >> 32) ^ c1 ^ k0;
-        c2 = static_cast<uint32_t>(x >> 32) ^ c3 ^ k1;
+        c0 = static_cast<uint32_t>(y >> 32) ^ c1 ^ a.keys[2 * round];
+        c2 = static_cast<uint32_t>(x >> 32) ^ c3 ^ a.keys[2 * round + 1];
         c1 = static_cast<uint32_t>(y);
         c3 = static_cast<uint32_t>(x);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     u[0] = c0, u[1] = c1, u[2] = c2, u[3] = c3;
 }
-__device__ __forceinline__ uint32_t half_of(const uint32_t (&u)[4], int i) { return i & 1 ? u[i >> 1] >> 16 : u[i >> 1] & 0xFFFFu; }
 
 // The E4M3 codes of four values |y| <= 448, each up iff u16 < p 2^16; u as random8 gives
 // it.  From 2^-6 on a float's upper bits are the code (less 960), and the 20 that go are
@@ -232,17 +263,20 @@ __device__ __forceinline__ uint2 encode_moment(Oct z, uint8_t& byte, const uint3
     return make_uint2(w[0], w[1]);
 }
 
-// bf16 values by 16-bit numbers: up where the number is below the 16 bits that go.
+// bf16 values by 16-bit numbers: up where the number is below the 16 bits that go, which is
+// where these and 2^16 - 1 - u16 carry.  A NaN becomes the one whose bits that go are 0.
 __device__ __forceinline__ void round_bf16_sr(Oct& p, const uint32_t (&u)[4])
 {
+    float m = max_abs(max_abs(max_abs(max_abs(0.0f, p.p[0]), p.p[1]), p.p[2]), p.p[3]);
+    if (m != m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p[i] != p[i])
+                p[i] = __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        uint32_t b = __float_as_uint(p[i]);
-        if ((b & 0x7F800000u) != 0x7F800000u)
-            b += half_of(u, i) < (b & 0xFFFFu) ? 0x10000u : 0u;
-        else if (b & 0x7FFFFFu)
-            b |= 0x400000u;  // a NaN stays one
-        p[i] = __uint_as_float(b & 0xFFFF0000u);
+        const uint32_t r = i & 1 ? ~u[i >> 1] >> 16 : ~u[i >> 1] & 0xFFFFu;
+        p[i] = __uint_as_float((__float_as_uint(p[i]) + r) & 0xFFFF0000u);
     }
 }
 
@@ -288,6 +322,11 @@ struct Loaded {
     std::conditional_t<BITS == 8, Codes, Values<float, ANY>> m, v;
 };
 
+// CTAs an SM that the registers are held to, 0: the compiler's choice.  Odd sizes, 100 tensors
+// of 300001 values, choice / three / four: fp32 180 / 178 / 195 us, bf16 stochastic 140 / 125 /
+// 133, 8-bit moments 121 / 120 / 129, stochastic 158 / 149 / 139.
+constexpr int least_ctas(int bits, bool sr, bool any) { return !any ? 0 : bits == 8 && sr ? 4 : 3; }
+
 // m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2, and the weight's step, which divides
 // by approximation (2^-21 of the step; a divisor below 2^-126 counts as that).
 // Of 8-bit moments the second one's root is kept: it spans half the octaves, and
@@ -298,7 +337,7 @@ struct Loaded {
 // 564 us (3.52 GB, 6.2 TB/s).  Stochastic rounding at odd addresses by instructions: 7.7e6
 // bf16 values 45 us, three sets of random numbers and the shifts.
 template <typename P, typename G, int BITS, bool SR, bool ANY>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwTable a)
+__global__ void __launch_bounds__(kThreads, least_ctas(BITS, SR, ANY)) adamw_kernel(const __grid_constant__ AdamwTable a)
 {
     constexpr int kOcts = octs_of(BITS);
     // octs whose loads are in flight together (a layer with 8-bit moments: one 573 us, two
@@ -509,8 +548,10 @@ int launch_adamw(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_o
     t.scale = scale;
     t.amax = reinterpret_cast<unsigned*>(amax);
     t.t = static_cast<uint32_t>(o.t);
-    t.k0 = static_cast<uint32_t>(o.seed);
-    t.k1 = static_cast<uint32_t>(o.seed >> 32);
+    for (uint32_t i = 0; i < 10; ++i) {
+        t.keys[2 * i] = static_cast<uint32_t>(o.seed) + i * 0x9E3779B9u;
+        t.keys[2 * i + 1] = static_cast<uint32_t>(o.seed >> 32) + i * 0xBB67AE85u;
+    }
     // one launch for each kind of tensor (types, 8-bit moments, alignment) and 128 of them
     auto kind_of = [](const mx_adamw_tensor& x) {
         const bool p16 = x.p_dtype == MX_OUT_BF16, g16 = x.g_dtype == MX_OUT_BF16, eight = x.bits == 8;
@@ -603,41 +644,29 @@ __device__ __forceinline__ double block_sum(double v)
     return v;
 }
 
-template <typename G>
+template <typename G, bool ANY>
 __device__ __forceinline__ float squares(const NormEntry& e, uint32_t tile)
 {
-    const bool any = e.n % 8 != 0 || reinterpret_cast<uintptr_t>(e.g) % (8 * sizeof(G)) != 0;
+    constexpr int kFlight = ANY && sizeof(G) == 4 ? 1 : kNormUnits;  // loads in flight, by registers
     const int64_t first = static_cast<int64_t>(tile - e.first) * (kThreads * kNormUnits) + threadIdx.x;
     float2 sum = both(0.0f);
-    auto add = [&](const Oct& o) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            sum = __ffma2_rn(o.p[j], o.p[j], sum);
-    };
-    auto place = [&](int k) {
-        const int64_t unit = first + k * kThreads;
-        return Place{0, static_cast<uint32_t>(unit), static_cast<int32_t>(max(min(e.n - unit * 8, int64_t{8}), int64_t{0}))};
-    };
-    if (!any) {
-        Values<G, false> w[kNormUnits];
-#pragma unroll
-        for (int k = 0; k < kNormUnits; ++k)
-            w[k].load(e.g, place(k), e.n);
-#pragma unroll
-        for (int k = 0; k < kNormUnits; ++k) {
-            Oct o;
-            w[k].get(o, 8);
-            add(o);
-        }
-    } else {
 #pragma unroll 1
-        for (int k = 0; k < kNormUnits; ++k) {
-            const Place at = place(k);
-            Unit<G, true> w;
-            w.load(e.g, 0, at, 1, e.n);
+    for (int batch = 0; batch < kNormUnits; batch += kFlight) {
+        Values<G, ANY> w[kFlight];
+        Place at[kFlight];
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const int64_t unit = first + (batch + k) * kThreads;
+            at[k] = {0, static_cast<uint32_t>(unit), static_cast<int32_t>(max(min(e.n - unit * 8, int64_t{8}), int64_t{0}))};
+            w[k].load(e.g, at[k], e.n);
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
             Oct o;
-            w.get(o, at.cols);
-            add(o);
+            w[k].get(o, at[k].cols);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum = __ffma2_rn(o.p[j], o.p[j], sum);
         }
     }
     return sum.x + sum.y;
@@ -662,7 +691,9 @@ __global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_const
                 hi = mid;
         }
         const NormEntry& e = a.e[lo];
-        sum += e.bf16 ? squares<__nv_bfloat16>(e, tile) : squares<float>(e, tile);
+        const bool any = e.n % 8 != 0 || reinterpret_cast<uintptr_t>(e.g) % (e.bf16 ? 16 : 32) != 0;
+        sum += any ? (e.bf16 ? squares<__nv_bfloat16, true>(e, tile) : squares<float, true>(e, tile))
+                   : (e.bf16 ? squares<__nv_bfloat16, false>(e, tile) : squares<float, false>(e, tile));
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0)
