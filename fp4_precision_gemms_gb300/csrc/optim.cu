@@ -335,7 +335,7 @@ constexpr int least_ctas(int bits, bool sr, bool any) { return !any ? 0 : bits =
 // Bound by DRAM: a layer of 218e6 values, fp32 with bf16 copies and maxima, 990 us (6.54
 // GB, 6.6 TB/s; 1408 with fp32 accesses of 16 bytes), 8-bit moments and bf16 gradients
 // 564 us (3.52 GB, 6.2 TB/s).  Stochastic rounding at odd addresses by instructions: 7.7e6
-// bf16 values 45 us, three sets of random numbers and the shifts.
+// bf16 values 37 us, three sets of random numbers and the shifts.
 template <typename P, typename G, int BITS, bool SR, bool ANY>
 __global__ void __launch_bounds__(kThreads, least_ctas(BITS, SR, ANY)) adamw_kernel(const __grid_constant__ AdamwTable a)
 {
