@@ -30,11 +30,11 @@ __device__ __forceinline__ uint4 load_words(const void* x, int64_t ld, int64_t o
 
 __device__ __forceinline__ float top_of(const Oct& o)
 {
-    float m = 0.0f;
+    float m = fabsf(o[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 1; i < 8; ++i)
         m = fmaxf(m, fabsf(o[i]));
-    return m;
+    return m;  // NaN where all are
 }
 // The maximum over the lanes that share a block of 16 or 32 values.
 template <int BLOCK>
@@ -132,11 +132,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(1024)
         w[k] = oct < octs ? load_words(x, ld, oct, per_row) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int k = 0; k < kMaxOcts; ++k) {
-        Oct o;
-        unpack_oct(w[k], o);
-        top = max(top, __float_as_uint(top_of(o)));
-    }
+    for (int k = 0; k < kMaxOcts; ++k)  // magnitudes by their bits, in pairs; a NaN is the largest
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[k].x & 0x7FFF7FFFu, w[k].y & 0x7FFF7FFFu),
+                                     __vmaxu2(w[k].z & 0x7FFF7FFFu, w[k].w & 0x7FFF7FFFu)));
+    top = max(top << 16, top & 0xFFFF0000u);
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if ((threadIdx.x & 31) == 0)
         of_warp[threadIdx.x >> 5] = top;

@@ -138,6 +138,21 @@ def test_few_tokens(mx, fmt, T, K, F):
         assert ((whole.double() - want).abs() <= 1.01 * bound).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("special", [0.0, -0.0, float("inf"), float("-inf"), float("nan"), 3.3e38, 1e-40, 2.0 ** -126])
+def test_few_tokens_with_special_values(mx, fmt, special):
+    """The tokens' quantization within the call treats every value as the one on its own does (K is too short for the
+    sums to be cut, so that the results are the same numbers)."""
+    X, W = data(7, 256, 56, 4)
+    X[2, 5] = special
+    X[4, 32:80] = special
+    X[5] *= 2.0 ** -100
+    w = mx.gated_weights(W, fmt)
+    got, want = mx.gated_fwd(X, w, fmt), mx.gemm_gated(mx.quantize(X, fmt), *w).h
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.float(), 1234.0), torch.nan_to_num(want.float(), 1234.0))
+
+
 def test_few_tokens_of_a_wide_matrix(mx):
     """More values than the small quantization holds, rows of a wider matrix, and both captured."""
     for T, K in ((64, 8192 + 256), (64, 8192), (5, 256)):
