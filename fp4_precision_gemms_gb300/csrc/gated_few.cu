@@ -367,12 +367,15 @@ __global__ void __launch_bounds__(512, 1)
             const int f = tile * 128 + q * 32 + lane;
             const int region = p.ts_region ? tile : 0;  // of 128 weight rows
             const float ag = __fmul_rn(ta, p.tsg ? p.tsg[region] : 1.0f), au = __fmul_rn(ta, p.tsu ? p.tsu[region] : 1.0f);
-            const bool ok =
-                __all_sync(0xffffffffu, mbar_wait_bounded(accf(n & 1), static_cast<uint32_t>(n >> 1) & 1u, p.wait_ns));
-            if (!ok) {
+            // after a wait that ran out the warp waits no more, but keeps meeting the others
+            const bool ok = !*abort_flag && mbar_wait_bounded(accf(n & 1), static_cast<uint32_t>(n >> 1) & 1u, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0)
                     fail();
-                break;
+                if (!whole)
+                    for (int k = 0; k < 3; ++k)
+                        named_barrier_sync(1, 256);
+                continue;
             }
             tc_fence_after();
             const uint32_t acc = tmem + (n & 1) * 2 * G::BN + (static_cast<uint32_t>(q * 32) << 16);
@@ -405,10 +408,10 @@ __global__ void __launch_bounds__(512, 1)
             const int c0 = ranges.cta_of(at), c1 = ranges.cta_of(at + num_kt - 1);
             __threadfence();
             named_barrier_sync(1, 256);
-            if (threadIdx.x == 256)
+            if (threadIdx.x == 256 && !*abort_flag)  // a piece that some warp did not write is not counted
                 *arrived = atomicAdd(p.counters + tile, 1u);
             named_barrier_sync(1, 256);
-            const bool join = *arrived == static_cast<uint32_t>(c1 - c0);
+            const bool join = __all_sync(0xffffffffu, !*abort_flag && *arrived == static_cast<uint32_t>(c1 - c0));
             named_barrier_sync(1, 256);  // the word is read before the next piece's arrival
             if (!join)
                 continue;
