@@ -1236,9 +1236,9 @@ class AdamW:
 
     def step(self, grads, grad_scale: torch.Tensor | None = None, amax_out: torch.Tensor | None = None, lr=None,
              t: int | None = None, stream=None) -> None:
-        """One step.  grads: one for each tensor, with as many values in the same order
-        (None: the tensor stays as it is).  grad_scale: one fp32 value on the device that multiplies them; NaN
-        leaves every tensor as it is.  amax_out: fp32 [tensors], max |weight| of each
+        """One step.  grads: one for each tensor, with as many values in the same order, in
+        memory that the step does not write (None: the tensor stays as it is).  grad_scale:
+        one fp32 value on the device that multiplies them; NaN leaves every tensor as it is.  amax_out: fp32 [tensors], max |weight| of each
         copy (of the parameter without one), for its next quantization.  lr: a number,
         or one fp32 value on the device; the default is the optimizer's.  t: this
         step's number (from 1), in place of the count."""

@@ -581,7 +581,7 @@ typedef struct mx_adamw_opts {
  *   amax_out    optional device floats [count]: max |value| of each tensor's
  *               copy, or param without one, as written; the w_amax / amax_in of
  *               its next quantization.  NaN if any is NaN.
- * No two of the written tensors may overlap.  Errors: MX_ERR_INVALID_ARG for
+ * No two of the written tensors may overlap, nor a gradient one of them.  Errors: MX_ERR_INVALID_ARG for
  * null pointers, sizes, enums and numbers out of range, MX_ERR_ALIGNMENT,
  * MX_ERR_UNSUPPORTED for a copy of a bf16 param. */
 int mx_adamw_step(const mx_adamw_tensor* tensors, int64_t count, const mx_adamw_opts* opts, const float* grad_scale,

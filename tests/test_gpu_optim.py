@@ -241,6 +241,34 @@ def test_many_tensors_and_kinds(mx):
 
 
 @pytest.mark.parametrize("state", ["fp32", "8bit"])
+@pytest.mark.parametrize("pt,gt,rounding", [(F32, F32, "rne"), (F32, BF, "sr"), (BF, BF, "sr"), (BF, F32, "rne")], ids=str)
+@pytest.mark.parametrize("n", [20000, 20003])
+def test_each_array_at_its_own_address(mx, state, pt, gt, rounding, n):
+    """Parameter, gradient and copy each at its own distance from an aligned address (16 bytes past one of 32, too):
+    the values that aligned ones get."""
+    p0, g0 = values(1, n).to(pt), values(2, n, 1e-2).to(gt)
+
+    def run(sp, sg, sc):
+        (p, room), (g, _) = placed(p0, pt, sp), placed(g0, gt, sg)
+        c, croom = placed(torch.zeros(n), BF, sc) if pt is F32 else (None, None)
+        top = torch.empty(1, device="cuda")
+        opt = mx.AdamW([p], state=state, rounding=rounding, seed=3, copies=[c])
+        for _ in range(2):
+            opt.step([g], amax_out=top)
+        for r, k in ((room, sp), (croom, sc)):
+            assert r is None or ((r[:k] == 7.0).all() and (r[k + n:] == 7.0).all())
+        m, v = (opt.m[0].codes, opt.v[0].codes) if state == "8bit" else (opt.m[0], opt.v[0])
+        norm = mx.grad_norm([g, p])[:1]
+        return [x.clone() for x in (p, m, v, top, p if c is None else c)], norm
+
+    want, norm = run(0, 0, 0)
+    for shifts in ((4, 0, 0), (0, 4, 8), (2, 12, 1), (8, 1, 4), (0, 0, 3), (5, 2, 0)):
+        got, other = run(*shifts)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert abs(float(other) / float(norm) - 1) <= 19 * U  # sums of other orders: 9.5 u on either side
+
+
+@pytest.mark.parametrize("state", ["fp32", "8bit"])
 def test_no_gradient_and_nan_scale_leave_tensors(mx, state):
     p0 = [values(i, 100 + i) for i in range(3)]
     for case in ("none", "nan"):
