@@ -6,8 +6,8 @@
 // Formats with a tensor scale need the tensor's maximum before the first code: one
 // cluster of eight CTAs holds the whole tensor in registers, exchanges its maxima
 // through distributed shared memory and encodes.  The others need no exchange and
-// take plain CTAs.  48 x 4096 NVFP4: 5 us in front of the product that it overlaps, in place
-// of two launches of 8.3; bound by the eight SMs' instructions (34 a value) and the exchange.
+// take plain CTAs.  48 x 4096 NVFP4: 4 us in front of the product that it overlaps, in place
+// of two launches of 8.3; bound by the eight SMs' instructions (some 30 a value) and the exchange.
 #include <cuda_bf16.h>
 
 #include "mx_act8.cuh"
