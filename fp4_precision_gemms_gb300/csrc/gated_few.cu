@@ -18,7 +18,7 @@
 // ranges' order.  No CTA waits for another.
 //
 // 14336 x 4096 with the tokens' quantization: MXFP8, 1 token 24 us (121 MB, 5.1 TB/s),
-// NVFP4, 48 tokens 16 us with the weights partly in L2, 19.5 without.  Bound by DRAM and by
+// NVFP4, 48 tokens 15 us with the weights partly in L2, 17.7 without.  Bound by DRAM and by
 // what does not stream: launch, first and last tile, 5 us.
 //
 // Every wait is bounded, as in gemm.cu.

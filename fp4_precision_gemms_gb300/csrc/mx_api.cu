@@ -1059,7 +1059,7 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
         parts = tail;
         counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T));
         fill_meta(&xq, T, Kin, fmt, 0);
-        rc = launch_quantize_few(X, ldx, &xq, counters, static_cast<int>((F + 127) / 128), s);
+        rc = launch_quantize_few(X, ldx, &xq, counters, static_cast<int>((F + 127) / 128), d, s);
     } else {
         rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
                            &xq, d, s);

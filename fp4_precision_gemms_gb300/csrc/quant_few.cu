@@ -4,10 +4,11 @@
 // quantize.cu's producers for round to nearest and the formats' default rules.
 //
 // Formats with a tensor scale need the tensor's maximum before the first code: one
-// cluster of eight CTAs holds the whole tensor in registers, exchanges its maxima
-// through distributed shared memory and encodes.  The others need no exchange and
-// take plain CTAs.  48 x 4096 NVFP4: 4 us in front of the product that it overlaps, in place
-// of two launches of 8.3; bound by the eight SMs' instructions (some 30 a value) and the exchange.
+// cluster of sixteen CTAs holds the whole tensor in registers, exchanges its maxima
+// through distributed shared memory and encodes.  (152 SMs in ten groups or fewer: one group
+// has the sixteen.)  The others need no exchange and take plain CTAs.  48 x 4096 NVFP4: 2 us
+// in front of the product that it overlaps (eight CTAs: 4), in place of two launches of 8.3;
+// bound by the latencies of the load, the exchange and the encoding.
 #include <cuda_bf16.h>
 
 #include "mx_act8.cuh"
@@ -18,8 +19,8 @@
 namespace mx {
 namespace {
 
-constexpr int kCluster = 8;
-constexpr int kMaxOcts = 8;  // of a thread
+constexpr int kCluster = 16;
+constexpr int kMaxOcts = 4;  // of a thread
 
 // A thread's eight values, as loaded.
 __device__ __forceinline__ uint4 load_words(const void* x, int64_t ld, int64_t oct, int per_row)
@@ -111,12 +112,13 @@ __global__ void __launch_bounds__(256) quantize_few_kernel(const void* x, int64_
     encode<FMT>(o, 1.0f, in, oct, per_row, kgroups, codes, sf);
 }
 
-// Thread t of the cluster holds octs t, t + 8192, ...
+// Thread t of the cluster holds octs t, t + 16384, ...
 template <int FMT>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(1024)
     quantize_few_cluster_kernel(const void* x, int64_t ld, int per_row, int octs, int64_t kgroups, uint8_t* codes, uint8_t* sf,
                                 float* amax, float* tensor_scale, unsigned* zero, int zeros)
 {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;");
     wait_for_launch_before();
     let_next_launch_start();
     for (int i = blockIdx.x * 1024 + threadIdx.x; i < zeros; i += kCluster * 1024)
@@ -139,6 +141,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(1024)
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if ((threadIdx.x & 31) == 0)
         of_warp[threadIdx.x >> 5] = top;
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA has started: its shared memory may be written
     __syncthreads();
     if (threadIdx.x < 32) {
         top = __reduce_max_sync(0xFFFFFFFFu, of_warp[threadIdx.x]);
@@ -170,17 +173,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(1024)
 }
 
 template <int FMT>
-int launch_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s)
+int launch_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, const Device& d, cudaStream_t s)
 {
     const int per_row = static_cast<int>(out->k / 8), octs = static_cast<int>(out->rows) * per_row;
     const int64_t kgroups = sf_kgroups(out->k / fmt_block(FMT));
     uint8_t* codes = static_cast<uint8_t*>(out->codes);
-    if constexpr (fmt_has_tensor_scale(FMT))
+    if constexpr (fmt_has_tensor_scale(FMT)) {
+        static int configured_device = -1;
+        if (configured_device != d.id) {
+            if (cudaFuncSetAttribute(quantize_few_cluster_kernel<FMT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                cudaSuccess)
+                return MX_ERR_CUDA;
+            configured_device = d.id;
+        }
         return launch_kernel(quantize_few_cluster_kernel<FMT>, kCluster, 1, 1024, 0, true, s, x, ld, per_row, octs, kgroups,
                              codes, out->sf, out->amax, out->tensor_scale, zero, zeros);
-    else
+    } else {
         return launch_kernel(quantize_few_kernel<FMT>, static_cast<unsigned>((octs + 255) / 256), 1, 256, 0, true, s, x, ld,
                              per_row, octs, kgroups, codes, out->sf, zero, zeros);
+    }
 }
 
 }  // namespace
@@ -190,13 +201,13 @@ bool quantize_few_takes(int64_t rows, int64_t k)
     return rows > 0 && rows <= kGatedFewTokens && k % 32 == 0 && rows * k <= int64_t{kCluster} * 1024 * kMaxOcts * 8;
 }
 
-int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, cudaStream_t s)
+int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, const Device& d, cudaStream_t s)
 {
     switch (out->fmt) {
-    case MX_FMT_MXFP8_E4M3: return launch_few<MX_FMT_MXFP8_E4M3>(x, ld, out, zero, zeros, s);
-    case MX_FMT_MXFP4_E2M1: return launch_few<MX_FMT_MXFP4_E2M1>(x, ld, out, zero, zeros, s);
-    case MX_FMT_MOSS_FP8: return launch_few<MX_FMT_MOSS_FP8>(x, ld, out, zero, zeros, s);
-    default: return launch_few<MX_FMT_NVFP4>(x, ld, out, zero, zeros, s);  // one region at most: the local scale is the tensor's
+    case MX_FMT_MXFP8_E4M3: return launch_few<MX_FMT_MXFP8_E4M3>(x, ld, out, zero, zeros, d, s);
+    case MX_FMT_MXFP4_E2M1: return launch_few<MX_FMT_MXFP4_E2M1>(x, ld, out, zero, zeros, d, s);
+    case MX_FMT_MOSS_FP8: return launch_few<MX_FMT_MOSS_FP8>(x, ld, out, zero, zeros, d, s);
+    default: return launch_few<MX_FMT_NVFP4>(x, ld, out, zero, zeros, d, s);  // one region at most: the local scale is the tensor's
     }
 }
 
