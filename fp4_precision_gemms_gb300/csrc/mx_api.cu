@@ -1105,10 +1105,18 @@ int mx_gated_fwd_save(const void* X, int64_t ldx, const void* W, int64_t T, int6
     const size_t off = carve(ws, fmt, T, Kin, &xq);
     carve_gated_weights(ws + off, fmt, Kin, F, &g);
     carve_saved(static_cast<uint8_t*>(saved), T, Kin, 2 * F, fmt, o.wgrad_hadamard, &xt, &wt);
-    rc = quantize_dual_impl(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE,
-                            o.wgrad_hadamard, x_amax, &xq, &xt, d, s);
+    // X beside W, on the side stream: one after the other small layers leave much of the GPU
+    // idle (forward and backward of 1152 x 1280 x 3392 90 us, so 85.5; large ones the same)
+    cudaStream_t sw = fork_begin(d, s);
+    rc = quantize_gated_weights(W, Kin, F, fmt, w_amax, &g, &wt, d, s);
     if (rc == MX_OK)
-        rc = quantize_gated_weights(W, Kin, F, fmt, w_amax, &g, &wt, d, s);
+        rc = quantize_dual_impl(X, T, Kin, ldx, fmt, fmt_block(fmt), MX_SCALE_DEFAULT, 0, 0, MX_ROUND_RNE, 0, MX_ROUND_RNE,
+                                o.wgrad_hadamard, x_amax, &xq, &xt, d, sw ? sw : s);
+    if (sw) {
+        const int rj = fork_end(d, sw, s);
+        if (rc == MX_OK)
+            rc = rj;
+    }
     return rc != MX_OK ? rc
                        : gemm_gated_impl(&xq, &g.gate, &g.up, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d, s);
 }
