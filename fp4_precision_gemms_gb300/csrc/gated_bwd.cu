@@ -70,7 +70,8 @@ __device__ __forceinline__ uint32_t encode_row(uint4 w, uint2& codes)
     uint32_t m = top_bf16x2(top_bf16x2(w.x, w.y), top_bf16x2(w.z, w.w));
     m = top_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = top_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2)) & 0x7FFF7FFFu;
-    const int e = pow2_exponent<ELEM>(__uint_as_float(max(m << 16, m & 0xFFFF0000u)), MX_SCALE_FLOOR);
+    // as floats: where one half of every word is NaN, which no maximum counts, the other half's values have a scale
+    const int e = pow2_exponent<ELEM>(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)), MX_SCALE_FLOOR);
     const float2 s = both(exp2_neg(e));
     const float2 a = scaled(w.x, s), b = scaled(w.y, s), c = scaled(w.z, s), d = scaled(w.w, s);
     if constexpr (ELEM == kElemE4M3) {
