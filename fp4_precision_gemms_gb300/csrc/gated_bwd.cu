@@ -10,9 +10,10 @@
 // directions.  First each thread computes eights of a row, encodes them (four lanes share
 // a block's maximum) and leaves the bf16 values in shared memory; then each thread
 // encodes two columns of 32 tokens.  Chunks of scale bytes are gathered in shared memory
-// and written whole.  Where F is an odd multiple of 64, up's columns of D start in the
-// middle of a chunk: tiles of 64 features then, whose scale bytes go out one by one.  Bytes: 2 + 2.06 a value of dH read, 4.12 written (FP8); the
-// two passes that this replaces move D's 4 bytes out and in again as well (149 + 166 us).
+// and written whole.  Where F is an odd multiple of 64 (MXFP8 only), up's columns of D start
+// in the middle of a chunk: tiles of 64 features then, whose scale bytes go out one by one.
+// Bytes: 2 + 2.06 a value of dH read, 4.12 written (FP8); the two passes that this replaces
+// move D's 4 bytes out and in again as well (149 + 166 us).
 // Bound by issue and latency together: 48 instructions a value of dH, 55 % of the issue
 // slots (66 % at 2048 tokens), two CTAs an SM whose loading and encoding phases overlap only
 // with each other's.
@@ -255,7 +256,10 @@ int launch(const BwdQuantParams& p, const Device& d, cudaStream_t s)
 template <int ACT, int ELEM>
 int launch(const BwdQuantParams& p, const Device& d, cudaStream_t s)
 {
-    return p.F % 128 == 0 ? launch<ACT, ELEM, 128>(p, d, s) : launch<ACT, ELEM, 64>(p, d, s);
+    if constexpr (ELEM == kElemE4M3)
+        if (p.F % 128 != 0)
+            return launch<ACT, ELEM, 64>(p, d, s);
+    return launch<ACT, ELEM, 128>(p, d, s);
 }
 template <int ELEM>
 int launch(int act, const BwdQuantParams& p, const Device& d, cudaStream_t s)
@@ -271,7 +275,9 @@ int launch(int act, const BwdQuantParams& p, const Device& d, cudaStream_t s)
 
 bool gated_bwd_quantize_takes(const ActArgs& a, int fmt)
 {
-    return (fmt == MX_FMT_MXFP8_E4M3 || fmt == MX_FMT_MXFP4_E2M1) && a.rows % kTokens == 0 && a.cols % 64 == 0 && a.ldh % 8 == 0 &&
+    // FP4's data gradient multiplies along 2 F in steps of 256: whole tiles of 128 features
+    const int64_t multiple = fmt == MX_FMT_MXFP8_E4M3 ? 64 : fmt == MX_FMT_MXFP4_E2M1 ? 128 : 0;
+    return multiple != 0 && a.rows % kTokens == 0 && a.cols % multiple == 0 && a.ldh % 8 == 0 &&
            reinterpret_cast<uintptr_t>(a.h) % 16 == 0 && (a.rows / kTokens) * (a.cols / 64) <= INT32_MAX;
 }
 
