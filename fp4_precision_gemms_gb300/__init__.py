@@ -1160,7 +1160,12 @@ class AdamW:
 
     m, v: the moments, one for each tensor (float32 views, or Act8 with one row;
     v holds roots there); m_all, v_all: the memory that holds them, each tensor's
-    from the next multiple of 32 values; a saved state is copied back into it.  t: steps made (with capturable: issued).
+    from the next multiple of 32 values.  t: the number of the last step (a step
+    that a NaN grad_scale left without effect counts too).
+
+    To save an optimizer keep m_all and v_all (with 8 bits their codes and sf) and
+    t beside the params; to go on, make one over the same tensors with the same
+    state, rounding and seed, copy the moments back into m_all and v_all, and set t.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
@@ -1177,7 +1182,7 @@ class AdamW:
         self.copies = tuple(copies) if copies is not None else (None,) * n
         if len(decay) != n or len(self.copies) != n:
             raise MXError(MX_ERR_INVALID_ARG, f"weight_decay and copies have one entry for each of the {n} tensors")
-        self.t = 0
+        self._t, self._t_dev = 0, None
         dev = self.device = self.params[0].device
         self._table = (_CAdamwTensor * n)()
         self._opts = _CAdamwOpts()
@@ -1205,10 +1210,36 @@ class AdamW:
                     setattr(row, name, a.data_ptr())
                 mine.append(a)
             first += g
-        self._t_dev = torch.zeros(1, dtype=torch.int64, device=dev) if capturable else None
+        if capturable:
+            self._t_dev = torch.zeros(1, dtype=torch.int64, device=dev)
         self._sizes = [row.n for row in self._table]
         self._words = memoryview(self._table).cast("B").cast("q"), memoryview(self._table).cast("B").cast("i")
         self._check_written()
+
+    def _number_is_free(self, what):
+        """A number on the device is not read or set by the host while a graph is captured: the graph would hold it."""
+        with torch.cuda.device(self.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise MXError(MX_ERR_UNSUPPORTED, f"{what} while a graph is captured")
+
+    @property
+    def t(self) -> int:
+        """The last step's number.  With capturable it is read from the device, behind what the current stream holds,
+        and counts the replays of captured steps; setting it is ordered likewise."""
+        if self._t_dev is None:
+            return self._t
+        self._number_is_free("the number is on the device and cannot be read")
+        return int(self._t_dev)
+
+    @t.setter
+    def t(self, number):
+        number = operator.index(number)
+        if number < 0:
+            raise MXError(MX_ERR_INVALID_ARG, "steps are numbered from 1")
+        if self._t_dev is not None:
+            self._number_is_free("the number cannot be set")
+            self._t_dev.fill_(number)
+        self._t = number
 
     def _check_written(self):
         """Takes the parameters' and copies' places; no two of what a step writes may share memory."""
@@ -1241,7 +1272,8 @@ class AdamW:
         one fp32 value on the device that multiplies them; NaN leaves every tensor as it is.  amax_out: fp32 [tensors], max |weight| of each
         copy (of the parameter without one), for its next quantization.  lr: a number,
         or one fp32 value on the device; the default is the optimizer's.  t: this
-        step's number (from 1), in place of the count."""
+        step's number (from 1), in place of the count (with capturable, not while a
+        graph is captured)."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.step(grads, grad_scale, amax_out, lr, t)
@@ -1271,25 +1303,31 @@ class AdamW:
             o.lr = lr
         o.beta1, o.beta2 = self.betas
         o.eps, o.seed, o.rounding = self.eps, self.seed, self._rounding
-        count = self.t + 1 if t is None else int(t)
+        count = self._t + 1 if t is None else int(t)
         if count < 1:
             raise MXError(MX_ERR_INVALID_ARG, "steps are numbered from 1")
+        if self._t_dev is not None and t is not None:
+            self._number_is_free("a step cannot be given its number")
         scale = _vec(grad_scale, 1, dev, "grad_scale") if grad_scale is not None else None
         top = _vec(amax_out, n, dev, "amax_out") if amax_out is not None else None
         if self._t_dev is not None:
             if t is None:
                 self._t_dev.add_(1)
             else:
+                before = self._t_dev.clone()
                 self._t_dev.fill_(count)
             o.t_at = self._t_dev.data_ptr()
         o.t = count
         try:
             _run(dev, "mx_adamw_step", lib().mx_adamw_step, self._table, n, o, scale, top)
         except MXError:
-            if self._t_dev is not None and t is None:
-                self._t_dev.sub_(1)
+            if self._t_dev is not None:
+                if t is None:
+                    self._t_dev.sub_(1)
+                else:
+                    self._t_dev.copy_(before)
             raise
-        self.t = count
+        self._t = count
 
 
 def last_device_status(stream=None) -> int:

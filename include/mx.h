@@ -577,7 +577,8 @@ typedef struct mx_adamw_opts {
  * changes a root by 0.05 %, far less than a code's distance to the next, 6 to
  * 12 %: rounded to nearest, 8-bit roots only ever follow large gradients up.)
  *   grad_scale  optional device float (NULL: 1).  NaN: params, m and v stay as
- *               they are (copies and amax_out are written all the same).
+ *               they are (copies and amax_out are written all the same); t
+ *               is the caller's to count or not.
  *   amax_out    optional device floats [count]: max |value| of each tensor's
  *               copy, or param without one, as written; the w_amax / amax_in of
  *               its next quantization.  NaN if any is NaN.
