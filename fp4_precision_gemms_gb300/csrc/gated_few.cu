@@ -11,8 +11,8 @@
 // weights took 514 ns (MXFP8) and 790 (NVFP4, twelve copies).  Launched with programmatic dependent launch behind
 // the tokens' quantization, the kernel fills its ring with weights before that has finished.
 //
-// Where the tiles are fewer than the SMs that it takes to read at the memory's rate, their
-// steps along K, one tile after another, are cut into equal ranges, one an SM.  A tile
+// Where the tiles are too few, or a little more than the SMs, their steps along K, one tile
+// after another, are cut into equal ranges, one an SM (gated_few_ranges).  A tile
 // that lies in several ranges leaves partial sums in a workspace; the CTA that counts
 // itself last for the tile, after its own partial sums are visible, adds them up in the
 // ranges' order.  No CTA waits for another.
@@ -95,10 +95,6 @@ struct Ranges {
         return static_cast<int>(((step + 1) * ctas - 1) / steps);
     }
 };
-// Tiles from which each is one CTA's: at 75 bytes a ns an SM, 96 of them ask for more
-// than the memory gives.  14336 x 4096 (112 tiles), whole / cut: MXFP8 1 token 24.2 /
-// 26.8 us, NVFP4 48 tokens 21.2 / 29.2, where the join is longer; one tile of 4096: 17.7 / 9.7.
-constexpr int kFewWholeTiles = 96;
 constexpr int kJoin = 2;  // fours of tokens whose partial sums are read together
 
 // Each thread of the warp reads 16 consecutive fp32 columns of its TMEM lane.
@@ -488,17 +484,43 @@ int launch_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s)
     p.amax_out = a.amax;
     p.status = d.status;
     p.wait_ns = kWaitLimitNs;
-    const int64_t tiles = (N + 127) / 128, steps = tiles * (K / G::BK);
-    // a tile a CTA where these read at the memory's rate, or without a workspace for
-    // partial sums; else ranges of at least four steps
-    const bool cut = a.parts && tiles < kFewWholeTiles;
-    const int64_t ctas = cut ? std::max<int64_t>(1, std::min<int64_t>(std::min(d.sms, kGatedFewCtas), steps / 4)) : tiles;
+    const int64_t tiles = (N + 127) / 128;
+    const int64_t ranges = a.parts ? gated_few_ranges(M, N, K, a.x->fmt) : 0, ctas = ranges ? ranges : tiles;
     p.parts = static_cast<float4*>(a.parts);
     p.counters = a.counters;
     return launch_kernel(gated_few_kernel<KIND>, static_cast<unsigned>(ctas), 1, 512, G::SMEM_ALLOC, early, s, mx, mg, mu, p);
 }
 
 }  // namespace
+
+// Cut where that takes less time: a tile a CTA, in as many waves as it takes, against equal
+// ranges of at least four steps and the join of the tiles that lie in several.  Times by
+// rates that 456 pairs of measurements gave (MXFP8 and NVFP4, K 1024 to 8192, 8 to 320
+// tiles, 1 to 64 tokens, weights not in L2): the memory 7500 bytes a ns, an SM 80, a wave
+// after the first 5 us, a join 2 us, 0.05 a token, and 0.2 and 0.015 a token for each of a
+// tile's pieces.  What is chosen is 0.2 % slower than the better of the two on average, 6 %
+// at most; on 900 other pairs (all kinds of format, K 768 to 5120, 4 to 460 tiles) 0.5 and
+// 13 %.  K = 4096, whole / cut in us: 32 tiles MXFP8 1 token 18.9 / 14.2, 64 tokens 19.9 /
+// 26.3; 80 tiles NVFP4 48 tokens 15.8 / 19.7; 112 tiles MXFP8 1 token 23.6 / 26.5; 160
+// tiles, of which 8 would be a wave of their own, 43.3 / 33.4; 304 tiles, as ranges of two
+// whole ones, 54.5 / 51.5.
+int64_t gated_few_ranges(int64_t tokens, int64_t features, int64_t k, int fmt)
+{
+    const int64_t num_kt = k / gemm_k_multiple(fmt), tiles = (features + 127) / 128, steps = tiles * num_kt;
+    if (steps == 0)
+        return 0;
+    const int64_t ranges = std::max<int64_t>(1, std::min<int64_t>(kGatedFewCtas, steps / 4));
+    const double step_us = 256.0 * static_cast<double>(codes_row_bytes(fmt, k) + k / fmt_block(fmt)) / static_cast<double>(num_kt) / 80e3;
+    const double memory_us = static_cast<double>(steps) * step_us * (80.0 / 7500.0);
+    const int64_t waves = (tiles + kGatedFewCtas - 1) / kGatedFewCtas;
+    const double whole_us = std::max(memory_us, static_cast<double>(waves * num_kt) * step_us) + 5.0 * static_cast<double>(waves - 1);
+    double cut_us = std::max(memory_us, static_cast<double>((steps + ranges - 1) / ranges) * step_us);
+    if (steps % ranges != 0 || steps / ranges % num_kt != 0) {
+        const double t = static_cast<double>(tokens), pieces = static_cast<double>((num_kt * ranges + steps - 1) / steps);
+        cut_us += 2.0 + 0.05 * t + pieces * (0.2 + 0.015 * t);
+    }
+    return cut_us < whole_us ? ranges : 0;
+}
 
 int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s)
 {

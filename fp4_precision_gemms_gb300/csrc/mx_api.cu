@@ -64,11 +64,6 @@ inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 bool valid_fmt(int fmt) { return fmt >= MX_FMT_MXFP8_E4M3 && fmt <= MX_FMT_NVFP4_LOCAL; }
 
-int64_t codes_row_bytes(int fmt, int64_t k) { return fmt_is_fp4(fmt) ? k / 2 : k; }
-
-// K granularity the GEMM consumes per pipeline stage.
-int64_t gemm_k_multiple(int fmt) { return fmt_is_fp4(fmt) ? 256 : 128; }
-
 int check_operand(const mx_tensor* t)
 {
     if (!t || !valid_fmt(t->fmt) || t->rows < 0 || t->k < 0 || t->block != fmt_block(t->fmt))
@@ -865,12 +860,13 @@ mx_tensor operand_rows(const mx_tensor& t, int64_t from, int64_t rows)
     return v;
 }
 
-// The kernel for few tokens: its partial sums and counters, at a workspace's end.
-size_t gated_few_bytes(int64_t T, int64_t F)
+// The kernel for few tokens: its partial sums and counters, at a workspace's end, where it cuts.
+size_t gated_few_bytes(int64_t T, int64_t Kin, int64_t F, int fmt)
 {
-    return T > 0 && T <= kGatedFewTokens
-               ? static_cast<size_t>(gated_few_part_bytes(T)) + round_up(static_cast<size_t>((F + 127) / 128) * sizeof(unsigned), 256)
-               : 0;
+    const int64_t ranges = T > 0 && T <= kGatedFewTokens ? gated_few_ranges(T, F, Kin, fmt) : 0;
+    return ranges ? static_cast<size_t>(gated_few_part_bytes(T, ranges)) +
+                        round_up(static_cast<size_t>((F + 127) / 128) * sizeof(unsigned), 256)
+                  : 0;
 }
 
 int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const float* amax_out)
@@ -1006,11 +1002,11 @@ size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int 
         return 0;
     if (pass == 0)
         return carve(nullptr, fmt, T, Kin, nullptr) + carve_gated_weights(nullptr, fmt, Kin, F, nullptr) +
-               gated_few_bytes(T, F);
+               gated_few_bytes(T, Kin, F, fmt);
     if (pass == 1)  // D, its maximum, and the linear layer's backward
         return round_up(static_cast<size_t>(T) * static_cast<size_t>(F) * 4, 256) + 256 +
                mx_linear_workspace_bytes(T, Kin, 2 * F, fmt, 2);
-    return pass == 2 ? carve(nullptr, fmt, T, Kin, nullptr) + gated_few_bytes(T, F) : 0;
+    return pass == 2 ? carve(nullptr, fmt, T, Kin, nullptr) + gated_few_bytes(T, Kin, F, fmt) : 0;
 }
 
 int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, int fmt, int act, const void* W,
@@ -1055,11 +1051,14 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
     void* parts = nullptr;
     unsigned* counters = nullptr;
     if (quantize_few_takes(T, Kin)) {
-        uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - gated_few_bytes(T, F);
-        parts = tail;
-        counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T));
+        const size_t room = gated_few_bytes(T, Kin, F, fmt);
+        if (room) {
+            uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - room;
+            parts = tail;
+            counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T, gated_few_ranges(T, F, Kin, fmt)));
+        }
         fill_meta(&xq, T, Kin, fmt, 0);
-        rc = launch_quantize_few(X, ldx, &xq, counters, static_cast<int>((F + 127) / 128), d, s);
+        rc = launch_quantize_few(X, ldx, &xq, counters, counters ? static_cast<int>((F + 127) / 128) : 0, d, s);
     } else {
         rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
                            &xq, d, s);

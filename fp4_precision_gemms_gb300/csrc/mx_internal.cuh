@@ -12,6 +12,9 @@ namespace mx {
 __host__ __device__ constexpr bool fmt_is_nvfp4(int fmt) { return fmt == MX_FMT_NVFP4 || fmt == MX_FMT_NVFP4_LOCAL; }
 __host__ __device__ constexpr bool fmt_is_fp4(int fmt) { return fmt == MX_FMT_MXFP4_E2M1 || fmt_is_nvfp4(fmt); }
 __host__ __device__ constexpr int fmt_block(int fmt) { return fmt_is_nvfp4(fmt) ? 16 : 32; }
+constexpr int64_t codes_row_bytes(int fmt, int64_t k) { return fmt_is_fp4(fmt) ? k / 2 : k; }
+// K granularity the GEMM consumes per pipeline stage.
+constexpr int64_t gemm_k_multiple(int fmt) { return fmt_is_fp4(fmt) ? 256 : 128; }
 __host__ __device__ constexpr bool fmt_has_tensor_scale(int fmt) { return fmt_is_nvfp4(fmt) || fmt == MX_FMT_MOSS_FP8; }
 __host__ __device__ constexpr bool fmt_is_local(int fmt) { return fmt == MX_FMT_NVFP4_LOCAL; }
 constexpr int kLocalRegion = MX_LOCAL_REGION;  // operand rows per FP32 scale (NVFP4_LOCAL)
@@ -198,15 +201,18 @@ struct GatedArgs {
     // the launch before this one wrote x, and was itself launched after everything before
     // it had finished: the weights may be read before it has
     bool early;
-    // few tokens: partial sums (gated_few_part_bytes) and a zero word for each 128 features,
-    // or null for both
+    // few tokens whose call is cut along K (gated_few_ranges): partial sums (gated_few_part_bytes)
+    // and a zero word for each 128 features; null for both: it is not cut
     void* parts;
     unsigned* counters;
 };
 constexpr int kGatedFewTokens = 64;  // up to here launch_gated takes gated_few.cu's kernel
 constexpr int kGatedFewCtas = 152;   // of that kernel, at most
-// Two slots a CTA of 2 x 128 sums for each token, tokens in fours.
-inline int64_t gated_few_part_bytes(int64_t tokens) { return int64_t{kGatedFewCtas} * 2 * 2 * 128 * ((tokens + 3) / 4) * 16; }
+// The equal ranges, one a CTA, that the kernel cuts all tiles' steps along K into, 0 where
+// each tile is a CTA's own.
+int64_t gated_few_ranges(int64_t tokens, int64_t features, int64_t k, int fmt);
+// Two slots a range of 2 x 128 sums for each token, tokens in fours.
+inline int64_t gated_few_part_bytes(int64_t tokens, int64_t ranges) { return ranges * 2 * 2 * 128 * ((tokens + 3) / 4) * 16; }
 int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s);
 // Rowwise quantization of a few rows with the default rules (quant_few.cu); out's
 // fields are set.  Sets `zeros` words from `zero` on to zero.  A launch that follows may

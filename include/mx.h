@@ -463,7 +463,9 @@ int mx_act_bwd(const void* dh, int64_t ldh, const void* gate, int64_t ldg, const
  * to bf16.  ldh >= F, ldh % 8 == 0, h 16-byte aligned.  gate8 / up8: checkpoints of
  * g and u (from fp32), both or neither.  amax_out (may be NULL): max |h|.
  * Operands carry no Hadamard transform (MX_ERR_UNSUPPORTED); other rules as
- * mx_gemm, and K > 0. */
+ * mx_gemm, and K > 0.  (Up to 64 tokens mx_gated_fwd may cut the products along K
+ * where that is faster, and adds the parts in an order that the shapes fix; this
+ * call, which has no workspace for them, never does.) */
 int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
                   const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* stream);
 
