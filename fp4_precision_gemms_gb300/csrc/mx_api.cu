@@ -1050,16 +1050,19 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
     // the tokens last: the weights are then complete before their quantization starts
     void* parts = nullptr;
     unsigned* counters = nullptr;
-    if (quantize_few_takes(T, Kin)) {
-        const size_t room = gated_few_bytes(T, Kin, F, fmt);
-        if (room) {
-            uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - room;
-            parts = tail;
-            counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T, gated_few_ranges(T, F, Kin, fmt)));
-        }
+    int zeros = 0;  // counters
+    if (const size_t room = gated_few_bytes(T, Kin, F, fmt)) {
+        uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - room;
+        parts = tail;
+        counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T, gated_few_ranges(T, F, Kin, fmt)));
+        zeros = static_cast<int>((F + 127) / 128);
+    }
+    if (quantize_few_takes(fmt, T, Kin)) {
         fill_meta(&xq, T, Kin, fmt, 0);
-        rc = launch_quantize_few(X, ldx, &xq, counters, counters ? static_cast<int>((F + 127) / 128) : 0, d, s);
+        rc = launch_quantize_few(X, ldx, &xq, counters, zeros, d, s);
     } else {
+        if (counters && cudaMemsetAsync(counters, 0, zeros * sizeof(unsigned), s) != cudaSuccess)
+            return MX_ERR_CUDA;
         rc = quantize_impl(X, T, Kin, ldx, MX_ROWWISE, fmt, fmt_block(fmt), MX_ROUND_RNE, MX_SCALE_DEFAULT, 0, 0, 0, nullptr,
                            &xq, d, s);
     }

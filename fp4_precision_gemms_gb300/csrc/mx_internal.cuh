@@ -217,7 +217,7 @@ int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s);
 // Rowwise quantization of a few rows with the default rules (quant_few.cu); out's
 // fields are set.  Sets `zeros` words from `zero` on to zero.  A launch that follows may
 // start early.
-bool quantize_few_takes(int64_t rows, int64_t k);
+bool quantize_few_takes(int fmt, int64_t rows, int64_t k);
 int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, const Device& d,
                         cudaStream_t s);
 int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s);

@@ -196,9 +196,12 @@ int launch_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, 
 
 }  // namespace
 
-bool quantize_few_takes(int64_t rows, int64_t k)
+// With a tensor scale as many values as the cluster's registers hold; else any number that
+// its 32-bit indexes reach.
+bool quantize_few_takes(int fmt, int64_t rows, int64_t k)
 {
-    return rows > 0 && rows <= kGatedFewTokens && k % 32 == 0 && rows * k <= int64_t{kCluster} * 1024 * kMaxOcts * 8;
+    const int64_t most = fmt_has_tensor_scale(fmt) ? int64_t{kCluster} * 1024 * kMaxOcts * 8 : int64_t{1} << 33;
+    return rows > 0 && rows <= kGatedFewTokens && k % 32 == 0 && rows * k <= most;
 }
 
 int launch_quantize_few(const void* x, int64_t ld, const mx_tensor* out, unsigned* zero, int zeros, const Device& d, cudaStream_t s)

@@ -137,3 +137,18 @@ def test_two_host_threads(mx):
         assert len(results[i]) == 20
         for r in results[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, alone[0]))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_wide_rows_are_cut(mx, fmt):
+    """Eight tiles of a long K are cut whatever quantizes the tokens: every tile's counter, at the workspace's end,
+    has been set to zero and counted its pieces."""
+    T, K, F = 48, 14336, 1024
+    X, W = data(T, K, F, 6)
+    w = mx.gated_weights(W, fmt)
+    ws = torch.full((mx.gated_workspace_bytes(T, K, F, fmt, "fwd_quantized"),), 0x5A, dtype=torch.uint8, device="cuda")
+    want = mx.gated_fwd(X, w, fmt)
+    for _ in range(2):
+        assert torch.equal(mx.gated_fwd(X, w, fmt, workspace=ws), want)
+        counts = ws[-256:].view(torch.int32)[:F // 128]
+        assert ((counts > 1) & (counts <= 152)).all()
