@@ -984,8 +984,9 @@ int launch_pair(const mx_tensor* A, const mx_tensor* B, float extra, void* C, in
 {
     using G = CfgPair<KIND, STAGES, BKB_, SFS>;
     auto kernel = bs_gemm_pair_kernel<KIND, STAGES, BKB_, SFS>;
-    static int configured_device = -1;
-    static int max_clusters = 0;
+    // a thread's own: another's could see the device before the number of clusters
+    static thread_local int configured_device = -1;
+    static thread_local int max_clusters = 0;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -519,8 +519,9 @@ template <class G, class Epi>
 int ws_max_clusters(const Device& d, int* clusters)
 {
     auto kernel = bs_gemm_ws_kernel<G, Epi>;
-    static int configured_device = -1;
-    static int max_clusters = 0;
+    // a thread's own: another's could see the device before the number of clusters
+    static thread_local int configured_device = -1;
+    static thread_local int max_clusters = 0;
     if (configured_device != d.id) {
         // The register split (setmaxnreg) assumes the kernel launches with 128
         // registers per thread: with fewer, the epilogue's increase could not be
