@@ -895,7 +895,8 @@ _GATED_PASSES = {"fwd": 0, "bwd": 1, "fwd_quantized": 2}
 
 def gated_workspace_bytes(T: int, Kin: int, F: int, fmt: str, pass_: str = "fwd") -> int:
     """Workspace of gated_fwd from W and gated_fwd_save ("fwd"), gated_bwd ("bwd") and
-    gated_fwd from quantized weights ("fwd_quantized")."""
+    gated_fwd from quantized weights ("fwd_quantized").  One for T tokens serves fewer, but
+    for up to 64 tokens in one for more than 64: there, the larger of the sizes for 64 and T."""
     return int(lib().mx_gated_workspace_bytes(T, Kin, F, _look_up(FORMATS, fmt, "fmt"),
                                               _look_up(_GATED_PASSES, pass_, "pass_")))
 

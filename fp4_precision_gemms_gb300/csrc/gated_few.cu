@@ -12,7 +12,7 @@
 // the tokens' quantization, the kernel fills its ring with weights before that has finished.
 //
 // Where the tiles are too few, or a little more than the SMs, their steps along K, one tile
-// after another, are cut into equal ranges, one an SM (gated_few_ranges).  A tile
+// after another, are cut into equal ranges, one an SM (gated_few_cut).  A tile
 // that lies in several ranges leaves partial sums in a workspace; the CTA that counts
 // itself last for the tile, after its own partial sums are visible, adds them up in the
 // ranges' order.  No CTA waits for another.
@@ -485,7 +485,7 @@ int launch_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s)
     p.status = d.status;
     p.wait_ns = kWaitLimitNs;
     const int64_t tiles = (N + 127) / 128;
-    const int64_t ranges = a.parts ? gated_few_ranges(M, N, K, a.x->fmt) : 0, ctas = ranges ? ranges : tiles;
+    const int64_t ctas = a.parts ? gated_few_cut(N, K, a.x->fmt).ranges : tiles;
     p.parts = static_cast<float4*>(a.parts);
     p.counters = a.counters;
     return launch_kernel(gated_few_kernel<KIND>, static_cast<unsigned>(ctas), 1, 512, G::SMEM_ALLOC, early, s, mx, mg, mu, p);
@@ -504,22 +504,22 @@ int launch_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s)
 // 26.3; 80 tiles NVFP4 48 tokens 15.8 / 19.7; 112 tiles MXFP8 1 token 23.6 / 26.5; 160
 // tiles, of which 8 would be a wave of their own, 43.3 / 33.4; 304 tiles, as ranges of two
 // whole ones, 54.5 / 51.5.
-int64_t gated_few_ranges(int64_t tokens, int64_t features, int64_t k, int fmt)
+FewCut gated_few_cut(int64_t features, int64_t k, int fmt)
 {
     const int64_t num_kt = k / gemm_k_multiple(fmt), tiles = (features + 127) / 128, steps = tiles * num_kt;
     if (steps == 0)
-        return 0;
+        return {0, 0};
     const int64_t ranges = std::max<int64_t>(1, std::min<int64_t>(kGatedFewCtas, steps / 4));
     const double step_us = 256.0 * static_cast<double>(codes_row_bytes(fmt, k) + k / fmt_block(fmt)) / static_cast<double>(num_kt) / 80e3;
     const double memory_us = static_cast<double>(steps) * step_us * (80.0 / 7500.0);
     const int64_t waves = (tiles + kGatedFewCtas - 1) / kGatedFewCtas;
     const double whole_us = std::max(memory_us, static_cast<double>(waves * num_kt) * step_us) + 5.0 * static_cast<double>(waves - 1);
-    double cut_us = std::max(memory_us, static_cast<double>((steps + ranges - 1) / ranges) * step_us);
-    if (steps % ranges != 0 || steps / ranges % num_kt != 0) {
-        const double t = static_cast<double>(tokens), pieces = static_cast<double>((num_kt * ranges + steps - 1) / steps);
-        cut_us += 2.0 + 0.05 * t + pieces * (0.2 + 0.015 * t);
-    }
-    return cut_us < whole_us ? ranges : 0;
+    const double spare_us = whole_us - std::max(memory_us, static_cast<double>((steps + ranges - 1) / ranges) * step_us);
+    if (steps % ranges == 0 && steps / ranges % num_kt == 0)  // ranges of whole tiles: nothing to join
+        return {ranges, spare_us > 0.0 ? kGatedFewTokens : 0};
+    const double pieces = static_cast<double>((num_kt * ranges + steps - 1) / steps);
+    const double most = (spare_us - 2.0 - 0.2 * pieces) / (0.05 + 0.015 * pieces);
+    return {ranges, std::max<int64_t>(0, static_cast<int64_t>(std::min<double>(most, kGatedFewTokens)))};
 }
 
 int launch_gated_few(const GatedArgs& a, bool early, const Device& d, cudaStream_t s)

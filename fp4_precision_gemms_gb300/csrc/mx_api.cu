@@ -860,13 +860,15 @@ mx_tensor operand_rows(const mx_tensor& t, int64_t from, int64_t rows)
     return v;
 }
 
-// The kernel for few tokens: its partial sums and counters, at a workspace's end, where it cuts.
+// The kernel for few tokens: its partial sums and counters, at a workspace's end, where it
+// cuts with these tokens or with fewer (whose calls may have the same workspace).
 size_t gated_few_bytes(int64_t T, int64_t Kin, int64_t F, int fmt)
 {
-    const int64_t ranges = T > 0 && T <= kGatedFewTokens ? gated_few_ranges(T, F, Kin, fmt) : 0;
-    return ranges ? static_cast<size_t>(gated_few_part_bytes(T, ranges)) +
-                        round_up(static_cast<size_t>((F + 127) / 128) * sizeof(unsigned), 256)
-                  : 0;
+    const FewCut c = T <= kGatedFewTokens ? gated_few_cut(F, Kin, fmt) : FewCut{};
+    const int64_t tokens = std::min(T, c.tokens);
+    return tokens > 0 ? static_cast<size_t>(gated_few_part_bytes(tokens, c.ranges)) +
+                            round_up(static_cast<size_t>((F + 127) / 128) * sizeof(unsigned), 256)
+                      : 0;
 }
 
 int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const float* amax_out)
@@ -1051,10 +1053,10 @@ int mx_gated_fwd(const void* X, int64_t ldx, int64_t T, int64_t Kin, int64_t F, 
     void* parts = nullptr;
     unsigned* counters = nullptr;
     int zeros = 0;  // counters
-    if (const size_t room = gated_few_bytes(T, Kin, F, fmt)) {
-        uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - room;
+    if (const FewCut c = gated_few_cut(F, Kin, fmt); T <= c.tokens) {
+        uint8_t* tail = ws + mx_gated_workspace_bytes(T, Kin, F, fmt, W ? 0 : 2) - gated_few_bytes(T, Kin, F, fmt);
         parts = tail;
-        counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T, gated_few_ranges(T, F, Kin, fmt)));
+        counters = reinterpret_cast<unsigned*>(tail + gated_few_part_bytes(T, c.ranges));
         zeros = static_cast<int>((F + 127) / 128);
     }
     if (quantize_few_takes(fmt, T, Kin)) {

@@ -201,16 +201,19 @@ struct GatedArgs {
     // the launch before this one wrote x, and was itself launched after everything before
     // it had finished: the weights may be read before it has
     bool early;
-    // few tokens whose call is cut along K (gated_few_ranges): partial sums (gated_few_part_bytes)
+    // few tokens whose call is cut along K (gated_few_cut): partial sums (gated_few_part_bytes)
     // and a zero word for each 128 features; null for both: it is not cut
     void* parts;
     unsigned* counters;
 };
 constexpr int kGatedFewTokens = 64;  // up to here launch_gated takes gated_few.cu's kernel
 constexpr int kGatedFewCtas = 152;   // of that kernel, at most
-// The equal ranges, one a CTA, that the kernel cuts all tiles' steps along K into, 0 where
-// each tile is a CTA's own.
-int64_t gated_few_ranges(int64_t tokens, int64_t features, int64_t k, int fmt);
+// The equal ranges, one a CTA, that the kernel cuts all tiles' steps along K into, and the
+// most tokens with which it does; with more each tile is a CTA's own.
+struct FewCut {
+    int64_t ranges, tokens;
+};
+FewCut gated_few_cut(int64_t features, int64_t k, int fmt);
 // Two slots a range of 2 x 128 sums for each token, tokens in fours.
 inline int64_t gated_few_part_bytes(int64_t tokens, int64_t ranges) { return ranges * 2 * 2 * 128 * ((tokens + 3) / 4) * 16; }
 int launch_gated(const GatedArgs& a, const Device& d, cudaStream_t s);

@@ -471,7 +471,9 @@ int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up
 
 /* Workspace bytes: pass 0 mx_gated_fwd from W and mx_gated_fwd_save, pass 1
  * mx_gated_bwd, pass 2 mx_gated_fwd from quantized weights; 0 for another pass or
- * invalid arguments. */
+ * invalid arguments.  With up to 64 tokens pass 0 and 2 may hold partial sums, and
+ * the bytes for T serve any smaller T; from 65 on they hold none, so that a
+ * workspace for both kinds of call has the larger of the bytes for 64 and for T. */
 size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int pass);
 
 /* The block from X[T, Kin] (bf16, row stride ldx, ldx % 8 == 0, 16-byte aligned),

@@ -22,9 +22,18 @@ def room(T, K, F, fmt):
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4", "moss"])
 @pytest.mark.parametrize("T,K,tiles", [(1, 4096, 112), (48, 4096, 112), (48, 4096, 80), (48, 4096, 86), (64, 1024, 86), (1, 1024, 32),
-                                       (64, 4096, 64), (64, 8192, 92), (1, 4096, 152), (64, 1024, 8)])
+                                       (64, 8192, 92), (1, 4096, 152), (64, 1024, 8)])
 def test_whole(fmt, T, K, tiles):
     assert room(T, K, 128 * tiles, fmt) < 4096
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4"])
+@pytest.mark.parametrize("K,tiles", [(1024, 8), (4096, 32), (4096, 64), (4096, 160), (8192, 8), (8192, 64), (768, 320), (4096, 304)])
+@pytest.mark.parametrize("pass_", ["fwd", "fwd_quantized"])
+def test_serves_fewer_tokens(fmt, K, tiles, pass_):
+    """Cut with few tokens and whole with more: the room for more holds what fewer need."""
+    sizes = [mx.gated_workspace_bytes(T, K, 128 * tiles, fmt, pass_) for T in range(1, 65)]
+    assert sizes == sorted(sizes)
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4", "moss"])

@@ -152,3 +152,15 @@ def test_wide_rows_are_cut(mx, fmt):
         assert torch.equal(mx.gated_fwd(X, w, fmt, workspace=ws), want)
         counts = ws[-256:].view(torch.int32)[:F // 128]
         assert ((counts > 1) & (counts <= 152)).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4", "nvfp4_local"])
+@pytest.mark.parametrize("K,tiles", [(4096, 32), (4096, 64), (1024, 8), (768, 200)])
+def test_one_workspace_for_every_batch(mx, fmt, K, tiles):
+    """A workspace for 64 tokens serves the batches that shrink and grow behind one another, cut or not."""
+    X, W = data(64, K, 128 * tiles, 8)
+    for weights in (mx.gated_weights(W, fmt), W):
+        ws = torch.full((mx.gated_workspace_bytes(64, K, 128 * tiles, fmt, "fwd" if weights is W else "fwd_quantized"),), 0x5A,
+                        dtype=torch.uint8, device="cuda")
+        for T in (64, 1, 48, 7, 16, 33, 64, 2):
+            assert torch.equal(mx.gated_fwd(X[:T], weights, fmt, workspace=ws), mx.gated_fwd(X[:T], weights, fmt))
