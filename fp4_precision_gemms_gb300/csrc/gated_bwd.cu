@@ -112,7 +112,7 @@ __device__ __forceinline__ void encode_columns(const uint32_t (&w)[32], uint8_t*
             a[i] = cvt_e4m3x2(p.x, q.x) | cvt_e4m3x2(r.x, t.x) << 16;
             b[i] = cvt_e4m3x2(p.y, q.y) | cvt_e4m3x2(r.y, t.y) << 16;
         }
-        store_sector(to_a, a);  // in two halves each: 266 us in place of 246
+        store_sector(to_a, a);  // in two halves each: 20 us more at 8192 x 14336 in an earlier form
         store_sector(to_b, b);
     } else {
         uint32_t a[4], b[4];

@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 256;
 // Octs (eight consecutive values) that a thread takes of a tile.  8-bit moments: four, 32
 // apart, so that a warp has 32 whole groups and reads and writes their exponent bytes as
-// one sector each (a quarter of a sector at a time: 602 us in place of 545 for a layer).
+// one sector each (a quarter of a sector at a time cost a layer 57 us more in an earlier form).
 __host__ __device__ constexpr int octs_of(int bits) { return bits == 8 ? 4 : 1; }
 
 // Eight fp32 values at a multiple of 32 bytes in one access.  (In two of 16 bytes each, a
@@ -334,8 +334,11 @@ constexpr int least_ctas(int bits, bool sr, bool any) { return !any ? 0 : bits =
 //
 // Bound by DRAM: a layer of 218e6 values, fp32 with bf16 copies and maxima, 990 us (6.54
 // GB, 6.6 TB/s; 1408 with fp32 accesses of 16 bytes), 8-bit moments and bf16 gradients
-// 564 us (3.52 GB, 6.2 TB/s).  Stochastic rounding at odd addresses by instructions: 7.7e6
-// bf16 values 37 us, three sets of random numbers and the shifts.
+// 564 us (3.52 GB, 6.2 TB/s).  Stochastic rounding of 8-bit moments is bound by
+// instructions, 125 a value at odd addresses against 60 to nearest: about 19 are the random
+// numbers (three sets for eight values), the others the two roundings to E4M3, bf16's and the
+// shifts.  7.7e6 bf16 values at odd addresses 37 us; 218e6 aligned ones with bf16 gradients and
+// no copies, stochastic / to nearest: fp32 813 / 516 us, bf16 833 / 470.
 template <typename P, typename G, int BITS, bool SR, bool ANY>
 __global__ void __launch_bounds__(kThreads, least_ctas(BITS, SR, ANY)) adamw_kernel(const __grid_constant__ AdamwTable a)
 {

@@ -511,8 +511,10 @@ int mx_gated_bwd(const void* dH, int64_t lddh, int64_t T, int64_t Kin, int64_t F
  * hold where they apply: stream order, no allocation, no reduction whose
  * result depends on the order of atomics, capture into CUDA graphs.  Arrays of
  * descriptors are host memory, read before the call returns; the tensors are
- * contiguous device memory that needs the alignment of its elements only
- * (16-byte aligned tensors of a multiple of eight values take wide accesses). */
+ * contiguous device memory that needs the alignment of its elements only.
+ * (Tensors of a multiple of eight values take wide accesses where bf16 arrays are
+ * 16-byte and fp32 arrays 32-byte aligned; of AdamW's tensors all arrays must be, but
+ * 8-bit moments.) */
 
 typedef struct mx_grad {
     const void* data;
