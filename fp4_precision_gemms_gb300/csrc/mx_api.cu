@@ -882,10 +882,8 @@ int check_gated_output(const void* h, int64_t ldh, int64_t T, int64_t F, const f
     return ldh % 8 == 0 && aligned16(h) ? MX_OK : MX_ERR_ALIGNMENT;
 }
 
-// early: A was written by the launch before this one, which waited for all before it, and
-// amax_out is zero already.  parts, counters: as GatedArgs has them.
-int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
-                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, bool early, void* parts, unsigned* counters, const Device& d, cudaStream_t s)
+int check_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, const void* h, int64_t ldh,
+                     const mx_act8* gate8, const mx_act8* up8, const float* amax_out)
 {
     for (const mx_tensor* t : {A, gate, up}) {
         const int rc = check_operand(t);
@@ -907,11 +905,18 @@ int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* 
     for (const mx_act8* c : {gate8, up8})
         if (c && rc == MX_OK)
             rc = check_checkpoint(c, T, F);
-    if (rc != MX_OK)
-        return rc;
+    return rc;
+}
+
+// With checked arguments.  early: A was written by the launch before this one, which waited
+// for all before it, and amax_out is zero already.  parts, counters: as GatedArgs has them.
+int gemm_gated_impl(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up, int act, void* h, int64_t ldh,
+                    const mx_act8* gate8, const mx_act8* up8, float* amax_out, bool early, void* parts, unsigned* counters,
+                    const Device& d, cudaStream_t s)
+{
     if (!early && amax_out && cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess)
         return MX_ERR_CUDA;
-    if (T == 0 || F == 0)
+    if (A->rows == 0 || gate->rows == 0)
         return MX_OK;
     GatedArgs a;
     a.x = A;
@@ -992,10 +997,11 @@ int mx_gemm_gated(const mx_tensor* A, const mx_tensor* gate, const mx_tensor* up
                   const mx_act8* gate8, const mx_act8* up8, float* amax_out, void* stream)
 {
     Device d;
-    const int rc = current_device(&d);
-    if (rc != MX_OK)
+    int rc = check_gemm_gated(A, gate, up, act, h, ldh, gate8, up8, amax_out);
+    if (rc != MX_OK || (rc = current_device(&d)) != MX_OK)
         return rc;
-    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d, static_cast<cudaStream_t>(stream));
+    return gemm_gated_impl(A, gate, up, act, h, ldh, gate8, up8, amax_out, false, nullptr, nullptr, d,
+                           static_cast<cudaStream_t>(stream));
 }
 
 size_t mx_gated_workspace_bytes(int64_t T, int64_t Kin, int64_t F, int fmt, int pass)
