@@ -24,7 +24,9 @@ namespace mx {
 namespace {
 
 struct GatedParams {
-    CUtensorMap map_h;  // h in boxes of 32 rows x 32 columns
+    CUtensorMap map_h;  // h's columns up to a multiple of eight, in boxes of 32 rows x 32 columns
+    __nv_bfloat16* h;
+    int64_t ldh;
     const float* tsa;
     const float* tsg;
     const float* tsu;
@@ -123,7 +125,7 @@ struct GatedEpilogue {
         au = __fmul_rn(ta, p.tsu ? *p.tsu : 1.0f);
     }
     // 64 bytes of each of the warp's 32 rows to column x on, by a tensor store that clips
-    // what lies outside the matrix.  The box is swizzled (16-byte pieces of a 64-byte row
+    // what lies outside the map.  The box is swizzled (16-byte pieces of a 64-byte row
     // exchanged by the row's pair number), which keeps the lanes' writes apart in the banks.
     // The stores that leave the chip then cost the load/store unit nothing, on which the
     // warps that feed the scales depend.
@@ -194,7 +196,16 @@ struct GatedEpilogue {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     top.word(pk[i]);
-            send(p.map_h, pk, col0, row0, lane, stg);
+            const int edge = p.N & ~7;  // a tensor store writes its last 16 bytes whole, past the columns too
+            if (col0 < edge)
+                send(p.map_h, pk, col0, row0, lane, stg);
+            if (col0 + 32 > edge && edge < p.N && row < p.M) {
+                uint16_t* to = reinterpret_cast<uint16_t*>(p.h) + static_cast<int64_t>(row) * p.ldh + col0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (col0 + i >= edge && i < n)
+                        to[i] = static_cast<uint16_t>(pk[i >> 1] >> (16 * (i & 1)));
+            }
         }
         if (!save)
             return;
@@ -220,13 +231,14 @@ struct GatedEpilogue {
     }
 };
 
-// 2-D map over h (row stride ld) for stores of 32 x 32 boxes with the 64-byte swizzle.
+// 2-D map over h (row stride ld) for stores of 32 x 32 boxes with the 64-byte swizzle.  With
+// fewer than eight columns no store is made through it.
 bool make_h_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc)
         return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(std::max<int64_t>(cols & ~int64_t{7}, 8)), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
     const cuuint32_t box[2] = {32u, 32u};
     const cuuint32_t estr[2] = {1u, 1u};
@@ -252,6 +264,8 @@ int launch_gated_ws(const GatedArgs& a, const Device& d, cudaStream_t s)
     GatedParams p;
     if (!make_h_map(&p.map_h, a.h, M, N, a.ldh))
         return MX_ERR_CUDA;
+    p.h = static_cast<__nv_bfloat16*>(a.h);
+    p.ldh = a.ldh;
     const bool ts = fmt_has_tensor_scale(a.x->fmt);
     p.tsa = ts ? a.x->tensor_scale : nullptr;
     p.tsg = ts ? a.gate->tensor_scale : nullptr;
