@@ -811,7 +811,8 @@ __global__ void __launch_bounds__(CfgPair<KIND, STAGES, BKB_, SFS_>::THREADS, 1)
         };
         int titer = 0;
         bool sf_good = true;
-        const bool tma_out = G::TMA_OUT && p.out_mode <= EPI_BF16;
+        // a tensor store writes the 16 bytes that hold a row's last column whole, past it too
+        const bool tma_out = G::TMA_OUT && p.out_mode <= EPI_BF16 && p.N % (p.out_mode == EPI_BF16 ? 8 : 4) == 0;
         bool stg_busy = false;  // this warp's staging box may still be read by a TMA store
         float am = 0.0f;        // output amax of this thread's rows (amax_out)
         for (int tile = cluster_id; tile < tiles && sf_good; tile += nclusters, ++titer) {
@@ -855,7 +856,7 @@ __global__ void __launch_bounds__(CfgPair<KIND, STAGES, BKB_, SFS_>::THREADS, 1)
             const int row = row0 + lane;
             if (tma_out) {
                 // 32 rows x 64 bytes per box: 32 bf16 columns, or 16 fp32 columns;
-                // the store clips rows >= M and columns >= N
+                // the store clips rows >= M and columns >= N (whole 16 bytes)
                 auto emit = [&](const uint32_t (&pk)[16], int col) {
                     if (row0 >= p.M)  // all of this warp's rows lie past the output
                         return;
