@@ -129,7 +129,9 @@ struct GatedEpilogue {
     // exchanged by the row's pair number), which keeps the lanes' writes apart in the banks.
     // The stores that leave the chip then cost the load/store unit nothing, on which the
     // warps that feed the scales depend.
-    __device__ __forceinline__ void send(const CUtensorMap& map, const uint32_t (&w)[16], int x, int row0, int lane, uint8_t* stg)
+    // A store writes its last 16 bytes whole, so the map ends at a multiple of eight columns;
+    // those after it the lanes take from the box one by one.
+    __device__ __forceinline__ void send(const GatedParams& p, const uint32_t (&w)[16], int x, int row0, int lane, uint8_t* stg)
     {
         if (busy) {  // the previous store has read the box
             if (lane == 0)
@@ -140,13 +142,23 @@ struct GatedEpilogue {
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(stg + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) =
                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(&map, smem_u32(stg), x, row0);
-            bulk_commit();
+        const int edge = p.N & ~7;
+        busy = x < edge;
+        if (busy) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(&p.map_h, smem_u32(stg), x, row0);
+                bulk_commit();
+            }
         }
-        busy = true;
+        if (x + 32 > edge && edge < p.N && row0 + lane < p.M) {
+            const uint8_t* from = stg + lane * 64 + (((edge - x) >> 3 ^ (lane >> 1)) & 3) * 16;
+            __nv_bfloat16* to = p.h + (row0 + lane) * p.ldh + edge;
+#pragma unroll 1
+            for (int i = 0; i < p.N - edge; ++i)
+                to[i] = reinterpret_cast<const __nv_bfloat16*>(from)[i];
+        }
     }
 
     // chunks 0, 1: gate columns, 2, 3: the same up columns
@@ -196,16 +208,7 @@ struct GatedEpilogue {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     top.word(pk[i]);
-            const int edge = p.N & ~7;  // a tensor store writes its last 16 bytes whole, past the columns too
-            if (col0 < edge)
-                send(p.map_h, pk, col0, row0, lane, stg);
-            if (col0 + 32 > edge && edge < p.N && row < p.M) {
-                uint16_t* to = reinterpret_cast<uint16_t*>(p.h) + static_cast<int64_t>(row) * p.ldh + col0;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (col0 + i >= edge && i < n)
-                        to[i] = static_cast<uint16_t>(pk[i >> 1] >> (16 * (i & 1)));
-            }
+            send(p, pk, col0, row0, lane, stg);
         }
         if (!save)
             return;
@@ -223,8 +226,8 @@ struct GatedEpilogue {
     }
     __device__ __forceinline__ void finish(const GatedParams& p)
     {
-        if (busy && (threadIdx.x & 31) == 0)
-            bulk_wait_all();
+        if ((threadIdx.x & 31) == 0)
+            bulk_wait_all();  // the box's next use may have waited for a store's reads only
         __syncwarp();
         if (p.amax_out)
             flush_top(p.amax_out, top);
